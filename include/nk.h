@@ -58,7 +58,10 @@ enum {
 enum {
   NK_STATUS_PAGE_RANGE = 1,  /* a table entry was outside [0, M)             */
   NK_STATUS_FRONTIER = 2,    /* a position reached past L*P of its row       */
-  NK_STATUS_TIMEOUT = 4      /* a bounded wait on a copy barrier ran out     */
+  NK_STATUS_TIMEOUT = 4,     /* a bounded wait on a copy barrier ran out     */
+  NK_STATUS_TOKEN_RANGE = 8, /* a drafted token outside [0, V), or no weight */
+                             /* anywhere to draw the next token from         */
+  NK_STATUS_PREFIX = 16      /* rows of a shared prefix named other pages    */
 };
 
 /* KV profiles ("Paged KV cache" page, pool contents paragraph: BF16,
@@ -257,6 +260,37 @@ int nk_paged_append_decode_attention(const void* q, int32_t Hq, nk_pool* pool, i
                                      float* lse, void* workspace, size_t workspace_bytes,
                                      void* stream);
 
+/* Workspace of nk_paged_shared_decode_attention for (B, T, Hq). */
+int nk_shared_decode_workspace_bytes(const nk_pool* pool, int32_t B, int32_t T, int32_t Hq,
+                                     size_t* bytes);
+
+/* nk_paged_decode_attention for a batch whose rows share their first
+ * *shared_pages pages (a common system prompt, a forked conversation: "Paged
+ * KV cache" page, Move / Fork section), which are attended once for all rows:
+ * they cross HBM once per call instead of once per row.  Same arguments,
+ * results and errors as nk_paged_decode_attention, and
+ *   shared_pages: device int32, one value in [0, L], read on the device (it
+ *   may change between the replays of a graph).  Row b takes part iff every
+ *   one of its query tokens sees all shared pages, frontiers[b] - T >= 64 *
+ *   *shared_pages; the leading *shared_pages table entries of those rows are
+ *   equal (checked: NK_STATUS_PREFIX, the affected results are then
+ *   undefined).  Rows that do not take part are attended in full by
+ *   themselves, and so are all rows for *shared_pages <= 0 or > L (a negative
+ *   value also records NK_STATUS_FRONTIER).
+ *   workspace: nk_shared_decode_workspace_bytes bytes, no initialisation
+ *   needed; two calls that share a workspace must not overlap.
+ * Three launches: the prefix on the tensor cores, all B * T * Hq / H query
+ * rows of a KV head in 128-row tiles (csrc/prefill.cu, csrc/qprefill.cu, with
+ * their rounding of softmax weights and values); each row's own pages
+ * (csrc/decode.cuh, csrc/vdecode.cu); the log-sum-exp merge (csrc/shared.cu).
+ * The pool's device must be current. */
+int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const nk_pool* pool, int32_t layer,
+                                     const int32_t* block_tables, const int32_t* table_rows,
+                                     const int32_t* frontiers, const int32_t* shared_pages,
+                                     int32_t B, int32_t T, float softmax_scale, void* out,
+                                     float* lse, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
 /* ---- host replicas: logical-order packed pages and transfer runs ----------
  * "Paged KV cache" page, host replica section: a host replica holds the pages
  * of one address space in logical order, without device page ids or block
@@ -288,6 +322,117 @@ int nk_pages_to_host(const nk_pool* pool, const int32_t* page_ids, int32_t n, vo
  * every layer and plane (a restore may target other physical pages than the
  * ones the replica came from).  Errors: as nk_pages_to_host. */
 int nk_pages_from_host(nk_pool* pool, const int32_t* page_ids, int32_t n, const void* host, void* stream);
+
+/* ---- norm, rotation and the append that does both --------------------------
+ * No counterpart on the design pages, which start at the codec: these calls
+ * take the rows of the QKV projection to the operands of the calls above. */
+
+/* How a rotation pairs the first rotary_dim dims of a head. */
+typedef enum {
+  NK_ROPE_HALVES = 0, /* dims i and i + rotary_dim / 2                        */
+  NK_ROPE_PAIRS = 1   /* dims 2i and 2i + 1                                   */
+} nk_rope_layout;
+
+/* Rows of one operand in device memory, bf16: dim d of head h of token n at
+ * ptr[n * token_stride + h * head_stride + d] (strides in elements, multiples
+ * of 8; ptr 16-byte aligned).  A fused QKV row is three of these with the same
+ * token_stride.  For [B][T] operands n = b * T + t. */
+typedef struct {
+  void* ptr;
+  int64_t token_stride;
+  int64_t head_stride;
+} nk_rows;
+
+/* Norm and rotation of one head row x of D elements, all in fp32:
+ *   y_d = x_d * rsqrt(mean(x^2) + eps) * (w_d + weight_offset)  (w not NULL)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)  for the pair of angle i,
+ *   i < rotary_dim / 2; dims from rotary_dim on are not rotated.
+ * The result is rounded once, to bf16 or to the codes of a page. */
+typedef struct {
+  const void* cos_sin;   /* device fp32 [positions][rotary_dim]: the cosines
+                            of the rotary_dim / 2 angles, then their sines;
+                            16-byte aligned; may be NULL for rotary_dim 0      */
+  int32_t positions;     /* rows of cos_sin; a position outside is skipped    */
+  int32_t rotary_dim;    /* multiple of 16 in [0, D]                          */
+  int32_t layout;        /* nk_rope_layout                                    */
+  float eps;             /* finite, >= 0                                      */
+  float weight_offset;   /* 0, or 1 for weights stored as w - 1               */
+  int32_t reserved;      /* 0                                                 */
+  const void* q_weight;  /* device bf16 [D], 16-byte aligned; NULL: no norm   */
+  const void* k_weight;
+} nk_rope;
+
+/* Per-head RMS norm and rotation of queries and keys in one pass.
+ *   q, k: rows of Hq and H heads of head_dim (64, 128 or 256), N tokens; one
+ *   of them may be NULL with its output.  positions: device int32 [N].
+ *   q_out, k_out: rows written.  An output may be its own input (same ptr and
+ *   strides); it must not overlap any other operand, and the rows of an output
+ *   must not overlap one another.
+ * A token whose position is outside [0, rope->positions) is skipped: its
+ * output rows keep what they hold, and NK_STATUS_FRONTIER is recorded.
+ * Runs on the current device.  Errors: NK_ERR_INVALID_ARG, NK_ERR_SHAPE,
+ * NK_ERR_UNSUPPORTED (head_dim, rotary_dim), NK_ERR_ALIGN, NK_ERR_CUDA. */
+int nk_qk_norm_rope(const nk_rope* rope, int32_t head_dim, const nk_rows* q, int32_t Hq,
+                    const nk_rows* k, int32_t H, const int32_t* positions, int32_t N,
+                    const nk_rows* q_out, const nk_rows* k_out, void* stream);
+
+/* nk_paged_kv_append with the norm and the rotation of the keys on the way,
+ * and the same for the tokens' queries in the same launch.  Token t <
+ * count_b of compact row b sits at position pos = write_pos[b] + t, which
+ * gives its page, its offset and its angles:
+ *   pages: K = codec(rotate(norm(k))) and V = codec(v), with the codec rules
+ *   of nk_profile applied to the fp32 result (one rounding: the codes are not
+ *   taken from a bf16 intermediate); BF16 values are the bits of v unchanged.
+ *   q_out: device bf16 [B][T][Hq][D] = rotate(norm(q)); the rows of tokens
+ *   t >= count_b are not written.  q and q_out may both be NULL.  q_out may be
+ *   q itself when q is contiguous.
+ *   k, v: rows of H heads, n = b * T + t; the rest as in nk_paged_kv_append.
+ * A token whose table row or position is out of range (also past
+ * rope->positions) is skipped whole (NK_STATUS_FRONTIER); one whose page id is
+ * out of range keeps its q_out (NK_STATUS_PAGE_RANGE).
+ * The pool's device must be current.  Errors: as nk_paged_kv_append and
+ * nk_qk_norm_rope. */
+int nk_paged_kv_append_rope(nk_pool* pool, int32_t layer, const int32_t* block_tables,
+                            const int32_t* table_rows, const int32_t* write_pos,
+                            const int32_t* counts, const nk_rope* rope, const nk_rows* k,
+                            const nk_rows* v, const nk_rows* q, int32_t Hq, void* q_out, int32_t B,
+                            int32_t T, void* stream);
+
+/* ---- verification of drafted tokens ----------------------------------------
+ * The step behind a verify attention (T = K + 1 tokens a row): which drafts of
+ * the speculative round stand, and the token that follows them.
+ * Sequence b has K_b = draft_len ? draft_len[b] : K drafts (clamped to
+ * [0, K]).  Draft i stands iff all before it do and
+ *   uniforms[b][i] * q_i(x_i) < p_i(x_i),
+ * compared without rounding; p_i and q_i are the target's and the draft
+ * model's probabilities (draft == NULL: q_i is 1 at x_i and 0 elsewhere), x_i
+ * the drafted token.  n = the number that stand.  The next token is the least
+ * j with
+ *   d_0 + .. + d_j > uniforms[b][K] * (d_0 + .. + d_{V-1}),
+ *   d = max(p_n - q_n, 0) for n < K_b (p_n itself where that is 0 everywhere),
+ *   d = p_{K_b} for n = K_b,
+ * summed in more than 46 bits; entries that are not positive and finite weigh
+ * 0 (p and q need not sum to 1).  Where rounding leaves no such j, or
+ * uniforms[b][K] is not below 1, the last token with weight is taken.
+ *   target: device fp32, row (b, i) of V at target + (b * (K + 1) + i) *
+ *   target_stride, i <= K;  draft: row (b, i) at draft + (b * K + i) *
+ *   draft_stride, i < K;  tokens: device int32 [B][K] (NULL for K = 0);
+ *   uniforms: device fp32 [B][K + 1] in [0, 1);  rows behind K_b are not read.
+ *   accepted: device int32 [B] = n;  out_tokens: device int32 [B][K + 1] =
+ *   the n drafts, the next token, then -1.
+ *   frontiers / frontiers_out: device int32 [B] or both NULL:
+ *   frontiers_out[b] = frontiers[b] - (K_b - n), the valid length once the
+ *   rejected tokens are trimmed (may be the same array).
+ * A drafted token outside [0, V) is rejected and a sequence without any weight
+ * gets -1 (NK_STATUS_TOKEN_RANGE).  Runs on the current device, which must
+ * hold every array.  The same inputs give the same bits on every call.
+ * Errors: NK_ERR_INVALID_ARG, NK_ERR_SHAPE (B in [1, 2^20], K in [0, 1024],
+ * V in [1, 2^24], strides >= V), NK_ERR_CUDA. */
+int nk_verify_drafts(const float* target, int64_t target_stride, const float* draft,
+                     int64_t draft_stride, const int32_t* tokens, const int32_t* draft_len,
+                     const float* uniforms, const int32_t* frontiers, int32_t B, int32_t K,
+                     int32_t V, int32_t* accepted, int32_t* out_tokens, int32_t* frontiers_out,
+                     void* stream);
 
 /* Size of the static device scratch of nk_paged_decode_attention_noalloc. */
 #define NK_NOALLOC_SCRATCH_BYTES (32u << 20)

@@ -10,21 +10,13 @@
 
 namespace nk {
 
-struct DecodePlan {
-  int nqt, R, target, ring_bytes;
-  int ctas = 0;  // CTAs per KV head (grid x)
-  int nseg = 0;  // > 0: pieces per head, several per CTA
-  size_t ws_ml_bytes, ws_bytes;
-  DecodeFn fn;
-};
-
 static void plan_sizes(DecodePlan* pl, int B, int H, int D) {
   const size_t parts = static_cast<size_t>(B) * H * pl->target * pl->R;
   pl->ws_ml_bytes = (parts * sizeof(float2) + 255) / 256 * 256;
   pl->ws_bytes = pl->ws_ml_bytes + parts * D * sizeof(float);
 }
 
-static int make_plan(const nk_pool* p, int B, int T, int Hq, DecodePlan* pl) {
+int make_plan(const nk_pool* p, int B, int T, int Hq, DecodePlan* pl) {
   const int H = p->desc.num_kv_heads, D = p->desc.head_dim;
   if (Hq < 1 || Hq % H) return fail(NK_ERR_SHAPE, "Hq must be a positive multiple of num_kv_heads");
   if (B < 1 || B > p->desc.max_concurrency) return fail(NK_ERR_SHAPE, "B must be in [1, C]");

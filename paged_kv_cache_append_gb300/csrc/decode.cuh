@@ -42,6 +42,7 @@
 #include "device.cuh"
 #include "encode.cuh"
 #include "internal.h"
+#include "shared.cuh"
 
 namespace nk {
 
@@ -76,7 +77,19 @@ struct DecodeArgs {
   int nseg = 0;  // > 0: pieces per head the chunking aims at, several per CTA (vdecode.cu)
   int ctas = 0;  // CTAs per KV head of the decode launch (read when nseg > 0)
   int head_major = 0;  // plane order
+  // Pages every row shares (device; nullptr: none).  A row that takes part
+  // (takes_part) is attended from its first own page on, its table and
+  // frontier moved by that many pages, and every row's partials go to the
+  // workspace, for the merge with the prefix's (shared.cu).
+  const int32_t* shared = nullptr;
 };
+
+// Pages of row (F, row) that the prefix pass covers.
+__device__ __forceinline__ int pages_before(const DecodeArgs& a, int F, int row) {
+  if (a.shared == nullptr) return 0;
+  const int pages = *a.shared;
+  return takes_part(pages, F, row, a.T, a.L, a.C) ? pages : 0;
+}
 
 template <int KIND>
 struct CodeRow {
@@ -249,7 +262,7 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
   uint64_t* app = empty + NSTAGE;                           // fused append done (NW arrivals)
   int* s_flags = reinterpret_cast<int*>(app + 1);           // [0] abort
   int* s_F = s_flags + 4;                                   // [8] valid length per row
-  int* s_row = s_flags + 12;                                // [8] table row per row
+  int* s_row = s_flags + 12;                                // [8] first table entry per row
   float* s_qmax = reinterpret_cast<float*>(s_flags + 20);   // [8] per-warp max|q|
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -287,8 +300,9 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
     const int F = a.frontiers[tid], row = a.table_rows[tid];
     const bool ok = F >= 0 && F <= a.L * 64 && row >= 0 && row < a.C && (a.k_new == nullptr || F >= a.T);
     if (!ok && blockIdx.x == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
-    s_F[tid] = ok ? F : 0;
-    s_row[tid] = ok ? row : 0;
+    const int before = pages_before(a, F, row);
+    s_F[tid] = ok ? F - 64 * before : 0;
+    s_row[tid] = ok ? row * a.L + before : 0;  // the row's first table entry
   }
   __syncthreads();
 
@@ -326,7 +340,7 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
 
   // ---- producer warp: stage pages p0 .. p0+n-1 ---------------------------------
   if (warp == NW) {
-    const int32_t* table = a.tables + static_cast<int64_t>(s_row[b]) * a.L + p0;
+    const int32_t* table = a.tables + s_row[b] + p0;
     int gnext = 0;
     bool app_seen = false;
     for (int i = 0; i < n; ++i) {
@@ -386,7 +400,7 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
   if (fused) {
     constexpr int KCBW = code_row_bytes<KK>(D), VCBW = code_row_bytes<KV>(D);
     constexpr int KSBW = scale_row_bytes<KK>(D), VSBW = scale_row_bytes<KV>(D);
-    const int32_t* trow = a.tables + static_cast<int64_t>(s_row[b]) * a.L;
+    const int32_t* trow = a.tables + s_row[b];
     for (int t = warp; t < a.T; t += NW) {
       const int pos = F - a.T + t;
       const int pg = pos >> 6;
@@ -1043,7 +1057,7 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
         }
   }
   consumer_sync<NCONS>();
-  const bool final_out = (nsplit == 1);
+  const bool final_out = nsplit == 1 && a.shared == nullptr;
   const int64_t part0 = (static_cast<int64_t>(b) * a.H + h) * a.target;
   const int64_t part = part0 + split;
   for (int idx = tid; idx < R_real * (D / 4); idx += NCONS) {
@@ -1198,7 +1212,7 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const De
     attr_set = true;
   }
   cudaError_t e = launch_pdl(k, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, tk, tv, a);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.shared != nullptr) return e;
   return launch_pdl(merge_kernel<D, NQT>, dim3(a.B, a.H, D / 32), dim3(256), 0, s, a);
 }
 
@@ -1268,6 +1282,17 @@ cudaError_t decode_k8v4(const nk_pool*, int, const DecodeArgs&, int, dim3, cudaS
 // pages whose codes are exact f16 operands (FP8-row, NVFP4-G16, K8V4); one
 // CTA per SM.  nullptr for other profiles / shapes.
 DecodeFn vdecode_for(int profile, int D, int nqt);
+
+// Split plan of one decode call (decode.cu).
+struct DecodePlan {
+  int nqt, R, target, ring_bytes;
+  int ctas = 0;  // CTAs per KV head (grid x)
+  int nseg = 0;  // > 0: pieces per head, several per CTA
+  size_t ws_ml_bytes, ws_bytes;
+  DecodeFn fn;
+};
+int make_plan(const nk_pool* p, int B, int T, int Hq, DecodePlan* pl);
+
 int occupancy_bf16(int, int, int*);
 int occupancy_int8(int, int, int*);
 int occupancy_fp8(int, int, int*);

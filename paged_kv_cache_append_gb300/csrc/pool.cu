@@ -118,7 +118,7 @@ static int check_desc(const nk_pool_desc* d) {
 
 using namespace nk;
 
-extern "C" int nk_version(void) { return 100; }
+extern "C" int nk_version(void) { return 200; }
 
 extern "C" const char* nk_last_error(void) { return t_error.c_str(); }
 

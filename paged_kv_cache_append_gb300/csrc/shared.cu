@@ -1,0 +1,286 @@
+// shared.cu -- decode / verify attention of a batch whose rows share a long
+// prefix of pages: the prefix is attended once for all rows.
+//
+// softmax(q K^T) V over a row's keys is the log-sum-exp merge of the same over
+// any partition of them.  Here the partition is the shared pages and the row's
+// own:
+//   prefix pass  the B T G query rows that read one KV head, of all rows of
+//                the batch, are the rows of 128-row tensor-core tiles
+//                (prefill.cu, qprefill.cu); the shared pages are cut into
+//                ranges, one CTA each, and every CTA leaves a partial
+//                (m, l, O) for all its query rows;
+//   own pages    the decode kernels (decode.cuh, vdecode.cu) on each row's
+//                pages behind the prefix, as partials too;
+//   merge        M = max m, out = sum 2^(m - M) O / sum 2^(m - M) l, below.
+// The shared pages cross HBM once per call instead of once per row.
+#include <cmath>
+
+#include "decode.cuh"
+#include "prefill_split.cuh"
+
+namespace nk {
+
+cudaError_t prefix_pass_bf16(const nk_pool* p, int layer, const void* q, const int32_t* tables,
+                             const int32_t* table_rows, int Hq, float scale_log2, const PrefillSplit& sp,
+                             const SharedPrefix& sh, cudaStream_t s);
+cudaError_t prefix_pass_quantized(const nk_pool* p, int layer, const void* q, const int32_t* tables,
+                                  const int32_t* table_rows, int Hq, float scale_log2, const PrefillSplit& sp,
+                                  const SharedPrefix& sh, cudaStream_t s);
+
+constexpr int kMaxPrefixSplits = 128;
+
+struct SharedPlan {
+  DecodePlan own;  // the rows' own pages
+  int tiles, nsplit;
+  size_t sh_ml_bytes, sh_bytes, ws_bytes;
+};
+
+static int make_shared_plan(const nk_pool* p, int B, int T, int Hq, SharedPlan* pl) {
+  int rc = make_plan(p, B, T, Hq, &pl->own);
+  if (rc) return rc;
+  const int H = p->desc.num_kv_heads, D = p->desc.head_dim, G = Hq / H;
+  pl->tiles = (B * T * G + 127) / 128;
+  const int fit = p->num_sms / (H * pl->tiles);  // one CTA per SM
+  pl->nsplit = fit < 1 ? 1 : fit > kMaxPrefixSplits ? kMaxPrefixSplits : fit;
+  const size_t parts = static_cast<size_t>(H) * pl->tiles * pl->nsplit * 128;
+  pl->sh_ml_bytes = parts * sizeof(float2);
+  pl->sh_bytes = pl->sh_ml_bytes + parts * D * sizeof(float);
+  pl->ws_bytes = pl->sh_bytes + pl->own.ws_bytes;
+  return NK_OK;
+}
+
+struct SharedMergeArgs {
+  DecodeArgs d;
+  const float2* sh_ml;  // [H][tiles][nsplit][128]
+  const float* sh_o;    // [H][tiles][nsplit][128][D]
+  int tiles, nsplit;
+};
+
+// One CTA per (row, KV head, 32 dims), as merge_kernel, over the row's own
+// splits followed by the prefix's.  Everything before the wait overlaps the
+// decode.  R_real <= 32 query rows, at most kMaxSplits + kMaxPrefixSplits
+// partials each.
+template <int D>
+__global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant__ SharedMergeArgs m) {
+  const DecodeArgs& a = m.d;
+  constexpr int S_MAX = kMaxSplits + kMaxPrefixSplits;
+  __shared__ int s_F[8];
+  __shared__ int s_row[8];
+  __shared__ float sw[32 * S_MAX];
+  const int b = blockIdx.x, h = blockIdx.y, d0 = blockIdx.z * 32, tid = threadIdx.x;
+  const int warp = tid >> 5, lane = tid & 31;
+  const int pages = *a.shared;
+  if (tid < a.B) {
+    const int F = a.frontiers[tid], row = a.table_rows[tid];
+    const bool ok = F >= 0 && F <= a.L * 64 && row >= 0 && row < a.C;
+    const int before = pages_before(a, F, row);
+    s_F[tid] = ok ? F - 64 * before : 0;
+    s_row[tid] = before > 0 ? row : -1;
+  }
+  __syncthreads();
+  int total = 0, maxp = 0, first = -1;
+  for (int bb = a.B - 1; bb >= 0; --bb) {
+    const int np = (s_F[bb] + 63) >> 6;
+    total += np;
+    maxp = max(maxp, np);
+    if (s_row[bb] >= 0) first = s_row[bb];
+  }
+  const int chunk = a.nseg > 0 ? piece_chunk(s_F, a, total, maxp) : wave_chunk(s_F, a.B, total, maxp, a.target);
+  const int own = max(1, (((s_F[b] + 63) >> 6) + chunk - 1) / chunk);
+  const bool part = s_row[b] >= 0;
+  const int per = part ? (pages + m.nsplit - 1) / m.nsplit : 1;
+  const int splits = own + (part ? (pages + per - 1) / per : 0);
+  if (h == 0 && d0 == 0) {  // the row's leading table entries are those the prefix pass read
+    if (pages < 0 && tid == 0) set_status(a.status, NK_STATUS_FRONTIER);
+    if (part && s_row[b] != first) {
+      const int32_t* mine = a.tables + static_cast<int64_t>(s_row[b]) * a.L;
+      const int32_t* read = a.tables + static_cast<int64_t>(first) * a.L;
+      for (int i = tid; i < pages; i += 256)
+        if (mine[i] != read[i]) set_status(a.status, NK_STATUS_PREFIX);
+    }
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int R = a.T * a.G <= 8 ? 8 : a.T * a.G <= 16 ? 16 : 32, R_real = a.T * a.G;
+  const int64_t own0 = (static_cast<int64_t>(b) * a.H + h) * a.target;
+  // partial k of query row qr: (m, l) and the first of its D accumulators
+  auto slot = [&](int qr, int k, const float2*& ml, const float*& o) {
+    if (k < own) {
+      const int64_t i = (own0 + k) * R + qr;
+      ml = a.ws_ml + i;
+      o = a.ws_acc + i * D;
+    } else {
+      const int flat = b * R_real + qr;
+      const int64_t i = ((static_cast<int64_t>(h) * m.tiles + flat / 128) * m.nsplit + (k - own)) * 128 + flat % 128;
+      ml = m.sh_ml + i;
+      o = m.sh_o + i * D;
+    }
+  };
+  for (int qr = warp; qr < R_real; qr += 8) {  // one warp per row, lanes over its partials
+    constexpr int N = S_MAX / 32;
+    float2 v[N];
+    float M = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int k = lane + 32 * u;
+      v[u] = make_float2(-INFINITY, 0.f);
+      if (k < splits) {
+        const float2* ml;
+        const float* o;
+        slot(qr, k, ml, o);
+        v[u] = __ldcg(ml);
+      }
+      M = fmaxf(M, v[u].x);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float L = 0.f;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      v[u].x = M == -INFINITY || !(v[u].y > 0.f) ? 0.f : ex2(v[u].x - M);
+      L += v[u].y * v[u].x;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int k = lane + 32 * u;
+      if (k < splits) sw[qr * S_MAX + k] = v[u].x * inv;
+    }
+    if (lane == 0 && a.lse && d0 == 0)
+      a.lse[(static_cast<int64_t>(b) * a.T + qr / a.G) * a.Hq + h * a.G + qr % a.G] =
+          L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+  }
+  __syncthreads();
+  // item = (query row, 4 dims); four threads take every fourth partial each
+  const int sub = tid & 3;
+  for (int item = tid >> 2; item < R_real * 8; item += 64) {
+    const int qr = item >> 3, d = d0 + (item & 7) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = sub; k < splits; k += 4) {
+      const float w = sw[qr * S_MAX + k];
+      const float2* ml;
+      const float* o;
+      slot(qr, k, ml, o);
+      if (w > 0.f) {  // a partial without keys has no accumulators
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(o + d));
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+      }
+    }
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+      acc.x += __shfl_xor_sync(0xffffffffu, acc.x, off);
+      acc.y += __shfl_xor_sync(0xffffffffu, acc.y, off);
+      acc.z += __shfl_xor_sync(0xffffffffu, acc.z, off);
+      acc.w += __shfl_xor_sync(0xffffffffu, acc.w, off);
+    }
+    if (sub == 0) {
+      __nv_bfloat16* dst = a.out + ((static_cast<int64_t>(b) * a.T + qr / a.G) * a.Hq + h * a.G + qr % a.G) * D + d;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    }
+  }
+}
+
+}  // namespace nk
+
+using namespace nk;
+
+extern "C" int nk_shared_decode_workspace_bytes(const nk_pool* pool, int32_t B, int32_t T, int32_t Hq,
+                                                size_t* bytes) {
+  clear_error();
+  if (!pool || !bytes) return fail(NK_ERR_INVALID_ARG, "null argument");
+  SharedPlan pl;
+  int rc = make_shared_plan(pool, B, T, Hq, &pl);
+  if (rc) return rc;
+  *bytes = pl.ws_bytes;
+  return NK_OK;
+}
+
+extern "C" int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const nk_pool* pool, int32_t layer,
+                                                const int32_t* block_tables, const int32_t* table_rows,
+                                                const int32_t* frontiers, const int32_t* shared_pages,
+                                                int32_t B, int32_t T, float softmax_scale, void* out,
+                                                float* lse, void* workspace, size_t workspace_bytes,
+                                                void* stream) {
+  clear_error();
+  if (!q || !pool || !block_tables || !table_rows || !frontiers || !shared_pages || !out)
+    return fail(NK_ERR_INVALID_ARG, "null argument to nk_paged_shared_decode_attention");
+  if (!std::isfinite(softmax_scale)) return fail(NK_ERR_INVALID_ARG, "softmax_scale is not finite");
+  if (layer < 0 || layer >= pool->desc.num_layers) return fail(NK_ERR_SHAPE, "layer out of range");
+  if (!aligned16(q) || !aligned16(out)) return fail(NK_ERR_ALIGN, "q / out must be 16-byte aligned");
+  SharedPlan pl;
+  int rc = make_shared_plan(pool, B, T, Hq, &pl);
+  if (rc) return rc;
+  if (!workspace || workspace_bytes < pl.ws_bytes)
+    return fail(NK_ERR_WORKSPACE, "workspace needs " + std::to_string(pl.ws_bytes) + " bytes");
+  if (!aligned16(workspace)) return fail(NK_ERR_ALIGN, "workspace must be 16-byte aligned");
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (dev != pool->device)
+    return fail(NK_ERR_INVALID_ARG, "the pool belongs to device " + std::to_string(pool->device) +
+                                        ", the current device is " + std::to_string(dev));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  SharedPrefix sh;
+  sh.pages = shared_pages;
+  sh.frontiers = frontiers;
+  sh.B = B;
+  sh.T = T;
+  PrefillSplit sp{};
+  sp.nsplit = pl.nsplit;
+  sp.tiles = pl.tiles;
+  sp.ws_ml = reinterpret_cast<float2*>(ws);
+  sp.ws_o = reinterpret_cast<float*>(ws + pl.sh_ml_bytes);
+  sp.partial = true;
+  auto pass = pool->desc.profile == NK_BF16 ? prefix_pass_bf16 : prefix_pass_quantized;
+  e = pass(pool, layer, q, block_tables, table_rows, Hq, softmax_scale * kLog2e, sp, sh, s);
+  if (e != cudaSuccess) return cuda_fail(e, "prefix pass launch");
+  SharedMergeArgs m;
+  DecodeArgs& a = m.d;
+  const int np = pool->n_planes;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.tables = block_tables;
+  a.table_rows = table_rows;
+  a.frontiers = frontiers;
+  a.ks = np == 4 ? static_cast<const uint8_t*>(pool->ptrs[layer * np + 2]) : nullptr;
+  a.vs = np == 4 ? static_cast<const uint8_t*>(pool->ptrs[layer * np + 3]) : nullptr;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.ws_ml = reinterpret_cast<float2*>(ws + pl.sh_bytes);
+  a.ws_acc = reinterpret_cast<float*>(ws + pl.sh_bytes + pl.own.ws_ml_bytes);
+  a.status = pool->status;
+  a.softmax_scale = softmax_scale;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.H = pool->desc.num_kv_heads;
+  a.G = Hq / a.H;
+  a.L = pool->L;
+  a.M = pool->M;
+  a.C = pool->desc.max_concurrency;
+  a.target = pl.own.target;
+  a.nseg = pl.own.nseg;
+  a.ctas = pl.own.ctas;
+  a.head_major = pool->desc.order == NK_HEAD_MAJOR;
+  a.shared = shared_pages;
+  e = pl.own.fn(pool, layer, a, pl.own.nqt, dim3(pl.own.ctas, a.H), s);
+  if (e != cudaSuccess) return cuda_fail(e, "decode launch");
+  m.sh_ml = sp.ws_ml;
+  m.sh_o = sp.ws_o;
+  m.tiles = pl.tiles;
+  m.nsplit = pl.nsplit;
+  const int D = pool->desc.head_dim;
+  const dim3 grid(B, a.H, D / 32);
+  e = D == 64    ? launch_pdl(shared_merge_kernel<64>, grid, dim3(256), 0, s, m)
+      : D == 128 ? launch_pdl(shared_merge_kernel<128>, grid, dim3(256), 0, s, m)
+                 : launch_pdl(shared_merge_kernel<256>, grid, dim3(256), 0, s, m);
+  if (e != cudaSuccess) return cuda_fail(e, "merge launch");
+  return NK_OK;
+}

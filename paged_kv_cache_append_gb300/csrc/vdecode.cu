@@ -243,8 +243,9 @@ __global__ void __launch_bounds__(448, 1)
     const int F = a.frontiers[tid], row = a.table_rows[tid];
     const bool ok = F >= 0 && F <= a.L * 64 && row >= 0 && row < a.C && (a.k_new == nullptr || F >= a.T);
     if (!ok && blockIdx.x == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
-    s_F[tid] = ok ? F : 0;
-    s_row[tid] = ok ? row : 0;
+    const int before = pages_before(a, F, row);
+    s_F[tid] = ok ? F - 64 * before : 0;
+    s_row[tid] = ok ? row * a.L + before : 0;  // the row's first table entry
   }
   if (warp == 0) {
     tc::alloc(tslot, 512);
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(448, 1)
   const int nt = (n + PPT - 1) / PPT;                  // key tiles
   const int app_lo = early ? (F - a.T) >> 6 : 0x7fffffff;
   const int R_real = a.T * a.G;
-  const int32_t* trow = a.tables + static_cast<int64_t>(b >= 0 ? s_row[b] : 0) * a.L;
+  const int32_t* trow = a.tables + (b >= 0 ? s_row[b] : 0);
 
   if (b < 0) {
     // no work: only the TMEM allocation is released below
@@ -694,7 +695,7 @@ __global__ void __launch_bounds__(448, 1)
     const int ot = orow / a.G, og = orow % a.G;
     if (ok) {
       // the split's result: final out / lse (one split) or the partial (m, l, acc)
-      const bool final_out = nsplit == 1;
+      const bool final_out = nsplit == 1 && a.shared == nullptr;
       const int64_t part = (static_cast<int64_t>(b) * a.H + h) * a.target + split;
       const float inv = lt > 0.f ? 1.f / lt : 0.f;
 #pragma unroll 1
@@ -1000,8 +1001,9 @@ __global__ void __launch_bounds__(448, 1)
     const int F = a.frontiers[tid], row = a.table_rows[tid];
     const bool ok = F >= 0 && F <= a.L * 64 && row >= 0 && row < a.C && (a.k_new == nullptr || F >= a.T);
     if (!ok && blockIdx.x == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
-    s_F[tid] = ok ? F : 0;
-    s_row[tid] = ok ? row : 0;
+    const int before = pages_before(a, F, row);
+    s_F[tid] = ok ? F - 64 * before : 0;
+    s_row[tid] = ok ? row * a.L + before : 0;  // the row's first table entry
   }
   if (warp == 0) {
     tc::alloc(tslot, 512);
@@ -1025,7 +1027,7 @@ __global__ void __launch_bounds__(448, 1)
   const int s_lo = static_cast<int>(static_cast<int64_t>(blockIdx.x) * nsegs / gridDim.x);
   const int s_hi = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * nsegs / gridDim.x);
   const int R_real = a.T * a.G;
-  auto trow_of = [&](int bb) { return a.tables + static_cast<int64_t>(s_row[bb]) * a.L; };
+  auto trow_of = [&](int bb) { return a.tables + s_row[bb]; };
 
   if (s_hi <= s_lo) {
     // no work: only the TMEM allocation is released below
@@ -1504,7 +1506,7 @@ __global__ void __launch_bounds__(448, 1)
       {
         const float lt = (sL[lane] + sL[32 + lane]) + (sL[64 + lane] + sL[96 + lane]);  // row `lane`
         const int b = g0.b;
-        const bool final_out = g0.ns == 1;
+        const bool final_out = g0.ns == 1 && a.shared == nullptr;
         const int64_t part = (static_cast<int64_t>(b) * a.H + h) * a.target + g0.k;
         const float unlift = KV == KIND_FP8 ? pow2i(-k_run) : 1.f;  // O^T carries 2^k_run
         const float inv_self = lt > 0.f ? unlift / lt : 0.f;
@@ -1573,7 +1575,7 @@ static cudaError_t launch_v(const nk_pool* p, int layer, const DecodeArgs& a, di
     attr = true;
   }
   cudaError_t e = launch_pdl(k, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.shared != nullptr) return e;
   return launch_pdl(merge_kernel<D, 4>, dim3(a.B, a.H, D / 32), dim3(256), 0, s, a);
 }
 
@@ -1588,7 +1590,7 @@ static cudaError_t launch_vt(const nk_pool* p, int layer, const DecodeArgs& a, d
     attr = true;
   }
   cudaError_t e = launch_pdl(k, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.shared != nullptr) return e;
   return launch_pdl(merge_kernel<D, 4>, dim3(a.B, a.H, D / 32), dim3(256), 0, s, a);
 }
 

@@ -22,6 +22,7 @@ NK_OK = 0
 ERRORS = {-1: "NK_ERR_INVALID_ARG", -2: "NK_ERR_SHAPE", -3: "NK_ERR_RANGE",
           -4: "NK_ERR_UNSUPPORTED", -5: "NK_ERR_ALIGN", -6: "NK_ERR_CUDA", -7: "NK_ERR_WORKSPACE"}
 STATUS_PAGE_RANGE, STATUS_FRONTIER, STATUS_TIMEOUT = 1, 2, 4
+STATUS_TOKEN_RANGE, STATUS_PREFIX = 8, 16
 PROFILES = {"bf16": 0, "int8_g64": 1, "fp8_row": 2, "nvfp4_g16": 3, "k8v4": 4}
 POOL_CHECK_BOUNDS = 1
 
@@ -32,7 +33,9 @@ SYMBOLS = ["nk_version", "nk_last_error", "nk_pool_plane_bytes", "nk_pool_capaci
            "nk_paged_decode_attention_noalloc",
            "nk_prefill_workspace_bytes", "nk_paged_prefill_attention",
            "nk_page_copy_columns", "nk_status_read", "nk_host_page_bytes", "nk_page_runs",
-           "nk_pages_to_host", "nk_pages_from_host", "nk_selftest_bounded_wait"]
+           "nk_pages_to_host", "nk_pages_from_host", "nk_selftest_bounded_wait",
+           "nk_shared_decode_workspace_bytes", "nk_paged_shared_decode_attention", "nk_qk_norm_rope",
+           "nk_paged_kv_append_rope", "nk_verify_drafts"]
 
 
 class NkError(RuntimeError):
@@ -47,8 +50,19 @@ class PoolDesc(C.Structure):
                 ("max_concurrency", C.c_int32), ("order", C.c_int32), ("flags", C.c_int32)]
 
 
+class Rows(C.Structure):
+    """nk_rows: element (token n, head h, dim d) at ptr[n * token_stride + h * head_stride + d]."""
+    _fields_ = [("ptr", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class RopeDesc(C.Structure):
+    _fields_ = [("cos_sin", C.c_void_p), ("positions", C.c_int32), ("rotary_dim", C.c_int32),
+                ("layout", C.c_int32), ("eps", C.c_float), ("weight_offset", C.c_float),
+                ("reserved", C.c_int32), ("q_weight", C.c_void_p), ("k_weight", C.c_void_p)]
+
+
 _lib = None
-_P, _I, _F, _S = C.c_void_p, C.c_int32, C.c_float, C.c_size_t
+_P, _I, _F, _S, _L = C.c_void_p, C.c_int32, C.c_float, C.c_size_t, C.c_int64
 
 
 def load(path: str | None = None) -> C.CDLL:
@@ -84,6 +98,14 @@ def load(path: str | None = None) -> C.CDLL:
         "nk_page_copy_columns": (C.c_int, [_P, _I, _I, _I, _P]),
         "nk_status_read": (C.c_int, [C.POINTER(_I), _I, _P]),
         "nk_selftest_bounded_wait": (C.c_int, [_I, _P, _P]),
+        "nk_shared_decode_workspace_bytes": (C.c_int, [_P, _I, _I, _I, C.POINTER(_S)]),
+        "nk_paged_shared_decode_attention": (C.c_int, [_P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _F, _P, _P, _P, _S,
+                                                       _P]),
+        "nk_qk_norm_rope": (C.c_int, [C.POINTER(RopeDesc), _I, C.POINTER(Rows), _I, C.POINTER(Rows), _I, _P, _I,
+                                      C.POINTER(Rows), C.POINTER(Rows), _P]),
+        "nk_paged_kv_append_rope": (C.c_int, [_P, _I, _P, _P, _P, _P, C.POINTER(RopeDesc), C.POINTER(Rows),
+                                              C.POINTER(Rows), C.POINTER(Rows), _I, _P, _I, _I, _P]),
+        "nk_verify_drafts": (C.c_int, [_P, _L, _P, _L, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -205,6 +227,37 @@ def nk_paged_prefill_attention(q, Hq, pool, layer, block_tables, table_rows, pre
                                              workspace_bytes, stream))
 
 
+def nk_shared_decode_workspace_bytes(pool, B, T, Hq) -> int:
+    n = _S()
+    _check(load().nk_shared_decode_workspace_bytes(pool, B, T, Hq, C.byref(n)))
+    return n.value
+
+
+def nk_paged_shared_decode_attention(q, Hq, pool, layer, block_tables, table_rows, frontiers, shared_pages,
+                                     B, T, scale, out, lse, workspace, workspace_bytes, stream):
+    _check(load().nk_paged_shared_decode_attention(q, Hq, pool, layer, block_tables, table_rows, frontiers,
+                                                   shared_pages, B, T, scale, out, lse, workspace,
+                                                   workspace_bytes, stream))
+
+
+def nk_qk_norm_rope(rope, head_dim, q, Hq, k, H, positions, N, q_out, k_out, stream):
+    """rope: RopeDesc; q, k, q_out, k_out: Rows or None."""
+    _check(load().nk_qk_norm_rope(rope, head_dim, q, Hq, k, H, positions, N, q_out, k_out, stream))
+
+
+def nk_paged_kv_append_rope(pool, layer, block_tables, table_rows, write_pos, counts, rope, k, v, q, Hq, q_out,
+                            B, T, stream):
+    """rope: RopeDesc; k, v, q: Rows (q may be None)."""
+    _check(load().nk_paged_kv_append_rope(pool, layer, block_tables, table_rows, write_pos, counts, rope, k, v,
+                                          q, Hq, q_out, B, T, stream))
+
+
+def nk_verify_drafts(target, target_stride, draft, draft_stride, tokens, draft_len, uniforms, frontiers, B, K, V,
+                     accepted, out_tokens, frontiers_out, stream):
+    _check(load().nk_verify_drafts(target, target_stride, draft, draft_stride, tokens, draft_len, uniforms,
+                                   frontiers, B, K, V, accepted, out_tokens, frontiers_out, stream))
+
+
 def nk_page_copy_columns(pool, src, dst, ncols, stream):
     _check(load().nk_page_copy_columns(pool, src, dst, ncols, stream))
 
@@ -229,6 +282,120 @@ def _stream(stream) -> int:
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
+
+
+def _rows(x, heads_dim: int, lead=None) -> Rows:
+    """nk_rows of a bf16 CUDA tensor [N, heads, D] or [B, T, heads, D] with any token and head strides."""
+    import torch
+    if not x.is_cuda or x.dtype != torch.bfloat16:
+        raise ValueError(f"expected a bf16 CUDA tensor, got {x.dtype} on {x.device}")
+    if x.dim() not in (3, 4) or x.shape[-1] != heads_dim or x.stride(-1) != 1:
+        raise ValueError(f"expected [..., heads, {heads_dim}] with a unit last stride, got {tuple(x.shape)}")
+    if x.dim() == 4 and x.shape[0] > 1 and x.shape[1] > 1 and x.stride(0) != x.shape[1] * x.stride(1):
+        raise ValueError("the tokens of [B, T, heads, D] rows must be one stride apart")
+    if lead is not None and x.shape[:-2] != lead:
+        raise ValueError(f"expected leading sizes {tuple(lead)}, got {tuple(x.shape[:-2])}")
+    token = x.stride(-3) if x.shape[-3] > 1 or x.dim() == 3 else x.stride(0)
+    tokens = x.shape[0] if x.dim() == 3 else x.shape[0] * x.shape[1]
+    # the stride of a dimension of size 1 says nothing
+    return Rows(x.data_ptr(), token if tokens > 1 else 0, x.stride(-2) if x.shape[-2] > 1 else 0)
+
+
+def _cuda(x, dtype, shape, name, device):
+    """Checks a contiguous tensor argument of a call on `device`."""
+    if x.device != device or x.dtype != dtype or tuple(x.shape) != tuple(shape) or not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {device}, got "
+                         f"{x.dtype} {tuple(x.shape)} on {x.device}")
+
+
+class Rope:
+    """Norm and rotation of head rows (nk.h, nk_rope).
+
+    ``cos_sin`` is a contiguous fp32 CUDA tensor [positions, rotary_dim] whose
+    row is the cosines of the rotary_dim / 2 angles, then their sines; the
+    weights are bf16 [D] or None (no norm).  Keeps its tensors alive.
+    """
+
+    def __init__(self, cos_sin, rotary_dim: int, interleaved: bool = False, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, weight_offset: float = 0.0):
+        import torch
+        if cos_sin.dtype != torch.float32 or not cos_sin.is_cuda or not cos_sin.is_contiguous() \
+                or cos_sin.dim() != 2 or cos_sin.shape[1] != rotary_dim:
+            raise ValueError(f"cos_sin must be a contiguous fp32 CUDA tensor [positions, {rotary_dim}]")
+        for w in (q_weight, k_weight):
+            if w is not None and (w.dtype != torch.bfloat16 or w.device != cos_sin.device or w.dim() != 1
+                                  or not w.is_contiguous()):
+                raise ValueError("norm weights must be contiguous bf16 vectors on the table's device")
+        self.cos_sin, self.q_weight, self.k_weight = cos_sin, q_weight, k_weight
+        self.device = cos_sin.device
+        self.desc = RopeDesc(_ptr(cos_sin), cos_sin.shape[0], rotary_dim, int(interleaved), eps, weight_offset, 0,
+                             _ptr(q_weight), _ptr(k_weight))
+
+    def check(self, D: int) -> None:
+        for w in (self.q_weight, self.k_weight):
+            if w is not None and w.numel() != D:
+                raise ValueError(f"norm weights have {w.numel()} elements, the heads {D}")
+
+
+def qk_norm_rope(q, k, positions, rope: Rope, q_out=None, k_out=None, stream=None):
+    """Per-head norm and rotation of q [N, Hq, D] and k [N, H, D] (bf16, any
+    token and head strides) at ``positions`` int32 [N]; returns (q_out, k_out),
+    new contiguous tensors unless given (q_out may be q itself, k_out k)."""
+    import torch
+    D = q.shape[-1]
+    lead = q.shape[:-2]
+    rope.check(D)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("outputs must have the shapes of their inputs")
+    rq, rk, oq, ok = (_rows(x, D, lead) for x in (q, k, q_out, k_out))
+    if any(x.device != rope.device for x in (q, k, q_out, k_out)):
+        raise ValueError("all operands must be on the device of the rotation table")
+    _cuda(positions, torch.int32, lead, "positions", q.device)
+    with torch.cuda.device(q.device):
+        nk_qk_norm_rope(rope.desc, D, rq, q.shape[-2], rk, k.shape[-2], positions.data_ptr(), positions.numel(),
+                        oq, ok, _stream(stream))
+    return q_out, k_out
+
+
+def verify_drafts(target, tokens, uniforms, draft=None, draft_len=None, frontiers=None, stream=None):
+    """Verification of drafted tokens (nk.h, nk_verify_drafts).
+
+    target fp32 [B, K+1, V] and draft fp32 [B, K, V] or None (their rows may be
+    padded: any row stride, contiguous batches of rows), tokens int32 [B, K],
+    uniforms fp32 [B, K+1], draft_len and frontiers int32 [B] or None.
+    Returns (accepted [B], tokens [B, K+1], frontiers [B] or None), int32.
+    """
+    import torch
+    B, K1, V = target.shape
+    K, dev = K1 - 1, target.device
+    strides = []
+    for x, n, name in ((target, K1, "target"), (draft, K, "draft")):
+        strides.append(V)
+        if x is None:
+            continue
+        if x.device != dev or not x.is_cuda or x.dtype != torch.float32 or tuple(x.shape) != (B, n, V):
+            raise ValueError(f"{name}: expected a float32 CUDA tensor {(B, n, V)}, got {x.dtype} {tuple(x.shape)}")
+        if B * n > 1:   # the stride of a dimension of size 1 says nothing
+            strides[-1] = x.stride(1) if n > 1 else x.stride(0)
+        if n and ((V > 1 and x.stride(2) != 1) or strides[-1] < V
+                  or (B > 1 and n > 1 and x.stride(0) != n * x.stride(1))):
+            raise ValueError(f"{name}: rows must be contiguous and one stride apart")
+    _cuda(tokens, torch.int32, (B, K), "tokens", dev)
+    _cuda(uniforms, torch.float32, (B, K1), "uniforms", dev)
+    for x, name in ((draft_len, "draft_len"), (frontiers, "frontiers")):
+        if x is not None:
+            _cuda(x, torch.int32, (B,), name, dev)
+    accepted = torch.empty(B, dtype=torch.int32, device=dev)
+    out = torch.empty((B, K1), dtype=torch.int32, device=dev)
+    after = torch.empty_like(frontiers) if frontiers is not None else None
+    with torch.cuda.device(dev):
+        nk_verify_drafts(target.data_ptr(), strides[0], _ptr(draft) if K else None, strides[1],
+                         _ptr(tokens) if K else None,
+                         _ptr(draft_len), uniforms.data_ptr(), _ptr(frontiers), B, K, V, accepted.data_ptr(),
+                         out.data_ptr(), _ptr(after), _stream(stream))
+    return accepted, out, after
 
 
 class Pool:
@@ -352,3 +519,74 @@ class Pool:
 
     def copy_columns(self, src, dst, ncols, stream=None):
         nk_page_copy_columns(self.handle, src, dst, ncols, _stream(stream))
+
+    def append_rope(self, layer, tables, table_rows, write_pos, k, v, rope: Rope, q=None, q_out=None, counts=None,
+                    stream=None):
+        """Appends k, v [B, T, H, D] with the norm and rotation of k on the
+        way, and returns q_out [B, T, Hq, D], the queries normed and rotated in
+        the same launch (None without q).  k, v, q: bf16, any token and head
+        strides, one token stride apart across rows; rows of q_out past a
+        row's count are not written."""
+        import torch
+        B, T = k.shape[0], k.shape[1]
+        dev = self.planes[0][0].device
+        rope.check(self.D)
+        if k.dim() != 4 or k.shape[2] != self.H or v.shape != k.shape:
+            raise ValueError(f"k and v must be [B, T, {self.H}, {self.D}]")
+        rk, rv = _rows(k, self.D), _rows(v, self.D)
+        rq = None
+        if q is not None:
+            rq = _rows(q, self.D, k.shape[:2])
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            _cuda(q_out, torch.bfloat16, q.shape, "q_out", dev)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        if any(x is not None and x.device != dev for x in (k, v, q, rope.cos_sin)):
+            raise ValueError("all operands must be on the pool's device")
+        _cuda(tables, torch.int32, (self.C, self.L), "tables", dev)
+        for x, name in ((table_rows, "table_rows"), (write_pos, "write_pos"), (counts, "counts")):
+            if x is not None:
+                _cuda(x, torch.int32, (B,), name, dev)
+        with torch.cuda.device(dev):
+            nk_paged_kv_append_rope(self.handle, layer, _ptr(tables), _ptr(table_rows), _ptr(write_pos),
+                                    _ptr(counts), rope.desc, rk, rv, rq, 0 if q is None else q.shape[2],
+                                    _ptr(q_out), B, T, _stream(stream))
+        return q_out
+
+    def shared_workspace(self, B, T, Hq):
+        """A workspace for ``shared_decode`` (one per stream or captured graph that may overlap others)."""
+        import torch
+        dev = self.planes[0][0].device
+        with torch.cuda.device(dev):
+            n = nk_shared_decode_workspace_bytes(self.handle, B, T, Hq)
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+
+    def shared_decode(self, layer, q, tables, table_rows, frontiers, shared_pages, scale, out=None, lse=None,
+                      workspace=None, stream=None):
+        """``decode`` of a batch whose rows share their first ``shared_pages``
+        (int32 device tensor of one value) pages, attended once for all rows.
+        Without ``workspace`` one is allocated for this call."""
+        import torch
+        B, T, Hq, D = q.shape
+        dev = self.planes[0][0].device
+        if D != self.D or not q.is_contiguous() or q.dtype != torch.bfloat16 or q.device != dev:
+            raise ValueError(f"q must be a contiguous bf16 tensor [B, T, Hq, {self.D}] on {dev}")
+        _cuda(tables, torch.int32, (self.C, self.L), "tables", dev)
+        _cuda(table_rows, torch.int32, (B,), "table_rows", dev)
+        _cuda(frontiers, torch.int32, (B,), "frontiers", dev)
+        if shared_pages.device != dev or shared_pages.dtype != torch.int32 or shared_pages.numel() != 1:
+            raise ValueError("shared_pages must be one int32 value on the pool's device")
+        out = torch.empty_like(q) if out is None else out
+        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev) if lse is None else lse
+        _cuda(out, torch.bfloat16, q.shape, "out", dev)
+        _cuda(lse, torch.float32, (B, T, Hq), "lse", dev)
+        ws = workspace if workspace is not None else self.shared_workspace(B, T, Hq)
+        with torch.cuda.device(dev):
+            s = _stream(stream)
+            if workspace is None and stream is not None:
+                ws.record_stream(stream)
+            nk_paged_shared_decode_attention(_ptr(q), Hq, self.handle, layer, _ptr(tables), _ptr(table_rows),
+                                             _ptr(frontiers), _ptr(shared_pages), B, T, float(scale), _ptr(out),
+                                             _ptr(lse), _ptr(ws), ws.numel(), s)
+        return out, lse
