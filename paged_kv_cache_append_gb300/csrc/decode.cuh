@@ -291,8 +291,11 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
   // at once and only the consumers wait, before they read q, k or v and before
   // any global write.  The plain decode waits here (a separate append may have
   // just written its pages).
+  // In the shared-prefix attention the kernel before is the prefix pass, which
+  // waited for everything before itself and shares nothing with this one: it
+  // is waited for at the end alone, for the merge behind both.
   const bool early = a.k_new != nullptr;
-  if (!early) griddep_wait();
+  if (!early && a.shared == nullptr) griddep_wait();
   griddep_launch_dependents();
 
   // ---- per-row lengths, loaded once in parallel ------------------------------
@@ -1094,6 +1097,7 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
       a.ws_ml[part * R + tid] = make_float2(row_M[tid], row_L[tid]);
     }
   }
+  if (a.shared != nullptr) griddep_wait();
 }
 
 // ---- log-sum-exp merge of the splits (separate launch) ----------------------------

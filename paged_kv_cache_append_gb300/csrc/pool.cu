@@ -8,6 +8,7 @@
 // section).
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -97,8 +98,15 @@ int device_sm_count(int device) {
 static __device__ int g_status_word;
 
 int* status_word() {
+  static std::atomic<int*> cache[64];
+  int device = -1;
+  if (cudaGetDevice(&device) != cudaSuccess) return nullptr;
+  const bool keep = device >= 0 && device < 64;
+  if (keep)
+    if (int* p = cache[device].load(std::memory_order_relaxed)) return p;
   void* p = nullptr;
   if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess) return nullptr;
+  if (keep) cache[device].store(static_cast<int*>(p), std::memory_order_relaxed);
   return static_cast<int*>(p);
 }
 

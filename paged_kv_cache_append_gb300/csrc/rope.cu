@@ -4,13 +4,23 @@
 //
 // Both are one pass over the data, bound by HBM for long inputs and by the
 // launch and two dependent loads for a decode step.  A warp holds 32 / (D/8)
-// rows (rope.cuh).  Units of work are (token, group of HPU heads of one
-// operand); a lane loads the position's angles once for the HPU heads.  The
-// units are laid out operand by operand (all q, then k, then v), each operand
-// padded to whole warps, so a warp never mixes operands.
+// rows (rope.cuh).  Units of work are (token, group of heads of one operand); a
+// lane reads the position's angles once for the heads of its unit.  The units
+// are laid out operand by operand (all of q, then k and v), each operand padded
+// to whole warps, so a warp never mixes operands.
 #include <cmath>
 
 #include "rope.cuh"
+
+#ifndef NK_WANT
+#define NK_WANT 16
+#endif
+#ifndef NK_RING
+#define NK_RING 4
+#endif
+#ifndef NK_MINB
+#define NK_MINB 8
+#endif
 
 namespace nk {
 
@@ -45,96 +55,151 @@ static RowsIn rows_in(const nk_rows* r) {
            : RowsIn{nullptr, 0, 0};
 }
 
+constexpr int kRopeThreads = 128;
+constexpr int kRing = NK_RING;  // rows of a lane in flight in a long unit
+
+// Work of one operand: units of `hpu` heads of one token, padded to whole
+// warps; a warp of rpw rows takes rpw units.
+struct Work {
+  int heads, hpu;
+  uint32_t groups, units;
+};
+
+// The unit of a group of LPR lanes; not live past the last one of its operand
+// (padding lanes stay in the warp for its shuffles).
+struct Unit {
+  int token, head0, heads;  // heads [head0, head0 + heads)
+  bool live;
+};
+
+__device__ __forceinline__ Unit unit_of(uint32_t u, uint32_t tokens, const Work& w) {
+  Unit x;
+  const uint32_t t = w.groups == 1 ? u : u / w.groups;
+  x.live = t < tokens;
+  x.token = x.live ? static_cast<int>(t) : 0;
+  x.head0 = static_cast<int>(u - t * w.groups) * w.hpu;
+  x.heads = min(w.hpu, w.heads - x.head0);
+  return x;
+}
+
+__device__ __forceinline__ void copy_async16(uint32_t smem, const void* p) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(p) : "memory");
+}
+
+// Rows 0 .. n - 1 of this lane (n alike in the warp): `src(i)` is the address of
+// its 16 bytes or nullptr, `begin()` runs while the first are on their way, then
+// `body(i, bytes)` for every row.  RING: a private ring of 16-byte slots in
+// shared memory, filled by cp.async kRing rows ahead (the bytes in flight cost
+// no registers, and a lane reads only what it copied, so no barrier is needed).
+// Otherwise, for up to two rows, plain loads.
+template <bool RING, class Src, class Begin, class Body>
+__device__ __forceinline__ void for_rows(uint4* slots, int n, Src src, Begin begin, Body body) {
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  if constexpr (RING) {
+    const uint32_t at = smem_u32(slots);
+    auto fetch = [&](int i) {
+      const __nv_bfloat16* p = i < n ? src(i) : nullptr;
+      if (p) copy_async16(at + (i % kRing) * (kRopeThreads * 16), p);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) fetch(i);
+    begin();
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+      body(i, src(i) ? slots[(i % kRing) * kRopeThreads] : zero);
+      fetch(i + kRing);
+    }
+  } else {
+    uint4 v[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __nv_bfloat16* p = i < n ? src(i) : nullptr;
+      v[i] = p ? *reinterpret_cast<const uint4*>(p) : zero;
+    }
+    begin();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (i < n) body(i, v[i]);
+  }
+}
+
 struct NormRopeArgs {
-  RowsIn in[2];           // q, k
-  RowsIn out[2];          // written
+  RowsIn in[2];   // q, k
+  RowsIn out[2];  // written
   const __nv_bfloat16* w[2];
   const int32_t* positions;
-  int heads[2], groups[2];
-  int64_t units[2];       // padded to whole warps
+  Work work[2];
   int N;
   int* status;
   RopeArgs rp;
 };
 
-// Which unit a group of LPR lanes takes: returns false past the last unit of
-// its operand (padding lanes stay in the warp for its shuffles).
-struct Unit {
-  int token, head0;
-  bool live;
-};
-
-template <int HPU>
-__device__ __forceinline__ Unit unit_of(int64_t u, int tokens, int groups) {
-  Unit x;
-  const int64_t t = u / groups;
-  x.live = t < tokens;
-  x.token = x.live ? static_cast<int>(t) : 0;
-  x.head0 = static_cast<int>(u - t * groups) * HPU;
-  return x;
-}
-
-template <int D, int HPU>
-__global__ void __launch_bounds__(128) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+template <int D, bool RING>
+__global__ void __launch_bounds__(kRopeThreads, RING ? NK_MINB : 1) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
+  __shared__ uint4 ring[RING ? kRing * kRopeThreads : 1];
   griddep_wait();  // launched with programmatic stream serialization
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, l = lane % LPR;
-  int64_t u = (static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5)) * RPW;  // the warp's first unit
-  const int op = u >= a.units[0];
-  if (op) u -= a.units[0];
-  if (u >= a.units[op]) return;
-  const Unit x = unit_of<HPU>(u + lane / LPR, a.N, a.groups[op]);
-  const int pos = x.live ? a.positions[x.token] : 0;
-  const bool ok = x.live && pos >= 0 && pos < a.rp.positions;
-  if (x.live && !ok && l == 0) set_status(a.status, NK_STATUS_FRONTIER);
+  uint32_t u = (blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5)) * RPW;  // the warp's first unit
+  const int op = u >= a.work[0].units;
+  if (op) u -= a.work[0].units;
+  if (u >= a.work[op].units) return;
+  const Unit x = unit_of(u + lane / LPR, a.N, a.work[op]);
   const RowsIn in = a.in[op], out = a.out[op];
-  const int heads = a.heads[op];
-  const int64_t base = x.token * in.token_stride + x.head0 * in.head_stride + 8 * l;
-  uint4 raw[HPU];
-#pragma unroll
-  for (int i = 0; i < HPU; ++i)
-    raw[i] = ok && x.head0 + i < heads ? *reinterpret_cast<const uint4*>(in.ptr + base + i * in.head_stride)
-                                       : make_uint4(0u, 0u, 0u, 0u);
-  Angles ang;
-  load_angles(a.rp, ok ? pos : 0, l, ang);
-  const int src = partner_lane(a.rp, lane, l);
-  Weights w;
-  load_weights(a.rp, a.w[op], lane, l, src, w);
+  const __nv_bfloat16* src = in.ptr + x.token * in.token_stride + x.head0 * in.head_stride + 8 * l;
   __nv_bfloat16* dst = const_cast<__nv_bfloat16*>(out.ptr) + x.token * out.token_stride + x.head0 * out.head_stride + 8 * l;
-#pragma unroll
-  for (int i = 0; i < HPU; ++i) {
-    float y[8];
-    norm_rotate<LPR>(raw[i], a.rp, ang, w, src, y);
-    if (ok && x.head0 + i < heads) *reinterpret_cast<uint4*>(dst + i * out.head_stride) = pack8_bf16(y);
-  }
+  Turn t;
+  bool ok = false;
+  for_rows<RING>(
+      ring + threadIdx.x, a.work[op].hpu,
+      [&](int i) { return x.live && i < x.heads ? src + i * in.head_stride : nullptr; },
+      [&] {
+        const int pos = x.live ? a.positions[x.token] : 0;
+        ok = x.live && pos >= 0 && pos < a.rp.positions;
+        if (x.live && !ok && l == 0) set_status(a.status, NK_STATUS_FRONTIER);
+        load_turn<LPR>(a.rp, a.w[op], ok ? pos : 0, lane, l, t);
+      },
+      [&](int i, const uint4& raw) {
+        F2 y[4];
+        norm_rotate<LPR>(raw, a.rp, t, y);
+        if (ok && i < x.heads) *reinterpret_cast<uint4*>(dst + i * out.head_stride) = pack8_bf16(y);
+      });
 }
 
-// Heads per unit: 4 once the launch has several waves of units (the angles of
-// a position are then read once for 4 heads and a lane keeps four 16-byte
-// loads in flight); 1 below, where spreading the rows over the SMs counts.
-static int heads_per_unit(int64_t rows, int lpr, int sms) { return rows * lpr >= int64_t(sms) * 8192 ? 4 : 1; }
-
-static int64_t padded(int64_t units, int rpw) { return (units + rpw - 1) / rpw * rpw; }
+// Heads per unit.  A unit reads its position's angles and weights once, so
+// long inputs take all heads of an operand in one unit; below that the heads
+// are spread over more units until the launch has about `want` warps.
+static void plan_work(Work* w, int heads, int64_t tokens, int rpw, int64_t want) {
+  w->heads = heads;
+  w->hpu = heads > 0 ? heads : 1;
+  auto units = [&] { return tokens * ((heads + w->hpu - 1) / w->hpu); };
+  while (w->hpu > 1 && units() / rpw < want) w->hpu = w->hpu > 8 ? 8 : w->hpu > 4 ? 4 : 1;
+  w->groups = heads > 0 ? (heads + w->hpu - 1) / w->hpu : 1;
+  w->units = static_cast<uint32_t>(heads > 0 ? (units() + rpw - 1) / rpw * rpw : 0);
+}
 
 template <int D>
 static cudaError_t launch_norm_rope(NormRopeArgs a, int sms, cudaStream_t s) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  const int hpu = heads_per_unit(static_cast<int64_t>(a.N) * (a.heads[0] + a.heads[1]), LPR, sms);
+  constexpr int RPW = 32 / (D / 8);
+  uint32_t warps = 0;
+  bool ring = false;
   for (int i = 0; i < 2; ++i) {
-    a.groups[i] = (a.heads[i] + hpu - 1) / hpu;
-    a.units[i] = padded(static_cast<int64_t>(a.N) * a.groups[i], RPW);
+    plan_work(&a.work[i], a.work[i].heads, a.N, RPW, int64_t(NK_WANT) * sms);
+    warps += a.work[i].units / RPW;
+    ring = ring || a.work[i].hpu > 1;
   }
-  const int64_t warps = (a.units[0] + a.units[1]) / RPW;
-  const dim3 grid(static_cast<unsigned>((warps + 3) / 4));
-  return hpu == 4 ? launch_pdl(norm_rope_kernel<D, 4>, grid, dim3(128), 0, s, a)
-                  : launch_pdl(norm_rope_kernel<D, 1>, grid, dim3(128), 0, s, a);
+  const dim3 grid((warps + 3) / 4);
+  return ring ? launch_pdl(norm_rope_kernel<D, true>, grid, dim3(kRopeThreads), 0, s, a)
+              : launch_pdl(norm_rope_kernel<D, false>, grid, dim3(kRopeThreads), 0, s, a);
 }
 
 // ---- append with the rotation on the way ------------------------------------
 
 struct AppendRopeArgs {
-  RowsIn in[3];  // q (may be absent), k, v; token index b * T + t
+  RowsIn q, k, v;  // q may be absent; token index b * T + t
   __nv_bfloat16* q_out;
   const __nv_bfloat16* w[2];  // q, k norm weights
   const int32_t* tables;
@@ -143,106 +208,109 @@ struct AppendRopeArgs {
   const int32_t* counts;
   uint8_t *kc, *vc, *ks, *vs;
   int* status;
-  int heads[3], groups[3];
-  int64_t units[3];
+  Work work[2];  // q heads; KV heads (a unit's keys, then its values)
   int B, T, L, M, C, head_major;
   RopeArgs rp;
 };
 
-template <int KK, int KV, int D, int HPU>
-__global__ void __launch_bounds__(128) append_rope_kernel(const __grid_constant__ AppendRopeArgs a) {
+template <int KK, int KV, int D, bool RING>
+__global__ void __launch_bounds__(kRopeThreads, RING ? NK_MINB : 1)
+    append_rope_kernel(const __grid_constant__ AppendRopeArgs a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
+  __shared__ uint4 ring[RING ? kRing * kRopeThreads : 1];
   griddep_wait();  // launched with programmatic stream serialization
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, l = lane % LPR;
-  int64_t u = (static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5)) * RPW;
-  int op = 0;
-  while (op < 3 && u >= a.units[op]) u -= a.units[op++];
-  if (op == 3) return;
-  const Unit x = unit_of<HPU>(u + lane / LPR, a.B * a.T, a.groups[op]);
+  uint32_t u = (blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5)) * RPW;
+  const int op = u >= a.work[0].units;
+  if (op) u -= a.work[0].units;
+  if (u >= a.work[op].units) return;
+  const Unit x = unit_of(u + lane / LPR, a.B * a.T, a.work[op]);
   const int b = x.token / a.T, t = x.token - b * a.T;
-  const int H = a.heads[1];
   bool ok = x.live && t < (a.counts ? a.counts[b] : a.T);
+  const int hpu = a.work[op].hpu;
+  Turn turn;
   int row = 0, pos = 0;
-  if (ok) {
-    row = a.table_rows[b];
-    pos = a.write_pos[b] + t;
-    // rows and positions out of range are skipped, never written
-    if (row < 0 || row >= a.C || pos < 0 || pos >= a.L * 64 || pos >= a.rp.positions) {
-      if (l == 0) set_status(a.status, NK_STATUS_FRONTIER);
-      ok = false;
+  auto begin = [&] {
+    const bool read = ok;
+    if (ok) {
+      row = a.table_rows[b];
+      pos = a.write_pos[b] + t;
+      // rows and positions out of range are skipped, never written
+      ok = row >= 0 && row < a.C && pos >= 0 && pos < a.L * 64 && pos < a.rp.positions;
     }
-  }
-  const RowsIn in = a.in[op];
-  const int heads = a.heads[op];
-  const int64_t base = x.token * in.token_stride + x.head0 * in.head_stride + 8 * l;
-  uint4 raw[HPU];
-#pragma unroll
-  for (int i = 0; i < HPU; ++i)
-    raw[i] = ok && x.head0 + i < heads ? *reinterpret_cast<const uint4*>(in.ptr + base + i * in.head_stride)
-                                       : make_uint4(0u, 0u, 0u, 0u);
-  int64_t tile0 = 0;  // first plane row of the token for head 0, and the heads' distance
-  int64_t pitch = 0;
-  if (op > 0 && ok) {
-    const int g = a.tables[static_cast<int64_t>(row) * a.L + (pos >> 6)];
-    if (g < 0 || g >= a.M) {
-      if (l == 0) set_status(a.status, NK_STATUS_PAGE_RANGE);
-      ok = false;
-    } else {
-      tile0 = tile_row(g, 0, H, a.M, a.head_major) + (pos & 63);
-      pitch = a.head_major ? static_cast<int64_t>(a.M) * 64 : 64;
-    }
-  }
-  if (op == 2) {  // values: the codec alone
-#pragma unroll
-    for (int i = 0; i < HPU; ++i) {
-      const bool live = ok && x.head0 + i < heads;
-      const int64_t r = tile0 + (x.head0 + i) * pitch;
-      if constexpr (KV == KIND_BF16) {  // the bits unchanged
-        if (live) *reinterpret_cast<uint4*>(a.vc + r * (2 * D) + 16 * l) = raw[i];
-      } else {
-        float y[8];
-        unpack8(raw[i], y);
-        encode8<KV, D>(y, a.vc + r * code_row_bytes<KV>(D), a.vs + r * scale_row_bytes<KV>(D), l, live);
-      }
-    }
+    if (read && !ok && l == 0) set_status(a.status, NK_STATUS_FRONTIER);
+    load_turn<LPR>(a.rp, a.w[op], ok ? pos : 0, lane, l, turn);
+  };
+  if (op == 0) {
+    const __nv_bfloat16* src = a.q.ptr + x.token * a.q.token_stride + x.head0 * a.q.head_stride + 8 * l;
+    __nv_bfloat16* dst = a.q_out + (static_cast<int64_t>(x.token) * a.work[0].heads + x.head0) * D + 8 * l;
+    const bool read = ok;
+    for_rows<RING>(
+        ring + threadIdx.x, hpu, [&](int i) { return read && i < x.heads ? src + i * a.q.head_stride : nullptr; },
+        begin,
+        [&](int i, const uint4& raw) {
+          F2 y[4];
+          norm_rotate<LPR>(raw, a.rp, turn, y);
+          if (ok && i < x.heads) *reinterpret_cast<uint4*>(dst + i * D) = pack8_bf16(y);
+        });
     return;
   }
-  Angles ang;
-  load_angles(a.rp, ok ? pos : 0, l, ang);
-  const int src = partner_lane(a.rp, lane, l);
-  Weights w;
-  load_weights(a.rp, a.w[op], lane, l, src, w);
-#pragma unroll
-  for (int i = 0; i < HPU; ++i) {
-    const bool live = ok && x.head0 + i < heads;
-    float y[8];
-    norm_rotate<LPR>(raw[i], a.rp, ang, w, src, y);
-    if (op == 0) {
-      if (live)
-        *reinterpret_cast<uint4*>(a.q_out + (static_cast<int64_t>(x.token) * heads + x.head0 + i) * D + 8 * l) =
-            pack8_bf16(y);
-    } else {
-      const int64_t r = tile0 + (x.head0 + i) * pitch;
-      encode8<KK, D>(y, a.kc + r * code_row_bytes<KK>(D), a.ks + r * scale_row_bytes<KK>(D), l, live);
-    }
-  }
+  const __nv_bfloat16* ksrc = a.k.ptr + x.token * a.k.token_stride + x.head0 * a.k.head_stride + 8 * l;
+  const __nv_bfloat16* vsrc = a.v.ptr + x.token * a.v.token_stride + x.head0 * a.v.head_stride + 8 * l;
+  int64_t tile0 = 0, pitch = 0;  // plane row of the token for the unit's first head, and the heads' distance
+  const bool read = ok;
+  for_rows<RING>(
+      ring + threadIdx.x, 2 * hpu,
+      [&](int i) -> const __nv_bfloat16* {
+        const int h = i < hpu ? i : i - hpu;
+        if (!read || h >= x.heads) return nullptr;
+        return i < hpu ? ksrc + h * a.k.head_stride : vsrc + h * a.v.head_stride;
+      },
+      [&] {
+        begin();
+        if (!ok) return;
+        const int g = a.tables[static_cast<int64_t>(row) * a.L + (pos >> 6)];
+        if (g < 0 || g >= a.M) {
+          if (l == 0) set_status(a.status, NK_STATUS_PAGE_RANGE);
+          ok = false;
+          return;
+        }
+        tile0 = tile_row(g, x.head0, a.work[1].heads, a.M, a.head_major) + (pos & 63);
+        pitch = a.head_major ? static_cast<int64_t>(a.M) * 64 : 64;
+      },
+      [&](int i, const uint4& raw) {
+        F2 y[4];
+        if (i < hpu) {
+          const int64_t r = tile0 + i * pitch;
+          norm_rotate<LPR>(raw, a.rp, turn, y);
+          encode8<KK, D>(y, a.kc + r * code_row_bytes<KK>(D), a.ks + r * scale_row_bytes<KK>(D), l, ok && i < x.heads);
+        } else {  // values: the codec alone
+          const bool live = ok && i - hpu < x.heads;
+          const int64_t r = tile0 + (i - hpu) * pitch;
+          if constexpr (KV == KIND_BF16) {  // the bits unchanged
+            if (live) *reinterpret_cast<uint4*>(a.vc + r * (2 * D) + 16 * l) = raw;
+          } else {
+            unpack8(raw, y);
+            encode8<KV, D>(y, a.vc + r * code_row_bytes<KV>(D), a.vs + r * scale_row_bytes<KV>(D), l, live);
+          }
+        }
+      });
 }
 
 template <int KK, int KV, int D>
 static cudaError_t launch_append_rope(AppendRopeArgs a, int sms, cudaStream_t s) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  const int64_t n = static_cast<int64_t>(a.B) * a.T;
-  const int hpu = heads_per_unit(n * (a.heads[0] + a.heads[1] + a.heads[2]), LPR, sms);
-  int64_t warps = 0;
-  for (int i = 0; i < 3; ++i) {
-    a.groups[i] = (a.heads[i] + hpu - 1) / hpu;
-    a.units[i] = padded(n * a.groups[i], RPW);
-    warps += a.units[i] / RPW;
+  constexpr int RPW = 32 / (D / 8);
+  uint32_t warps = 0;
+  bool ring = false;
+  for (int i = 0; i < 2; ++i) {
+    plan_work(&a.work[i], a.work[i].heads, static_cast<int64_t>(a.B) * a.T, RPW, int64_t(NK_WANT) * sms);
+    warps += a.work[i].units / RPW;
+    ring = ring || a.work[i].hpu > 1;
   }
-  const dim3 grid(static_cast<unsigned>((warps + 3) / 4));
-  return hpu == 4 ? launch_pdl(append_rope_kernel<KK, KV, D, 4>, grid, dim3(128), 0, s, a)
-                  : launch_pdl(append_rope_kernel<KK, KV, D, 1>, grid, dim3(128), 0, s, a);
+  const dim3 grid((warps + 3) / 4);
+  return ring ? launch_pdl(append_rope_kernel<KK, KV, D, true>, grid, dim3(kRopeThreads), 0, s, a)
+              : launch_pdl(append_rope_kernel<KK, KV, D, false>, grid, dim3(kRopeThreads), 0, s, a);
 }
 
 template <int KK, int KV>
@@ -283,8 +351,8 @@ extern "C" int nk_qk_norm_rope(const nk_rope* rope, int32_t head_dim, const nk_r
   a.w[0] = static_cast<const __nv_bfloat16*>(rope->q_weight);
   a.w[1] = static_cast<const __nv_bfloat16*>(rope->k_weight);
   a.positions = positions;
-  a.heads[0] = q ? Hq : 0;
-  a.heads[1] = k ? H : 0;
+  a.work[0].heads = q ? Hq : 0;
+  a.work[1].heads = k ? H : 0;
   a.N = N;
   a.status = status_word();
   int dev = 0;
@@ -328,9 +396,9 @@ extern "C" int nk_paged_kv_append_rope(nk_pool* pool, int32_t layer, const int32
     return fail(NK_ERR_INVALID_ARG, "the pool belongs to device " + std::to_string(pool->device) +
                                         ", the current device is " + std::to_string(dev));
   const int np = pool->n_planes;
-  a.in[0] = rows_in(q);
-  a.in[1] = rows_in(k);
-  a.in[2] = rows_in(v);
+  a.q = rows_in(q);
+  a.k = rows_in(k);
+  a.v = rows_in(v);
   a.q_out = static_cast<__nv_bfloat16*>(q_out);
   a.w[0] = static_cast<const __nv_bfloat16*>(rope->q_weight);
   a.w[1] = static_cast<const __nv_bfloat16*>(rope->k_weight);
@@ -343,8 +411,8 @@ extern "C" int nk_paged_kv_append_rope(nk_pool* pool, int32_t layer, const int32
   a.ks = np == 4 ? static_cast<uint8_t*>(pool->ptrs[layer * np + 2]) : nullptr;
   a.vs = np == 4 ? static_cast<uint8_t*>(pool->ptrs[layer * np + 3]) : nullptr;
   a.status = pool->status;
-  a.heads[0] = q ? Hq : 0;
-  a.heads[1] = a.heads[2] = H;
+  a.work[0].heads = q ? Hq : 0;
+  a.work[1].heads = H;
   a.B = B;
   a.T = T;
   a.L = pool->L;

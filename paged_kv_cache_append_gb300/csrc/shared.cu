@@ -56,18 +56,23 @@ struct SharedMergeArgs {
   int tiles, nsplit;
 };
 
-// One CTA per (row, KV head, 32 dims), as merge_kernel, over the row's own
-// splits followed by the prefix's.  Everything before the wait overlaps the
-// decode.  R_real <= 32 query rows, at most kMaxSplits + kMaxPrefixSplits
-// partials each.
+constexpr int kMergeRows = 8;  // query rows of one merge CTA
+
+// One CTA per (row, KV head, 8 query rows, 32 dims): the row's own splits
+// followed by the prefix's, at most kMaxSplits + kMaxPrefixSplits partials a
+// query row.  The plan (before the wait) overlaps the kernels before.  Bound by
+// the latency of three dependent reads and, for many partials, by L2: the
+// accumulators are read as whole 128-byte lines, eight loads of a thread in
+// flight, the first eight before the weights are known.
 template <int D>
 __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant__ SharedMergeArgs m) {
   const DecodeArgs& a = m.d;
-  constexpr int S_MAX = kMaxSplits + kMaxPrefixSplits;
+  constexpr int S_MAX = kMaxSplits + kMaxPrefixSplits, U = 8;
   __shared__ int s_F[8];
   __shared__ int s_row[8];
-  __shared__ float sw[32 * S_MAX];
-  const int b = blockIdx.x, h = blockIdx.y, d0 = blockIdx.z * 32, tid = threadIdx.x;
+  __shared__ float s_w[kMergeRows * S_MAX];  // weights
+  const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+  const int d0 = (blockIdx.z % (D / 32)) * 32, q0 = (blockIdx.z / (D / 32)) * kMergeRows;
   const int warp = tid >> 5, lane = tid & 31;
   const int pages = *a.shared;
   if (tid < a.B) {
@@ -89,8 +94,8 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
   const int own = max(1, (((s_F[b] + 63) >> 6) + chunk - 1) / chunk);
   const bool part = s_row[b] >= 0;
   const int per = part ? (pages + m.nsplit - 1) / m.nsplit : 1;
-  const int splits = own + (part ? (pages + per - 1) / per : 0);
-  if (h == 0 && d0 == 0) {  // the row's leading table entries are those the prefix pass read
+  const int pre = part ? (pages + per - 1) / per : 0;
+  if (h == 0 && blockIdx.z == 0) {  // the row's leading table entries are those the prefix pass read
     if (pages < 0 && tid == 0) set_status(a.status, NK_STATUS_FRONTIER);
     if (part && s_row[b] != first) {
       const int32_t* mine = a.tables + static_cast<int64_t>(s_row[b]) * a.L;
@@ -99,47 +104,53 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
         if (mine[i] != read[i]) set_status(a.status, NK_STATUS_PREFIX);
     }
   }
+  const int R_all = a.T * a.G;
+  const int R = R_all <= 8 ? 8 : R_all <= 16 ? 16 : 32;  // rows of an own partial's slot
+  const int R_real = min(kMergeRows, R_all - q0);
+  const int64_t own0 = (static_cast<int64_t>(b) * a.H + h) * a.target;  // the row's first own slot
+  // slot of query row q0 + r in the first prefix partial of its tile; the next
+  // partial is 128 slots on
+  auto prefix0 = [&](int r) {
+    const int flat = b * R_all + q0 + r;
+    return (static_cast<int64_t>(h) * m.tiles + flat / 128) * m.nsplit * 128 + flat % 128;
+  };
   griddep_wait();
   griddep_launch_dependents();
 
-  const int R = a.T * a.G <= 8 ? 8 : a.T * a.G <= 16 ? 16 : 32, R_real = a.T * a.G;
-  const int64_t own0 = (static_cast<int64_t>(b) * a.H + h) * a.target;
-  // partial k of query row qr: (m, l) and the first of its D accumulators
-  auto slot = [&](int qr, int k, const float2*& ml, const float*& o) {
-    if (k < own) {
-      const int64_t i = (own0 + k) * R + qr;
-      ml = a.ws_ml + i;
-      o = a.ws_acc + i * D;
-    } else {
-      const int flat = b * R_real + qr;
-      const int64_t i = ((static_cast<int64_t>(h) * m.tiles + flat / 128) * m.nsplit + (k - own)) * 128 + flat % 128;
-      ml = m.sh_ml + i;
-      o = m.sh_o + i * D;
-    }
+  // thread = (query row r, 4 dims, every fourth partial from `sub` on)
+  const int sub = tid & 3, r = tid >> 5, d = d0 + ((tid >> 2) & 7) * 4;
+  const bool live = r < R_real;
+  const int splits = own + pre;
+  const float* own_o = a.ws_acc + (own0 * R + q0 + r) * D + d;
+  const float* pre_o = m.sh_o + (live ? prefix0(r) : 0) * D + d;
+  auto acc_at = [&](int k) {
+    const float* p = k < own ? own_o + static_cast<int64_t>(k) * R * D : pre_o + static_cast<int64_t>(k - own) * 128 * D;
+    return __ldcg(reinterpret_cast<const float4*>(p));
   };
-  for (int qr = warp; qr < R_real; qr += 8) {  // one warp per row, lanes over its partials
+  float4 v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) v[u] = live && sub + 4 * u < splits ? acc_at(sub + 4 * u) : make_float4(0.f, 0.f, 0.f, 0.f);
+
+  if (warp < R_real) {  // the weights of query row q0 + warp, lanes over its partials
+    const float2* own_ml = a.ws_ml + own0 * R + q0 + warp;
+    const float2* pre_ml = m.sh_ml + prefix0(warp);
     constexpr int N = S_MAX / 32;
-    float2 v[N];
+    float2 w[N];
     float M = -INFINITY;
 #pragma unroll
     for (int u = 0; u < N; ++u) {
       const int k = lane + 32 * u;
-      v[u] = make_float2(-INFINITY, 0.f);
-      if (k < splits) {
-        const float2* ml;
-        const float* o;
-        slot(qr, k, ml, o);
-        v[u] = __ldcg(ml);
-      }
-      M = fmaxf(M, v[u].x);
+      w[u] = k >= splits ? make_float2(-INFINITY, 0.f) : __ldcg(k < own ? own_ml + k * R : pre_ml + (k - own) * 128);
     }
+#pragma unroll
+    for (int u = 0; u < N; ++u) M = fmaxf(M, w[u].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float L = 0.f;
 #pragma unroll
     for (int u = 0; u < N; ++u) {
-      v[u].x = M == -INFINITY || !(v[u].y > 0.f) ? 0.f : ex2(v[u].x - M);
-      L += v[u].y * v[u].x;
+      w[u].x = M == -INFINITY || !(w[u].y > 0.f) ? 0.f : ex2(w[u].x - M);
+      L += w[u].y * w[u].x;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
@@ -147,43 +158,47 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
 #pragma unroll
     for (int u = 0; u < N; ++u) {
       const int k = lane + 32 * u;
-      if (k < splits) sw[qr * S_MAX + k] = v[u].x * inv;
+      if (k < splits) s_w[warp * S_MAX + k] = w[u].x * inv;
     }
-    if (lane == 0 && a.lse && d0 == 0)
+    if (lane == 0 && a.lse && d0 == 0) {
+      const int qr = q0 + warp;
       a.lse[(static_cast<int64_t>(b) * a.T + qr / a.G) * a.Hq + h * a.G + qr % a.G] =
           L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    }
   }
-  __syncthreads();
-  // item = (query row, 4 dims); four threads take every fourth partial each
-  const int sub = tid & 3;
-  for (int item = tid >> 2; item < R_real * 8; item += 64) {
-    const int qr = item >> 3, d = d0 + (item & 7) * 4;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int k = sub; k < splits; k += 4) {
-      const float w = sw[qr * S_MAX + k];
-      const float2* ml;
-      const float* o;
-      slot(qr, k, ml, o);
-      if (w > 0.f) {  // a partial without keys has no accumulators
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(o + d));
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
-      }
+  __syncwarp();  // a warp's weights are its own threads': r == warp
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = sub; k0 < splits; k0 += 4 * U) {
+    float4 nx[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + 4 * (U + u);
+      nx[u] = live && k < splits ? acc_at(k) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
-    for (int off = 1; off < 4; off <<= 1) {
-      acc.x += __shfl_xor_sync(0xffffffffu, acc.x, off);
-      acc.y += __shfl_xor_sync(0xffffffffu, acc.y, off);
-      acc.z += __shfl_xor_sync(0xffffffffu, acc.z, off);
-      acc.w += __shfl_xor_sync(0xffffffffu, acc.w, off);
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + 4 * u;
+      const float w = live && k < splits ? s_w[r * S_MAX + k] : 0.f;
+      if (w > 0.f) {  // a partial without keys has no accumulators
+        acc.x = fmaf(w, v[u].x, acc.x);
+        acc.y = fmaf(w, v[u].y, acc.y);
+        acc.z = fmaf(w, v[u].z, acc.z);
+        acc.w = fmaf(w, v[u].w, acc.w);
+      }
+      v[u] = nx[u];
     }
-    if (sub == 0) {
-      __nv_bfloat16* dst = a.out + ((static_cast<int64_t>(b) * a.T + qr / a.G) * a.Hq + h * a.G + qr % a.G) * D + d;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-    }
+  }
+#pragma unroll
+  for (int off = 1; off < 4; off <<= 1) {
+    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, off);
+    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, off);
+    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, off);
+    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, off);
+  }
+  if (sub == 0 && live) {
+    const int qr = q0 + r;
+    __nv_bfloat16* dst = a.out + ((static_cast<int64_t>(b) * a.T + qr / a.G) * a.Hq + h * a.G + qr % a.G) * D + d;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
   }
 }
 
@@ -277,7 +292,7 @@ extern "C" int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const
   m.tiles = pl.tiles;
   m.nsplit = pl.nsplit;
   const int D = pool->desc.head_dim;
-  const dim3 grid(B, a.H, D / 32);
+  const dim3 grid(B, a.H, D / 32 * ((T * a.G + kMergeRows - 1) / kMergeRows));
   e = D == 64    ? launch_pdl(shared_merge_kernel<64>, grid, dim3(256), 0, s, m)
       : D == 128 ? launch_pdl(shared_merge_kernel<128>, grid, dim3(256), 0, s, m)
                  : launch_pdl(shared_merge_kernel<256>, grid, dim3(256), 0, s, m);

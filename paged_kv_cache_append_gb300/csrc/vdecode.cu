@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(448, 1)
   // the programmatic dependency wait (see decode.cuh); q, k, v and every
   // global write come after it.
   const bool early = a.k_new != nullptr;
-  if (!early) griddep_wait();
+  if (!early && a.shared == nullptr) griddep_wait();  // (see decode.cuh)
   griddep_launch_dependents();
   if (tid < a.B) {
     const int F = a.frontiers[tid], row = a.table_rows[tid];
@@ -742,6 +742,7 @@ __global__ void __launch_bounds__(448, 1)
   __syncthreads();
   tc::fence_after();
   if (warp == 0) tc::dealloc(tmem, 512);
+  if (a.shared != nullptr) griddep_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -995,7 +996,7 @@ __global__ void __launch_bounds__(448, 1)
     prefetch_tmap(&tmv);
   }
   const bool early = a.k_new != nullptr;
-  if (!early) griddep_wait();
+  if (!early && a.shared == nullptr) griddep_wait();  // (see decode.cuh)
   griddep_launch_dependents();
   if (tid < a.B) {
     const int F = a.frontiers[tid], row = a.table_rows[tid];
@@ -1562,6 +1563,7 @@ __global__ void __launch_bounds__(448, 1)
   __syncthreads();
   tc::fence_after();
   if (warp == 0) tc::dealloc(tmem, 512);
+  if (a.shared != nullptr) griddep_wait();
 }
 
 template <int KK, int KV, int D>

@@ -12,25 +12,26 @@
 // the least j with d_0 + .. + d_j > u_K (d_0 + .. + d_{V-1}).
 //
 // The sums decide at borders whose distance is a token's own probability, so
-// they are held in more than fp32: a thread adds its fp32 differences, with
-// the rounding error of each difference and of each addition, as an unevaluated
-// pair of fp32 values (Knuth's TwoSum; about 48 bits, at the fp32 rate, where
-// this chip's fp64 units are a small fraction of it), and everything above a
-// thread in fp64.
+// they are held in more than fp32, as unevaluated pairs of fp32 values (Knuth's
+// TwoSum on every difference and every addition: about 48 bits), two elements
+// to a packed instruction.
 //
-// One cluster of CTAs works on a sequence, each CTA on a contiguous slice of
-// the vocabulary, staged tile by tile in shared memory with coalesced loads
-// (rows of an odd vocabulary are not 16-byte aligned) and then read back as
-// one contiguous run per thread, so that the thread sums are in vocabulary
-// order.  The slice sums meet over distributed shared memory; every CTA then
-// knows which slice holds the border, and that one finds the tile, warp, lane
-// and element.  Only the two rows that are needed are read, once.
-#include <cooperative_groups.h>
-
+// One cluster of CTAs works on a sequence.  Its warps take contiguous chunks of
+// the vocabulary and read them with coalesced 4-byte loads (rows of an odd
+// vocabulary are not 16-byte aligned), every lane adding its own stride, so
+// nothing is staged and the loads of many warps are in flight.  The CTAs' sums
+// meet over distributed shared memory.  What follows is serial and short, so
+// one warp does it: it finds whose slice holds the border and, in that CTA,
+// the warp chunk from the chunk sums that were kept; the chunk is read again
+// (some KB, from L2), a long one in W contiguous parts by all warps; and the
+// last part is scanned 256 elements at a time, 8 consecutive ones a lane.
 #include <cfloat>
+
+#include <cooperative_groups.h>
 
 #include "device.cuh"
 #include "internal.h"
+#include "packed.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -51,12 +52,32 @@ struct VerifyArgs {
   int K, V;
 };
 
-constexpr int kVThreads = 512, kVWarps = kVThreads / 32;
-constexpr int kVRun = 25;                       // elements of a thread's run (odd: no bank conflicts)
-constexpr int kVTile = kVThreads * kVRun;       // elements of a staged tile
-constexpr int kVMaxTiles = 128;                 // tiles of a slice
+constexpr int kVMaxWarps = 16;
 constexpr int kVMaxVocab = 1 << 24;
-constexpr size_t kVSmem = 2ull * kVTile * sizeof(float);
+
+// A sum held as an unevaluated pair of fp32 values.
+struct Pair {
+  float h, l;
+};
+
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+  const float t = a.h + b.h, bb = t - a.h;
+  const float l = ((a.h - (t - bb)) + (b.h - bb)) + (a.l + b.l);
+  const float h = t + l;
+  return Pair{h, l - (h - t)};
+}
+
+__device__ __forceinline__ bool pair_greater(Pair a, Pair b) {
+  const float t = a.h - b.h, bb = t - a.h;
+  return t + (((a.h - (t - bb)) - (b.h + bb)) + (a.l - b.l)) > 0.f;
+}
+
+// u * a: the rounding error of the first product is in the second value.
+__device__ __forceinline__ Pair pair_scale(Pair a, float u) {
+  const float t = u * a.h, e = fmaf(u, a.h, -t) + u * a.l;
+  const float h = t + e;
+  return Pair{h, e - (h - t)};
+}
 
 // d = max(p - q, 0) as s + e exactly (s the rounded difference); weights that
 // are not finite count as 0.
@@ -76,192 +97,288 @@ __device__ __forceinline__ int pick(uint32_t over, uint32_t positive) {
 }
 
 // Inclusive scan over the warp's lanes.
-__device__ __forceinline__ double warp_scan(double x, int lane) {
+__device__ __forceinline__ Pair warp_scan(Pair x, int lane) {
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, x, off);
-    if (lane >= off) x += y;
+    const Pair y{__shfl_up_sync(0xffffffffu, x.h, off), __shfl_up_sync(0xffffffffu, x.l, off)};
+    if (lane >= off) x = pair_add(y, x);
   }
   return x;
 }
 
-__global__ void __launch_bounds__(kVThreads, 1) verify_kernel(const __grid_constant__ VerifyArgs a) {
+__device__ __forceinline__ Pair warp_sum(Pair x) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    x = pair_add(x, Pair{__shfl_xor_sync(0xffffffffu, x.h, off), __shfl_xor_sync(0xffffffffu, x.l, off)});
+  return x;
+}
+
+__device__ __forceinline__ Pair shuffle(Pair x, int lane) {
+  return Pair{__shfl_sync(0xffffffffu, x.h, lane), __shfl_sync(0xffffffffu, x.l, lane)};
+}
+
+// One level of the search, done alike by every warp that calls it: lane i holds
+// the sum of part i and all parts follow `base`.  Returns the part with the
+// border (-1 for none with weight) and moves `base` to where it begins.
+__device__ __forceinline__ int find(Pair part, Pair border, int lane, Pair& base) {
+  const Pair at = pair_add(base, warp_scan(part, lane));
+  const uint32_t over = __ballot_sync(0xffffffffu, pair_greater(at, border));
+  const int i = pick(over, __ballot_sync(0xffffffffu, part.h > 0.f));
+  const Pair before = shuffle(at, max(i - 1, 0));
+  if (i > 0) base = before;
+  return i;
+}
+
+// u q < p without rounding: the product and its error, or fp64 where they
+// could underflow.
+__device__ __forceinline__ bool accepts(float u, float q, float p) {
+  const float t = u * q;
+  if (fabsf(t) < 1e-30f) return static_cast<double>(u) * static_cast<double>(q) < static_cast<double>(p);
+  return t < p || (t == p && fmaf(u, q, -t) < 0.f);
+}
+
+// The weights of one sequence's next token.
+struct Weights {
+  const float* p;
+  const float* q;  // nullptr: none is taken off
+  int zero;        // a token without weight (-1: none)
+
+  __device__ __forceinline__ void at(int j, int end, float& s, float& e) const {
+    const bool in = j < end && j != zero;
+    weight(in ? p[j] : 0.f, in && q ? q[j] : 0.f, s, e);
+  }
+};
+
+// h + l += s + e, exactly but for the last bits of l.
+__device__ __forceinline__ void pair_acc(float& h, float& l, float s, float e) {
+  const float t = h + s, bb = t - h;
+  l += ((h - (t - bb)) + (s - bb)) + e;
+  h = t;
+}
+
+// The sum of one lane over its stride of [lo, hi), element by element.
+__device__ __forceinline__ void lane_sum(const Weights& w, int lo, int hi, int lane, float& h, float& l) {
+  for (int j = lo + lane; j < hi; j += 32) {
+    float s, e;
+    w.at(j, hi, s, e);
+    pair_acc(h, l, s, e);
+  }
+}
+
+// The sum over [lo, hi) of one warp, in every lane.  Whole blocks of 256
+// elements take the packed path: with m = max(p, q), m - q is the weight, 0
+// where p <= q or p is NaN.  Entries that are not finite leave a sum that is
+// not, and the warp then does it over, element by element.
+template <bool Q>
+__device__ __forceinline__ Pair chunk_sum(const Weights& w, int lo, int hi, int lane) {
+  constexpr int U = 8;
+  float h = 0.f, l = 0.f;
+  int j = lo;
+  if (w.zero < lo || w.zero >= hi) {
+    const F2 minus = pack2(-1.f, -1.f);
+    F2 h2 = 0ull, l2 = 0ull;
+    for (; j + 32 * U <= hi; j += 32 * U) {
+      float x[U], y[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) x[k] = __ldcs(w.p + j + 32 * k + lane);
+#pragma unroll
+      for (int k = 0; k < U; ++k) y[k] = Q ? __ldcs(w.q + j + 32 * k + lane) : 0.f;
+#pragma unroll
+      for (int k = 0; k < U; k += 2) {
+        const F2 m = pack2(fmaxf(x[k], y[k]), fmaxf(x[k + 1], y[k + 1]));
+        F2 s = m, e = 0ull;
+        if constexpr (Q) {
+          const F2 q = pack2(y[k], y[k + 1]);
+          s = fma2(q, minus, m);
+          const F2 bb = fma2(m, minus, s);
+          e = fma2(add2(q, bb), minus, fma2(fma2(bb, minus, s), minus, m));
+        }
+        const F2 t = add2(h2, s), bb = fma2(h2, minus, t);
+        l2 = add2(l2, add2(add2(fma2(fma2(bb, minus, t), minus, h2), fma2(bb, minus, s)), e));
+        h2 = t;
+      }
+    }
+    float h1, l1;
+    unpack2(h2, h, h1);
+    unpack2(l2, l, l1);
+    pair_acc(h, l, h1, l1);
+    if (!__all_sync(0xffffffffu, fabsf(h) <= FLT_MAX && fabsf(l) <= FLT_MAX)) {
+      h = l = 0.f;
+      j = lo;
+    }
+  }
+  lane_sum(w, j, hi, lane, h, l);
+  const float t = h + l;
+  return warp_sum(Pair{t, l - (t - h)});
+}
+
+__device__ __forceinline__ Pair chunk_sum(const Weights& w, int lo, int hi, int lane) {
+  return w.q ? chunk_sum<true>(w, lo, hi, lane) : chunk_sum<false>(w, lo, hi, lane);
+}
+
+// The token of [lo, hi) where the running sum from `base` on passes the border
+// (the last one with weight if none does, -1 without weight), by one warp.
+__device__ __forceinline__ int scan_token(const Weights& w, int lo, int hi, Pair base, Pair border, int lane) {
+  constexpr int E = 8;
+  int token = -1;
+  for (int j = lo; j < hi; j += 32 * E) {
+    float s[E], e[E];
+    Pair sum{0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < E; ++k) w.at(j + E * lane + k, hi, s[k], e[k]);
+#pragma unroll
+    for (int k = 0; k < E; ++k) sum = pair_add(sum, Pair{s[k], e[k]});
+    const Pair at = pair_add(base, warp_scan(sum, lane));
+    const uint32_t positive = __ballot_sync(0xffffffffu, sum.h > 0.f);
+    const uint32_t over = __ballot_sync(0xffffffffu, pair_greater(at, border)) & positive;
+    if (positive) {
+      const int i = over ? __ffs(over) - 1 : 31 - __clz(positive);  // the lane that holds it
+      const Pair before = shuffle(at, max(i - 1, 0));
+      Pair run = i > 0 ? before : base;
+      int last = -1, first = -1;
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        run = pair_add(run, Pair{s[k], e[k]});
+        if (s[k] > 0.f) {
+          last = k;
+          if (first < 0 && pair_greater(run, border)) first = k;
+        }
+      }
+      token = j + E * i + __shfl_sync(0xffffffffu, first >= 0 ? first : last, i);
+    }
+    if (over) break;
+    base = shuffle(at, 31);
+  }
+  return token;
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
+// CTAs of 32 W threads, W <= 16, in clusters that share a sequence.
+__global__ void __launch_bounds__(512, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = cluster.num_blocks(), rank = cluster.block_rank();
   const int b = blockIdx.x / nc;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  extern __shared__ float smem_v[];
-  float* sp = smem_v;
-  float* sq = smem_v + kVTile;
-  __shared__ double s_slice;              // this CTA's slice sum, read by the cluster
-  __shared__ double s_warp[kVWarps];
-  __shared__ double s_tile[kVMaxTiles];
-  __shared__ int s_n;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = blockDim.x >> 5;
+  __shared__ Pair s_slice;              // this CTA's sum, read by the cluster
+  __shared__ Pair s_chunk[kVMaxWarps];  // the warp chunks' sums
+  __shared__ Pair s_part[kVMaxWarps];   // the parts' sums of the chunk with the border
+  __shared__ int s_owner, s_where;      // slice and warp chunk with the border
   griddep_wait();  // launched with programmatic stream serialization
   griddep_launch_dependents();
 
-  // ---- acceptance (every CTA for itself) --------------------------------------
+  // ---- acceptance (every warp for itself) ---------------------------------------
   const int K = a.K, V = a.V;
-  int Kb = a.draft_len ? a.draft_len[b] : K;
-  Kb = min(max(Kb, 0), K);
   const float* prow0 = a.target + static_cast<int64_t>(b) * (K + 1) * a.target_stride;
   const float* qrow0 = a.draft ? a.draft + static_cast<int64_t>(b) * K * a.draft_stride : nullptr;
   const float* u = a.u + static_cast<int64_t>(b) * (K + 1);
-  if (warp == 0) {
-    int n = Kb;
-    for (int i0 = 0; i0 < Kb; i0 += 32) {
-      const int i = i0 + lane;
-      bool ok = false;
-      if (i < Kb) {
-        const int x = a.tokens[static_cast<int64_t>(b) * K + i];
-        if (x >= 0 && x < V) {
-          const float p = prow0[i * a.target_stride + x];
-          const float q = qrow0 ? qrow0[i * a.draft_stride + x] : 1.f;
-          ok = static_cast<double>(u[i]) * static_cast<double>(q) < static_cast<double>(p);
-        } else if (rank == 0) {
-          set_status(a.status, NK_STATUS_TOKEN_RANGE);
-        }
-      }
-      const uint32_t no = __ballot_sync(0xffffffffu, !ok && i < Kb);
-      if (no) {
-        n = i0 + __ffs(no) - 1;
-        break;
+  const int32_t* drafts = a.tokens + static_cast<int64_t>(b) * K;
+  int Kb = a.draft_len ? a.draft_len[b] : K;
+  Kb = min(max(Kb, 0), K);
+  int n = Kb;
+  for (int i0 = 0; i0 < K; i0 += 32) {
+    const int i = i0 + lane;
+    bool ok = false;
+    if (i < K) {
+      const int x = drafts[i];
+      const float ui = u[i];
+      if (x >= 0 && x < V) {
+        const bool used = i < Kb;  // rows behind the last draft are not read
+        const float p = used ? prow0[i * a.target_stride + x] : 0.f;
+        const float q = !used ? 0.f : qrow0 ? qrow0[i * a.draft_stride + x] : 1.f;
+        ok = accepts(ui, q, p);
+      } else if (i < Kb && rank == 0 && warp == 0) {
+        set_status(a.status, NK_STATUS_TOKEN_RANGE);
       }
     }
-    if (lane == 0) s_n = n;
+    const uint32_t no = __ballot_sync(0xffffffffu, !ok && i < Kb);
+    if (no) {
+      n = i0 + __ffs(no) - 1;
+      break;
+    }
   }
-  __syncthreads();
-  const int n = s_n;
   const bool cut = n < Kb;
-  const float* prow = prow0 + n * a.target_stride;
-  const float* qrow = cut && qrow0 ? qrow0 + n * a.draft_stride : nullptr;
-  const int certain = cut && !qrow0 ? a.tokens[static_cast<int64_t>(b) * K + n] : -1;  // weight 0
 
-  // ---- this CTA's slice ---------------------------------------------------------
+  // ---- this warp's chunk of this CTA's slice ----------------------------------------
   const int per = (V + nc - 1) / nc;
   const int lo = min(rank * per, V), hi = min(lo + per, V);
-  const int tiles = (hi - lo + kVTile - 1) / kVTile;
+  const int cper = (hi - lo + W - 1) / W;
+  const int c_lo = min(lo + warp * cper, hi), c_hi = min(c_lo + cper, hi);
+  const bool parts = cper > 512;  // a chunk that one warp would scan for too long
 
-  // Stages tile t; elements past the slice weigh 0.
-  auto stage = [&](int t, bool residual) {
-    const int at = lo + t * kVTile;
-#pragma unroll 5
-    for (int k = 0; k < kVRun; ++k) {
-      const int j = at + k * kVThreads + tid;
-      const bool in = j < hi && !(residual && j == certain);
-      sp[k * kVThreads + tid] = in ? prow[j] : 0.f;
-      sq[k * kVThreads + tid] = in && residual && qrow ? qrow[j] : 0.f;
-    }
-  };
-  // The sum of this thread's run of the staged tile.
-  auto run_sum = [&]() {
-    float h = 0.f, l = 0.f;
-#pragma unroll 5
-    for (int k = 0; k < kVRun; ++k) {
-      float s, e;
-      weight(sp[tid * kVRun + k], sq[tid * kVRun + k], s, e);
-      const float t = h + s, bb = t - h;
-      l += (h - (t - bb)) + (s - bb) + e;
-      h = t;
-    }
-    return static_cast<double>(h) + static_cast<double>(l);
-  };
-
-  int token = -1;
+  bool found = false;
   // The residual weights; where they are all zero (p_n and q_n equal in every
   // token they give weight to) the target's own.
   for (int pass = 0; pass < 2; ++pass) {
     const bool residual = pass == 0 && cut;
-    double mine = 0.0;   // sum of the last staged tile's run
-    double scan = 0.0;   // inclusive scan of the runs in this warp
-    double slice = 0.0;
-    for (int t = 0; t < tiles; ++t) {
-      stage(t, residual);
-      __syncthreads();
-      mine = run_sum();
-      scan = warp_scan(mine, lane);
-      if (lane == 31) s_warp[warp] = scan;
-      __syncthreads();
-      double tile = 0.0;
-#pragma unroll
-      for (int w = 0; w < kVWarps; ++w) tile += s_warp[w];
-      if (tid == 0) s_tile[t] = tile;
-      slice += tile;
-      if (t + 1 < tiles) __syncthreads();  // s_warp and the tile are read before they are overwritten
+    Weights w;
+    w.p = prow0 + n * a.target_stride;
+    w.q = residual && qrow0 ? qrow0 + n * a.draft_stride : nullptr;
+    w.zero = residual && !qrow0 ? drafts[n] : -1;
+    const Pair sum = chunk_sum(w, c_lo, c_hi, lane);
+    if (lane == 0) s_chunk[warp] = sum;
+    __syncthreads();
+    const Pair none{0.f, 0.f};
+    Pair border = none, base = none, chunk = none;
+    if (warp == 0) {
+      chunk = lane < W ? s_chunk[lane] : none;
+      const Pair all = warp_sum(chunk);
+      if (lane == 0) s_slice = all;
     }
-    if (tid == 0) s_slice = slice;
-    cluster.sync();
-    // the slice sums of the cluster, one per lane, scanned by every warp alike
-    const double part = lane < nc ? *cluster.map_shared_rank(&s_slice, lane) : 0.0;
-    const double incl = warp_scan(part, lane);
-    const double total = __shfl_sync(0xffffffffu, incl, 31);
-    const double border = static_cast<double>(u[K]) * total;
-    const int owner = pick(__ballot_sync(0xffffffffu, incl > border), __ballot_sync(0xffffffffu, part > 0.0));
-    const double before_owner = __shfl_sync(0xffffffffu, incl - part, max(owner, 0));
-    cluster.sync();  // every slice sum has been read before a second pass or an exit
-    if (owner >= 0) {
-      if (owner == rank) {
-        // the tile that holds the border (all threads alike)
-        double base = before_owner;
-        int t = -1, last = -1;
-        double last_base = base;
-        for (int k = 0; k < tiles; ++k) {
-          const double x = s_tile[k];
-          if (x > 0.0) {
-            last = k;
-            last_base = base;
-            if (base + x > border) {
-              t = k;
-              break;
-            }
-          }
-          base += x;
-        }
-        if (t < 0) t = last, base = last_base;
-        if (t != tiles - 1) {  // not the staged one any more
-          __syncthreads();
-          stage(t, residual);
-          __syncthreads();
-          mine = run_sum();
-          scan = warp_scan(mine, lane);
-          if (lane == 31) s_warp[warp] = scan;
-          __syncthreads();
-        }
-        const double ws = lane < kVWarps ? s_warp[lane] : 0.0;
-        const double wincl = warp_scan(ws, lane);
-        const int w = pick(__ballot_sync(0xffffffffu, base + wincl > border), __ballot_sync(0xffffffffu, ws > 0.0));
-        const double wbase = base + __shfl_sync(0xffffffffu, wincl - ws, max(w, 0));
-        if (warp == w) {
-          const int ln = pick(__ballot_sync(0xffffffffu, wbase + scan > border), __ballot_sync(0xffffffffu, mine > 0.0));
-          const double lbase = wbase + __shfl_sync(0xffffffffu, scan - mine, max(ln, 0));
-          // that lane's run, one element per lane
-          const int e0 = (warp * 32 + max(ln, 0)) * kVRun;
-          float s = 0.f, e = 0.f;
-          if (lane < kVRun) weight(sp[e0 + lane], sq[e0 + lane], s, e);
-          const double d = static_cast<double>(s) + static_cast<double>(e);
-          const double dincl = warp_scan(d, lane);
-          const int el = pick(__ballot_sync(0xffffffffu, lbase + dincl > border), __ballot_sync(0xffffffffu, d > 0.0));
-          token = lo + t * kVTile + e0 + max(el, 0);
-          if (lane == 0) a.out[static_cast<int64_t>(b) * (K + 1) + n] = token;
+    cluster_arrive();
+    cluster_wait();
+    if (warp == 0) {
+      const Pair slice = lane < nc ? *cluster.map_shared_rank(&s_slice, lane) : none;
+      border = pair_scale(warp_sum(slice), u[K]);
+      const int owner = find(slice, border, lane, base);
+      const int c = owner == rank ? max(find(chunk, border, lane, base), 0) : 0;
+      if (lane == 0) {
+        s_owner = owner;
+        s_where = c;
+      }
+    }
+    __syncthreads();
+    cluster_arrive_relaxed();  // this CTA has read the slice sums
+    const int owner = s_owner;
+    found = owner >= 0;
+    if (owner == rank) {
+      const int b_lo = min(lo + s_where * cper, hi), b_hi = min(b_lo + cper, hi);  // the chunk with the border
+      int p_lo = b_lo, p_hi = b_hi;
+      if (parts) {
+        const int pper = (b_hi - b_lo + W - 1) / W;
+        const int m_lo = min(b_lo + warp * pper, b_hi);
+        const Pair mine = chunk_sum(w, m_lo, min(m_lo + pper, b_hi), lane);
+        if (lane == 0) s_part[warp] = mine;
+        __syncthreads();
+        if (warp == 0) {
+          const int r = max(find(lane < W ? s_part[lane] : none, border, lane, base), 0);
+          p_lo = min(b_lo + r * pper, b_hi);
+          p_hi = min(p_lo + pper, b_hi);
         }
       }
-      token = 0;  // found (by the owner)
-      break;
+      if (warp == 0) {
+        const int token = scan_token(w, p_lo, p_hi, base, border, lane);
+        if (lane == 0) a.out[static_cast<int64_t>(b) * (K + 1) + n] = token;
+      }
     }
-    if (!cut) break;
+    cluster_wait();  // every CTA has read this one's sum: it may change, or the CTA end
+    if (found || !cut) break;
   }
 
   if (rank == 0) {
-    for (int i = tid; i <= K; i += kVThreads) {
+    for (int i = tid; i <= K; i += 32 * W) {
       int32_t* o = a.out + static_cast<int64_t>(b) * (K + 1) + i;
-      if (i < n) *o = a.tokens[static_cast<int64_t>(b) * K + i];
-      else if (i > n) *o = -1;
-      else if (token < 0) *o = -1;  // no weight anywhere
+      if (i < n) *o = drafts[i];
+      else if (i > n || !found) *o = -1;  // i == n: no weight anywhere
     }
     if (tid == 0) {
       a.accepted[b] = n;
       if (a.frontiers_out) a.frontiers_out[b] = a.frontiers[b] - (Kb - n);
-      if (token < 0) set_status(a.status, NK_STATUS_TOKEN_RANGE);
+      if (!found) set_status(a.status, NK_STATUS_TOKEN_RANGE);
     }
   }
 }
@@ -302,16 +419,20 @@ extern "C" int nk_verify_drafts(const float* target, int64_t target_stride, cons
   a.K = K;
   a.V = V;
   if (!a.status) return fail(NK_ERR_CUDA, "status word address unavailable");
-  cudaError_t e = cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kVSmem));
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return cuda_fail(e, "verify attributes");
-  // CTAs per sequence: enough that a slice is one tile, at most 16
-  int nc = 1;
-  while (nc < 16 && static_cast<int64_t>(nc) * kVTile < V) nc *= 2;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const int sms = device_sm_count(dev);
+  // CTAs of 16 warps; 8 of them per sequence while all run at once, 4 beyond
+  // (fewer, longer chunks: 64 sequences of 200003 tokens took 25.0 us with 4
+  // and 28.7 with 8, 8 sequences of 131072 took 12.1 and 9.4), and fewer where
+  // a warp would get less than 64 tokens
+  constexpr int W = 16;
+  int nc = static_cast<int64_t>(B) * 8 <= sms ? 8 : 4;
+  while (nc > 1 && static_cast<int64_t>(nc) * W * 64 > V) nc /= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(B) * nc);
-  cfg.blockDim = dim3(kVThreads);
-  cfg.dynamicSmemBytes = kVSmem;
+  cfg.blockDim = dim3(32 * W);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

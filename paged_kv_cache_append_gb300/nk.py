@@ -278,34 +278,52 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream(device: int) -> int:
+    """Handle of the current stream of a device, without building a Stream object where torch can do without."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(device)
+
+
 def _stream(stream) -> int:
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    return stream.cuda_stream if stream is not None else _current_stream(torch.cuda.current_device())
 
 
-def _rows(x, heads_dim: int, lead=None) -> Rows:
-    """nk_rows of a bf16 CUDA tensor [N, heads, D] or [B, T, heads, D] with any token and head strides."""
+def _rows(x, D: int, device: int, lead=None) -> Rows:
+    """nk_rows of a bf16 tensor [N, heads, D] or [B, T, heads, D] on CUDA device
+    `device`, with any token and head strides; `lead`: its sizes before the heads."""
     import torch
-    if not x.is_cuda or x.dtype != torch.bfloat16:
-        raise ValueError(f"expected a bf16 CUDA tensor, got {x.dtype} on {x.device}")
-    if x.dim() not in (3, 4) or x.shape[-1] != heads_dim or x.stride(-1) != 1:
-        raise ValueError(f"expected [..., heads, {heads_dim}] with a unit last stride, got {tuple(x.shape)}")
-    if x.dim() == 4 and x.shape[0] > 1 and x.shape[1] > 1 and x.stride(0) != x.shape[1] * x.stride(1):
-        raise ValueError("the tokens of [B, T, heads, D] rows must be one stride apart")
-    if lead is not None and x.shape[:-2] != lead:
-        raise ValueError(f"expected leading sizes {tuple(lead)}, got {tuple(x.shape[:-2])}")
-    token = x.stride(-3) if x.shape[-3] > 1 or x.dim() == 3 else x.stride(0)
-    tokens = x.shape[0] if x.dim() == 3 else x.shape[0] * x.shape[1]
+    shape, stride = x.shape, x.stride()
+    n = len(shape)
+    if x.dtype is not torch.bfloat16 or x.get_device() != device:
+        raise ValueError(f"expected a bf16 tensor on CUDA device {device}, got {x.dtype} on {x.device}")
+    if not 3 <= n <= 4 or shape[-1] != D or stride[-1] != 1 or (lead is not None and shape[:-2] != lead):
+        raise ValueError(f"expected {'...' if lead is None else tuple(lead)} + (heads, {D}) with a unit last stride, "
+                         f"got {tuple(shape)} with strides {stride}")
+    token = stride[-3]
+    if n == 4 and shape[0] > 1:
+        if shape[1] == 1:
+            token = stride[0]
+        elif stride[0] != shape[1] * token:
+            raise ValueError("the tokens of [B, T, heads, D] rows must be one stride apart")
     # the stride of a dimension of size 1 says nothing
-    return Rows(x.data_ptr(), token if tokens > 1 else 0, x.stride(-2) if x.shape[-2] > 1 else 0)
+    one = shape[0] == 1 and (n == 3 or shape[1] == 1)
+    return Rows(x.data_ptr(), 0 if one else token, stride[-2] if shape[-2] > 1 else 0)
 
 
-def _cuda(x, dtype, shape, name, device):
-    """Checks a contiguous tensor argument of a call on `device`."""
-    if x.device != device or x.dtype != dtype or tuple(x.shape) != tuple(shape) or not x.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {device}, got "
+def _cuda(x, dtype, shape, name, device: int) -> int:
+    """Checks a contiguous tensor argument on CUDA device `device`; its address."""
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != device or not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on CUDA device {device}, got "
                          f"{x.dtype} {tuple(x.shape)} on {x.device}")
+    return x.data_ptr()
 
 
 class Rope:
@@ -326,15 +344,20 @@ class Rope:
             if w is not None and (w.dtype != torch.bfloat16 or w.device != cos_sin.device or w.dim() != 1
                                   or not w.is_contiguous()):
                 raise ValueError("norm weights must be contiguous bf16 vectors on the table's device")
+        if q_weight is not None and k_weight is not None and q_weight.numel() != k_weight.numel():
+            raise ValueError("the norm weights must have one size")
+        w = q_weight if q_weight is not None else k_weight
         self.cos_sin, self.q_weight, self.k_weight = cos_sin, q_weight, k_weight
-        self.device = cos_sin.device
+        self.device = cos_sin.get_device()
+        self.head_dim = None if w is None else w.numel()
         self.desc = RopeDesc(_ptr(cos_sin), cos_sin.shape[0], rotary_dim, int(interleaved), eps, weight_offset, 0,
                              _ptr(q_weight), _ptr(k_weight))
 
-    def check(self, D: int) -> None:
-        for w in (self.q_weight, self.k_weight):
-            if w is not None and w.numel() != D:
-                raise ValueError(f"norm weights have {w.numel()} elements, the heads {D}")
+    def check(self, D: int, device: int) -> None:
+        if self.head_dim is not None and self.head_dim != D:
+            raise ValueError(f"norm weights have {self.head_dim} elements, the heads {D}")
+        if self.device != device:
+            raise ValueError("all operands must be on the device of the rotation table")
 
 
 def qk_norm_rope(q, k, positions, rope: Rope, q_out=None, k_out=None, stream=None):
@@ -342,20 +365,23 @@ def qk_norm_rope(q, k, positions, rope: Rope, q_out=None, k_out=None, stream=Non
     token and head strides) at ``positions`` int32 [N]; returns (q_out, k_out),
     new contiguous tensors unless given (q_out may be q itself, k_out k)."""
     import torch
-    D = q.shape[-1]
-    lead = q.shape[:-2]
-    rope.check(D)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-    if q_out.shape != q.shape or k_out.shape != k.shape:
+    dev, qs, ks = q.get_device(), q.shape, k.shape
+    if dev >= 0 and torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return qk_norm_rope(q, k, positions, rope, q_out, k_out, stream)
+    D, lead = qs[-1], qs[:-2]
+    rope.check(D, dev)
+    if q_out is None:
+        q_out = torch.empty(qs, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(ks, dtype=k.dtype, device=k.device)
+    if q_out.shape != qs or k_out.shape != ks:
         raise ValueError("outputs must have the shapes of their inputs")
-    rq, rk, oq, ok = (_rows(x, D, lead) for x in (q, k, q_out, k_out))
-    if any(x.device != rope.device for x in (q, k, q_out, k_out)):
-        raise ValueError("all operands must be on the device of the rotation table")
-    _cuda(positions, torch.int32, lead, "positions", q.device)
-    with torch.cuda.device(q.device):
-        nk_qk_norm_rope(rope.desc, D, rq, q.shape[-2], rk, k.shape[-2], positions.data_ptr(), positions.numel(),
-                        oq, ok, _stream(stream))
+    rq, rk = _rows(q, D, dev), _rows(k, D, dev, lead)
+    oq = rq if q_out is q else _rows(q_out, D, dev)
+    ok = rk if k_out is k else _rows(k_out, D, dev)
+    pos = _cuda(positions, torch.int32, lead, "positions", dev)
+    nk_qk_norm_rope(rope.desc, D, rq, qs[-2], rk, ks[-2], pos, positions.numel(), oq, ok, _stream(stream))
     return q_out, k_out
 
 
@@ -369,32 +395,37 @@ def verify_drafts(target, tokens, uniforms, draft=None, draft_len=None, frontier
     """
     import torch
     B, K1, V = target.shape
-    K, dev = K1 - 1, target.device
-    strides = []
-    for x, n, name in ((target, K1, "target"), (draft, K, "draft")):
-        strides.append(V)
+    K, dev = K1 - 1, target.get_device()
+    if dev < 0:
+        raise ValueError("target: expected a CUDA tensor")
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return verify_drafts(target, tokens, uniforms, draft, draft_len, frontiers, stream)
+    strides = [V, V]
+    for i, (x, n) in enumerate(((target, K1), (draft, K))):
         if x is None:
             continue
-        if x.device != dev or not x.is_cuda or x.dtype != torch.float32 or tuple(x.shape) != (B, n, V):
-            raise ValueError(f"{name}: expected a float32 CUDA tensor {(B, n, V)}, got {x.dtype} {tuple(x.shape)}")
+        if x.dtype is not torch.float32 or x.shape != (B, n, V) or x.get_device() != dev:
+            raise ValueError(f"{('target', 'draft')[i]}: expected a float32 tensor {(B, n, V)} on CUDA device {dev}, "
+                             f"got {x.dtype} {tuple(x.shape)} on {x.device}")
+        st = x.stride()
         if B * n > 1:   # the stride of a dimension of size 1 says nothing
-            strides[-1] = x.stride(1) if n > 1 else x.stride(0)
-        if n and ((V > 1 and x.stride(2) != 1) or strides[-1] < V
-                  or (B > 1 and n > 1 and x.stride(0) != n * x.stride(1))):
-            raise ValueError(f"{name}: rows must be contiguous and one stride apart")
-    _cuda(tokens, torch.int32, (B, K), "tokens", dev)
-    _cuda(uniforms, torch.float32, (B, K1), "uniforms", dev)
-    for x, name in ((draft_len, "draft_len"), (frontiers, "frontiers")):
-        if x is not None:
-            _cuda(x, torch.int32, (B,), name, dev)
-    accepted = torch.empty(B, dtype=torch.int32, device=dev)
-    out = torch.empty((B, K1), dtype=torch.int32, device=dev)
-    after = torch.empty_like(frontiers) if frontiers is not None else None
-    with torch.cuda.device(dev):
-        nk_verify_drafts(target.data_ptr(), strides[0], _ptr(draft) if K else None, strides[1],
-                         _ptr(tokens) if K else None,
-                         _ptr(draft_len), uniforms.data_ptr(), _ptr(frontiers), B, K, V, accepted.data_ptr(),
-                         out.data_ptr(), _ptr(after), _stream(stream))
+            strides[i] = st[1] if n > 1 else st[0]
+        if n and ((V > 1 and st[2] != 1) or strides[i] < V or (B > 1 and n > 1 and st[0] != n * st[1])):
+            raise ValueError(f"{('target', 'draft')[i]}: rows must be contiguous and one stride apart")
+    pt = _cuda(tokens, torch.int32, (B, K), "tokens", dev)
+    pu = _cuda(uniforms, torch.float32, (B, K1), "uniforms", dev)
+    pl = None if draft_len is None else _cuda(draft_len, torch.int32, (B,), "draft_len", dev)
+    where = dict(dtype=torch.int32, device=target.device)
+    accepted, out = torch.empty(B, **where), torch.empty((B, K1), **where)
+    pf = pa = after = None
+    if frontiers is not None:
+        pf = _cuda(frontiers, torch.int32, (B,), "frontiers", dev)
+        after = torch.empty(B, **where)
+        pa = after.data_ptr()
+    nk_verify_drafts(target.data_ptr(), strides[0], draft.data_ptr() if draft is not None and K else None,
+                     strides[1], pt if K else None, pl, pu, pf, B, K, V, accepted.data_ptr(), out.data_ptr(), pa,
+                     _stream(stream))
     return accepted, out, after
 
 
@@ -528,39 +559,36 @@ class Pool:
         strides, one token stride apart across rows; rows of q_out past a
         row's count are not written."""
         import torch
-        B, T = k.shape[0], k.shape[1]
-        dev = self.planes[0][0].device
-        rope.check(self.D)
+        dev = self.planes[0][0].get_device()
+        if torch.cuda.current_device() != dev:
+            with torch.cuda.device(dev):
+                return self.append_rope(layer, tables, table_rows, write_pos, k, v, rope, q, q_out, counts, stream)
+        rope.check(self.D, dev)
+        lead = k.shape[:2]
         if k.dim() != 4 or k.shape[2] != self.H or v.shape != k.shape:
             raise ValueError(f"k and v must be [B, T, {self.H}, {self.D}]")
-        rk, rv = _rows(k, self.D), _rows(v, self.D)
-        rq = None
+        B, T = lead
+        rk, rv, rq, Hq, pq = _rows(k, self.D, dev), _rows(v, self.D, dev), None, 0, None
         if q is not None:
-            rq = _rows(q, self.D, k.shape[:2])
+            rq, Hq = _rows(q, self.D, dev, lead), q.shape[2]
             if q_out is None:
                 q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            _cuda(q_out, torch.bfloat16, q.shape, "q_out", dev)
+            pq = _cuda(q_out, torch.bfloat16, q.shape, "q_out", dev)
         elif q_out is not None:
             raise ValueError("q_out without q")
-        if any(x is not None and x.device != dev for x in (k, v, q, rope.cos_sin)):
-            raise ValueError("all operands must be on the pool's device")
-        _cuda(tables, torch.int32, (self.C, self.L), "tables", dev)
-        for x, name in ((table_rows, "table_rows"), (write_pos, "write_pos"), (counts, "counts")):
-            if x is not None:
-                _cuda(x, torch.int32, (B,), name, dev)
-        with torch.cuda.device(dev):
-            nk_paged_kv_append_rope(self.handle, layer, _ptr(tables), _ptr(table_rows), _ptr(write_pos),
-                                    _ptr(counts), rope.desc, rk, rv, rq, 0 if q is None else q.shape[2],
-                                    _ptr(q_out), B, T, _stream(stream))
+        pt = _cuda(tables, torch.int32, (self.C, self.L), "tables", dev)
+        pr = _cuda(table_rows, torch.int32, (B,), "table_rows", dev)
+        pw = _cuda(write_pos, torch.int32, (B,), "write_pos", dev)
+        pc = None if counts is None else _cuda(counts, torch.int32, (B,), "counts", dev)
+        nk_paged_kv_append_rope(self.handle, layer, pt, pr, pw, pc, rope.desc, rk, rv, rq, Hq, pq, B, T,
+                                _stream(stream))
         return q_out
 
     def shared_workspace(self, B, T, Hq):
         """A workspace for ``shared_decode`` (one per stream or captured graph that may overlap others)."""
         import torch
-        dev = self.planes[0][0].device
-        with torch.cuda.device(dev):
-            n = nk_shared_decode_workspace_bytes(self.handle, B, T, Hq)
-        return torch.empty(n, dtype=torch.uint8, device=dev)
+        n = nk_shared_decode_workspace_bytes(self.handle, B, T, Hq)
+        return torch.empty(n, dtype=torch.uint8, device=self.planes[0][0].device)
 
     def shared_decode(self, layer, q, tables, table_rows, frontiers, shared_pages, scale, out=None, lse=None,
                       workspace=None, stream=None):
@@ -569,24 +597,28 @@ class Pool:
         Without ``workspace`` one is allocated for this call."""
         import torch
         B, T, Hq, D = q.shape
-        dev = self.planes[0][0].device
-        if D != self.D or not q.is_contiguous() or q.dtype != torch.bfloat16 or q.device != dev:
-            raise ValueError(f"q must be a contiguous bf16 tensor [B, T, Hq, {self.D}] on {dev}")
-        _cuda(tables, torch.int32, (self.C, self.L), "tables", dev)
-        _cuda(table_rows, torch.int32, (B,), "table_rows", dev)
-        _cuda(frontiers, torch.int32, (B,), "frontiers", dev)
-        if shared_pages.device != dev or shared_pages.dtype != torch.int32 or shared_pages.numel() != 1:
+        dev = self.planes[0][0].get_device()
+        if torch.cuda.current_device() != dev:
+            with torch.cuda.device(dev):
+                return self.shared_decode(layer, q, tables, table_rows, frontiers, shared_pages, scale, out, lse,
+                                          workspace, stream)
+        pq = _cuda(q, torch.bfloat16, (B, T, Hq, self.D), "q", dev)
+        pt = _cuda(tables, torch.int32, (self.C, self.L), "tables", dev)
+        pr = _cuda(table_rows, torch.int32, (B,), "table_rows", dev)
+        pf = _cuda(frontiers, torch.int32, (B,), "frontiers", dev)
+        if shared_pages.get_device() != dev or shared_pages.dtype is not torch.int32 or shared_pages.numel() != 1:
             raise ValueError("shared_pages must be one int32 value on the pool's device")
-        out = torch.empty_like(q) if out is None else out
-        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev) if lse is None else lse
-        _cuda(out, torch.bfloat16, q.shape, "out", dev)
-        _cuda(lse, torch.float32, (B, T, Hq), "lse", dev)
-        ws = workspace if workspace is not None else self.shared_workspace(B, T, Hq)
-        with torch.cuda.device(dev):
-            s = _stream(stream)
-            if workspace is None and stream is not None:
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
+        po = _cuda(out, torch.bfloat16, q.shape, "out", dev)
+        pl = _cuda(lse, torch.float32, (B, T, Hq), "lse", dev)
+        ws = workspace
+        if ws is None:
+            ws = self.shared_workspace(B, T, Hq)
+            if stream is not None:
                 ws.record_stream(stream)
-            nk_paged_shared_decode_attention(_ptr(q), Hq, self.handle, layer, _ptr(tables), _ptr(table_rows),
-                                             _ptr(frontiers), _ptr(shared_pages), B, T, float(scale), _ptr(out),
-                                             _ptr(lse), _ptr(ws), ws.numel(), s)
+        nk_paged_shared_decode_attention(pq, Hq, self.handle, layer, pt, pr, pf, shared_pages.data_ptr(), B, T,
+                                         float(scale), po, pl, ws.data_ptr(), ws.numel(), _stream(stream))
         return out, lse

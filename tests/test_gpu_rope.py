@@ -97,8 +97,8 @@ def test_norm_rope_one_operand_and_one_token():
     qo, ko = nk.qk_norm_rope(q, k, pos, rope)
     a, b = torch.zeros_like(q), torch.zeros_like(k)
     s = torch.cuda.current_stream().cuda_stream
-    nk.nk_qk_norm_rope(rope.desc, D, nk._rows(q, D), Hq, None, 0, pos.data_ptr(), 1, nk._rows(a, D), None, s)
-    nk.nk_qk_norm_rope(rope.desc, D, None, 0, nk._rows(k, D), H, pos.data_ptr(), 1, None, nk._rows(b, D), s)
+    nk.nk_qk_norm_rope(rope.desc, D, nk._rows(q, D, 0), Hq, None, 0, pos.data_ptr(), 1, nk._rows(a, D, 0), None, s)
+    nk.nk_qk_norm_rope(rope.desc, D, None, 0, nk._rows(k, D, 0), H, pos.data_ptr(), 1, None, nk._rows(b, D, 0), s)
     assert torch.equal(a, qo) and torch.equal(b, ko)
 
 

@@ -165,6 +165,6 @@ def test_python_wrappers_refuse_cpu_tensors():
     with pytest.raises(ValueError):
         nk.Rope(torch.zeros((4, 32)), 32)
     with pytest.raises(ValueError):
-        nk._rows(t, 64)
+        nk._rows(t, 64, 0)
     with pytest.raises(ValueError):
         nk.verify_drafts(torch.zeros((1, 2, 5)), torch.zeros((1, 1), dtype=torch.int32), torch.zeros((1, 2)))
