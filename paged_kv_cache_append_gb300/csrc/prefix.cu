@@ -1,0 +1,737 @@
+// prefix.cu -- the prefix pass of the shared-prefix attention at head_dim 64
+// and 128 (shared.cu): the R = B T G query rows of a batch that read one KV
+// head, at most 256, against the pages that all of them share, on the
+// 5th-generation tensor cores.
+//
+// A CTA takes one KV head and one range of the shared pages and leaves one
+// partial (m, l, O) for all R rows.  It runs two pipelines of 128 query rows,
+//   S_w = Q_w K^T   tcgen05.mma M 128 x N 64 x K D, Q_w and the K page in
+//                   shared memory, S_w in one of two TMEM buffers
+//   O_w += P_w V    tcgen05.mma M 128 x N D x K 64, P_w over its S_w (TMEM)
+// each with its own MMA-issuing thread and softmax warpgroup:
+//   R > 128   the pipelines hold the two halves of the rows and read every
+//             page, which is loaded and dequantized once for both;
+//   R <= 128  they hold the same rows and take the even and the odd pages;
+//             their partials are merged before they leave the CTA.
+// One issuing thread is what bounds the one-pipeline kernels (prefill.cu,
+// qprefill.cu): N = 64 products and the waits around them keep it busy.
+//
+// Operands and their exactness are those of qprefill.cu (dequantization in
+// shared memory, FP8 keys raw at head_dim 128, INT8 keys as two tiles, per-key
+// factors, the lift of FP8-row values) and of prefill.cu for BF16, except that
+// BF16 softmax weights enter as two bf16 terms (hi + lo, 16 bits): the tensor
+// time of the second product hides behind HBM there.  No mask: every row sees
+// every page whole.
+//
+// The softmax reads each score once on most pages: it computes the weights
+// against the reference maximum that it has, with the page's maximum on the
+// side, and only where that passes the reference by more than 2^8 does it read
+// the scores again (they are intact until P is stored).  32 columns are in
+// registers at a time, which 608 threads (96 registers) need.
+//
+// Warps: 0-3 and 4-7 softmax and output of the pipelines, 8 TMA producer, 9
+// and 10 MMA issuers, 11-18 converters (quantized pools).  All waits are
+// bounded.
+#include "internal.h"
+#include "prefill_split.cuh"
+#include "qtile.cuh"
+#include "shared.cuh"
+#include "tcgen05.cuh"
+
+namespace nk {
+
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+struct PrefixArgs {
+  const __nv_bfloat16* q;  // [B][T][Hq][D]
+  const int32_t* tables;
+  const int32_t* table_rows;
+  const uint8_t* ks;  // scale planes of the layer
+  const uint8_t* vs;
+  float2* ml;  // [H][tiles][nsplit][128]
+  float* o;    // [H][tiles][nsplit][128][D]
+  int* status;
+  float scale_log2;
+  int rows;  // R
+  int nsplit, Hq, H, G, L, M, C, head_major;
+  SharedPrefix sh;
+};
+
+template <int KK, int KV, int D>
+struct PrefixCfg {
+  static constexpr bool RAW = KK != KIND_BF16;  // quantized: raw rings and converters
+  using Q = QCfg<RAW ? KK : KIND_FP8, RAW ? KV : KIND_FP8, D>;  // (their geometry)
+  static constexpr int THREADS = RAW ? 608 : 352;
+  static constexpr int F16 = 64 * D * 2;
+  // Rings: those of qprefill.cu where 64 KB (32 KB at head_dim 64) of Q fit
+  // next to them.
+  static constexpr bool WIDE = D == 128;
+  static constexpr int NK = !RAW ? (WIDE ? 4 : 6) : Q::NK == 0 ? 0 : !WIDE ? Q::NK : KK == KIND_INT8 ? 2 : 3;
+  static constexpr int NV = !RAW ? NK : Q::NK == 0 ? Q::NV : !WIDE ? Q::NV : 3;
+  static constexpr int NRK = !RAW ? 0 : WIDE && KK == KIND_INT8 ? 2 : Q::NRK;
+  static constexpr int NRV = !RAW ? 0 : WIDE && KK == KIND_INT8 ? 3 : Q::NRV;
+  static constexpr int NF = RAW ? Q::NF : 0;
+  static constexpr int NKF = NK;
+  static constexpr int K_STAGE = RAW ? Q::K_STAGE : F16;
+  static constexpr int OFF_V = NK * K_STAGE;
+  static constexpr int OFF_RK = OFF_V + NV * F16;
+  static constexpr int OFF_RV = OFF_RK + NRK * (RAW ? Q::RK_STAGE : 0);
+  static constexpr int OFF_Q = OFF_RV + NRV * (RAW ? Q::RV_STAGE : 0);
+  // Q of a pipeline: blocks of 128 rows x 128 bytes (64 bf16 / f16 dims; the
+  // hi, then the lo E4M3 terms of 128 dims), 128-byte swizzle
+  static constexpr int Q_BYTES = 128 * D * 2;
+  static constexpr int OFF_F = OFF_Q + 2 * Q_BYTES;
+  static constexpr int OFF_ML = OFF_F + NF * 512;  // [128] float2: pipeline 1's (m, l)
+  static constexpr int OFF_BAR = OFF_ML + 1024;
+  static constexpr int NBAR = 2 * NKF + 2 * NV + 2 * NRK + 2 * NRV + 2 * NF + 10;
+  // at least half of the SM's shared memory: one CTA per SM owns all 512 TMEM columns
+  static constexpr int USED = OFF_BAR + NBAR * 8 + 64 + 1024;
+  static constexpr int SMEM = USED > 116 * 1024 ? USED : 116 * 1024;
+  // output rows on their way to global memory, over the rings and Q
+  static constexpr int PITCH = D + 4;
+  static_assert(256 * PITCH * 4 <= OFF_F, "staged output rows");
+  static constexpr uint32_t COL_S = 0, COL_O = 256;  // + 128 w + 64 (buffer), + 128 w
+  static constexpr bool K8MMA = RAW && Q::K8MMA;
+  static constexpr bool K_SPLIT = RAW && Q::K_SPLIT;
+  static constexpr uint32_t ID_S = !RAW    ? tc::idesc_bf16(128, 64, false, false)
+                                   : K8MMA ? tc::idesc_e4m3(128, 64)
+                                           : tc::idesc_f16(128, 64, false, false);
+  static constexpr uint32_t ID_O = RAW ? tc::idesc_f16(128, D, false, true) : tc::idesc_bf16(128, D, false, true);
+  static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+};
+
+// One query row (D bf16 values at src, zeros for nullptr) to row m of the
+// pipeline's Q in shared memory, in the form its MMA reads; returns 2^-e of
+// its power-of-two scale (1 for BF16).
+template <int KK, int KV, int D>
+__device__ __forceinline__ float prefix_query(const uint4* src, uint8_t* sq, int m) {
+  using Cfg = PrefixCfg<KK, KV, D>;
+  const auto x = [&](int u) { return src ? src[u] : make_uint4(0u, 0u, 0u, 0u); };
+  // 16-byte chunk c of row m
+  auto put = [&](int c, uint4 v) {
+    *reinterpret_cast<uint4*>(sq + (c >> 3) * 16384 + swz<128>(m, (c & 7) * 16)) = v;
+  };
+  if constexpr (!Cfg::RAW) {
+#pragma unroll
+    for (int u = 0; u < D / 8; ++u) put(u, x(u));
+    return 1.f;
+  } else {
+    float mx = 0.f;
+#pragma unroll
+    for (int u = 0; u < D / 8; ++u) {
+      const uint4 y = x(u);
+      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
+    }
+    int ex = 0;
+    if (mx > 0.f) frexpf(mx, &ex);
+    // f16 q: max|q| 2^e in [2^14, 2^15); E4M3 q: in [2^7, 2^8), as hi + lo (see qprefill.cu)
+    const int e = mx > 0.f ? min((Cfg::K8MMA ? 8 : 15) - ex, 100) : 0;
+    const float qf = ldexpf(1.f, e);
+    if constexpr (Cfg::K8MMA) {
+      static_assert(D == 128, "one 128-byte block per term");
+#pragma unroll 2
+      for (int c = 0; c < D / 16; ++c) {  // 16 dims: 16 bytes of hi, 16 of lo
+        uint32_t hv[4], lv[4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint4 y = x(2 * c + u);
+          const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+          uint32_t hp[4], lp[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float x0 = __uint_as_float(w[k] << 16) * qf, x1 = __uint_as_float(w[k] & 0xFFFF0000u) * qf;
+            const uint16_t h2 = f32x2_to_e4m3x2(x0, x1);
+            const uint32_t hb32 = e4m3x2_to_f16x2(h2);
+            const __half2 hb = *reinterpret_cast<const __half2*>(&hb32);
+            hp[k] = h2;
+            lp[k] = f32x2_to_e4m3x2(x0 - __low2float(hb), x1 - __high2float(hb));
+          }
+          hv[2 * u] = hp[0] | (hp[1] << 16);
+          hv[2 * u + 1] = hp[2] | (hp[3] << 16);
+          lv[2 * u] = lp[0] | (lp[1] << 16);
+          lv[2 * u + 1] = lp[2] | (lp[3] << 16);
+        }
+        put(c, make_uint4(hv[0], hv[1], hv[2], hv[3]));
+        put(8 + c, make_uint4(lv[0], lv[1], lv[2], lv[3]));
+      }
+    } else {
+#pragma unroll 4
+      for (int u = 0; u < D / 8; ++u) {
+        const uint4 y = x(u);
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+        uint32_t v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[k] = pack_f16x2(__uint_as_float(w[k] << 16) * qf, __uint_as_float(w[k] & 0xFFFF0000u) * qf);
+        put(u, make_uint4(v[0], v[1], v[2], v[3]));
+      }
+    }
+    return ldexpf(1.f, -e);
+  }
+}
+
+template <int KK, int KV, int D>
+__global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                  const __grid_constant__ PrefixArgs a) {
+  using Cfg = PrefixCfg<KK, KV, D>;
+  using QC = typename Cfg::Q;
+  constexpr int NK = Cfg::NK, NV = Cfg::NV, NRK = Cfg::NRK, NRV = Cfg::NRV, NF = Cfg::NF;
+  constexpr int NCONV = QC::NCONV;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sK = smem;
+  uint8_t* sV = smem + Cfg::OFF_V;
+  uint8_t* sRK = smem + Cfg::OFF_RK;
+  uint8_t* sRV = smem + Cfg::OFF_RV;
+  uint8_t* sQ = smem + Cfg::OFF_Q;
+  float* sF = reinterpret_cast<float*>(smem + Cfg::OFF_F);  // [NF][128]: 64 K factors, 64 V factors
+  float2* sML = reinterpret_cast<float2*>(smem + Cfg::OFF_ML);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
+  uint64_t* k_full = bars;               // K tile ready for the MMA
+  uint64_t* k_empty = k_full + Cfg::NKF;  // read by its last S
+  uint64_t* v_full = k_empty + Cfg::NKF;
+  uint64_t* v_empty = v_full + NV;
+  uint64_t* rk_full = v_empty + NV;  // raw tiles landed / consumed
+  uint64_t* rk_empty = rk_full + NRK;
+  uint64_t* rv_full = rk_empty + NRK;
+  uint64_t* rv_empty = rv_full + NRV;
+  uint64_t* f_full = rv_empty + NRV;  // per-key factors of a page
+  uint64_t* f_empty = f_full + NF;
+  uint64_t* s_full = f_empty + NF;  // [2][2] scores of pipeline w in buffer i & 1
+  uint64_t* p_full = s_full + 4;    // [2] its weights stored
+  uint64_t* o_done = p_full + 2;    // [2] its P V accumulated
+  uint64_t* q_ready = o_done + 2;
+  uint64_t* drain = q_ready + 1;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = blockIdx.x, h = blockIdx.y;
+  const bool two = a.rows > 128;   // the pipelines hold different rows
+  const int readers = two ? 2 : 1;  // pipelines that read a page
+  if (tid == 0) {
+    for (int i = 0; i < Cfg::NKF; ++i) {
+      mbar_init(&k_full[i], Cfg::RAW ? NCONV : 1);
+      mbar_init(&k_empty[i], readers);
+    }
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(&v_full[i], Cfg::RAW ? NCONV : 1);
+      mbar_init(&v_empty[i], readers);
+    }
+    for (int i = 0; i < NRK; ++i) {
+      mbar_init(&rk_full[i], 1);
+      mbar_init(&rk_empty[i], Cfg::K8MMA ? readers + NCONV : NCONV);
+    }
+    for (int i = 0; i < NRV; ++i) {
+      mbar_init(&rv_full[i], 1);
+      mbar_init(&rv_empty[i], NCONV);
+    }
+    for (int i = 0; i < NF; ++i) {
+      mbar_init(&f_full[i], NCONV);
+      mbar_init(&f_empty[i], 4 * readers);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&s_full[2 * w], 1);
+      mbar_init(&s_full[2 * w + 1], 1);
+      mbar_init(&p_full[w], 4);
+      mbar_init(&o_done[w], 1);
+    }
+    mbar_init(q_ready, 8);
+    mbar_init(drain, 2);
+    *s_abort = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tmk);
+    prefetch_tmap(&tmv);
+  }
+  if (warp == 0) {
+    tc::alloc(tslot, 512);
+    tc::relinquish();
+  }
+  griddep_wait();  // launched with programmatic stream serialization
+  griddep_launch_dependents();
+
+  // ---- this CTA's pages [p_lo, p_lo + n) -----------------------------------------
+  const int pages = *a.sh.pages;
+  const int row = prefix_row(a.sh, a.table_rows, pages, a.L, a.C);
+  const int all = row < 0 ? 0 : pages;
+  const int per = (all + a.nsplit - 1) / a.nsplit;
+  const int p_lo = min(split * per, all);
+  const int n = min(p_lo + per, all) - p_lo;
+  const int32_t* table = a.tables + static_cast<int64_t>(max(row, 0)) * a.L + p_lo;
+  // page i of pipeline w, and how many it takes
+  auto page_of = [&](int w, int i) { return two ? i : 2 * i + w; };
+  auto count_of = [&](int w) { return two ? n : (n - w + 1) / 2; };
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tslot;
+
+  if (warp == 8) {
+    // ------------------------------ TMA producer ---------------------------------
+    int gnext = 0;
+    for (int j = 0; j < n; ++j) {
+      if ((j & 31) == 0) gnext = (j + lane < n) ? table[j + lane] : 0;
+      int g = __shfl_sync(0xffffffffu, gnext, j & 31);
+      int stop = 0;
+      if (lane == 0) {
+        if (g < 0 || g >= a.M) {  // never copy from outside the pool
+          set_status(a.status, NK_STATUS_PAGE_RANGE);
+          g = 0;
+        }
+        const int y = static_cast<int>(tile_row(g, h, a.H, a.M, a.head_major));
+        if constexpr (Cfg::RAW) {
+          const int rk = j % NRK, rv = j % NRV;
+          if (j >= NRK && !mbar_wait_bounded(&rk_empty[rk], ((j / NRK) - 1) & 1, a.status)) stop = 1;
+          if (!stop) {
+            uint8_t* st = sRK + rk * QC::RK_STAGE;
+            mbar_arrive_expect_tx(&rk_full[rk], 64 * QC::KCB + 64 * QC::KSB);
+#pragma unroll
+            for (int c = 0; c < QC::KCB / QC::K_RB; ++c)
+              tma_load_2d(st + c * 64 * QC::K_RB, &tmk, c * QC::K_RB, y, &rk_full[rk]);
+            bulk_load(st + QC::RK_CODES, a.ks + static_cast<int64_t>(y) * QC::KSB, 64 * QC::KSB, &rk_full[rk]);
+          }
+          if (!stop && j >= NRV && !mbar_wait_bounded(&rv_empty[rv], ((j / NRV) - 1) & 1, a.status)) stop = 1;
+          if (!stop) {
+            uint8_t* st = sRV + rv * QC::RV_STAGE;
+            mbar_arrive_expect_tx(&rv_full[rv], 64 * QC::VCB + 64 * QC::VSB);
+#pragma unroll
+            for (int c = 0; c < QC::VCB / QC::V_RB; ++c)
+              tma_load_2d(st + c * 64 * QC::V_RB, &tmv, c * QC::V_RB, y, &rv_full[rv]);
+            bulk_load(st + QC::RV_CODES, a.vs + static_cast<int64_t>(y) * QC::VSB, 64 * QC::VSB, &rv_full[rv]);
+          }
+        } else {
+          const int ks = j % NK, vs = j % NV;
+          if (j >= NK && !mbar_wait_bounded(&k_empty[ks], ((j / NK) - 1) & 1, a.status)) stop = 1;
+          if (!stop) {
+            mbar_arrive_expect_tx(&k_full[ks], Cfg::F16);
+#pragma unroll
+            for (int kb = 0; kb < D / 64; ++kb)
+              tma_load_2d(sK + ks * Cfg::F16 + kb * 8192, &tmk, kb * 128, y, &k_full[ks]);
+          }
+          if (!stop && j >= NV && !mbar_wait_bounded(&v_empty[vs], ((j / NV) - 1) & 1, a.status)) stop = 1;
+          if (!stop) {
+            mbar_arrive_expect_tx(&v_full[vs], Cfg::F16);
+#pragma unroll
+            for (int kb = 0; kb < D / 64; ++kb)
+              tma_load_2d(sV + vs * Cfg::F16 + kb * 8192, &tmv, kb * 128, y, &v_full[vs]);
+          }
+        }
+        if (stop) *s_abort = 1;
+      }
+      if (__shfl_sync(0xffffffffu, stop, 0)) break;
+    }
+  } else if (warp >= 11) {
+    // ------------- converters: K(0), K(1), V(0), K(2), V(1), ... -------------------
+    if constexpr (Cfg::RAW) {
+      const int ct = tid - 352;
+      bool ok = true;
+      for (int i = 0; ok && i <= n; ++i) {
+        if (i < n) {  // K(i) and the factors of page i
+          const int rk = i % NRK, rv = i % NRV, fs = i % NF;
+          ok = mbar_wait_bounded(&rk_full[rk], (i / NRK) & 1, a.status) && !*s_abort;
+          if (!ok) break;
+          const uint8_t* raw = sRK + rk * QC::RK_STAGE;
+          const float kf = ct < 64 ? key_factor<KK, D>(raw + QC::RK_CODES, ct) * a.scale_log2 : 0.f;
+          if constexpr (!Cfg::K8MMA) {
+            const int ks = i % NK;
+            if (i >= NK) ok = mbar_wait_bounded(&k_empty[ks], ((i / NK) - 1) & 1, a.status) && !*s_abort;
+            if (!ok) break;
+            convert_tile<KK, D, QC::K_RB, 32 * NCONV, Cfg::K_SPLIT>(raw, QC::RK_CODES, sK + ks * Cfg::K_STAGE, ct, 64);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              arrive(&rk_empty[rk]);
+              arrive(&k_full[ks]);
+            }
+          }
+          ok = mbar_wait_bounded(&rv_full[rv], (i / NRV) & 1, a.status) && !*s_abort;
+          if (ok && i >= NF) ok = mbar_wait_bounded(&f_empty[fs], ((i / NF) - 1) & 1, a.status) && !*s_abort;
+          if (!ok) break;
+          if (ct < 64) {
+            float* fac = sF + fs * 128;
+            fac[ct] = kf;
+            fac[64 + ct] = key_factor<KV, D>(sRV + rv * QC::RV_STAGE + QC::RV_CODES, ct);
+          }
+          __syncwarp();
+          if (lane == 0) {
+            arrive(&f_full[fs]);
+            if constexpr (Cfg::K8MMA) arrive(&rk_empty[rk]);  // with the commits of the page's S
+          }
+        }
+        if (i >= 1) {  // V(i - 1)
+          const int jj = i - 1, rv = jj % NRV, vs = jj % NV;
+          ok = mbar_wait_bounded(&rv_full[rv], (jj / NRV) & 1, a.status) && !*s_abort;
+          if (ok && jj >= NV) ok = mbar_wait_bounded(&v_empty[vs], ((jj / NV) - 1) & 1, a.status) && !*s_abort;
+          if (!ok) break;
+          convert_tile<KV, D, QC::V_RB, 32 * NCONV>(sRV + rv * QC::RV_STAGE, QC::RV_CODES, sV + vs * Cfg::F16, ct, 64);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            arrive(&rv_empty[rv]);
+            arrive(&v_full[vs]);
+          }
+        }
+      }
+      if (!ok) *s_abort = 1;
+    }
+  } else if (warp >= 9) {
+    // --------------------- MMA issuer of pipeline w ---------------------------
+    // S(0), S(1), P(0) V, S(2), P(1) V, ...: the MMAs of one thread run in
+    // issue order, so S(i + 1) cannot overwrite the P(i - 1) in its buffer early
+    if (lane == 0) {
+      const int w = warp - 9, count = count_of(w), step = two ? 1 : 2;
+      const uint32_t tS = tmem + Cfg::COL_S + 128 * w, tO = tmem + Cfg::COL_O + 128 * w;
+      const uint64_t qd = tc::smem_desc(smem_u32(sQ + w * Cfg::Q_BYTES), 16, 1024);
+      constexpr int RK = Cfg::K8MMA ? NRK : NK, KS = Cfg::K8MMA ? QC::RK_STAGE : Cfg::K_STAGE;
+      const uint64_t kd0 = tc::smem_desc(smem_u32(Cfg::K8MMA ? sRK : sK), 16, 1024);
+      const uint64_t vd0 = tc::smem_desc(smem_u32(sV), 8192, 1024);
+      uint64_t* kfull = Cfg::K8MMA ? rk_full : k_full;
+      uint64_t* kempty = Cfg::K8MMA ? rk_empty : k_empty;
+      int ks = two ? 0 : w, kph = 0, vs = ks, vph = 0;  // ring slots and parities of the next K and V page
+      auto scores = [&](int i) {
+        if (!mbar_wait_bounded(&kfull[ks], kph, a.status)) return false;
+        tc::fence_after();
+        const uint32_t d = tS + 64 * (i & 1);
+        const uint64_t kd = kd0 + static_cast<uint64_t>((ks * KS) >> 4);
+        if constexpr (Cfg::K8MMA) {
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              tc::mma_ss_f8(d, qd + static_cast<uint64_t>((part * 16384 + kk * 32) >> 4),
+                            kd + static_cast<uint64_t>((kk * 32) >> 4), Cfg::ID_S, part > 0 || kk > 0);
+        } else {
+#pragma unroll
+          for (int part = 0; part < (Cfg::K_SPLIT ? 2 : 1); ++part)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma_ss(d, qd + static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                         kd + static_cast<uint64_t>((part * Cfg::F16 + (kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
+                         part > 0 ? tc::idesc_negate_b(Cfg::ID_S) : Cfg::ID_S, part > 0 || kk > 0);
+        }
+        tc::commit(&s_full[2 * w + (i & 1)]);
+        tc::commit(&kempty[ks]);
+        if ((ks += step) >= RK) ks -= RK, kph ^= 1;
+        return true;
+      };
+      bool ok = mbar_wait_bounded(q_ready, 0, a.status);
+      tc::fence_after();
+      if (ok && count > 0) ok = scores(0);
+      for (int i = 0; ok && i < count; ++i) {
+        if (i + 1 < count) ok = scores(i + 1);
+        if (ok) ok = mbar_wait_bounded(&v_full[vs], vph, a.status);
+        if (ok) ok = mbar_wait_bounded(&p_full[w], i & 1, a.status) && !*s_abort;
+        if (!ok) break;
+        tc::fence_after();
+        const uint64_t vd = vd0 + static_cast<uint64_t>((vs * Cfg::F16) >> 4);
+#pragma unroll
+        for (int part = 0; part < (Cfg::RAW ? 1 : 2); ++part)  // BF16: the hi and the lo weights
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc::mma_ts(tO, tS + 64 * (i & 1) + 32 * part + kk * 8, vd + static_cast<uint64_t>((kk * 2048) >> 4),
+                       Cfg::ID_O, i > 0 || part > 0 || kk > 0);
+        tc::commit(&o_done[w]);
+        tc::commit(&v_empty[vs]);
+        if ((vs += step) >= NV) vs -= NV, vph ^= 1;
+      }
+      if (!ok) *s_abort = 1;
+      tc::commit(drain);  // arrives once every MMA issued above has completed
+    }
+  } else {
+    // --------------------- softmax warps of pipeline w ---------------------------
+    const int w = warp >> 2, m = tid & 127;
+    const int flat = (two ? 128 * w : 0) + m;
+    const bool row_valid = flat < a.rows;
+    const bool live = __any_sync(0xffffffffu, row_valid);  // warps without rows only hand on
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tO = tmem + lane_base + Cfg::COL_O + 128 * w;
+    const uint4* src = nullptr;
+    if (row_valid) {
+      const int token = flat / a.G, g = flat % a.G;
+      src = reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(token) * a.Hq + h * a.G + g) * D);
+    }
+    const float rs = prefix_query<KK, KV, D>(src, sQ + w * Cfg::Q_BYTES, m);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) arrive(q_ready);
+
+    constexpr bool KEY_FAC = Cfg::RAW && KK != KIND_NVFP4;  // per-key score factors
+    constexpr bool VAL_FAC = Cfg::RAW && KV != KIND_NVFP4;  // per-key weight factors
+    constexpr int PK = Cfg::RAW ? 32 : 64;                  // columns of P
+    float m_used = -INFINITY, l = 0.f;
+    int k_run = KV == KIND_FP8 ? kVLiftInit : 0;  // FP8-row V: the weights, l and O carry 2^k_run (v_lift)
+    bool ok = true;
+    const int count = count_of(w);
+    for (int i = 0; i < count; ++i) {
+      const int j = page_of(w, i), fs = Cfg::RAW ? j % (NF > 0 ? NF : 1) : 0;
+      const uint32_t tS = tmem + lane_base + Cfg::COL_S + 128 * w + 64 * (i & 1);
+      ok = mbar_wait_bounded(&s_full[2 * w + (i & 1)], (i >> 1) & 1, a.status) && !*s_abort;
+      if constexpr (Cfg::RAW)
+        if (ok) ok = mbar_wait_bounded(&f_full[fs], (j / NF) & 1, a.status) && !*s_abort;
+      if (!ok) break;
+      tc::fence_after();
+      if (live) {
+        const float* ksc = sF + fs * 128;
+        const float* vsc = ksc + 64;
+        // 32 scores from column c0 on, times their factors
+        auto scaled = [&](int c0, float (&z)[32]) {
+          uint32_t v[32];
+          tc::ld32(tS + c0, v);
+          tc::wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            float4 f = make_float4(a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2);
+            if constexpr (KEY_FAC) f = *reinterpret_cast<const float4*>(ksc + c0 + c);
+            z[c] = __uint_as_float(v[c]) * f.x;
+            z[c + 1] = __uint_as_float(v[c + 1]) * f.y;
+            z[c + 2] = __uint_as_float(v[c + 2]) * f.z;
+            z[c + 3] = __uint_as_float(v[c + 3]) * f.w;
+          }
+        };
+        auto max32 = [](const float (&z)[32]) {
+          float t[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) t[c] = fmaxf(fmaxf(z[c], z[c + 8]), fmaxf(z[c + 16], z[c + 24]));
+          return fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+        };
+        int knew = k_run;
+        if constexpr (KV == KIND_FP8) {
+          const float2 s2 = *reinterpret_cast<const float2*>(vsc + 2 * lane);
+          knew = v_lift(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(s2.x, s2.y))), k_run);
+        }
+        float mnew = m_used;
+        if (__any_sync(0xffffffffu, m_used == -INFINITY)) {  // the first page: its maximum first
+          float z[32];
+          scaled(0, z);
+          float mx = max32(z);
+          scaled(32, z);
+          mx = fmaxf(mx, max32(z));
+          if (m_used == -INFINITY) mnew = mx == -INFINITY ? -INFINITY : mx * rs;
+        }
+        uint32_t pk[PK];
+        float sum = 0.f;
+        // p = 2^(z - mnew + knew); returns the page's largest z
+        auto weights = [&]() {
+          const float mu = (mnew == -INFINITY ? 0.f : mnew) - static_cast<float>(knew);
+          float mx = -INFINITY;
+          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+          for (int c0 = 0; c0 < 64; c0 += 32) {
+            float z[32];
+            scaled(c0, z);
+            mx = fmaxf(mx, max32(z));
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              float p0 = ex2(fmaf(z[c], rs, -mu)), p1 = ex2(fmaf(z[c + 1], rs, -mu));
+              float p2 = ex2(fmaf(z[c + 2], rs, -mu)), p3 = ex2(fmaf(z[c + 3], rs, -mu));
+              s0 += p0, s1 += p1, s2 += p2, s3 += p3;
+              if constexpr (VAL_FAC) {
+                const float4 f = *reinterpret_cast<const float4*>(vsc + c0 + c);
+                p0 *= f.x, p1 *= f.y, p2 *= f.z, p3 *= f.w;
+              }
+              const int k = (c0 + c) / 2;
+              if constexpr (Cfg::RAW) {
+                pk[k] = pack_f16x2(p0, p1);
+                pk[k + 1] = pack_f16x2(p2, p3);
+              } else {
+                pk[k] = pack_bf16x2(p0, p1);
+                pk[k + 1] = pack_bf16x2(p2, p3);
+                pk[32 + k] = pack_bf16x2(p0 - __uint_as_float(pk[k] << 16), p1 - __uint_as_float(pk[k] & 0xFFFF0000u));
+                pk[33 + k] = pack_bf16x2(p2 - __uint_as_float(pk[k + 1] << 16),
+                                         p3 - __uint_as_float(pk[k + 1] & 0xFFFF0000u));
+              }
+            }
+          }
+          sum = (s0 + s1) + (s2 + s3);
+          return mx;
+        };
+        const float top = weights() * rs;
+        const bool over = top > mnew + kLazyThr;
+        if (__any_sync(0xffffffffu, over)) {
+          if (over) mnew = top;
+          weights();
+        }
+        const bool resc = mnew != m_used || knew != k_run;
+        const float factor = m_used == -INFINITY ? 0.f
+                             : resc              ? ex2((m_used - mnew) + static_cast<float>(knew - k_run))
+                                                 : 1.f;
+        l = l * factor + sum;
+        m_used = mnew;
+        k_run = knew;
+        __syncwarp();
+        if constexpr (Cfg::RAW)
+          if (lane == 0) arrive(&f_empty[fs]);
+        // PV(i - 1) is consumed on every page: a parity wait is sound one phase at a time
+        if (i >= 1) {
+          ok = mbar_wait_bounded(&o_done[w], (i - 1) & 1, a.status) && !*s_abort;
+          if (!ok) break;
+          tc::fence_after();
+          if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t ov[32];
+              tc::ld32(tO + c0, ov);
+              tc::wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * factor);
+              tc::st32(tO + c0, ov);
+            }
+          }
+        }
+#pragma unroll
+        for (int c0 = 0; c0 < PK; c0 += 32) tc::st32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(&pk[c0]));
+        tc::wait_st();
+      } else {  // a warp without rows hands on, in step: it must not arrive for P(i) before P(i - 1) is used
+        if constexpr (Cfg::RAW)
+          if (lane == 0) arrive(&f_empty[fs]);
+        if (i >= 1) ok = mbar_wait_bounded(&o_done[w], (i - 1) & 1, a.status) && !*s_abort;
+        if (!ok) break;
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(&p_full[w]);
+    }
+
+    // ---- the CTA's partial: rows by way of shared memory, whole lines out ---------
+    ok = mbar_wait_bounded(drain, 0, a.status) && ok && !*s_abort;  // every MMA done: the rings are free
+    tc::fence_after();
+    const float m_eff = m_used == -INFINITY ? -INFINITY : m_used - static_cast<float>(k_run);
+    float* stage = reinterpret_cast<float*>(smem);
+    float* mine = stage + flat * Cfg::PITCH;
+    const int tiles = two ? 2 : 1;
+    // pipeline w's output times f, plus f1 times what the row holds already
+    auto put = [&](bool has, float f, bool add, float f1) {
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t ov[32];
+        if (has) {
+          tc::ld32(tO + c0, ov);
+          tc::wait_ld();
+        }
+        if (!row_valid) continue;
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          float4* at = reinterpret_cast<float4*>(mine + c0 + c);
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (add) {
+            v = *at;
+            v.x *= f1, v.y *= f1, v.z *= f1, v.w *= f1;
+          }
+          if (has) {
+            v.x = fmaf(__uint_as_float(ov[c]), f, v.x);
+            v.y = fmaf(__uint_as_float(ov[c + 1]), f, v.y);
+            v.z = fmaf(__uint_as_float(ov[c + 2]), f, v.z);
+            v.w = fmaf(__uint_as_float(ov[c + 3]), f, v.w);
+          }
+          *at = v;
+        }
+      }
+    };
+    float M = m_eff, L = l;
+    if (two) {
+      if (ok && live && n > 0) put(true, 1.f, false, 0.f);
+    } else {
+      if (w == 1) {
+        sML[m] = make_float2(m_eff, l);
+        if (ok && live && count > 0) put(true, 1.f, false, 0.f);
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (w == 0 && count_of(1) > 0) {
+        const float2 o = sML[m];
+        M = fmaxf(m_eff, o.x);
+        const float f0 = m_eff == -INFINITY ? 0.f : ex2(m_eff - M), f1 = o.x == -INFINITY ? 0.f : ex2(o.x - M);
+        L = l * f0 + o.y * f1;
+        if (ok && live) put(true, f0, true, f1);
+      } else if (w == 0 && n > 0) {
+        if (ok && live) put(true, 1.f, false, 0.f);
+      }
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (ok) {
+      if (row_valid && (two || w == 0)) {
+        const int64_t part = (static_cast<int64_t>(h) * tiles + flat / 128) * a.nsplit + split;
+        a.ml[part * 128 + flat % 128] = make_float2(n > 0 ? M : -INFINITY, n > 0 ? L : 0.f);
+      }
+      if (n > 0) {
+        for (int idx = tid; idx < a.rows * (D / 4); idx += 256) {
+          const int r = idx / (D / 4), c = (idx % (D / 4)) * 4;
+          const int64_t part = (static_cast<int64_t>(h) * tiles + r / 128) * a.nsplit + split;
+          *reinterpret_cast<float4*>(a.o + (part * 128 + r % 128) * D + c) =
+              *reinterpret_cast<const float4*>(stage + r * Cfg::PITCH + c);
+        }
+      }
+    }
+  }
+
+  // ---- teardown: every issued MMA has completed before TMEM is freed ---------
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 0) tc::dealloc(tmem, 512);
+}
+
+template <int KK, int KV, int D>
+static cudaError_t launch_prefix(const nk_pool* p, int layer, const PrefixArgs& a, cudaStream_t s) {
+  using Cfg = PrefixCfg<KK, KV, D>;
+  auto k = prefix_kernel<KK, KV, D>;
+  static bool attr = false;
+  if (!attr) {
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+    if (e != cudaSuccess) return e;
+    attr = true;
+  }
+  return launch_pdl(k, dim3(a.nsplit, a.H), dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0],
+                    p->tmap[layer * 2 + 1], a);
+}
+
+// head_dim 64 or 128, at most 256 query rows per KV head.
+cudaError_t prefix_pass(const nk_pool* p, int layer, const void* q, const int32_t* tables, const int32_t* table_rows,
+                        int Hq, float scale_log2, const PrefillSplit& sp, const SharedPrefix& sh, cudaStream_t s) {
+  const int np = p->n_planes;
+  PrefixArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.tables = tables;
+  a.table_rows = table_rows;
+  a.ks = np == 4 ? static_cast<const uint8_t*>(p->ptrs[layer * np + 2]) : nullptr;
+  a.vs = np == 4 ? static_cast<const uint8_t*>(p->ptrs[layer * np + 3]) : nullptr;
+  a.ml = sp.ws_ml;
+  a.o = sp.ws_o;
+  a.status = p->status;
+  a.scale_log2 = scale_log2;
+  a.nsplit = sp.nsplit;
+  a.Hq = Hq;
+  a.H = p->desc.num_kv_heads;
+  a.G = Hq / a.H;
+  a.rows = sh.B * sh.T * a.G;
+  a.L = p->L;
+  a.M = p->M;
+  a.C = p->desc.max_concurrency;
+  a.head_major = p->desc.order == NK_HEAD_MAJOR;
+  a.sh = sh;
+  const bool wide = p->desc.head_dim == 128;
+  switch (p->desc.profile) {
+    case NK_BF16:
+      return wide ? launch_prefix<KIND_BF16, KIND_BF16, 128>(p, layer, a, s)
+                  : launch_prefix<KIND_BF16, KIND_BF16, 64>(p, layer, a, s);
+    case NK_INT8_G64:
+      return wide ? launch_prefix<KIND_INT8, KIND_INT8, 128>(p, layer, a, s)
+                  : launch_prefix<KIND_INT8, KIND_INT8, 64>(p, layer, a, s);
+    case NK_FP8_E4M3_ROW:
+      return wide ? launch_prefix<KIND_FP8, KIND_FP8, 128>(p, layer, a, s)
+                  : launch_prefix<KIND_FP8, KIND_FP8, 64>(p, layer, a, s);
+    case NK_NVFP4_G16:
+      return wide ? launch_prefix<KIND_NVFP4, KIND_NVFP4, 128>(p, layer, a, s)
+                  : launch_prefix<KIND_NVFP4, KIND_NVFP4, 64>(p, layer, a, s);
+    default:
+      return wide ? launch_prefix<KIND_FP8, KIND_NVFP4, 128>(p, layer, a, s)
+                  : launch_prefix<KIND_FP8, KIND_NVFP4, 64>(p, layer, a, s);
+  }
+}
+
+}  // namespace nk

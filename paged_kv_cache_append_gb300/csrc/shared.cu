@@ -27,6 +27,9 @@ cudaError_t prefix_pass_quantized(const nk_pool* p, int layer, const void* q, co
                                   const int32_t* table_rows, int Hq, float scale_log2, const PrefillSplit& sp,
                                   const SharedPrefix& sh, cudaStream_t s);
 
+cudaError_t prefix_pass(const nk_pool* p, int layer, const void* q, const int32_t* tables, const int32_t* table_rows,
+                        int Hq, float scale_log2, const PrefillSplit& sp, const SharedPrefix& sh, cudaStream_t s);
+
 constexpr int kMaxPrefixSplits = 128;
 
 struct SharedPlan {
@@ -40,7 +43,8 @@ static int make_shared_plan(const nk_pool* p, int B, int T, int Hq, SharedPlan* 
   if (rc) return rc;
   const int H = p->desc.num_kv_heads, D = p->desc.head_dim, G = Hq / H;
   pl->tiles = (B * T * G + 127) / 128;
-  const int fit = p->num_sms / (H * pl->tiles);  // one CTA per SM
+  // one CTA per SM; at head_dim 64 and 128 one CTA takes both tiles of a head
+  const int fit = p->num_sms / (H * (D == 256 ? pl->tiles : 1));
   pl->nsplit = fit < 1 ? 1 : fit > kMaxPrefixSplits ? kMaxPrefixSplits : fit;
   const size_t parts = static_cast<size_t>(H) * pl->tiles * pl->nsplit * 128;
   pl->sh_ml_bytes = parts * sizeof(float2);
@@ -254,7 +258,9 @@ extern "C" int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const
   sp.ws_ml = reinterpret_cast<float2*>(ws);
   sp.ws_o = reinterpret_cast<float*>(ws + pl.sh_ml_bytes);
   sp.partial = true;
-  auto pass = pool->desc.profile == NK_BF16 ? prefix_pass_bf16 : prefix_pass_quantized;
+  auto pass = pool->desc.head_dim <= 128       ? prefix_pass
+              : pool->desc.profile == NK_BF16 ? prefix_pass_bf16
+                                              : prefix_pass_quantized;
   e = pass(pool, layer, q, block_tables, table_rows, Hq, softmax_scale * kLog2e, sp, sh, s);
   if (e != cudaSuccess) return cuda_fail(e, "prefix pass launch");
   SharedMergeArgs m;

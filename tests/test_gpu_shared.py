@@ -157,6 +157,32 @@ def test_any_number_of_shared_pages(profile, pages):
     assert nk.nk_status_read(True, s) == (nk.STATUS_FRONTIER if pages < 0 else 0)
 
 
+@pytest.mark.parametrize("profile", PROFILES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,G,T,pages", [(2, 1, 1, 25), (8, 1, 3, 24), (3, 16, 2, 15), (6, 8, 4, 26), (8, 4, 4, 13)])
+def test_many_pages_per_range(profile, D, B, G, T, pages):
+    """So many KV heads that a range is many pages: the rings, the score
+    buffers and the parities go around several times; 2 to 192 query rows, so
+    that warps and whole pipelines are without rows."""
+    if T * G > (16 if D == 256 and profile in ("bf16", "int8_g64") else 32):
+        pytest.skip("not a decode of this profile")
+    H = 38
+    b = Batch(profile, D, H, G, T, pages, [64 * pages + T + 30 * i for i in range(B)])
+    out, lse = b.run(pages)
+    o2, l2 = (x.cpu() for x in b.gpu.decode(0, b.d["q"], b.d["tables"], b.d["rows"], b.d["F"], b.scale))
+    # every head against the decode (A <= max |v| < 6 for N(0, 1) values; both sides rounded), three against the oracle
+    assert (out.float() - o2.float()).abs().max() <= 2.0 ** -7 * o2.float().abs().max() + 2 * (2.0 ** -9 + 2e-3) * 6
+    assert (lse - l2).abs().max() <= 2e-3
+    rows = [r for h in (0, 17, H - 1) for r in range(h * G, (h + 1) * G)]
+    q = OF.bf16_bits_to_f64(bf16_to_bits(b.q))
+    for i in (0, B - 1):
+        K, V = b.img.gather(0, b.tables[b.rows[i]], int(b.F[i]))
+        heads = [0, 17, H - 1]
+        o, l = OA.decode(q[i][:, rows], K[:, heads], V[:, heads], int(b.F[i]), b.scale)
+        a, _ = OA.decode(q[i][:, rows], K[:, heads], np.abs(V[:, heads]), int(b.F[i]), b.scale)
+        check(out[i][:, rows], lse[i][:, rows], (o, l, a))
+
+
 def test_head_major_and_spare_table_rows():
     b = Batch("fp8_row", 128, 3, 4, 1, 6, [400, 500, 385], order="head_major", C=7)
     check(*b.run(6), b.reference())
