@@ -26,13 +26,15 @@
 // The softmax reads each score once on most pages: it computes the weights
 // against the reference maximum that it has, with the page's maximum on the
 // side, and only where that passes the reference by more than 2^8 does it read
-// the scores again (they are intact until P is stored).  32 columns are in
-// registers at a time, which 608 threads (96 registers) need.
+// the scores again (they are intact until P is stored).  16 columns are in
+// registers while the next 16 load, and two scores share an instruction where
+// fp32 has packed forms.
 //
 // Warps: 0-3 and 4-7 softmax and output of the pipelines, 8 TMA producer, 9
 // and 10 MMA issuers, 11-18 converters (quantized pools).  All waits are
 // bounded.
 #include "internal.h"
+#include "packed.cuh"
 #include "prefill_split.cuh"
 #include "qtile.cuh"
 #include "shared.cuh"
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
       const int token = flat / a.G, g = flat % a.G;
       src = reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(token) * a.Hq + h * a.G + g) * D);
     }
-    const float rs = prefix_query<KK, KV, D>(src, sQ + w * Cfg::Q_BYTES, m);
+    float rs = prefix_query<KK, KV, D>(src, sQ + w * Cfg::Q_BYTES, m);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) arrive(q_ready);
@@ -464,6 +466,11 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
     constexpr bool KEY_FAC = Cfg::RAW && KK != KIND_NVFP4;  // per-key score factors
     constexpr bool VAL_FAC = Cfg::RAW && KV != KIND_NVFP4;  // per-key weight factors
     constexpr int PK = Cfg::RAW ? 32 : 64;                  // columns of P
+    // exponents are z rs - m; without key factors z is the raw score and the
+    // softmax scale is in rs, with its sign in the direction of the maximum
+    const bool up = a.scale_log2 >= 0.f;
+    if constexpr (!KEY_FAC) rs *= a.scale_log2;
+    const float zmul = KEY_FAC ? rs : fabsf(rs);
     float m_used = -INFINITY, l = 0.f;
     int k_run = KV == KIND_FP8 ? kVLiftInit : 0;  // FP8-row V: the weights, l and O carry 2^k_run (v_lift)
     bool ok = true;
@@ -479,26 +486,43 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
       if (live) {
         const float* ksc = sF + fs * 128;
         const float* vsc = ksc + 64;
-        // 32 scores from column c0 on, times their factors
-        auto scaled = [&](int c0, float (&z)[32]) {
-          uint32_t v[32];
-          tc::ld32(tS + c0, v);
-          tc::wait_ld();
+        // The page's scores times their factors, 16 columns at a time, to
+        // body(c0, z[8 pairs]); the next 16 load while the body runs.
+        auto each16 = [&](auto body) {
+          uint32_t v[2][16];
+          tc::ld16(tS, v[0]);
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            float4 f = make_float4(a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2);
-            if constexpr (KEY_FAC) f = *reinterpret_cast<const float4*>(ksc + c0 + c);
-            z[c] = __uint_as_float(v[c]) * f.x;
-            z[c + 1] = __uint_as_float(v[c + 1]) * f.y;
-            z[c + 2] = __uint_as_float(v[c + 2]) * f.z;
-            z[c + 3] = __uint_as_float(v[c + 3]) * f.w;
+          for (int k = 0; k < 4; ++k) {
+            uint32_t(&u)[16] = v[k & 1];
+            tc::wait_ld16(u);
+            if (k < 3) tc::ld16(tS + 16 * (k + 1), v[(k + 1) & 1]);
+            F2 z[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) z[c] = pack2(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1]));
+            if constexpr (KEY_FAC) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(ksc + 16 * k + 4 * c);
+                z[2 * c] = mul2(z[2 * c], f.x);
+                z[2 * c + 1] = mul2(z[2 * c + 1], f.y);
+              }
+            }
+            body(16 * k, z);
           }
         };
-        auto max32 = [](const float (&z)[32]) {
-          float t[8];
+        // the larger of m and the eight pairs, of -z for a negative uniform scale
+        auto max16 = [&](float m, const F2 (&z)[8]) {
+          float x[16];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) t[c] = fmaxf(fmaxf(z[c], z[c + 8]), fmaxf(z[c + 16], z[c + 24]));
-          return fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+          for (int c = 0; c < 8; ++c) unpack2(z[c], x[2 * c], x[2 * c + 1]);
+          if (KEY_FAC || up) {
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) m = max3(m, x[c], x[c + 1]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) m = max3(m, -x[c], -x[c + 1]);
+          }
+          return m;
         };
         int knew = k_run;
         if constexpr (KV == KIND_FP8) {
@@ -507,35 +531,35 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
         }
         float mnew = m_used;
         if (__any_sync(0xffffffffu, m_used == -INFINITY)) {  // the first page: its maximum first
-          float z[32];
-          scaled(0, z);
-          float mx = max32(z);
-          scaled(32, z);
-          mx = fmaxf(mx, max32(z));
-          if (m_used == -INFINITY) mnew = mx == -INFINITY ? -INFINITY : mx * rs;
+          float mx = -INFINITY;
+          each16([&](int, const F2 (&z)[8]) { mx = max16(mx, z); });
+          if (m_used == -INFINITY) mnew = mx == -INFINITY ? -INFINITY : mx * zmul;
         }
         uint32_t pk[PK];
         float sum = 0.f;
-        // p = 2^(z - mnew + knew); returns the page's largest z
+        // p = 2^(z rs - mnew + knew); returns the page's largest score
         auto weights = [&]() {
           const float mu = (mnew == -INFINITY ? 0.f : mnew) - static_cast<float>(knew);
+          const F2 rs2 = pack2(rs, rs), nmu2 = pack2(-mu, -mu);
           float mx = -INFINITY;
-          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+          F2 s0 = 0ull, s1 = 0ull;
+          each16([&](int c0, const F2 (&z)[8]) {
+            mx = max16(mx, z);
 #pragma unroll
-          for (int c0 = 0; c0 < 64; c0 += 32) {
-            float z[32];
-            scaled(c0, z);
-            mx = fmaxf(mx, max32(z));
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              float p0 = ex2(fmaf(z[c], rs, -mu)), p1 = ex2(fmaf(z[c + 1], rs, -mu));
-              float p2 = ex2(fmaf(z[c + 2], rs, -mu)), p3 = ex2(fmaf(z[c + 3], rs, -mu));
-              s0 += p0, s1 += p1, s2 += p2, s3 += p3;
+            for (int c = 0; c < 8; c += 2) {
+              float p0, p1, p2, p3;
+              unpack2(fma2(z[c], rs2, nmu2), p0, p1);
+              unpack2(fma2(z[c + 1], rs2, nmu2), p2, p3);
+              p0 = ex2(p0), p1 = ex2(p1), p2 = ex2(p2), p3 = ex2(p3);
+              F2 pa = pack2(p0, p1), pb = pack2(p2, p3);
+              s0 = add2(s0, pa);
+              s1 = add2(s1, pb);
               if constexpr (VAL_FAC) {
-                const float4 f = *reinterpret_cast<const float4*>(vsc + c0 + c);
-                p0 *= f.x, p1 *= f.y, p2 *= f.z, p3 *= f.w;
+                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(vsc + c0 + 2 * c);
+                unpack2(mul2(pa, f.x), p0, p1);
+                unpack2(mul2(pb, f.y), p2, p3);
               }
-              const int k = (c0 + c) / 2;
+              const int k = c0 / 2 + c;
               if constexpr (Cfg::RAW) {
                 pk[k] = pack_f16x2(p0, p1);
                 pk[k + 1] = pack_f16x2(p2, p3);
@@ -547,11 +571,14 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
                                          p3 - __uint_as_float(pk[k + 1] & 0xFFFF0000u));
               }
             }
-          }
-          sum = (s0 + s1) + (s2 + s3);
+          });
+          float a0, a1, b0, b1;
+          unpack2(s0, a0, a1);
+          unpack2(s1, b0, b1);
+          sum = (a0 + a1) + (b0 + b1);
           return mx;
         };
-        const float top = weights() * rs;
+        const float top = weights() * zmul;
         const bool over = top > mnew + kLazyThr;
         if (__any_sync(0xffffffffu, over)) {
           if (over) mnew = top;

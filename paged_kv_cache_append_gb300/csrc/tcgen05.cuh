@@ -66,6 +66,17 @@ __device__ __forceinline__ void ld16(uint32_t addr, uint32_t (&v)[16]) {
       : "r"(addr));
 }
 
+// wait_ld for registers that other work separates from their use: they pass
+// through the wait, so that no use moves ahead of it.
+__device__ __forceinline__ void wait_ld16(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                 "+r"(v[15])
+               :
+               : "memory");
+}
+
 // Each thread of the warp writes 32 consecutive 32-bit columns of its lane.
 __device__ __forceinline__ void st32(uint32_t addr, const uint32_t (&v)[32]) {
   asm volatile(
