@@ -26,12 +26,12 @@
 // The softmax reads each score once on most pages: it computes the weights
 // against the reference maximum that it has, with the page's maximum on the
 // side, and only where that passes the reference by more than 2^8 does it read
-// the scores again (they are intact until P is stored).  16 columns are in
-// registers while the next 16 load, and two scores share an instruction where
-// fp32 has packed forms.
+// the scores again (they are intact until P is stored).  32 columns (16 where
+// registers are short) are worked on while the next ones load, and two scores
+// share an instruction where fp32 has packed forms.
 //
 // Warps: 0-3 and 4-7 softmax and output of the pipelines, 8 TMA producer, 9
-// and 10 MMA issuers, 11-18 converters (quantized pools).  All waits are
+// and 10 MMA issuers, 11 on converters (quantized pools).  All waits are
 // bounded.
 #include "internal.h"
 #include "packed.cuh"
@@ -65,7 +65,11 @@ template <int KK, int KV, int D>
 struct PrefixCfg {
   static constexpr bool RAW = KK != KIND_BF16;  // quantized: raw rings and converters
   using Q = QCfg<RAW ? KK : KIND_FP8, RAW ? KV : KIND_FP8, D>;  // (their geometry)
-  static constexpr int THREADS = RAW ? 608 : 352;
+  // converter warps: 8 where head_dim 128 tiles of keys and values are both
+  // converted, else 4, which leaves every thread 128 registers instead of 96
+  static constexpr int NCONV = !RAW ? 0 : (D == 128 && KK != KIND_FP8) ? 8 : 4;
+  static constexpr int THREADS = 32 * (11 + NCONV);
+  static constexpr int CH = NCONV == 8 ? 16 : 32;  // score columns in registers while the next ones load
   static constexpr int F16 = 64 * D * 2;
   // Rings: those of qprefill.cu where 64 KB (32 KB at head_dim 64) of Q fit
   // next to them.
@@ -184,7 +188,7 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
   using Cfg = PrefixCfg<KK, KV, D>;
   using QC = typename Cfg::Q;
   constexpr int NK = Cfg::NK, NV = Cfg::NV, NRK = Cfg::NRK, NRV = Cfg::NRV, NF = Cfg::NF;
-  constexpr int NCONV = QC::NCONV;
+  constexpr int NCONV = Cfg::NCONV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem;
@@ -344,7 +348,7 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
             const int ks = i % NK;
             if (i >= NK) ok = mbar_wait_bounded(&k_empty[ks], ((i / NK) - 1) & 1, a.status) && !*s_abort;
             if (!ok) break;
-            convert_tile<KK, D, QC::K_RB, 32 * NCONV, Cfg::K_SPLIT>(raw, QC::RK_CODES, sK + ks * Cfg::K_STAGE, ct, 64);
+            convert_tile<KK, D, QC::K_RB, 32 * (NCONV > 0 ? NCONV : 8), Cfg::K_SPLIT>(raw, QC::RK_CODES, sK + ks * Cfg::K_STAGE, ct, 64);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
           ok = mbar_wait_bounded(&rv_full[rv], (jj / NRV) & 1, a.status) && !*s_abort;
           if (ok && jj >= NV) ok = mbar_wait_bounded(&v_empty[vs], ((jj / NV) - 1) & 1, a.status) && !*s_abort;
           if (!ok) break;
-          convert_tile<KV, D, QC::V_RB, 32 * NCONV>(sRV + rv * QC::RV_STAGE, QC::RV_CODES, sV + vs * Cfg::F16, ct, 64);
+          convert_tile<KV, D, QC::V_RB, 32 * (NCONV > 0 ? NCONV : 8)>(sRV + rv * QC::RV_STAGE, QC::RV_CODES, sV + vs * Cfg::F16, ct, 64);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
@@ -465,6 +469,7 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
 
     constexpr bool KEY_FAC = Cfg::RAW && KK != KIND_NVFP4;  // per-key score factors
     constexpr bool VAL_FAC = Cfg::RAW && KV != KIND_NVFP4;  // per-key weight factors
+    constexpr int CH = Cfg::CH;
     constexpr int PK = Cfg::RAW ? 32 : 64;                  // columns of P
     // exponents are z rs - m; without key factors z is the raw score and the
     // softmax scale is in rs, with its sign in the direction of the maximum
@@ -486,43 +491,41 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
       if (live) {
         const float* ksc = sF + fs * 128;
         const float* vsc = ksc + 64;
-        // The page's scores times their factors, 16 columns at a time, to
-        // body(c0, z[8 pairs]); the next 16 load while the body runs.
-        auto each16 = [&](auto body) {
-          uint32_t v[2][16];
-          tc::ld16(tS, v[0]);
+        // The page's scores times their factors, CH columns at a time, to
+        // body(c0, z[CH / 2 pairs]); the next ones load while the body runs.
+        auto each = [&](auto body) {
+          uint32_t v[2][CH];
+          tc::ldn(tS, v[0]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t(&u)[16] = v[k & 1];
-            tc::wait_ld16(u);
-            if (k < 3) tc::ld16(tS + 16 * (k + 1), v[(k + 1) & 1]);
-            F2 z[8];
+          for (int k = 0; k < 64 / CH; ++k) {
+            uint32_t(&u)[CH] = v[k & 1];
+            tc::wait_ldn(u);
+            if (k + 1 < 64 / CH) tc::ldn(tS + CH * (k + 1), v[(k + 1) & 1]);
+            F2 z[CH / 2];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) z[c] = pack2(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1]));
+            for (int c = 0; c < CH / 2; ++c) z[c] = pack2(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1]));
             if constexpr (KEY_FAC) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(ksc + 16 * k + 4 * c);
+              for (int c = 0; c < CH / 4; ++c) {
+                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(ksc + CH * k + 4 * c);
                 z[2 * c] = mul2(z[2 * c], f.x);
                 z[2 * c + 1] = mul2(z[2 * c + 1], f.y);
               }
             }
-            body(16 * k, z);
+            body(CH * k, z);
           }
         };
-        // the larger of m and the eight pairs, of -z for a negative uniform scale
-        auto max16 = [&](float m, const F2 (&z)[8]) {
-          float x[16];
+        // the larger of m and the pairs, of -z for a negative uniform scale
+        auto max_of = [&](float m, const F2 (&z)[CH / 2]) {
+          float t[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 8; ++c) unpack2(z[c], x[2 * c], x[2 * c + 1]);
-          if (KEY_FAC || up) {
-#pragma unroll
-            for (int c = 0; c < 16; c += 2) m = max3(m, x[c], x[c + 1]);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 16; c += 2) m = max3(m, -x[c], -x[c + 1]);
+          for (int c = 0; c < CH / 2; ++c) {
+            float x, y;
+            unpack2(z[c], x, y);
+            if (KEY_FAC || up) t[c & 3] = max3(t[c & 3], x, y);
+            else t[c & 3] = max3(t[c & 3], -x, -y);
           }
-          return m;
+          return max3(fmaxf(t[0], t[1]), t[2], t[3]);
         };
         int knew = k_run;
         if constexpr (KV == KIND_FP8) {
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
         float mnew = m_used;
         if (__any_sync(0xffffffffu, m_used == -INFINITY)) {  // the first page: its maximum first
           float mx = -INFINITY;
-          each16([&](int, const F2 (&z)[8]) { mx = max16(mx, z); });
+          each([&](int, const F2 (&z)[CH / 2]) { mx = max_of(mx, z); });
           if (m_used == -INFINITY) mnew = mx == -INFINITY ? -INFINITY : mx * zmul;
         }
         uint32_t pk[PK];
@@ -543,10 +546,10 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
           const F2 rs2 = pack2(rs, rs), nmu2 = pack2(-mu, -mu);
           float mx = -INFINITY;
           F2 s0 = 0ull, s1 = 0ull;
-          each16([&](int c0, const F2 (&z)[8]) {
-            mx = max16(mx, z);
+          each([&](int c0, const F2 (&z)[CH / 2]) {
+            mx = max_of(mx, z);
 #pragma unroll
-            for (int c = 0; c < 8; c += 2) {
+            for (int c = 0; c < CH / 2; c += 2) {
               float p0, p1, p2, p3;
               unpack2(fma2(z[c], rs2, nmu2), p0, p1);
               unpack2(fma2(z[c + 1], rs2, nmu2), p2, p3);

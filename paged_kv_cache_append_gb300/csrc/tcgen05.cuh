@@ -66,13 +66,28 @@ __device__ __forceinline__ void ld16(uint32_t addr, uint32_t (&v)[16]) {
       : "r"(addr));
 }
 
-// wait_ld for registers that other work separates from their use: they pass
-// through the wait, so that no use moves ahead of it.
-__device__ __forceinline__ void wait_ld16(uint32_t (&v)[16]) {
+// ld16 / ld32 by the array's size, and wait_ld for registers that other work
+// separates from their use: they pass through the wait, so that no use moves
+// ahead of it.
+__device__ __forceinline__ void ldn(uint32_t addr, uint32_t (&v)[16]) { ld16(addr, v); }
+__device__ __forceinline__ void ldn(uint32_t addr, uint32_t (&v)[32]) { ld32(addr, v); }
+
+__device__ __forceinline__ void wait_ldn(uint32_t (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
                  "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
                  "+r"(v[15])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void wait_ldn(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                 "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                 "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+                 "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
                :
                : "memory");
 }
