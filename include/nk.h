@@ -273,23 +273,30 @@ int nk_shared_decode_workspace_bytes(const nk_pool* pool, int32_t B, int32_t T, 
  *   may change between the replays of a graph).  Row b takes part iff every
  *   one of its query tokens sees all shared pages, frontiers[b] - T >= 64 *
  *   *shared_pages; the leading *shared_pages table entries of those rows are
- *   equal (checked: NK_STATUS_PREFIX, the affected results are then
- *   undefined).  Rows that do not take part are attended in full by
- *   themselves, and so are all rows for *shared_pages <= 0 or > L (a negative
- *   value also records NK_STATUS_FRONTIER).
+ *   equal (checked where they are attended once: NK_STATUS_PREFIX, the
+ *   affected results are then undefined).  Rows that do not take part are
+ *   attended in full by themselves, and so are all rows for *shared_pages <= 0
+ *   or > L.
+ *   share_from: the prefix is attended once from this many repeated page bytes
+ *   on, (B - 1) * *shared_pages * H * bytes of one page and head; each row by
+ *   itself below, where the pass over the prefix costs more than it saves.  0:
+ *   always;  negative: the library's measured choice, 96 MiB, and 32 MiB for
+ *   T * Hq / H > 16.
  *   workspace: nk_shared_decode_workspace_bytes bytes, no initialisation
  *   needed; two calls that share a workspace must not overlap.
  * Three launches: the prefix on the tensor cores, all B * T * Hq / H query
- * rows of a KV head in 128-row tiles (csrc/prefill.cu, csrc/qprefill.cu, with
- * their rounding of softmax weights and values); each row's own pages
+ * rows of a KV head in 128-row tiles (csrc/prefix.cu; csrc/prefill.cu and
+ * csrc/qprefill.cu at head_dim 256; softmax weights and values are rounded as
+ * in nk_paged_prefill_attention, BF16 weights at head_dim 64 and 128 to 16
+ * bits instead of 8); each row's own pages
  * (csrc/decode.cuh, csrc/vdecode.cu); the log-sum-exp merge (csrc/shared.cu).
  * The pool's device must be current. */
 int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const nk_pool* pool, int32_t layer,
                                      const int32_t* block_tables, const int32_t* table_rows,
                                      const int32_t* frontiers, const int32_t* shared_pages,
                                      int32_t B, int32_t T, float softmax_scale, void* out,
-                                     float* lse, void* workspace, size_t workspace_bytes,
-                                     void* stream);
+                                     float* lse, int64_t share_from, void* workspace,
+                                     size_t workspace_bytes, void* stream);
 
 /* ---- host replicas: logical-order packed pages and transfer runs ----------
  * "Paged KV cache" page, host replica section: a host replica holds the pages

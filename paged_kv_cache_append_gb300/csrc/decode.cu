@@ -77,7 +77,7 @@ namespace nk {
 
 // Shared by the decode entry points: checks, plan, arguments, launch.
 // k_new / v_new non-null: fused append of the T new tokens first.
-static int run_decode(const void* q, int32_t Hq, const nk_pool* pool, int32_t layer,
+int run_decode(const void* q, int32_t Hq, const nk_pool* pool, int32_t layer,
                       const int32_t* block_tables, const int32_t* table_rows,
                       const int32_t* frontiers, const void* k_new, const void* v_new, int32_t B,
                       int32_t T, float softmax_scale, void* out, float* lse, void* workspace,

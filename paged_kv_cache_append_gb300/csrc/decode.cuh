@@ -82,13 +82,14 @@ struct DecodeArgs {
   // frontier moved by that many pages, and every row's partials go to the
   // workspace, for the merge with the prefix's (shared.cu).
   const int32_t* shared = nullptr;
+  int shared_least = 1;
 };
 
 // Pages of row (F, row) that the prefix pass covers.
 __device__ __forceinline__ int pages_before(const DecodeArgs& a, int F, int row) {
   if (a.shared == nullptr) return 0;
   const int pages = *a.shared;
-  return takes_part(pages, F, row, a.T, a.L, a.C) ? pages : 0;
+  return takes_part(pages, a.shared_least, F, row, a.T, a.L, a.C) ? pages : 0;
 }
 
 template <int KIND>
@@ -1296,6 +1297,10 @@ struct DecodePlan {
   DecodeFn fn;
 };
 int make_plan(const nk_pool* p, int B, int T, int Hq, DecodePlan* pl);
+int run_decode(const void* q, int32_t Hq, const nk_pool* pool, int32_t layer, const int32_t* block_tables,
+               const int32_t* table_rows, const int32_t* frontiers, const void* k_new, const void* v_new, int32_t B,
+               int32_t T, float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+               cudaStream_t s, const char* what);
 
 int occupancy_bf16(int, int, int*);
 int occupancy_int8(int, int, int*);

@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(192, 1)
   const int per = (nkt + a.sp.nsplit - 1) / a.sp.nsplit;
   const int p_lo = min(split * per, nkt);
   const int n = min(p_lo + per, nkt) - p_lo;
+  if (shared && n == 0) return;  // the merge reads no partial of this range
   const int32_t* table = a.tables + static_cast<int64_t>(max(row, 0)) * a.L + p_lo;
 
   if (tid == 0) {

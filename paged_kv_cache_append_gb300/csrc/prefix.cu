@@ -221,6 +221,18 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
   const int split = blockIdx.x, h = blockIdx.y;
   const bool two = a.rows > 128;   // the pipelines hold different rows
   const int readers = two ? 2 : 1;  // pipelines that read a page
+  griddep_wait();  // launched with programmatic stream serialization
+  griddep_launch_dependents();
+
+  // ---- this CTA's pages [p_lo, p_lo + n) -----------------------------------------
+  const int pages = *a.sh.pages;
+  const int row = prefix_row(a.sh, a.table_rows, pages, a.L, a.C);
+  const int all = row < 0 ? 0 : pages;
+  const int per = (all + a.nsplit - 1) / a.nsplit;
+  const int p_lo = min(split * per, all);
+  const int n = min(p_lo + per, all) - p_lo;
+  if (n == 0) return;  // the merge reads no partial of this range
+  const int32_t* table = a.tables + static_cast<int64_t>(max(row, 0)) * a.L + p_lo;
   if (tid == 0) {
     for (int i = 0; i < Cfg::NKF; ++i) {
       mbar_init(&k_full[i], Cfg::RAW ? NCONV : 1);
@@ -259,17 +271,6 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
     tc::alloc(tslot, 512);
     tc::relinquish();
   }
-  griddep_wait();  // launched with programmatic stream serialization
-  griddep_launch_dependents();
-
-  // ---- this CTA's pages [p_lo, p_lo + n) -----------------------------------------
-  const int pages = *a.sh.pages;
-  const int row = prefix_row(a.sh, a.table_rows, pages, a.L, a.C);
-  const int all = row < 0 ? 0 : pages;
-  const int per = (all + a.nsplit - 1) / a.nsplit;
-  const int p_lo = min(split * per, all);
-  const int n = min(p_lo + per, all) - p_lo;
-  const int32_t* table = a.tables + static_cast<int64_t>(max(row, 0)) * a.L + p_lo;
   // page i of pipeline w, and how many it takes
   auto page_of = [&](int w, int i) { return two ? i : 2 * i + w; };
   auto count_of = [&](int w) { return two ? n : (n - w + 1) / 2; };
@@ -636,14 +637,12 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
     float* mine = stage + flat * Cfg::PITCH;
     const int tiles = two ? 2 : 1;
     // pipeline w's output times f, plus f1 times what the row holds already
-    auto put = [&](bool has, float f, bool add, float f1) {
+    auto put = [&](float f, bool add, float f1) {
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
         uint32_t ov[32];
-        if (has) {
-          tc::ld32(tO + c0, ov);
-          tc::wait_ld();
-        }
+        tc::ld32(tO + c0, ov);
+        tc::wait_ld();
         if (!row_valid) continue;
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
@@ -653,23 +652,21 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
             v = *at;
             v.x *= f1, v.y *= f1, v.z *= f1, v.w *= f1;
           }
-          if (has) {
-            v.x = fmaf(__uint_as_float(ov[c]), f, v.x);
-            v.y = fmaf(__uint_as_float(ov[c + 1]), f, v.y);
-            v.z = fmaf(__uint_as_float(ov[c + 2]), f, v.z);
-            v.w = fmaf(__uint_as_float(ov[c + 3]), f, v.w);
-          }
+          v.x = fmaf(__uint_as_float(ov[c]), f, v.x);
+          v.y = fmaf(__uint_as_float(ov[c + 1]), f, v.y);
+          v.z = fmaf(__uint_as_float(ov[c + 2]), f, v.z);
+          v.w = fmaf(__uint_as_float(ov[c + 3]), f, v.w);
           *at = v;
         }
       }
     };
     float M = m_eff, L = l;
     if (two) {
-      if (ok && live && n > 0) put(true, 1.f, false, 0.f);
+      if (ok && live) put(1.f, false, 0.f);
     } else {
       if (w == 1) {
         sML[m] = make_float2(m_eff, l);
-        if (ok && live && count > 0) put(true, 1.f, false, 0.f);
+        if (ok && live && count > 0) put(1.f, false, 0.f);
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (w == 0 && count_of(1) > 0) {
@@ -677,24 +674,22 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
         M = fmaxf(m_eff, o.x);
         const float f0 = m_eff == -INFINITY ? 0.f : ex2(m_eff - M), f1 = o.x == -INFINITY ? 0.f : ex2(o.x - M);
         L = l * f0 + o.y * f1;
-        if (ok && live) put(true, f0, true, f1);
-      } else if (w == 0 && n > 0) {
-        if (ok && live) put(true, 1.f, false, 0.f);
+        if (ok && live) put(f0, true, f1);
+      } else if (w == 0) {
+        if (ok && live) put(1.f, false, 0.f);
       }
     }
     asm volatile("bar.sync 1, 256;" ::: "memory");
     if (ok) {
       if (row_valid && (two || w == 0)) {
         const int64_t part = (static_cast<int64_t>(h) * tiles + flat / 128) * a.nsplit + split;
-        a.ml[part * 128 + flat % 128] = make_float2(n > 0 ? M : -INFINITY, n > 0 ? L : 0.f);
+        a.ml[part * 128 + flat % 128] = make_float2(M, L);
       }
-      if (n > 0) {
-        for (int idx = tid; idx < a.rows * (D / 4); idx += 256) {
-          const int r = idx / (D / 4), c = (idx % (D / 4)) * 4;
-          const int64_t part = (static_cast<int64_t>(h) * tiles + r / 128) * a.nsplit + split;
-          *reinterpret_cast<float4*>(a.o + (part * 128 + r % 128) * D + c) =
-              *reinterpret_cast<const float4*>(stage + r * Cfg::PITCH + c);
-        }
+      for (int idx = tid; idx < a.rows * (D / 4); idx += 256) {
+        const int r = idx / (D / 4), c = (idx % (D / 4)) * 4;
+        const int64_t part = (static_cast<int64_t>(h) * tiles + r / 128) * a.nsplit + split;
+        *reinterpret_cast<float4*>(a.o + (part * 128 + r % 128) * D + c) =
+            *reinterpret_cast<const float4*>(stage + r * Cfg::PITCH + c);
       }
     }
   }

@@ -30,7 +30,16 @@ cudaError_t prefix_pass_quantized(const nk_pool* p, int layer, const void* q, co
 cudaError_t prefix_pass(const nk_pool* p, int layer, const void* q, const int32_t* tables, const int32_t* table_rows,
                         int Hq, float scale_log2, const PrefillSplit& sp, const SharedPrefix& sh, cudaStream_t s);
 
+#ifndef NK_SHARE
+#define NK_SHARE (96 << 20)
+#define NK_SHARE_T (32 << 20)
+#endif
 constexpr int kMaxPrefixSplits = 128;
+
+// Repeated page bytes, (rows - 1) * pages * heads * page bytes, from which the
+// pass over the prefix pays for itself (its launch, its partials and their
+// merge) -- see nk_paged_shared_decode_attention.
+constexpr int64_t kShareFrom = NK_SHARE, kShareFromTensor = NK_SHARE_T;
 
 struct SharedPlan {
   DecodePlan own;  // the rows' own pages
@@ -68,10 +77,10 @@ constexpr int kMergeRows = 8;  // query rows of one merge CTA
 // the latency of three dependent reads and, for many partials, by L2: the
 // accumulators are read as whole 128-byte lines, eight loads of a thread in
 // flight, the first eight before the weights are known.
-template <int D>
-__global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant__ SharedMergeArgs m) {
+template <int D, int SUB>
+__global__ void __launch_bounds__(kMergeRows * 8 * SUB) shared_merge_kernel(const __grid_constant__ SharedMergeArgs m) {
   const DecodeArgs& a = m.d;
-  constexpr int S_MAX = kMaxSplits + kMaxPrefixSplits, U = 8;
+  constexpr int S_MAX = kMaxSplits + kMaxPrefixSplits, U = 8, THREADS = kMergeRows * 8 * SUB;
   __shared__ int s_F[8];
   __shared__ int s_row[8];
   __shared__ float s_w[kMergeRows * S_MAX];  // weights
@@ -100,11 +109,10 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
   const int per = part ? (pages + m.nsplit - 1) / m.nsplit : 1;
   const int pre = part ? (pages + per - 1) / per : 0;
   if (h == 0 && blockIdx.z == 0) {  // the row's leading table entries are those the prefix pass read
-    if (pages < 0 && tid == 0) set_status(a.status, NK_STATUS_FRONTIER);
     if (part && s_row[b] != first) {
       const int32_t* mine = a.tables + static_cast<int64_t>(s_row[b]) * a.L;
       const int32_t* read = a.tables + static_cast<int64_t>(first) * a.L;
-      for (int i = tid; i < pages; i += 256)
+      for (int i = tid; i < pages; i += THREADS)
         if (mine[i] != read[i]) set_status(a.status, NK_STATUS_PREFIX);
     }
   }
@@ -121,8 +129,8 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
   griddep_wait();
   griddep_launch_dependents();
 
-  // thread = (query row r, 4 dims, every fourth partial from `sub` on)
-  const int sub = tid & 3, r = tid >> 5, d = d0 + ((tid >> 2) & 7) * 4;
+  // thread = (query row r, 4 dims, every SUB-th partial from `sub` on)
+  const int sub = tid % SUB, r = tid / (8 * SUB), d = d0 + (tid / SUB % 8) * 4;
   const bool live = r < R_real;
   const int splits = own + pre;
   const float* own_o = a.ws_acc + (own0 * R + q0 + r) * D + d;
@@ -133,11 +141,11 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
   };
   float4 v[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) v[u] = live && sub + 4 * u < splits ? acc_at(sub + 4 * u) : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int u = 0; u < U; ++u) v[u] = live && sub + SUB * u < splits ? acc_at(sub + SUB * u) : make_float4(0.f, 0.f, 0.f, 0.f);
 
-  if (warp < R_real) {  // the weights of query row q0 + warp, lanes over its partials
-    const float2* own_ml = a.ws_ml + own0 * R + q0 + warp;
-    const float2* pre_ml = m.sh_ml + prefix0(warp);
+  for (int wr = warp; wr < R_real; wr += THREADS / 32) {  // the weights of query row q0 + wr, lanes over its partials
+    const float2* own_ml = a.ws_ml + own0 * R + q0 + wr;
+    const float2* pre_ml = m.sh_ml + prefix0(wr);
     constexpr int N = S_MAX / 32;
     float2 w[N];
     float M = -INFINITY;
@@ -162,26 +170,26 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
 #pragma unroll
     for (int u = 0; u < N; ++u) {
       const int k = lane + 32 * u;
-      if (k < splits) s_w[warp * S_MAX + k] = w[u].x * inv;
+      if (k < splits) s_w[wr * S_MAX + k] = w[u].x * inv;
     }
     if (lane == 0 && a.lse && d0 == 0) {
-      const int qr = q0 + warp;
+      const int qr = q0 + wr;
       a.lse[(static_cast<int64_t>(b) * a.T + qr / a.G) * a.Hq + h * a.G + qr % a.G] =
           L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
     }
   }
-  __syncwarp();  // a warp's weights are its own threads': r == warp
+  __syncthreads();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = sub; k0 < splits; k0 += 4 * U) {
+  for (int k0 = sub; k0 < splits; k0 += SUB * U) {
     float4 nx[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = k0 + 4 * (U + u);
+      const int k = k0 + SUB * (U + u);
       nx[u] = live && k < splits ? acc_at(k) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = k0 + 4 * u;
+      const int k = k0 + SUB * u;
       const float w = live && k < splits ? s_w[r * S_MAX + k] : 0.f;
       if (w > 0.f) {  // a partial without keys has no accumulators
         acc.x = fmaf(w, v[u].x, acc.x);
@@ -193,7 +201,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
     }
   }
 #pragma unroll
-  for (int off = 1; off < 4; off <<= 1) {
+  for (int off = 1; off < SUB; off <<= 1) {
     acc.x += __shfl_xor_sync(0xffffffffu, acc.x, off);
     acc.y += __shfl_xor_sync(0xffffffffu, acc.y, off);
     acc.z += __shfl_xor_sync(0xffffffffu, acc.z, off);
@@ -204,6 +212,17 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
     __nv_bfloat16* dst = a.out + ((static_cast<int64_t>(b) * a.T + qr / a.G) * a.Hq + h * a.G + qr % a.G) * D + d;
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
   }
+}
+
+// SUB threads share 4 dims of a query row.  Over 16 query rows a row, with four
+// times the CTAs, 2 take less than 4 (116 against 121 us for the 4-token verify
+// of 8 rows); below, 4 (40.5 against 44.8 us for one token of 8 rows).
+template <int SUB>
+static cudaError_t launch_merge(int D, dim3 grid, cudaStream_t s, const SharedMergeArgs& m) {
+  const dim3 block(kMergeRows * 8 * SUB);
+  return D == 64    ? launch_pdl(shared_merge_kernel<64, SUB>, grid, block, 0, s, m)
+         : D == 128 ? launch_pdl(shared_merge_kernel<128, SUB>, grid, block, 0, s, m)
+                    : launch_pdl(shared_merge_kernel<256, SUB>, grid, block, 0, s, m);
 }
 
 }  // namespace nk
@@ -225,8 +244,8 @@ extern "C" int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const
                                                 const int32_t* block_tables, const int32_t* table_rows,
                                                 const int32_t* frontiers, const int32_t* shared_pages,
                                                 int32_t B, int32_t T, float softmax_scale, void* out,
-                                                float* lse, void* workspace, size_t workspace_bytes,
-                                                void* stream) {
+                                                float* lse, int64_t share_from, void* workspace,
+                                                size_t workspace_bytes, void* stream) {
   clear_error();
   if (!q || !pool || !block_tables || !table_rows || !frontiers || !shared_pages || !out)
     return fail(NK_ERR_INVALID_ARG, "null argument to nk_paged_shared_decode_attention");
@@ -246,12 +265,22 @@ extern "C" int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const
     return fail(NK_ERR_INVALID_ARG, "the pool belongs to device " + std::to_string(pool->device) +
                                         ", the current device is " + std::to_string(dev));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // the least number of shared pages worth the prefix pass
+  int64_t page_bytes = 0;
+  for (int i = 0; i < pool->n_planes; ++i) page_bytes += int64_t(NK_PAGE_TOKENS) * pool->plane[i].row_bytes;
+  if (share_from < 0) share_from = T * (Hq / pool->desc.num_kv_heads) > 16 ? kShareFromTensor : kShareFrom;
+  const int64_t repeated = (B - 1) * page_bytes * pool->desc.num_kv_heads;  // per shared page
+  const int64_t least = share_from == 0 ? 1 : repeated == 0 ? INT32_MAX : (share_from + repeated - 1) / repeated;
+  if (least > pool->L)  // no row has that many pages
+    return run_decode(q, Hq, pool, layer, block_tables, table_rows, frontiers, nullptr, nullptr, B, T, softmax_scale,
+                      out, lse, workspace, workspace_bytes, s, "nk_paged_shared_decode_attention");
   char* ws = static_cast<char*>(workspace);
   SharedPrefix sh;
   sh.pages = shared_pages;
   sh.frontiers = frontiers;
   sh.B = B;
   sh.T = T;
+  sh.least = static_cast<int>(least);
   PrefillSplit sp{};
   sp.nsplit = pl.nsplit;
   sp.tiles = pl.tiles;
@@ -291,6 +320,7 @@ extern "C" int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const
   a.ctas = pl.own.ctas;
   a.head_major = pool->desc.order == NK_HEAD_MAJOR;
   a.shared = shared_pages;
+  a.shared_least = sh.least;
   e = pl.own.fn(pool, layer, a, pl.own.nqt, dim3(pl.own.ctas, a.H), s);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   m.sh_ml = sp.ws_ml;
@@ -299,9 +329,7 @@ extern "C" int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const
   m.nsplit = pl.nsplit;
   const int D = pool->desc.head_dim;
   const dim3 grid(B, a.H, D / 32 * ((T * a.G + kMergeRows - 1) / kMergeRows));
-  e = D == 64    ? launch_pdl(shared_merge_kernel<64>, grid, dim3(256), 0, s, m)
-      : D == 128 ? launch_pdl(shared_merge_kernel<128>, grid, dim3(256), 0, s, m)
-                 : launch_pdl(shared_merge_kernel<256>, grid, dim3(256), 0, s, m);
+  e = T * a.G > 16 ? launch_merge<2>(D, grid, s, m) : launch_merge<4>(D, grid, s, m);
   if (e != cudaSuccess) return cuda_fail(e, "merge launch");
   return NK_OK;
 }

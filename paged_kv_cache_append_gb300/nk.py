@@ -99,7 +99,7 @@ def load(path: str | None = None) -> C.CDLL:
         "nk_status_read": (C.c_int, [C.POINTER(_I), _I, _P]),
         "nk_selftest_bounded_wait": (C.c_int, [_I, _P, _P]),
         "nk_shared_decode_workspace_bytes": (C.c_int, [_P, _I, _I, _I, C.POINTER(_S)]),
-        "nk_paged_shared_decode_attention": (C.c_int, [_P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _F, _P, _P, _P, _S,
+        "nk_paged_shared_decode_attention": (C.c_int, [_P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _F, _P, _P, _L, _P, _S,
                                                        _P]),
         "nk_qk_norm_rope": (C.c_int, [C.POINTER(RopeDesc), _I, C.POINTER(Rows), _I, C.POINTER(Rows), _I, _P, _I,
                                       C.POINTER(Rows), C.POINTER(Rows), _P]),
@@ -234,9 +234,9 @@ def nk_shared_decode_workspace_bytes(pool, B, T, Hq) -> int:
 
 
 def nk_paged_shared_decode_attention(q, Hq, pool, layer, block_tables, table_rows, frontiers, shared_pages,
-                                     B, T, scale, out, lse, workspace, workspace_bytes, stream):
+                                     B, T, scale, out, lse, share_from, workspace, workspace_bytes, stream):
     _check(load().nk_paged_shared_decode_attention(q, Hq, pool, layer, block_tables, table_rows, frontiers,
-                                                   shared_pages, B, T, scale, out, lse, workspace,
+                                                   shared_pages, B, T, scale, out, lse, share_from, workspace,
                                                    workspace_bytes, stream))
 
 
@@ -591,17 +591,19 @@ class Pool:
         return torch.empty(n, dtype=torch.uint8, device=self.planes[0][0].device)
 
     def shared_decode(self, layer, q, tables, table_rows, frontiers, shared_pages, scale, out=None, lse=None,
-                      workspace=None, stream=None):
+                      workspace=None, stream=None, share_from: int = -1):
         """``decode`` of a batch whose rows share their first ``shared_pages``
-        (int32 device tensor of one value) pages, attended once for all rows.
-        Without ``workspace`` one is allocated for this call."""
+        (int32 device tensor of one value) pages, attended once for all rows
+        from ``share_from`` repeated page bytes on (nk.h; -1: the library's
+        choice, 0: always).  Without ``workspace`` one is allocated for this
+        call."""
         import torch
         B, T, Hq, D = q.shape
         dev = self.planes[0][0].get_device()
         if torch.cuda.current_device() != dev:
             with torch.cuda.device(dev):
                 return self.shared_decode(layer, q, tables, table_rows, frontiers, shared_pages, scale, out, lse,
-                                          workspace, stream)
+                                          workspace, stream, share_from)
         pq = _cuda(q, torch.bfloat16, (B, T, Hq, self.D), "q", dev)
         pt = _cuda(tables, torch.int32, (self.C, self.L), "tables", dev)
         pr = _cuda(table_rows, torch.int32, (B,), "table_rows", dev)
@@ -620,5 +622,5 @@ class Pool:
             if stream is not None:
                 ws.record_stream(stream)
         nk_paged_shared_decode_attention(pq, Hq, self.handle, layer, pt, pr, pf, shared_pages.data_ptr(), B, T,
-                                         float(scale), po, pl, ws.data_ptr(), ws.numel(), _stream(stream))
+                                         float(scale), po, pl, share_from, ws.data_ptr(), ws.numel(), _stream(stream))
         return out, lse

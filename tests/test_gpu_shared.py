@@ -81,7 +81,7 @@ class Batch:
     def run(self, pages, **kw):
         shared = dev([pages], torch.int32)
         out, lse = self.gpu.shared_decode(0, self.d["q"], self.d["tables"], self.d["rows"], self.d["F"], shared,
-                                          self.scale, **kw)
+                                          self.scale, **dict(dict(share_from=0), **kw))
         torch.cuda.synchronize()
         return out.cpu(), lse.cpu()
 
@@ -154,7 +154,7 @@ def test_any_number_of_shared_pages(profile, pages):
     s = torch.cuda.current_stream().cuda_stream
     nk.nk_status_read(True, s)
     check(*b.run(min(pages, 3) if pages < 100 else pages), b.reference())
-    assert nk.nk_status_read(True, s) == (nk.STATUS_FRONTIER if pages < 0 else 0)
+    assert nk.nk_status_read(True, s) == 0
 
 
 @pytest.mark.parametrize("profile", PROFILES)
@@ -181,6 +181,16 @@ def test_many_pages_per_range(profile, D, B, G, T, pages):
         o, l = OA.decode(q[i][:, rows], K[:, heads], V[:, heads], int(b.F[i]), b.scale)
         a, _ = OA.decode(q[i][:, rows], K[:, heads], np.abs(V[:, heads]), int(b.F[i]), b.scale)
         check(out[i][:, rows], lse[i][:, rows], (o, l, a))
+
+
+@pytest.mark.parametrize("profile,G,T", [("bf16", 8, 1), ("k8v4", 8, 4), ("int8_g64", 4, 2)])
+@pytest.mark.parametrize("share_from", [-1, 1, 1 << 20, 1 << 40])
+def test_the_choice_does_not_change_results(profile, G, T, share_from):
+    """Whichever side of `share_from` the call falls on (repeated bytes here:
+    3 rows * 20 pages * 2 heads * 9 to 32 KB), also one row, which repeats none."""
+    for F in ([64 * 20 + 9, 64 * 20 + 100, 64 * 20 + T, 64 * 20 + 64], [64 * 20 + 33]):
+        b = Batch(profile, 128, 2, G, T, 20, F)
+        check(*b.run(20, share_from=share_from), b.reference())
 
 
 def test_head_major_and_spare_table_rows():
@@ -284,7 +294,8 @@ def test_two_streams_with_their_own_workspaces():
     for _ in range(5):
         for b, s in zip(bs, streams):
             with torch.cuda.stream(s):
-                outs.append(b.gpu.shared_decode(0, b.d["q"], b.d["tables"], b.d["rows"], b.d["F"], shared, b.scale))
+                outs.append(b.gpu.shared_decode(0, b.d["q"], b.d["tables"], b.d["rows"], b.d["F"], shared, b.scale,
+                                                share_from=0))
     torch.cuda.synchronize()
     for i, (o, l) in enumerate(outs):
         assert torch.equal(o.cpu(), refs[i % 2][0]) and torch.equal(l.cpu(), refs[i % 2][1])
@@ -321,7 +332,7 @@ def test_speculative_steps_in_one_graph(profile, D):
         pool.append_rope(0, batch.d["tables"], batch.d["rows"], committed, k, v, rope, q=q, q_out=q_out)
         frontier = committed + T
         pool.shared_decode(0, q_out, batch.d["tables"], batch.d["rows"], frontier, shared, batch.scale, out=out,
-                           lse=lse, workspace=ws)
+                           lse=lse, workspace=ws, share_from=0)
         n, tok, after = nk.verify_drafts(target, tokens, u, draft=draft, frontiers=frontier)
         committed.copy_(after)
         return n, tok

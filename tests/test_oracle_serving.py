@@ -154,8 +154,8 @@ def test_verify_refusals(lib, kw, code):
 def test_pool_calls_refuse_null(lib):
     n = ctypes.c_size_t()
     assert lib.nk_shared_decode_workspace_bytes(None, 1, 1, 8, ctypes.byref(n)) == -1
-    assert lib.nk_paged_shared_decode_attention(None, 8, None, 0, None, None, None, None, 1, 1, 1.0, None, None, None,
-                                                0, None) == -1
+    assert lib.nk_paged_shared_decode_attention(None, 8, None, 0, None, None, None, None, 1, 1, 1.0, None, None, -1,
+                                                None, 0, None) == -1
     assert lib.nk_paged_kv_append_rope(None, 0, None, None, None, None, None, None, None, None, 0, None, 1, 1,
                                        None) == -1
 
