@@ -277,17 +277,16 @@ int nk_shared_decode_workspace_bytes(const nk_pool* pool, int32_t B, int32_t T, 
  *   affected results are then undefined).  Rows that do not take part are
  *   attended in full by themselves, and so are all rows for *shared_pages <= 0
  *   or > L.
- *   share_from: the prefix is attended once from this many repeated page bytes
- *   on, (B - 1) * *shared_pages * H * bytes of one page and head; each row by
- *   itself below, where the pass over the prefix costs more than it saves.  0:
- *   always;  negative: the library's measured choice, 96 MiB, and 32 MiB for
- *   T * Hq / H > 16.
+ *   share_from: the prefix is attended once where that saves at least this
+ *   many page bytes, (B - c) * *shared_pages * H * bytes of one page and head,
+ *   c = 3 (2 for T * Hq / H > 16) being what attending it once costs, in rows;
+ *   each row attends it by itself otherwise.  0: always;  negative: the
+ *   library's measured choice, 64 MiB (32 MiB for T * Hq / H > 16).
  *   workspace: nk_shared_decode_workspace_bytes bytes, no initialisation
  *   needed; two calls that share a workspace must not overlap.
  * Three launches: the prefix on the tensor cores, all B * T * Hq / H query
- * rows of a KV head in 128-row tiles (csrc/prefix.cu; csrc/prefill.cu and
- * csrc/qprefill.cu at head_dim 256; softmax weights and values are rounded as
- * in nk_paged_prefill_attention, BF16 weights at head_dim 64 and 128 to 16
+ * rows of a KV head in 128-row tiles (csrc/prefix.cu; softmax weights and
+ * values are rounded as in nk_paged_prefill_attention, but BF16 weights to 16
  * bits instead of 8); each row's own pages
  * (csrc/decode.cuh, csrc/vdecode.cu); the log-sum-exp merge (csrc/shared.cu).
  * The pool's device must be current. */

@@ -37,7 +37,6 @@
 
 #include "internal.h"
 #include "prefill_split.cuh"
-#include "shared.cuh"
 #include "tcgen05.cuh"
 
 namespace nk {
@@ -55,11 +54,6 @@ struct PrefillArgs {
   int B, Tc, Hq, H, G, L, M, C;
   PrefillSplit sp;
   int head_major;  // plane order
-  // Prefix pass of the shared-prefix attention (pages not nullptr): the query
-  // rows are the Tc = B T tokens of all rows of the batch, flat over tokens and
-  // heads, and every one of them sees the same pages, all of them whole.  Only
-  // partials are written.
-  SharedPrefix sh;
 };
 
 template <int D>
@@ -116,28 +110,22 @@ __global__ void __launch_bounds__(192, 1)
   griddep_launch_dependents();
 
   // ---- row geometry (uniform across the CTA) -------------------------------
-  const bool shared = a.sh.pages != nullptr;
-  const int spages = shared ? *a.sh.pages : 0;
-  const int row = shared ? prefix_row(a.sh, a.table_rows, spages, a.L, a.C) : a.table_rows[b];
-  const int prefix = shared ? (row < 0 ? 0 : 64 * spages) : a.prefix_len[b];
-  const int chunk = shared ? a.Tc : a.chunk_len[b];
-  if (shared) {
-    // whole pages of one table row, or none
-  } else if (row < 0 || row >= a.C || prefix < 0 || chunk < 0 || chunk > a.Tc ||
+  const int row = a.table_rows[b];
+  int prefix = a.prefix_len[b], chunk = a.chunk_len[b];
+  if (row < 0 || row >= a.C || prefix < 0 || chunk < 0 || chunk > a.Tc ||
       static_cast<int64_t>(prefix) + chunk > static_cast<int64_t>(a.L) * 64) {
     if (tid == 0 && qt == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
     return;
   }
   const int t0 = qt * TQ;
-  if (!shared && t0 >= chunk) return;  // no query of this tile is in the chunk
+  if (t0 >= chunk) return;  // no query of this tile is in the chunk
   const int t_last = min(t0 + TQ, chunk) - 1;
-  const int nkt = shared ? prefix / 64 : (prefix + t_last + 1 + 63) / 64;  // key pages of the tile
+  const int nkt = (prefix + t_last + 1 + 63) / 64;  // key pages of the tile
   // this split's pages [p_lo, p_lo + n); local page i is absolute page p_lo + i
   const int per = (nkt + a.sp.nsplit - 1) / a.sp.nsplit;
   const int p_lo = min(split * per, nkt);
   const int n = min(p_lo + per, nkt) - p_lo;
-  if (shared && n == 0) return;  // the merge reads no partial of this range
-  const int32_t* table = a.tables + static_cast<int64_t>(max(row, 0)) * a.L + p_lo;
+  const int32_t* table = a.tables + static_cast<int64_t>(row) * a.L + p_lo;
 
   if (tid == 0) {
     for (int i = 0; i < NK; ++i) {
@@ -240,9 +228,8 @@ __global__ void __launch_bounds__(192, 1)
   } else {
     // ------------------------------ softmax warps -----------------------------
     const int m = tid;  // query row = TMEM lane
-    const int flat = qt * 128 + m;  // shared prefix: any group size, tiles of 128 flat rows
-    const int g = shared ? flat % G : m % G;
-    const int token = shared ? flat / G : t0 + m / G;
+    const int tl = m / G, g = m % G;
+    const int token = t0 + tl;
     const bool row_valid = token < chunk;
     const int pos = prefix + token;  // keys <= pos are visible
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
@@ -397,35 +384,6 @@ static cudaError_t launch_prefill(const nk_pool* p, int layer, const PrefillArgs
     attr = true;
   }
   return launch_pdl(k, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
-}
-
-// Prefix pass of the shared-prefix attention over a BF16 pool (shared.cu): one
-// row of B T query tokens, nsplit page ranges per 128-row tile.
-cudaError_t prefix_pass_bf16(const nk_pool* p, int layer, const void* q, const int32_t* tables,
-                             const int32_t* table_rows, int Hq, float scale_log2, const PrefillSplit& sp,
-                             const SharedPrefix& sh, cudaStream_t s) {
-  const int D = p->desc.head_dim;
-  PrefillArgs a = {};
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.tables = tables;
-  a.table_rows = table_rows;
-  a.status = p->status;
-  a.scale_log2 = scale_log2;
-  a.B = 1;
-  a.Tc = sh.B * sh.T;
-  a.Hq = Hq;
-  a.H = p->desc.num_kv_heads;
-  a.G = Hq / a.H;
-  a.L = p->L;
-  a.M = p->M;
-  a.C = p->desc.max_concurrency;
-  a.head_major = p->desc.order == NK_HEAD_MAJOR;
-  a.sp = sp;
-  a.sh = sh;
-  const dim3 grid(sp.tiles * sp.nsplit, a.H, 1);
-  return D == 256   ? launch_prefill<256>(p, layer, a, grid, s)
-         : D == 128 ? launch_prefill<128>(p, layer, a, grid, s)
-                    : launch_prefill<64>(p, layer, a, grid, s);
 }
 
 }  // namespace nk

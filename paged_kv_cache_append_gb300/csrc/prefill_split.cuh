@@ -24,7 +24,6 @@ struct PrefillSplit {
   int* counters;   // [B][H][tiles], zero between calls
   float2* ws_ml;   // [B][H][tiles][nsplit][128] (m, l)
   float* ws_o;     // [B][H][tiles][nsplit][128][D]
-  bool partial = false;  // every split leaves its partial, merged elsewhere; no counters
 };
 
 // Layout of the split workspace after `base` bytes of other scratch.
@@ -71,7 +70,7 @@ template <int D>
 __device__ __forceinline__ void prefill_store(uint32_t tmem_o, bool has_o, bool row_valid, float m_used, float l,
                                               __nv_bfloat16* out_row, float* lse_at, const PrefillSplit& sp,
                                               int64_t tile, int split, int m, volatile int* s_last) {
-  if (sp.nsplit <= 1 && !sp.partial) {
+  if (sp.nsplit <= 1) {
     const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += 32) {
@@ -103,13 +102,11 @@ __device__ __forceinline__ void prefill_store(uint32_t tmem_o, bool has_o, bool 
       uint32_t ov[32];
       tc::ld32(tmem_o + c0, ov);
       tc::wait_ld();
-      if (sp.partial && !row_valid) continue;
 #pragma unroll
       for (int c = 0; c < 8; ++c)
         *reinterpret_cast<uint4*>(po + c0 + 4 * c) = make_uint4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]);
     }
   }
-  if (sp.partial) return;
   asm volatile("bar.sync 1, 128;" ::: "memory");
   if (m == 0) {
     __threadfence();

@@ -1,23 +1,25 @@
-// prefix.cu -- the prefix pass of the shared-prefix attention at head_dim 64
-// and 128 (shared.cu): the R = B T G query rows of a batch that read one KV
-// head, at most 256, against the pages that all of them share, on the
-// 5th-generation tensor cores.
+// prefix.cu -- the prefix pass of the shared-prefix attention (shared.cu): the
+// R = B T G query rows of a batch that read one KV head, at most 256, against
+// the pages that all of them share, on the 5th-generation tensor cores.
 //
 // A CTA takes one KV head and one range of the shared pages and leaves one
-// partial (m, l, O) for all R rows.  It runs two pipelines of 128 query rows,
-//   S_w = Q_w K^T   tcgen05.mma M 128 x N 64 x K D, Q_w and the K page in
-//                   shared memory, S_w in one of two TMEM buffers
-//   O_w += P_w V    tcgen05.mma M 128 x N D x K 64, P_w over its S_w (TMEM)
-// each with its own MMA-issuing thread and softmax warpgroup:
-//   R > 128   the pipelines hold the two halves of the rows and read every
-//             page, which is loaded and dequantized once for both;
-//   R <= 128  they hold the same rows and take the even and the odd pages;
-//             their partials are merged before they leave the CTA.
-// One issuing thread is what bounds the one-pipeline kernels (prefill.cu,
-// qprefill.cu): N = 64 products and the waits around them keep it busy.
+// partial (m, l, O) for its query rows.  A pipeline is 128 query rows,
+//   S = Q K^T   tcgen05.mma M 128 x N 64 x K D, the K page in shared memory, S
+//               in one of two TMEM buffers
+//   O += P V    tcgen05.mma M 128 x N D x K 64, P over its S (TMEM)
+// with a softmax warpgroup of its own.  One issuing thread is what bounds the
+// prefill kernels (prefill.cu, qprefill.cu): N = 64 products and the waits
+// around them keep it busy.  Here two threads issue.
+//   head_dim 64, 128: two pipelines, an issuer each, all rows in one CTA.
+//     R > 128   the pipelines hold the two halves of the rows and read every
+//               page, which is loaded and dequantized once for both;
+//     R <= 128  they hold the same rows and take the even and the odd pages;
+//               their partials are merged before they leave the CTA.
+//   head_dim 256: O takes half of the tensor memory, so one pipeline of 128
+//     rows a CTA, one thread issuing the scores and one the values.
 //
 // Operands and their exactness are those of qprefill.cu (dequantization in
-// shared memory, FP8 keys raw at head_dim 128, INT8 keys as two tiles, per-key
+// shared memory, FP8 keys raw from head_dim 128 on, INT8 keys as two tiles, per-key
 // factors, the lift of FP8-row values) and of prefill.cu for BF16, except that
 // BF16 softmax weights enter as two bf16 terms (hi + lo, 16 bits): the tensor
 // time of the second product hides behind HBM there.  No mask: every row sees
@@ -30,12 +32,10 @@
 // registers are short) are worked on while the next ones load, and two scores
 // share an instruction where fp32 has packed forms.
 //
-// Warps: 0-3 and 4-7 softmax and output of the pipelines, 8 TMA producer, 9
-// and 10 MMA issuers, 11 on converters (quantized pools).  All waits are
-// bounded.
+// Warps: 4 softmax and output warps a pipeline, then the TMA producer, two MMA
+// issuers and the converters (quantized pools).  All waits are bounded.
 #include "internal.h"
 #include "packed.cuh"
-#include "prefill_split.cuh"
 #include "qtile.cuh"
 #include "shared.cuh"
 #include "tcgen05.cuh"
@@ -57,6 +57,7 @@ struct PrefixArgs {
   int* status;
   float scale_log2;
   int rows;  // R
+  int tiles;  // of 128 rows
   int nsplit, Hq, H, G, L, M, C, head_major;
   SharedPrefix sh;
 };
@@ -65,19 +66,21 @@ template <int KK, int KV, int D>
 struct PrefixCfg {
   static constexpr bool RAW = KK != KIND_BF16;  // quantized: raw rings and converters
   using Q = QCfg<RAW ? KK : KIND_FP8, RAW ? KV : KIND_FP8, D>;  // (their geometry)
-  // converter warps: 8 where head_dim 128 tiles of keys and values are both
-  // converted, else 4, which leaves every thread 128 registers instead of 96
-  static constexpr int NCONV = !RAW ? 0 : (D == 128 && KK != KIND_FP8) ? 8 : 4;
-  static constexpr int THREADS = 32 * (11 + NCONV);
-  static constexpr int CH = NCONV == 8 ? 16 : 32;  // score columns in registers while the next ones load
+  static constexpr int NP = D == 256 ? 1 : 2;  // pipelines
+  // converter warps: 8 where tiles of keys and values are both converted or
+  // are large, else 4; threads have 128 registers (96 with 19 warps)
+  static constexpr int NCONV = !RAW ? 0 : D == 256 || (D == 128 && KK != KIND_FP8) ? 8 : 4;
+  static constexpr int W_TMA = 4 * NP, W_MMA = W_TMA + 1, W_CONV = W_MMA + 2;
+  static constexpr int THREADS = 32 * (W_CONV + NCONV);
+  static constexpr int CH = THREADS > 512 ? 16 : 32;  // score columns in registers while the next ones load
   static constexpr int F16 = 64 * D * 2;
-  // Rings: those of qprefill.cu where 64 KB (32 KB at head_dim 64) of Q fit
+  // Rings: those of qprefill.cu; smaller at head_dim 128 where 64 KB of Q lie
   // next to them.
-  static constexpr bool WIDE = D == 128;
-  static constexpr int NK = !RAW ? (WIDE ? 4 : 6) : Q::NK == 0 ? 0 : !WIDE ? Q::NK : KK == KIND_INT8 ? 2 : 3;
-  static constexpr int NV = !RAW ? NK : Q::NK == 0 ? Q::NV : !WIDE ? Q::NV : 3;
-  static constexpr int NRK = !RAW ? 0 : WIDE && KK == KIND_INT8 ? 2 : Q::NRK;
-  static constexpr int NRV = !RAW ? 0 : WIDE && KK == KIND_INT8 ? 3 : Q::NRV;
+  static constexpr bool QW = D == 128;
+  static constexpr int NK = !RAW ? (D == 256 ? 3 : QW ? 4 : 6) : Q::NK == 0 ? 0 : !QW ? Q::NK : KK == KIND_INT8 ? 2 : 3;
+  static constexpr int NV = !RAW ? NK : Q::NK == 0 ? Q::NV : !QW ? Q::NV : 3;
+  static constexpr int NRK = !RAW ? 0 : QW && KK == KIND_INT8 ? 2 : Q::NRK;
+  static constexpr int NRV = !RAW ? 0 : QW && KK == KIND_INT8 ? 3 : Q::NRV;
   static constexpr int NF = RAW ? Q::NF : 0;
   static constexpr int NKF = NK;
   static constexpr int K_STAGE = RAW ? Q::K_STAGE : F16;
@@ -86,19 +89,21 @@ struct PrefixCfg {
   static constexpr int OFF_RV = OFF_RK + NRK * (RAW ? Q::RK_STAGE : 0);
   static constexpr int OFF_Q = OFF_RV + NRV * (RAW ? Q::RV_STAGE : 0);
   // Q of a pipeline: blocks of 128 rows x 128 bytes (64 bf16 / f16 dims; the
-  // hi, then the lo E4M3 terms of 128 dims), 128-byte swizzle
-  static constexpr int Q_BYTES = 128 * D * 2;
-  static constexpr int OFF_F = OFF_Q + 2 * Q_BYTES;
+  // hi, then the lo E4M3 terms of 128 dims), 128-byte swizzle; at head_dim 256
+  // in tensor memory instead, which S and O leave 128 columns of
+  static constexpr bool Q_TMEM = D == 256;
+  static constexpr int Q_BYTES = Q_TMEM ? 0 : 128 * D * 2;
+  static constexpr int OFF_F = OFF_Q + NP * Q_BYTES;
   static constexpr int OFF_ML = OFF_F + NF * 512;  // [128] float2: pipeline 1's (m, l)
   static constexpr int OFF_BAR = OFF_ML + 1024;
-  static constexpr int NBAR = 2 * NKF + 2 * NV + 2 * NRK + 2 * NRV + 2 * NF + 10;
+  static constexpr int NBAR = 2 * NKF + 2 * NV + 2 * NRK + 2 * NRV + 2 * NF + 12;
   // at least half of the SM's shared memory: one CTA per SM owns all 512 TMEM columns
   static constexpr int USED = OFF_BAR + NBAR * 8 + 64 + 1024;
   static constexpr int SMEM = USED > 116 * 1024 ? USED : 116 * 1024;
   // output rows on their way to global memory, over the rings and Q
   static constexpr int PITCH = D + 4;
-  static_assert(256 * PITCH * 4 <= OFF_F, "staged output rows");
-  static constexpr uint32_t COL_S = 0, COL_O = 256;  // + 128 w + 64 (buffer), + 128 w
+  static_assert(128 * NP * PITCH * 4 <= OFF_F, "staged output rows");
+  static constexpr uint32_t COL_S = 0, COL_Q = 128, COL_O = 256;  // S + 128 w + 64 (buffer), O + 128 w
   static constexpr bool K8MMA = RAW && Q::K8MMA;
   static constexpr bool K_SPLIT = RAW && Q::K_SPLIT;
   static constexpr uint32_t ID_S = !RAW    ? tc::idesc_bf16(128, 64, false, false)
@@ -108,24 +113,28 @@ struct PrefixCfg {
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
 
-// One query row (D bf16 values at src, zeros for nullptr) to row m of the
-// pipeline's Q in shared memory, in the form its MMA reads; returns 2^-e of
-// its power-of-two scale (1 for BF16).
+// One query row (D bf16 values at src, zeros for nullptr) in the form its MMA
+// reads: row m of the pipeline's Q in shared memory, or the TMEM columns at
+// `taddr` of this lane.  Returns 2^-e of its power-of-two scale (1 for BF16).
 template <int KK, int KV, int D>
-__device__ __forceinline__ float prefix_query(const uint4* src, uint8_t* sq, int m) {
+__device__ __forceinline__ float prefix_query(const uint4* src, uint8_t* sq, uint32_t taddr, int m) {
   using Cfg = PrefixCfg<KK, KV, D>;
   const auto x = [&](int u) { return src ? src[u] : make_uint4(0u, 0u, 0u, 0u); };
-  // 16-byte chunk c of row m
+  // 16-byte chunk c of row m: four TMEM columns, or 16 bytes of a block
   auto put = [&](int c, uint4 v) {
-    *reinterpret_cast<uint4*>(sq + (c >> 3) * 16384 + swz<128>(m, (c & 7) * 16)) = v;
+    if constexpr (Cfg::Q_TMEM) {
+      tc::st4(taddr + 4 * c, v.x, v.y, v.z, v.w);
+    } else {
+      *reinterpret_cast<uint4*>(sq + (c >> 3) * 16384 + swz<128>(m, (c & 7) * 16)) = v;
+    }
   };
   if constexpr (!Cfg::RAW) {
-#pragma unroll
+#pragma unroll 16
     for (int u = 0; u < D / 8; ++u) put(u, x(u));
     return 1.f;
   } else {
     float mx = 0.f;
-#pragma unroll
+#pragma unroll 16
     for (int u = 0; u < D / 8; ++u) {
       const uint4 y = x(u);
       const uint32_t w[4] = {y.x, y.y, y.z, y.w};
@@ -139,7 +148,6 @@ __device__ __forceinline__ float prefix_query(const uint4* src, uint8_t* sq, int
     const int e = mx > 0.f ? min((Cfg::K8MMA ? 8 : 15) - ex, 100) : 0;
     const float qf = ldexpf(1.f, e);
     if constexpr (Cfg::K8MMA) {
-      static_assert(D == 128, "one 128-byte block per term");
 #pragma unroll 2
       for (int c = 0; c < D / 16; ++c) {  // 16 dims: 16 bytes of hi, 16 of lo
         uint32_t hv[4], lv[4];
@@ -163,7 +171,7 @@ __device__ __forceinline__ float prefix_query(const uint4* src, uint8_t* sq, int
           lv[2 * u + 1] = lp[2] | (lp[3] << 16);
         }
         put(c, make_uint4(hv[0], hv[1], hv[2], hv[3]));
-        put(8 + c, make_uint4(lv[0], lv[1], lv[2], lv[3]));
+        put(D / 16 + c, make_uint4(lv[0], lv[1], lv[2], lv[3]));
       }
     } else {
 #pragma unroll 4
@@ -212,14 +220,16 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
   uint64_t* s_full = f_empty + NF;  // [2][2] scores of pipeline w in buffer i & 1
   uint64_t* p_full = s_full + 4;    // [2] its weights stored
   uint64_t* o_done = p_full + 2;    // [2] its P V accumulated
-  uint64_t* q_ready = o_done + 2;
+  uint64_t* s_empty = o_done + 2;   // [2] one pipeline: P V from the buffer done
+  uint64_t* q_ready = s_empty + 2;
   uint64_t* drain = q_ready + 1;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int split = blockIdx.x, h = blockIdx.y;
-  const bool two = a.rows > 128;   // the pipelines hold different rows
+  constexpr int NP = Cfg::NP;
+  const int split = blockIdx.x, h = blockIdx.y % a.H, tile = blockIdx.y / a.H;  // tile: one pipeline a CTA
+  const bool two = NP == 2 && a.rows > 128;  // the pipelines hold different rows
   const int readers = two ? 2 : 1;  // pipelines that read a page
   griddep_wait();  // launched with programmatic stream serialization
   griddep_launch_dependents();
@@ -254,13 +264,15 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
       mbar_init(&f_full[i], NCONV);
       mbar_init(&f_empty[i], 4 * readers);
     }
-    for (int w = 0; w < 2; ++w) {
+    for (int w = 0; w < NP; ++w) {
       mbar_init(&s_full[2 * w], 1);
       mbar_init(&s_full[2 * w + 1], 1);
       mbar_init(&p_full[w], 4);
       mbar_init(&o_done[w], 1);
     }
-    mbar_init(q_ready, 8);
+    mbar_init(&s_empty[0], 1);
+    mbar_init(&s_empty[1], 1);
+    mbar_init(q_ready, 4 * NP);
     mbar_init(drain, 2);
     *s_abort = 0;
     fence_barrier_init();
@@ -272,14 +284,15 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
     tc::relinquish();
   }
   // page i of pipeline w, and how many it takes
-  auto page_of = [&](int w, int i) { return two ? i : 2 * i + w; };
-  auto count_of = [&](int w) { return two ? n : (n - w + 1) / 2; };
+  const int step = NP == 1 || two ? 1 : 2;
+  auto page_of = [&](int w, int i) { return step == 1 ? i : 2 * i + w; };
+  auto count_of = [&](int w) { return step == 1 ? n : (n - w + 1) / 2; };
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tslot;
 
-  if (warp == 8) {
+  if (warp == Cfg::W_TMA) {
     // ------------------------------ TMA producer ---------------------------------
     int gnext = 0;
     for (int j = 0; j < n; ++j) {
@@ -333,10 +346,10 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
       }
       if (__shfl_sync(0xffffffffu, stop, 0)) break;
     }
-  } else if (warp >= 11) {
+  } else if (warp >= Cfg::W_CONV) {
     // ------------- converters: K(0), K(1), V(0), K(2), V(1), ... -------------------
     if constexpr (Cfg::RAW) {
-      const int ct = tid - 352;
+      const int ct = tid - 32 * Cfg::W_CONV;
       bool ok = true;
       for (int i = 0; ok && i <= n; ++i) {
         if (i < n) {  // K(i) and the factors of page i
@@ -387,54 +400,59 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
       }
       if (!ok) *s_abort = 1;
     }
-  } else if (warp >= 9) {
-    // --------------------- MMA issuer of pipeline w ---------------------------
-    // S(0), S(1), P(0) V, S(2), P(1) V, ...: the MMAs of one thread run in
-    // issue order, so S(i + 1) cannot overwrite the P(i - 1) in its buffer early
+  } else if (warp >= Cfg::W_MMA) {
+    // ----------------------------- MMA issuers --------------------------------
+    // Two pipelines: issuer w does all of pipeline w,
+    //   S(0), S(1), P(0) V, S(2), P(1) V, ...
+    // and the MMAs of one thread run in issue order, so S(i + 1) cannot
+    // overwrite the P(i - 1) in its buffer early.  One pipeline: issuer 0 does
+    // the scores, after P(i - 2) V has completed, and issuer 1 the values.
     if (lane == 0) {
-      const int w = warp - 9, count = count_of(w), step = two ? 1 : 2;
+      const int me = warp - Cfg::W_MMA, w = NP == 2 ? me : 0, count = count_of(w);
       const uint32_t tS = tmem + Cfg::COL_S + 128 * w, tO = tmem + Cfg::COL_O + 128 * w;
-      const uint64_t qd = tc::smem_desc(smem_u32(sQ + w * Cfg::Q_BYTES), 16, 1024);
+      const uint64_t qd = Cfg::Q_TMEM ? 0 : tc::smem_desc(smem_u32(sQ + w * Cfg::Q_BYTES), 16, 1024);
       constexpr int RK = Cfg::K8MMA ? NRK : NK, KS = Cfg::K8MMA ? QC::RK_STAGE : Cfg::K_STAGE;
       const uint64_t kd0 = tc::smem_desc(smem_u32(Cfg::K8MMA ? sRK : sK), 16, 1024);
       const uint64_t vd0 = tc::smem_desc(smem_u32(sV), 8192, 1024);
       uint64_t* kfull = Cfg::K8MMA ? rk_full : k_full;
       uint64_t* kempty = Cfg::K8MMA ? rk_empty : k_empty;
-      int ks = two ? 0 : w, kph = 0, vs = ks, vph = 0;  // ring slots and parities of the next K and V page
+      int ks = step == 1 ? 0 : w, kph = 0, vs = ks, vph = 0;  // ring slots and parities of the next K and V page
       auto scores = [&](int i) {
         if (!mbar_wait_bounded(&kfull[ks], kph, a.status)) return false;
         tc::fence_after();
         const uint32_t d = tS + 64 * (i & 1);
         const uint64_t kd = kd0 + static_cast<uint64_t>((ks * KS) >> 4);
-        if constexpr (Cfg::K8MMA) {
+        // 32 bytes of K per product: 16 f16 or 32 E4M3 dims, 8 TMEM columns of Q
+        auto product = [&](int part, int kk, uint64_t k, uint32_t id) {
+          const uint32_t acc = part > 0 || kk > 0;
+          if constexpr (Cfg::Q_TMEM) {
+            const uint32_t q = tmem + Cfg::COL_Q + (Cfg::K8MMA ? part * (D / 4) : 0) + kk * 8;
+            if constexpr (Cfg::K8MMA) tc::mma_ts_f8(d, q, k, id, acc);
+            else tc::mma_ts(d, q, k, id, acc);
+          } else {
+            const int at = Cfg::K8MMA ? part * 16384 + kk * 32 : (kk >> 2) * 16384 + (kk & 3) * 32;
+            const uint64_t q = qd + static_cast<uint64_t>(at >> 4);
+            if constexpr (Cfg::K8MMA) tc::mma_ss_f8(d, q, k, id, acc);
+            else tc::mma_ss(d, q, k, id, acc);
+          }
+        };
+        constexpr int KPARTS = Cfg::K8MMA || Cfg::K_SPLIT ? 2 : 1;
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
+        for (int part = 0; part < KPARTS; ++part)
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-              tc::mma_ss_f8(d, qd + static_cast<uint64_t>((part * 16384 + kk * 32) >> 4),
-                            kd + static_cast<uint64_t>((kk * 32) >> 4), Cfg::ID_S, part > 0 || kk > 0);
-        } else {
-#pragma unroll
-          for (int part = 0; part < (Cfg::K_SPLIT ? 2 : 1); ++part)
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc::mma_ss(d, qd + static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                         kd + static_cast<uint64_t>((part * Cfg::F16 + (kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
-                         part > 0 ? tc::idesc_negate_b(Cfg::ID_S) : Cfg::ID_S, part > 0 || kk > 0);
-        }
+          for (int kk = 0; kk < (Cfg::K8MMA ? D / 32 : D / 16); ++kk)
+            product(part, kk,
+                    kd + static_cast<uint64_t>(((Cfg::K_SPLIT ? part * Cfg::F16 : 0) + (kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
+                    Cfg::K_SPLIT && part > 0 ? tc::idesc_negate_b(Cfg::ID_S) : Cfg::ID_S);
         tc::commit(&s_full[2 * w + (i & 1)]);
         tc::commit(&kempty[ks]);
         if ((ks += step) >= RK) ks -= RK, kph ^= 1;
         return true;
       };
-      bool ok = mbar_wait_bounded(q_ready, 0, a.status);
-      tc::fence_after();
-      if (ok && count > 0) ok = scores(0);
-      for (int i = 0; ok && i < count; ++i) {
-        if (i + 1 < count) ok = scores(i + 1);
-        if (ok) ok = mbar_wait_bounded(&v_full[vs], vph, a.status);
+      auto values = [&](int i) {
+        bool ok = mbar_wait_bounded(&v_full[vs], vph, a.status);
         if (ok) ok = mbar_wait_bounded(&p_full[w], i & 1, a.status) && !*s_abort;
-        if (!ok) break;
+        if (!ok) return false;
         tc::fence_after();
         const uint64_t vd = vd0 + static_cast<uint64_t>((vs * Cfg::F16) >> 4);
 #pragma unroll
@@ -445,7 +463,28 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
                        Cfg::ID_O, i > 0 || part > 0 || kk > 0);
         tc::commit(&o_done[w]);
         tc::commit(&v_empty[vs]);
+        if constexpr (NP == 1) tc::commit(&s_empty[i & 1]);
         if ((vs += step) >= NV) vs -= NV, vph ^= 1;
+        return true;
+      };
+      bool ok = true;
+      if (NP == 2 || me == 0) {
+        ok = mbar_wait_bounded(q_ready, 0, a.status);
+        tc::fence_after();
+      }
+      if constexpr (NP == 2) {
+        if (ok && count > 0) ok = scores(0);
+        for (int i = 0; ok && i < count; ++i) {
+          if (i + 1 < count) ok = scores(i + 1);
+          if (ok) ok = values(i);
+        }
+      } else if (me == 0) {
+        for (int i = 0; ok && i < count; ++i) {
+          if (i >= 2) ok = mbar_wait_bounded(&s_empty[i & 1], ((i >> 1) - 1) & 1, a.status) && !*s_abort;
+          if (ok) ok = scores(i);
+        }
+      } else {
+        for (int i = 0; ok && i < count; ++i) ok = values(i);
       }
       if (!ok) *s_abort = 1;
       tc::commit(drain);  // arrives once every MMA issued above has completed
@@ -453,7 +492,7 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
   } else {
     // --------------------- softmax warps of pipeline w ---------------------------
     const int w = warp >> 2, m = tid & 127;
-    const int flat = (two ? 128 * w : 0) + m;
+    const int flat = 128 * (NP == 1 ? tile : two ? w : 0) + m;
     const bool row_valid = flat < a.rows;
     const bool live = __any_sync(0xffffffffu, row_valid);  // warps without rows only hand on
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -463,8 +502,13 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
       const int token = flat / a.G, g = flat % a.G;
       src = reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(token) * a.Hq + h * a.G + g) * D);
     }
-    float rs = prefix_query<KK, KV, D>(src, sQ + w * Cfg::Q_BYTES, m);
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    float rs = prefix_query<KK, KV, D>(src, sQ + w * Cfg::Q_BYTES, tmem + lane_base + Cfg::COL_Q, m);
+    if constexpr (Cfg::Q_TMEM) {
+      tc::wait_st();
+      tc::fence_before();
+    } else {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
     __syncwarp();
     if (lane == 0) arrive(q_ready);
 
@@ -634,8 +678,7 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
     tc::fence_after();
     const float m_eff = m_used == -INFINITY ? -INFINITY : m_used - static_cast<float>(k_run);
     float* stage = reinterpret_cast<float*>(smem);
-    float* mine = stage + flat * Cfg::PITCH;
-    const int tiles = two ? 2 : 1;
+    float* mine = stage + (NP == 1 ? m : flat) * Cfg::PITCH;
     // pipeline w's output times f, plus f1 times what the row holds already
     auto put = [&](float f, bool add, float f1) {
 #pragma unroll 1
@@ -661,14 +704,14 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
       }
     };
     float M = m_eff, L = l;
-    if (two) {
+    if (NP == 1 || two) {
       if (ok && live) put(1.f, false, 0.f);
     } else {
       if (w == 1) {
         sML[m] = make_float2(m_eff, l);
         if (ok && live && count > 0) put(1.f, false, 0.f);
       }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      asm volatile("bar.sync 1, %0;" ::"n"(128 * NP) : "memory");
       if (w == 0 && count_of(1) > 0) {
         const float2 o = sML[m];
         M = fmaxf(m_eff, o.x);
@@ -679,16 +722,15 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
         if (ok && live) put(1.f, false, 0.f);
       }
     }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(128 * NP) : "memory");
     if (ok) {
-      if (row_valid && (two || w == 0)) {
-        const int64_t part = (static_cast<int64_t>(h) * tiles + flat / 128) * a.nsplit + split;
-        a.ml[part * 128 + flat % 128] = make_float2(M, L);
-      }
-      for (int idx = tid; idx < a.rows * (D / 4); idx += 256) {
+      // slot of query row r: [h][tile][split][row]
+      auto slot = [&](int r) { return ((static_cast<int64_t>(h) * a.tiles + r / 128) * a.nsplit + split) * 128 + r % 128; };
+      if (row_valid && (NP == 1 || two || w == 0)) a.ml[slot(flat)] = make_float2(M, L);
+      const int r0 = NP == 1 ? tile * 128 : 0, rows = NP == 1 ? min(a.rows - r0, 128) : a.rows;
+      for (int idx = tid; idx < rows * (D / 4); idx += 128 * NP) {
         const int r = idx / (D / 4), c = (idx % (D / 4)) * 4;
-        const int64_t part = (static_cast<int64_t>(h) * tiles + r / 128) * a.nsplit + split;
-        *reinterpret_cast<float4*>(a.o + (part * 128 + r % 128) * D + c) =
+        *reinterpret_cast<float4*>(a.o + slot(r0 + r) * D + c) =
             *reinterpret_cast<const float4*>(stage + r * Cfg::PITCH + c);
       }
     }
@@ -711,13 +753,20 @@ static cudaError_t launch_prefix(const nk_pool* p, int layer, const PrefixArgs& 
     if (e != cudaSuccess) return e;
     attr = true;
   }
-  return launch_pdl(k, dim3(a.nsplit, a.H), dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0],
+  return launch_pdl(k, dim3(a.nsplit, a.H * (Cfg::NP == 1 ? a.tiles : 1)), dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0],
                     p->tmap[layer * 2 + 1], a);
 }
 
-// head_dim 64 or 128, at most 256 query rows per KV head.
+template <int KK, int KV>
+static cudaError_t launch_prefix_d(int D, const nk_pool* p, int layer, const PrefixArgs& a, cudaStream_t s) {
+  return D == 256   ? launch_prefix<KK, KV, 256>(p, layer, a, s)
+         : D == 128 ? launch_prefix<KK, KV, 128>(p, layer, a, s)
+                    : launch_prefix<KK, KV, 64>(p, layer, a, s);
+}
+
+// At most 256 query rows per KV head.
 cudaError_t prefix_pass(const nk_pool* p, int layer, const void* q, const int32_t* tables, const int32_t* table_rows,
-                        int Hq, float scale_log2, const PrefillSplit& sp, const SharedPrefix& sh, cudaStream_t s) {
+                        int Hq, float scale_log2, const PrefixParts& parts, const SharedPrefix& sh, cudaStream_t s) {
   const int np = p->n_planes;
   PrefixArgs a;
   a.q = static_cast<const __nv_bfloat16*>(q);
@@ -725,11 +774,12 @@ cudaError_t prefix_pass(const nk_pool* p, int layer, const void* q, const int32_
   a.table_rows = table_rows;
   a.ks = np == 4 ? static_cast<const uint8_t*>(p->ptrs[layer * np + 2]) : nullptr;
   a.vs = np == 4 ? static_cast<const uint8_t*>(p->ptrs[layer * np + 3]) : nullptr;
-  a.ml = sp.ws_ml;
-  a.o = sp.ws_o;
+  a.ml = parts.ml;
+  a.o = parts.o;
   a.status = p->status;
   a.scale_log2 = scale_log2;
-  a.nsplit = sp.nsplit;
+  a.tiles = parts.tiles;
+  a.nsplit = parts.nsplit;
   a.Hq = Hq;
   a.H = p->desc.num_kv_heads;
   a.G = Hq / a.H;
@@ -739,23 +789,13 @@ cudaError_t prefix_pass(const nk_pool* p, int layer, const void* q, const int32_
   a.C = p->desc.max_concurrency;
   a.head_major = p->desc.order == NK_HEAD_MAJOR;
   a.sh = sh;
-  const bool wide = p->desc.head_dim == 128;
+  const int D = p->desc.head_dim;
   switch (p->desc.profile) {
-    case NK_BF16:
-      return wide ? launch_prefix<KIND_BF16, KIND_BF16, 128>(p, layer, a, s)
-                  : launch_prefix<KIND_BF16, KIND_BF16, 64>(p, layer, a, s);
-    case NK_INT8_G64:
-      return wide ? launch_prefix<KIND_INT8, KIND_INT8, 128>(p, layer, a, s)
-                  : launch_prefix<KIND_INT8, KIND_INT8, 64>(p, layer, a, s);
-    case NK_FP8_E4M3_ROW:
-      return wide ? launch_prefix<KIND_FP8, KIND_FP8, 128>(p, layer, a, s)
-                  : launch_prefix<KIND_FP8, KIND_FP8, 64>(p, layer, a, s);
-    case NK_NVFP4_G16:
-      return wide ? launch_prefix<KIND_NVFP4, KIND_NVFP4, 128>(p, layer, a, s)
-                  : launch_prefix<KIND_NVFP4, KIND_NVFP4, 64>(p, layer, a, s);
-    default:
-      return wide ? launch_prefix<KIND_FP8, KIND_NVFP4, 128>(p, layer, a, s)
-                  : launch_prefix<KIND_FP8, KIND_NVFP4, 64>(p, layer, a, s);
+    case NK_BF16: return launch_prefix_d<KIND_BF16, KIND_BF16>(D, p, layer, a, s);
+    case NK_INT8_G64: return launch_prefix_d<KIND_INT8, KIND_INT8>(D, p, layer, a, s);
+    case NK_FP8_E4M3_ROW: return launch_prefix_d<KIND_FP8, KIND_FP8>(D, p, layer, a, s);
+    case NK_NVFP4_G16: return launch_prefix_d<KIND_NVFP4, KIND_NVFP4>(D, p, layer, a, s);
+    default: return launch_prefix_d<KIND_FP8, KIND_NVFP4>(D, p, layer, a, s);
   }
 }
 

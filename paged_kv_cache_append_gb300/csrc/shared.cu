@@ -6,9 +6,8 @@
 // own:
 //   prefix pass  the B T G query rows that read one KV head, of all rows of
 //                the batch, are the rows of 128-row tensor-core tiles
-//                (prefill.cu, qprefill.cu); the shared pages are cut into
-//                ranges, one CTA each, and every CTA leaves a partial
-//                (m, l, O) for all its query rows;
+//                (prefix.cu); the shared pages are cut into ranges, and every
+//                range leaves a partial (m, l, O) for all query rows;
 //   own pages    the decode kernels (decode.cuh, vdecode.cu) on each row's
 //                pages behind the prefix, as partials too;
 //   merge        M = max m, out = sum 2^(m - M) O / sum 2^(m - M) l, below.
@@ -16,30 +15,24 @@
 #include <cmath>
 
 #include "decode.cuh"
-#include "prefill_split.cuh"
 
 namespace nk {
 
-cudaError_t prefix_pass_bf16(const nk_pool* p, int layer, const void* q, const int32_t* tables,
-                             const int32_t* table_rows, int Hq, float scale_log2, const PrefillSplit& sp,
-                             const SharedPrefix& sh, cudaStream_t s);
-cudaError_t prefix_pass_quantized(const nk_pool* p, int layer, const void* q, const int32_t* tables,
-                                  const int32_t* table_rows, int Hq, float scale_log2, const PrefillSplit& sp,
-                                  const SharedPrefix& sh, cudaStream_t s);
-
 cudaError_t prefix_pass(const nk_pool* p, int layer, const void* q, const int32_t* tables, const int32_t* table_rows,
-                        int Hq, float scale_log2, const PrefillSplit& sp, const SharedPrefix& sh, cudaStream_t s);
+                        int Hq, float scale_log2, const PrefixParts& parts, const SharedPrefix& sh, cudaStream_t s);
 
-#ifndef NK_SHARE
-#define NK_SHARE (96 << 20)
-#define NK_SHARE_T (32 << 20)
-#endif
 constexpr int kMaxPrefixSplits = 128;
 
-// Repeated page bytes, (rows - 1) * pages * heads * page bytes, from which the
-// pass over the prefix pays for itself (its launch, its partials and their
-// merge) -- see nk_paged_shared_decode_attention.
-constexpr int64_t kShareFrom = NK_SHARE, kShareFromTensor = NK_SHARE_T;
+// When the prefix gets a pass of its own.  The pass costs about as much as c
+// rows' own attention to the prefix (c = 1.8 to 2.9 measured over the profiles
+// with the warp-level decode, 1.5 with the tensor-core one) and, for its
+// launch, its partials and their merge, a fixed 6 to 10 us.  So it is taken
+// from (B - c) * pages * heads * page bytes >= kShareFrom on.  Crossings seen
+// with B = 8: 140 pages for BF16 at 2 heads of 256 (92 MB), 310 for FP8-row
+// there (102 MB), 230 for K8V4 at 4 heads of 128 (59 MB), 115 for its 4-token
+// verify (36 MB).
+constexpr int64_t kShareFrom = 64 << 20, kShareFromTensor = 32 << 20;
+constexpr int kShareRows = 3, kShareRowsTensor = 2;
 
 struct SharedPlan {
   DecodePlan own;  // the rows' own pages
@@ -64,9 +57,7 @@ static int make_shared_plan(const nk_pool* p, int B, int T, int Hq, SharedPlan* 
 
 struct SharedMergeArgs {
   DecodeArgs d;
-  const float2* sh_ml;  // [H][tiles][nsplit][128]
-  const float* sh_o;    // [H][tiles][nsplit][128][D]
-  int tiles, nsplit;
+  PrefixParts prefix;
 };
 
 constexpr int kMergeRows = 8;  // query rows of one merge CTA
@@ -106,7 +97,7 @@ __global__ void __launch_bounds__(kMergeRows * 8 * SUB) shared_merge_kernel(cons
   const int chunk = a.nseg > 0 ? piece_chunk(s_F, a, total, maxp) : wave_chunk(s_F, a.B, total, maxp, a.target);
   const int own = max(1, (((s_F[b] + 63) >> 6) + chunk - 1) / chunk);
   const bool part = s_row[b] >= 0;
-  const int per = part ? (pages + m.nsplit - 1) / m.nsplit : 1;
+  const int per = part ? (pages + m.prefix.nsplit - 1) / m.prefix.nsplit : 1;
   const int pre = part ? (pages + per - 1) / per : 0;
   if (h == 0 && blockIdx.z == 0) {  // the row's leading table entries are those the prefix pass read
     if (part && s_row[b] != first) {
@@ -124,7 +115,7 @@ __global__ void __launch_bounds__(kMergeRows * 8 * SUB) shared_merge_kernel(cons
   // partial is 128 slots on
   auto prefix0 = [&](int r) {
     const int flat = b * R_all + q0 + r;
-    return (static_cast<int64_t>(h) * m.tiles + flat / 128) * m.nsplit * 128 + flat % 128;
+    return (static_cast<int64_t>(h) * m.prefix.tiles + flat / 128) * m.prefix.nsplit * 128 + flat % 128;
   };
   griddep_wait();
   griddep_launch_dependents();
@@ -134,7 +125,7 @@ __global__ void __launch_bounds__(kMergeRows * 8 * SUB) shared_merge_kernel(cons
   const bool live = r < R_real;
   const int splits = own + pre;
   const float* own_o = a.ws_acc + (own0 * R + q0 + r) * D + d;
-  const float* pre_o = m.sh_o + (live ? prefix0(r) : 0) * D + d;
+  const float* pre_o = m.prefix.o + (live ? prefix0(r) : 0) * D + d;
   auto acc_at = [&](int k) {
     const float* p = k < own ? own_o + static_cast<int64_t>(k) * R * D : pre_o + static_cast<int64_t>(k - own) * 128 * D;
     return __ldcg(reinterpret_cast<const float4*>(p));
@@ -145,7 +136,7 @@ __global__ void __launch_bounds__(kMergeRows * 8 * SUB) shared_merge_kernel(cons
 
   for (int wr = warp; wr < R_real; wr += THREADS / 32) {  // the weights of query row q0 + wr, lanes over its partials
     const float2* own_ml = a.ws_ml + own0 * R + q0 + wr;
-    const float2* pre_ml = m.sh_ml + prefix0(wr);
+    const float2* pre_ml = m.prefix.ml + prefix0(wr);
     constexpr int N = S_MAX / 32;
     float2 w[N];
     float M = -INFINITY;
@@ -268,9 +259,10 @@ extern "C" int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const
   // the least number of shared pages worth the prefix pass
   int64_t page_bytes = 0;
   for (int i = 0; i < pool->n_planes; ++i) page_bytes += int64_t(NK_PAGE_TOKENS) * pool->plane[i].row_bytes;
-  if (share_from < 0) share_from = T * (Hq / pool->desc.num_kv_heads) > 16 ? kShareFromTensor : kShareFrom;
-  const int64_t repeated = (B - 1) * page_bytes * pool->desc.num_kv_heads;  // per shared page
-  const int64_t least = share_from == 0 ? 1 : repeated == 0 ? INT32_MAX : (share_from + repeated - 1) / repeated;
+  const bool tensor = T * (Hq / pool->desc.num_kv_heads) > 16;
+  if (share_from < 0) share_from = tensor ? kShareFromTensor : kShareFrom;
+  const int64_t saved = (B - (tensor ? kShareRowsTensor : kShareRows)) * page_bytes * pool->desc.num_kv_heads;  // a page
+  const int64_t least = share_from == 0 ? 1 : saved <= 0 ? INT32_MAX : (share_from + saved - 1) / saved;
   if (least > pool->L)  // no row has that many pages
     return run_decode(q, Hq, pool, layer, block_tables, table_rows, frontiers, nullptr, nullptr, B, T, softmax_scale,
                       out, lse, workspace, workspace_bytes, s, "nk_paged_shared_decode_attention");
@@ -281,16 +273,9 @@ extern "C" int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const
   sh.B = B;
   sh.T = T;
   sh.least = static_cast<int>(least);
-  PrefillSplit sp{};
-  sp.nsplit = pl.nsplit;
-  sp.tiles = pl.tiles;
-  sp.ws_ml = reinterpret_cast<float2*>(ws);
-  sp.ws_o = reinterpret_cast<float*>(ws + pl.sh_ml_bytes);
-  sp.partial = true;
-  auto pass = pool->desc.head_dim <= 128       ? prefix_pass
-              : pool->desc.profile == NK_BF16 ? prefix_pass_bf16
-                                              : prefix_pass_quantized;
-  e = pass(pool, layer, q, block_tables, table_rows, Hq, softmax_scale * kLog2e, sp, sh, s);
+  const PrefixParts parts{pl.tiles, pl.nsplit, reinterpret_cast<float2*>(ws),
+                          reinterpret_cast<float*>(ws + pl.sh_ml_bytes)};
+  e = prefix_pass(pool, layer, q, block_tables, table_rows, Hq, softmax_scale * kLog2e, parts, sh, s);
   if (e != cudaSuccess) return cuda_fail(e, "prefix pass launch");
   SharedMergeArgs m;
   DecodeArgs& a = m.d;
@@ -323,10 +308,7 @@ extern "C" int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const
   a.shared_least = sh.least;
   e = pl.own.fn(pool, layer, a, pl.own.nqt, dim3(pl.own.ctas, a.H), s);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
-  m.sh_ml = sp.ws_ml;
-  m.sh_o = sp.ws_o;
-  m.tiles = pl.tiles;
-  m.nsplit = pl.nsplit;
+  m.prefix = parts;
   const int D = pool->desc.head_dim;
   const dim3 grid(B, a.H, D / 32 * ((T * a.G + kMergeRows - 1) / kMergeRows));
   e = T * a.G > 16 ? launch_merge<2>(D, grid, s, m) : launch_merge<4>(D, grid, s, m);

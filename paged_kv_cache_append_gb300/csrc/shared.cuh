@@ -20,6 +20,14 @@ struct SharedPrefix {
   int least = 1;  // fewer shared pages than this are not worth a pass of their own
 };
 
+// Where the prefix pass leaves its partials: of page range `split` of `nsplit`
+// and tile of 128 query rows, for every KV head.
+struct PrefixParts {
+  int tiles, nsplit;
+  float2* ml;  // [H][tiles][nsplit][128] (m, l), O relative to 2^m
+  float* o;    // [H][tiles][nsplit][128][D]
+};
+
 __device__ __forceinline__ bool takes_part(int pages, int least, int F, int row, int T, int L, int C) {
   return pages >= least && pages <= L && F <= L * 64 && F - T >= 64 * pages && row >= 0 && row < C;
 }

@@ -2,9 +2,9 @@
 serving step that uses it with the rotated append and the draft verification.
 
 Tolerances, derived.  Beyond half a bf16 step of the output (2^-8 of it):
-softmax weights are rounded to bf16 in the BF16 prefix pass (2^-9 each) and to
-f16 elsewhere (2^-12, INT8-G64 and FP8-row values 2^-12 more), so the output
-moves by at most 2^-9 A, A = sum p |v| / sum p, which the oracle gives as the
+softmax weights and INT8-G64 and FP8-row values are rounded to f16 (2^-12 each;
+2^-17 for the two-term weights over BF16 pages), so the output moves by at most
+2^-9 A, A = sum p |v| / sum p, which the oracle gives as the
 attention over |V|.  Scores over FP8-row keys take q in two E4M3 terms, each
 element to 2^-17 of the largest: with |q| <= 4.5, sum |k| <= 256 and a scale of
 1/8 to 1/16 a score is off by at most 2^-17 * 4.5 * 256 / 16 = 6e-4, a weight by
@@ -186,8 +186,8 @@ def test_many_pages_per_range(profile, D, B, G, T, pages):
 @pytest.mark.parametrize("profile,G,T", [("bf16", 8, 1), ("k8v4", 8, 4), ("int8_g64", 4, 2)])
 @pytest.mark.parametrize("share_from", [-1, 1, 1 << 20, 1 << 40])
 def test_the_choice_does_not_change_results(profile, G, T, share_from):
-    """Whichever side of `share_from` the call falls on (repeated bytes here:
-    3 rows * 20 pages * 2 heads * 9 to 32 KB), also one row, which repeats none."""
+    """Whichever side of `share_from` the call falls on (page bytes saved here:
+    up to 2 rows * 20 pages * 2 heads * 12 to 32 KB), also one row, which saves none."""
     for F in ([64 * 20 + 9, 64 * 20 + 100, 64 * 20 + T, 64 * 20 + 64], [64 * 20 + 33]):
         b = Batch(profile, 128, 2, G, T, 20, F)
         check(*b.run(20, share_from=share_from), b.reference())
