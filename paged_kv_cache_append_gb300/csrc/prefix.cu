@@ -94,7 +94,8 @@ struct PrefixCfg {
   static constexpr bool Q_TMEM = D == 256;
   static constexpr int Q_BYTES = Q_TMEM ? 0 : 128 * D * 2;
   static constexpr int OFF_F = OFF_Q + NP * Q_BYTES;
-  static constexpr int OFF_ML = OFF_F + NF * 512;  // [128] float2: pipeline 1's (m, l)
+  // [256] floats: the rows' query scales; then [128] float2: pipeline 1's (m, l)
+  static constexpr int OFF_ML = OFF_F + NF * 512;
   static constexpr int OFF_BAR = OFF_ML + 1024;
   static constexpr int NBAR = 2 * NKF + 2 * NV + 2 * NRK + 2 * NRV + 2 * NF + 12;
   // at least half of the SM's shared memory: one CTA per SM owns all 512 TMEM columns
@@ -110,82 +111,91 @@ struct PrefixCfg {
                                    : K8MMA ? tc::idesc_e4m3(128, 64)
                                            : tc::idesc_f16(128, 64, false, false);
   static constexpr uint32_t ID_O = RAW ? tc::idesc_f16(128, D, false, true) : tc::idesc_bf16(128, D, false, true);
+  static_assert(!Q_TMEM || NV * F16 >= 128 * 2 * D, "queries on their way to tensor memory");
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
 
-// One query row (D bf16 values at src, zeros for nullptr) in the form its MMA
-// reads: row m of the pipeline's Q in shared memory, or the TMEM columns at
-// `taddr` of this lane.  Returns 2^-e of its power-of-two scale (1 for BF16).
+// Query rows [first, first + n) of the head whose first query row is at `q`, by
+// warp `pw` of the PW that share them, in the form the MMAs read: row m of the
+// 128-row blocks at `sq` (blocks of head_dim 256 are rows of 2 D bytes on their
+// way to tensor memory), and 2^-e of its power-of-two scale to s_rs[m].  A warp
+// reads whole rows, 16 bytes a lane.  Rows past the last are left as they are:
+// whatever is in them stays in their own scores and outputs, which nobody
+// reads.  (The softmax threads alone, a row each, took 5.3 us for 64 rows of
+// FP8 pages at head_dim 256, most of it converting.)
 template <int KK, int KV, int D>
-__device__ __forceinline__ float prefix_query(const uint4* src, uint8_t* sq, uint32_t taddr, int m) {
+__device__ __forceinline__ void prefix_queries(const __nv_bfloat16* q, int first, int n, int G, int Hq, uint8_t* sq,
+                                               float* s_rs, int pw, int PW, int lane) {
   using Cfg = PrefixCfg<KK, KV, D>;
-  const auto x = [&](int u) { return src ? src[u] : make_uint4(0u, 0u, 0u, 0u); };
-  // 16-byte chunk c of row m: four TMEM columns, or 16 bytes of a block
-  auto put = [&](int c, uint4 v) {
-    if constexpr (Cfg::Q_TMEM) {
-      tc::st4(taddr + 4 * c, v.x, v.y, v.z, v.w);
-    } else {
-      *reinterpret_cast<uint4*>(sq + (c >> 3) * 16384 + swz<128>(m, (c & 7) * 16)) = v;
+  constexpr int LPR = D / 8, RPI = 32 / LPR, BATCH = 4;  // lanes a row, rows a load, loads in flight
+  const int sub = lane / LPR, c = lane % LPR;
+#pragma unroll 1
+  for (int g0 = pw; g0 * RPI < n; g0 += BATCH * PW) {
+    uint4 x[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int m = (g0 + k * PW) * RPI + sub, flat = first + m;
+      x[k] = m < n ? *reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(flat / G) * Hq + flat % G) * D + 8 * c)
+                   : make_uint4(0u, 0u, 0u, 0u);
     }
-  };
-  if constexpr (!Cfg::RAW) {
-#pragma unroll 16
-    for (int u = 0; u < D / 8; ++u) put(u, x(u));
-    return 1.f;
-  } else {
-    float mx = 0.f;
-#pragma unroll 16
-    for (int u = 0; u < D / 8; ++u) {
-      const uint4 y = x(u);
-      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
-    }
-    int ex = 0;
-    if (mx > 0.f) frexpf(mx, &ex);
-    // f16 q: max|q| 2^e in [2^14, 2^15); E4M3 q: in [2^7, 2^8), as hi + lo (see qprefill.cu)
-    const int e = mx > 0.f ? min((Cfg::K8MMA ? 8 : 15) - ex, 100) : 0;
-    const float qf = ldexpf(1.f, e);
-    if constexpr (Cfg::K8MMA) {
-#pragma unroll 2
-      for (int c = 0; c < D / 16; ++c) {  // 16 dims: 16 bytes of hi, 16 of lo
-        uint32_t hv[4], lv[4];
+    for (int k = 0; k < BATCH; ++k) {
+      const int m = (g0 + k * PW) * RPI + sub;
+      if ((g0 + k * PW) * RPI >= n) break;  // the same for the warp
+      const bool live = m < n;
+      // 16-byte chunk j of the row
+      auto at = [&](int j) {
+        if constexpr (Cfg::Q_TMEM) return sq + m * (2 * D) + ((j ^ m) & (2 * D / 16 - 1)) * 16;
+        else return sq + (m >> 7) * Cfg::Q_BYTES + (j >> 3) * 16384 + swz<128>(m & 127, (j & 7) * 16);
+      };
+      if constexpr (!Cfg::RAW) {
+        if (live) *reinterpret_cast<uint4*>(at(c)) = x[k];
+      } else {
+        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        float v[8], mx = 0.f;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint4 y = x(2 * c + u);
-          const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-          uint32_t hp[4], lp[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x0 = __uint_as_float(w[k] << 16) * qf, x1 = __uint_as_float(w[k] & 0xFFFF0000u) * qf;
-            const uint16_t h2 = f32x2_to_e4m3x2(x0, x1);
-            const uint32_t hb32 = e4m3x2_to_f16x2(h2);
-            const __half2 hb = *reinterpret_cast<const __half2*>(&hb32);
-            hp[k] = h2;
-            lp[k] = f32x2_to_e4m3x2(x0 - __low2float(hb), x1 - __high2float(hb));
-          }
-          hv[2 * u] = hp[0] | (hp[1] << 16);
-          hv[2 * u + 1] = hp[2] | (hp[3] << 16);
-          lv[2 * u] = lp[0] | (lp[1] << 16);
-          lv[2 * u + 1] = lp[2] | (lp[3] << 16);
+        for (int u = 0; u < 4; ++u) {
+          v[2 * u] = __uint_as_float(w[u] << 16);
+          v[2 * u + 1] = __uint_as_float(w[u] & 0xFFFF0000u);
+          mx = fmaxf(mx, fmaxf(fabsf(v[2 * u]), fabsf(v[2 * u + 1])));
         }
-        put(c, make_uint4(hv[0], hv[1], hv[2], hv[3]));
-        put(D / 16 + c, make_uint4(lv[0], lv[1], lv[2], lv[3]));
-      }
-    } else {
-#pragma unroll 4
-      for (int u = 0; u < D / 8; ++u) {
-        const uint4 y = x(u);
-        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-        uint32_t v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          v[k] = pack_f16x2(__uint_as_float(w[k] << 16) * qf, __uint_as_float(w[k] & 0xFFFF0000u) * qf);
-        put(u, make_uint4(v[0], v[1], v[2], v[3]));
+        for (int off = 1; off < LPR; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        // f16 q: max|q| 2^e in [2^14, 2^15); E4M3 q: in [2^7, 2^8), as hi + lo
+        // (see qprefill.cu); max|q| = f 2^ex, f in [1/2, 1)
+        const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 126;
+        const int e = mx > 0.f ? min((Cfg::K8MMA ? 8 : 15) - ex, 100) : 0;
+        const float qf = pow2i(e);
+        if (live && c == 0) s_rs[m] = pow2i(-e);
+        if constexpr (Cfg::K8MMA) {
+          uint32_t hv[2], lv[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint32_t hp[2], lp[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const float x0 = v[4 * u + 2 * p] * qf, x1 = v[4 * u + 2 * p + 1] * qf;
+              const uint16_t h2 = f32x2_to_e4m3x2(x0, x1);
+              const uint32_t hb32 = e4m3x2_to_f16x2(h2);
+              const __half2 hb = *reinterpret_cast<const __half2*>(&hb32);
+              hp[p] = h2;
+              lp[p] = f32x2_to_e4m3x2(x0 - __low2float(hb), x1 - __high2float(hb));
+            }
+            hv[u] = hp[0] | (hp[1] << 16);
+            lv[u] = lp[0] | (lp[1] << 16);
+          }
+          if (live) {
+            *reinterpret_cast<uint2*>(at(c >> 1) + 8 * (c & 1)) = make_uint2(hv[0], hv[1]);
+            *reinterpret_cast<uint2*>(at(D / 16 + (c >> 1)) + 8 * (c & 1)) = make_uint2(lv[0], lv[1]);
+          }
+        } else {
+          uint32_t h[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) h[u] = pack_f16x2(v[2 * u] * qf, v[2 * u + 1] * qf);
+          if (live) *reinterpret_cast<uint4*>(at(c)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
       }
     }
-    return ldexpf(1.f, -e);
   }
 }
 
@@ -291,6 +301,18 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tslot;
+  // partial slot of query row r: [h][tile][split][row]
+  auto slot = [&](int r) { return ((static_cast<int64_t>(h) * a.tiles + r / 128) * a.nsplit + split) * 128 + r % 128; };
+
+  // the queries, by the softmax and the converter warps
+  if (warp < Cfg::W_TMA || warp >= Cfg::W_CONV) {
+    const int first = NP == 1 ? tile * 128 : 0;
+    prefix_queries<KK, KV, D>(a.q + static_cast<int64_t>(h) * a.G * D, first, min(a.rows - first, 128 * NP), a.G, a.Hq,
+                              Cfg::Q_TMEM ? sV : sQ, reinterpret_cast<float*>(sML),
+                              warp < Cfg::W_TMA ? warp : warp - Cfg::W_CONV + Cfg::W_TMA, Cfg::W_TMA + NCONV, lane);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    asm volatile("bar.sync 2, %0;" ::"n"(32 * (Cfg::W_TMA + NCONV)) : "memory");
+  }
 
   if (warp == Cfg::W_TMA) {
     // ------------------------------ TMA producer ---------------------------------
@@ -334,6 +356,8 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
             for (int kb = 0; kb < D / 64; ++kb)
               tma_load_2d(sK + ks * Cfg::F16 + kb * 8192, &tmk, kb * 128, y, &k_full[ks]);
           }
+          // the V ring holds the queries on their way to tensor memory at first
+          if (Cfg::Q_TMEM && !stop && j == 0 && !mbar_wait_bounded(q_ready, 0, a.status)) stop = 1;
           if (!stop && j >= NV && !mbar_wait_bounded(&v_empty[vs], ((j / NV) - 1) & 1, a.status)) stop = 1;
           if (!stop) {
             mbar_arrive_expect_tx(&v_full[vs], Cfg::F16);
@@ -387,6 +411,7 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
         if (i >= 1) {  // V(i - 1)
           const int jj = i - 1, rv = jj % NRV, vs = jj % NV;
           ok = mbar_wait_bounded(&rv_full[rv], (jj / NRV) & 1, a.status) && !*s_abort;
+          if (Cfg::Q_TMEM && ok && jj == 0) ok = mbar_wait_bounded(q_ready, 0, a.status);  // (queries in the V ring)
           if (ok && jj >= NV) ok = mbar_wait_bounded(&v_empty[vs], ((jj / NV) - 1) & 1, a.status) && !*s_abort;
           if (!ok) break;
           convert_tile<KV, D, QC::V_RB, 32 * (NCONV > 0 ? NCONV : 8)>(sRV + rv * QC::RV_STAGE, QC::RV_CODES, sV + vs * Cfg::F16, ct, 64);
@@ -410,7 +435,7 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
     if (lane == 0) {
       const int me = warp - Cfg::W_MMA, w = NP == 2 ? me : 0, count = count_of(w);
       const uint32_t tS = tmem + Cfg::COL_S + 128 * w, tO = tmem + Cfg::COL_O + 128 * w;
-      const uint64_t qd = Cfg::Q_TMEM ? 0 : tc::smem_desc(smem_u32(sQ + w * Cfg::Q_BYTES), 16, 1024);
+      const uint64_t qd = Cfg::Q_TMEM ? 0 : tc::smem_desc(smem_u32(sQ + (two ? w * Cfg::Q_BYTES : 0)), 16, 1024);
       constexpr int RK = Cfg::K8MMA ? NRK : NK, KS = Cfg::K8MMA ? QC::RK_STAGE : Cfg::K_STAGE;
       const uint64_t kd0 = tc::smem_desc(smem_u32(Cfg::K8MMA ? sRK : sK), 16, 1024);
       const uint64_t vd0 = tc::smem_desc(smem_u32(sV), 8192, 1024);
@@ -497,17 +522,21 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
     const bool live = __any_sync(0xffffffffu, row_valid);  // warps without rows only hand on
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tO = tmem + lane_base + Cfg::COL_O + 128 * w;
-    const uint4* src = nullptr;
-    if (row_valid) {
-      const int token = flat / a.G, g = flat % a.G;
-      src = reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(token) * a.Hq + h * a.G + g) * D);
-    }
-    float rs = prefix_query<KK, KV, D>(src, sQ + w * Cfg::Q_BYTES, tmem + lane_base + Cfg::COL_Q, m);
-    if constexpr (Cfg::Q_TMEM) {
+    float rs = 1.f;
+    if constexpr (Cfg::RAW) rs = reinterpret_cast<const float*>(sML)[NP == 1 ? m : flat];
+    if constexpr (Cfg::Q_TMEM) {  // the lane's row: 2 D bytes, a 32-bit column each
+#pragma unroll 1
+      for (int j0 = 0; j0 < 2 * D / 16; j0 += 8) {
+        uint32_t v[32];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint4 y = *reinterpret_cast<const uint4*>(sV + m * (2 * D) + (((j0 + u) ^ m) & (2 * D / 16 - 1)) * 16);
+          v[4 * u] = y.x, v[4 * u + 1] = y.y, v[4 * u + 2] = y.z, v[4 * u + 3] = y.w;
+        }
+        tc::st32(tmem + lane_base + Cfg::COL_Q + 4 * j0, v);
+      }
       tc::wait_st();
       tc::fence_before();
-    } else {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     __syncwarp();
     if (lane == 0) arrive(q_ready);
@@ -722,24 +751,24 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
         if (ok && live) put(1.f, false, 0.f);
       }
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(128 * NP) : "memory");
-    if (ok) {
-      // slot of query row r: [h][tile][split][row]
-      auto slot = [&](int r) { return ((static_cast<int64_t>(h) * a.tiles + r / 128) * a.nsplit + split) * 128 + r % 128; };
-      if (row_valid && (NP == 1 || two || w == 0)) a.ml[slot(flat)] = make_float2(M, L);
-      const int r0 = NP == 1 ? tile * 128 : 0, rows = NP == 1 ? min(a.rows - r0, 128) : a.rows;
-      for (int idx = tid; idx < rows * (D / 4); idx += 128 * NP) {
-        const int r = idx / (D / 4), c = (idx % (D / 4)) * 4;
-        *reinterpret_cast<float4*>(a.o + slot(r0 + r) * D + c) =
-            *reinterpret_cast<const float4*>(stage + r * Cfg::PITCH + c);
-      }
-    }
+    if (!ok) *s_abort = 1;
+    else if (row_valid && (NP == 1 || two || w == 0)) a.ml[slot(flat)] = make_float2(M, L);
   }
 
-  // ---- teardown: every issued MMA has completed before TMEM is freed ---------
+  // ---- rows out, and the teardown: every issued MMA has completed ----------------
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
+  if (!*s_abort) {
+    const int r0 = NP == 1 ? tile * 128 : 0, rows = NP == 1 ? min(a.rows - r0, 128) : a.rows;
+    const float* stage = reinterpret_cast<const float*>(smem);
+#pragma unroll 4
+    for (int idx = tid; idx < rows * (D / 4); idx += Cfg::THREADS) {
+      const int r = idx / (D / 4), c = (idx % (D / 4)) * 4;
+      *reinterpret_cast<float4*>(a.o + slot(r0 + r) * D + c) =
+          *reinterpret_cast<const float4*>(stage + r * Cfg::PITCH + c);
+    }
+  }
   if (warp == 0) tc::dealloc(tmem, 512);
 }
 

@@ -116,13 +116,6 @@ __device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&v)[16]) {
       : "memory");
 }
 
-// Each thread of the warp writes 4 consecutive 32-bit columns of its lane.
-__device__ __forceinline__ void st4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
-               "r"(d)
-               : "memory");
-}
-
 // 16x256b shape, 8 repetitions (64 columns) of the warp's lanes [0, 16):
 // thread t holds, for repetition k, v[4k], v[4k+1] = lane t/4, columns
 // 8k + 2(t%4) and 8k + 2(t%4) + 1, and v[4k+2], v[4k+3] = lane t/4 + 8, same
