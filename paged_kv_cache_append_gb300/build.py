@@ -1,4 +1,5 @@
-"""Builds libnk.so in-tree with nvcc for sm_103a.
+"""Builds libnk.so in-tree with nvcc for sm_103a, and the CPython module that
+marshals arguments for it (``_pyargs.so``, gcc).
 
 Each translation unit under ``csrc/`` is compiled in parallel into
 ``_build/`` and linked into ``paged_kv_cache_append_gb300/libnk.so``; the
@@ -13,12 +14,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnk.so")
+PYARGS = os.path.join(PKG, "_pyargs.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
@@ -49,10 +52,27 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def build_pyargs() -> str:
+    """Compiles csrc/pyargs.c against this interpreter's headers; returns its path."""
+    src = os.path.join(CSRC, "pyargs.c")
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(ROOT, "include", "nk.h")))
+    if os.path.exists(PYARGS) and os.path.getmtime(PYARGS) >= newest:
+        return PYARGS
+    tmp = PYARGS + ".tmp"
+    cmd = ["gcc", "-O2", "-Wall", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"], "-I",
+           os.path.join(ROOT, "include"), src, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for pyargs.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, PYARGS)
+    return PYARGS
+
+
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     """Compiles every CUDA source and links libnk.so; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
     extra = extra or []
+    build_pyargs()
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))

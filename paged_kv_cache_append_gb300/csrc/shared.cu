@@ -21,9 +21,6 @@ namespace nk {
 cudaError_t prefix_pass(const nk_pool* p, int layer, const void* q, const int32_t* tables, const int32_t* table_rows,
                         int Hq, float scale_log2, const PrefixParts& parts, const SharedPrefix& sh, cudaStream_t s);
 
-#ifndef NK_FRAC
-#define NK_FRAC 100
-#endif
 constexpr int kMaxPrefixSplits = 128;
 
 // When the prefix gets a pass of its own.  The pass costs about as much as c
@@ -49,7 +46,7 @@ static int make_shared_plan(const nk_pool* p, int B, int T, int Hq, SharedPlan* 
   const int H = p->desc.num_kv_heads, D = p->desc.head_dim, G = Hq / H;
   pl->tiles = (B * T * G + 127) / 128;
   // one CTA per SM; at head_dim 64 and 128 one CTA takes both tiles of a head
-  const int fit = p->num_sms * NK_FRAC / 100 / (H * (D == 256 ? pl->tiles : 1));
+  const int fit = p->num_sms / (H * (D == 256 ? pl->tiles : 1));
   pl->nsplit = fit < 1 ? 1 : fit > kMaxPrefixSplits ? kMaxPrefixSplits : fit;
   const size_t parts = static_cast<size_t>(H) * pl->tiles * pl->nsplit * 128;
   pl->sh_ml_bytes = parts * sizeof(float2);

@@ -296,34 +296,25 @@ def _stream(stream) -> int:
     return stream.cuda_stream if stream is not None else _current_stream(torch.cuda.current_device())
 
 
-def _rows(x, D: int, device: int, lead=None) -> Rows:
-    """nk_rows of a bf16 tensor [N, heads, D] or [B, T, heads, D] on CUDA device
-    `device`, with any token and head strides; `lead`: its sizes before the heads."""
-    import torch
-    shape, stride = x.shape, x.stride()
-    n = len(shape)
-    if x.dtype is not torch.bfloat16 or x.get_device() != device:
-        raise ValueError(f"expected a bf16 tensor on CUDA device {device}, got {x.dtype} on {x.device}")
-    if not 3 <= n <= 4 or shape[-1] != D or stride[-1] != 1 or (lead is not None and shape[:-2] != lead):
-        raise ValueError(f"expected {'...' if lead is None else tuple(lead)} + (heads, {D}) with a unit last stride, "
-                         f"got {tuple(shape)} with strides {stride}")
-    token = stride[-3]
-    if n == 4 and shape[0] > 1:
-        if shape[1] == 1:
-            token = stride[0]
-        elif stride[0] != shape[1] * token:
-            raise ValueError("the tokens of [B, T, heads, D] rows must be one stride apart")
-    # the stride of a dimension of size 1 says nothing
-    one = shape[0] == 1 and (n == 3 or shape[1] == 1)
-    return Rows(x.data_ptr(), 0 if one else token, stride[-2] if shape[-2] > 1 else 0)
+_pyargs = None
 
 
-def _cuda(x, dtype, shape, name, device: int) -> int:
-    """Checks a contiguous tensor argument on CUDA device `device`; its address."""
-    if x.dtype is not dtype or x.shape != shape or x.get_device() != device or not x.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on CUDA device {device}, got "
-                         f"{x.dtype} {tuple(x.shape)} on {x.device}")
-    return x.data_ptr()
+def _args():
+    """The CPython module that checks and marshals tensor arguments (csrc/pyargs.c)."""
+    global _pyargs
+    if _pyargs is None:
+        import torch
+
+        try:
+            from . import _pyargs as m
+        except ImportError as e:
+            raise RuntimeError("_pyargs is not built; run paged_kv_cache_append_gb300.build.build()") from e
+        lib = load()
+        m.init(*(C.cast(f, C.c_void_p).value for f in (lib.nk_qk_norm_rope, lib.nk_paged_kv_append_rope,
+                                                       lib.nk_paged_shared_decode_attention, lib.nk_verify_drafts)),
+               torch.bfloat16, torch.float32, torch.int32)
+        _pyargs = m
+    return _pyargs
 
 
 class Rope:
@@ -349,15 +340,10 @@ class Rope:
         w = q_weight if q_weight is not None else k_weight
         self.cos_sin, self.q_weight, self.k_weight = cos_sin, q_weight, k_weight
         self.device = cos_sin.get_device()
-        self.head_dim = None if w is None else w.numel()
+        self.head_dim = 0 if w is None else w.numel()   # 0: any
         self.desc = RopeDesc(_ptr(cos_sin), cos_sin.shape[0], rotary_dim, int(interleaved), eps, weight_offset, 0,
                              _ptr(q_weight), _ptr(k_weight))
-
-    def check(self, D: int, device: int) -> None:
-        if self.head_dim is not None and self.head_dim != D:
-            raise ValueError(f"norm weights have {self.head_dim} elements, the heads {D}")
-        if self.device != device:
-            raise ValueError("all operands must be on the device of the rotation table")
+        self.address = C.addressof(self.desc)
 
 
 def qk_norm_rope(q, k, positions, rope: Rope, q_out=None, k_out=None, stream=None):
@@ -365,23 +351,16 @@ def qk_norm_rope(q, k, positions, rope: Rope, q_out=None, k_out=None, stream=Non
     token and head strides) at ``positions`` int32 [N]; returns (q_out, k_out),
     new contiguous tensors unless given (q_out may be q itself, k_out k)."""
     import torch
-    dev, qs, ks = q.get_device(), q.shape, k.shape
-    if dev >= 0 and torch.cuda.current_device() != dev:
+    dev = rope.device
+    if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             return qk_norm_rope(q, k, positions, rope, q_out, k_out, stream)
-    D, lead = qs[-1], qs[:-2]
-    rope.check(D, dev)
     if q_out is None:
-        q_out = torch.empty(qs, dtype=q.dtype, device=q.device)
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if k_out is None:
-        k_out = torch.empty(ks, dtype=k.dtype, device=k.device)
-    if q_out.shape != qs or k_out.shape != ks:
-        raise ValueError("outputs must have the shapes of their inputs")
-    rq, rk = _rows(q, D, dev), _rows(k, D, dev, lead)
-    oq = rq if q_out is q else _rows(q_out, D, dev)
-    ok = rk if k_out is k else _rows(k_out, D, dev)
-    pos = _cuda(positions, torch.int32, lead, "positions", dev)
-    nk_qk_norm_rope(rope.desc, D, rq, qs[-2], rk, ks[-2], pos, positions.numel(), oq, ok, _stream(stream))
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    _check((_pyargs or _args()).norm_rope(q, k, positions, q_out, k_out, rope.address, rope.head_dim, dev,
+                                          _current_stream(dev) if stream is None else stream.cuda_stream))
     return q_out, k_out
 
 
@@ -394,38 +373,20 @@ def verify_drafts(target, tokens, uniforms, draft=None, draft_len=None, frontier
     Returns (accepted [B], tokens [B, K+1], frontiers [B] or None), int32.
     """
     import torch
-    B, K1, V = target.shape
-    K, dev = K1 - 1, target.get_device()
+    dev = target.get_device()
     if dev < 0:
         raise ValueError("target: expected a CUDA tensor")
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             return verify_drafts(target, tokens, uniforms, draft, draft_len, frontiers, stream)
-    strides = [V, V]
-    for i, (x, n) in enumerate(((target, K1), (draft, K))):
-        if x is None:
-            continue
-        if x.dtype is not torch.float32 or x.shape != (B, n, V) or x.get_device() != dev:
-            raise ValueError(f"{('target', 'draft')[i]}: expected a float32 tensor {(B, n, V)} on CUDA device {dev}, "
-                             f"got {x.dtype} {tuple(x.shape)} on {x.device}")
-        st = x.stride()
-        if B * n > 1:   # the stride of a dimension of size 1 says nothing
-            strides[i] = st[1] if n > 1 else st[0]
-        if n and ((V > 1 and st[2] != 1) or strides[i] < V or (B > 1 and n > 1 and st[0] != n * st[1])):
-            raise ValueError(f"{('target', 'draft')[i]}: rows must be contiguous and one stride apart")
-    pt = _cuda(tokens, torch.int32, (B, K), "tokens", dev)
-    pu = _cuda(uniforms, torch.float32, (B, K1), "uniforms", dev)
-    pl = None if draft_len is None else _cuda(draft_len, torch.int32, (B,), "draft_len", dev)
-    where = dict(dtype=torch.int32, device=target.device)
-    accepted, out = torch.empty(B, **where), torch.empty((B, K1), **where)
-    pf = pa = after = None
-    if frontiers is not None:
-        pf = _cuda(frontiers, torch.int32, (B,), "frontiers", dev)
-        after = torch.empty(B, **where)
-        pa = after.data_ptr()
-    nk_verify_drafts(target.data_ptr(), strides[0], draft.data_ptr() if draft is not None and K else None,
-                     strides[1], pt if K else None, pl, pu, pf, B, K, V, accepted.data_ptr(), out.data_ptr(), pa,
-                     _stream(stream))
+    B, K1, _ = target.shape
+    out = torch.empty((B, K1), dtype=torch.int32, device=target.device)
+    if frontiers is None:
+        accepted, after = torch.empty(B, dtype=torch.int32, device=target.device), None
+    else:
+        accepted, after = torch.empty_like(frontiers), torch.empty_like(frontiers)
+    _check((_pyargs or _args()).verify(target, draft, tokens, draft_len, uniforms, frontiers, accepted, out, after, dev,
+                                       _current_stream(dev) if stream is None else stream.cuda_stream))
     return accepted, out, after
 
 
@@ -449,6 +410,7 @@ class Pool:
         self.n_planes, self.plane_bytes, self.row_bytes = nk_pool_plane_bytes(self.desc, M)
         self.planes = [[torch.zeros(nb, dtype=torch.uint8, device=device) for nb in self.plane_bytes]
                        for _ in range(num_layers)]
+        self.device = self.planes[0][0].get_device()
         ptrs = [p.data_ptr() for layer in self.planes for p in layer]
         self.handle = nk_pool_create(self.desc, M, ptrs)
         self._ws = None
@@ -559,29 +521,17 @@ class Pool:
         strides, one token stride apart across rows; rows of q_out past a
         row's count are not written."""
         import torch
-        dev = self.planes[0][0].get_device()
+        dev = self.device
         if torch.cuda.current_device() != dev:
             with torch.cuda.device(dev):
                 return self.append_rope(layer, tables, table_rows, write_pos, k, v, rope, q, q_out, counts, stream)
-        rope.check(self.D, dev)
-        lead = k.shape[:2]
-        if k.dim() != 4 or k.shape[2] != self.H or v.shape != k.shape:
-            raise ValueError(f"k and v must be [B, T, {self.H}, {self.D}]")
-        B, T = lead
-        rk, rv, rq, Hq, pq = _rows(k, self.D, dev), _rows(v, self.D, dev), None, 0, None
-        if q is not None:
-            rq, Hq = _rows(q, self.D, dev, lead), q.shape[2]
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            pq = _cuda(q_out, torch.bfloat16, q.shape, "q_out", dev)
-        elif q_out is not None:
-            raise ValueError("q_out without q")
-        pt = _cuda(tables, torch.int32, (self.C, self.L), "tables", dev)
-        pr = _cuda(table_rows, torch.int32, (B,), "table_rows", dev)
-        pw = _cuda(write_pos, torch.int32, (B,), "write_pos", dev)
-        pc = None if counts is None else _cuda(counts, torch.int32, (B,), "counts", dev)
-        nk_paged_kv_append_rope(self.handle, layer, pt, pr, pw, pc, rope.desc, rk, rv, rq, Hq, pq, B, T,
-                                _stream(stream))
+        if rope.device != dev:
+            raise ValueError("the rotation table is on another device than the pool")
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _check((_pyargs or _args()).append_rope(
+            self.handle, self.H, self.D, self.C, self.L, layer, tables, table_rows, write_pos, k, v, q, q_out, counts,
+            rope.address, rope.head_dim, dev, _current_stream(dev) if stream is None else stream.cuda_stream))
         return q_out
 
     def shared_workspace(self, B, T, Hq):
@@ -598,29 +548,22 @@ class Pool:
         choice, 0: always).  Without ``workspace`` one is allocated for this
         call."""
         import torch
-        B, T, Hq, D = q.shape
-        dev = self.planes[0][0].get_device()
+        dev = self.device
         if torch.cuda.current_device() != dev:
             with torch.cuda.device(dev):
                 return self.shared_decode(layer, q, tables, table_rows, frontiers, shared_pages, scale, out, lse,
                                           workspace, stream, share_from)
-        pq = _cuda(q, torch.bfloat16, (B, T, Hq, self.D), "q", dev)
-        pt = _cuda(tables, torch.int32, (self.C, self.L), "tables", dev)
-        pr = _cuda(table_rows, torch.int32, (B,), "table_rows", dev)
-        pf = _cuda(frontiers, torch.int32, (B,), "frontiers", dev)
-        if shared_pages.get_device() != dev or shared_pages.dtype is not torch.int32 or shared_pages.numel() != 1:
-            raise ValueError("shared_pages must be one int32 value on the pool's device")
         if out is None:
             out = torch.empty_like(q)
         if lse is None:
-            lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
-        po = _cuda(out, torch.bfloat16, q.shape, "out", dev)
-        pl = _cuda(lse, torch.float32, (B, T, Hq), "lse", dev)
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
         ws = workspace
         if ws is None:
-            ws = self.shared_workspace(B, T, Hq)
+            ws = self.shared_workspace(*q.shape[:3])
             if stream is not None:
                 ws.record_stream(stream)
-        nk_paged_shared_decode_attention(pq, Hq, self.handle, layer, pt, pr, pf, shared_pages.data_ptr(), B, T,
-                                         float(scale), po, pl, share_from, ws.data_ptr(), ws.numel(), _stream(stream))
+        _check((_pyargs or _args()).shared_decode(
+            self.handle, self.D, self.C, self.L, layer, q, tables, table_rows, frontiers, shared_pages, float(scale),
+            out, lse, share_from, ws.data_ptr(), ws.numel(), dev,
+            _current_stream(dev) if stream is None else stream.cuda_stream))
         return out, lse

@@ -97,8 +97,9 @@ def test_norm_rope_one_operand_and_one_token():
     qo, ko = nk.qk_norm_rope(q, k, pos, rope)
     a, b = torch.zeros_like(q), torch.zeros_like(k)
     s = torch.cuda.current_stream().cuda_stream
-    nk.nk_qk_norm_rope(rope.desc, D, nk._rows(q, D, 0), Hq, None, 0, pos.data_ptr(), 1, nk._rows(a, D, 0), None, s)
-    nk.nk_qk_norm_rope(rope.desc, D, None, 0, nk._rows(k, D, 0), H, pos.data_ptr(), 1, None, nk._rows(b, D, 0), s)
+    rows = lambda t: nk.Rows(t.data_ptr(), t.stride(0), t.stride(1))  # noqa: E731
+    nk.nk_qk_norm_rope(rope.desc, D, rows(q), Hq, None, 0, pos.data_ptr(), 1, rows(a), None, s)
+    nk.nk_qk_norm_rope(rope.desc, D, None, 0, rows(k), H, pos.data_ptr(), 1, None, rows(b), s)
     assert torch.equal(a, qo) and torch.equal(b, ko)
 
 

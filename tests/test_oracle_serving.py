@@ -160,11 +160,117 @@ def test_pool_calls_refuse_null(lib):
                                        None) == -1
 
 
-def test_python_wrappers_refuse_cpu_tensors():
-    t = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
+def test_python_wrappers_refuse_cpu_tensors(lib):
     with pytest.raises(ValueError):
         nk.Rope(torch.zeros((4, 32)), 32)
     with pytest.raises(ValueError):
-        nk._rows(t, 64, 0)
-    with pytest.raises(ValueError):
         nk.verify_drafts(torch.zeros((1, 2, 5)), torch.zeros((1, 1), dtype=torch.int32), torch.zeros((1, 2)))
+
+
+class Fake:
+    """A tensor as far as the argument checks look: shape, strides, type, device, address."""
+
+    def __init__(self, *shape, stride=None, dtype=torch.bfloat16, device=0, ptr=64):
+        step, st = 1, []
+        for n in reversed(shape):
+            st.append(step)
+            step *= n
+        self.shape, self.dtype = torch.Size(shape), dtype
+        self._stride, self._device, self._ptr = stride or tuple(reversed(st)), device, ptr
+
+    def stride(self):
+        return self._stride
+
+    def get_device(self):
+        return self._device
+
+    def data_ptr(self):
+        return self._ptr
+
+
+def _args_norm(**kw):
+    d = dict(q=Fake(3, 4, 64), k=Fake(3, 2, 64), pos=Fake(3, dtype=torch.int32), qo=Fake(3, 4, 64), ko=Fake(3, 2, 64),
+             rope=_rope(layout=9), hd=0)
+    d.update(kw)
+    return nk._args().norm_rope(d["q"], d["k"], d["pos"], d["qo"], d["ko"], ctypes.addressof(d["rope"]), d["hd"], 0, 0)
+
+
+I32, F32 = torch.int32, torch.float32
+
+
+@pytest.mark.parametrize("bad", [
+    dict(q=Fake(3, 4, 64, dtype=F32)), dict(q=Fake(3, 4, 64, device=1)), dict(q=Fake(3, 4, 64, device=-1)),
+    dict(q=Fake(4, 64)), dict(q=Fake(3, 4, 64, stride=(256, 64, 2))), dict(k=Fake(2, 2, 64)), dict(k=Fake(3, 2, 128)),
+    dict(qo=Fake(3, 5, 64)), dict(ko=Fake(3, 2, 64, dtype=F32)), dict(pos=Fake(3)), dict(pos=Fake(4, dtype=I32)),
+    dict(pos=Fake(3, dtype=I32, stride=(2,))), dict(hd=128), dict(q=Fake(1, 2, 3, 4, 64)),
+    dict(q=Fake(2, 3, 4, 64, stride=(1000, 256, 64, 1)), k=Fake(2, 3, 2, 64))])
+def test_argument_checks_norm_rope(lib, bad):
+    assert _args_norm() == -1                       # good arguments reach the library, which refuses the layout
+    with pytest.raises(ValueError):
+        _args_norm(**bad)
+
+
+def test_argument_checks_sizes_of_one_and_rows_apart(lib):
+    """Strides of dimensions of size 1 say nothing; [B, 1] tokens may be any stride apart."""
+    odd = Fake(1, 1, 64, stride=(7, 3, 1))
+    assert _args_norm(q=odd, qo=odd, k=odd, ko=odd, pos=Fake(1, dtype=I32, stride=(5,))) == -1
+    apart = dict(q=Fake(2, 1, 4, 64, stride=(1000, 3, 64, 1)), qo=Fake(2, 1, 4, 64), k=Fake(2, 1, 2, 64),
+                 ko=Fake(2, 1, 2, 64), pos=Fake(2, 1, dtype=I32))
+    assert _args_norm(**apart) == -1
+
+
+def _args_verify(**kw):
+    d = dict(p=Fake(2, 3, 10, dtype=F32), q=Fake(2, 2, 10, dtype=F32), x=Fake(2, 2, dtype=I32), dl=None,
+             u=Fake(2, 3, dtype=F32), f=None, acc=Fake(2, dtype=I32, ptr=0), out=Fake(2, 3, dtype=I32), after=None)
+    d.update(kw)
+    return nk._args().verify(d["p"], d["q"], d["x"], d["dl"], d["u"], d["f"], d["acc"], d["out"], d["after"], 0, 0)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(p=Fake(2, 3, 10)), dict(p=Fake(6, 10, dtype=F32)), dict(p=Fake(2, 0, 10, dtype=F32)),
+    dict(p=Fake(2, 3, 10, dtype=F32, stride=(30, 9, 1))), dict(p=Fake(2, 3, 10, dtype=F32, stride=(40, 12, 1))),
+    dict(q=Fake(2, 3, 10, dtype=F32)), dict(q=Fake(2, 2, 9, dtype=F32)), dict(x=Fake(2, 2, dtype=torch.int64)),
+    dict(x=Fake(2, 3, dtype=I32)), dict(u=Fake(2, 2, dtype=F32)), dict(dl=Fake(3, dtype=I32)),
+    dict(f=Fake(2, dtype=F32), after=Fake(2, dtype=I32))])
+def test_argument_checks_verify(lib, bad):
+    assert _args_verify() == -1                     # reaches the library, which refuses the NULL output
+    assert _args_verify(p=Fake(2, 3, 10, dtype=F32, stride=(36, 12, 1))) == -1
+    with pytest.raises(ValueError):
+        _args_verify(**bad)
+
+
+def _args_append(**kw):
+    d = dict(layer=0, t=Fake(3, 5, dtype=I32), r=Fake(2, dtype=I32), w=Fake(2, dtype=I32), k=Fake(2, 4, 2, 64),
+             v=Fake(2, 4, 2, 64), q=Fake(2, 4, 8, 64), qo=Fake(2, 4, 8, 64), c=None, hd=64)
+    d.update(kw)
+    return nk._args().append_rope(0, 2, 64, 3, 5, d["layer"], d["t"], d["r"], d["w"], d["k"], d["v"], d["q"], d["qo"],
+                                  d["c"], ctypes.addressof(_rope()), d["hd"], 0, 0)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(t=Fake(2, 5, dtype=I32)), dict(r=Fake(3, dtype=I32)), dict(w=Fake(2)), dict(k=Fake(2, 4, 3, 64)),
+    dict(k=Fake(8, 2, 64)), dict(v=Fake(2, 3, 2, 64)), dict(q=Fake(2, 5, 8, 64)), dict(q=Fake(2, 4, 8, 128)),
+    dict(qo=Fake(2, 4, 7, 64)), dict(q=None), dict(c=Fake(1, dtype=I32)), dict(hd=128)])
+def test_argument_checks_append_rope(lib, bad):
+    assert _args_append() == -1                     # reaches the library, which refuses the NULL pool
+    assert _args_append(q=None, qo=None) == -1
+    with pytest.raises(ValueError):
+        _args_append(**bad)
+
+
+def _args_shared(**kw):
+    d = dict(q=Fake(2, 1, 8, 64), t=Fake(3, 5, dtype=I32), r=Fake(2, dtype=I32), f=Fake(2, dtype=I32),
+             s=Fake(1, dtype=I32), o=Fake(2, 1, 8, 64), l=Fake(2, 1, 8, dtype=F32))
+    d.update(kw)
+    return nk._args().shared_decode(0, 64, 3, 5, 0, d["q"], d["t"], d["r"], d["f"], d["s"], 0.1, d["o"], d["l"], -1, 64,
+                                    64, 0, 0)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(q=Fake(2, 1, 8, 128)), dict(q=Fake(2, 8, 64)), dict(q=Fake(2, 1, 8, 64, stride=(1024, 512, 64, 1))),
+    dict(t=Fake(3, 6, dtype=I32)), dict(r=Fake(1, dtype=I32)), dict(f=Fake(2, dtype=F32)), dict(s=Fake(2, dtype=I32)),
+    dict(s=Fake(1)), dict(o=Fake(2, 1, 4, 64)), dict(l=Fake(2, 1, 8))])
+def test_argument_checks_shared_decode(lib, bad):
+    assert _args_shared() == -1                     # reaches the library, which refuses the NULL pool
+    with pytest.raises(ValueError):
+        _args_shared(**bad)
