@@ -254,7 +254,8 @@ static int prob_rows(PyObject* x, const char* name, long dev, const int64_t* siz
 /* (target, draft or None, tokens, draft_len or None, uniforms, frontiers or None, accepted, out, after or None,
  *  device, stream); the last three tensors are nk.py's own */
 static PyObject* verify(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  Tensor p, q, x, dl, u, f, acc, out, after;
+  Tensor p, q, x, dl, u, f;
+  long long acc, out, after = 0;
   int64_t ps, qs = 0;
   if (!want(n, 11)) return NULL;
   const long dev = PyLong_AsLong(a[9]);
@@ -264,20 +265,21 @@ static PyObject* verify(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (B > INT32_MAX || K > INT32_MAX || V > INT32_MAX) return refuse("target", "expected smaller sizes", a[0]), NULL;
   const int64_t size[3] = {B, K, V}, bk1[2] = {B, K + 1};
   if (!prob_rows(a[0], "target", dev, p.size, &p, &ps)) return NULL;
-  q.ptr = dl.ptr = f.ptr = after.ptr = NULL;
+  q.ptr = dl.ptr = f.ptr = NULL;
   if (!NONE(a[1]) && !prob_rows(a[1], "draft", dev, size, &q, &qs)) return NULL;
   if (!plain(a[2], "tokens", t_i32, dev, 2, size, &x) || !plain(a[4], "uniforms", t_f32, dev, 2, bk1, &u)) return NULL;
   if (!NONE(a[3]) && !plain(a[3], "draft_len", t_i32, dev, 1, size, &dl)) return NULL;
   if (!NONE(a[5]) && (!plain(a[5], "frontiers", t_i32, dev, 1, size, &f) ||
-                      !plain(a[8], "frontiers", t_i32, dev, 1, size, &after)))
+                      !long_of(PyObject_CallMethodNoArgs(a[8], n_data_ptr), &after)))
     return NULL;
-  if (!plain(a[6], "accepted", t_i32, dev, 1, size, &acc) || !plain(a[7], "tokens", t_i32, dev, 2, bk1, &out))
+  if (!long_of(PyObject_CallMethodNoArgs(a[6], n_data_ptr), &acc) ||
+      !long_of(PyObject_CallMethodNoArgs(a[7], n_data_ptr), &out))
     return NULL;
   void* stream = ADDRESS(a[10]);
   if (PyErr_Occurred()) return NULL;
   int rc;
   CALL(rc, lib.verify(p.ptr, ps, K ? q.ptr : NULL, qs, K ? x.ptr : NULL, dl.ptr, u.ptr, f.ptr, (int32_t)B, (int32_t)K,
-                      (int32_t)V, acc.ptr, out.ptr, after.ptr, stream))
+                      (int32_t)V, (int32_t*)acc, (int32_t*)out, (int32_t*)after, stream))
   return PyLong_FromLong(rc);
 }
 

@@ -3,7 +3,7 @@
 // (nk_paged_kv_append_rope, with the step's queries in the same launch).
 //
 // Both are one pass over the data, bound by HBM for long inputs and by the
-// launch and two dependent loads for a decode step.  A warp holds 32 / (D/8)
+// launch and two dependent loads for a decode step.  A warp holds 32 / (D/16)
 // rows (rope.cuh).  Units of work are (token, group of heads of one operand); a
 // lane reads the position's angles once for the heads of its unit.  The units
 // are laid out operand by operand (all of q, then k and v), each operand padded
@@ -11,16 +11,6 @@
 #include <cmath>
 
 #include "rope.cuh"
-
-#ifndef NK_WANT
-#define NK_WANT 16
-#endif
-#ifndef NK_RING
-#define NK_RING 4
-#endif
-#ifndef NK_MINB
-#define NK_MINB 8
-#endif
 
 namespace nk {
 
@@ -56,7 +46,17 @@ static RowsIn rows_in(const nk_rows* r) {
 }
 
 constexpr int kRopeThreads = 128;
-constexpr int kRing = NK_RING;  // rows of a lane in flight in a long unit
+// Long inputs are bound by HBM and close behind by the issue rate.  Rows of a
+// lane in flight, blocks per SM and warps per SM below which the heads of a
+// token are spread over more units, with the times of 32749 tokens of 32 + 4
+// heads of 128, an append of 8 x 2048 ragged tokens of 16 + 2 + 2 heads of 256
+// and 2048 tokens of 16 + 2 heads of 256, in us (the copy rate gives 91.5, 42.3
+// and 5.9):
+//   4 rows, 5 blocks, 8 warps    94.5  52.4   9.2   (taken)
+//   2 rows                       97.3  55.3
+//   4 blocks / 6 blocks          94.4  55.8  /  95.4  51.3
+//   16 warps / 32 warps                       10.6  /  14.9
+constexpr int kRing = 4, kRopeBlocks = 5, kRopeWarps = 8;
 
 // Work of one operand: units of `hpu` heads of one token, padded to whole
 // warps; a warp of rpw rows takes rpw units.
@@ -86,20 +86,23 @@ __device__ __forceinline__ void copy_async16(uint32_t smem, const void* p) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(p) : "memory");
 }
 
-// Rows 0 .. n - 1 of this lane (n alike in the warp): `src(i)` is the address of
-// its 16 bytes or nullptr, `begin()` runs while the first are on their way, then
-// `body(i, bytes)` for every row.  RING: a private ring of 16-byte slots in
+// Rows 0 .. n - 1 of this lane (n alike in the warp): `src(i)` is the row's
+// address or nullptr, `begin()` runs while the first are on their way, then
+// `body(i, chunks)` for every row.  RING: a private ring of 16-byte slots in
 // shared memory, filled by cp.async kRing rows ahead (the bytes in flight cost
 // no registers, and a lane reads only what it copied, so no barrier is needed).
 // Otherwise, for up to two rows, plain loads.
 template <bool RING, class Src, class Begin, class Body>
-__device__ __forceinline__ void for_rows(uint4* slots, int n, Src src, Begin begin, Body body) {
+__device__ __forceinline__ void for_rows(uint4* slots, int n, const Chunks& ch, Src src, Begin begin, Body body) {
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   if constexpr (RING) {
     const uint32_t at = smem_u32(slots);
     auto fetch = [&](int i) {
       const __nv_bfloat16* p = i < n ? src(i) : nullptr;
-      if (p) copy_async16(at + (i % kRing) * (kRopeThreads * 16), p);
+      if (p) {
+        copy_async16(at + (2 * (i % kRing)) * (kRopeThreads * 16), p + ch.a);
+        copy_async16(at + (2 * (i % kRing) + 1) * (kRopeThreads * 16), p + ch.b);
+      }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
@@ -108,15 +111,21 @@ __device__ __forceinline__ void for_rows(uint4* slots, int n, Src src, Begin beg
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
-      body(i, src(i) ? slots[(i % kRing) * kRopeThreads] : zero);
+      uint4 v[2] = {zero, zero};
+      if (src(i)) {
+        v[0] = slots[(2 * (i % kRing)) * kRopeThreads];
+        v[1] = slots[(2 * (i % kRing) + 1) * kRopeThreads];
+      }
+      body(i, v);
       fetch(i + kRing);
     }
   } else {
-    uint4 v[2];
+    uint4 v[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const __nv_bfloat16* p = i < n ? src(i) : nullptr;
-      v[i] = p ? *reinterpret_cast<const uint4*>(p) : zero;
+      v[i][0] = p ? *reinterpret_cast<const uint4*>(p + ch.a) : zero;
+      v[i][1] = p ? *reinterpret_cast<const uint4*>(p + ch.b) : zero;
     }
     begin();
 #pragma unroll
@@ -137,9 +146,9 @@ struct NormRopeArgs {
 };
 
 template <int D, bool RING>
-__global__ void __launch_bounds__(kRopeThreads, RING ? NK_MINB : 1) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  __shared__ uint4 ring[RING ? kRing * kRopeThreads : 1];
+__global__ void __launch_bounds__(kRopeThreads, RING ? kRopeBlocks : 1) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+  constexpr int LPR = D / 16, RPW = 32 / LPR;
+  __shared__ uint4 ring[RING ? 2 * kRing * kRopeThreads : 1];
   griddep_wait();  // launched with programmatic stream serialization
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, l = lane % LPR;
@@ -149,23 +158,27 @@ __global__ void __launch_bounds__(kRopeThreads, RING ? NK_MINB : 1) norm_rope_ke
   if (u >= a.work[op].units) return;
   const Unit x = unit_of(u + lane / LPR, a.N, a.work[op]);
   const RowsIn in = a.in[op], out = a.out[op];
-  const __nv_bfloat16* src = in.ptr + x.token * in.token_stride + x.head0 * in.head_stride + 8 * l;
-  __nv_bfloat16* dst = const_cast<__nv_bfloat16*>(out.ptr) + x.token * out.token_stride + x.head0 * out.head_stride + 8 * l;
+  const Chunks ch = chunks_of(a.rp, l);
+  const __nv_bfloat16* src = in.ptr + x.token * in.token_stride + x.head0 * in.head_stride;
+  __nv_bfloat16* dst = const_cast<__nv_bfloat16*>(out.ptr) + x.token * out.token_stride + x.head0 * out.head_stride;
   Turn t;
   bool ok = false;
   for_rows<RING>(
-      ring + threadIdx.x, a.work[op].hpu,
+      ring + threadIdx.x, a.work[op].hpu, ch,
       [&](int i) { return x.live && i < x.heads ? src + i * in.head_stride : nullptr; },
       [&] {
         const int pos = x.live ? a.positions[x.token] : 0;
         ok = x.live && pos >= 0 && pos < a.rp.positions;
         if (x.live && !ok && l == 0) set_status(a.status, NK_STATUS_FRONTIER);
-        load_turn<LPR>(a.rp, a.w[op], ok ? pos : 0, lane, l, t);
+        load_turn(a.rp, a.w[op], ok ? pos : 0, ch, t);
       },
-      [&](int i, const uint4& raw) {
-        F2 y[4];
-        norm_rotate<LPR>(raw, a.rp, t, y);
-        if (ok && i < x.heads) *reinterpret_cast<uint4*>(dst + i * out.head_stride) = pack8_bf16(y);
+      [&](int i, const uint4 (&raw)[2]) {
+        Row16 y;
+        norm_rotate<LPR>(raw, a.rp, ch, t, y);
+        if (ok && i < x.heads) {
+          *reinterpret_cast<uint4*>(dst + i * out.head_stride + ch.a) = pack8_bf16(y);
+          *reinterpret_cast<uint4*>(dst + i * out.head_stride + ch.b) = pack8_bf16(y + 4);
+        }
       });
 }
 
@@ -183,11 +196,11 @@ static void plan_work(Work* w, int heads, int64_t tokens, int rpw, int64_t want)
 
 template <int D>
 static cudaError_t launch_norm_rope(NormRopeArgs a, int sms, cudaStream_t s) {
-  constexpr int RPW = 32 / (D / 8);
+  constexpr int RPW = 32 / (D / 16);
   uint32_t warps = 0;
   bool ring = false;
   for (int i = 0; i < 2; ++i) {
-    plan_work(&a.work[i], a.work[i].heads, a.N, RPW, int64_t(NK_WANT) * sms);
+    plan_work(&a.work[i], a.work[i].heads, a.N, RPW, int64_t(kRopeWarps) * sms);
     warps += a.work[i].units / RPW;
     ring = ring || a.work[i].hpu > 1;
   }
@@ -214,10 +227,10 @@ struct AppendRopeArgs {
 };
 
 template <int KK, int KV, int D, bool RING>
-__global__ void __launch_bounds__(kRopeThreads, RING ? NK_MINB : 1)
+__global__ void __launch_bounds__(kRopeThreads, RING ? kRopeBlocks : 1)
     append_rope_kernel(const __grid_constant__ AppendRopeArgs a) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  __shared__ uint4 ring[RING ? kRing * kRopeThreads : 1];
+  constexpr int LPR = D / 16, RPW = 32 / LPR;
+  __shared__ uint4 ring[RING ? 2 * kRing * kRopeThreads : 1];
   griddep_wait();  // launched with programmatic stream serialization
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, l = lane % LPR;
@@ -229,6 +242,7 @@ __global__ void __launch_bounds__(kRopeThreads, RING ? NK_MINB : 1)
   const int b = x.token / a.T, t = x.token - b * a.T;
   bool ok = x.live && t < (a.counts ? a.counts[b] : a.T);
   const int hpu = a.work[op].hpu;
+  const Chunks ch = chunks_of(a.rp, l);
   Turn turn;
   int row = 0, pos = 0;
   auto begin = [&] {
@@ -240,28 +254,33 @@ __global__ void __launch_bounds__(kRopeThreads, RING ? NK_MINB : 1)
       ok = row >= 0 && row < a.C && pos >= 0 && pos < a.L * 64 && pos < a.rp.positions;
     }
     if (read && !ok && l == 0) set_status(a.status, NK_STATUS_FRONTIER);
-    load_turn<LPR>(a.rp, a.w[op], ok ? pos : 0, lane, l, turn);
+    load_turn(a.rp, a.w[op], ok ? pos : 0, ch, turn);
   };
+  const bool read = ok;
   if (op == 0) {
-    const __nv_bfloat16* src = a.q.ptr + x.token * a.q.token_stride + x.head0 * a.q.head_stride + 8 * l;
-    __nv_bfloat16* dst = a.q_out + (static_cast<int64_t>(x.token) * a.work[0].heads + x.head0) * D + 8 * l;
-    const bool read = ok;
+    const __nv_bfloat16* src = a.q.ptr + x.token * a.q.token_stride + x.head0 * a.q.head_stride;
+    __nv_bfloat16* dst = a.q_out + (static_cast<int64_t>(x.token) * a.work[0].heads + x.head0) * D;
     for_rows<RING>(
-        ring + threadIdx.x, hpu, [&](int i) { return read && i < x.heads ? src + i * a.q.head_stride : nullptr; },
+        ring + threadIdx.x, hpu, ch, [&](int i) { return read && i < x.heads ? src + i * a.q.head_stride : nullptr; },
         begin,
-        [&](int i, const uint4& raw) {
-          F2 y[4];
-          norm_rotate<LPR>(raw, a.rp, turn, y);
-          if (ok && i < x.heads) *reinterpret_cast<uint4*>(dst + i * D) = pack8_bf16(y);
+        [&](int i, const uint4 (&raw)[2]) {
+          Row16 y;
+          norm_rotate<LPR>(raw, a.rp, ch, turn, y);
+          if (ok && i < x.heads) {
+            *reinterpret_cast<uint4*>(dst + i * D + ch.a) = pack8_bf16(y);
+            *reinterpret_cast<uint4*>(dst + i * D + ch.b) = pack8_bf16(y + 4);
+          }
         });
     return;
   }
-  const __nv_bfloat16* ksrc = a.k.ptr + x.token * a.k.token_stride + x.head0 * a.k.head_stride + 8 * l;
-  const __nv_bfloat16* vsrc = a.v.ptr + x.token * a.v.token_stride + x.head0 * a.v.head_stride + 8 * l;
+  const __nv_bfloat16* ksrc = a.k.ptr + x.token * a.k.token_stride + x.head0 * a.k.head_stride;
+  const __nv_bfloat16* vsrc = a.v.ptr + x.token * a.v.token_stride + x.head0 * a.v.head_stride;
+  constexpr bool GROUPS = KK == KIND_INT8 || KV == KIND_NVFP4;  // scales of part of a row
+  __shared__ float s_max[GROUPS ? kRopeThreads * 2 : 1];
+  float* maxima = GROUPS ? s_max + (threadIdx.x / LPR) * (D / 8) : s_max;
   int64_t tile0 = 0, pitch = 0;  // plane row of the token for the unit's first head, and the heads' distance
-  const bool read = ok;
   for_rows<RING>(
-      ring + threadIdx.x, 2 * hpu,
+      ring + threadIdx.x, 2 * hpu, ch,
       [&](int i) -> const __nv_bfloat16* {
         const int h = i < hpu ? i : i - hpu;
         if (!read || h >= x.heads) return nullptr;
@@ -279,20 +298,25 @@ __global__ void __launch_bounds__(kRopeThreads, RING ? NK_MINB : 1)
         tile0 = tile_row(g, x.head0, a.work[1].heads, a.M, a.head_major) + (pos & 63);
         pitch = a.head_major ? static_cast<int64_t>(a.M) * 64 : 64;
       },
-      [&](int i, const uint4& raw) {
-        F2 y[4];
+      [&](int i, const uint4 (&raw)[2]) {
+        Row16 y;
         if (i < hpu) {
           const int64_t r = tile0 + i * pitch;
-          norm_rotate<LPR>(raw, a.rp, turn, y);
-          encode8<KK, D>(y, a.kc + r * code_row_bytes<KK>(D), a.ks + r * scale_row_bytes<KK>(D), l, ok && i < x.heads);
+          norm_rotate<LPR>(raw, a.rp, ch, turn, y);
+          encode16<KK, D>(y, a.kc + r * code_row_bytes<KK>(D), a.ks + r * scale_row_bytes<KK>(D), ch, l,
+                          ok && i < x.heads, maxima);
         } else {  // values: the codec alone
           const bool live = ok && i - hpu < x.heads;
           const int64_t r = tile0 + (i - hpu) * pitch;
           if constexpr (KV == KIND_BF16) {  // the bits unchanged
-            if (live) *reinterpret_cast<uint4*>(a.vc + r * (2 * D) + 16 * l) = raw;
+            if (live) {
+              *reinterpret_cast<uint4*>(a.vc + r * (2 * D) + 2 * ch.a) = raw[0];
+              *reinterpret_cast<uint4*>(a.vc + r * (2 * D) + 2 * ch.b) = raw[1];
+            }
           } else {
-            unpack8(raw, y);
-            encode8<KV, D>(y, a.vc + r * code_row_bytes<KV>(D), a.vs + r * scale_row_bytes<KV>(D), l, live);
+            unpack8(raw[0], y);
+            unpack8(raw[1], y + 4);
+            encode16<KV, D>(y, a.vc + r * code_row_bytes<KV>(D), a.vs + r * scale_row_bytes<KV>(D), ch, l, live, maxima);
           }
         }
       });
@@ -300,11 +324,11 @@ __global__ void __launch_bounds__(kRopeThreads, RING ? NK_MINB : 1)
 
 template <int KK, int KV, int D>
 static cudaError_t launch_append_rope(AppendRopeArgs a, int sms, cudaStream_t s) {
-  constexpr int RPW = 32 / (D / 8);
+  constexpr int RPW = 32 / (D / 16);
   uint32_t warps = 0;
   bool ring = false;
   for (int i = 0; i < 2; ++i) {
-    plan_work(&a.work[i], a.work[i].heads, static_cast<int64_t>(a.B) * a.T, RPW, int64_t(NK_WANT) * sms);
+    plan_work(&a.work[i], a.work[i].heads, static_cast<int64_t>(a.B) * a.T, RPW, int64_t(kRopeWarps) * sms);
     warps += a.work[i].units / RPW;
     ring = ring || a.work[i].hpu > 1;
   }

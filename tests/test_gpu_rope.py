@@ -271,6 +271,29 @@ def test_append_rope_without_rope_is_the_append(profile, D):
     assert torch.equal(a.q_out, a.q)
 
 
+@pytest.mark.parametrize("profile", PROFILES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T", [3, 5000])
+def test_append_rope_without_rope_of_any_bits(profile, D, T):
+    """Every bit pattern a row can hold (infinities, NaN, subnormals, both
+    zeros), few tokens and many: the append's bytes.  Only a NaN of a BF16 key
+    or query may change its payload."""
+    a = Appended(profile, D, 4, 3, T, [0, 33], rd=0, norm=False, fused=False, S=5100, positions=5100)
+    g = torch.Generator().manual_seed(D + T)
+    for x in (a.q, a.k, a.v):
+        bits = torch.randint(-2 ** 15, 2 ** 15, x.shape, dtype=torch.int16, generator=g)
+        bits[:, ::2] &= -0x4001                               # every other token of magnitudes below 2
+        x.copy_(bits.view(torch.bfloat16))
+    a.run()
+    plain = nk.Pool(profile, 2, a.H, D, 5100, 2, a.pool.M)
+    plain.append(1, a.d["tables"], a.d["rows"], a.d["at"], a.k, a.v)
+    same = lambda x, y: torch.equal(x.isnan(), y.isnan()) and torch.equal(  # noqa: E731
+        x.view(torch.int16)[~x.isnan()], y.view(torch.int16)[~y.isnan()])
+    for i, (x, y) in enumerate(zip(a.pool.planes[1], plain.planes[1])):
+        assert same(x.view(torch.bfloat16), y.view(torch.bfloat16)) if profile == "bf16" and i == 0 else torch.equal(x, y)
+    assert same(a.q_out, a.q)
+
+
 def test_append_rope_equals_norm_rope_then_append_in_bf16():
     """Over a BF16 pool the result is rounded once either way: the same bits."""
     a = Appended("bf16", 128, 8, 2, 9, [60, 7])

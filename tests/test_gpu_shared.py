@@ -158,8 +158,8 @@ def test_any_number_of_shared_pages(profile, pages):
 
 
 @pytest.mark.parametrize("profile", PROFILES)
-@pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("B,G,T,pages", [(2, 1, 1, 25), (8, 1, 3, 24), (3, 16, 2, 15), (6, 8, 4, 26), (8, 4, 4, 13)])
+@pytest.mark.parametrize("D,B,G,T,pages", [(64, 8, 1, 3, 24), (64, 6, 8, 4, 26), (128, 2, 1, 1, 25), (128, 3, 16, 2, 15),
+                                           (128, 8, 4, 4, 26), (256, 2, 8, 1, 25), (256, 8, 4, 4, 13)])
 def test_many_pages_per_range(profile, D, B, G, T, pages):
     """So many KV heads that a range is many pages: the rings, the score
     buffers and the parities go around several times; 2 to 192 query rows, so
