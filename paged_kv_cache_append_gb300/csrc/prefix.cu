@@ -314,6 +314,7 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
     asm volatile("bar.sync 2, %0;" ::"n"(32 * (Cfg::W_TMA + NCONV)) : "memory");
   }
 
+  int k_sent = 0, v_sent = 0;  // tiles whose copies were issued (by the producer's lane 0)
   if (warp == Cfg::W_TMA) {
     // ------------------------------ TMA producer ---------------------------------
     int gnext = 0;
@@ -337,6 +338,7 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
             for (int c = 0; c < QC::KCB / QC::K_RB; ++c)
               tma_load_2d(st + c * 64 * QC::K_RB, &tmk, c * QC::K_RB, y, &rk_full[rk]);
             bulk_load(st + QC::RK_CODES, a.ks + static_cast<int64_t>(y) * QC::KSB, 64 * QC::KSB, &rk_full[rk]);
+            ++k_sent;
           }
           if (!stop && j >= NRV && !mbar_wait_bounded(&rv_empty[rv], ((j / NRV) - 1) & 1, a.status)) stop = 1;
           if (!stop) {
@@ -346,6 +348,7 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
             for (int c = 0; c < QC::VCB / QC::V_RB; ++c)
               tma_load_2d(st + c * 64 * QC::V_RB, &tmv, c * QC::V_RB, y, &rv_full[rv]);
             bulk_load(st + QC::RV_CODES, a.vs + static_cast<int64_t>(y) * QC::VSB, 64 * QC::VSB, &rv_full[rv]);
+            ++v_sent;
           }
         } else {
           const int ks = j % NK, vs = j % NV;
@@ -355,6 +358,7 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
 #pragma unroll
             for (int kb = 0; kb < D / 64; ++kb)
               tma_load_2d(sK + ks * Cfg::F16 + kb * 8192, &tmk, kb * 128, y, &k_full[ks]);
+            ++k_sent;
           }
           // the V ring holds the queries on their way to tensor memory at first
           if (Cfg::Q_TMEM && !stop && j == 0 && !mbar_wait_bounded(q_ready, 0, a.status)) stop = 1;
@@ -364,6 +368,7 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
 #pragma unroll
             for (int kb = 0; kb < D / 64; ++kb)
               tma_load_2d(sV + vs * Cfg::F16 + kb * 8192, &tmv, kb * 128, y, &v_full[vs]);
+            ++v_sent;
           }
         }
         if (stop) *s_abort = 1;
@@ -768,6 +773,11 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
       *reinterpret_cast<float4*>(a.o + slot(r0 + r) * D + c) =
           *reinterpret_cast<const float4*>(stage + r * Cfg::PITCH + c);
     }
+  } else if (warp == Cfg::W_TMA && lane == 0) {  // after an abort, the copies still in flight land before the CTA exits
+    constexpr int RK = Cfg::RAW ? NRK : NK, RV = Cfg::RAW ? NRV : NV;
+    uint64_t *kf = Cfg::RAW ? rk_full : k_full, *vf = Cfg::RAW ? rv_full : v_full;
+    for (int j = max(0, k_sent - RK); j < k_sent; ++j) mbar_wait_bounded(&kf[j % RK], (j / RK) & 1, a.status, 100000000ull);
+    for (int j = max(0, v_sent - RV); j < v_sent; ++j) mbar_wait_bounded(&vf[j % RV], (j / RV) & 1, a.status, 100000000ull);
   }
   if (warp == 0) tc::dealloc(tmem, 512);
 }
@@ -776,11 +786,11 @@ template <int KK, int KV, int D>
 static cudaError_t launch_prefix(const nk_pool* p, int layer, const PrefixArgs& a, cudaStream_t s) {
   using Cfg = PrefixCfg<KK, KV, D>;
   auto k = prefix_kernel<KK, KV, D>;
-  static bool attr = false;
-  if (!attr) {
+  static int attr = -1;  // the device that has it
+  if (attr != p->device) {
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
     if (e != cudaSuccess) return e;
-    attr = true;
+    attr = p->device;
   }
   return launch_pdl(k, dim3(a.nsplit, a.H * (Cfg::NP == 1 ? a.tiles : 1)), dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0],
                     p->tmap[layer * 2 + 1], a);

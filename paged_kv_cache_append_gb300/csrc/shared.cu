@@ -12,6 +12,7 @@
 //                pages behind the prefix, as partials too;
 //   merge        M = max m, out = sum 2^(m - M) O / sum 2^(m - M) l, below.
 // The shared pages cross HBM once per call instead of once per row.
+#include <algorithm>
 #include <cmath>
 
 #include "decode.cuh"
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(kMergeRows * 8 * SUB) shared_merge_kernel(cons
   constexpr int S_MAX = kMaxSplits + kMaxPrefixSplits, U = 8, THREADS = kMergeRows * 8 * SUB;
   __shared__ int s_F[8];
   __shared__ int s_row[8];
-  __shared__ float s_w[kMergeRows * S_MAX];  // weights
+  __shared__ float s_w[kMergeRows * S_MAX];  // weights; -1: a partial without keys, which has no accumulators
   const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
   const int d0 = (blockIdx.z % (D / 32)) * 32, q0 = (blockIdx.z / (D / 32)) * kMergeRows;
   const int warp = tid >> 5, lane = tid & 31;
@@ -151,22 +152,22 @@ __global__ void __launch_bounds__(kMergeRows * 8 * SUB) shared_merge_kernel(cons
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float L = 0.f;
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
-      w[u].x = M == -INFINITY || !(w[u].y > 0.f) ? 0.f : ex2(w[u].x - M);
-      L += w[u].y * w[u].x;
+    for (int u = 0; u < N; ++u) {  // (a NaN sum goes on into L and from there into every weight)
+      w[u].x = w[u].y == 0.f ? -1.f : ex2(w[u].x - M);
+      L += w[u].y == 0.f ? 0.f : w[u].y * w[u].x;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = 1.f / L;
 #pragma unroll
     for (int u = 0; u < N; ++u) {
       const int k = lane + 32 * u;
-      if (k < splits) s_w[wr * S_MAX + k] = w[u].x * inv;
+      if (k < splits) s_w[wr * S_MAX + k] = w[u].x == -1.f ? -1.f : w[u].x * inv;
     }
     if (lane == 0 && a.lse && d0 == 0) {
       const int qr = q0 + wr;
       a.lse[(static_cast<int64_t>(b) * a.T + qr / a.G) * a.Hq + h * a.G + qr % a.G] =
-          L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+          L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
     }
   }
   __syncthreads();
@@ -181,8 +182,8 @@ __global__ void __launch_bounds__(kMergeRows * 8 * SUB) shared_merge_kernel(cons
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = k0 + SUB * u;
-      const float w = live && k < splits ? s_w[r * S_MAX + k] : 0.f;
-      if (w > 0.f) {  // a partial without keys has no accumulators
+      const float w = live && k < splits ? s_w[r * S_MAX + k] : -1.f;
+      if (w != -1.f) {
         acc.x = fmaf(w, v[u].x, acc.x);
         acc.y = fmaf(w, v[u].y, acc.y);
         acc.z = fmaf(w, v[u].z, acc.z);
@@ -260,6 +261,7 @@ extern "C" int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const
   int64_t page_bytes = 0;
   for (int i = 0; i < pool->n_planes; ++i) page_bytes += int64_t(NK_PAGE_TOKENS) * pool->plane[i].row_bytes;
   const bool tensor = T * (Hq / pool->desc.num_kv_heads) > 16;
+  share_from = std::min(share_from, int64_t(1) << 60);  // (above every pool's)
   if (share_from < 0) share_from = tensor ? kShareFromTensor : kShareFrom;
   const int64_t saved = (B - (tensor ? kShareRowsTensor : kShareRows)) * page_bytes * pool->desc.num_kv_heads;  // a page
   const int64_t least = share_from == 0 ? 1 : saved <= 0 ? INT32_MAX : (share_from + saved - 1) / saved;

@@ -116,6 +116,40 @@ def test_norm_rope_positions_out_of_range_are_skipped():
     check_bf16(qo[[0, 3]], ref[[0, 3]], m[[0, 3]])
 
 
+def test_norm_rope_strides_past_32_bits():
+    """Tokens 2^30 + 64 elements apart (the last one 4 GB and more into the
+    buffer), in place: the bits of the packed rows."""
+    rope, *_ = make_rope(64, 32, True, True)
+    step = 2 ** 30 + 64
+    buf = torch.empty(2 * step + 4 * 64, dtype=torch.bfloat16, device=DEV)
+    x = buf.as_strided((3, 4, 64), (step, 64, 1))
+    x.copy_(normal((3, 4, 64), 6))
+    pos = torch.tensor([1, 2, 500], dtype=torch.int32, device=DEV)
+    ref = nk.qk_norm_rope(x[:, :3].contiguous(), x[:, 3:].contiguous(), pos, rope)
+    nk.qk_norm_rope(x[:, :3], x[:, 3:], pos, rope, q_out=x[:, :3], k_out=x[:, 3:])
+    assert torch.equal(x[:, :3], ref[0]) and torch.equal(x[:, 3:], ref[1])
+
+
+def test_norm_rope_captured_on_another_stream():
+    """Captured on a side stream and replayed with other rows and positions."""
+    rope, cs, wq, wk = make_rope(128, 128, False, True)
+    q, k = torch.zeros((9, 4, 128), dtype=torch.bfloat16, device=DEV), torch.zeros((9, 2, 128), dtype=torch.bfloat16, device=DEV)
+    qo, ko, pos = torch.empty_like(q), torch.empty_like(k), torch.zeros(9, dtype=torch.int32, device=DEV)
+    nk.qk_norm_rope(q, k, pos, rope, q_out=qo, k_out=ko)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        nk.qk_norm_rope(q, k, pos, rope, q_out=qo, k_out=ko)
+    for turn in range(3):
+        x, y = normal((9, 4, 128), 50 + turn), normal((9, 2, 128), 60 + turn)
+        p = np.random.default_rng(turn).integers(0, 512, 9).astype(np.int32)
+        q.copy_(x), k.copy_(y), pos.copy_(torch.from_numpy(p))
+        g.replay()
+        for got, src, w in ((qo, x, wq), (ko, y, wk)):
+            ref, m = OR.norm_rotate(f64(src), cs, p, 128, False, w)
+            check_bf16(got, ref, m)
+
+
 def test_norm_rope_extremes():
     """A zero row stays zero under the norm, the largest bf16 magnitudes stay
     finite without it, and infinities and NaN stay in their own rows."""

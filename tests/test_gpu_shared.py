@@ -262,6 +262,83 @@ def test_bad_rows_and_pages_do_not_fault():
     check(out[[0, 2]], lse[[0, 2]], [r[[0, 2]] for r in ref])
 
 
+@pytest.mark.parametrize("profile,D", [("bf16", 128), ("bf16", 256), ("fp8_row", 64), ("fp8_row", 256), ("k8v4", 128)])
+@pytest.mark.parametrize("plane", [0, 1])
+@pytest.mark.parametrize("page,token", [(1, 5), (4, 63), (6, 3)])
+def test_a_visible_nan_is_not_lost(profile, D, plane, page, token):
+    """A key or value of NaN in a shared page (1, 4) or in a row's own (6) makes
+    the outputs that see it NaN, and no others: as the plain decode."""
+    if profile == "k8v4" and plane == 1:
+        pytest.skip("E2M1 codes have no NaN")
+    b = Batch(profile, D, 2, 4, 1, 6, [64 * 6 + x for x in (1, 4, 70, 200)])
+    rows = b.gpu.planes[0][plane].view(b.gpu.M, b.H, 64, -1)
+    rows[int(b.tables[b.rows[2], page]), 1, token] = 0xFF
+    out, lse = b.run(6)
+    ref, _ = b.gpu.decode(0, b.d["q"], b.d["tables"], b.d["rows"], b.d["F"], b.scale)
+    nan = torch.zeros(out.shape, dtype=torch.bool)
+    nan[slice(None) if page < 6 else 2, :, 4:] = True
+    assert torch.equal(out.isnan(), nan) and torch.equal(ref.cpu().isnan(), nan)
+    assert torch.equal(lse.isnan(), nan[..., 0]) if plane == 0 else not lse.isnan().any()
+
+
+def test_pool_past_32_bits():
+    """Planes of 5 GB, every page behind the first 4 GB: the rotated append and
+    the attention give a small pool's bits."""
+    D, H, G, pages = 128, 8, 4, 6
+    F = [64 * pages + x for x in (3, 70)]
+    small = Batch("bf16", D, H, G, 1, pages, F)
+    L, M = 20000, 40000
+    big = nk.Pool("bf16", 1, H, D, 64 * L, 2, M)
+    far = small.tables + np.int32(M - 1 - small.tables.max())
+    wide = np.full((2, L), M, np.int32)
+    wide[:, :far.shape[1]] = far
+    assert int(far.min()) * H * 64 * D * 2 > 2 ** 32
+    for p, s in zip(big.planes[0], small.gpu.planes[0]):
+        p = p.view(M, -1)
+        p[torch.from_numpy(far.ravel()).to(DEV).long()] = s.view(small.gpu.M, -1)[dev(small.tables.ravel()).long()]
+    rope = nk.Rope(dev(OR.table(1024, D)), D, q_weight=normal(D, 1).to(DEV), k_weight=normal(D, 2).to(DEV))
+    x = normal((2, 1, H * G + 2 * H, D), 7).to(DEV)
+    q, k, v = x.split([H * G, H, H], 2)
+    got = []
+    for pool, tables in ((small.gpu, small.d["tables"]), (big, dev(wide))):
+        qr = pool.append_rope(0, tables, small.d["rows"], small.d["F"], k, v, rope, q=q)
+        o, l = pool.shared_decode(0, qr, tables, small.d["rows"], small.d["F"] + 1, dev([pages], torch.int32),
+                                  small.scale, share_from=0)
+        got.append((qr, o, l))
+    for a, c in zip(*got):
+        assert torch.equal(a, c)
+    for p, s in zip(big.planes[0], small.gpu.planes[0]):
+        assert torch.equal(p.view(M, -1)[torch.from_numpy(far.ravel()).to(DEV).long()],
+                           s.view(small.gpu.M, -1)[dev(small.tables.ravel()).long()])
+
+
+def test_two_graphs_that_share_a_workspace():
+    """Two captured calls of different shapes over one workspace, replayed in
+    turn on one stream with other numbers of shared pages and frontiers."""
+    a = Batch("fp8_row", 128, 2, 8, 1, 20, [64 * 20 + 9 * i + 1 for i in range(8)])
+    b = Batch("k8v4", 128, 4, 4, 4, 12, [64 * 12 + 50 * i + 5 for i in range(5)])
+    ws = torch.empty(max(x.gpu.shared_workspace(x.B, x.T, x.Hq).numel() for x in (a, b)), dtype=torch.uint8, device=DEV)
+    graphs, outs, shared = [], [], [dev([20], torch.int32), dev([12], torch.int32)]
+    for x, n in zip((a, b), shared):
+        x.gpu.shared_decode(0, x.d["q"], x.d["tables"], x.d["rows"], x.d["F"], n, x.scale, workspace=ws, share_from=0)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(x.gpu.shared_decode(0, x.d["q"], x.d["tables"], x.d["rows"], x.d["F"], n, x.scale,
+                                            workspace=ws, share_from=0))
+        graphs.append(g)
+    refs = [x.reference() for x in (a, b)]
+    for take in ((20, 12), (7, 3), (0, 12), (20, 0)):     # pages attended once: the same results
+        for n, t in zip(shared, take):
+            n.fill_(t)
+        for _ in range(2):
+            for g in graphs:
+                g.replay()
+        torch.cuda.synchronize()
+        for (o, l), ref in zip(outs, refs):
+            check(o.cpu(), l.cpu(), ref)
+
+
 def test_refusals():
     b = Batch("bf16", 64, 1, 4, 1, 2, [140, 150])
     with pytest.raises(nk.NkError) as e:

@@ -155,6 +155,23 @@ def test_many_sequences_and_repeats():
         assert all(np.array_equal(a, b) for a, b in zip(first[:2], again[:2]))
 
 
+def test_rows_past_32_bits():
+    """Largest vocabulary, more than 2^31 probabilities on both sides: the last
+    sequences' draws come from the last rows."""
+    B, K, V = 20, 7, 1 << 24
+    p, q = torch.zeros((B, K + 1, V), device=DEV), torch.zeros((B, K, V), device=DEV)
+    x = torch.arange(B * K, dtype=torch.int32, device=DEV).view(B, K) * 100003 % V
+    p.scatter_(2, x.long()[..., None], 0.75)
+    p[:, K, V - 1], p[:, K, 5] = 0.5, 0.25                    # u = 0.5: behind token 5
+    q.scatter_(2, x.long()[..., None], 1.0)
+    p[B - 1, K - 1], q[B - 1, K - 1] = 0.0, 0.0               # the last draft of the last sequence falls
+    p[B - 1, K - 1, V - 2], q[B - 1, K - 1, V - 2] = 0.5, 0.25
+    n, tok, _ = nk.verify_drafts(p, x, torch.full((B, K + 1), 0.5, device=DEV), draft=q)
+    assert n.tolist() == [K] * (B - 1) + [K - 1]
+    assert torch.equal(tok[:-1, :K], x[:-1]) and tok[:-1, K].tolist() == [V - 1] * (B - 1)
+    assert tok[-1].tolist() == x[-1, :K - 1].tolist() + [V - 2, -1]
+
+
 def test_frontiers_in_place_and_other_stream():
     rng = np.random.default_rng(6)
     p, q = rows(rng, (4, 3), 500, 20), rows(rng, (4, 2), 500, 20)
