@@ -123,21 +123,30 @@ struct PrefixCfg {
 // whatever is in them stays in their own scores and outputs, which nobody
 // reads.  (The softmax threads alone, a row each, took 5.3 us for 64 rows of
 // FP8 pages at head_dim 256, most of it converting.)
+constexpr int kQBatch = 4;  // loads of a lane in flight
+
+template <int D>
+__device__ __forceinline__ void load_queries(const __nv_bfloat16* q, int first, int n, int G, int Hq, int g0, int PW,
+                                             int lane, uint4 (&x)[kQBatch]) {
+  constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows a load
+#pragma unroll
+  for (int k = 0; k < kQBatch; ++k) {
+    const int m = (g0 + k * PW) * RPI + lane / LPR, flat = first + m;
+    x[k] = m < n ? *reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(flat / G) * Hq + flat % G) * D +
+                                                   8 * (lane % LPR))
+                 : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
 template <int KK, int KV, int D>
 __device__ __forceinline__ void prefix_queries(const __nv_bfloat16* q, int first, int n, int G, int Hq, uint8_t* sq,
-                                               float* s_rs, int pw, int PW, int lane) {
+                                               float* s_rs, int pw, int PW, int lane, uint4 (&x)[kQBatch]) {
   using Cfg = PrefixCfg<KK, KV, D>;
-  constexpr int LPR = D / 8, RPI = 32 / LPR, BATCH = 4;  // lanes a row, rows a load, loads in flight
+  constexpr int LPR = D / 8, RPI = 32 / LPR, BATCH = kQBatch;
   const int sub = lane / LPR, c = lane % LPR;
 #pragma unroll 1
   for (int g0 = pw; g0 * RPI < n; g0 += BATCH * PW) {
-    uint4 x[BATCH];
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      const int m = (g0 + k * PW) * RPI + sub, flat = first + m;
-      x[k] = m < n ? *reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(flat / G) * Hq + flat % G) * D + 8 * c)
-                   : make_uint4(0u, 0u, 0u, 0u);
-    }
+    if (g0 != pw) load_queries<D>(q, first, n, G, Hq, g0, PW, lane, x);
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       const int m = (g0 + k * PW) * RPI + sub;
@@ -244,6 +253,15 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
   griddep_wait();  // launched with programmatic stream serialization
   griddep_launch_dependents();
 
+  // the first of the queries that this warp prepares (below), on their way with the plan's reads
+  const int q_first = NP == 1 ? tile * 128 : 0, q_rows = min(a.rows - q_first, 128 * NP);
+  const int q_warp = warp < Cfg::W_TMA ? warp : warp - Cfg::W_CONV + Cfg::W_TMA;
+  constexpr int QWARPS = Cfg::W_TMA + NCONV;
+  const __nv_bfloat16* q_head = a.q + static_cast<int64_t>(h) * a.G * D;
+  uint4 q_x[kQBatch];
+  const bool q_mine = warp < Cfg::W_TMA || warp >= Cfg::W_CONV;
+  if (q_mine) load_queries<D>(q_head, q_first, q_rows, a.G, a.Hq, q_warp, QWARPS, lane, q_x);
+
   // ---- this CTA's pages [p_lo, p_lo + n) -----------------------------------------
   const int pages = *a.sh.pages;
   const int row = prefix_row(a.sh, a.table_rows, pages, a.L, a.C);
@@ -305,13 +323,11 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
   auto slot = [&](int r) { return ((static_cast<int64_t>(h) * a.tiles + r / 128) * a.nsplit + split) * 128 + r % 128; };
 
   // the queries, by the softmax and the converter warps
-  if (warp < Cfg::W_TMA || warp >= Cfg::W_CONV) {
-    const int first = NP == 1 ? tile * 128 : 0;
-    prefix_queries<KK, KV, D>(a.q + static_cast<int64_t>(h) * a.G * D, first, min(a.rows - first, 128 * NP), a.G, a.Hq,
-                              Cfg::Q_TMEM ? sV : sQ, reinterpret_cast<float*>(sML),
-                              warp < Cfg::W_TMA ? warp : warp - Cfg::W_CONV + Cfg::W_TMA, Cfg::W_TMA + NCONV, lane);
+  if (q_mine) {
+    prefix_queries<KK, KV, D>(q_head, q_first, q_rows, a.G, a.Hq, Cfg::Q_TMEM ? sV : sQ, reinterpret_cast<float*>(sML),
+                              q_warp, QWARPS, lane, q_x);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    asm volatile("bar.sync 2, %0;" ::"n"(32 * (Cfg::W_TMA + NCONV)) : "memory");
+    asm volatile("bar.sync 2, %0;" ::"n"(32 * QWARPS) : "memory");
   }
 
   int k_sent = 0, v_sent = 0;  // tiles whose copies were issued (by the producer's lane 0)

@@ -61,9 +61,9 @@ struct SharedMergeArgs {
   PrefixParts prefix;
 };
 
-constexpr int kMergeRows = 8;  // query rows of one merge CTA
+constexpr int kMergeRows = 4;  // query rows of one merge CTA
 
-// One CTA per (row, KV head, 8 query rows, 32 dims): the row's own splits
+// One CTA per (row, KV head, 4 query rows, 32 dims): the row's own splits
 // followed by the prefix's, at most kMaxSplits + kMaxPrefixSplits partials a
 // query row.  The plan (before the wait) overlaps the kernels before.  Bound by
 // the latency of three dependent reads and, for many partials, by L2: the
@@ -207,8 +207,10 @@ __global__ void __launch_bounds__(kMergeRows * 8 * SUB) shared_merge_kernel(cons
 }
 
 // SUB threads share 4 dims of a query row.  Over 16 query rows a row, with four
-// times the CTAs, 2 take less than 4 (116 against 121 us for the 4-token verify
-// of 8 rows); below, 4 (40.5 against 44.8 us for one token of 8 rows).
+// times the CTAs, 2 take less than 4 (116 against 120 us for the 4-token verify
+// of 8 rows); below, 8 take less than 4 (35.0 against 37.2 us for one token of 8
+// rows; CTAs of 8 query rows 35.9 either way, 4 or 14 loads of a thread in
+// flight 40.3 and 37.9).
 template <int SUB>
 static cudaError_t launch_merge(int D, dim3 grid, cudaStream_t s, const SharedMergeArgs& m) {
   const dim3 block(kMergeRows * 8 * SUB);
@@ -313,7 +315,7 @@ extern "C" int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const
   m.prefix = parts;
   const int D = pool->desc.head_dim;
   const dim3 grid(B, a.H, D / 32 * ((T * a.G + kMergeRows - 1) / kMergeRows));
-  e = T * a.G > 16 ? launch_merge<2>(D, grid, s, m) : launch_merge<4>(D, grid, s, m);
+  e = T * a.G > 16 ? launch_merge<2>(D, grid, s, m) : launch_merge<8>(D, grid, s, m);
   if (e != cudaSuccess) return cuda_fail(e, "merge launch");
   return NK_OK;
 }
