@@ -284,6 +284,8 @@ int nk_shared_decode_workspace_bytes(const nk_pool* pool, int32_t B, int32_t T, 
  *   library's measured choice, 64 MiB (32 MiB for T * Hq / H > 16).
  *   workspace: nk_shared_decode_workspace_bytes bytes, no initialisation
  *   needed; two calls that share a workspace must not overlap.
+ * A NaN among the keys or values that a row sees makes its outputs NaN (an
+ * infinite value may too).
  * Three launches: the prefix on the tensor cores, all B * T * Hq / H query
  * rows of a KV head in 128-row tiles (csrc/prefix.cu; softmax weights and
  * values are rounded as in nk_paged_prefill_attention, but BF16 weights to 16
@@ -418,7 +420,7 @@ int nk_paged_kv_append_rope(nk_pool* pool, int32_t layer, const int32_t* block_t
  *   d = max(p_n - q_n, 0) for n < K_b (p_n itself where that is 0 everywhere),
  *   d = p_{K_b} for n = K_b,
  * summed in more than 46 bits; entries that are not positive and finite weigh
- * 0 (p and q need not sum to 1).  Where rounding leaves no such j, or
+ * 0 (p and q need not sum to 1; their sums have to be finite in fp32).  Where rounding leaves no such j, or
  * uniforms[b][K] is not below 1, the last token with weight is taken.
  *   target: device fp32, row (b, i) of V at target + (b * (K + 1) + i) *
  *   target_stride, i <= K;  draft: row (b, i) at draft + (b * K + i) *
@@ -432,6 +434,8 @@ int nk_paged_kv_append_rope(nk_pool* pool, int32_t layer, const int32_t* block_t
  * A drafted token outside [0, V) is rejected and a sequence without any weight
  * gets -1 (NK_STATUS_TOKEN_RANGE).  Runs on the current device, which must
  * hold every array.  The same inputs give the same bits on every call.
+ * nk_paged_append_decode_attention reads its frontiers before the kernel ahead
+ * of it has ended: frontiers_out is not for such a call launched right behind.
  * Errors: NK_ERR_INVALID_ARG, NK_ERR_SHAPE (B in [1, 2^20], K in [0, 1024],
  * V in [1, 2^24], strides >= V), NK_ERR_CUDA. */
 int nk_verify_drafts(const float* target, int64_t target_stride, const float* draft,

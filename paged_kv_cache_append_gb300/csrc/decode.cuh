@@ -80,14 +80,15 @@ struct DecodeArgs {
   // Pages every row shares (device; nullptr: none).  A row that takes part
   // (takes_part) is attended from its first own page on, its table and
   // frontier moved by that many pages, and every row's partials go to the
-  // workspace, for the merge with the prefix's (shared.cu).
+  // workspace, for the merge with the prefix's (shared.cu).  The kernels are
+  // instantiated for it (SHARED): as a choice at run time it cost the plain
+  // decode of FP8-row pages at head_dim 256 0.9%.
   const int32_t* shared = nullptr;
   int shared_least = 1;
 };
 
 // Pages of row (F, row) that the prefix pass covers.
 __device__ __forceinline__ int pages_before(const DecodeArgs& a, int F, int row) {
-  if (a.shared == nullptr) return 0;
   const int pages = *a.shared;
   return takes_part(pages, a.shared_least, F, row, a.T, a.L, a.C) ? pages : 0;
 }
@@ -239,7 +240,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-template <int KK, int KV, int D, int NQT>
+template <int KK, int KV, int D, int NQT, bool SHARED>
 __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeCfg<KK, KV, D, NQT>::MINB))
     decode_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                   DecodeArgs a) {
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
   uint64_t* app = empty + NSTAGE;                           // fused append done (NW arrivals)
   int* s_flags = reinterpret_cast<int*>(app + 1);           // [0] abort
   int* s_F = s_flags + 4;                                   // [8] valid length per row
-  int* s_row = s_flags + 12;                                // [8] first table entry per row
+  int* s_row = s_flags + 12;                                // [8] table row per row; SHARED: its first entry
   float* s_qmax = reinterpret_cast<float*>(s_flags + 20);   // [8] per-warp max|q|
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -295,8 +296,8 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
   // In the shared-prefix attention the kernel before is the prefix pass, which
   // waited for everything before itself and shares nothing with this one: it
   // is waited for at the end alone, for the merge behind both.
-  const bool early = a.k_new != nullptr;
-  if (!early && a.shared == nullptr) griddep_wait();
+  const bool early = !SHARED && a.k_new != nullptr;
+  if (!early && !SHARED) griddep_wait();
   griddep_launch_dependents();
 
   // ---- per-row lengths, loaded once in parallel ------------------------------
@@ -304,9 +305,10 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
     const int F = a.frontiers[tid], row = a.table_rows[tid];
     const bool ok = F >= 0 && F <= a.L * 64 && row >= 0 && row < a.C && (a.k_new == nullptr || F >= a.T);
     if (!ok && blockIdx.x == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
-    const int before = pages_before(a, F, row);
+    int before = 0;
+    if constexpr (SHARED) before = pages_before(a, F, row);
     s_F[tid] = ok ? F - 64 * before : 0;
-    s_row[tid] = ok ? row * a.L + before : 0;  // the row's first table entry
+    s_row[tid] = ok ? (SHARED ? row * a.L + before : row) : 0;
   }
   __syncthreads();
 
@@ -338,13 +340,13 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
   const int F = s_F[b];
   const int p0 = split * chunk;
   const int n = min(chunk, npages - p0);  // pages of this CTA (0 only for a row without keys)
-  const bool fused = a.k_new != nullptr;
+  const bool fused = !SHARED && a.k_new != nullptr;
   const int app_lo = fused ? (F - a.T) >> 6 : 0x7fffffff;  // first page that receives new tokens
   const int R_real = a.T * a.G;
 
   // ---- producer warp: stage pages p0 .. p0+n-1 ---------------------------------
   if (warp == NW) {
-    const int32_t* table = a.tables + s_row[b] + p0;
+    const int32_t* table = a.tables + (SHARED ? s_row[b] : static_cast<int64_t>(s_row[b]) * a.L) + p0;
     int gnext = 0;
     bool app_seen = false;
     for (int i = 0; i < n; ++i) {
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
   if (fused) {
     constexpr int KCBW = code_row_bytes<KK>(D), VCBW = code_row_bytes<KV>(D);
     constexpr int KSBW = scale_row_bytes<KK>(D), VSBW = scale_row_bytes<KV>(D);
-    const int32_t* trow = a.tables + s_row[b];
+    const int32_t* trow = a.tables + static_cast<int64_t>(s_row[b]) * a.L;
     for (int t = warp; t < a.T; t += NW) {
       const int pos = F - a.T + t;
       const int pg = pos >> 6;
@@ -1061,7 +1063,7 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
         }
   }
   consumer_sync<NCONS>();
-  const bool final_out = nsplit == 1 && a.shared == nullptr;
+  const bool final_out = !SHARED && nsplit == 1;
   const int64_t part0 = (static_cast<int64_t>(b) * a.H + h) * a.target;
   const int64_t part = part0 + split;
   for (int idx = tid; idx < R_real * (D / 4); idx += NCONS) {
@@ -1098,7 +1100,7 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
       a.ws_ml[part * R + tid] = make_float2(row_M[tid], row_L[tid]);
     }
   }
-  if (a.shared != nullptr) griddep_wait();
+  if constexpr (SHARED) griddep_wait();
 }
 
 // ---- log-sum-exp merge of the splits (separate launch) ----------------------------
@@ -1205,11 +1207,11 @@ __global__ void __launch_bounds__(256) merge_kernel(DecodeArgs a) {
   }
 }
 
-template <int KK, int KV, int D, int NQT>
+template <int KK, int KV, int D, int NQT, bool SHARED>
 cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a,
                           dim3 grid, cudaStream_t s) {
   using Cfg = DecodeCfg<KK, KV, D, NQT>;
-  auto k = decode_kernel<KK, KV, D, NQT>;
+  auto k = decode_kernel<KK, KV, D, NQT, SHARED>;
   static bool attr_set = false;
   if (!attr_set) {
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
@@ -1217,7 +1219,7 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const De
     attr_set = true;
   }
   cudaError_t e = launch_pdl(k, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, tk, tv, a);
-  if (e != cudaSuccess || a.shared != nullptr) return e;
+  if (e != cudaSuccess || SHARED) return e;
   return launch_pdl(merge_kernel<D, NQT>, dim3(a.B, a.H, D / 32), dim3(256), 0, s, a);
 }
 
@@ -1233,7 +1235,7 @@ int decode_ctas_per_sm() {
   using Cfg = DecodeCfg<KK, KV, D, NQT>;
   static int cached = 0;
   if (!cached) {
-    auto k = decode_kernel<KK, KV, D, NQT>;
+    auto k = decode_kernel<KK, KV, D, NQT, false>;
     cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
     int n = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, Cfg::THREADS, Cfg::SMEM) != cudaSuccess || n < 1)
@@ -1255,7 +1257,9 @@ cudaError_t decode_dispatch(const nk_pool* p, int layer, const DecodeArgs& a, in
   const CUtensorMap& tv = p->tmap[layer * 2 + 1];
   const int D = p->desc.head_dim;
 #define NK_CASE(DD, Q) \
-  if (D == DD && nqt == Q) return launch_decode<KK, KV, DD, Q>(tk, tv, a, grid, s);
+  if (D == DD && nqt == Q)                                                            \
+    return a.shared ? launch_decode<KK, KV, DD, Q, true>(tk, tv, a, grid, s)          \
+                    : launch_decode<KK, KV, DD, Q, false>(tk, tv, a, grid, s);
   NK_CASE(64, 1) NK_CASE(64, 2) NK_CASE(64, 4)
   NK_CASE(128, 1) NK_CASE(128, 2) NK_CASE(128, 4)
   NK_CASE(256, 1) NK_CASE(256, 2)

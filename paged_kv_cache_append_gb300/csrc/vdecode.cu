@@ -173,7 +173,7 @@ __device__ __forceinline__ void v_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-template <int KK, int KV, int D>
+template <int KK, int KV, int D, bool SHARED>
 __global__ void __launch_bounds__(448, 1)
     vdecode_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, DecodeArgs a) {
   using Cfg = VCfg<KK, KV, D>;
@@ -236,16 +236,17 @@ __global__ void __launch_bounds__(448, 1)
   // The fused call reads tables, row map, frontiers and earlier pages before
   // the programmatic dependency wait (see decode.cuh); q, k, v and every
   // global write come after it.
-  const bool early = a.k_new != nullptr;
-  if (!early && a.shared == nullptr) griddep_wait();  // (see decode.cuh)
+  const bool early = !SHARED && a.k_new != nullptr;
+  if (!early && !SHARED) griddep_wait();  // (see decode.cuh)
   griddep_launch_dependents();
   if (tid < a.B) {
     const int F = a.frontiers[tid], row = a.table_rows[tid];
     const bool ok = F >= 0 && F <= a.L * 64 && row >= 0 && row < a.C && (a.k_new == nullptr || F >= a.T);
     if (!ok && blockIdx.x == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
-    const int before = pages_before(a, F, row);
+    int before = 0;
+    if constexpr (SHARED) before = pages_before(a, F, row);
     s_F[tid] = ok ? F - 64 * before : 0;
-    s_row[tid] = ok ? row * a.L + before : 0;  // the row's first table entry
+    s_row[tid] = ok ? (SHARED ? row * a.L + before : row) : 0;
   }
   if (warp == 0) {
     tc::alloc(tslot, 512);
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(448, 1)
   const int nt = (n + PPT - 1) / PPT;                  // key tiles
   const int app_lo = early ? (F - a.T) >> 6 : 0x7fffffff;
   const int R_real = a.T * a.G;
-  const int32_t* trow = a.tables + (b >= 0 ? s_row[b] : 0);
+  const int32_t* trow = a.tables + static_cast<int64_t>(b >= 0 ? s_row[b] : 0) * (SHARED ? 1 : a.L);
 
   if (b < 0) {
     // no work: only the TMEM allocation is released below
@@ -695,7 +696,7 @@ __global__ void __launch_bounds__(448, 1)
     const int ot = orow / a.G, og = orow % a.G;
     if (ok) {
       // the split's result: final out / lse (one split) or the partial (m, l, acc)
-      const bool final_out = nsplit == 1 && a.shared == nullptr;
+      const bool final_out = !SHARED && nsplit == 1;
       const int64_t part = (static_cast<int64_t>(b) * a.H + h) * a.target + split;
       const float inv = lt > 0.f ? 1.f / lt : 0.f;
 #pragma unroll 1
@@ -742,7 +743,7 @@ __global__ void __launch_bounds__(448, 1)
   __syncthreads();
   tc::fence_after();
   if (warp == 0) tc::dealloc(tmem, 512);
-  if (a.shared != nullptr) griddep_wait();
+  if constexpr (SHARED) griddep_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -917,7 +918,7 @@ __device__ __forceinline__ VSeg vt_seg(int sg, const int* s_F, int B, int chunk)
   return r;
 }
 
-template <int KK, int KV, int D>
+template <int KK, int KV, int D, bool SHARED>
 __global__ void __launch_bounds__(448, 1)
     vtdecode_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, DecodeArgs a) {
   using Cfg = VTCfg<KK, KV, D>;
@@ -995,16 +996,17 @@ __global__ void __launch_bounds__(448, 1)
     prefetch_tmap(&tmk);
     prefetch_tmap(&tmv);
   }
-  const bool early = a.k_new != nullptr;
-  if (!early && a.shared == nullptr) griddep_wait();  // (see decode.cuh)
+  const bool early = !SHARED && a.k_new != nullptr;
+  if (!early && !SHARED) griddep_wait();  // (see decode.cuh)
   griddep_launch_dependents();
   if (tid < a.B) {
     const int F = a.frontiers[tid], row = a.table_rows[tid];
     const bool ok = F >= 0 && F <= a.L * 64 && row >= 0 && row < a.C && (a.k_new == nullptr || F >= a.T);
     if (!ok && blockIdx.x == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
-    const int before = pages_before(a, F, row);
+    int before = 0;
+    if constexpr (SHARED) before = pages_before(a, F, row);
     s_F[tid] = ok ? F - 64 * before : 0;
-    s_row[tid] = ok ? row * a.L + before : 0;  // the row's first table entry
+    s_row[tid] = ok ? (SHARED ? row * a.L + before : row) : 0;
   }
   if (warp == 0) {
     tc::alloc(tslot, 512);
@@ -1028,7 +1030,7 @@ __global__ void __launch_bounds__(448, 1)
   const int s_lo = static_cast<int>(static_cast<int64_t>(blockIdx.x) * nsegs / gridDim.x);
   const int s_hi = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * nsegs / gridDim.x);
   const int R_real = a.T * a.G;
-  auto trow_of = [&](int bb) { return a.tables + s_row[bb]; };
+  auto trow_of = [&](int bb) { return a.tables + static_cast<int64_t>(s_row[bb]) * (SHARED ? 1 : a.L); };
 
   if (s_hi <= s_lo) {
     // no work: only the TMEM allocation is released below
@@ -1507,7 +1509,7 @@ __global__ void __launch_bounds__(448, 1)
       {
         const float lt = (sL[lane] + sL[32 + lane]) + (sL[64 + lane] + sL[96 + lane]);  // row `lane`
         const int b = g0.b;
-        const bool final_out = g0.ns == 1 && a.shared == nullptr;
+        const bool final_out = !SHARED && g0.ns == 1;
         const int64_t part = (static_cast<int64_t>(b) * a.H + h) * a.target + g0.k;
         const float unlift = KV == KIND_FP8 ? pow2i(-k_run) : 1.f;  // O^T carries 2^k_run
         const float inv_self = lt > 0.f ? unlift / lt : 0.f;
@@ -1563,13 +1565,13 @@ __global__ void __launch_bounds__(448, 1)
   __syncthreads();
   tc::fence_after();
   if (warp == 0) tc::dealloc(tmem, 512);
-  if (a.shared != nullptr) griddep_wait();
+  if constexpr (SHARED) griddep_wait();
 }
 
-template <int KK, int KV, int D>
+template <int KK, int KV, int D, bool SHARED>
 static cudaError_t launch_v(const nk_pool* p, int layer, const DecodeArgs& a, dim3 grid, cudaStream_t s) {
   using Cfg = VCfg<KK, KV, D>;
-  auto k = vdecode_kernel<KK, KV, D>;
+  auto k = vdecode_kernel<KK, KV, D, SHARED>;
   static bool attr = false;
   if (!attr) {
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
@@ -1577,14 +1579,14 @@ static cudaError_t launch_v(const nk_pool* p, int layer, const DecodeArgs& a, di
     attr = true;
   }
   cudaError_t e = launch_pdl(k, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
-  if (e != cudaSuccess || a.shared != nullptr) return e;
+  if (e != cudaSuccess || SHARED) return e;
   return launch_pdl(merge_kernel<D, 4>, dim3(a.B, a.H, D / 32), dim3(256), 0, s, a);
 }
 
-template <int KK, int KV, int D>
+template <int KK, int KV, int D, bool SHARED>
 static cudaError_t launch_vt(const nk_pool* p, int layer, const DecodeArgs& a, dim3 grid, cudaStream_t s) {
   using Cfg = VTCfg<KK, KV, D>;
-  auto k = vtdecode_kernel<KK, KV, D>;
+  auto k = vtdecode_kernel<KK, KV, D, SHARED>;
   static bool attr = false;
   if (!attr) {
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
@@ -1592,19 +1594,24 @@ static cudaError_t launch_vt(const nk_pool* p, int layer, const DecodeArgs& a, d
     attr = true;
   }
   cudaError_t e = launch_pdl(k, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
-  if (e != cudaSuccess || a.shared != nullptr) return e;
+  if (e != cudaSuccess || SHARED) return e;
   return launch_pdl(merge_kernel<D, 4>, dim3(a.B, a.H, D / 32), dim3(256), 0, s, a);
+}
+
+template <int KK, int KV, bool SHARED>
+static cudaError_t vdispatch_d(const nk_pool* p, int layer, const DecodeArgs& a, dim3 grid, cudaStream_t s) {
+  switch (p->desc.head_dim) {
+    case 64: return launch_vt<KK, KV, 64, SHARED>(p, layer, a, grid, s);
+    case 128: return launch_vt<KK, KV, 128, SHARED>(p, layer, a, grid, s);
+    case 256: return launch_v<KK, KV, 256, SHARED>(p, layer, a, grid, s);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 template <int KK, int KV>
 static cudaError_t vdispatch(const nk_pool* p, int layer, const DecodeArgs& a, int nqt, dim3 grid, cudaStream_t s) {
   if (nqt != 4) return cudaErrorInvalidValue;
-  switch (p->desc.head_dim) {
-    case 64: return launch_vt<KK, KV, 64>(p, layer, a, grid, s);
-    case 128: return launch_vt<KK, KV, 128>(p, layer, a, grid, s);
-    case 256: return launch_v<KK, KV, 256>(p, layer, a, grid, s);
-    default: return cudaErrorInvalidValue;
-  }
+  return a.shared ? vdispatch_d<KK, KV, true>(p, layer, a, grid, s) : vdispatch_d<KK, KV, false>(p, layer, a, grid, s);
 }
 
 DecodeFn vdecode_for(int profile, int D, int nqt) {
