@@ -26,11 +26,12 @@
 // every page whole.
 //
 // The softmax reads each score once on most pages: it computes the weights
-// against the reference maximum that it has, with the page's maximum on the
-// side, and only where that passes the reference by more than 2^8 does it read
-// the scores again (they are intact until P is stored).  32 columns (16 where
+// against the reference maximum that it has, and only where their sum passes
+// 2^8 (so that none is above it) does it take the page's maximum and compute
+// them again (the scores are intact until P is stored).  32 columns (16 where
 // registers are short) are worked on while the next ones load, and two scores
-// share an instruction where fp32 has packed forms.
+// share an instruction where fp32 has packed forms.  Each of the two steps
+// stands in the code once: a second copy of them on the rare path cost 6%.
 //
 // Warps: 4 softmax and output warps a pipeline, then the TMA producer, two MMA
 // issuers and the converters (quantized pools).  All waits are bounded.
@@ -627,22 +628,21 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
           const float2 s2 = *reinterpret_cast<const float2*>(vsc + 2 * lane);
           knew = v_lift(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(s2.x, s2.y))), k_run);
         }
-        float mnew = m_used;
-        if (__any_sync(0xffffffffu, m_used == -INFINITY)) {  // the first page: its maximum first
+        // the page's largest score, of the rows that ask for it
+        auto top = [&] {
           float mx = -INFINITY;
           each([&](int, const F2 (&z)[CH / 2]) { mx = max_of(mx, z); });
-          if (m_used == -INFINITY) mnew = mx == -INFINITY ? -INFINITY : mx * zmul;
-        }
+          return mx == -INFINITY ? -INFINITY : mx * zmul;
+        };
+        float mnew = m_used;
         uint32_t pk[PK];
         float sum = 0.f;
-        // p = 2^(z rs - mnew + knew); returns the page's largest score
+        // p = 2^(z rs - mnew + knew)
         auto weights = [&]() {
           const float mu = (mnew == -INFINITY ? 0.f : mnew) - static_cast<float>(knew);
           const F2 rs2 = pack2(rs, rs), nmu2 = pack2(-mu, -mu);
-          float mx = -INFINITY;
           F2 s0 = 0ull, s1 = 0ull;
           each([&](int c0, const F2 (&z)[CH / 2]) {
-            mx = max_of(mx, z);
 #pragma unroll
             for (int c = 0; c < CH / 2; c += 2) {
               float p0, p1, p2, p3;
@@ -674,13 +674,19 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
           unpack2(s0, a0, a1);
           unpack2(s1, b0, b1);
           sum = (a0 + a1) + (b0 + b1);
-          return mx;
         };
-        const float top = weights() * zmul;
-        const bool over = top > mnew + kLazyThr;
-        if (__any_sync(0xffffffffu, over)) {
-          if (over) mnew = top;
+        // the first page takes its maximum first, a page with too large a weight afterwards, and then again
+        bool ask = m_used == -INFINITY;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+          if (__any_sync(0xffffffffu, ask)) {
+            const float mx = top();
+            if (ask) mnew = mx;
+          } else if (pass > 0) {
+            break;
+          }
           weights();
+          ask = sum > ex2(kLazyThr + static_cast<float>(knew));
         }
         const bool resc = mnew != m_used || knew != k_run;
         const float factor = m_used == -INFINITY ? 0.f
