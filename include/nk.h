@@ -375,7 +375,7 @@ typedef struct {
  *   of them may be NULL with its output.  positions: device int32 [N].
  *   q_out, k_out: rows written.  An output may be its own input (same ptr and
  *   strides); it must not overlap any other operand, and the rows of an output
- *   must not overlap one another.
+ *   must not overlap one another (NK_ERR_SHAPE).
  * A token whose position is outside [0, rope->positions) is skipped: its
  * output rows keep what they hold, and NK_STATUS_FRONTIER is recorded.
  * Runs on the current device.  Errors: NK_ERR_INVALID_ARG, NK_ERR_SHAPE,

@@ -40,6 +40,17 @@ static int check_rows(const nk_rows* r, const char* name) {
   return NK_OK;
 }
 
+// No element is written twice: the rows of a token lie behind one another and
+// the tokens do, or the other way round.
+static bool rows_apart(const nk_rows* r, int64_t tokens, int64_t heads, int D) {
+  using Wide = __int128;
+  const Wide t = r->token_stride < 0 ? -Wide(r->token_stride) : Wide(r->token_stride);
+  const Wide h = r->head_stride < 0 ? -Wide(r->head_stride) : Wide(r->head_stride);
+  if (tokens == 1) return heads == 1 || h >= D;
+  if (heads == 1) return t >= D;
+  return (h >= D && t >= (heads - 1) * h + D) || (t >= D && h >= (tokens - 1) * t + D);
+}
+
 static RowsIn rows_in(const nk_rows* r) {
   return r ? RowsIn{static_cast<const __nv_bfloat16*>(r->ptr), r->token_stride, r->head_stride}
            : RowsIn{nullptr, 0, 0};
@@ -366,6 +377,8 @@ extern "C" int nk_qk_norm_rope(const nk_rope* rope, int32_t head_dim, const nk_r
   const char* names[4] = {"q", "k", "q_out", "k_out"};
   for (int i = 0; i < 4; ++i)
     if (rows[i] && (rc = check_rows(rows[i], names[i]))) return rc;
+  if ((q && !rows_apart(q_out, N, Hq, head_dim)) || (k && !rows_apart(k_out, N, H, head_dim)))
+    return fail(NK_ERR_SHAPE, "output rows overlap");
   const int heads = (q ? Hq : 0) + (k ? H : 0);
   if (static_cast<int64_t>(N) * heads > (int64_t(1) << 30)) return fail(NK_ERR_SHAPE, "too many head rows in one call");
   a.in[0] = rows_in(q);

@@ -29,7 +29,7 @@ struct PrefixParts {
 };
 
 __device__ __forceinline__ bool takes_part(int pages, int least, int F, int row, int T, int L, int C) {
-  return pages >= least && pages <= L && F <= L * 64 && F - T >= 64 * pages && row >= 0 && row < C;
+  return pages >= least && pages <= L && F >= T && F <= L * 64 && F - T >= 64 * pages && row >= 0 && row < C;
 }
 
 // The table row whose pages the prefix pass reads: the first one that takes

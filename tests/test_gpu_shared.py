@@ -262,6 +262,19 @@ def test_bad_rows_and_pages_do_not_fault():
     check(out[[0, 2]], lse[[0, 2]], [r[[0, 2]] for r in ref])
 
 
+def test_the_least_frontier_takes_no_part():
+    """frontiers - T must not wrap around: a row of -2^31 valid tokens is a bad row, not one behind the prefix."""
+    b = Batch("bf16", 64, 1, 4, 2, 3, [200, 230, 260])
+    ref = b.reference()
+    b.d["F"] = dev(np.array([200, -2 ** 31, 260], np.int32))
+    s = torch.cuda.current_stream().cuda_stream
+    nk.nk_status_read(True, s)
+    out, lse = b.run(3)
+    assert nk.nk_status_read(True, s) == nk.STATUS_FRONTIER
+    check(out[[0, 2]], lse[[0, 2]], [r[[0, 2]] for r in ref])
+    assert torch.all(out[1] == 0) and torch.all(torch.isneginf(lse[1]))
+
+
 @pytest.mark.parametrize("profile,D", [("bf16", 128), ("bf16", 256), ("fp8_row", 64), ("fp8_row", 256), ("k8v4", 128)])
 @pytest.mark.parametrize("plane", [0, 1])
 @pytest.mark.parametrize("page,token", [(1, 5), (4, 63), (6, 3)])

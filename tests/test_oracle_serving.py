@@ -132,7 +132,8 @@ def _norm_rope(lib, rope=None, D=64, q=(64, 256, 64), Hq=4, k=(64, 128, 64), H=2
     (dict(rope=_rope(weight_offset=float("inf"))), -1), (dict(q=None), -1), (dict(qo=None), -1), (dict(pos=None), -1),
     (dict(q=None, qo=None, k=None, ko=None), -1), (dict(N=0), -2), (dict(Hq=0), -2), (dict(H=-1), -2),
     (dict(q=(72, 256, 64)), -5), (dict(q=(64, 260, 64)), -5), (dict(ko=(64, 128, 60)), -5), (dict(q=(None, 8, 8)), -1),
-    (dict(N=1 << 30, Hq=4), -2)])
+    (dict(N=1 << 30, Hq=4), -2), (dict(qo=(64, 0, 64)), -2), (dict(qo=(64, 256, 0)), -2), (dict(qo=(64, 192, 64)), -2),
+    (dict(ko=(64, 64, 128)), -2), (dict(ko=(64, 56, 1 << 40)), -2), (dict(ko=(64, -120, 64)), -2)])
 def test_norm_rope_refusals(lib, kw, code):
     assert _norm_rope(lib, **kw) == code
     assert nk.load().nk_last_error()
