@@ -277,11 +277,9 @@ int nk_shared_decode_workspace_bytes(const nk_pool* pool, int32_t B, int32_t T, 
  *   affected results are then undefined).  Rows that do not take part are
  *   attended in full by themselves, and so are all rows for *shared_pages <= 0
  *   or > L.
- *   share_from: the prefix is attended once where that saves at least this
- *   many page bytes, (B - c) * *shared_pages * H * bytes of one page and head,
- *   c = 3 (2 for T * Hq / H > 16) being what attending it once costs, in rows;
- *   each row attends it by itself otherwise.  0: always;  negative: the
- *   library's measured choice, 64 MiB (32 MiB for T * Hq / H > 16).
+ *   share_from: the prefix is attended once from this many shared pages on (0
+ *   as 1: always); with fewer, each row attends it by itself.  Negative: the
+ *   library's measured choice by sizes and profile.
  *   workspace: nk_shared_decode_workspace_bytes bytes, no initialisation
  *   needed; two calls that share a workspace must not overlap.
  * A NaN among the keys or values that a row sees makes its outputs NaN (an

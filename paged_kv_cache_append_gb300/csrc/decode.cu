@@ -42,6 +42,7 @@ int make_plan(const nk_pool* p, int B, int T, int Hq, DecodePlan* pl) {
     pl->fn = vfn;
     per_sm = 1;
   }
+  pl->per_sm = per_sm;
   pl->target = p->num_sms * per_sm / H;
   if (pl->target < 1) pl->target = 1;
   // A budget below B (many KV heads) leaves every row one split, which still

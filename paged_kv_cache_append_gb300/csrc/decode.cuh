@@ -85,6 +85,7 @@ struct DecodeArgs {
   // decode of FP8-row pages at head_dim 256 0.9%.
   const int32_t* shared = nullptr;
   int shared_least = 1;
+  ShareShape shape;
 };
 
 // Pages of row (F, row) that the prefix pass covers.
@@ -220,10 +221,20 @@ __host__ __device__ __forceinline__ int seg_chunk(int total, int nseg) {
 // total / nseg while that leaves pieces of at least 64 pages; shorter pieces
 // would cost more in per-piece hand-offs than they win in balance, so the
 // plan falls back to one wave-filling split per CTA.
-__device__ __forceinline__ int piece_chunk(const int* s_F, const DecodeArgs& a, int total, int maxp) {
-  const int c = seg_chunk(total, a.nseg);
+__device__ __forceinline__ int piece_chunk(const int* s_F, const DecodeArgs& a, int total, int maxp, int nseg, int ctas) {
+  const int c = seg_chunk(total, nseg);
   if (c >= 64) return max(c, (maxp + kMaxSplits - 1) / kMaxSplits);
-  return wave_chunk(s_F, a.B, total, maxp, min(a.ctas, a.target));
+  return wave_chunk(s_F, a.B, total, maxp, min(ctas, a.target));
+}
+
+__device__ __forceinline__ int piece_chunk(const int* s_F, const DecodeArgs& a, int total, int maxp) {
+  return piece_chunk(s_F, a, total, maxp, a.nseg, a.ctas);
+}
+
+// The chunk of the shared-prefix attention's own pages, for `ctas` CTAs a head.
+__device__ __forceinline__ int own_chunk(const int* s_F, const DecodeArgs& a, int total, int maxp, int ctas) {
+  return a.nseg > 0 ? piece_chunk(s_F, a, total, maxp, min(4 * ctas, a.nseg), ctas)
+                    : wave_chunk(s_F, a.B, total, maxp, min(ctas, a.target));
 }
 
 __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
@@ -271,7 +282,14 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
   const int r = lane >> 2, c = lane & 3;
   // consumers: keys [16 pair, +16), dims [half DH, +DH)
   const int pair = NH == 2 ? warp >> 1 : warp, half = NH == 2 ? warp & 1 : 0;
-  const int h = blockIdx.y;
+  // the CTAs of the shared-prefix form that have work come first in the launch
+  const int h = SHARED ? blockIdx.x : blockIdx.y, cta = SHARED ? blockIdx.y : blockIdx.x;
+  OwnRow own{0, 0, 0};
+  int ctas = 0;
+  if constexpr (SHARED) {
+    own = own_row(a.shape, a.shared, a.shared_least, a.frontiers, a.table_rows, a.B, a.T, a.L, a.C, lane, ctas);
+    if (cta >= ctas) return;
+  }
 
   if (tid == 0) {
     for (int s = 0; s < NSTAGE; ++s) {
@@ -294,21 +312,19 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
   // any global write.  The plain decode waits here (a separate append may have
   // just written its pages).
   // In the shared-prefix attention the kernel before is the prefix pass, which
-  // waited for everything before itself and shares nothing with this one: it
-  // is waited for at the end alone, for the merge behind both.
+  // waited for everything before itself and shares nothing with this one: one
+  // CTA waits for it, at its end, for the merge behind both.
   const bool early = !SHARED && a.k_new != nullptr;
   if (!early && !SHARED) griddep_wait();
   griddep_launch_dependents();
 
   // ---- per-row lengths, loaded once in parallel ------------------------------
   if (tid < a.B) {
-    const int F = a.frontiers[tid], row = a.table_rows[tid];
+    const int F = SHARED ? own.F : a.frontiers[tid], row = SHARED ? own.row : a.table_rows[tid];
     const bool ok = F >= 0 && F <= a.L * 64 && row >= 0 && row < a.C && (a.k_new == nullptr || F >= a.T);
-    if (!ok && blockIdx.x == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
-    int before = 0;
-    if constexpr (SHARED) before = pages_before(a, F, row);
-    s_F[tid] = ok ? F - 64 * before : 0;
-    s_row[tid] = ok ? (SHARED ? row * a.L + before : row) : 0;
+    if (!ok && cta == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
+    s_F[tid] = ok ? F - 64 * own.before : 0;
+    s_row[tid] = ok ? (SHARED ? row * a.L + own.before : row) : 0;
   }
   __syncthreads();
 
@@ -319,16 +335,16 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
     total += np;
     maxp = max(maxp, np);
   }
-  const int chunk = wave_chunk(s_F, a.B, total, maxp, a.target);
+  const int chunk = SHARED ? own_chunk(s_F, a, total, maxp, ctas) : wave_chunk(s_F, a.B, total, maxp, a.target);
   int b = -1, split = 0, nsplit = 0, npages = 0;
   {
     int acc = 0;
     for (int bb = 0; bb < a.B; ++bb) {
       const int np = (s_F[bb] + 63) >> 6;
       const int ns = max(1, (np + chunk - 1) / chunk);  // a row without keys still writes out / lse
-      if (static_cast<int>(blockIdx.x) < acc + ns) {
+      if (cta < acc + ns) {
         b = bb;
-        split = blockIdx.x - acc;
+        split = cta - acc;
         nsplit = ns;
         npages = np;
         break;
@@ -1020,6 +1036,7 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
     if (tid == 0)
       for (int k = i; k < min(n, i + NSTAGE); ++k)
         mbar_wait_bounded(&full[k % NSTAGE], (k / NSTAGE) & 1, a.status, 100000000ull);
+    if (SHARED && cta == 0 && h == 0) griddep_wait();
     return;
   }
   if (tid < R) {
@@ -1100,7 +1117,7 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
       a.ws_ml[part * R + tid] = make_float2(row_M[tid], row_L[tid]);
     }
   }
-  if constexpr (SHARED) griddep_wait();
+  if (SHARED && cta == 0 && h == 0) griddep_wait();
 }
 
 // ---- log-sum-exp merge of the splits (separate launch) ----------------------------
@@ -1218,7 +1235,7 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const De
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
-  cudaError_t e = launch_pdl(k, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, tk, tv, a);
+  cudaError_t e = launch_pdl(k, SHARED ? dim3(grid.y, grid.x) : grid, dim3(Cfg::THREADS), Cfg::SMEM, s, tk, tv, a);
   if (e != cudaSuccess || SHARED) return e;
   return launch_pdl(merge_kernel<D, NQT>, dim3(a.B, a.H, D / 32), dim3(256), 0, s, a);
 }
@@ -1295,6 +1312,7 @@ DecodeFn vdecode_for(int profile, int D, int nqt);
 // Split plan of one decode call (decode.cu).
 struct DecodePlan {
   int nqt, R, target, ring_bytes;
+  int per_sm = 1;
   int ctas = 0;  // CTAs per KV head (grid x)
   int nseg = 0;  // > 0: pieces per head, several per CTA
   size_t ws_ml_bytes, ws_bytes;

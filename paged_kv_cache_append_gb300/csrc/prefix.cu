@@ -265,9 +265,11 @@ __global__ void __launch_bounds__((PrefixCfg<KK, KV, D>::THREADS), 1)
 
   // ---- this CTA's pages [p_lo, p_lo + n) -----------------------------------------
   const int pages = *a.sh.pages;
-  const int row = prefix_row(a.sh, a.table_rows, pages, a.L, a.C);
+  int own;
+  const int row = prefix_row(a.sh, a.table_rows, pages, a.L, a.C, own);
   const int all = row < 0 ? 0 : pages;
-  const int per = (all + a.nsplit - 1) / a.nsplit;
+  const int nsplit = share_split(a.sh.shape, all, own).nsplit;
+  const int per = (all + nsplit - 1) / nsplit;
   const int p_lo = min(split * per, all);
   const int n = min(p_lo + per, all) - p_lo;
   if (n == 0) return;  // the merge reads no partial of this range
@@ -814,8 +816,24 @@ static cudaError_t launch_prefix(const nk_pool* p, int layer, const PrefixArgs& 
     if (e != cudaSuccess) return e;
     attr = p->device;
   }
-  return launch_pdl(k, dim3(a.nsplit, a.H * (Cfg::NP == 1 ? a.tiles : 1)), dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0],
-                    p->tmap[layer * 2 + 1], a);
+  // In clusters of two, which lie on one TPC (two SMs), so that the SMs left to
+  // the own pages (share_split) are whole TPCs: where the two kernels shared
+  // TPCs, the own-pages CTAs took up to 160 us instead of 99.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.nsplit, a.H * (Cfg::NP == 1 ? a.tiles : 1));
+  cfg.blockDim = dim3(Cfg::THREADS);
+  cfg.dynamicSmemBytes = Cfg::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.y = cfg.gridDim.y % 2 ? 1 : 2;
+  at[1].val.clusterDim.x = cfg.gridDim.y % 2 && cfg.gridDim.x % 2 == 0 ? 2 : 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
 }
 
 template <int KK, int KV>

@@ -24,17 +24,6 @@ cudaError_t prefix_pass(const nk_pool* p, int layer, const void* q, const int32_
 
 constexpr int kMaxPrefixSplits = 128;
 
-// When the prefix gets a pass of its own.  The pass costs about as much as c
-// rows' own attention to the prefix (c = 1.8 to 2.9 measured over the profiles
-// with the warp-level decode, 1.5 with the tensor-core one) and, for its
-// launch, its partials and their merge, a fixed 6 to 10 us.  So it is taken
-// from (B - c) * pages * heads * page bytes >= kShareFrom on.  Crossings seen
-// with B = 8: 140 pages for BF16 at 2 heads of 256 (92 MB), 310 for FP8-row
-// there (102 MB), 230 for K8V4 at 4 heads of 128 (59 MB), 115 for its 4-token
-// verify (36 MB).
-constexpr int64_t kShareFrom = 64 << 20, kShareFromTensor = 32 << 20;
-constexpr int kShareRows = 3, kShareRowsTensor = 2;
-
 struct SharedPlan {
   DecodePlan own;  // the rows' own pages
   int tiles, nsplit;
@@ -54,6 +43,53 @@ static int make_shared_plan(const nk_pool* p, int B, int T, int Hq, SharedPlan* 
   pl->sh_bytes = pl->sh_ml_bytes + parts * D * sizeof(float);
   pl->ws_bytes = pl->sh_bytes + pl->own.ws_bytes;
   return NK_OK;
+}
+
+// Measured times of one page of a KV head on one SM, in us: a row's own decode
+// of it, from L2 and (`cold`) from HBM, and the prefix pass's for a tile of rows.
+struct PageCosts {
+  float own, own_cold, prefix;
+  bool tensor;  // the tensor-core decode
+};
+
+static PageCosts page_costs(const nk_pool* p, int B, int R, int64_t page_bytes) {
+  const int D = p->desc.head_dim;
+  const float d = D == 64 ? 0.75f : D == 128 ? 1.f : 2.2f;
+  PageCosts c;
+  c.tensor = R > 16 && p->desc.profile != NK_BF16 && p->desc.profile != NK_INT8_G64;
+  c.own = d * (R <= 8 ? 0.3f : R <= 16 ? 0.56f : c.tensor ? 0.68f : 0.85f);
+  c.own_cold = fmaxf(D / 128.f * (R <= 8 ? 0.28f : R <= 16 ? 0.56f : c.tensor ? 0.8f : 1.35f), page_bytes / 40e3f);
+  c.prefix = D == 256 ? 1.25f * ((B * R + 127) / 128) : B * R > 128 ? 1.3f : D == 64 ? 1.25f : 0.95f;
+  if (p->desc.profile == NK_INT8_G64) c.prefix += 0.6f;  // two key tiles a page
+  return c;
+}
+
+// When the prefix gets a pass of its own: where its pages cost the pass less than
+// the rows by as much as its launch, its partials and their merge cost, about
+// 4.5 us of the chip, or 1 over 16 query rows, where the plain decode has more of
+// a start itself.  Crossings seen, in shared pages: 8 rows of FP8-row, BF16 at 2
+// heads of 256: 90, 85; 4 rows of FP8-row there 120; 8 rows of K8V4, BF16 at 4
+// heads of 128: 130, 150, and less than 16 for their 4-token verify; 8 rows at 8
+// heads of 64: 195; 2 rows, and 3 of 2 query heads a KV head: never.
+static int64_t share_least(const nk_pool* p, int B, int R, const PageCosts& c) {
+  const float gain = p->desc.num_kv_heads * (B * c.own - c.prefix);
+  return gain <= 0.f ? INT32_MAX : static_cast<int64_t>(p->num_sms * (R > 16 ? 1.f : 4.5f) / gain) + 1;
+}
+
+// (share_split; the own-pages kernel alone takes 4 to 13 us)
+static ShareShape share_shape(const nk_pool* p, const SharedPlan& pl, int B, int R, const PageCosts& c) {
+  const int H = p->desc.num_kv_heads, D = p->desc.head_dim;
+  ShareShape g;
+  g.sms = p->num_sms;
+  g.range_ctas = H * (D == 256 ? pl.tiles : 1);
+  g.nsplit = pl.nsplit;
+  g.ctas = pl.own.ctas;
+  g.least = (B * H + pl.own.per_sm - 1) / pl.own.per_sm;
+  g.ranges_per_sm = 1.f / g.range_ctas;
+  g.ctas_per_sm = static_cast<float>(pl.own.per_sm) / H;
+  g.own_page = H * c.own_cold / 1.25f;
+  g.own_start = c.tensor ? 10.f : (R <= 8 ? 4.f : R <= 16 ? 6.f : 8.f) * D / 128;
+  return g;
 }
 
 struct SharedMergeArgs {
@@ -95,10 +131,11 @@ __global__ void __launch_bounds__(kMergeRows * 8 * SUB) shared_merge_kernel(cons
     maxp = max(maxp, np);
     if (s_row[bb] >= 0) first = s_row[bb];
   }
-  const int chunk = a.nseg > 0 ? piece_chunk(s_F, a, total, maxp) : wave_chunk(s_F, a.B, total, maxp, a.target);
+  const ShareSplit split = share_split(a.shape, first >= 0 ? pages : 0, total);
+  const int chunk = own_chunk(s_F, a, total, maxp, split.ctas);
   const int own = max(1, (((s_F[b] + 63) >> 6) + chunk - 1) / chunk);
   const bool part = s_row[b] >= 0;
-  const int per = part ? (pages + m.prefix.nsplit - 1) / m.prefix.nsplit : 1;
+  const int per = part ? (pages + split.nsplit - 1) / split.nsplit : 1;
   const int pre = part ? (pages + per - 1) / per : 0;
   if (h == 0 && blockIdx.z == 0) {  // the row's leading table entries are those the prefix pass read
     if (part && s_row[b] != first) {
@@ -259,14 +296,11 @@ extern "C" int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const
     return fail(NK_ERR_INVALID_ARG, "the pool belongs to device " + std::to_string(pool->device) +
                                         ", the current device is " + std::to_string(dev));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // the least number of shared pages worth the prefix pass
   int64_t page_bytes = 0;
   for (int i = 0; i < pool->n_planes; ++i) page_bytes += int64_t(NK_PAGE_TOKENS) * pool->plane[i].row_bytes;
-  const bool tensor = T * (Hq / pool->desc.num_kv_heads) > 16;
-  share_from = std::min(share_from, int64_t(1) << 60);  // (above every pool's)
-  if (share_from < 0) share_from = tensor ? kShareFromTensor : kShareFrom;
-  const int64_t saved = (B - (tensor ? kShareRowsTensor : kShareRows)) * page_bytes * pool->desc.num_kv_heads;  // a page
-  const int64_t least = share_from == 0 ? 1 : saved <= 0 ? INT32_MAX : (share_from + saved - 1) / saved;
+  const int R = T * (Hq / pool->desc.num_kv_heads);
+  const PageCosts costs = page_costs(pool, B, R, page_bytes);
+  const int64_t least = share_from < 0 ? share_least(pool, B, R, costs) : std::max<int64_t>(share_from, 1);
   if (least > pool->L)  // no row has that many pages
     return run_decode(q, Hq, pool, layer, block_tables, table_rows, frontiers, nullptr, nullptr, B, T, softmax_scale,
                       out, lse, workspace, workspace_bytes, s, "nk_paged_shared_decode_attention");
@@ -277,6 +311,7 @@ extern "C" int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const
   sh.B = B;
   sh.T = T;
   sh.least = static_cast<int>(least);
+  sh.shape = share_shape(pool, pl, B, R, costs);
   const PrefixParts parts{pl.tiles, pl.nsplit, reinterpret_cast<float2*>(ws),
                           reinterpret_cast<float*>(ws + pl.sh_ml_bytes)};
   e = prefix_pass(pool, layer, q, block_tables, table_rows, Hq, softmax_scale * kLog2e, parts, sh, s);
@@ -310,6 +345,7 @@ extern "C" int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const
   a.head_major = pool->desc.order == NK_HEAD_MAJOR;
   a.shared = shared_pages;
   a.shared_least = sh.least;
+  a.shape = sh.shape;
   e = pl.own.fn(pool, layer, a, pl.own.nqt, dim3(pl.own.ctas, a.H), s);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   m.prefix = parts;

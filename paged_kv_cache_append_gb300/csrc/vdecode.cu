@@ -205,7 +205,13 @@ __global__ void __launch_bounds__(448, 1)
   int* s_row = s_F + 8;                             // [8]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.y;
+  const int h = SHARED ? blockIdx.x : blockIdx.y, cta = SHARED ? blockIdx.y : blockIdx.x;  // (see decode.cuh)
+  OwnRow own{0, 0, 0};
+  int ctas = gridDim.x;
+  if constexpr (SHARED) {
+    own = own_row(a.shape, a.shared, a.shared_least, a.frontiers, a.table_rows, a.B, a.T, a.L, a.C, threadIdx.x & 31, ctas);
+    if (cta >= ctas) return;
+  }
   if (tid == 0) {
     for (int i = 0; i < NR; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -240,13 +246,11 @@ __global__ void __launch_bounds__(448, 1)
   if (!early && !SHARED) griddep_wait();  // (see decode.cuh)
   griddep_launch_dependents();
   if (tid < a.B) {
-    const int F = a.frontiers[tid], row = a.table_rows[tid];
+    const int F = SHARED ? own.F : a.frontiers[tid], row = SHARED ? own.row : a.table_rows[tid];
     const bool ok = F >= 0 && F <= a.L * 64 && row >= 0 && row < a.C && (a.k_new == nullptr || F >= a.T);
-    if (!ok && blockIdx.x == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
-    int before = 0;
-    if constexpr (SHARED) before = pages_before(a, F, row);
-    s_F[tid] = ok ? F - 64 * before : 0;
-    s_row[tid] = ok ? (SHARED ? row * a.L + before : row) : 0;
+    if (!ok && cta == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
+    s_F[tid] = ok ? F - 64 * own.before : 0;
+    s_row[tid] = ok ? (SHARED ? row * a.L + own.before : row) : 0;
   }
   if (warp == 0) {
     tc::alloc(tslot, 512);
@@ -264,16 +268,16 @@ __global__ void __launch_bounds__(448, 1)
     total += np;
     maxp = max(maxp, np);
   }
-  const int chunk = wave_chunk(s_F, a.B, total, maxp, a.target);
+  const int chunk = SHARED ? own_chunk(s_F, a, total, maxp, ctas) : wave_chunk(s_F, a.B, total, maxp, a.target);
   int b = -1, split = 0, nsplit = 0, npages = 0;
   {
     int acc = 0;
     for (int bb = 0; bb < a.B; ++bb) {
       const int np = (s_F[bb] + 63) >> 6;
       const int ns = max(1, (np + chunk - 1) / chunk);
-      if (static_cast<int>(blockIdx.x) < acc + ns) {
+      if (cta < acc + ns) {
         b = bb;
-        split = blockIdx.x - acc;
+        split = cta - acc;
         nsplit = ns;
         npages = np;
         break;
@@ -743,7 +747,7 @@ __global__ void __launch_bounds__(448, 1)
   __syncthreads();
   tc::fence_after();
   if (warp == 0) tc::dealloc(tmem, 512);
-  if constexpr (SHARED) griddep_wait();
+  if (SHARED && cta == 0 && h == 0) griddep_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -961,7 +965,13 @@ __global__ void __launch_bounds__(448, 1)
   int* s_row = s_F + 8;                             // [8]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.y;
+  const int h = SHARED ? blockIdx.x : blockIdx.y, cta = SHARED ? blockIdx.y : blockIdx.x;  // (see decode.cuh)
+  OwnRow own{0, 0, 0};
+  int ctas = gridDim.x;
+  if constexpr (SHARED) {
+    own = own_row(a.shape, a.shared, a.shared_least, a.frontiers, a.table_rows, a.B, a.T, a.L, a.C, threadIdx.x & 31, ctas);
+    if (cta >= ctas) return;
+  }
   if (tid == 0) {
     for (int i = 0; i < NR; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -1000,13 +1010,11 @@ __global__ void __launch_bounds__(448, 1)
   if (!early && !SHARED) griddep_wait();  // (see decode.cuh)
   griddep_launch_dependents();
   if (tid < a.B) {
-    const int F = a.frontiers[tid], row = a.table_rows[tid];
+    const int F = SHARED ? own.F : a.frontiers[tid], row = SHARED ? own.row : a.table_rows[tid];
     const bool ok = F >= 0 && F <= a.L * 64 && row >= 0 && row < a.C && (a.k_new == nullptr || F >= a.T);
-    if (!ok && blockIdx.x == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
-    int before = 0;
-    if constexpr (SHARED) before = pages_before(a, F, row);
-    s_F[tid] = ok ? F - 64 * before : 0;
-    s_row[tid] = ok ? (SHARED ? row * a.L + before : row) : 0;
+    if (!ok && cta == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
+    s_F[tid] = ok ? F - 64 * own.before : 0;
+    s_row[tid] = ok ? (SHARED ? row * a.L + own.before : row) : 0;
   }
   if (warp == 0) {
     tc::alloc(tslot, 512);
@@ -1024,11 +1032,11 @@ __global__ void __launch_bounds__(448, 1)
     total += np;
     maxp = max(maxp, np);
   }
-  const int chunk = piece_chunk(s_F, a, total, maxp);
+  const int chunk = SHARED ? own_chunk(s_F, a, total, maxp, ctas) : piece_chunk(s_F, a, total, maxp);
   int nsegs = 0;
   for (int bb = 0; bb < a.B; ++bb) nsegs += max(1, (((s_F[bb] + 63) >> 6) + chunk - 1) / chunk);
-  const int s_lo = static_cast<int>(static_cast<int64_t>(blockIdx.x) * nsegs / gridDim.x);
-  const int s_hi = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * nsegs / gridDim.x);
+  const int s_lo = static_cast<int>(static_cast<int64_t>(cta) * nsegs / ctas);
+  const int s_hi = static_cast<int>(static_cast<int64_t>(cta + 1) * nsegs / ctas);
   const int R_real = a.T * a.G;
   auto trow_of = [&](int bb) { return a.tables + static_cast<int64_t>(s_row[bb]) * (SHARED ? 1 : a.L); };
 
@@ -1565,7 +1573,7 @@ __global__ void __launch_bounds__(448, 1)
   __syncthreads();
   tc::fence_after();
   if (warp == 0) tc::dealloc(tmem, 512);
-  if constexpr (SHARED) griddep_wait();
+  if (SHARED && cta == 0 && h == 0) griddep_wait();
 }
 
 template <int KK, int KV, int D, bool SHARED>
@@ -1578,7 +1586,7 @@ static cudaError_t launch_v(const nk_pool* p, int layer, const DecodeArgs& a, di
     if (e != cudaSuccess) return e;
     attr = true;
   }
-  cudaError_t e = launch_pdl(k, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
+  cudaError_t e = launch_pdl(k, SHARED ? dim3(grid.y, grid.x) : grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
   if (e != cudaSuccess || SHARED) return e;
   return launch_pdl(merge_kernel<D, 4>, dim3(a.B, a.H, D / 32), dim3(256), 0, s, a);
 }
@@ -1593,7 +1601,7 @@ static cudaError_t launch_vt(const nk_pool* p, int layer, const DecodeArgs& a, d
     if (e != cudaSuccess) return e;
     attr = true;
   }
-  cudaError_t e = launch_pdl(k, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
+  cudaError_t e = launch_pdl(k, SHARED ? dim3(grid.y, grid.x) : grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
   if (e != cudaSuccess || SHARED) return e;
   return launch_pdl(merge_kernel<D, 4>, dim3(a.B, a.H, D / 32), dim3(256), 0, s, a);
 }

@@ -544,9 +544,8 @@ class Pool:
                       workspace=None, stream=None, share_from: int = -1):
         """``decode`` of a batch whose rows share their first ``shared_pages``
         (int32 device tensor of one value) pages, attended once for all rows
-        where that saves ``share_from`` page bytes (nk.h; -1: the library's
-        choice, 0: always).  Without ``workspace`` one is allocated for this
-        call."""
+        from ``share_from`` of them on (-1: the library's choice, 0: always).
+        Without ``workspace`` one is allocated for this call."""
         import torch
         dev = self.device
         if torch.cuda.current_device() != dev:

@@ -184,10 +184,9 @@ def test_many_pages_per_range(profile, D, B, G, T, pages):
 
 
 @pytest.mark.parametrize("profile,G,T", [("bf16", 8, 1), ("k8v4", 8, 4), ("int8_g64", 4, 2)])
-@pytest.mark.parametrize("share_from", [-1, 1, 1 << 20, 1 << 40])
+@pytest.mark.parametrize("share_from", [-1, 1, 20, 21, 1 << 20, 1 << 40])
 def test_the_choice_does_not_change_results(profile, G, T, share_from):
-    """Whichever side of `share_from` the call falls on (page bytes saved here:
-    up to 2 rows * 20 pages * 2 heads * 12 to 32 KB), also one row, which saves none."""
+    """Whichever side of `share_from` the call falls on, also one row."""
     for F in ([64 * 20 + 9, 64 * 20 + 100, 64 * 20 + T, 64 * 20 + 64], [64 * 20 + 33]):
         b = Batch(profile, 128, 2, G, T, 20, F)
         check(*b.run(20, share_from=share_from), b.reference())
