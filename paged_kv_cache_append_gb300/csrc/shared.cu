@@ -58,7 +58,7 @@ static PageCosts page_costs(const nk_pool* p, int B, int R, int64_t page_bytes) 
   PageCosts c;
   c.tensor = R > 16 && p->desc.profile != NK_BF16 && p->desc.profile != NK_INT8_G64;
   c.own = d * (R <= 8 ? 0.3f : R <= 16 ? 0.56f : c.tensor ? 0.68f : 0.85f);
-  c.own_cold = fmaxf(D / 128.f * (R <= 8 ? 0.28f : R <= 16 ? 0.56f : c.tensor ? 0.8f : 1.35f), page_bytes / 40e3f);
+  c.own_cold = fmaxf(D / 128.f * (R <= 8 ? 0.28f : R <= 16 ? 0.56f : c.tensor ? 0.72f : 1.35f), page_bytes / 40e3f);
   c.prefix = D == 256 ? 1.25f * ((B * R + 127) / 128) : B * R > 128 ? 1.3f : D == 64 ? 1.25f : 0.95f;
   if (p->desc.profile == NK_INT8_G64) c.prefix += 0.6f;  // two key tiles a page
   return c;
@@ -85,10 +85,13 @@ static ShareShape share_shape(const nk_pool* p, const SharedPlan& pl, int B, int
   g.nsplit = pl.nsplit;
   g.ctas = pl.own.ctas;
   g.least = (B * H + pl.own.per_sm - 1) / pl.own.per_sm;
+  g.step = static_cast<float>(B * H) / pl.own.per_sm;
+  g.all_sms = fmaxf(floorf(p->num_sms / g.step), 1.f) * g.step;
   g.ranges_per_sm = 1.f / g.range_ctas;
   g.ctas_per_sm = static_cast<float>(pl.own.per_sm) / H;
   g.own_page = H * c.own_cold / 1.25f;
-  g.own_start = c.tensor ? 10.f : (R <= 8 ? 4.f : R <= 16 ? 6.f : 8.f) * D / 128;
+  g.own_start = c.tensor ? 8.f : (R <= 8 ? 4.f : R <= 16 ? 6.f : 8.f) * D / 128;
+  g.turn_start = !c.tensor ? g.own_start : D == 256 ? 10.f : 14.f;
   return g;
 }
 

@@ -30,9 +30,12 @@ struct ShareShape {
   int ctas = 0;        // own-pages CTAs of a KV head at most
   int least = 0;       // SMs on which every row has a CTA per head
   float ranges_per_sm = 0.f, ctas_per_sm = 0.f;  // 1 / range_ctas; own-pages CTAs of a head per SM
+  // rows of equal length use whole multiples of `step` SMs, of all SMs all_sms
+  float step = 0.f, all_sms = 0.f;
   // in units of the prefix pass's time for a page: own_page of a row's own page
-  // of all heads on one SM, own_start of the own-pages kernel without any page
-  float own_page = 0.f, own_start = 0.f;
+  // of all heads on one SM, own_start of the own-pages kernel without any page,
+  // turn_start of it when it follows the prefix pass
+  float own_page = 0.f, own_start = 0.f, turn_start = 0.f;
 };
 
 struct SharedPrefix {
@@ -78,10 +81,11 @@ __device__ __forceinline__ ShareSplit share_split(const ShareShape& g, int pages
   if (nsplit < 1) return ShareSplit{g.nsplit, g.ctas};
   const int per = (pages + nsplit - 1) / nsplit, used = (pages + per - 1) / per;
   const int left = g.sms - used * g.range_ctas;
+  const float busy = __fmul_rn(floorf(__fdividef(__fadd_rn(left, 0.01f), g.step)), g.step);
   const float at_once = __fadd_rn(
-      kTail, fmaxf(__fadd_rn(kPrefixStart, per), __fadd_rn(g.own_start, __fdividef(own_work, left))));
+      kTail, fmaxf(__fadd_rn(kPrefixStart, per), __fadd_rn(g.own_start, __fdividef(own_work, busy))));
   const float in_turn = __fadd_rn(__fadd_rn(kPrefixStart, __fdividef(pages, g.nsplit)),
-                                  __fadd_rn(g.own_start, __fdividef(own_work, g.sms)));
+                                  __fadd_rn(g.turn_start, __fdividef(own_work, g.all_sms)));
   if (!(at_once < in_turn)) return ShareSplit{g.nsplit, g.ctas};
   return ShareSplit{nsplit, min(__float2int_rz(__fmul_rn(__fadd_rn(left, 0.001f), g.ctas_per_sm)), g.ctas)};
 }
