@@ -3,7 +3,8 @@
 // the pages that all of them share, on the 5th-generation tensor cores.
 //
 // A CTA takes one KV head and one range of the shared pages and leaves one
-// partial (m, l, O) for its query rows.  A pipeline is 128 query rows,
+// partial (m, l, O) for its query rows; the ranges cover all SMs or those that
+// share_split leaves to the pass.  A pipeline is 128 query rows,
 //   S = Q K^T   tcgen05.mma M 128 x N 64 x K D, the K page in shared memory, S
 //               in one of two TMEM buffers
 //   O += P V    tcgen05.mma M 128 x N D x K 64, P over its S (TMEM)

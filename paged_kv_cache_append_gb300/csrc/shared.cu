@@ -9,7 +9,8 @@
 //                (prefix.cu); the shared pages are cut into ranges, and every
 //                range leaves a partial (m, l, O) for all query rows;
 //   own pages    the decode kernels (decode.cuh, vdecode.cu) on each row's
-//                pages behind the prefix, as partials too;
+//                pages behind the prefix, as partials too, after the prefix
+//                pass or next to it (share_split, shared.cuh);
 //   merge        M = max m, out = sum 2^(m - M) O / sum 2^(m - M) l, below.
 // The shared pages cross HBM once per call instead of once per row.
 #include <algorithm>
@@ -46,7 +47,7 @@ static int make_shared_plan(const nk_pool* p, int B, int T, int Hq, SharedPlan* 
 }
 
 // Measured times of one page of a KV head on one SM, in us: a row's own decode
-// of it, from L2 and (`cold`) from HBM, and the prefix pass's for a tile of rows.
+// of it, from L2 and (`cold`) from HBM, and the prefix pass's for its rows.
 struct PageCosts {
   float own, own_cold, prefix;
   bool tensor;  // the tensor-core decode
@@ -76,7 +77,8 @@ static int64_t share_least(const nk_pool* p, int B, int R, const PageCosts& c) {
   return gain <= 0.f ? INT32_MAX : static_cast<int64_t>(p->num_sms * (R > 16 ? 1.f : 4.5f) / gain) + 1;
 }
 
-// (share_split; the own-pages kernel alone takes 4 to 13 us)
+// The own-pages kernel without pages takes 3 to 10 us, behind the prefix pass up
+// to 17 on the tensor cores (share_split).
 static ShareShape share_shape(const nk_pool* p, const SharedPlan& pl, int B, int R, const PageCosts& c) {
   const int H = p->desc.num_kv_heads, D = p->desc.head_dim;
   ShareShape g;
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kMergeRows * 8 * SUB) shared_merge_kernel(cons
 // times the CTAs, 2 take less than 4 (116 against 120 us for the 4-token verify
 // of 8 rows); below, 8 take less than 4 (35.0 against 37.2 us for one token of 8
 // rows; CTAs of 8 query rows 35.9 either way, 4 or 14 loads of a thread in
-// flight 40.3 and 37.9).
+// flight 40.3 and 37.9; the two attention kernels in turn).
 template <int SUB>
 static cudaError_t launch_merge(int D, dim3 grid, cudaStream_t s, const SharedMergeArgs& m) {
   const dim3 block(kMergeRows * 8 * SUB);

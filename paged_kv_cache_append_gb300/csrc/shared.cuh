@@ -18,9 +18,9 @@ namespace nk {
 // other on all SMs, or at once, each on SMs of its own (their CTAs do not fit
 // one SM together), where that is expected to take less time.  At once hides
 // the start and the tail of one behind the other: 8 rows of one token over 480
-// FP8-row pages and 2000 own tokens take 25.7 us against 30.6, 4 tokens over 1920
-// K8V4 pages and 8000 own tokens 106.4 against 112.3, over 128 pages and 700 own
-// tokens 28.2 against 36.8; but 189 against 225 over 2000 NVFP4 pages of
+// FP8-row pages and 2000 own tokens take 26.5 us against 30.6, 4 tokens over 1920
+// K8V4 pages and 8000 own tokens 107 against 112, over 128 pages and 700 own
+// tokens 28.4 against 36.8; but 225 against 189 over 2000 NVFP4 pages of
 // head_dim 256 and 64 own tokens, whose rows need 32 SMs for their CTAs alone.
 // Working this out costs about 1 us a call.
 struct ShareShape {
