@@ -192,6 +192,50 @@ def test_the_choice_does_not_change_results(profile, G, T, share_from):
         check(*b.run(20, share_from=share_from), b.reference())
 
 
+@pytest.mark.parametrize("seed", range(4))
+def test_random_batches_against_the_decode(seed):
+    """Any profile, heads, lengths and rows that do not take part, over a
+    workspace of NaN: both ways to divide the SMs, within the two calls'
+    tolerances (a softmax scale s / sqrt(D) scales the scores' errors by s)."""
+    rng = np.random.default_rng(500 + seed)
+    stream = torch.cuda.current_stream().cuda_stream
+    done = 0
+    while done < 25:
+        profile, D = rng.choice(PROFILES), int(rng.choice([64, 128, 256]))
+        G, T, H = int(rng.choice([1, 2, 4, 5, 8, 16])), int(rng.choice([1, 1, 2, 3, 4])), int(rng.choice([1, 2, 3, 5, 8, 16]))
+        if G * T > (16 if D == 256 and profile in ("bf16", "int8_g64") else 32):
+            continue
+        done += 1
+        B, pages = int(rng.integers(1, 9)), int(2 ** rng.uniform(0, 8))
+        F = [int(rng.integers(0, 64 * pages + 1)) if rng.random() < 0.1
+             else 64 * pages + T + int(2 ** rng.uniform(0, rng.choice([6, 11]))) for _ in range(B)]
+        S = max(F) + 64
+        L = -(-S // 64)
+        M = pages + B * (L - pages)
+        pool = nk.Pool(str(profile), 1, H, D, S, B, M, order=str(rng.choice(["page_major", "head_major"])))
+        perm = rng.permutation(M).astype(np.int32)
+        tables = np.concatenate([np.tile(perm[:pages], (B, 1)), perm[pages:].reshape(B, L - pages)], 1)
+        tables, rows, F = dev(tables), dev(rng.permutation(B).astype(np.int32)), dev(np.array(F, np.int32))
+        g = torch.Generator(DEV).manual_seed(int(rng.integers(1 << 30)))
+        new = lambda *shape: torch.randn(shape, device=DEV, generator=g).bfloat16()  # noqa: E731
+        for b in range(B):
+            pool.append(0, tables, rows[b:b + 1].contiguous(), dev([0], torch.int32), new(1, 64 * L, H, D), new(1, 64 * L, H, D))
+        q, s = new(B, T, H * G, D), float(rng.choice([1, 3, -1]))
+        o2, l2 = pool.decode(0, q, tables, rows, F, s / math.sqrt(D))
+        ws = torch.full((pool.shared_workspace(B, T, H * G).numel(),), 0xFF, dtype=torch.uint8, device=DEV)
+        nk.nk_status_read(True, stream)
+        for _ in range(2):
+            out, lse = pool.shared_decode(0, q, tables, rows, F, dev([pages], torch.int32), s / math.sqrt(D),
+                                          workspace=ws, share_from=0)
+        assert nk.nk_status_read(True, stream) == 0
+        what = f"{profile} D {D} G {G} T {T} H {H} pages {pages} F {F.tolist()}"
+        limit = 2.0 ** -7 * o2.float().abs().max() + 2 * (2.0 ** -9 + 2e-3 * abs(s)) * 6
+        assert (out.float() - o2.float()).abs().max() <= limit, what
+        fin = torch.isfinite(l2)
+        assert torch.equal(torch.isfinite(lse), fin), what
+        assert not fin.any() or (lse - l2)[fin].abs().max() <= 2e-3 * abs(s), what
+
+
 def test_head_major_and_spare_table_rows():
     b = Batch("fp8_row", 128, 3, 4, 1, 6, [400, 500, 385], order="head_major", C=7)
     check(*b.run(6), b.reference())
