@@ -4,7 +4,9 @@ Argument marshalling only: every step of the hot path runs in libnk's CUDA
 kernels.  Functions named ``nk_*`` mirror the C entry points one to one and
 take raw integers for device pointers and streams; ``Pool`` is a convenience
 wrapper that allocates the planes as torch tensors (device memory), keeps them
-alive and passes ``torch.cuda.current_stream()``.
+alive and passes ``torch.cuda.current_stream()``.  A call with ``stream=`` runs
+on that stream: what it allocates (outputs, a workspace) belongs to it, and the
+caller orders the given tensors' other uses against it.
 
 There is no CPU fallback: ``load()`` raises when ``libnk.so`` has not been
 built, and every call raises ``NkError`` on a non-zero status.
@@ -12,6 +14,7 @@ built, and every call raises ``NkError`` on a non-zero status.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -296,6 +299,25 @@ def _stream(stream) -> int:
     return stream.cuda_stream if stream is not None else _current_stream(torch.cuda.current_device())
 
 
+def _on(stream):
+    """Where a call on `stream` (None: the current one) makes its tensors: in
+    that stream's order, so that the block they get is free by the time the
+    call runs and is not handed out again before it has."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(stream)
+
+
+def _handle(stream, dev: int) -> int:
+    """Stream handle of a call on device `dev`."""
+    if stream is None:
+        return _current_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream: expected a stream of device {dev}, got one of device {stream.device_index}")
+    return stream.cuda_stream
+
+
 _pyargs = None
 
 
@@ -355,12 +377,14 @@ def qk_norm_rope(q, k, positions, rope: Rope, q_out=None, k_out=None, stream=Non
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             return qk_norm_rope(q, k, positions, rope, q_out, k_out, stream)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    _check((_pyargs or _args()).norm_rope(q, k, positions, q_out, k_out, rope.address, rope.head_dim, dev,
-                                          _current_stream(dev) if stream is None else stream.cuda_stream))
+    at = _handle(stream, dev)
+    if q_out is None or k_out is None:
+        with _on(stream):
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if k_out is None:
+                k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    _check((_pyargs or _args()).norm_rope(q, k, positions, q_out, k_out, rope.address, rope.head_dim, dev, at))
     return q_out, k_out
 
 
@@ -379,14 +403,16 @@ def verify_drafts(target, tokens, uniforms, draft=None, draft_len=None, frontier
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             return verify_drafts(target, tokens, uniforms, draft, draft_len, frontiers, stream)
+    at = _handle(stream, dev)
     B, K1, _ = target.shape
-    out = torch.empty((B, K1), dtype=torch.int32, device=target.device)
-    if frontiers is None:
-        accepted, after = torch.empty(B, dtype=torch.int32, device=target.device), None
-    else:
-        accepted, after = torch.empty_like(frontiers), torch.empty_like(frontiers)
+    with _on(stream):
+        out = torch.empty((B, K1), dtype=torch.int32, device=target.device)
+        if frontiers is None:
+            accepted, after = torch.empty(B, dtype=torch.int32, device=target.device), None
+        else:
+            accepted, after = torch.empty_like(frontiers), torch.empty_like(frontiers)
     _check((_pyargs or _args()).verify(target, draft, tokens, draft_len, uniforms, frontiers, accepted, out, after, dev,
-                                       _current_stream(dev) if stream is None else stream.cuda_stream))
+                                       at))
     return accepted, out, after
 
 
@@ -435,6 +461,8 @@ class Pool:
                            _ptr(counts), _ptr(k), _ptr(v), B, T, _stream(stream))
 
     def workspace(self, B, T, Hq):
+        """The workspace that ``decode`` and ``append_decode`` use unless given
+        one: one for all calls of this pool, which then must not overlap."""
         import torch
         n = nk_decode_workspace_bytes(self.handle, B, T, Hq)
         if self._ws is None or self._ws.numel() < n:   # zero-filled once (split counters)
@@ -445,11 +473,12 @@ class Pool:
                workspace=None, stream=None):
         import torch
         B, T, Hq, D = q.shape
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
-        ws = workspace if workspace is not None else self.workspace(B, T, Hq)
+        with _on(stream if out is None or lse is None or workspace is None else None):
+            if out is None:
+                out = torch.empty_like(q)
+            if lse is None:
+                lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
+            ws = workspace if workspace is not None else self.workspace(B, T, Hq)
         nk_paged_decode_attention(_ptr(q), Hq, self.handle, layer, _ptr(tables), _ptr(table_rows),
                                   _ptr(frontiers), B, T, float(scale), _ptr(out), _ptr(lse),
                                   _ptr(ws), ws.numel(), _stream(stream))
@@ -461,11 +490,12 @@ class Pool:
         frontiers - T .. frontiers - 1, then attends (one launch)."""
         import torch
         B, T, Hq, D = q.shape
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
-        ws = workspace if workspace is not None else self.workspace(B, T, Hq)
+        with _on(stream if out is None or lse is None or workspace is None else None):
+            if out is None:
+                out = torch.empty_like(q)
+            if lse is None:
+                lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
+            ws = workspace if workspace is not None else self.workspace(B, T, Hq)
         nk_paged_append_decode_attention(_ptr(q), Hq, self.handle, layer, _ptr(tables), _ptr(table_rows),
                                          _ptr(frontiers), _ptr(k), _ptr(v), B, T, float(scale), _ptr(out),
                                          _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
@@ -495,16 +525,17 @@ class Pool:
                 lse=None, workspace=None, stream=None):
         import torch
         B, Tc, Hq, D = q.shape
-        if out is None:
-            out = torch.zeros_like(q)
-        if lse is None:
-            lse = torch.full((B, Tc, Hq), float("-inf"), dtype=torch.float32, device=q.device)
         n = nk_prefill_workspace_bytes(self.handle, B, Tc, Hq)
         ws = workspace
-        if ws is None and n:   # split partials and counters, zero-filled once, kept for reuse
-            if getattr(self, "_pws", None) is None or self._pws.numel() < n:
-                self._pws = torch.zeros(n, dtype=torch.uint8, device=q.device)
-            ws = self._pws
+        with _on(stream if out is None or lse is None or workspace is None else None):
+            if out is None:
+                out = torch.zeros_like(q)
+            if lse is None:
+                lse = torch.full((B, Tc, Hq), float("-inf"), dtype=torch.float32, device=q.device)
+            if ws is None and n:   # split partials and counters, zero-filled once, kept for reuse
+                if getattr(self, "_pws", None) is None or self._pws.numel() < n:
+                    self._pws = torch.zeros(n, dtype=torch.uint8, device=q.device)
+                ws = self._pws
         nk_paged_prefill_attention(_ptr(q), Hq, self.handle, layer, _ptr(tables), _ptr(table_rows),
                                    _ptr(prefix_len), _ptr(chunk_len), B, Tc, float(scale), _ptr(out),
                                    _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream))
@@ -527,11 +558,13 @@ class Pool:
                 return self.append_rope(layer, tables, table_rows, write_pos, k, v, rope, q, q_out, counts, stream)
         if rope.device != dev:
             raise ValueError("the rotation table is on another device than the pool")
+        at = _handle(stream, dev)
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            with _on(stream):
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         _check((_pyargs or _args()).append_rope(
             self.handle, self.H, self.D, self.C, self.L, layer, tables, table_rows, write_pos, k, v, q, q_out, counts,
-            rope.address, rope.head_dim, dev, _current_stream(dev) if stream is None else stream.cuda_stream))
+            rope.address, rope.head_dim, dev, at))
         return q_out
 
     def shared_workspace(self, B, T, Hq):
@@ -552,17 +585,17 @@ class Pool:
             with torch.cuda.device(dev):
                 return self.shared_decode(layer, q, tables, table_rows, frontiers, shared_pages, scale, out, lse,
                                           workspace, stream, share_from)
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        at = _handle(stream, dev)
         ws = workspace
-        if ws is None:
-            ws = self.shared_workspace(*q.shape[:3])
-            if stream is not None:
-                ws.record_stream(stream)
+        if out is None or lse is None or ws is None:
+            with _on(stream):
+                if out is None:
+                    out = torch.empty_like(q)
+                if lse is None:
+                    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+                if ws is None:
+                    ws = self.shared_workspace(*q.shape[:3])
         _check((_pyargs or _args()).shared_decode(
             self.handle, self.D, self.C, self.L, layer, q, tables, table_rows, frontiers, shared_pages, float(scale),
-            out, lse, share_from, ws.data_ptr(), ws.numel(), dev,
-            _current_stream(dev) if stream is None else stream.cuda_stream))
+            out, lse, share_from, ws.data_ptr(), ws.numel(), dev, at))
         return out, lse
