@@ -22,7 +22,7 @@ static struct {
                 const int32_t*, int32_t, int32_t, int32_t, int32_t*, int32_t*, int32_t*, void*);
 } lib;
 
-static PyObject *n_shape, *n_dtype, *n_stride, *n_get_device, *n_data_ptr;
+static PyObject *n_shape, *n_dtype, *n_stride, *n_get_device, *n_data_ptr, *n_element_size;
 static PyObject *t_bf16, *t_f32, *t_i32;
 
 typedef struct {
@@ -60,12 +60,12 @@ static int refuse(const char* name, const char* what, PyObject* x) {
   return 0;
 }
 
-/* Reads a tensor that has to be of `type` on CUDA device `dev`. */
+/* Reads a tensor that has to be of `type` (NULL: any) on CUDA device `dev`. */
 static int look(PyObject* x, const char* name, PyObject* type, long dev, Tensor* t) {
   PyObject* dtype = PyObject_GetAttr(x, n_dtype);
   if (!dtype) return 0;
   Py_DECREF(dtype); /* dtypes are objects for the life of the process */
-  if (dtype != type) return refuse(name, type == t_bf16  ? "expected a bf16 tensor"
+  if (type && dtype != type) return refuse(name, type == t_bf16  ? "expected a bf16 tensor"
                                          : type == t_f32 ? "expected a float32 tensor"
                                                          : "expected an int32 tensor", x);
   long long on, ptr;
@@ -113,6 +113,24 @@ static int rows_of(PyObject* x, const char* name, long dev, Tensor* t, nk_rows* 
   r->ptr = t->ptr;
   r->token_stride = one ? 0 : token;
   r->head_stride = t->size[n - 2] > 1 ? t->stride[n - 2] : 0;
+  return 1;
+}
+
+/* Scratch memory: a contiguous tensor of any type, or its address with *bytes
+ * given. */
+static int scratch(PyObject* x, long dev, void** ptr, size_t* bytes) {
+  if (PyLong_Check(x)) {
+    *ptr = PyLong_AsVoidPtr(x);
+    return !(!*ptr && PyErr_Occurred());
+  }
+  Tensor t;
+  long long each;
+  if (!look(x, "workspace", NULL, dev, &t) || !plain(x, "workspace", NULL, dev, t.nd, t.size, &t) ||
+      !long_of(PyObject_CallMethodNoArgs(x, n_element_size), &each))
+    return 0;
+  *ptr = t.ptr;
+  *bytes = (size_t)each;
+  for (int i = 0; i < t.nd; ++i) *bytes *= (size_t)t.size[i];
   return 1;
 }
 
@@ -208,13 +226,17 @@ static PyObject* append_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 /* (pool address, D, C, L, layer, q, tables, table_rows, frontiers, shared_pages, scale, out, lse, share_from,
- *  workspace address, workspace bytes, device, stream) */
+ *  workspace, device, stream), or the workspace's address and bytes for it */
 static PyObject* shared_decode(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   Tensor q, t, r, f, s, o, l;
-  if (!want(n, 18)) return NULL;
+  void* ws;
+  size_t bytes = 0;
+  const int given = n == 18; /* bytes of the workspace */
+  if (!given && !want(n, 17)) return NULL;
+  const Py_ssize_t at = 15 + given;
   const int64_t D = PyLong_AsLong(a[1]);
   const int64_t table[2] = {PyLong_AsLong(a[2]), PyLong_AsLong(a[3])};
-  const long layer = PyLong_AsLong(a[4]), dev = PyLong_AsLong(a[16]);
+  const long layer = PyLong_AsLong(a[4]), dev = PyLong_AsLong(a[at]);
   if (!look(a[5], "q", t_bf16, dev, &q)) return NULL;
   if (q.nd != 4 || q.size[3] != D) return refuse("q", "expected [B, T, query heads, head_dim] of the pool", a[5]), NULL;
   if (!plain(a[5], "q", t_bf16, dev, 4, q.size, &q) || !plain(a[6], "tables", t_i32, dev, 2, table, &t) ||
@@ -227,9 +249,9 @@ static PyObject* shared_decode(PyObject* self, PyObject* const* a, Py_ssize_t n)
   const double scale = PyFloat_AsDouble(a[10]);
   const long long from = PyLong_AsLongLong(a[13]);
   nk_pool* pool = ADDRESS(a[0]);
-  void *ws = ADDRESS(a[14]), *stream = ADDRESS(a[17]);
-  const size_t bytes = PyLong_AsSize_t(a[15]);
-  if (PyErr_Occurred()) return NULL;
+  void* stream = ADDRESS(a[at + 1]);
+  if (given) bytes = PyLong_AsSize_t(a[15]);
+  if (PyErr_Occurred() || !scratch(a[14], dev, &ws, &bytes)) return NULL;
   for (int i = 0; i < 3; ++i)
     if (q.size[i] > INT32_MAX) return refuse("q", "expected smaller sizes", a[5]), NULL;
   int rc;
@@ -315,6 +337,7 @@ PyMODINIT_FUNC PyInit__pyargs(void) {
   n_stride = PyUnicode_InternFromString("stride");
   n_get_device = PyUnicode_InternFromString("get_device");
   n_data_ptr = PyUnicode_InternFromString("data_ptr");
-  if (!n_shape || !n_dtype || !n_stride || !n_get_device || !n_data_ptr) return NULL;
+  n_element_size = PyUnicode_InternFromString("element_size");
+  if (!n_shape || !n_dtype || !n_stride || !n_get_device || !n_data_ptr || !n_element_size) return NULL;
   return PyModule_Create(&module);
 }

@@ -578,7 +578,8 @@ class Pool:
         """``decode`` of a batch whose rows share their first ``shared_pages``
         (int32 device tensor of one value) pages, attended once for all rows
         from ``share_from`` of them on (-1: the library's choice, 0: always).
-        Without ``workspace`` one is allocated for this call."""
+        ``workspace``: contiguous, of any type; without it one is allocated
+        for this call."""
         import torch
         dev = self.device
         if torch.cuda.current_device() != dev:
@@ -597,5 +598,5 @@ class Pool:
                     ws = self.shared_workspace(*q.shape[:3])
         _check((_pyargs or _args()).shared_decode(
             self.handle, self.D, self.C, self.L, layer, q, tables, table_rows, frontiers, shared_pages, float(scale),
-            out, lse, share_from, ws.data_ptr(), ws.numel(), dev, at))
+            out, lse, share_from, ws, dev, at))
         return out, lse

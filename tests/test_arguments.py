@@ -1,0 +1,51 @@
+"""Refusals of the binding's argument checks, decided on the host before any launch."""
+
+import pytest
+import torch
+
+from paged_kv_cache_append_gb300 import nk
+from tests.test_oracle_serving import F32, I32, Fake, lib  # noqa: F401
+
+
+class Scratch(Fake):
+    """A workspace as far as the checks look."""
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+
+def shared(*ws, **kw):
+    d = dict(pool=0, layer=0, scale=0.1)
+    d.update(kw)
+    return nk._args().shared_decode(d["pool"], 64, 3, 5, d["layer"], Fake(2, 1, 8, 64), Fake(3, 5, dtype=I32),
+                                    Fake(2, dtype=I32), Fake(2, dtype=I32), Fake(1, dtype=I32), d["scale"],
+                                    Fake(2, 1, 8, 64), Fake(2, 1, 8, dtype=F32), -1, *ws, 0, 0)
+
+
+U8 = torch.uint8
+
+
+@pytest.mark.parametrize("bad", [
+    Scratch(4096, dtype=U8, device=-1), Scratch(4096, dtype=U8, device=1), Scratch(4096, dtype=U8, stride=(0,)),
+    Scratch(4096, dtype=U8, stride=(2,)), Scratch(64, 64, dtype=F32, stride=(1, 64)),
+    Scratch(2, 64, dtype=U8, stride=(0, 1))])
+def test_workspace_is_checked(lib, bad):  # noqa: F811
+    assert shared(Scratch(4096, dtype=U8)) == -1        # reaches the library, which refuses the NULL pool
+    assert shared(Scratch(64, 64, dtype=F32)) == -1
+    assert shared(64, 4096) == -1                       # an address and its bytes
+    with pytest.raises(ValueError, match="workspace"):
+        shared(bad)
+
+
+def test_shared_decode_refuses_a_host_workspace(lib, monkeypatch):  # noqa: F811
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(nk, "_current_stream", lambda dev: 0)
+    p = nk.Pool.__new__(nk.Pool)
+    p.handle, p.D, p.C, p.L, p.device = 0, 64, 3, 5, 0
+    args = (0, Fake(2, 1, 8, 64), Fake(3, 5, dtype=I32), Fake(2, dtype=I32), Fake(2, dtype=I32), Fake(1, dtype=I32), 0.1,
+            Fake(2, 1, 8, 64), Fake(2, 1, 8, dtype=F32))
+    with pytest.raises(nk.NkError, match="null"):
+        p.shared_decode(*args, workspace=Scratch(4096, dtype=U8))
+    for bad in (torch.empty(4096, dtype=U8), torch.empty(1, dtype=U8).expand(4096)):
+        with pytest.raises(ValueError, match="workspace"):
+            p.shared_decode(*args, workspace=bad)
