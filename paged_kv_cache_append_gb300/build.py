@@ -68,14 +68,18 @@ def build_pyargs() -> str:
     return PYARGS
 
 
-def build(verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Compiles every CUDA source and links libnk.so; returns its path."""
+def objects(extra: list[str] | None = None) -> list[str]:
+    """Compiles the CUDA sources whose objects are not up to date; returns all objects' paths."""
     os.makedirs(BUILD, exist_ok=True)
-    extra = extra or []
-    build_pyargs()
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
-        objs = list(ex.map(lambda s: _compile(s, extra), srcs))
+        return list(ex.map(lambda s: _compile(s, extra or []), srcs))
+
+
+def build(verbose: bool = False, extra: list[str] | None = None) -> str:
+    """Compiles every CUDA source and links libnk.so; returns its path."""
+    build_pyargs()
+    objs = objects(extra)
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

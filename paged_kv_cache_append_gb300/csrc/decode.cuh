@@ -1229,13 +1229,10 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const De
                           dim3 grid, cudaStream_t s) {
   using Cfg = DecodeCfg<KK, KV, D, NQT>;
   auto k = decode_kernel<KK, KV, D, NQT, SHARED>;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
-  cudaError_t e = launch_pdl(k, SHARED ? dim3(grid.y, grid.x) : grid, dim3(Cfg::THREADS), Cfg::SMEM, s, tk, tv, a);
+  static std::atomic<uint64_t> granted{0};
+  cudaError_t e = grant_smem(granted, k, Cfg::SMEM);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(k, SHARED ? dim3(grid.y, grid.x) : grid, dim3(Cfg::THREADS), Cfg::SMEM, s, tk, tv, a);
   if (e != cudaSuccess || SHARED) return e;
   return launch_pdl(merge_kernel<D, NQT>, dim3(a.B, a.H, D / 32), dim3(256), 0, s, a);
 }
@@ -1250,16 +1247,18 @@ int decode_ring_bytes() {
 template <int KK, int KV, int D, int NQT>
 int decode_ctas_per_sm() {
   using Cfg = DecodeCfg<KK, KV, D, NQT>;
-  static int cached = 0;
-  if (!cached) {
-    auto k = decode_kernel<KK, KV, D, NQT, false>;
-    cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
-    int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, Cfg::THREADS, Cfg::SMEM) != cudaSuccess || n < 1)
-      n = 1;
-    cached = n;
-  }
-  return cached;
+  static std::atomic<uint64_t> granted{0};
+  static std::atomic<int> cached[64];
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return 1;
+  int n = device < 64 ? cached[device].load(std::memory_order_relaxed) : 0;
+  if (n) return n;
+  auto k = decode_kernel<KK, KV, D, NQT, false>;
+  if (grant_smem(granted, k, Cfg::SMEM) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, Cfg::THREADS, Cfg::SMEM) != cudaSuccess || n < 1)
+    n = 1;
+  if (device < 64) cached[device].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 // Per-profile entry points (defined in decode_<profile>.cu).

@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "nk.h"
@@ -41,6 +42,22 @@ __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wa
 // waits for this grid to complete).
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Grants `kernel` its dynamic shared memory on the current device, once per
+// device: the limit is a property of the kernel on one device.  `granted` is
+// the launcher's own set of the devices that have it (beyond the first 64 it is
+// granted every time).
+template <typename... KArgs>
+inline cudaError_t grant_smem(std::atomic<uint64_t>& granted, void (*kernel)(KArgs...), int bytes) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+  if (granted.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) granted.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // Launches `kernel` with programmatic stream serialization, so its CTAs may

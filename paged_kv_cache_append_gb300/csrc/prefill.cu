@@ -377,12 +377,9 @@ template <int D>
 static cudaError_t launch_prefill(const nk_pool* p, int layer, const PrefillArgs& a, dim3 grid, cudaStream_t s) {
   using Cfg = PrefillCfg<D>;
   auto k = prefill_kernel<D>;
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+  static std::atomic<uint64_t> granted{0};
+  cudaError_t e = grant_smem(granted, k, Cfg::SMEM);
+  if (e != cudaSuccess) return e;
   return launch_pdl(k, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
 }
 

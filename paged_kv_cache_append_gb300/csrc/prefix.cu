@@ -811,12 +811,9 @@ template <int KK, int KV, int D>
 static cudaError_t launch_prefix(const nk_pool* p, int layer, const PrefixArgs& a, cudaStream_t s) {
   using Cfg = PrefixCfg<KK, KV, D>;
   auto k = prefix_kernel<KK, KV, D>;
-  static int attr = -1;  // the device that has it
-  if (attr != p->device) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
-    if (e != cudaSuccess) return e;
-    attr = p->device;
-  }
+  static std::atomic<uint64_t> granted{0};
+  cudaError_t e = grant_smem(granted, k, Cfg::SMEM);
+  if (e != cudaSuccess) return e;
   // In clusters of two, which lie on one TPC (two SMs), so that the SMs left to
   // the own pages (share_split) are whole TPCs: where the two kernels shared
   // TPCs, the own-pages CTAs took up to 160 us instead of 99.

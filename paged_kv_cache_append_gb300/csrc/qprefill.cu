@@ -574,12 +574,9 @@ template <int KK, int KV, int D>
 static cudaError_t launch_q(const CUtensorMap& tk, const CUtensorMap& tv, const QArgs& a, cudaStream_t s) {
   using Cfg = QCfg<KK, KV, D>;
   auto k = qprefill_kernel<KK, KV, D>;
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+  static std::atomic<uint64_t> granted{0};
+  cudaError_t e = grant_smem(granted, k, Cfg::SMEM);
+  if (e != cudaSuccess) return e;
   return launch_pdl(k, dim3(a.sp.tiles * a.sp.nsplit, a.H, a.B), dim3(Cfg::THREADS), Cfg::SMEM, s, tk, tv, a);
 }
 

@@ -1580,13 +1580,10 @@ template <int KK, int KV, int D, bool SHARED>
 static cudaError_t launch_v(const nk_pool* p, int layer, const DecodeArgs& a, dim3 grid, cudaStream_t s) {
   using Cfg = VCfg<KK, KV, D>;
   auto k = vdecode_kernel<KK, KV, D, SHARED>;
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
-  cudaError_t e = launch_pdl(k, SHARED ? dim3(grid.y, grid.x) : grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
+  static std::atomic<uint64_t> granted{0};
+  cudaError_t e = grant_smem(granted, k, Cfg::SMEM);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(k, SHARED ? dim3(grid.y, grid.x) : grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
   if (e != cudaSuccess || SHARED) return e;
   return launch_pdl(merge_kernel<D, 4>, dim3(a.B, a.H, D / 32), dim3(256), 0, s, a);
 }
@@ -1595,13 +1592,10 @@ template <int KK, int KV, int D, bool SHARED>
 static cudaError_t launch_vt(const nk_pool* p, int layer, const DecodeArgs& a, dim3 grid, cudaStream_t s) {
   using Cfg = VTCfg<KK, KV, D>;
   auto k = vtdecode_kernel<KK, KV, D, SHARED>;
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
-  cudaError_t e = launch_pdl(k, SHARED ? dim3(grid.y, grid.x) : grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
+  static std::atomic<uint64_t> granted{0};
+  cudaError_t e = grant_smem(granted, k, Cfg::SMEM);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(k, SHARED ? dim3(grid.y, grid.x) : grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
   if (e != cudaSuccess || SHARED) return e;
   return launch_pdl(merge_kernel<D, 4>, dim3(a.B, a.H, D / 32), dim3(256), 0, s, a);
 }
