@@ -17,11 +17,11 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 
 @pytest.fixture(scope="module")
 def fake_path(tmp_path_factory):
-    """libnk's objects linked to the fake runtime."""
+    """libnk's objects linked to the fake runtime (and to that one where torch has loaded the real one)."""
     at = tmp_path_factory.mktemp("fake")
     rt, so = str(at / "cudart.o"), str(at / "libnk_fake.so")
     subprocess.run(["gcc", "-O1", "-Wall", "-fPIC", "-c", os.path.join(HERE, "fake_cudart.c"), "-o", rt], check=True)
-    subprocess.run(["g++", "-shared", "-o", so, rt, *build.objects()], check=True)
+    subprocess.run(["g++", "-shared", "-Wl,-Bsymbolic", "-o", so, rt, *build.objects()], check=True)
     return so
 
 
