@@ -250,8 +250,9 @@ int nk_paged_decode_attention(const void* q, int32_t Hq, const nk_pool* pool, in
  * Ordering: launched with programmatic stream serialization, the call reads
  * the block tables, table_rows, frontiers and the pool pages of earlier tokens
  * before it waits for the previous kernel in the stream (it overlaps that
- * kernel's tail); only q, k and v may be produced by that kernel.  After a
- * separate nk_paged_kv_append into the same rows, use nk_paged_decode_attention.
+ * kernel's tail); only q, k and v may be produced by that kernel, and the
+ * frontiers where it is nk_verify_drafts.  After a separate nk_paged_kv_append
+ * or nk_paged_kv_append_rope into the same rows, use nk_paged_decode_attention.
  * Errors: as nk_paged_decode_attention. */
 int nk_paged_append_decode_attention(const void* q, int32_t Hq, nk_pool* pool, int32_t layer,
                                      const int32_t* block_tables, const int32_t* table_rows,
@@ -432,8 +433,8 @@ int nk_paged_kv_append_rope(nk_pool* pool, int32_t layer, const int32_t* block_t
  * A drafted token outside [0, V) is rejected and a sequence without any weight
  * gets -1 (NK_STATUS_TOKEN_RANGE).  Runs on the current device, which must
  * hold every array.  The same inputs give the same bits on every call.
- * nk_paged_append_decode_attention reads its frontiers before the kernel ahead
- * of it has ended: frontiers_out is not for such a call launched right behind.
+ * frontiers_out may feed nk_paged_append_decode_attention right behind: it is
+ * published before that call starts.
  * Errors: NK_ERR_INVALID_ARG, NK_ERR_SHAPE (B in [1, 2^20], K in [0, 1024],
  * V in [1, 2^24], strides >= V), NK_ERR_CUDA. */
 int nk_verify_drafts(const float* target, int64_t target_stride, const float* draft,

@@ -306,8 +306,9 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
   // Launched with programmatic stream serialization: everything above overlaps
   // the previous kernel's tail; nothing it wrote is read before the wait.
   // The fused call's contract leaves only q and the new k / v to the previous
-  // kernel (block tables, row map, frontiers and the pages of earlier tokens
-  // are complete before it), so there the split plan and the page loads start
+  // kernel (block tables, row map and the pages of earlier tokens are complete
+  // before it, and so are the frontiers, but for the draft verification, which
+  // publishes them before it lets this kernel start), so there the split plan and the page loads start
   // at once and only the consumers wait, before they read q, k or v and before
   // any global write.  The plain decode waits here (a separate append may have
   // just written its pages).
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__((DecodeCfg<KK, KV, D, NQT>::THREADS), (DecodeC
 
   // ---- per-row lengths, loaded once in parallel ------------------------------
   if (tid < a.B) {
-    const int F = SHARED ? own.F : a.frontiers[tid], row = SHARED ? own.row : a.table_rows[tid];
+    const int F = SHARED ? own.F : load_published(a.frontiers + tid), row = SHARED ? own.row : a.table_rows[tid];
     const bool ok = F >= 0 && F <= a.L * 64 && row >= 0 && row < a.C && (a.k_new == nullptr || F >= a.T);
     if (!ok && cta == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
     s_F[tid] = ok ? F - 64 * own.before : 0;
@@ -1138,7 +1139,7 @@ __global__ void __launch_bounds__(256) merge_kernel(DecodeArgs a) {
   const int b = blockIdx.x, h = blockIdx.y, d0 = blockIdx.z * 32, tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
   if (tid < a.B) {
-    const int F = a.frontiers[tid], row = a.table_rows[tid];
+    const int F = load_published(a.frontiers + tid), row = a.table_rows[tid];
     const bool ok = F >= 0 && F <= a.L * 64 && row >= 0 && row < a.C && (a.k_new == nullptr || F >= a.T);
     s_F[tid] = ok ? F : 0;
   }

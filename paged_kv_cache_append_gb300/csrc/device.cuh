@@ -44,6 +44,14 @@ __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A value that the kernel ahead may have written before it let this one start:
+// from L2, past the SM's own cache.
+__device__ __forceinline__ int32_t load_published(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // Grants `kernel` its dynamic shared memory on the current device, once per
 // device: the limit is a property of the kernel on one device.  `granted` is
 // the launcher's own set of the devices that have it (beyond the first 64 it is

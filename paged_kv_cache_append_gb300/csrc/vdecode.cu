@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(448, 1)
   if (!early && !SHARED) griddep_wait();  // (see decode.cuh)
   griddep_launch_dependents();
   if (tid < a.B) {
-    const int F = SHARED ? own.F : a.frontiers[tid], row = SHARED ? own.row : a.table_rows[tid];
+    const int F = SHARED ? own.F : load_published(a.frontiers + tid), row = SHARED ? own.row : a.table_rows[tid];
     const bool ok = F >= 0 && F <= a.L * 64 && row >= 0 && row < a.C && (a.k_new == nullptr || F >= a.T);
     if (!ok && cta == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
     s_F[tid] = ok ? F - 64 * own.before : 0;
@@ -1010,7 +1010,7 @@ __global__ void __launch_bounds__(448, 1)
   if (!early && !SHARED) griddep_wait();  // (see decode.cuh)
   griddep_launch_dependents();
   if (tid < a.B) {
-    const int F = SHARED ? own.F : a.frontiers[tid], row = SHARED ? own.row : a.table_rows[tid];
+    const int F = SHARED ? own.F : load_published(a.frontiers + tid), row = SHARED ? own.row : a.table_rows[tid];
     const bool ok = F >= 0 && F <= a.L * 64 && row >= 0 && row < a.C && (a.k_new == nullptr || F >= a.T);
     if (!ok && cta == 0 && h == 0) set_status(a.status, NK_STATUS_FRONTIER);
     s_F[tid] = ok ? F - 64 * own.before : 0;

@@ -269,7 +269,6 @@ __global__ void __launch_bounds__(512, 2) verify_kernel(const __grid_constant__ 
   __shared__ Pair s_part[kVMaxWarps];   // the parts' sums of the chunk with the border
   __shared__ int s_owner, s_where;      // slice and warp chunk with the border
   griddep_wait();  // launched with programmatic stream serialization
-  griddep_launch_dependents();
 
   // ---- acceptance (every warp for itself) ---------------------------------------
   const int K = a.K, V = a.V;
@@ -302,6 +301,16 @@ __global__ void __launch_bounds__(512, 2) verify_kernel(const __grid_constant__ 
     }
   }
   const bool cut = n < Kb;
+  // The trimmed length goes out before the next kernel may start: the fused
+  // append + decode reads its frontiers while this one still runs.  The fence
+  // makes it visible to the whole GPU first (the reader takes it from L2).
+  if (tid == 0) {
+    if (rank == 0 && a.frontiers_out) {
+      a.frontiers_out[b] = a.frontiers[b] - (Kb - n);
+      __threadfence();
+    }
+    griddep_launch_dependents();
+  }
 
   // ---- this warp's chunk of this CTA's slice ----------------------------------------
   const int per = (V + nc - 1) / nc;
@@ -377,7 +386,6 @@ __global__ void __launch_bounds__(512, 2) verify_kernel(const __grid_constant__ 
     }
     if (tid == 0) {
       a.accepted[b] = n;
-      if (a.frontiers_out) a.frontiers_out[b] = a.frontiers[b] - (Kb - n);
       if (!found) set_status(a.status, NK_STATUS_TOKEN_RANGE);
     }
   }
