@@ -418,7 +418,8 @@ int nk_paged_kv_append_rope(nk_pool* pool, int32_t layer, const int32_t* block_t
  *   d_0 + .. + d_j > uniforms[b][K] * (d_0 + .. + d_{V-1}),
  *   d = max(p_n - q_n, 0) for n < K_b (p_n itself where that is 0 everywhere),
  *   d = p_{K_b} for n = K_b,
- * summed in more than 46 bits; entries that are not positive and finite weigh
+ * compared to within 2^-40 of the total for every V (rounding at its worst;
+ * 2^-46 in practice); entries that are not positive and finite weigh
  * 0 (p and q need not sum to 1; their sums have to be finite in fp32).  Where rounding leaves no such j, or
  * uniforms[b][K] is not below 1, the last token with weight is taken.
  *   target: device fp32, row (b, i) of V at target + (b * (K + 1) + i) *

@@ -13,8 +13,15 @@
 //
 // The sums decide at borders whose distance is a token's own probability, so
 // they are held in more than fp32, as unevaluated pairs of fp32 values (Knuth's
-// TwoSum on every difference and every addition: about 48 bits), two elements
-// to a packed instruction.
+// TwoSum on every difference and every addition), two elements to a packed
+// instruction; a lane's sum over many blocks has a third value.  With u = 2^-24
+// and every addition of two pairs of positive values good to 3 u^2, a lane's
+// blocks are off by at most 13 u^2 of their sum, whatever their number; its two
+// halves and the tail, the five levels over a warp, the four over its CTA and the
+// three over the cluster add 43 to that, the steps of the search and the last 8
+// tokens 36, and the border has the first 56 and 3 of its own: a running sum and
+// its border are compared to within 2^-40 of the total.  Where roundings do not
+// conspire it is 2^-47 (log-normal weights, up to 2^24 tokens).
 //
 // One cluster of CTAs works on a sequence.  Its warps take contiguous chunks of
 // the vocabulary and read them with coalesced 4-byte loads (rows of an odd
@@ -149,40 +156,89 @@ struct Weights {
   }
 };
 
-// h + l += s + e, exactly but for the last bits of l.
-__device__ __forceinline__ void pair_acc(float& h, float& l, float s, float e) {
-  const float t = h + s, bb = t - h;
-  l += ((h - (t - bb)) + (s - bb)) + e;
-  h = t;
+// a + b as the rounded sum (returned) and its error.
+__device__ __forceinline__ float two_sum(float a, float b, float& err) {
+  const float t = a + b, bb = t - a;
+  err = (a - (t - bb)) + (b - bb);
+  return t;
 }
 
-// The sum of one lane over its stride of [lo, hi), element by element.
-__device__ __forceinline__ void lane_sum(const Weights& w, int lo, int hi, int lane, float& h, float& l) {
-  for (int j = lo + lane; j < hi; j += 32) {
-    float s, e;
-    w.at(j, hi, s, e);
-    pair_acc(h, l, s, e);
+__device__ __forceinline__ F2 two_sum(F2 a, F2 b, F2& err) {
+  const F2 minus = pack2(-1.f, -1.f), t = add2(a, b), bb = fma2(a, minus, t);
+  err = add2(fma2(fma2(bb, minus, t), minus, a), fma2(bb, minus, b));
+  return t;
+}
+
+__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ F2 plus(F2 a, F2 b) { return add2(a, b); }
+
+// A lane's running sum h + l + c of float or, two at once, F2, without rounding
+// but in c, which holds what l lost: a pair would lose what is below 2^-24 of its
+// second value, in every addition anew (up to 2^-30 of the sum over the 2048
+// additions of a lane of the largest vocabulary: a few heavy tokens, then a
+// long light tail).
+template <class T>
+struct Running {
+  T h = T(0), l = T(0), c = T(0);
+
+  __device__ __forceinline__ void add(T s, T e) {
+    T e0, e1, e2;
+    h = two_sum(h, s, e0);
+    l = two_sum(l, e, e1);
+    l = two_sum(l, e0, e2);
+    c = plus(c, plus(e1, e2));
   }
+};
+
+__device__ __forceinline__ Pair pair_of(float h, float l, float c) {
+  const float t = h + l;
+  return Pair{t, (l - (t - h)) + c};
+}
+
+// h + l += s + e, exactly but for the last bits of l.
+__device__ __forceinline__ void pair_acc(float& h, float& l, float s, float e) {
+  float err;
+  h = two_sum(h, s, err);
+  l += err + e;
+}
+
+// The sum of one lane over its stride of [lo, hi), any elements, four at a time.
+__device__ __forceinline__ Pair lane_sum(const Weights& w, int lo, int hi, int lane) {
+  constexpr int U = 4;
+  Running<float> sum;
+  for (int j = lo + lane; j < hi; j += 32 * U) {
+    float s[U], e[U], h = 0.f, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < U; ++k) w.at(j + 32 * k, hi, s[k], e[k]);
+#pragma unroll
+    for (int k = 0; k < U; ++k) pair_acc(h, l, s[k], e[k]);
+    if (j - lane == lo) sum.h = h, sum.l = l;
+    else sum.add(h, l);
+  }
+  return pair_of(sum.h, sum.l, sum.c);
 }
 
 // The sum over [lo, hi) of one warp, in every lane.  Whole blocks of 256
 // elements take the packed path: with m = max(p, q), m - q is the weight, 0
-// where p <= q or p is NaN.  Entries that are not finite leave a sum that is
-// not, and the warp then does it over, element by element.
+// where p <= q or p is NaN.  A lane adds the block's elements to a pair of its
+// own, whose few roundings are below 2^-44 of the block, and the pair to its
+// running sum.  Entries that are not finite leave a sum that is not, and the
+// warp then does it over, element by element.
 template <bool Q>
 __device__ __forceinline__ Pair chunk_sum(const Weights& w, int lo, int hi, int lane) {
   constexpr int U = 8;
-  float h = 0.f, l = 0.f;
+  Pair sum{0.f, 0.f};
   int j = lo;
   if (w.zero < lo || w.zero >= hi) {
     const F2 minus = pack2(-1.f, -1.f);
-    F2 h2 = 0ull, l2 = 0ull;
+    Running<F2> run;
     for (; j + 32 * U <= hi; j += 32 * U) {
       float x[U], y[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) x[k] = __ldcs(w.p + j + 32 * k + lane);
 #pragma unroll
       for (int k = 0; k < U; ++k) y[k] = Q ? __ldcs(w.q + j + 32 * k + lane) : 0.f;
+      F2 bh = 0ull, bl = 0ull;  // the block
 #pragma unroll
       for (int k = 0; k < U; k += 2) {
         const F2 m = pack2(fmaxf(x[k], y[k]), fmaxf(x[k + 1], y[k + 1]));
@@ -193,23 +249,30 @@ __device__ __forceinline__ Pair chunk_sum(const Weights& w, int lo, int hi, int 
           const F2 bb = fma2(m, minus, s);
           e = fma2(add2(q, bb), minus, fma2(fma2(bb, minus, s), minus, m));
         }
-        const F2 t = add2(h2, s), bb = fma2(h2, minus, t);
-        l2 = add2(l2, add2(add2(fma2(fma2(bb, minus, t), minus, h2), fma2(bb, minus, s)), e));
-        h2 = t;
+        if (k == 0) {
+          bh = s;
+          bl = e;
+        } else {
+          F2 err;
+          bh = two_sum(bh, s, err);
+          bl = add2(bl, Q ? add2(err, e) : err);
+        }
       }
+      if (j == lo) run.h = bh, run.l = bl;
+      else run.add(bh, bl);
     }
-    float h1, l1;
-    unpack2(h2, h, h1);
-    unpack2(l2, l, l1);
-    pair_acc(h, l, h1, l1);
-    if (!__all_sync(0xffffffffu, fabsf(h) <= FLT_MAX && fabsf(l) <= FLT_MAX)) {
-      h = l = 0.f;
+    float h[2], l[2], c[2];
+    unpack2(run.h, h[0], h[1]);
+    unpack2(run.l, l[0], l[1]);
+    unpack2(run.c, c[0], c[1]);
+    sum = pair_add(pair_of(h[0], l[0], c[0]), pair_of(h[1], l[1], c[1]));
+    if (!__all_sync(0xffffffffu, fabsf(sum.h) <= FLT_MAX && fabsf(sum.l) <= FLT_MAX)) {
+      sum = Pair{0.f, 0.f};
       j = lo;
     }
   }
-  lane_sum(w, j, hi, lane, h, l);
-  const float t = h + l;
-  return warp_sum(Pair{t, l - (t - h)});
+  if (j < hi) sum = pair_add(sum, lane_sum(w, j, hi, lane));
+  return warp_sum(sum);
 }
 
 __device__ __forceinline__ Pair chunk_sum(const Weights& w, int lo, int hi, int lane) {
@@ -221,6 +284,7 @@ __device__ __forceinline__ Pair chunk_sum(const Weights& w, int lo, int hi, int 
 __device__ __forceinline__ int scan_token(const Weights& w, int lo, int hi, Pair base, Pair border, int lane) {
   constexpr int E = 8;
   int token = -1;
+  Running<float> done;  // the blocks before j
   for (int j = lo; j < hi; j += 32 * E) {
     float s[E], e[E];
     Pair sum{0.f, 0.f};
@@ -228,13 +292,13 @@ __device__ __forceinline__ int scan_token(const Weights& w, int lo, int hi, Pair
     for (int k = 0; k < E; ++k) w.at(j + E * lane + k, hi, s[k], e[k]);
 #pragma unroll
     for (int k = 0; k < E; ++k) sum = pair_add(sum, Pair{s[k], e[k]});
-    const Pair at = pair_add(base, warp_scan(sum, lane));
+    const Pair scan = warp_scan(sum, lane), start = pair_add(base, pair_of(done.h, done.l, done.c)), at = pair_add(start, scan);
     const uint32_t positive = __ballot_sync(0xffffffffu, sum.h > 0.f);
     const uint32_t over = __ballot_sync(0xffffffffu, pair_greater(at, border)) & positive;
     if (positive) {
       const int i = over ? __ffs(over) - 1 : 31 - __clz(positive);  // the lane that holds it
       const Pair before = shuffle(at, max(i - 1, 0));
-      Pair run = i > 0 ? before : base;
+      Pair run = i > 0 ? before : start;
       int last = -1, first = -1;
 #pragma unroll
       for (int k = 0; k < E; ++k) {
@@ -247,7 +311,8 @@ __device__ __forceinline__ int scan_token(const Weights& w, int lo, int hi, Pair
       token = j + E * i + __shfl_sync(0xffffffffu, first >= 0 ? first : last, i);
     }
     if (over) break;
-    base = shuffle(at, 31);
+    const Pair block = shuffle(scan, 31);
+    done.add(block.h, block.l);
   }
   return token;
 }
