@@ -1,5 +1,5 @@
 """Builds libnk.so in-tree with nvcc for sm_103a, and the CPython module that
-marshals arguments for it (``_pyargs.so``, gcc).
+marshals arguments for it (``_pyargs`` with the interpreter's ABI tag, gcc).
 
 Each translation unit under ``csrc/`` is compiled in parallel into
 ``_build/`` and linked into ``paged_kv_cache_append_gb300/libnk.so``; the
@@ -21,7 +21,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnk.so")
-PYARGS = os.path.join(PKG, "_pyargs.so")
+# One file per interpreter ABI: it is built against one version's headers, and
+# another version looks for its own.
+PYARGS = os.path.join(PKG, "_pyargs" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
@@ -55,6 +57,9 @@ def _compile(src: str, extra: list[str]) -> str:
 def build_pyargs() -> str:
     """Compiles csrc/pyargs.c against this interpreter's headers; returns its path."""
     src = os.path.join(CSRC, "pyargs.c")
+    untagged = os.path.join(PKG, "_pyargs.so")   # any version would load it
+    if os.path.exists(untagged):
+        os.remove(untagged)
     newest = max(os.path.getmtime(p) for p in (src, os.path.join(ROOT, "include", "nk.h")))
     if os.path.exists(PYARGS) and os.path.getmtime(PYARGS) >= newest:
         return PYARGS

@@ -1,9 +1,12 @@
 """Refusals of the binding's argument checks, decided on the host before any launch."""
 
+import os
+import sysconfig
+
 import pytest
 import torch
 
-from paged_kv_cache_append_gb300 import nk
+from paged_kv_cache_append_gb300 import build, nk
 from tests.test_oracle_serving import F32, I32, Fake, lib  # noqa: F401
 
 
@@ -49,3 +52,19 @@ def test_shared_decode_refuses_a_host_workspace(lib, monkeypatch):  # noqa: F811
     for bad in (torch.empty(4096, dtype=U8), torch.empty(1, dtype=U8).expand(4096)):
         with pytest.raises(ValueError, match="workspace"):
             p.shared_decode(*args, workspace=bad)
+
+
+def test_the_argument_module_is_named_for_its_interpreter(lib):  # noqa: F811
+    """Built against one version's headers: another version must not find it,
+    nor one without a tag, which every version would load."""
+    untagged = os.path.join(nk.PKG, "_pyargs.so")
+    with open(untagged, "wb"):
+        pass
+    try:
+        path = build.build_pyargs()
+        assert os.path.basename(path) == "_pyargs" + sysconfig.get_config_var("EXT_SUFFIX")
+        assert not os.path.exists(untagged)
+        assert nk._args().__file__ == path
+    finally:
+        if os.path.exists(untagged):
+            os.remove(untagged)
