@@ -163,6 +163,7 @@ static PyObject* norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   nk_rows rq, rk, oq, ok;
   if (!want(n, 9)) return NULL;
   const long hd = PyLong_AsLong(a[6]), dev = PyLong_AsLong(a[7]);
+  if (PyErr_Occurred()) return NULL; /* no call to Python with an error set */
   if (!rows_of(a[0], "q", dev, &q, &rq) || !rows_of(a[1], "k", dev, &k, &rk)) return NULL;
   const int D = q.nd - 1, lead = q.nd - 2;
   if (!same_size(&q, &k, lead) || k.size[D] != q.size[D] || (hd && hd != q.size[D]))
@@ -194,6 +195,7 @@ static PyObject* append_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   const int64_t H = PyLong_AsLong(a[1]), D = PyLong_AsLong(a[2]);
   const int64_t table[2] = {PyLong_AsLong(a[3]), PyLong_AsLong(a[4])};
   const long layer = PyLong_AsLong(a[5]), hd = PyLong_AsLong(a[15]), dev = PyLong_AsLong(a[16]);
+  if (PyErr_Occurred()) return NULL;
   const int has_q = !NONE(a[11]);
   if (!rows_of(a[9], "k", dev, &k, &rk) || !rows_of(a[10], "v", dev, &v, &rv)) return NULL;
   if (k.nd != 4 || k.size[2] != H || k.size[3] != D || (hd && hd != D))
@@ -237,6 +239,7 @@ static PyObject* shared_decode(PyObject* self, PyObject* const* a, Py_ssize_t n)
   const int64_t D = PyLong_AsLong(a[1]);
   const int64_t table[2] = {PyLong_AsLong(a[2]), PyLong_AsLong(a[3])};
   const long layer = PyLong_AsLong(a[4]), dev = PyLong_AsLong(a[at]);
+  if (PyErr_Occurred()) return NULL;
   if (!look(a[5], "q", t_bf16, dev, &q)) return NULL;
   if (q.nd != 4 || q.size[3] != D) return refuse("q", "expected [B, T, query heads, head_dim] of the pool", a[5]), NULL;
   if (!plain(a[5], "q", t_bf16, dev, 4, q.size, &q) || !plain(a[6], "tables", t_i32, dev, 2, table, &t) ||
@@ -281,6 +284,7 @@ static PyObject* verify(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   int64_t ps, qs = 0;
   if (!want(n, 11)) return NULL;
   const long dev = PyLong_AsLong(a[9]);
+  if (PyErr_Occurred()) return NULL;
   if (!look(a[0], "target", t_f32, dev, &p)) return NULL;
   if (p.nd != 3 || p.size[1] < 1) return refuse("target", "expected [B, K + 1, V]", a[0]), NULL;
   const int64_t B = p.size[0], K = p.size[1] - 1, V = p.size[2];

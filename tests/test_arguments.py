@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from paged_kv_cache_append_gb300 import build, nk
-from tests.test_oracle_serving import F32, I32, Fake, lib  # noqa: F401
+from tests.test_oracle_serving import F32, I32, Fake, _args_append, lib  # noqa: F401
 
 
 class Scratch(Fake):
@@ -68,3 +68,13 @@ def test_the_argument_module_is_named_for_its_interpreter(lib):  # noqa: F811
     finally:
         if os.path.exists(untagged):
             os.remove(untagged)
+
+
+@pytest.mark.parametrize("layer,error", [(None, TypeError), ("0", TypeError), (1.5, TypeError), (1 << 70, OverflowError)])
+def test_a_layer_that_is_no_number_is_named(lib, layer, error):  # noqa: F811
+    """The error that the number raises, not one of the calls that follow."""
+    assert shared(64, 4096, layer=0) == -1 and _args_append(layer=0) == -1
+    with pytest.raises(error):
+        shared(64, 4096, layer=layer)
+    with pytest.raises(error):
+        _args_append(layer=layer)
