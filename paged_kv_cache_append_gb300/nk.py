@@ -303,10 +303,8 @@ def _on(stream):
     """Where a call on `stream` (None: the current one) makes its tensors: in
     that stream's order, so that the block they get is free by the time the
     call runs and is not handed out again before it has."""
-    if stream is None:
-        return contextlib.nullcontext()
     import torch
-    return torch.cuda.stream(stream)
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
 def _handle(stream, dev: int) -> int:
@@ -388,6 +386,15 @@ def qk_norm_rope(q, k, positions, rope: Rope, q_out=None, k_out=None, stream=Non
     return q_out, k_out
 
 
+def _verify_outputs(target, frontiers):
+    import torch
+    B, K1, _ = target.shape
+    out = torch.empty((B, K1), dtype=torch.int32, device=target.device)
+    if frontiers is None:
+        return torch.empty(B, dtype=torch.int32, device=target.device), out, None
+    return torch.empty_like(frontiers), out, torch.empty_like(frontiers)
+
+
 def verify_drafts(target, tokens, uniforms, draft=None, draft_len=None, frontiers=None, stream=None):
     """Verification of drafted tokens (nk.h, nk_verify_drafts).
 
@@ -404,13 +411,11 @@ def verify_drafts(target, tokens, uniforms, draft=None, draft_len=None, frontier
         with torch.cuda.device(dev):
             return verify_drafts(target, tokens, uniforms, draft, draft_len, frontiers, stream)
     at = _handle(stream, dev)
-    B, K1, _ = target.shape
-    with _on(stream):
-        out = torch.empty((B, K1), dtype=torch.int32, device=target.device)
-        if frontiers is None:
-            accepted, after = torch.empty(B, dtype=torch.int32, device=target.device), None
-        else:
-            accepted, after = torch.empty_like(frontiers), torch.empty_like(frontiers)
+    if stream is None:
+        accepted, out, after = _verify_outputs(target, frontiers)
+    else:
+        with _on(stream):
+            accepted, out, after = _verify_outputs(target, frontiers)
     _check((_pyargs or _args()).verify(target, draft, tokens, draft_len, uniforms, frontiers, accepted, out, after, dev,
                                        at))
     return accepted, out, after
@@ -473,12 +478,15 @@ class Pool:
                workspace=None, stream=None):
         import torch
         B, T, Hq, D = q.shape
-        with _on(stream if out is None or lse is None or workspace is None else None):
-            if out is None:
-                out = torch.empty_like(q)
-            if lse is None:
-                lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
-            ws = workspace if workspace is not None else self.workspace(B, T, Hq)
+        ws = workspace
+        if out is None or lse is None or ws is None:
+            with _on(stream):
+                if out is None:
+                    out = torch.empty_like(q)
+                if lse is None:
+                    lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
+                if ws is None:
+                    ws = self.workspace(B, T, Hq)
         nk_paged_decode_attention(_ptr(q), Hq, self.handle, layer, _ptr(tables), _ptr(table_rows),
                                   _ptr(frontiers), B, T, float(scale), _ptr(out), _ptr(lse),
                                   _ptr(ws), ws.numel(), _stream(stream))
@@ -490,12 +498,15 @@ class Pool:
         frontiers - T .. frontiers - 1, then attends (one launch)."""
         import torch
         B, T, Hq, D = q.shape
-        with _on(stream if out is None or lse is None or workspace is None else None):
-            if out is None:
-                out = torch.empty_like(q)
-            if lse is None:
-                lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
-            ws = workspace if workspace is not None else self.workspace(B, T, Hq)
+        ws = workspace
+        if out is None or lse is None or ws is None:
+            with _on(stream):
+                if out is None:
+                    out = torch.empty_like(q)
+                if lse is None:
+                    lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
+                if ws is None:
+                    ws = self.workspace(B, T, Hq)
         nk_paged_append_decode_attention(_ptr(q), Hq, self.handle, layer, _ptr(tables), _ptr(table_rows),
                                          _ptr(frontiers), _ptr(k), _ptr(v), B, T, float(scale), _ptr(out),
                                          _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
@@ -527,15 +538,16 @@ class Pool:
         B, Tc, Hq, D = q.shape
         n = nk_prefill_workspace_bytes(self.handle, B, Tc, Hq)
         ws = workspace
-        with _on(stream if out is None or lse is None or workspace is None else None):
-            if out is None:
-                out = torch.zeros_like(q)
-            if lse is None:
-                lse = torch.full((B, Tc, Hq), float("-inf"), dtype=torch.float32, device=q.device)
-            if ws is None and n:   # split partials and counters, zero-filled once, kept for reuse
-                if getattr(self, "_pws", None) is None or self._pws.numel() < n:
-                    self._pws = torch.zeros(n, dtype=torch.uint8, device=q.device)
-                ws = self._pws
+        if out is None or lse is None or ws is None:
+            with _on(stream):
+                if out is None:
+                    out = torch.zeros_like(q)
+                if lse is None:
+                    lse = torch.full((B, Tc, Hq), float("-inf"), dtype=torch.float32, device=q.device)
+                if ws is None and n:   # split partials and counters, zero-filled once, kept for reuse
+                    if getattr(self, "_pws", None) is None or self._pws.numel() < n:
+                        self._pws = torch.zeros(n, dtype=torch.uint8, device=q.device)
+                    ws = self._pws
         nk_paged_prefill_attention(_ptr(q), Hq, self.handle, layer, _ptr(tables), _ptr(table_rows),
                                    _ptr(prefix_len), _ptr(chunk_len), B, Tc, float(scale), _ptr(out),
                                    _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream))
