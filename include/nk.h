@@ -288,7 +288,9 @@ int nk_shared_decode_workspace_bytes(const nk_pool* pool, int32_t B, int32_t T, 
  * Three launches: the prefix on the tensor cores, all B * T * Hq / H query
  * rows of a KV head in 128-row tiles (csrc/prefix.cu; softmax weights and
  * values are rounded as in nk_paged_prefill_attention, but BF16 weights to 16
- * bits instead of 8); each row's own pages
+ * bits instead of 8, and so are the queries: over FP8-row and K8V4 keys of
+ * head_dim 128 and 256 each element to 2^-17 of its row's largest, which
+ * nk_paged_decode_attention keeps to 2^-31); each row's own pages
  * (csrc/decode.cuh, csrc/vdecode.cu); the log-sum-exp merge (csrc/shared.cu).
  * The pool's device must be current. */
 int nk_paged_shared_decode_attention(const void* q, int32_t Hq, const nk_pool* pool, int32_t layer,

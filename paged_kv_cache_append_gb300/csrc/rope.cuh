@@ -158,7 +158,9 @@ __device__ __forceinline__ uint4 pack8_bf16(const F2* y) {
 }
 
 // x / s rounded once, from inv = 1 / s rounded once: the quotient's error is
-// taken off with one exact remainder, which leaves the rounded quotient (a
+// taken off with one exact remainder (Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990), which leaves the
+// rounded quotient (a
 // quotient that fp32 holds, such as a tie between two codes, comes out exactly:
 // the remainder then is its error times s).  The sign is x's, also of a zero.
 // For finite x and s in binary16's or E4M3's range.

@@ -5,9 +5,9 @@
 // p_{K_b} and the draft model's rows q_0 .. q_{K_b - 1} (without them each
 // draft is taken as certain: q_i is 1 at x_i).  Draft i is accepted iff
 //   u_i q_i(x_i) < p_i(x_i)
-// (compared exactly: the fp64 product of two fp32 values has no rounding); n
-// is the first draft that is not, K_b if there is none.  The next token is
-// drawn by inverse transform from the weights
+// (compared exactly: the rounded product and its error); n is the first draft
+// that is not, K_b if there is none.  The next token is drawn by inverse
+// transform from the weights
 //   d_j = max(p_n(j) - q_n(j), 0)  (n < K_b),   d_j = p_n(j)  (n = K_b):
 // the least j with d_0 + .. + d_j > u_K (d_0 + .. + d_{V-1}).
 //
