@@ -61,7 +61,8 @@ enum {
   NK_STATUS_TIMEOUT = 4,     /* a bounded wait on a copy barrier ran out     */
   NK_STATUS_TOKEN_RANGE = 8, /* a drafted token outside [0, V), or no weight */
                              /* anywhere to draw the next token from         */
-  NK_STATUS_PREFIX = 16      /* rows of a shared prefix named other pages    */
+  NK_STATUS_PREFIX = 16,     /* rows of a shared prefix named other pages    */
+  NK_STATUS_PAGES = 32       /* a row needed more pages than were free       */
 };
 
 /* KV profiles ("Paged KV cache" page, pool contents paragraph: BF16,
@@ -445,6 +446,159 @@ int nk_verify_drafts(const float* target, int64_t target_stride, const float* dr
                      const float* uniforms, const int32_t* frontiers, int32_t B, int32_t K,
                      int32_t V, int32_t* accepted, int32_t* out_tokens, int32_t* frontiers_out,
                      void* stream);
+
+/* ---- differential attention over the pages ---------------------------------
+ * No counterpart on the design pages: an attention whose heads come in pairs.
+ * Query heads 2i and 2i + 1 are the two maps of head i (i < Hq / 2), KV heads
+ * 2j and 2j + 1 hold their two keys, and the values of both side by side are
+ * the head's one value of 2 D elements, V = [V^_2j  V^_2j+1];  j = i / (Hq / H).
+ * The pool and every append are those of a plain cache of H heads.
+ *   o = softmax(s1) V - lambda softmax(s2) V,   s_m = softmax_scale <q_2i+m, K^_2j+m>
+ *   out = o * rsqrt(mean(o^2) + eps) * w * out_scale     (w not NULL)
+ *   out = o * out_scale                                   (w NULL)
+ * with the mean over the 2 D elements, all sums in fp32 and one rounding, to
+ * bf16, at the end. */
+typedef struct {
+  const float* lambda;      /* device fp32: that of head i of token n at
+                               lambda[n * lambda_stride + i] (n = b * T + t)    */
+  int64_t lambda_stride;    /* elements; 0: the same for every token            */
+  const void* norm_weight;  /* device bf16 [2 D], 16-byte aligned; NULL: no norm */
+  float eps;                /* finite, > 0                                      */
+  float out_scale;          /* finite                                           */
+} nk_diff;
+
+/* Workspace of nk_paged_diff_decode_attention for (B, T, Hq) on the current device. */
+int nk_diff_decode_workspace_bytes(const nk_pool* pool, int32_t B, int32_t T, int32_t Hq,
+                                   size_t* bytes);
+
+/* Differential attention of decode / verify tokens: frontiers, visibility and
+ * the operands' layouts as in nk_paged_decode_attention, every page read once
+ * for both maps.
+ *   q:    device bf16 [B][T][Hq][D];   out: device bf16 [B][T][Hq / 2][2 D];
+ *   lse:  device fp32 [B][T][Hq] or NULL, ln of each map's own sum;
+ *   a token that sees no key (F_b - T + t < 0) gets out = 0, lse = -inf.
+ *   workspace: nk_diff_decode_workspace_bytes bytes, no initialisation needed;
+ *   two calls that share a workspace must not overlap.
+ * A NaN among the keys or values that a token sees makes its outputs NaN, and
+ * a NaN or an infinity among the values of a row's T tokens may reach the
+ * outputs of all T; stale bytes past the frontier do not enter.
+ * Two launches (csrc/diff_decode.cuh): split-K over the pages, then the join of
+ * the splits with the difference and the norm.  Softmax weights and values are
+ * rounded as in nk_paged_decode_attention's warp-level kernel.
+ * The pool's device must be current.
+ * Errors: NK_ERR_INVALID_ARG, NK_ERR_SHAPE (H odd, Hq not a multiple of H, B > C,
+ * T < 1), NK_ERR_UNSUPPORTED (head_dim 256; T * Hq / H > 64), NK_ERR_ALIGN,
+ * NK_ERR_WORKSPACE, NK_ERR_CUDA. */
+int nk_paged_diff_decode_attention(const void* q, int32_t Hq, const nk_pool* pool, int32_t layer,
+                                   const int32_t* block_tables, const int32_t* table_rows,
+                                   const int32_t* frontiers, int32_t B, int32_t T,
+                                   float softmax_scale, const nk_diff* diff, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace of nk_paged_diff_prefill_attention for (B, Tc, Hq); it does not
+ * depend on the pool's context length. */
+int nk_diff_prefill_workspace_bytes(const nk_pool* pool, int32_t B, int32_t Tc, int32_t Hq,
+                                    size_t* bytes);
+
+/* Differential attention of prompt chunks: prefix_len, chunk_len, visibility
+ * and the operands' layouts as in nk_paged_prefill_attention, out and lambda as
+ * above (n = b * Tc + i).  Rows i >= chunk_len[b] of out and lse are not written.
+ *   workspace: nk_diff_prefill_workspace_bytes bytes, no initialisation needed;
+ *   two calls that share a workspace must not overlap.
+ * A NaN or an infinity among the values of a chunk may reach all of its outputs.
+ * Two launches: on the tensor cores (csrc/diff_prefill.cu, csrc/diff_qprefill.cu)
+ * and for the join.  Softmax weights and values are rounded as in
+ * nk_paged_prefill_attention.
+ * The pool's device must be current.
+ * Errors: as nk_paged_diff_decode_attention; NK_ERR_UNSUPPORTED for Hq / H > 64. */
+int nk_paged_diff_prefill_attention(const void* q_chunk, int32_t Hq, const nk_pool* pool,
+                                    int32_t layer, const int32_t* block_tables,
+                                    const int32_t* table_rows, const int32_t* prefix_len,
+                                    const int32_t* chunk_len, int32_t B, int32_t Tc,
+                                    float softmax_scale, const nk_diff* diff, void* out,
+                                    float* lse, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* ---- norms around a block ---------------------------------------------------
+ * What stands between two blocks of a layer, in one pass over their rows
+ * (y: the block's output, r: the residual stream, g: a gate):
+ *   u = y * rsqrt(mean(y^2) + eps) * (post + weight_offset)   (post_weight not NULL, else y)
+ *   h = residual_scale * r + scale * (gate ? act(g) * u : u)   (y NULL: residual_scale * r)
+ *   x = h * rsqrt(mean(h^2) + eps) * (weight + weight_offset)
+ * with act the identity or the logistic function.  Everything is fp32 until h
+ * is rounded to the residual's type and x, from the unrounded h, to bf16. */
+typedef struct {
+  const void* weight;       /* device bf16 [dim], 16-byte aligned; NULL: no x   */
+  const void* post_weight;  /* device bf16 [dim], 16-byte aligned; NULL: u = y  */
+  float eps;                /* finite, > 0                                      */
+  float weight_offset;      /* 0, or 1 for weights stored as w - 1              */
+  float scale;              /* finite                                           */
+  float residual_scale;     /* finite                                           */
+  int32_t sigmoid_gate;     /* 0: act(g) = g, 1: 1 / (1 + exp(-g))              */
+  int32_t residual_fp32;    /* the residual's type: 0 bf16, 1 fp32              */
+} nk_block_norm;
+
+/* dim: a multiple of 8 in [8, 16384].  Row n of an operand is dim contiguous
+ * elements at n * stride (elements, multiples of 8; pointers 16-byte aligned).
+ *   y, gate: device bf16 [N][dim], either may be NULL (gate only with y;
+ *   post_weight only with y); gate_stride 0: one gate row for all tokens.
+ *   residual, residual_out: device, of the residual's type; residual_out may be
+ *   NULL (h is then not stored) or the residual itself (same pointer, stride).
+ *   x_out: device bf16, NULL iff weight is; it may be y (same pointer, stride).
+ * Outputs must not overlap any other operand, nor rows of an output one another
+ * (NK_ERR_SHAPE).  Runs on the current device.
+ * Errors: NK_ERR_INVALID_ARG (also: no output), NK_ERR_SHAPE, NK_ERR_UNSUPPORTED
+ * (dim), NK_ERR_ALIGN, NK_ERR_CUDA. */
+int nk_residual_norm(const nk_block_norm* norm, int32_t dim, int32_t N, const void* y,
+                     int64_t y_stride, const void* gate, int64_t gate_stride,
+                     const void* residual, int64_t residual_stride, void* residual_out,
+                     int64_t residual_out_stride, void* x_out, int64_t x_stride, void* stream);
+
+/* ---- pages of a step, from the requests' lengths -----------------------------
+ * The device-side form of the mapping that precedes a step ("Paged KV cache"
+ * page: decode page growth, trim of rejected speculative tails): each row of the
+ * batch is brought to exactly nk_pages_needed(its tokens after the step) pages,
+ * taken from or returned to a stack of free page ids, without the host.
+ * Compact row b has committed[b] valid tokens and count_b = counts ? counts[b] :
+ * T new ones (0 <= count_b <= T; T = 0 only trims), F_b = committed[b] +
+ * count_b, need_b = ceil(F_b / 64), and mapped[table_rows[b]] pages now.
+ *  1. Rows above max(need_b, keep_b) return their pages behind it: rows from the
+ *     last to the first, each from its last page on, are pushed on the stack.
+ *     keep_b = keep ? keep[table_rows[b]] : 0 protects leading pages that the
+ *     row shares with others and does not own.
+ *  2. Rows below need_b take pages: rows from the first to the last, each for
+ *     its next logical page, pop the stack.  A row takes all that it needs or
+ *     none: with fewer free pages it is left as it was (NK_STATUS_PAGES) and the
+ *     next row is tried.
+ * So pages that a call takes and the next one returns leave the stack as it was.
+ *   block_tables: device int32 [C][L]; entries at and behind a row's mapped
+ *   count are not read, and those of returned pages keep what they hold.
+ *   mapped, mapped_out: device int32 [C]; mapped_out may be mapped; rows that
+ *   are not in the batch keep their value.
+ *   free_pages: device int32 [M], the first *free_count entries are the free
+ *   ids; free_count, free_count_out: device int32, may be the same.
+ *   frontiers: device int32 [B] = F_b, or 0 for a row that did not get its pages
+ *   (nk_paged_append_decode_attention then writes nothing for it); may be
+ *   committed.
+ *   positions: device int32 [B][T] or NULL = committed[b] + t for t < count_b,
+ *   else -1 (which nk_qk_norm_rope skips).
+ *   slots: device int64 [B][T] or NULL = 64 * page + offset of that position,
+ *   else -1: the row of a per-token array of the caller's own beside the planes.
+ * A table row outside [0, C) or named before in the batch, a negative length, a
+ * count outside [0, T], F_b > 64 L, a mapped count outside [0, L] and a free
+ * count outside [0, M] are refused on the device: the row is left as it was and
+ * gets frontier 0 (NK_STATUS_FRONTIER; NK_STATUS_PAGE_RANGE for the free count,
+ * which then counts as 0 and takes nothing back).  Other arrays must not
+ * overlap.  Page ids are moved as they are, not looked at.
+ * The next call may read every output at once, nk_paged_append_decode_attention
+ * among them.  The pool's device must be current.
+ * Errors: NK_ERR_INVALID_ARG, NK_ERR_SHAPE (B in [1, C], T >= 0, B * T <= 2^30),
+ * NK_ERR_CUDA. */
+int nk_pages_grow(const nk_pool* pool, int32_t* block_tables, const int32_t* table_rows,
+                  const int32_t* committed, const int32_t* counts, const int32_t* keep,
+                  const int32_t* mapped, int32_t* mapped_out, int32_t* free_pages,
+                  const int32_t* free_count, int32_t* free_count_out, int32_t B, int32_t T,
+                  int32_t* frontiers, int32_t* positions, int64_t* slots, void* stream);
 
 /* Size of the static device scratch of nk_paged_decode_attention_noalloc. */
 #define NK_NOALLOC_SCRATCH_BYTES (32u << 20)

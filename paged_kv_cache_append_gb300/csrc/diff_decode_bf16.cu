@@ -1,0 +1,10 @@
+// diff_decode_bf16.cu -- differential decode instantiations of the BF16 profile.
+#include "diff_decode.cuh"
+
+namespace nk {
+
+cudaError_t diff_decode_bf16(const nk_pool* p, int layer, const DiffDecodeArgs* a, int rows, int* per_sm, cudaStream_t s) {
+  return diff_decode_dispatch<KIND_BF16, KIND_BF16>(p, layer, a, rows, per_sm, s);
+}
+
+}  // namespace nk

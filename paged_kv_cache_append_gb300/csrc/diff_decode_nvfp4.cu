@@ -1,0 +1,10 @@
+// diff_decode_nvfp4.cu -- differential decode instantiations of the NVFP4-G16 profile.
+#include "diff_decode.cuh"
+
+namespace nk {
+
+cudaError_t diff_decode_nvfp4(const nk_pool* p, int layer, const DiffDecodeArgs* a, int rows, int* per_sm, cudaStream_t s) {
+  return diff_decode_dispatch<KIND_NVFP4, KIND_NVFP4>(p, layer, a, rows, per_sm, s);
+}
+
+}  // namespace nk

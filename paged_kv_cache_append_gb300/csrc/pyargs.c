@@ -20,10 +20,18 @@ static struct {
                 const int32_t*, int32_t, int32_t, float, void*, float*, int64_t, void*, size_t, void*);
   int (*verify)(const float*, int64_t, const float*, int64_t, const int32_t*, const int32_t*, const float*,
                 const int32_t*, int32_t, int32_t, int32_t, int32_t*, int32_t*, int32_t*, void*);
+  int (*diff_decode)(const void*, int32_t, const nk_pool*, int32_t, const int32_t*, const int32_t*, const int32_t*,
+                     int32_t, int32_t, float, const nk_diff*, void*, float*, void*, size_t, void*);
+  int (*diff_prefill)(const void*, int32_t, const nk_pool*, int32_t, const int32_t*, const int32_t*, const int32_t*,
+                      const int32_t*, int32_t, int32_t, float, const nk_diff*, void*, float*, void*, size_t, void*);
+  int (*residual_norm)(const nk_block_norm*, int32_t, int32_t, const void*, int64_t, const void*, int64_t, const void*,
+                       int64_t, void*, int64_t, void*, int64_t, void*);
+  int (*grow)(const nk_pool*, int32_t*, const int32_t*, const int32_t*, const int32_t*, const int32_t*, const int32_t*,
+              int32_t*, int32_t*, const int32_t*, int32_t*, int32_t, int32_t, int32_t*, int32_t*, int64_t*, void*);
 } lib;
 
 static PyObject *n_shape, *n_dtype, *n_stride, *n_get_device, *n_data_ptr, *n_element_size;
-static PyObject *t_bf16, *t_f32, *t_i32;
+static PyObject *t_bf16, *t_f32, *t_i32, *t_i64;
 
 typedef struct {
   int nd;
@@ -67,6 +75,7 @@ static int look(PyObject* x, const char* name, PyObject* type, long dev, Tensor*
   Py_DECREF(dtype); /* dtypes are objects for the life of the process */
   if (type && dtype != type) return refuse(name, type == t_bf16  ? "expected a bf16 tensor"
                                          : type == t_f32 ? "expected a float32 tensor"
+                                         : type == t_i64 ? "expected an int64 tensor"
                                                          : "expected an int32 tensor", x);
   long long on, ptr;
   if (!long_of(PyObject_CallMethodNoArgs(x, n_get_device), &on)) return 0;
@@ -309,19 +318,162 @@ static PyObject* verify(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(rc);
 }
 
-/* (the four entry points' addresses, torch.bfloat16, torch.float32, torch.int32) */
+/* (prefill, pool address, D, C, L, layer, q, tables, table_rows, frontiers or prefix_len, None or chunk_len, scale,
+ *  diff address, its heads, tokens (0: any) and norm size (0: any), out, lse, workspace, device, stream) */
+static PyObject* diff(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Tensor q, t, r, f, c, o, l;
+  void* ws;
+  size_t bytes = 0;
+  if (!want(n, 21)) return NULL;
+  const int prefill = PyObject_IsTrue(a[0]);
+  if (prefill < 0) return NULL;
+  const int64_t D = PyLong_AsLong(a[2]);
+  const int64_t table[2] = {PyLong_AsLong(a[3]), PyLong_AsLong(a[4])};
+  const long layer = PyLong_AsLong(a[5]), dev = PyLong_AsLong(a[19]);
+  const int64_t heads = PyLong_AsLongLong(a[13]), tokens = PyLong_AsLongLong(a[14]), width = PyLong_AsLongLong(a[15]);
+  if (PyErr_Occurred()) return NULL;
+  if (!look(a[6], "q", t_bf16, dev, &q)) return NULL;
+  if (q.nd != 4 || q.size[3] != D || q.size[2] % 2)
+    return refuse("q", "expected [B, T, an even number of query heads, head_dim] of the pool", a[6]), NULL;
+  for (int i = 0; i < 3; ++i)
+    if (q.size[i] > INT32_MAX) return refuse("q", "expected smaller sizes", a[6]), NULL;
+  if (heads != q.size[2] / 2 || (tokens && tokens != q.size[0] * q.size[1]) || (width && width != 2 * D))
+    return refuse("q", "expected the heads, tokens and head_dim of lam and the norm weight", a[6]), NULL;
+  const int64_t out[4] = {q.size[0], q.size[1], q.size[2] / 2, 2 * D};
+  if (!plain(a[6], "q", t_bf16, dev, 4, q.size, &q) || !plain(a[7], "tables", t_i32, dev, 2, table, &t) ||
+      !plain(a[8], "table_rows", t_i32, dev, 1, q.size, &r) ||
+      !plain(a[9], prefill ? "prefix_len" : "frontiers", t_i32, dev, 1, q.size, &f) ||
+      (prefill && !plain(a[10], "chunk_len", t_i32, dev, 1, q.size, &c)) ||
+      !plain(a[16], "out", t_bf16, dev, 4, out, &o) || !plain(a[17], "lse", t_f32, dev, 3, q.size, &l))
+    return NULL;
+  const double scale = PyFloat_AsDouble(a[11]);
+  nk_pool* pool = ADDRESS(a[1]);
+  const nk_diff* d = ADDRESS(a[12]);
+  void* stream = ADDRESS(a[20]);
+  if (PyErr_Occurred() || !scratch(a[18], dev, &ws, &bytes)) return NULL;
+  int rc;
+  if (prefill) {
+    CALL(rc, lib.diff_prefill(q.ptr, (int32_t)q.size[2], pool, layer32(layer), t.ptr, r.ptr, f.ptr, c.ptr,
+                              (int32_t)q.size[0], (int32_t)q.size[1], (float)scale, d, o.ptr, l.ptr, ws, bytes, stream))
+  } else {
+    CALL(rc, lib.diff_decode(q.ptr, (int32_t)q.size[2], pool, layer32(layer), t.ptr, r.ptr, f.ptr, (int32_t)q.size[0],
+                             (int32_t)q.size[1], (float)scale, d, o.ptr, l.ptr, ws, bytes, stream))
+  }
+  return PyLong_FromLong(rc);
+}
+
+/* Rows [N, dim] or [B, T, dim] with a unit last stride and tokens one stride
+ * apart; *tokens and *stride are theirs. */
+static int flat_rows(PyObject* x, const char* name, PyObject* type, long dev, Tensor* t, int64_t* tokens,
+                     int64_t* stride) {
+  if (!look(x, name, type, dev, t)) return 0;
+  const int n = t->nd;
+  if (n < 2 || n > 3 || (t->stride[n - 1] != 1 && t->size[n - 1] > 1))
+    return refuse(name, "expected [..., dim] of two or three dimensions with a unit last stride", x);
+  *tokens = n == 2 ? t->size[0] : t->size[0] * t->size[1];
+  *stride = t->stride[n - 2];
+  if (n == 3 && t->size[0] > 1) {
+    if (t->size[1] == 1) *stride = t->stride[0];
+    else if (t->stride[0] != t->size[1] * *stride) return refuse(name, "expected tokens one stride apart", x);
+  }
+  if (*tokens == 1) *stride = 0; /* the stride of a dimension of size 1 says nothing */
+  return 1;
+}
+
+/* (norm address, weights' dim or 0, y or None, residual, gate or None, x_out or None, residual_out, fp32 residual,
+ *  device, stream) */
+static PyObject* residual_norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Tensor y, r, g, x, o;
+  int64_t N, m, ys = 0, rs = 0, gs = 0, xs = 0, os = 0;
+  if (!want(n, 10)) return NULL;
+  const long dim = PyLong_AsLong(a[1]), dev = PyLong_AsLong(a[8]);
+  const int wide = PyObject_IsTrue(a[7]);
+  if (PyErr_Occurred()) return NULL;
+  PyObject* type = wide ? t_f32 : t_bf16;
+  if (!flat_rows(a[3], "residual", type, dev, &r, &N, &rs)) return NULL;
+  const int D = r.nd - 1;
+  if (dim && dim != r.size[D]) return refuse("residual", "expected the dim of the norm weights", a[3]), NULL;
+  y.ptr = g.ptr = x.ptr = NULL;
+  if (!NONE(a[2])) {
+    if (!flat_rows(a[2], "y", t_bf16, dev, &y, &m, &ys)) return NULL;
+    if (!same_size(&y, &r, r.nd)) return refuse("y", "expected the sizes of residual", a[2]), NULL;
+  }
+  if (!NONE(a[4])) {
+    if (!look(a[4], "gate", t_bf16, dev, &g)) return NULL;
+    if (g.nd == 1) {
+      if (!plain(a[4], "gate", t_bf16, dev, 1, &r.size[D], &g)) return NULL;
+    } else {
+      if (!flat_rows(a[4], "gate", t_bf16, dev, &g, &m, &gs)) return NULL;
+      if (!same_size(&g, &r, r.nd)) return refuse("gate", "expected the sizes of residual or [dim]", a[4]), NULL;
+    }
+  }
+  if (!NONE(a[5])) {
+    if (!flat_rows(a[5], "out", t_bf16, dev, &x, &m, &xs)) return NULL;
+    if (!same_size(&x, &r, r.nd)) return refuse("out", "expected the sizes of residual", a[5]), NULL;
+  }
+  if (!flat_rows(a[6], "residual_out", type, dev, &o, &m, &os)) return NULL;
+  if (!same_size(&o, &r, r.nd)) return refuse("residual_out", "expected the sizes of residual", a[6]), NULL;
+  const nk_block_norm* norm = ADDRESS(a[0]);
+  void* stream = ADDRESS(a[9]);
+  if (PyErr_Occurred()) return NULL;
+  if (N > INT32_MAX || r.size[D] > INT32_MAX) return refuse("residual", "expected smaller sizes", a[3]), NULL;
+  int rc;
+  CALL(rc, lib.residual_norm(norm, (int32_t)r.size[D], (int32_t)N, y.ptr, ys, g.ptr, gs, r.ptr, rs, o.ptr, os, x.ptr, xs,
+                             stream))
+  return PyLong_FromLong(rc);
+}
+
+/* (pool address, C, L, M, T, tables, table_rows, committed, counts or None, keep or None, mapped, mapped_out,
+ *  free_pages, free_count, free_count_out, frontiers, positions or None, slots or None, device, stream) */
+static PyObject* grow(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Tensor t, r, c, k, p, m, mo, fp, fc, fo, f, pos, slot;
+  if (!want(n, 20)) return NULL;
+  const int64_t C = PyLong_AsLong(a[1]), M = PyLong_AsLong(a[3]), T = PyLong_AsLong(a[4]), one = 1;
+  const int64_t table[2] = {C, PyLong_AsLong(a[2])};
+  const long dev = PyLong_AsLong(a[18]);
+  if (PyErr_Occurred()) return NULL;
+  if (!look(a[7], "committed", t_i32, dev, &c)) return NULL;
+  if (c.nd != 1 || c.size[0] > INT32_MAX) return refuse("committed", "expected [B]", a[7]), NULL;
+  const int64_t bt[2] = {c.size[0], T};
+  k.ptr = p.ptr = pos.ptr = slot.ptr = NULL;
+  if (!plain(a[7], "committed", t_i32, dev, 1, bt, &c) || !plain(a[5], "tables", t_i32, dev, 2, table, &t) ||
+      !plain(a[6], "table_rows", t_i32, dev, 1, bt, &r) ||
+      (!NONE(a[8]) && !plain(a[8], "counts", t_i32, dev, 1, bt, &k)) ||
+      (!NONE(a[9]) && !plain(a[9], "keep", t_i32, dev, 1, table, &p)) ||
+      !plain(a[10], "mapped", t_i32, dev, 1, table, &m) || !plain(a[11], "mapped_out", t_i32, dev, 1, table, &mo) ||
+      !plain(a[12], "free_pages", t_i32, dev, 1, &M, &fp) || !plain(a[13], "free_count", t_i32, dev, 1, &one, &fc) ||
+      !plain(a[14], "free_count_out", t_i32, dev, 1, &one, &fo) ||
+      !plain(a[15], "frontiers", t_i32, dev, 1, bt, &f) ||
+      (!NONE(a[16]) && !plain(a[16], "positions", t_i32, dev, 2, bt, &pos)) ||
+      (!NONE(a[17]) && !plain(a[17], "slots", t_i64, dev, 2, bt, &slot)))
+    return NULL;
+  nk_pool* pool = ADDRESS(a[0]);
+  void* stream = ADDRESS(a[19]);
+  if (PyErr_Occurred()) return NULL;
+  int rc;
+  CALL(rc, lib.grow(pool, t.ptr, r.ptr, c.ptr, k.ptr, p.ptr, m.ptr, mo.ptr, fp.ptr, fc.ptr, fo.ptr, (int32_t)c.size[0],
+                    T < 0 || T > INT32_MAX ? -1 : (int32_t)T, f.ptr, pos.ptr, slot.ptr, stream))
+  return PyLong_FromLong(rc);
+}
+
+/* (the eight entry points' addresses, torch.bfloat16, torch.float32, torch.int32, torch.int64) */
 static PyObject* init(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  if (!want(n, 7)) return NULL;
-  void* f[4];
-  for (int i = 0; i < 4; ++i) f[i] = PyLong_AsVoidPtr(a[i]);
+  if (!want(n, 12)) return NULL;
+  void* f[8];
+  for (int i = 0; i < 8; ++i) f[i] = PyLong_AsVoidPtr(a[i]);
   if (PyErr_Occurred()) return NULL;
   *(void**)&lib.norm_rope = f[0];
   *(void**)&lib.append_rope = f[1];
   *(void**)&lib.shared = f[2];
   *(void**)&lib.verify = f[3];
-  t_bf16 = Py_NewRef(a[4]);
-  t_f32 = Py_NewRef(a[5]);
-  t_i32 = Py_NewRef(a[6]);
+  *(void**)&lib.diff_decode = f[4];
+  *(void**)&lib.diff_prefill = f[5];
+  *(void**)&lib.residual_norm = f[6];
+  *(void**)&lib.grow = f[7];
+  t_bf16 = Py_NewRef(a[8]);
+  t_f32 = Py_NewRef(a[9]);
+  t_i32 = Py_NewRef(a[10]);
+  t_i64 = Py_NewRef(a[11]);
   Py_RETURN_NONE;
 }
 
@@ -331,6 +483,9 @@ static PyMethodDef methods[] = {
     {"append_rope", (PyCFunction)(void (*)(void))append_rope, METH_FASTCALL, NULL},
     {"shared_decode", (PyCFunction)(void (*)(void))shared_decode, METH_FASTCALL, NULL},
     {"verify", (PyCFunction)(void (*)(void))verify, METH_FASTCALL, NULL},
+    {"diff", (PyCFunction)(void (*)(void))diff, METH_FASTCALL, NULL},
+    {"residual_norm", (PyCFunction)(void (*)(void))residual_norm, METH_FASTCALL, NULL},
+    {"grow", (PyCFunction)(void (*)(void))grow, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pyargs", NULL, -1, methods, NULL, NULL, NULL, NULL};

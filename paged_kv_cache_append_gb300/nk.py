@@ -25,7 +25,7 @@ NK_OK = 0
 ERRORS = {-1: "NK_ERR_INVALID_ARG", -2: "NK_ERR_SHAPE", -3: "NK_ERR_RANGE",
           -4: "NK_ERR_UNSUPPORTED", -5: "NK_ERR_ALIGN", -6: "NK_ERR_CUDA", -7: "NK_ERR_WORKSPACE"}
 STATUS_PAGE_RANGE, STATUS_FRONTIER, STATUS_TIMEOUT = 1, 2, 4
-STATUS_TOKEN_RANGE, STATUS_PREFIX = 8, 16
+STATUS_TOKEN_RANGE, STATUS_PREFIX, STATUS_PAGES = 8, 16, 32
 PROFILES = {"bf16": 0, "int8_g64": 1, "fp8_row": 2, "nvfp4_g16": 3, "k8v4": 4}
 POOL_CHECK_BOUNDS = 1
 
@@ -38,7 +38,9 @@ SYMBOLS = ["nk_version", "nk_last_error", "nk_pool_plane_bytes", "nk_pool_capaci
            "nk_page_copy_columns", "nk_status_read", "nk_host_page_bytes", "nk_page_runs",
            "nk_pages_to_host", "nk_pages_from_host", "nk_selftest_bounded_wait",
            "nk_shared_decode_workspace_bytes", "nk_paged_shared_decode_attention", "nk_qk_norm_rope",
-           "nk_paged_kv_append_rope", "nk_verify_drafts"]
+           "nk_paged_kv_append_rope", "nk_verify_drafts", "nk_diff_decode_workspace_bytes",
+           "nk_paged_diff_decode_attention", "nk_diff_prefill_workspace_bytes", "nk_paged_diff_prefill_attention",
+           "nk_residual_norm", "nk_pages_grow"]
 
 
 class NkError(RuntimeError):
@@ -62,6 +64,19 @@ class RopeDesc(C.Structure):
     _fields_ = [("cos_sin", C.c_void_p), ("positions", C.c_int32), ("rotary_dim", C.c_int32),
                 ("layout", C.c_int32), ("eps", C.c_float), ("weight_offset", C.c_float),
                 ("reserved", C.c_int32), ("q_weight", C.c_void_p), ("k_weight", C.c_void_p)]
+
+
+class DiffDesc(C.Structure):
+    """nk_diff"""
+    _fields_ = [("lam", C.c_void_p), ("lambda_stride", C.c_int64), ("norm_weight", C.c_void_p), ("eps", C.c_float),
+                ("out_scale", C.c_float)]
+
+
+class BlockNormDesc(C.Structure):
+    """nk_block_norm"""
+    _fields_ = [("weight", C.c_void_p), ("post_weight", C.c_void_p), ("eps", C.c_float), ("weight_offset", C.c_float),
+                ("scale", C.c_float), ("residual_scale", C.c_float), ("sigmoid_gate", C.c_int32),
+                ("residual_fp32", C.c_int32)]
 
 
 _lib = None
@@ -109,6 +124,14 @@ def load(path: str | None = None) -> C.CDLL:
         "nk_paged_kv_append_rope": (C.c_int, [_P, _I, _P, _P, _P, _P, C.POINTER(RopeDesc), C.POINTER(Rows),
                                               C.POINTER(Rows), C.POINTER(Rows), _I, _P, _I, _I, _P]),
         "nk_verify_drafts": (C.c_int, [_P, _L, _P, _L, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
+        "nk_diff_decode_workspace_bytes": (C.c_int, [_P, _I, _I, _I, C.POINTER(_S)]),
+        "nk_paged_diff_decode_attention": (C.c_int, [_P, _I, _P, _I, _P, _P, _P, _I, _I, _F, C.POINTER(DiffDesc), _P,
+                                                     _P, _P, _S, _P]),
+        "nk_diff_prefill_workspace_bytes": (C.c_int, [_P, _I, _I, _I, C.POINTER(_S)]),
+        "nk_paged_diff_prefill_attention": (C.c_int, [_P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _F, C.POINTER(DiffDesc),
+                                                      _P, _P, _P, _S, _P]),
+        "nk_residual_norm": (C.c_int, [C.POINTER(BlockNormDesc), _I, _I, _P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _P]),
+        "nk_pages_grow": (C.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -261,6 +284,45 @@ def nk_verify_drafts(target, target_stride, draft, draft_stride, tokens, draft_l
                                    frontiers, B, K, V, accepted, out_tokens, frontiers_out, stream))
 
 
+def nk_diff_decode_workspace_bytes(pool, B, T, Hq) -> int:
+    n = _S()
+    _check(load().nk_diff_decode_workspace_bytes(pool, B, T, Hq, C.byref(n)))
+    return n.value
+
+
+def nk_paged_diff_decode_attention(q, Hq, pool, layer, block_tables, table_rows, frontiers, B, T, scale, diff, out,
+                                   lse, workspace, workspace_bytes, stream):
+    """diff: DiffDesc."""
+    _check(load().nk_paged_diff_decode_attention(q, Hq, pool, layer, block_tables, table_rows, frontiers, B, T, scale,
+                                                 diff, out, lse, workspace, workspace_bytes, stream))
+
+
+def nk_diff_prefill_workspace_bytes(pool, B, Tc, Hq) -> int:
+    n = _S()
+    _check(load().nk_diff_prefill_workspace_bytes(pool, B, Tc, Hq, C.byref(n)))
+    return n.value
+
+
+def nk_paged_diff_prefill_attention(q, Hq, pool, layer, block_tables, table_rows, prefix_len, chunk_len, B, Tc, scale,
+                                    diff, out, lse, workspace, workspace_bytes, stream):
+    """diff: DiffDesc."""
+    _check(load().nk_paged_diff_prefill_attention(q, Hq, pool, layer, block_tables, table_rows, prefix_len, chunk_len,
+                                                  B, Tc, scale, diff, out, lse, workspace, workspace_bytes, stream))
+
+
+def nk_residual_norm(norm, dim, N, y, y_stride, gate, gate_stride, residual, residual_stride, residual_out,
+                     residual_out_stride, x_out, x_stride, stream):
+    """norm: BlockNormDesc."""
+    _check(load().nk_residual_norm(norm, dim, N, y, y_stride, gate, gate_stride, residual, residual_stride, residual_out,
+                                   residual_out_stride, x_out, x_stride, stream))
+
+
+def nk_pages_grow(pool, block_tables, table_rows, committed, counts, keep, mapped, mapped_out, free_pages, free_count,
+                  free_count_out, B, T, frontiers, positions, slots, stream):
+    _check(load().nk_pages_grow(pool, block_tables, table_rows, committed, counts, keep, mapped, mapped_out, free_pages,
+                                free_count, free_count_out, B, T, frontiers, positions, slots, stream))
+
+
 def nk_page_copy_columns(pool, src, dst, ncols, stream):
     _check(load().nk_page_copy_columns(pool, src, dst, ncols, stream))
 
@@ -330,9 +392,10 @@ def _args():
         except ImportError as e:
             raise RuntimeError("_pyargs is not built; run paged_kv_cache_append_gb300.build.build()") from e
         lib = load()
-        m.init(*(C.cast(f, C.c_void_p).value for f in (lib.nk_qk_norm_rope, lib.nk_paged_kv_append_rope,
-                                                       lib.nk_paged_shared_decode_attention, lib.nk_verify_drafts)),
-               torch.bfloat16, torch.float32, torch.int32)
+        m.init(*(C.cast(f, C.c_void_p).value for f in (
+            lib.nk_qk_norm_rope, lib.nk_paged_kv_append_rope, lib.nk_paged_shared_decode_attention, lib.nk_verify_drafts,
+            lib.nk_paged_diff_decode_attention, lib.nk_paged_diff_prefill_attention, lib.nk_residual_norm,
+            lib.nk_pages_grow)), torch.bfloat16, torch.float32, torch.int32, torch.int64)
         _pyargs = m
     return _pyargs
 
@@ -419,6 +482,95 @@ def verify_drafts(target, tokens, uniforms, draft=None, draft_len=None, frontier
     _check((_pyargs or _args()).verify(target, draft, tokens, draft_len, uniforms, frontiers, accepted, out, after, dev,
                                        at))
     return accepted, out, after
+
+
+class Diff:
+    """What a differential attention has besides queries and pages (nk.h, nk_diff).
+
+    ``lam`` is fp32: [heads] (the same for every token) or [..., heads], a row
+    for each token of the call; ``norm_weight`` bf16 [2 D] or None (no norm).
+    Keeps its tensors alive.
+    """
+
+    def __init__(self, lam, norm_weight=None, eps: float = 1e-5, out_scale: float = 1.0):
+        import torch
+        if lam.dtype != torch.float32 or not lam.is_cuda or not lam.is_contiguous() or lam.dim() < 1 \
+                or lam.numel() < 1:
+            raise ValueError("lam must be a contiguous fp32 CUDA tensor [..., heads]")
+        if norm_weight is not None and (norm_weight.dtype != torch.bfloat16 or norm_weight.device != lam.device
+                                        or norm_weight.dim() != 1 or not norm_weight.is_contiguous()):
+            raise ValueError("norm_weight must be a contiguous bf16 vector on lam's device")
+        self.lam, self.norm_weight = lam, norm_weight
+        self.device, self.heads = lam.get_device(), lam.shape[-1]
+        self.tokens = 0 if lam.dim() == 1 else lam.numel() // self.heads   # 0: the same for every token
+        self.width = 0 if norm_weight is None else norm_weight.numel()     # 0: any
+        self.desc = DiffDesc(_ptr(lam), self.heads if lam.dim() > 1 else 0, _ptr(norm_weight), eps, out_scale)
+        self.address = C.addressof(self.desc)
+
+    @classmethod
+    def from_vectors(cls, q1, k1, q2, k2, lambda_init: float, heads: int, norm_weight=None, eps: float = 1e-5):
+        """lambda = exp(q1 . k1) - exp(q2 . k2) + lambda_init from learned vectors [D] or [heads, D], once per
+        model; the output is scaled by 1 - lambda_init."""
+        import torch
+        dot = [(a.double() * b.double()).sum(-1).exp() for a, b in ((q1, k1), (q2, k2))]
+        lam = (dot[0] - dot[1] + lambda_init).to(torch.float32).expand(heads).contiguous()
+        return cls(lam, norm_weight, eps, 1.0 - lambda_init)
+
+
+class ResidualNorm:
+    """Norms, gate and scales around a block (nk.h, nk_block_norm).
+
+    ``weight`` and ``post_weight`` are bf16 [dim]; without ``weight`` only the
+    residual is updated.  Keeps its tensors alive.
+    """
+
+    def __init__(self, weight, post_weight=None, eps: float = 1e-6, scale: float = 1.0, residual_scale: float = 1.0,
+                 weight_offset: float = 0.0, sigmoid_gate: bool = False):
+        import torch
+        given = [w for w in (weight, post_weight) if w is not None]
+        for w in given:
+            if w.dtype != torch.bfloat16 or not w.is_cuda or w.device != given[0].device or w.dim() != 1 \
+                    or not w.is_contiguous() or w.numel() != given[0].numel():
+                raise ValueError("norm weights must be contiguous bf16 CUDA vectors of one size on one device")
+        self.weight, self.post_weight = weight, post_weight
+        self.dim = given[0].numel() if given else 0                  # 0: any
+        self.device = given[0].get_device() if given else None      # None: any
+        desc = (_ptr(weight), _ptr(post_weight), eps, weight_offset, scale, residual_scale, int(sigmoid_gate))
+        self.descs = BlockNormDesc(*desc, 0), BlockNormDesc(*desc, 1)   # a bf16 residual, an fp32 one
+        self.addresses = tuple(C.addressof(d) for d in self.descs)
+
+
+def residual_norm(y, residual, norm: ResidualNorm, gate=None, out=None, residual_out=None, stream=None):
+    """h = residual_scale * residual + scale * act(gate) * post(y) and x, its norm (nk.h, nk_residual_norm).
+
+    y bf16 [N, dim] or [B, T, dim] or None; residual of the same sizes, bf16 or
+    fp32; gate bf16 of the same sizes or [dim], or None.  Rows may be padded (any
+    row stride, one for all tokens).  Returns (x, h): new contiguous tensors
+    unless given (residual_out may be residual itself, out may be y); x is None
+    without a weight.
+    """
+    import torch
+    dev = residual.get_device()
+    if dev < 0:
+        raise ValueError("residual: expected a CUDA tensor")
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return residual_norm(y, residual, norm, gate, out, residual_out, stream)
+    if norm.device is not None and norm.device != dev:
+        raise ValueError("the norm weights are on another device than the residual")
+    if norm.weight is None and out is not None:
+        raise ValueError("out: there is no norm weight to make it with")
+    at = _handle(stream, dev)
+    if residual_out is None or (out is None and norm.weight is not None):
+        with _on(stream):
+            if residual_out is None:
+                residual_out = torch.empty(residual.shape, dtype=residual.dtype, device=residual.device)
+            if out is None and norm.weight is not None:
+                out = torch.empty(residual.shape, dtype=torch.bfloat16, device=residual.device)
+    wide = residual.dtype == torch.float32
+    _check((_pyargs or _args()).residual_norm(norm.addresses[wide], norm.dim, y, residual, gate, out, residual_out,
+                                              wide, dev, at))
+    return out, residual_out
 
 
 class Pool:
@@ -612,3 +764,101 @@ class Pool:
             self.handle, self.D, self.C, self.L, layer, q, tables, table_rows, frontiers, shared_pages, float(scale),
             out, lse, share_from, ws, dev, at))
         return out, lse
+
+    def diff_decode_workspace(self, B, T, Hq):
+        """A workspace for ``diff_decode`` (one per stream or captured graph that may overlap others)."""
+        import torch
+        n = nk_diff_decode_workspace_bytes(self.handle, B, T, Hq)
+        return torch.empty(n, dtype=torch.uint8, device=self.planes[0][0].device)
+
+    def diff_prefill_workspace(self, B, Tc, Hq):
+        """A workspace for ``diff_prefill`` (one per stream or captured graph that may overlap others)."""
+        import torch
+        n = nk_diff_prefill_workspace_bytes(self.handle, B, Tc, Hq)
+        return torch.empty(n, dtype=torch.uint8, device=self.planes[0][0].device)
+
+    def diff_decode(self, layer, q, tables, table_rows, frontiers, scale, diff: Diff, out=None, lse=None,
+                    workspace=None, stream=None):
+        """Differential attention of the T newest tokens of every row (nk.h,
+        nk_paged_diff_decode_attention): q [B, T, Hq, D], head i's maps in query
+        heads 2i and 2i + 1; returns out [B, T, Hq / 2, 2 D] and lse [B, T, Hq].
+        Without ``workspace`` one is allocated for this call."""
+        return self._diff(False, layer, q, tables, table_rows, frontiers, None, scale, diff, out, lse, workspace, stream)
+
+    def diff_prefill(self, layer, q, tables, table_rows, prefix_len, chunk_len, scale, diff: Diff, out=None, lse=None,
+                     workspace=None, stream=None):
+        """Differential attention of prompt chunks (nk.h,
+        nk_paged_diff_prefill_attention): q [B, Tc, Hq, D] as in ``diff_decode``;
+        rows behind chunk_len are not written (0 and -inf in tensors that this
+        call makes)."""
+        return self._diff(True, layer, q, tables, table_rows, prefix_len, chunk_len, scale, diff, out, lse, workspace,
+                          stream)
+
+    def _diff(self, prefill, layer, q, tables, table_rows, lengths, chunk_len, scale, diff, out, lse, workspace, stream):
+        import torch
+        dev = self.device
+        if torch.cuda.current_device() != dev:
+            with torch.cuda.device(dev):
+                return self._diff(prefill, layer, q, tables, table_rows, lengths, chunk_len, scale, diff, out, lse,
+                                  workspace, stream)
+        if diff.device != dev:
+            raise ValueError("lam is on another device than the pool")
+        at = _handle(stream, dev)
+        ws = workspace
+        if out is None or lse is None or ws is None:
+            if len(q.shape) != 4 or q.shape[2] % 2:
+                raise ValueError("q: expected [B, T, an even number of query heads, head_dim]")
+            B, T, Hq, D = q.shape
+            with _on(stream):
+                if out is None:
+                    make = torch.zeros if prefill else torch.empty
+                    out = make((B, T, Hq // 2, 2 * D), dtype=torch.bfloat16, device=q.device)
+                if lse is None:
+                    lse = torch.full((B, T, Hq), float("-inf"), dtype=torch.float32, device=q.device)
+                if ws is None:
+                    ws = (self.diff_prefill_workspace if prefill else self.diff_decode_workspace)(B, T, Hq)
+        _check((_pyargs or _args()).diff(
+            prefill, self.handle, self.D, self.C, self.L, layer, q, tables, table_rows, lengths, chunk_len, float(scale),
+            diff.address, diff.heads, diff.tokens, diff.width, out, lse, ws, dev, at))
+        return out, lse
+
+    def free_pages(self):
+        """The state of an empty pool for ``grow``: tables [C, L] (-1), mapped [C] (0), the stack of free pages [M]
+        (all, page 0 on top) and their number [1], int32."""
+        import torch
+        kw = dict(dtype=torch.int32, device=self.planes[0][0].device)
+        return (torch.full((self.C, self.L), -1, **kw), torch.zeros(self.C, **kw),
+                torch.arange(self.M - 1, -1, -1, **kw), torch.full((1,), self.M, **kw))
+
+    def grow(self, tables, table_rows, committed, mapped, free_pages, free_count, T, counts=None, keep=None,
+             mapped_out=None, free_count_out=None, frontiers=None, positions=None, slots=None, stream=None):
+        """Brings every row of the batch to the pages of its committed + count tokens (nk.h, nk_pages_grow).
+
+        tables [C, L], mapped [C], free_pages [M] and free_count [1] are updated
+        in place (mapped_out, free_count_out: written instead of mapped and
+        free_count); committed, counts (None: T each) [B]; keep [C] or None.
+        Returns (frontiers [B], positions [B, T], slots [B, T] int64): new tensors
+        unless given; positions=False, slots=False: not made (None).
+        """
+        import torch
+        dev = self.device
+        if torch.cuda.current_device() != dev:
+            with torch.cuda.device(dev):
+                return self.grow(tables, table_rows, committed, mapped, free_pages, free_count, T, counts, keep,
+                                 mapped_out, free_count_out, frontiers, positions, slots, stream)
+        at = _handle(stream, dev)
+        if frontiers is None or positions is None or slots is None:
+            B = committed.shape[0]
+            with _on(stream):
+                if frontiers is None:
+                    frontiers = torch.empty((B,), dtype=torch.int32, device=committed.device)
+                if positions is None:
+                    positions = torch.empty((B, T), dtype=torch.int32, device=committed.device)
+                if slots is None:
+                    slots = torch.empty((B, T), dtype=torch.int64, device=committed.device)
+        positions, slots = (None if x is False else x for x in (positions, slots))
+        _check((_pyargs or _args()).grow(
+            self.handle, self.C, self.L, self.M, T, tables, table_rows, committed, counts, keep, mapped,
+            mapped if mapped_out is None else mapped_out, free_pages, free_count,
+            free_count if free_count_out is None else free_count_out, frontiers, positions, slots, dev, at))
+        return frontiers, positions, slots
