@@ -506,7 +506,7 @@ int nk_diff_prefill_workspace_bytes(const nk_pool* pool, int32_t B, int32_t Tc, 
  *   workspace: nk_diff_prefill_workspace_bytes bytes, no initialisation needed;
  *   two calls that share a workspace must not overlap.
  * A NaN or an infinity among the values of a chunk may reach all of its outputs.
- * Two launches: on the tensor cores (csrc/diff_prefill.cu, csrc/diff_qprefill.cu)
+ * Two launches: on the tensor cores (csrc/diff_tile.cuh)
  * and for the join.  Softmax weights and values are rounded as in
  * nk_paged_prefill_attention.
  * The pool's device must be current.

@@ -44,6 +44,43 @@ __device__ __forceinline__ uint2 diff_finish(const float (&o)[4], float f, const
   return make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
 }
 
+// Pages per split of a decode: the smallest count (at least ceil(maxp /
+// max_splits)) whose splits, max(1, ceil(N_b / c)) for every row, add up to at
+// most `ctas`.
+__device__ __forceinline__ int diff_chunk(const int* F, int B, int ctas, int max_splits) {
+  int total = 0, maxp = 0;
+  for (int b = 0; b < B; ++b) {
+    const int n = (F[b] + 63) >> 6;
+    total += n;
+    maxp = max(maxp, n);
+  }
+  const int least = max(1, (maxp + max_splits - 1) / max_splits);
+  const int room = max(ctas - B, 1);
+  int hi = max((total + room - 1) / room, least);  // always fits: sum ceil(N_b / c) <= total / c + B
+  int lo = min(max(least, (total + ctas - 1) / ctas), hi);
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    int n = 0;
+    for (int b = 0; b < B; ++b) n += max(1, (((F[b] + 63) >> 6) + mid - 1) / mid);
+    if (n <= ctas) hi = mid;
+    else lo = mid + 1;
+  }
+  return hi;
+}
+
+// Valid length of row b as the decode kernels take it (0: refused, no keys).
+__device__ __forceinline__ int diff_length(const int32_t* frontiers, const int32_t* table_rows, int b, int L, int C,
+                                           int* row_out, int* report) {
+  const int F = frontiers[b], row = table_rows[b];
+  const bool ok = F >= 0 && F <= L * 64 && row >= 0 && row < C;
+  if (!ok && report) set_status(report, NK_STATUS_FRONTIER);
+  *row_out = ok ? row : 0;
+  return ok ? F : 0;
+}
+
+// At most this many splits of a decoded row: bounds the join's work.
+constexpr int kDiffMaxSplits = 128;
+
 // Checks that decode and prefill share; fills `o`.
 int check_diff(const char* what, const void* q, int32_t Hq, const nk_pool* pool, int32_t layer, const int32_t* tables,
                const int32_t* table_rows, const int32_t* lengths, int32_t B, int32_t T, float scale, const nk_diff* diff,

@@ -1,5 +1,7 @@
-// diff_decode.cu -- host side of the differential decode: checks, plan, launch.
+// diff_decode.cu -- differential decode: the join of the splits, and the host side
+// (checks, plan, launches).
 #include "diff_decode.cuh"
+#include "diff_tile.cuh"
 
 namespace nk {
 
@@ -39,35 +41,157 @@ int check_diff(const char* what, const void* q, int32_t Hq, const nk_pool* pool,
   return NK_OK;
 }
 
+struct DiffJoinArgs {
+  const int32_t* table_rows;
+  const int32_t* frontiers;
+  const float2* ws_ml;  // [pair][ctas][2][RB]
+  const float* ws_o;    // [pair][ctas][2][RB][2 D]
+  int B, T, Hq, G, L, C, ctas, RB;
+  DiffOut o;
+};
+
+// ---- the join of the splits, the difference and the norm -------------------------------
+// One CTA per (row, token, head).  A thread owns 4 dims of one map and every
+// LANES-th split; the shares are added in a fixed order in shared memory.
+template <int D>
+__global__ void __launch_bounds__(512) diff_join_kernel(DiffJoinArgs a) {
+  constexpr int COLS = D;  // 2 maps x 2 D / 4
+  constexpr int LANES = 512 / COLS, EACH = kDiffMaxSplits / LANES, STEP = 8;
+  __shared__ int s_F[8], s_row[8];
+  __shared__ float s_w[2][kDiffMaxSplits];
+  __shared__ float4 s_acc[LANES][COLS];
+  __shared__ float s_sum[16];
+  __shared__ int s_any;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int head = blockIdx.x, bt = blockIdx.y, b = bt / a.T, t = bt % a.T;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (tid < a.B) s_F[tid] = diff_length(a.frontiers, a.table_rows, tid, a.L, a.C, &s_row[tid], nullptr);
+  __syncthreads();
+  const int chunk = diff_chunk(s_F, a.B, a.ctas, kDiffMaxSplits);
+  int at = 0, ns = 0;
+  for (int i = 0; i <= b; ++i) {
+    at += ns;
+    ns = max(1, (((s_F[i] + 63) >> 6) + chunk - 1) / chunk);
+  }
+  const int RB = a.RB, r = t * a.G + head % a.G;
+  const int64_t slot0 = static_cast<int64_t>(head / a.G) * a.ctas + at;
+  const int map = tid % COLS / (COLS / 2), d = tid % (COLS / 2) * 4, sub = tid / COLS;
+  const float* src = a.ws_o + ((slot0 * 2 + map) * RB + r) * (2 * D) + d;
+  const int64_t step = static_cast<int64_t>(2) * RB * 2 * D;
+  if (warp < 2) {  // weights of map `warp`
+    float2 ml[kDiffMaxSplits / 32];
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int k = 0; k < kDiffMaxSplits / 32; ++k) {
+      const int s = lane + 32 * k;
+      ml[k] = s < ns ? a.ws_ml[((slot0 + s) * 2 + warp) * RB + r] : make_float2(-INFINITY, 0.f);
+      M = fmaxf(M, ml[k].x);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+#pragma unroll
+    for (int k = 0; k < kDiffMaxSplits / 32; ++k) {
+      ml[k].x = ml[k].y == 0.f ? 0.f : ex2(ml[k].x - M);  // a split that saw no key weighs nothing
+      L += ml[k].x * ml[k].y;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    const bool none = L == 0.f;
+#pragma unroll
+    for (int k = 0; k < kDiffMaxSplits / 32; ++k)
+      if (lane + 32 * k < ns) s_w[warp][lane + 32 * k] = none ? 0.f : ml[k].x / L;
+    if (lane == 0) {
+      if (warp == 0) s_any = !none;
+      if (a.o.lse) a.o.lse[static_cast<int64_t>(bt) * a.Hq + 2 * head + warp] = none ? -INFINITY : (M + log2f(L)) * kDiffLn2;
+    }
+  }
+  __syncthreads();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < EACH && sub + k0 * LANES < ns; k0 += STEP) {
+    float4 v[STEP];
+#pragma unroll
+    for (int k = 0; k < STEP; ++k) {
+      const int s = sub + (k0 + k) * LANES;
+      v[k] = s < ns ? *reinterpret_cast<const float4*>(src + s * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < STEP; ++k) {
+      const int s = sub + (k0 + k) * LANES;
+      const float w = s < ns ? s_w[map][s] : 0.f;
+      acc.x = fmaf(w, v[k].x, acc.x);
+      acc.y = fmaf(w, v[k].y, acc.y);
+      acc.z = fmaf(w, v[k].z, acc.z);
+      acc.w = fmaf(w, v[k].w, acc.w);
+    }
+  }
+  s_acc[sub][tid % COLS] = acc;
+  __syncthreads();
+  float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+  if (tid < COLS / 2) {
+    const float lambda = a.o.lambda[bt * a.o.lambda_stride + head];
+    float x[2][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      float4 v = s_acc[0][m * (COLS / 2) + tid];
+#pragma unroll
+      for (int k = 1; k < LANES; ++k) {
+        const float4 y = s_acc[k][m * (COLS / 2) + tid];
+        v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+      }
+      x[m][0] = v.x, x[m][1] = v.y, x[m][2] = v.z, x[m][3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[i] = s_any ? fmaf(-lambda, x[1][i], x[0][i]) : 0.f;
+      sum = fmaf(o[i], o[i], sum);
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  if (tid < COLS / 2) {
+    sum = s_sum[0];
+#pragma unroll
+    for (int w = 1; w < COLS / 64; ++w) sum += s_sum[w];
+    const float f = a.o.w ? rsqrtf(sum / (2 * D) + a.o.eps) * a.o.out_scale : a.o.out_scale;
+    __nv_bfloat16* dst = a.o.out + (static_cast<int64_t>(bt) * (a.Hq / 2) + head) * (2 * D) + tid * 4;
+    *reinterpret_cast<uint2*>(dst) = diff_finish(o, f, a.o.w, tid * 4);
+  }
+}
+
 struct DiffPlan {
-  DiffDecodeFn fn;
-  int rows, blocks, ctas;
+  DiffDecodeFn fn;  // nullptr: the tensor-core tiles
+  int RB, ctas;
   size_t ml_bytes, bytes;
 };
 
-// Query rows of one pair go in blocks of 4, 8 or 16 (two maps of a block in one
-// CTA); more rows take several blocks, which read the same pages side by side.
+// Up to 8 query rows a map the warp-level kernel (4 or 8 rows of both maps in
+// one column tile or two), beyond that the 64-row tiles, one CTA per SM.
 static int diff_plan(const nk_pool* p, int B, int T, int Hq, DiffPlan* pl) {
   const int rc = check_diff_shape(p, B, T, Hq);
   if (rc) return rc;
   const int H = p->desc.num_kv_heads, D = p->desc.head_dim;
   const int64_t rows = static_cast<int64_t>(T) * (Hq / H);
   if (rows > 64) return fail(NK_ERR_UNSUPPORTED, "T * Hq / num_kv_heads must be <= 64");
-  switch (p->desc.profile) {
-    case NK_BF16: pl->fn = diff_decode_bf16; break;
-    case NK_INT8_G64: pl->fn = diff_decode_int8; break;
-    case NK_FP8_E4M3_ROW: pl->fn = diff_decode_fp8; break;
-    case NK_NVFP4_G16: pl->fn = diff_decode_nvfp4; break;
-    default: pl->fn = diff_decode_k8v4; break;
-  }
-  pl->rows = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
-  pl->blocks = static_cast<int>((rows + pl->rows - 1) / pl->rows);
+  pl->RB = rows <= 4 ? 4 : rows <= 8 ? 8 : 64;
+  pl->fn = nullptr;
   int per_sm = 1;
-  const cudaError_t e = pl->fn(p, 0, nullptr, pl->rows, &per_sm, nullptr);
-  if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
-  const int target = p->num_sms * per_sm / (H / 2 * pl->blocks);
+  if (pl->RB < 64) {
+    switch (p->desc.profile) {
+      case NK_BF16: pl->fn = diff_decode_bf16; break;
+      case NK_INT8_G64: pl->fn = diff_decode_int8; break;
+      case NK_FP8_E4M3_ROW: pl->fn = diff_decode_fp8; break;
+      case NK_NVFP4_G16: pl->fn = diff_decode_nvfp4; break;
+      default: pl->fn = diff_decode_k8v4; break;
+    }
+    const cudaError_t e = pl->fn(p, 0, nullptr, pl->RB == 4, &per_sm, nullptr);
+    if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
+  }
+  const int target = p->num_sms * per_sm / (H / 2);
   pl->ctas = target > B ? target : B;
-  const size_t slots = static_cast<size_t>(H / 2) * pl->blocks * pl->ctas * 2 * pl->rows;
+  const size_t slots = static_cast<size_t>(H / 2) * pl->ctas * 2 * pl->RB;
   pl->ml_bytes = (slots * sizeof(float2) + 255) / 256 * 256;
   pl->bytes = pl->ml_bytes + slots * 2 * D * sizeof(float);
   return NK_OK;
@@ -93,38 +217,35 @@ extern "C" int nk_paged_diff_decode_attention(const void* q, int32_t Hq, const n
                                               const nk_diff* diff, void* out, float* lse, void* workspace,
                                               size_t workspace_bytes, void* stream) {
   clear_error();
-  DiffDecodeArgs a;
+  DiffJoinArgs j;
   int rc = check_diff("nk_paged_diff_decode_attention", q, Hq, pool, layer, block_tables, table_rows, frontiers, B, T,
-                      softmax_scale, diff, out, lse, &a.o);
+                      softmax_scale, diff, out, lse, &j.o);
   if (rc) return rc;
   DiffPlan pl;
   if ((rc = diff_plan(pool, B, T, Hq, &pl))) return rc;
   if (!workspace || workspace_bytes < pl.bytes)
     return fail(NK_ERR_WORKSPACE, "workspace needs " + std::to_string(pl.bytes) + " bytes");
   if (!aligned16(workspace)) return fail(NK_ERR_ALIGN, "workspace must be 16-byte aligned");
-  const int np = pool->n_planes;
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.tables = block_tables;
-  a.table_rows = table_rows;
-  a.frontiers = frontiers;
-  a.ks = np == 4 ? static_cast<const uint8_t*>(pool->ptrs[layer * np + 2]) : nullptr;
-  a.vs = np == 4 ? static_cast<const uint8_t*>(pool->ptrs[layer * np + 3]) : nullptr;
-  a.ws_ml = static_cast<float2*>(workspace);
-  a.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.ml_bytes);
-  a.status = pool->status;
-  a.softmax_scale = softmax_scale;
-  a.B = B;
-  a.T = T;
-  a.Hq = Hq;
-  a.H = pool->desc.num_kv_heads;
-  a.G = Hq / a.H;
-  a.L = pool->L;
-  a.M = pool->M;
-  a.C = pool->desc.max_concurrency;
-  a.ctas = pl.ctas;
-  a.blocks = pl.blocks;
-  a.head_major = pool->desc.order == NK_HEAD_MAJOR;
-  const cudaError_t e = pl.fn(pool, layer, &a, pl.rows, nullptr, static_cast<cudaStream_t>(stream));
+  const DiffTileArgs t = [&] {
+    DiffTileArgs x = diff_tile_args(pool, layer, q, Hq, block_tables, table_rows, frontiers, B, T, softmax_scale,
+                                    workspace, pl.ml_bytes);
+    x.ctas = pl.ctas;
+    return x;
+  }();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (pl.fn) {
+    const DiffDecodeArgs a{t.q, t.tables, t.table_rows, t.lengths, t.ks, t.vs, t.ws_ml, t.ws_o, t.status, softmax_scale,
+                           t.B, t.T, t.Hq, t.H, t.G, t.L, t.M, t.C, t.ctas, t.head_major};
+    e = pl.fn(pool, layer, &a, pl.RB == 4, nullptr, s);
+  } else {
+    e = diff_tile_for(pool->desc.profile)(pool, layer, t, true, dim3(pl.ctas, t.H / 2), s);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
+  j = DiffJoinArgs{t.table_rows, t.lengths, t.ws_ml, t.ws_o, B, T, Hq, t.G, t.L, t.C, pl.ctas, pl.RB, j.o};
+  const dim3 grid(Hq / 2, B * T);
+  e = pool->desc.head_dim == 64 ? launch_pdl(diff_join_kernel<64>, grid, dim3(512), 0, s, j)
+                                : launch_pdl(diff_join_kernel<128>, grid, dim3(512), 0, s, j);
+  if (e != cudaSuccess) return cuda_fail(e, "differential decode join launch");
   return NK_OK;
 }

@@ -4,9 +4,9 @@
 //
 // For KV heads 2j, 2j + 1 (keys K1, K2; values V = [V1 V2]) and the query rows
 // of the heads that share them, o = softmax(Q1 K1^T) V - lambda softmax(Q2 K2^T) V.
-// A CTA owns one (row b, pair j, block of query rows, page range) and stages the
-// four code tiles of a page together.  Its eight consumer warps are four slabs of
-// 16 keys times two sides: the warp of side m
+// Up to 8 query rows a map (more go to diff_tile.cuh).  A CTA owns one (row b, pair
+// j, page range) and stages the four code tiles of a page together.  Its eight
+// consumer warps are four slabs of 16 keys times two sides: the warp of side m
 //   * computes S_m = K_m Q_m^T of its slab and the softmax of map m (its own
 //     running maximum, moved lazily as in decode.cuh),
 //   * hands P_m (and the rescale factors) to the other side's warp through
@@ -18,8 +18,7 @@
 // operand: map 1 in columns 0-3, map 2 in columns 4-7, half the MMAs and
 // accumulators.
 //
-// Partials of (map, query row) go to the workspace; diff_join_kernel, launched
-// right behind, joins the splits, takes the difference and norms it.
+// Partials of (map, query row) go to the workspace, for the join (diff_decode.cu).
 #pragma once
 
 #include "diff.cuh"
@@ -33,19 +32,14 @@ struct DiffDecodeArgs {
   const int32_t* frontiers;
   const uint8_t* ks;  // scale planes of the layer (nullptr for BF16)
   const uint8_t* vs;
-  float2* ws_ml;  // [pair][row block][ctas][2][RB] (m, l)
-  float* ws_o;    // [pair][row block][ctas][2][RB][2 D]
+  float2* ws_ml;  // [pair][ctas][2][RB] (m, l)
+  float* ws_o;    // [pair][ctas][2][RB][2 D]
   int* status;
   float softmax_scale;
   int B, T, Hq, H, G, L, M, C;
-  int ctas;    // CTAs (= partial slots) per (pair, row block)
-  int blocks;  // blocks of RB query rows
+  int ctas;  // CTAs (= partial slots) per pair
   int head_major;
-  DiffOut o;
 };
-
-// At most this many splits of a row: bounds the join's work.
-constexpr int kDiffMaxSplits = 128;
 
 constexpr int diff_align(int x, int a) { return (x + a - 1) / a * a; }
 
@@ -58,13 +52,12 @@ constexpr int diff_scale_bytes(int D) {
   return KIND == KIND_BF16 ? 0 : KIND == KIND_INT8 ? 2 * (D / 64) : KIND == KIND_FP8 ? 2 : D / 16;
 }
 
-template <int KK, int KV, int D, int NQT, bool PACK>
+template <int KK, int KV, int D, bool PACK>
 struct DiffCfg {
-  static_assert(!PACK || NQT == 1, "two maps of four rows fill one column tile");
   static constexpr int NW = 8, NCONS = 32 * NW, THREADS = NCONS + 32;
-  static constexpr int R = 8 * NQT;             // columns of one map's S
-  static constexpr int RB = PACK ? 4 : R;       // query rows of a block
-  static constexpr int NT = PACK ? 1 : 2 * NQT; // column tiles of P V
+  static constexpr int R = 8;             // columns of one map's S
+  static constexpr int RB = PACK ? 4 : R; // query rows of a partial
+  static constexpr int NT = PACK ? 1 : 2; // column tiles of P V
   static constexpr int KCB = diff_code_bytes<KK>(D), VCB = diff_code_bytes<KV>(D);
   static constexpr int KSB = diff_scale_bytes<KK>(D), VSB = diff_scale_bytes<KV>(D);
   static constexpr int K_RB = KCB < 128 ? KCB : 128, V_RB = VCB < 128 ? VCB : 128;
@@ -79,8 +72,7 @@ struct DiffCfg {
   // CTAs per SM: the accumulators and the tiles of a page decide
   static constexpr int MINB = OREGS > 64 || STAGE > 48 * 1024 ? 1 : 2;
   static constexpr int Q_PITCH = D * 2 + 32;
-  static constexpr bool Q_SMEM = D / 16 * NQT * 2 > 16;
-  static constexpr int XW = PARTS * NQT * 2 + NQT * 2 + 1;  // words a lane hands over
+  static constexpr int XW = PARTS * 2 + 3;  // words a lane hands over
   static constexpr int VW_BYTES = KV == KIND_BF16 ? 0 : 16 * D * 2;  // a warp's 16 keys of V as f16
   static constexpr int O_PITCH = 2 * D + 4;  // floats: rows of the combine in different banks
   static constexpr int COMB = 4 * 2 * RB * O_PITCH * 4;
@@ -97,38 +89,6 @@ struct DiffCfg {
   static constexpr int SMEM = OFF_BAR + 2 * NSTAGE * 8 + 32 * 4 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
-
-// Pages per split: the smallest count (at least ceil(maxp / kDiffMaxSplits))
-// whose splits, max(1, ceil(N_b / c)) for every row, add up to at most `ctas`.
-__device__ __forceinline__ int diff_chunk(const int* F, int B, int ctas) {
-  int total = 0, maxp = 0;
-  for (int b = 0; b < B; ++b) {
-    const int n = (F[b] + 63) >> 6;
-    total += n;
-    maxp = max(maxp, n);
-  }
-  const int least = max(1, (maxp + kDiffMaxSplits - 1) / kDiffMaxSplits);
-  const int room = max(ctas - B, 1);
-  int hi = max((total + room - 1) / room, least);  // always fits: sum ceil(N_b / c) <= total / c + B
-  int lo = min(max(least, (total + ctas - 1) / ctas), hi);
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    int n = 0;
-    for (int b = 0; b < B; ++b) n += max(1, (((F[b] + 63) >> 6) + mid - 1) / mid);
-    if (n <= ctas) hi = mid;
-    else lo = mid + 1;
-  }
-  return hi;
-}
-
-// Valid length of row b as the kernels take it (0: refused, no keys).
-__device__ __forceinline__ int diff_length(const DiffDecodeArgs& a, int b, int* row_out, bool report) {
-  const int F = a.frontiers[b], row = a.table_rows[b];
-  const bool ok = F >= 0 && F <= a.L * 64 && row >= 0 && row < a.C;
-  if (!ok && report) set_status(a.status, NK_STATUS_FRONTIER);
-  *row_out = ok ? row : 0;
-  return ok ? F : 0;
-}
 
 template <int KIND>
 __device__ __forceinline__ int diff_q_dim(int s, int i, int c) {
@@ -155,32 +115,25 @@ __device__ __forceinline__ void diff_arrive(uint64_t* bar) {
 
 __device__ __forceinline__ float f16_at(const uint8_t* p) { return __half2float(*reinterpret_cast<const __half*>(p)); }
 
-// S (16 keys of slab `slab` x R rows) += K Q^T over a staged K tile of one head,
+// S (16 keys of slab `slab` x 8 rows) = K Q^T over a staged K tile of one head,
 // its scales applied: INT8 group and FP8 row scales multiply fp32 sums, NVFP4
-// scales the f16 operand (an exact product).  qb(s, j, b0, b1): q operand of
-// k-step s, column tile j.
-template <int KK, int D, int NQT, class Q>
-__device__ __forceinline__ void diff_scores(const uint8_t* tile, const uint8_t* scales, int slab, int lane, Q&& qb,
-                                            float (&S)[NQT][4]) {
+// scales the f16 operand (an exact product).  q: the operands of the k-steps.
+template <int KK, int D>
+__device__ __forceinline__ void diff_scores(const uint8_t* tile, const uint8_t* scales, int slab, int lane,
+                                            const uint32_t (&q)[D / 16][2], float (&S)[4]) {
   constexpr int KCB = diff_code_bytes<KK>(D), KSB = diff_scale_bytes<KK>(D), RB = KCB < 128 ? KCB : 128;
   const int r = lane >> 2, c = lane & 3;
   const int ld = 16 * slab + (lane & 7) + ((lane >> 3) & 1) * 8;  // ldmatrix row of this lane
   const int k0 = 16 * slab + r, k1 = k0 + 8;                      // keys of this lane's S rows
   const uint32_t base = smem_u32(tile);
-#pragma unroll
-  for (int j = 0; j < NQT; ++j) S[j][0] = S[j][1] = S[j][2] = S[j][3] = 0.f;
+  S[0] = S[1] = S[2] = S[3] = 0.f;
   if constexpr (KK == KIND_BF16) {
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
       const int col = (2 * s + (lane >> 4)) * 16;
       uint32_t A[4];
       ldsm_x4(base + (col / 128) * (64 * 128) + swz<128>(ld, col % 128), A[0], A[1], A[2], A[3]);
-#pragma unroll
-      for (int j = 0; j < NQT; ++j) {
-        uint32_t b0, b1;
-        qb(s, j, b0, b1);
-        mma16816<true>(S[j], A, b0, b1);
-      }
+      mma16816<true>(S, A, q[s][0], q[s][1]);
     }
   } else if constexpr (KK == KIND_NVFP4) {
 #pragma unroll
@@ -199,25 +152,17 @@ __device__ __forceinline__ void diff_scores(const uint8_t* tile, const uint8_t* 
                                 hmul2_u32(e2m1x2_byte_to_f16x2<1>(w0), f0), hmul2_u32(e2m1x2_byte_to_f16x2<1>(w1), f1)};
         const uint32_t A1[4] = {hmul2_u32(e2m1x2_byte_to_f16x2<2>(w0), f0), hmul2_u32(e2m1x2_byte_to_f16x2<2>(w1), f1),
                                 hmul2_u32(e2m1x2_byte_to_f16x2<3>(w0), f0), hmul2_u32(e2m1x2_byte_to_f16x2<3>(w1), f1)};
-#pragma unroll
-        for (int j = 0; j < NQT; ++j) {
-          uint32_t b0, b1, e0, e1;
-          qb(2 * (cw + u), j, b0, b1);
-          qb(2 * (cw + u) + 1, j, e0, e1);
-          mma16816<false>(S[j], A0, b0, b1);
-          mma16816<false>(S[j], A1, e0, e1);
-        }
+        const int s = 2 * (cw + u);
+        mma16816<false>(S, A0, q[s][0], q[s][1]);
+        mma16816<false>(S, A1, q[s + 1][0], q[s + 1][1]);
       }
     }
   } else {  // 8-bit codes: 16 dims per 16-byte chunk
-    float Sg[NQT][4];
+    float Sg[4];
 #pragma unroll
     for (int cw = 0; cw < KCB / 16; cw += 2) {
       if constexpr (KK == KIND_INT8) {
-        if ((cw & 3) == 0) {
-#pragma unroll
-          for (int j = 0; j < NQT; ++j) Sg[j][0] = Sg[j][1] = Sg[j][2] = Sg[j][3] = 0.f;
-        }
+        if ((cw & 3) == 0) Sg[0] = Sg[1] = Sg[2] = Sg[3] = 0.f;
       }
       const int col = (cw + (lane >> 4)) * 16;
       uint32_t d[4];
@@ -226,31 +171,21 @@ __device__ __forceinline__ void diff_scores(const uint8_t* tile, const uint8_t* 
       for (int u = 0; u < 2; ++u) {
         const uint32_t A[4] = {diff_cvt_pair<KK, false>(d[2 * u]), diff_cvt_pair<KK, false>(d[2 * u + 1]),
                                diff_cvt_pair<KK, true>(d[2 * u]), diff_cvt_pair<KK, true>(d[2 * u + 1])};
-#pragma unroll
-        for (int j = 0; j < NQT; ++j) {
-          uint32_t b0, b1;
-          qb(cw + u, j, b0, b1);
-          if constexpr (KK == KIND_INT8) mma16816<false>(Sg[j], A, b0, b1);
-          else mma16816<false>(S[j], A, b0, b1);
-        }
+        mma16816<false>(KK == KIND_INT8 ? Sg : S, A, q[cw + u][0], q[cw + u][1]);
       }
       if constexpr (KK == KIND_INT8) {
         if ((cw & 3) == 2) {  // end of a 64-dim group
           const float g0 = f16_at(scales + k0 * KSB + 2 * (cw >> 2)), g1 = f16_at(scales + k1 * KSB + 2 * (cw >> 2));
-#pragma unroll
-          for (int j = 0; j < NQT; ++j) {
-            S[j][0] = fmaf(Sg[j][0], g0, S[j][0]);
-            S[j][1] = fmaf(Sg[j][1], g0, S[j][1]);
-            S[j][2] = fmaf(Sg[j][2], g1, S[j][2]);
-            S[j][3] = fmaf(Sg[j][3], g1, S[j][3]);
-          }
+          S[0] = fmaf(Sg[0], g0, S[0]);
+          S[1] = fmaf(Sg[1], g0, S[1]);
+          S[2] = fmaf(Sg[2], g1, S[2]);
+          S[3] = fmaf(Sg[3], g1, S[3]);
         }
       }
     }
     if constexpr (KK == KIND_FP8) {
       const float g0 = f16_at(scales + k0 * KSB), g1 = f16_at(scales + k1 * KSB);
-#pragma unroll
-      for (int j = 0; j < NQT; ++j) S[j][0] *= g0, S[j][1] *= g0, S[j][2] *= g1, S[j][3] *= g1;
+      S[0] *= g0, S[1] *= g0, S[2] *= g1, S[3] *= g1;
     }
   }
 }
@@ -316,11 +251,11 @@ __device__ __forceinline__ void diff_values(const uint8_t* tile, const uint8_t* 
   }
 }
 
-template <int KK, int KV, int D, int NQT, bool PACK>
-__global__ void __launch_bounds__((DiffCfg<KK, KV, D, NQT, PACK>::THREADS), (DiffCfg<KK, KV, D, NQT, PACK>::MINB))
+template <int KK, int KV, int D, bool PACK>
+__global__ void __launch_bounds__((DiffCfg<KK, KV, D, PACK>::THREADS), (DiffCfg<KK, KV, D, PACK>::MINB))
     diff_decode_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                        DiffDecodeArgs a) {
-  using Cfg = DiffCfg<KK, KV, D, NQT, PACK>;
+  using Cfg = DiffCfg<KK, KV, D, PACK>;
   constexpr int R = Cfg::R, RB = Cfg::RB, NT = Cfg::NT, NSTAGE = Cfg::NSTAGE, NW = Cfg::NW, NCONS = Cfg::NCONS;
   constexpr int PARTS = Cfg::PARTS, MT = D / 16, XW = Cfg::XW;
   extern __shared__ uint8_t smem_raw[];
@@ -341,7 +276,7 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, NQT, PACK>::THREADS), (Dif
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, c = lane & 3;
   const int slab = warp >> 1, side = warp & 1;  // consumers: keys [16 slab, +16), map and V half
-  const int cta = blockIdx.x / a.blocks, blk = blockIdx.x % a.blocks, pair = blockIdx.y;
+  const int cta = blockIdx.x, pair = blockIdx.y;
 
   if (tid == 0) {
     for (int s = 0; s < NSTAGE; ++s) {
@@ -355,11 +290,13 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, NQT, PACK>::THREADS), (Dif
   }
   griddep_wait();  // pages, lengths and q may come from the kernel ahead
   griddep_launch_dependents();
-  if (tid < a.B) s_F[tid] = diff_length(a, tid, &s_row[tid], cta == 0 && blk == 0 && pair == 0);
+  if (tid < a.B)
+    s_F[tid] = diff_length(a.frontiers, a.table_rows, tid, a.L, a.C, &s_row[tid],
+                           cta == 0 && pair == 0 ? a.status : nullptr);
   __syncthreads();
 
   // ---- which (row, split) this CTA owns ----------------------------------------
-  const int chunk = diff_chunk(s_F, a.B, a.ctas);
+  const int chunk = diff_chunk(s_F, a.B, a.ctas, kDiffMaxSplits);
   int b = -1, split = 0, npages = 0;
   for (int i = 0, at = 0; i < a.B; ++i) {
     const int np = (s_F[i] + 63) >> 6, ns = max(1, (np + chunk - 1) / chunk);
@@ -372,7 +309,7 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, NQT, PACK>::THREADS), (Dif
   if (b < 0) return;
   const int F = s_F[b], p0 = split * chunk;
   const int n = min(chunk, npages - p0);  // 0 only for a row without keys
-  const int row0 = blk * RB, rows = min(RB, a.T * a.G - row0);  // this block's query rows
+  const int rows = a.T * a.G;  // query rows of a map
 
   // ---- producer warp --------------------------------------------------------------
   if (warp == NW) {
@@ -430,7 +367,7 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, NQT, PACK>::THREADS), (Dif
       const int qr = PACK ? col - 4 * m : col;
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
       if (qr >= 0 && qr < rows) {
-        const int t = (row0 + qr) / a.G, g = (row0 + qr) % a.G;
+        const int t = qr / a.G, g = qr % a.G;
         v = *reinterpret_cast<const uint4*>(
             a.q + ((static_cast<int64_t>(b) * a.T + t) * a.Hq + 2 * (pair * a.G + g) + m) * D + d8 * 8);
       }
@@ -444,7 +381,7 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, NQT, PACK>::THREADS), (Dif
     if (lane == 0) s_qmax[warp] = mx;
   }
   asm volatile("bar.sync 1, %0;" ::"n"(NCONS) : "memory");
-  auto q_exponent = [&](int m) {
+  const auto q_exponent = [&](int m) {
     float mx = 0.f;
 #pragma unroll
     for (int w = 0; w < 4; ++w) mx = fmaxf(mx, s_qmax[4 * m + w]);
@@ -463,42 +400,24 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, NQT, PACK>::THREADS), (Dif
     sc *= exp2f(-static_cast<float>(q_exponent(side)));
     asm volatile("bar.sync 1, %0;" ::"n"(NCONS) : "memory");
   }
-  auto qfrag = [&](int s, int j, uint32_t& b0, uint32_t& b1) {
-    const uint8_t* p = qs + (side * R + 8 * j + r) * Cfg::Q_PITCH;
-    if constexpr (KK == KIND_BF16) {
-      b0 = *reinterpret_cast<const uint32_t*>(p + 2 * diff_q_dim<KK>(s, 0, c));
-      b1 = *reinterpret_cast<const uint32_t*>(p + 2 * diff_q_dim<KK>(s, 2, c));
-    } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(p + 2 * diff_q_dim<KK>(s, 0, c));
-      b0 = v.x;
-      b1 = v.y;
-    }
-  };
-  uint32_t qreg[Cfg::Q_SMEM ? 1 : D / 16][Cfg::Q_SMEM ? 1 : NQT][2];
-  if constexpr (!Cfg::Q_SMEM) {
+  uint32_t q[D / 16][2];  // operands of this side's map
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-      for (int j = 0; j < NQT; ++j) qfrag(s, j, qreg[s][j][0], qreg[s][j][1]);
+  for (int s = 0; s < D / 16; ++s) {
+    const uint8_t* p = qs + (side * R + r) * Cfg::Q_PITCH;
+    q[s][0] = *reinterpret_cast<const uint32_t*>(p + 2 * diff_q_dim<KK>(s, 0, c));
+    q[s][1] = *reinterpret_cast<const uint32_t*>(p + 2 * diff_q_dim<KK>(s, 2, c));
   }
-  auto qb = [&](int s, int j, uint32_t& b0, uint32_t& b1) {
-    if constexpr (Cfg::Q_SMEM) qfrag(s, j, b0, b1);
-    else b0 = qreg[s][j][0], b1 = qreg[s][j][1];
-  };
 
   // ---- running state: map `side` for the softmax, both maps for this half of V --------
-  float nm[NQT][2], l_part[NQT][2];  // minus the reference maximum; sum
-  float o[MT][NT][4];                // tiles: own map's NQT, then the other's (PACK: one for both)
-  int k_run = 0;                     // O carries 2^k_run (INT8 / FP8 values near the f16 limit, v_lift)
-  int lim[NQT][2];                   // last key that a column's query sees
+  float nm[2] = {0.f, 0.f}, l_part[2] = {0.f, 0.f};  // minus the reference maximum; sum
+  float o[MT][NT][4];                                // tiles: own map, the other's (PACK: one for both)
+  int k_run = 0;  // O carries 2^k_run (INT8 / FP8 values near the f16 limit, v_lift)
+  int lim[2];     // last key that a column's query sees
 #pragma unroll
-  for (int j = 0; j < NQT; ++j)
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      nm[j][u] = l_part[j][u] = 0.f;
-      const int col = 8 * j + 2 * c + u, qr = PACK ? max(0, col - 4 * side) : col;
-      lim[j][u] = min(F - a.T + (row0 + qr) / a.G, F - 1);
-    }
+  for (int u = 0; u < 2; ++u) {
+    const int col = 2 * c + u, qr = PACK ? max(0, col - 4 * side) : col;
+    lim[u] = min(F - a.T + qr / a.G, F - 1);
+  }
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -533,54 +452,42 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, NQT, PACK>::THREADS), (Dif
       knew = v_lift(__reduce_max_sync(0xffffffffu, __float_as_uint(smax)), k_run);
     }
 
-    float S[NQT][4];
-    diff_scores<KK, D, NQT>(st + side * Cfg::K_TILE, st + Cfg::OFF_KS + side * Cfg::KS_TILE, slab, lane, qb, S);
+    float S[4];
+    diff_scores<KK, D>(st + side * Cfg::K_TILE, st + Cfg::OFF_KS + side * Cfg::KS_TILE, slab, lane, q, S);
 
     // ---- softmax of this side's map over the slab's keys (lazy reference, base 2) ------
     const int kg0 = key0 + kr0, kg1 = key0 + kr1;
     const bool first = i == 0;
-    float alpha[NQT][2], vloc[NQT][2];
-    bool need = first, rescale = false;
-#pragma unroll
-    for (int j = 0; j < NQT; ++j) {
-      S[j][0] = kg0 <= lim[j][0] ? fmaf(S[j][0], sc, nm[j][0]) : -INFINITY;
-      S[j][1] = kg0 <= lim[j][1] ? fmaf(S[j][1], sc, nm[j][1]) : -INFINITY;
-      S[j][2] = kg1 <= lim[j][0] ? fmaf(S[j][2], sc, nm[j][0]) : -INFINITY;
-      S[j][3] = kg1 <= lim[j][1] ? fmaf(S[j][3], sc, nm[j][1]) : -INFINITY;
+    float alpha[2] = {1.f, 1.f}, top[2];
+    S[0] = kg0 <= lim[0] ? fmaf(S[0], sc, nm[0]) : -INFINITY;
+    S[1] = kg0 <= lim[1] ? fmaf(S[1], sc, nm[1]) : -INFINITY;
+    S[2] = kg1 <= lim[0] ? fmaf(S[2], sc, nm[0]) : -INFINITY;
+    S[3] = kg1 <= lim[1] ? fmaf(S[3], sc, nm[1]) : -INFINITY;
+    top[0] = fmaxf(S[0], S[2]);
+    top[1] = fmaxf(S[1], S[3]);
+    bool rescale = false;
+    if (__any_sync(0xffffffffu, first || top[0] > 8.f || top[1] > 8.f)) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        vloc[j][u] = fmaxf(S[j][u], S[j][2 + u]);
-        need |= vloc[j][u] > 8.f;
-        alpha[j][u] = 1.f;
+        float v = top[u];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+        // the first page takes the exact maximum (a query's keys are a prefix:
+        // one that sees none here sees none later), later ones the excess
+        const float shift = first ? (v == -INFINITY ? 0.f : v) : fmaxf(v, 0.f);
+        alpha[u] = first ? 0.f : ex2(-shift);
+        rescale |= shift > 0.f;
+        nm[u] -= shift;
+        S[u] -= shift;
+        S[2 + u] -= shift;
+        l_part[u] *= alpha[u];
       }
     }
-    if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
-      for (int j = 0; j < NQT; ++j)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float v = vloc[j][u];
-#pragma unroll
-          for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-          // the first page takes the exact maximum (a query's keys are a prefix:
-          // one that sees none here sees none later), later ones the excess
-          const float shift = first ? (v == -INFINITY ? 0.f : v) : fmaxf(v, 0.f);
-          alpha[j][u] = first ? 0.f : ex2(-shift);
-          rescale |= shift > 0.f;
-          nm[j][u] -= shift;
-          S[j][u] = ex2(S[j][u] - shift);
-          S[j][2 + u] = ex2(S[j][2 + u] - shift);
-          l_part[j][u] = l_part[j][u] * alpha[j][u] + S[j][u] + S[j][2 + u];
-        }
-    } else {
-#pragma unroll
-      for (int j = 0; j < NQT; ++j)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          S[j][u] = ex2(S[j][u]);
-          S[j][2 + u] = ex2(S[j][2 + u]);
-          l_part[j][u] += S[j][u] + S[j][2 + u];
-        }
+    for (int u = 0; u < 2; ++u) {
+      S[u] = ex2(S[u]);
+      S[2 + u] = ex2(S[2 + u]);
+      l_part[u] += S[u] + S[2 + u];
     }
     rescale = __any_sync(0xffffffffu, rescale) && !first;  // O is 0 before the first page
 
@@ -589,59 +496,50 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, NQT, PACK>::THREADS), (Dif
     float al[NT][2];
     {
       uint32_t mine[XW];
+      if constexpr (Cfg::MMA_BF16) {  // bf16 weights as hi + lo (about 16 significant bits)
 #pragma unroll
-      for (int j = 0; j < NQT; ++j) {
-        if constexpr (Cfg::MMA_BF16) {  // bf16 weights as hi + lo (about 16 significant bits)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(S[j][2 * h], S[j][2 * h + 1]);
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(S[j][2 * h] - __low2float(hi), S[j][2 * h + 1] - __high2float(hi));
-            mine[2 * j + h] = diff_movm(*reinterpret_cast<const uint32_t*>(&hi));
-            mine[(PARTS - 1) * NQT * 2 + 2 * j + h] = diff_movm(*reinterpret_cast<const uint32_t*>(&lo));
-          }
-        } else {
-          mine[2 * j] = diff_movm(pack_f16x2(S[j][0], S[j][1]));
-          mine[2 * j + 1] = diff_movm(pack_f16x2(S[j][2], S[j][3]));
+        for (int h = 0; h < 2; ++h) {
+          const __nv_bfloat162 hi = __floats2bfloat162_rn(S[2 * h], S[2 * h + 1]);
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(S[2 * h] - __low2float(hi), S[2 * h + 1] - __high2float(hi));
+          mine[h] = diff_movm(*reinterpret_cast<const uint32_t*>(&hi));
+          mine[2 * (PARTS - 1) + h] = diff_movm(*reinterpret_cast<const uint32_t*>(&lo));
         }
-        mine[PARTS * NQT * 2 + 2 * j] = __float_as_uint(alpha[j][0]);
-        mine[PARTS * NQT * 2 + 2 * j + 1] = __float_as_uint(alpha[j][1]);
+      } else {
+        mine[0] = diff_movm(pack_f16x2(S[0], S[1]));
+        mine[1] = diff_movm(pack_f16x2(S[2], S[3]));
       }
+      mine[2 * PARTS] = __float_as_uint(alpha[0]);
+      mine[2 * PARTS + 1] = __float_as_uint(alpha[1]);
       mine[XW - 1] = rescale;
       uint32_t* to = sx + ((i & 1) * NW + warp) * (XW * 32) + lane;
       const uint32_t* from = sx + ((i & 1) * NW + (warp ^ 1)) * (XW * 32) + lane;
 #pragma unroll
-      for (int w = 0; w < XW; ++w) to[w * 32] = mine[w];
+      for (int x = 0; x < XW; ++x) to[x * 32] = mine[x];
       asm volatile("bar.sync %0, 64;" ::"r"(2 + slab) : "memory");
       uint32_t other[XW];
 #pragma unroll
-      for (int w = 0; w < XW; ++w) other[w] = from[w * 32];
+      for (int x = 0; x < XW; ++x) other[x] = from[x * 32];
       rescale |= other[XW - 1] != 0u;
 #pragma unroll
-      for (int part = 0; part < PARTS; ++part)
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int j = 0; j < NQT; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int w = part * NQT * 2 + 2 * j + h;
-            if constexpr (PACK) {
-              pb[part][0][h] = own_r ? mine[w] : other[w];
-            } else {
-              pb[part][j][h] = mine[w];
-              pb[part][NQT + j][h] = other[w];
-            }
-          }
-#pragma unroll
-      for (int j = 0; j < NQT; ++j)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int w = PARTS * NQT * 2 + 2 * j + u;
+        for (int part = 0; part < PARTS; ++part) {
+          const int x = 2 * part + h;
           if constexpr (PACK) {
-            al[0][u] = __uint_as_float(own_c ? mine[w] : other[w]);
+            pb[part][0][h] = own_r ? mine[x] : other[x];
           } else {
-            al[j][u] = __uint_as_float(mine[w]);
-            al[NQT + j][u] = __uint_as_float(other[w]);
+            pb[part][0][h] = mine[x];
+            pb[part][NT - 1][h] = other[x];
           }
         }
+        const int x = 2 * PARTS + h;
+        if constexpr (PACK) {
+          al[0][h] = __uint_as_float(own_c ? mine[x] : other[x]);
+        } else {
+          al[0][h] = __uint_as_float(mine[x]);
+          al[NT - 1][h] = __uint_as_float(other[x]);
+        }
+      }
     }
     if (rescale || knew != k_run) {
       const float kf = pow2i(knew - k_run);
@@ -702,18 +600,16 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, NQT, PACK>::THREADS), (Dif
   // Sums of a column over the lanes that hold its keys; the reference maximum is
   // -inf for a query that saw no key (one that saw a key has l >= 1; NaN stays).
 #pragma unroll
-  for (int j = 0; j < NQT; ++j)
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      float v = l_part[j][u];
-      v += __shfl_xor_sync(0xffffffffu, v, 4);
-      v += __shfl_xor_sync(0xffffffffu, v, 8);
-      v += __shfl_xor_sync(0xffffffffu, v, 16);
-      if (r == 0) {
-        red_m[(slab * 2 + side) * R + 8 * j + 2 * c + u] = v == 0.f ? -INFINITY : -nm[j][u];
-        red_l[(slab * 2 + side) * R + 8 * j + 2 * c + u] = v;
-      }
+  for (int u = 0; u < 2; ++u) {
+    float v = l_part[u];
+    v += __shfl_xor_sync(0xffffffffu, v, 4);
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+    v += __shfl_xor_sync(0xffffffffu, v, 16);
+    if (r == 0) {
+      red_m[(slab * 2 + side) * R + 2 * c + u] = v == 0.f ? -INFINITY : -nm[u];
+      red_l[(slab * 2 + side) * R + 2 * c + u] = v;
     }
+  }
   if (aborted && lane == 0) s_flags[0] = 1;
   asm volatile("bar.sync 1, %0;" ::"n"(NCONS) : "memory");
   if (s_flags[0]) {  // copies in flight land before the CTA leaves
@@ -742,8 +638,7 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, NQT, PACK>::THREADS), (Dif
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int col = PACK ? 2 * c + u : 8 * (j % NQT) + 2 * c + u;
-        const int map = PACK ? c >> 1 : (j < NQT ? side : side ^ 1);
+        const int col = 2 * c + u, map = PACK ? c >> 1 : side ^ j;
         const int qr = PACK ? col & 3 : col;
         const float m = red_m[(slab * 2 + map) * R + col];
         const float f = m == -INFINITY ? 0.f : ex2(m - row_M[map * R + col]) * unlift;
@@ -756,7 +651,7 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, NQT, PACK>::THREADS), (Dif
       }
   }
   asm volatile("bar.sync 1, %0;" ::"n"(NCONS) : "memory");
-  const int64_t slot = (static_cast<int64_t>(pair) * a.blocks + blk) * a.ctas + cta;
+  const int64_t slot = static_cast<int64_t>(pair) * a.ctas + cta;
   for (int idx = tid; idx < 2 * rows * (D / 2); idx += NCONS) {
     const int d = (idx % (D / 2)) * 4, map = idx / (D / 2) / rows, qr = idx / (D / 2) % rows;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -773,140 +668,27 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, NQT, PACK>::THREADS), (Dif
   }
 }
 
-// ---- the join of the splits, the difference and the norm -------------------------------
-// One CTA per (row, token, head).  A thread owns 4 dims of one map and every
-// LANES-th split; the shares are added in a fixed order in shared memory.
-template <int D>
-__global__ void __launch_bounds__(512) diff_join_kernel(DiffDecodeArgs a, int RB) {
-  constexpr int COLS = D;  // 2 maps x 2 D / 4
-  constexpr int LANES = 512 / COLS, EACH = kDiffMaxSplits / LANES, STEP = 8;
-  __shared__ int s_F[8], s_row[8];
-  __shared__ float s_w[2][kDiffMaxSplits];
-  __shared__ float4 s_acc[LANES][COLS];
-  __shared__ float s_sum[16];
-  __shared__ int s_any;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int head = blockIdx.x, bt = blockIdx.y, b = bt / a.T, t = bt % a.T;
-  griddep_wait();
-  griddep_launch_dependents();
-  if (tid < a.B) s_F[tid] = diff_length(a, tid, &s_row[tid], false);
-  __syncthreads();
-  const int chunk = diff_chunk(s_F, a.B, a.ctas);
-  int at = 0, ns = 0;
-  for (int i = 0; i <= b; ++i) {
-    at += ns;
-    ns = max(1, (((s_F[i] + 63) >> 6) + chunk - 1) / chunk);
-  }
-  const int pair = head / a.G, qr = t * a.G + head % a.G, blk = qr / RB, r = qr % RB;
-  const int64_t slot0 = (static_cast<int64_t>(pair) * a.blocks + blk) * a.ctas + at;
-  const int map = tid % COLS / (COLS / 2), d = tid % (COLS / 2) * 4, sub = tid / COLS;
-  const float* src = a.ws_o + ((slot0 * 2 + map) * RB + r) * (2 * D) + d;
-  const int64_t step = static_cast<int64_t>(2) * RB * 2 * D;
-  if (warp < 2) {  // weights of map `warp`
-    float2 ml[kDiffMaxSplits / 32];
-    float M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int k = 0; k < kDiffMaxSplits / 32; ++k) {
-      const int s = lane + 32 * k;
-      ml[k] = s < ns ? a.ws_ml[((slot0 + s) * 2 + warp) * RB + r] : make_float2(-INFINITY, 0.f);
-      M = fmaxf(M, ml[k].x);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-#pragma unroll
-    for (int k = 0; k < kDiffMaxSplits / 32; ++k) {
-      ml[k].x = ml[k].y == 0.f ? 0.f : ex2(ml[k].x - M);  // a split that saw no key weighs nothing
-      L += ml[k].x * ml[k].y;
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-    const bool none = L == 0.f;
-#pragma unroll
-    for (int k = 0; k < kDiffMaxSplits / 32; ++k)
-      if (lane + 32 * k < ns) s_w[warp][lane + 32 * k] = none ? 0.f : ml[k].x / L;
-    if (lane == 0) {
-      if (warp == 0) s_any = !none;
-      if (a.o.lse) a.o.lse[static_cast<int64_t>(bt) * a.Hq + 2 * head + warp] = none ? -INFINITY : (M + log2f(L)) * kDiffLn2;
-    }
-  }
-  __syncthreads();
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < EACH && sub + k0 * LANES < ns; k0 += STEP) {
-    float4 v[STEP];
-#pragma unroll
-    for (int k = 0; k < STEP; ++k) {
-      const int s = sub + (k0 + k) * LANES;
-      v[k] = s < ns ? *reinterpret_cast<const float4*>(src + s * step) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int k = 0; k < STEP; ++k) {
-      const int s = sub + (k0 + k) * LANES;
-      const float w = s < ns ? s_w[map][s] : 0.f;
-      acc.x = fmaf(w, v[k].x, acc.x);
-      acc.y = fmaf(w, v[k].y, acc.y);
-      acc.z = fmaf(w, v[k].z, acc.z);
-      acc.w = fmaf(w, v[k].w, acc.w);
-    }
-  }
-  s_acc[sub][tid % COLS] = acc;
-  __syncthreads();
-  float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-  if (tid < COLS / 2) {
-    const float lambda = a.o.lambda[bt * a.o.lambda_stride + head];
-    float x[2][4];
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      float4 v = s_acc[0][m * (COLS / 2) + tid];
-#pragma unroll
-      for (int k = 1; k < LANES; ++k) {
-        const float4 y = s_acc[k][m * (COLS / 2) + tid];
-        v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
-      }
-      x[m][0] = v.x, x[m][1] = v.y, x[m][2] = v.z, x[m][3] = v.w;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[i] = s_any ? fmaf(-lambda, x[1][i], x[0][i]) : 0.f;
-      sum = fmaf(o[i], o[i], sum);
-    }
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if (lane == 0) s_sum[warp] = sum;
-  __syncthreads();
-  if (tid < COLS / 2) {
-    sum = s_sum[0];
-#pragma unroll
-    for (int w = 1; w < COLS / 64; ++w) sum += s_sum[w];
-    const float f = a.o.w ? rsqrtf(sum / (2 * D) + a.o.eps) * a.o.out_scale : a.o.out_scale;
-    __nv_bfloat16* dst = a.o.out + (static_cast<int64_t>(bt) * (a.Hq / 2) + head) * (2 * D) + tid * 4;
-    *reinterpret_cast<uint2*>(dst) = diff_finish(o, f, a.o.w, tid * 4);
-  }
-}
-
-template <int KK, int KV, int D, int NQT, bool PACK>
+template <int KK, int KV, int D, bool PACK>
 cudaError_t launch_diff_decode(const nk_pool* p, int layer, const DiffDecodeArgs& a, cudaStream_t s) {
-  using Cfg = DiffCfg<KK, KV, D, NQT, PACK>;
-  auto k = diff_decode_kernel<KK, KV, D, NQT, PACK>;
+  using Cfg = DiffCfg<KK, KV, D, PACK>;
+  auto k = diff_decode_kernel<KK, KV, D, PACK>;
   static std::atomic<uint64_t> granted{0};
-  cudaError_t e = grant_smem(granted, k, Cfg::SMEM);
+  const cudaError_t e = grant_smem(granted, k, Cfg::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k, dim3(a.ctas * a.blocks, a.H / 2), dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0],
-                 p->tmap[layer * 2 + 1], a);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(diff_join_kernel<D>, dim3(a.Hq / 2, a.B * a.T), dim3(512), 0, s, a, Cfg::RB);
+  return launch_pdl(k, dim3(a.ctas, a.H / 2), dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0],
+                    p->tmap[layer * 2 + 1], a);
 }
 
-template <int KK, int KV, int D, int NQT, bool PACK>
+template <int KK, int KV, int D, bool PACK>
 int diff_ctas_per_sm() {
-  using Cfg = DiffCfg<KK, KV, D, NQT, PACK>;
+  using Cfg = DiffCfg<KK, KV, D, PACK>;
   static std::atomic<uint64_t> granted{0};
   static std::atomic<int> cached[64];
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return 1;
   int n = device < 64 ? cached[device].load(std::memory_order_relaxed) : 0;
   if (n) return n;
-  auto k = diff_decode_kernel<KK, KV, D, NQT, PACK>;
+  auto k = diff_decode_kernel<KK, KV, D, PACK>;
   if (grant_smem(granted, k, Cfg::SMEM) != cudaSuccess ||
       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, Cfg::THREADS, Cfg::SMEM) != cudaSuccess || n < 1)
     n = 1;
@@ -914,35 +696,32 @@ int diff_ctas_per_sm() {
   return n;
 }
 
-// Per-profile entries (diff_decode_*.cu).  rows: the query rows of a block (4, 8
-// or 16).  a == nullptr: only the CTAs per SM are asked, in *per_sm.
-using DiffDecodeFn = cudaError_t (*)(const nk_pool*, int layer, const DiffDecodeArgs* a, int rows, int* per_sm,
+// Per-profile entries (diff_decode_*.cu).  pack: up to 4 query rows.  a ==
+// nullptr: only the CTAs per SM are asked, in *per_sm.
+using DiffDecodeFn = cudaError_t (*)(const nk_pool*, int layer, const DiffDecodeArgs* a, bool pack, int* per_sm,
                                      cudaStream_t);
 
-template <int KK, int KV, int D>
-cudaError_t diff_decode_rows(const nk_pool* p, int layer, const DiffDecodeArgs* a, int rows, int* per_sm,
-                             cudaStream_t s) {
-  if (rows == 4)
-    return a ? launch_diff_decode<KK, KV, D, 1, true>(p, layer, *a, s)
-             : (*per_sm = diff_ctas_per_sm<KK, KV, D, 1, true>(), cudaSuccess);
-  if (rows == 8)
-    return a ? launch_diff_decode<KK, KV, D, 1, false>(p, layer, *a, s)
-             : (*per_sm = diff_ctas_per_sm<KK, KV, D, 1, false>(), cudaSuccess);
-  return a ? launch_diff_decode<KK, KV, D, 2, false>(p, layer, *a, s)
-           : (*per_sm = diff_ctas_per_sm<KK, KV, D, 2, false>(), cudaSuccess);
+template <int KK, int KV, int D, bool PACK>
+cudaError_t diff_decode_one(const nk_pool* p, int layer, const DiffDecodeArgs* a, int* per_sm, cudaStream_t s) {
+  if (a) return launch_diff_decode<KK, KV, D, PACK>(p, layer, *a, s);
+  *per_sm = diff_ctas_per_sm<KK, KV, D, PACK>();
+  return cudaSuccess;
 }
 
 template <int KK, int KV>
-cudaError_t diff_decode_dispatch(const nk_pool* p, int layer, const DiffDecodeArgs* a, int rows, int* per_sm,
+cudaError_t diff_decode_dispatch(const nk_pool* p, int layer, const DiffDecodeArgs* a, bool pack, int* per_sm,
                                  cudaStream_t s) {
-  return p->desc.head_dim == 64 ? diff_decode_rows<KK, KV, 64>(p, layer, a, rows, per_sm, s)
-                                : diff_decode_rows<KK, KV, 128>(p, layer, a, rows, per_sm, s);
+  if (p->desc.head_dim == 64)
+    return pack ? diff_decode_one<KK, KV, 64, true>(p, layer, a, per_sm, s)
+                : diff_decode_one<KK, KV, 64, false>(p, layer, a, per_sm, s);
+  return pack ? diff_decode_one<KK, KV, 128, true>(p, layer, a, per_sm, s)
+              : diff_decode_one<KK, KV, 128, false>(p, layer, a, per_sm, s);
 }
 
-cudaError_t diff_decode_bf16(const nk_pool*, int, const DiffDecodeArgs*, int, int*, cudaStream_t);
-cudaError_t diff_decode_int8(const nk_pool*, int, const DiffDecodeArgs*, int, int*, cudaStream_t);
-cudaError_t diff_decode_fp8(const nk_pool*, int, const DiffDecodeArgs*, int, int*, cudaStream_t);
-cudaError_t diff_decode_nvfp4(const nk_pool*, int, const DiffDecodeArgs*, int, int*, cudaStream_t);
-cudaError_t diff_decode_k8v4(const nk_pool*, int, const DiffDecodeArgs*, int, int*, cudaStream_t);
+cudaError_t diff_decode_bf16(const nk_pool*, int, const DiffDecodeArgs*, bool, int*, cudaStream_t);
+cudaError_t diff_decode_int8(const nk_pool*, int, const DiffDecodeArgs*, bool, int*, cudaStream_t);
+cudaError_t diff_decode_fp8(const nk_pool*, int, const DiffDecodeArgs*, bool, int*, cudaStream_t);
+cudaError_t diff_decode_nvfp4(const nk_pool*, int, const DiffDecodeArgs*, bool, int*, cudaStream_t);
+cudaError_t diff_decode_k8v4(const nk_pool*, int, const DiffDecodeArgs*, bool, int*, cudaStream_t);
 
 }  // namespace nk

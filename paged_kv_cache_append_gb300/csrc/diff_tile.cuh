@@ -1,0 +1,828 @@
+// diff_tile.cuh -- differential attention of 128 query rows at a time on the
+// 5th-generation tensor cores (kernel template; instantiated per profile in
+// diff_tile_*.cu): prompt chunks, and decode / verify tokens of many query rows.
+//
+// Chunks (BOTH = false).  A CTA owns 128 query rows of one map of one (row b,
+// pair of KV heads): TQ = floor(128 / G) consecutive tokens times the G heads that
+// share the pair, and one range of pages.  Per page of 64 keys
+//   S = Q_m K_m^T   M 128 x N 64 x K D;   P = exp2(S - m);
+//   O += P [V1 V2]  M 128 x N 2 D x K 64,
+// 2 D + 4 D flops per (query row, key): the least for two maps over one wide value.
+// Decode / verify (BOTH = true).  Lanes 0-63 are the (up to 64) query rows of map
+// 1, lanes 64-127 those of map 2, so that every page is read and converted once:
+//   S = [Q1; 0] K1^T + [0; Q2] K2^T, two MMAs into one S.
+//
+// Tensor memory: S buffers [0, 64) and [64, 128), Q [128, 128 + D / 2) (BOTH: two
+// operands), O [256, 256 + 2 D).  P goes over the S it was computed from.
+//
+// Operands.  Scores: BF16 pages as they are; FP8-row keys of head_dim 128 as raw
+// E4M3 codes with q in two E4M3 terms, other quantized keys as exact f16 tiles
+// (INT8-G64: two), their per-key factors applied to the scores in fp32, as in
+// qprefill.cu.  P is f16 for every profile, so that its weights keep 11 bits, and
+// V therefore too:
+//   * NVFP4 values carry their scales exactly; one P serves both heads, N = 2 D;
+//   * FP8-row and INT8-G64 values leave a factor per key to the weights, so each
+//     head has its own P (columns [0, 32) and [32, 64) of the S buffer), N = D twice;
+//   * BF16 values are rewritten in place, v 2^k with a power of two per strip of 2 D /
+//     8 dims that brings the strip's largest value so far to [2^10, 2^15): exact for
+//     every element above its 2^-27th.  k only falls (then O is rescaled), and the
+//     store divides it out.
+// FP8-row value factors are lifted by a power of two of their own (v_lift).
+//
+// Warps (576 threads): 0-7 softmax, warp w lanes 32 (w & 3) and keys 32 (w >> 2) of
+// a page (the two warps of a row exchange its maximum through shared memory and move
+// the reference lazily); 8 TMA producer; 9 MMA issuer; 10-17 converters.
+//
+// All waits are bounded.  Where warps meet at named barriers, a wait that ran out
+// lets the loop run on without waiting, so that they stay matched; the CTA leaves
+// without results once the copies in flight have landed.
+#pragma once
+
+#include "diff.cuh"
+#include "packed.cuh"
+#include "qtile.cuh"
+#include "tcgen05.cuh"
+
+namespace nk {
+
+struct DiffTileArgs {
+  const __nv_bfloat16* q;  // [B][T][Hq][D]
+  const int32_t* tables;
+  const int32_t* table_rows;
+  const int32_t* lengths;    // chunks: prefix_len; decode: frontiers
+  const int32_t* chunk_len;  // chunks
+  const uint8_t* ks;         // scale planes of the layer (nullptr for BF16)
+  const uint8_t* vs;
+  float2* ws_ml;  // [part][128] (m, l); chunks: part = (((b pairs + pair) tiles + qt) nsplit + split) 2 + map,
+  float* ws_o;    // [part][128][2 D];   decode: part = pair ctas + cta
+  int* status;
+  float scale_log2;  // |softmax_scale| log2 e, > 0
+  int negate;        // softmax_scale < 0: the queries change sign
+  int B, T, Hq, H, G, L, M, C;
+  int TQ, tiles, nsplit;  // chunks
+  int ctas;               // decode: CTAs per pair
+  int head_major;
+};
+
+// At least this many pages per range of a chunk's tile: shorter ones cost more in
+// start-up and partials than they win.
+constexpr int kDiffSplitPages = 4;
+
+template <int KK, int KV, int D, bool BOTH>
+struct DiffTileCfg {
+  static constexpr int NSOFT = 8, NCONV = 8, THREADS = 32 * (NSOFT + 2 + NCONV);
+  static constexpr bool BF16 = KK == KIND_BF16;
+  static constexpr int KCB = BF16 ? 2 * D : code_row_bytes<KK>(D), VCB = BF16 ? 2 * D : code_row_bytes<KV>(D);
+  static constexpr int KSB = scale_row_bytes<KK>(D), VSB = scale_row_bytes<KV>(D);
+  static constexpr int K_RB = KCB < 128 ? KCB : 128, V_RB = VCB < 128 ? VCB : 128;
+  static constexpr int F16 = 64 * D * 2;                     // one head's f16 page tile
+  static constexpr bool K_SPLIT = KK == KIND_INT8;           // exact INT8 keys: two f16 tiles
+  static constexpr bool K8MMA = KK == KIND_FP8 && D >= 128;  // raw E4M3 keys to the tensor cores
+  static constexpr bool K_RAW = BF16 || K8MMA;               // the raw K tile is the operand
+  static constexpr bool KEY_FAC = KK == KIND_FP8 || KK == KIND_INT8;  // scores take a factor per key
+  static constexpr bool VAL_FAC = KV == KIND_FP8 || KV == KIND_INT8;  // weights take one per key and head
+  static constexpr bool HAS_F = KEY_FAC || VAL_FAC || BF16;
+  static constexpr int KH = BOTH ? 2 : 1;  // K tiles of a page
+  static constexpr int RK_CODES = (64 * KCB + 1023) / 1024 * 1024, RV_CODES = (64 * VCB + 1023) / 1024 * 1024;
+  static constexpr int RK_HEAD = (RK_CODES + 64 * KSB + 1023) / 1024 * 1024, RK_STAGE = KH * RK_HEAD;
+  static constexpr int RV_HEAD = (RV_CODES + 64 * VSB + 1023) / 1024 * 1024, RV_STAGE = BF16 ? 0 : 2 * RV_HEAD;
+  static constexpr int K_HEAD = K_SPLIT ? 2 * F16 : F16, K_STAGE = K_RAW ? 0 : KH * K_HEAD;
+  static constexpr int V_STAGE = 2 * F16;
+  // ring depths, as shared memory allows
+  static constexpr int NRK = D == 64 ? (BF16 && !BOTH ? 8 : 4) : K_SPLIT ? (BOTH ? 2 : 3) : BOTH && KV != KIND_NVFP4 ? 3 : BOTH && !K_RAW ? 3 : 4;
+  static constexpr int NK = K_RAW ? 1 : D == 64 ? (K_SPLIT && BOTH ? 2 : 3) : K_SPLIT ? (BOTH ? 1 : 2) : BOTH ? 2 : 3;
+  static constexpr int NV = D == 64 ? 4 : K_SPLIT ? 2 : K_RAW && !BOTH && KV != KIND_FP8 ? 4 : 3;
+  static constexpr int NRV = BF16 ? NV : D == 64 ? 4 : K_SPLIT ? 2 : BOTH && !K_RAW ? 2 : 3;
+  static constexpr int NF = 4;  // factor ring: 1 KB per page
+  static constexpr int OFF_V = NK * K_STAGE;
+  static constexpr int OFF_RK = OFF_V + NV * V_STAGE;
+  static constexpr int OFF_RV = OFF_RK + NRK * RK_STAGE;
+  static constexpr int OFF_F = OFF_RV + NRV * RV_STAGE;
+  static constexpr int OFF_X = OFF_F + NF * 1024;  // [2][2][128] maxima of the rows' halves
+  static constexpr int OFF_BAR = OFF_X + 2048;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NRK + 2 * NRV + 2 * NF + 8;
+  static constexpr int SMEM = OFF_BAR + NBAR * 8 + 64 + 1024;
+  static constexpr uint32_t COL_S = 0, COL_Q = 128, COL_O = 256;
+  static constexpr uint32_t ID_S = K8MMA  ? tc::idesc_e4m3(128, 64)
+                                   : BF16 ? tc::idesc_bf16(128, 64, false, false)
+                                          : tc::idesc_f16(128, 64, false, false);
+  static constexpr uint32_t ID_O = tc::idesc_f16(128, VAL_FAC ? D : 2 * D, false, true);
+  static constexpr int STRIP = 2 * D / NCONV;  // dims that a converter warp of BF16 values owns
+  static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+  static_assert(SMEM > 114 * 1024, "one CTA per SM: each takes all of the tensor memory");
+};
+
+// What a CTA works on; n < 0: nothing.
+struct DiffWork {
+  int b, pair, map, row, F, t0, limit, pos0, p_lo, n;
+  int64_t part;
+};
+
+// Chunks: later tiles see more keys and are launched first; the two maps of a
+// tile are neighbours.
+__device__ __forceinline__ DiffWork diff_chunk_work(const DiffTileArgs& a) {
+  DiffWork w;
+  w.map = blockIdx.x & 1;
+  const int x = blockIdx.x >> 1, split = x % a.nsplit, qt = a.tiles - 1 - x / a.nsplit;
+  w.pair = blockIdx.y;
+  w.b = blockIdx.z;
+  w.row = a.table_rows[w.b];
+  const int prefix = a.lengths[w.b], chunk = a.chunk_len[w.b];
+  w.n = -1;
+  if (w.row < 0 || w.row >= a.C || prefix < 0 || chunk < 0 || chunk > a.T ||
+      static_cast<int64_t>(prefix) + chunk > static_cast<int64_t>(a.L) * 64) {
+    if (threadIdx.x == 0 && blockIdx.x == 0 && w.pair == 0) set_status(a.status, NK_STATUS_FRONTIER);
+    return w;
+  }
+  w.t0 = qt * a.TQ;
+  if (w.t0 >= chunk) return w;
+  w.limit = chunk;
+  w.F = prefix + chunk;
+  w.pos0 = prefix;
+  const int pages = (prefix + min(w.t0 + a.TQ, chunk) - 1 + 64) / 64;
+  const int per = max((pages + a.nsplit - 1) / a.nsplit, kDiffSplitPages);
+  w.p_lo = min(split * per, pages);
+  w.n = min(w.p_lo + per, pages) - w.p_lo;
+  w.part = (((static_cast<int64_t>(w.b) * (a.H / 2) + w.pair) * a.tiles + qt) * a.nsplit + split) * 2 + w.map;
+  return w;
+}
+
+// Decode: the split plan of all rows, from the frontiers (scratch: 16 ints of
+// shared memory; every thread of the CTA takes part).
+__device__ __forceinline__ DiffWork diff_decode_work(const DiffTileArgs& a, int* s_F) {
+  DiffWork w;
+  const int cta = blockIdx.x, tid = threadIdx.x;
+  w.pair = blockIdx.y;
+  w.map = 0;
+  w.n = -1;
+  if (tid < a.B)
+    s_F[tid] = diff_length(a.lengths, a.table_rows, tid, a.L, a.C, &s_F[8 + tid],
+                           cta == 0 && w.pair == 0 ? a.status : nullptr);
+  __syncthreads();
+  const int chunk = diff_chunk(s_F, a.B, a.ctas, kDiffMaxSplits);
+  for (int b = 0, at = 0; b < a.B; ++b) {
+    const int np = (s_F[b] + 63) >> 6, ns = max(1, (np + chunk - 1) / chunk);
+    if (cta < at + ns) {
+      w.b = b;
+      w.row = s_F[8 + b];
+      w.F = s_F[b];
+      w.t0 = 0;
+      w.limit = a.T;
+      w.pos0 = w.F - a.T;
+      w.p_lo = (cta - at) * chunk;
+      w.n = min(chunk, np - w.p_lo);  // 0 only for a row without keys
+      w.part = static_cast<int64_t>(w.pair) * a.ctas + cta;
+      break;
+    }
+    at += ns;
+  }
+  return w;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_lift(uint32_t w, float f) {  // two bf16 values times f as f16x2
+  return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+}
+
+// Converter warps of BF16 values: warp cw rewrites its strip of every staged V
+// tile, bf16 -> f16 of v 2^k in place, and publishes what its k did.
+template <int D>
+struct StripOf {
+  static constexpr int CH = 2 * D / 8 / 8;  // 16-byte chunks of the strip in a key's row
+  static constexpr int UNITS = 64 * CH / 32;
+};
+
+// 2^k that takes the largest bf16 magnitude (its 15 bits) to [2^10, 2^11).
+__device__ __forceinline__ int strip_lift(uint32_t bits) {
+  const int e = static_cast<int>(bits >> 7);
+  return max(-117, min(110, 137 - e));
+}
+
+template <int KK, int KV, int D, bool BOTH>
+__global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
+    diff_tile_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, DiffTileArgs a) {
+  using Cfg = DiffTileCfg<KK, KV, D, BOTH>;
+  constexpr int NK = Cfg::NK, NV = Cfg::NV, NRK = Cfg::NRK, NRV = Cfg::NRV, NF = Cfg::NF, KH = Cfg::KH;
+  constexpr int NCT = 32 * Cfg::NCONV;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sK = smem;
+  uint8_t* sV = smem + Cfg::OFF_V;
+  uint8_t* sRK = smem + Cfg::OFF_RK;
+  uint8_t* sRV = Cfg::BF16 ? sV : smem + Cfg::OFF_RV;
+  float* sF = reinterpret_cast<float*>(smem + Cfg::OFF_F);  // [NF][256]: K factors of 2 heads, V factors of 2 heads
+  float* sX = reinterpret_cast<float*>(smem + Cfg::OFF_X);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);  // f16 K tiles ready (converters)
+  uint64_t* k_empty = k_full + NK;                                      // their S done (MMA commit)
+  uint64_t* v_full = k_empty + NK;                                      // f16 V tiles ready
+  uint64_t* v_empty = v_full + NV;
+  uint64_t* rk_full = v_empty + NV;  // raw K landed (TMA)
+  uint64_t* rk_empty = rk_full + NRK;
+  uint64_t* rv_full = rk_empty + NRK;  // raw V landed
+  uint64_t* rv_empty = rv_full + NRV;
+  uint64_t* f_full = rv_empty + NRV;  // factors of a page written
+  uint64_t* f_empty = f_full + NF;
+  uint64_t* s_full = f_empty + NF;  // [2]
+  uint64_t* p_full = s_full + 2;    // [2]
+  uint64_t* o_done = p_full + 2;    // [2]
+  uint64_t* q_ready = o_done + 2;
+  uint64_t* drain = q_ready + 1;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_wait();  // launched with programmatic stream serialization
+  griddep_launch_dependents();
+  DiffWork w;
+  if constexpr (BOTH) w = diff_decode_work(a, reinterpret_cast<int*>(sX));
+  else w = diff_chunk_work(a);
+  const int n = w.n;
+  if (n < 0) return;
+  const int32_t* table = a.tables + static_cast<int64_t>(w.row) * a.L + w.p_lo;
+
+  if (tid == 0) {
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(&k_full[i], Cfg::NCONV);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(&v_full[i], Cfg::NCONV);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < NRK; ++i) {
+      mbar_init(&rk_full[i], 1);
+      // released by the converters; a raw operand by the MMA's commit, and where
+      // its scales are read (FP8-row) by both
+      mbar_init(&rk_empty[i], Cfg::BF16 ? 1 : Cfg::K8MMA ? 1 + Cfg::NCONV : Cfg::NCONV);
+    }
+    for (int i = 0; i < NRV; ++i) {
+      mbar_init(&rv_full[i], 1);
+      mbar_init(&rv_empty[i], Cfg::NCONV);
+    }
+    for (int i = 0; i < NF; ++i) {
+      mbar_init(&f_full[i], Cfg::NCONV);
+      mbar_init(&f_empty[i], Cfg::NSOFT);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], Cfg::NSOFT);
+      mbar_init(&o_done[i], 1);
+    }
+    mbar_init(q_ready, Cfg::NSOFT);
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tmk);
+    prefetch_tmap(&tmv);
+  }
+  if (warp == 0) {
+    tc::alloc(tslot, 512);
+    tc::relinquish();
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tslot;
+  const auto wait = [&](uint64_t* bar, int use) { return mbar_wait_bounded(bar, use & 1, a.status) && !*s_abort; };
+
+  if (warp == Cfg::NSOFT) {
+    // ------------- TMA producer: code and scale tiles of each page ---------------
+    int gnext = 0, nk = 0, nv = 0;  // copies issued (lane 0)
+    for (int j = 0; j < n; ++j) {
+      if ((j & 31) == 0) gnext = (j + lane < n) ? table[j + lane] : 0;
+      int g = __shfl_sync(0xffffffffu, gnext, j & 31);
+      int stop = 0;
+      if (lane == 0) {
+        if (g < 0 || g >= a.M) {  // never copy from outside the pool
+          set_status(a.status, NK_STATUS_PAGE_RANGE);
+          g = 0;
+        }
+        const int y[2] = {static_cast<int>(tile_row(g, 2 * w.pair, a.H, a.M, a.head_major)),
+                          static_cast<int>(tile_row(g, 2 * w.pair + 1, a.H, a.M, a.head_major))};
+        const int rk = j % NRK, rv = j % NRV;
+        if (j >= NRK && !wait(&rk_empty[rk], j / NRK - 1)) stop = 1;
+        if (!stop) {
+          mbar_arrive_expect_tx(&rk_full[rk], KH * (64 * Cfg::KCB + 64 * Cfg::KSB));
+#pragma unroll
+          for (int i = 0; i < KH; ++i) {
+            uint8_t* st = sRK + rk * Cfg::RK_STAGE + i * Cfg::RK_HEAD;
+            const int yk = BOTH ? y[i] : y[w.map];
+#pragma unroll
+            for (int c = 0; c < Cfg::KCB / Cfg::K_RB; ++c)
+              tma_load_2d(st + c * 64 * Cfg::K_RB, &tmk, c * Cfg::K_RB, yk, &rk_full[rk]);
+            if constexpr (Cfg::KSB > 0)
+              bulk_load(st + Cfg::RK_CODES, a.ks + static_cast<int64_t>(yk) * Cfg::KSB, 64 * Cfg::KSB, &rk_full[rk]);
+          }
+          ++nk;
+        }
+        // BF16 values land where the MMA reads them: their slot is free once it has
+        if (!stop && j >= NRV && !wait(Cfg::BF16 ? &v_empty[rv] : &rv_empty[rv], j / NRV - 1)) stop = 1;
+        if (!stop) {
+          mbar_arrive_expect_tx(&rv_full[rv], 2 * (64 * Cfg::VCB + 64 * Cfg::VSB));
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            uint8_t* st = Cfg::BF16 ? sV + rv * Cfg::V_STAGE + v * Cfg::F16 : sRV + rv * Cfg::RV_STAGE + v * Cfg::RV_HEAD;
+#pragma unroll
+            for (int c = 0; c < Cfg::VCB / Cfg::V_RB; ++c)
+              tma_load_2d(st + c * 64 * Cfg::V_RB, &tmv, c * Cfg::V_RB, y[v], &rv_full[rv]);
+            if constexpr (Cfg::VSB > 0)
+              bulk_load(st + Cfg::RV_CODES, a.vs + static_cast<int64_t>(y[v]) * Cfg::VSB, 64 * Cfg::VSB, &rv_full[rv]);
+          }
+          ++nv;
+        }
+        if (stop) *s_abort = 1;
+      }
+      if (__shfl_sync(0xffffffffu, stop, 0)) break;
+    }
+    if (lane == 0) {  // every copy lands before the CTA may leave
+      for (int j = max(0, nk - NRK); j < nk; ++j) mbar_wait_bounded(&rk_full[j % NRK], (j / NRK) & 1, a.status);
+      for (int j = max(0, nv - NRV); j < nv; ++j) mbar_wait_bounded(&rv_full[j % NRV], (j / NRV) & 1, a.status);
+    }
+  } else if (warp > Cfg::NSOFT + 1) {
+    const int ct = tid - 32 * (Cfg::NSOFT + 2);
+    bool ok = true;
+    if constexpr (Cfg::BF16) {
+      // ------------- converters of BF16 values: a strip of dims per warp -----------
+      using St = StripOf<D>;
+      const int cw = ct >> 5, col = cw * Cfg::STRIP;
+      const int chunk0 = (col % 64) / 8, blk = (col / D) * Cfg::F16 + (col % D) / 64 * 8192;
+      int k = 0;
+      for (int i = 0; ok && i < n; ++i) {
+        const int vs = i % NV, fs = i % NF, kvalid = w.F - 64 * (w.p_lo + i);
+        ok = wait(&rv_full[vs], i / NV);
+        if (!ok) break;
+        uint8_t* tile = sV + vs * Cfg::V_STAGE + blk;
+        uint4 v[St::UNITS];
+        uint32_t most = 0u;  // largest magnitudes of the pairs' low and high halves
+        int off[St::UNITS];
+#pragma unroll
+        for (int u = 0; u < St::UNITS; ++u) {
+          const int x = u * 32 + lane, r = x / St::CH, c = chunk0 + x % St::CH;
+          off[u] = r * 128 + ((c ^ (r & 7)) << 4);
+          v[u] = *reinterpret_cast<const uint4*>(tile + off[u]);
+          if (r >= kvalid) v[u] = make_uint4(0u, 0u, 0u, 0u);  // stale keys
+          most = __vmaxu2(most, __vmaxu2(__vmaxu2(v[u].x & 0x7FFF7FFFu, v[u].y & 0x7FFF7FFFu),
+                                         __vmaxu2(v[u].z & 0x7FFF7FFFu, v[u].w & 0x7FFF7FFFu)));
+        }
+        most = __reduce_max_sync(0xffffffffu, max(most & 0xFFFFu, most >> 16));
+        // a new k where the strip's largest value leaves [., 2^15), and on its first page
+        const int e = static_cast<int>(most >> 7) - 127;
+        const int was = k;
+        if (i == 0) k = strip_lift(most);
+        else if (most && e + k >= 15) k = min(k, strip_lift(most));
+        if (i >= NF) ok = wait(&f_empty[fs], i / NF - 1);
+        if (!ok) break;
+        if (lane == 0) {
+          float* slot = sF + fs * 256;
+          reinterpret_cast<uint8_t*>(slot)[cw] = i > 0 && k != was;
+          slot[8 + cw] = pow2i(i > 0 ? max(k - was, -126) : 0);
+          reinterpret_cast<int*>(slot)[16 + cw] = k;
+        }
+        const float f = pow2i(k);
+#pragma unroll
+        for (int u = 0; u < St::UNITS; ++u)
+          *reinterpret_cast<uint4*>(tile + off[u]) = make_uint4(bf16x2_lift(v[u].x, f), bf16x2_lift(v[u].y, f),
+                                                                bf16x2_lift(v[u].z, f), bf16x2_lift(v[u].w, f));
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          q_arrive(&f_full[fs]);
+          q_arrive(&v_full[vs]);
+        }
+      }
+    } else {
+      // ------------- converters: K(0), K(1), V(0), K(2), V(1), ... -----------------
+      for (int i = 0; ok && i <= n; ++i) {
+        if (i < n) {  // K(i) and the factors of page i
+          const int rk = i % NRK, rv = i % NRV, fs = i % NF;
+          if constexpr (!Cfg::K_RAW || Cfg::HAS_F) {
+            ok = wait(&rk_full[rk], i / NRK);
+            if (!ok) break;
+          }
+          const uint8_t* raw = sRK + rk * Cfg::RK_STAGE;
+          const int kvalid = w.F - 64 * (w.p_lo + i);
+          const int key = ct & 63, what = ct >> 6;  // threads 0-127: K factors, 128-255: V factors
+          const bool live = key < kvalid;
+          float fac = 0.f;  // of the K scales, read before their slot can be released
+          if constexpr (Cfg::KEY_FAC)
+            if (what < KH && live) fac = key_factor<KK, D>(raw + what * Cfg::RK_HEAD + Cfg::RK_CODES, key) * a.scale_log2;
+          if constexpr (!Cfg::K_RAW) {
+            const int ks = i % NK;
+            if (i >= NK) ok = wait(&k_empty[ks], i / NK - 1);
+            if (!ok) break;
+#pragma unroll
+            for (int h = 0; h < KH; ++h)
+              convert_tile<KK, D, Cfg::K_RB, NCT, Cfg::K_SPLIT>(raw + h * Cfg::RK_HEAD, Cfg::RK_CODES,
+                                                               sK + ks * Cfg::K_STAGE + h * Cfg::K_HEAD, ct, kvalid);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              q_arrive(&rk_empty[rk]);
+              q_arrive(&k_full[ks]);
+            }
+          }
+          if constexpr (Cfg::HAS_F) {
+            if constexpr (Cfg::VAL_FAC) ok = wait(&rv_full[rv], i / NRV);
+            if (ok && i >= NF) ok = wait(&f_empty[fs], i / NF - 1);
+            if (!ok) break;
+            if constexpr (Cfg::VAL_FAC)
+              if (what >= 2 && live)
+                fac = key_factor<KV, D>(sRV + rv * Cfg::RV_STAGE + (what - 2) * Cfg::RV_HEAD + Cfg::RV_CODES, key);
+            sF[fs * 256 + ct] = fac;
+            __syncwarp();
+            if (lane == 0) {
+              q_arrive(&f_full[fs]);
+              if constexpr (Cfg::K8MMA) q_arrive(&rk_empty[rk]);
+            }
+          }
+        }
+        if (i >= 1) {  // V(i - 1), both heads
+          const int jj = i - 1, rv = jj % NRV, vs = jj % NV;
+          ok = wait(&rv_full[rv], jj / NRV);
+          if (ok && jj >= NV) ok = wait(&v_empty[vs], jj / NV - 1);
+          if (!ok) break;
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+            convert_tile<KV, D, Cfg::V_RB, NCT>(sRV + rv * Cfg::RV_STAGE + v * Cfg::RV_HEAD, Cfg::RV_CODES,
+                                                sV + vs * Cfg::V_STAGE + v * Cfg::F16, ct, w.F - 64 * (w.p_lo + jj));
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            q_arrive(&rv_empty[rv]);
+            q_arrive(&v_full[vs]);
+          }
+        }
+      }
+    }
+    if (!ok) *s_abort = 1;
+  } else if (warp == Cfg::NSOFT + 1) {
+    // ------------------------------ MMA issuer --------------------------------
+    if (lane == 0) {
+      bool ok = wait(q_ready, 0);
+      tc::fence_after();
+      for (int j = 0; ok && j <= n; ++j) {
+        if (j < n) {  // S(j) into buffer j & 1
+          const uint32_t s_at = tmem + Cfg::COL_S + 64 * (j & 1);
+          const int ring = Cfg::K_RAW ? NRK : NK, ks = j % ring;
+          ok = wait(Cfg::K_RAW ? &rk_full[ks] : &k_full[ks], j / ring);
+          if (!ok) break;
+          tc::fence_after();
+#pragma unroll
+          for (int h = 0; h < KH; ++h) {
+            const uint32_t qa = tmem + Cfg::COL_Q + h * (D / 2);
+#pragma unroll
+            for (int part = 0; part < (Cfg::K_SPLIT || Cfg::K8MMA ? 2 : 1); ++part) {
+              const uint8_t* tile = Cfg::K_RAW ? sRK + ks * Cfg::RK_STAGE + h * Cfg::RK_HEAD
+                                               : sK + ks * Cfg::K_STAGE + h * Cfg::K_HEAD + part * Cfg::F16;
+              const uint64_t kd = tc::smem_desc(smem_u32(tile), 16, 1024);
+              if constexpr (Cfg::K8MMA) {  // q_hi, then q_lo, in D / 4 columns each
+#pragma unroll
+                for (int kk = 0; kk < D / 32; ++kk)
+                  tc::mma_ts_f8(s_at, qa + part * (D / 4) + kk * 8,
+                                kd + static_cast<uint64_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), Cfg::ID_S,
+                                h > 0 || part > 0 || kk > 0);
+              } else {  // INT8-G64: Q k1^T - Q k2'^T
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                  tc::mma_ts(s_at, qa + kk * 8, kd + static_cast<uint64_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
+                             part > 0 ? tc::idesc_negate_b(Cfg::ID_S) : Cfg::ID_S, h > 0 || part > 0 || kk > 0);
+              }
+            }
+          }
+          tc::commit(&s_full[j & 1]);
+          tc::commit(Cfg::K_RAW ? &rk_empty[ks] : &k_empty[ks]);
+        }
+        if (j >= 1) {  // O += P(j - 1) V(j - 1)
+          const int jj = j - 1, vs = jj % NV;
+          ok = wait(&v_full[vs], jj / NV);
+          if (ok) ok = wait(&p_full[jj & 1], jj >> 1);
+          if (!ok) break;
+          tc::fence_after();
+#pragma unroll
+          for (int v = 0; v < (Cfg::VAL_FAC ? 2 : 1); ++v) {
+            const uint64_t vd = tc::smem_desc(smem_u32(sV + vs * Cfg::V_STAGE + v * Cfg::F16), 8192, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_ts(tmem + Cfg::COL_O + v * D, tmem + Cfg::COL_S + 64 * (jj & 1) + 32 * v + kk * 8,
+                         vd + static_cast<uint64_t>((kk * 2048) >> 4), Cfg::ID_O, (jj > 0 || kk > 0));
+          }
+          tc::commit(&o_done[jj & 1]);
+          tc::commit(&v_empty[vs]);
+        }
+      }
+      if (!ok) *s_abort = 1;
+      tc::commit(drain);  // arrives once every MMA issued above has completed
+    }
+  } else {
+    // ------------------------------ softmax warps -----------------------------
+    const int half = warp >> 2, m = tid & 127;  // query row = TMEM lane; keys [32 half, +32) of a page
+    const int map = BOTH ? m >> 6 : w.map, r = BOTH ? m & 63 : m;
+    const int tl = r / a.G, g = r % a.G, token = w.t0 + tl;
+    const bool valid = (BOTH || tl < a.TQ) && token < w.limit;
+    const int pos = w.pos0 + token;  // keys <= pos are visible
+    const uint32_t quad = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    float rs = 1.f;  // 2^-e of this query row
+    {
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + ((static_cast<int64_t>(w.b) * a.T + token) * a.Hq + 2 * (w.pair * a.G + g) + map) * D);
+      const uint32_t flip = a.negate ? 0x80008000u : 0u;
+      float qf = 1.f;
+      if constexpr (!Cfg::BF16) {
+        float mx = 0.f;
+        if (valid)
+          for (int u = 0; u < D / 8; ++u) {
+            const uint4 x = src[u];
+            const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(__bfloat162float(e[k])));
+          }
+        int ex = 0;
+        if (mx > 0.f) frexpf(mx, &ex);
+        // f16 q: max|q| 2^e in [2^14, 2^15); E4M3 q: max|q| 2^e in [2^7, 2^8)
+        const int e = mx > 0.f ? min((Cfg::K8MMA ? 8 : 15) - ex, 100) : 0;
+        qf = ldexpf(1.f, e);
+        rs = ldexpf(1.f, -e);
+      }
+      // this half's dims [half D / 2, +D / 2), 32 at a time; BOTH: zeros in the other map's operand
+      const uint32_t q_at = quad + Cfg::COL_Q + (BOTH ? map * (D / 2) : 0);
+      const uint32_t z_at = quad + Cfg::COL_Q + (map ^ 1) * (D / 2);
+      const uint32_t zero[16] = {};
+#pragma unroll 1
+      for (int d0 = half * (D / 2); d0 < (half + 1) * (D / 2); d0 += (Cfg::K8MMA ? 64 : 32)) {
+        if constexpr (Cfg::K8MMA) {  // q' = hi + lo in E4M3, as in qprefill.cu
+          uint32_t hv[16], lv[16];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const uint4 x = valid ? src[d0 / 8 + u] : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t xw[4] = {x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip};
+            uint32_t hp[4], lp[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float x0 = __uint_as_float(xw[k] << 16) * qf, x1 = __uint_as_float(xw[k] & 0xFFFF0000u) * qf;
+              const uint16_t h2 = f32x2_to_e4m3x2(x0, x1);
+              const uint32_t h32 = e4m3x2_to_f16x2(h2);
+              const __half2 hb = *reinterpret_cast<const __half2*>(&h32);
+              hp[k] = h2;
+              lp[k] = f32x2_to_e4m3x2(x0 - __low2float(hb), x1 - __high2float(hb));
+            }
+            hv[2 * u] = hp[0] | (hp[1] << 16);
+            hv[2 * u + 1] = hp[2] | (hp[3] << 16);
+            lv[2 * u] = lp[0] | (lp[1] << 16);
+            lv[2 * u + 1] = lp[2] | (lp[3] << 16);
+          }
+          tc::st16(q_at + d0 / 4, hv);
+          tc::st16(q_at + D / 4 + d0 / 4, lv);
+          if constexpr (BOTH) {
+            tc::st16(z_at + d0 / 4, zero);
+            tc::st16(z_at + D / 4 + d0 / 4, zero);
+          }
+        } else {
+          uint32_t qv[16];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint4 x = valid ? src[d0 / 8 + u] : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t xw[4] = {x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) qv[4 * u + k] = Cfg::BF16 ? xw[k] : bf16x2_lift(xw[k], qf);
+          }
+          tc::st16(q_at + d0 / 2, qv);
+          if constexpr (BOTH) tc::st16(z_at + d0 / 2, zero);
+        }
+      }
+      tc::wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) q_arrive(q_ready);
+    }
+    // what turns a raw score into one in base 2: per key and row, or for all keys
+    const float c_row = Cfg::KEY_FAC ? rs : fmaxf(a.scale_log2 * rs, 1.17549435e-38f);
+    const F2 c2 = pack2(c_row, c_row);
+    float m_used = -INFINITY, l = 0.f;
+    int k_run = KV == KIND_FP8 ? kVLiftInit : 0;  // FP8-row V: the weights, l and O carry 2^k_run, one lift for both heads
+    bool live = true;
+    for (int j = 0; j < n; ++j) {
+      const int sb = j & 1, fs = j % NF;
+      const uint32_t s_at = quad + Cfg::COL_S + 64 * sb;
+      if (live) live = wait(&s_full[sb], j >> 1);
+      if constexpr (Cfg::HAS_F)
+        if (live) live = wait(&f_full[fs], j / NF);
+      tc::fence_after();
+      uint32_t sv[32];
+      tc::ld32(s_at + 32 * half, sv);
+      tc::wait_ld();
+      const float* ksc = sF + fs * 256 + (BOTH ? 64 * map : 0) + 32 * half;
+      const float* vsc = sF + fs * 256 + 128;
+      const int kmax = (valid ? pos - 64 * (w.p_lo + j) : -1) - 32 * half;  // of this half's keys
+      if constexpr (Cfg::KEY_FAC) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 k4 = *reinterpret_cast<const float4*>(ksc + c);
+          float x[4];
+          unpack2(mul2(pack2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), pack2(k4.x, k4.y)), x[0], x[1]);
+          unpack2(mul2(pack2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), pack2(k4.z, k4.w)), x[2], x[3]);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) sv[c + u] = __float_as_uint(x[u]);
+        }
+      }
+      if (!__all_sync(0xffffffffu, kmax >= 31)) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (c > kmax) sv[c] = 0xFF800000u;  // -inf
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) top = max3(top, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+      // the row's maximum over both halves (both have read their S by then, so
+      // that P may go over it)
+      float* x_at = sX + sb * 256 + m;
+      x_at[128 * half] = top;
+      asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3)) : "memory");
+      top = fmaxf(top, x_at[128 * (half ^ 1)]);
+      const float rmax = top == -INFINITY ? -INFINITY : top * c_row;
+      int knew = k_run;
+      if constexpr (KV == KIND_FP8) {
+        const float4 s4 = *reinterpret_cast<const float4*>(vsc + 4 * lane);  // both heads' 128 scales
+        knew = v_lift(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(s4.x, s4.y), fmaxf(s4.z, s4.w)))), k_run);
+      }
+      // lazy: the reference moves when a score passes it by more than 2^8, or the lift drops
+      float factor = 1.f;
+      const float mnew = fmaxf(m_used, rmax);
+      bool resc = false;
+      if (mnew != -INFINITY && (m_used == -INFINITY || mnew > m_used + kLazyThr || knew != k_run)) {
+        factor = m_used == -INFINITY ? 0.f : ex2((m_used - mnew) + static_cast<float>(knew - k_run));
+        m_used = mnew;
+        resc = true;
+      }
+      k_run = knew;
+      const float mu = m_used == -INFINITY ? 0.f : m_used - static_cast<float>(k_run);
+      const F2 mu2 = pack2(-mu, -mu);
+      F2 sum2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        float x, y;
+        unpack2(fma2(pack2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), c2, mu2), x, y);
+        x = ex2(x);
+        y = ex2(y);
+        sum2[(c >> 1) & 1] = add2(sum2[(c >> 1) & 1], pack2(x, y));
+        sv[c] = __float_as_uint(x);
+        sv[c + 1] = __float_as_uint(y);
+      }
+      float s0, s1;
+      unpack2(add2(sum2[0], sum2[1]), s0, s1);
+      l = l * factor + (s0 + s1);
+      bool strips = false;  // BF16 values: a strip's k fell
+      if constexpr (Cfg::BF16) strips = *reinterpret_cast<const unsigned long long*>(sF + fs * 256) != 0ull;
+      // PV(j - 2) is complete (so the other P buffer's barriers may turn), and
+      // PV(j - 1) before a rescale
+      if (j >= 2 && live) live = wait(&o_done[sb], (j - 2) >> 1);
+      if (j >= 1 && __any_sync(0xffffffffu, resc || strips)) {
+        if (live) live = wait(&o_done[sb ^ 1], (j - 1) >> 1);
+        tc::fence_after();
+        const float f = resc ? factor : 1.f;
+#pragma unroll 1
+        for (int c0 = half * D; c0 < (half + 1) * D; c0 += 16) {
+          uint32_t ov[16];
+          tc::ld16(quad + Cfg::COL_O + c0, ov);
+          tc::wait_ld();
+          float fc = f;
+          if constexpr (Cfg::BF16) fc *= sF[fs * 256 + 8 + c0 / Cfg::STRIP];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * fc);
+          tc::st16(quad + Cfg::COL_O + c0, ov);
+        }
+      }
+      // P over the S that was read: this half's 16 columns, of each head's P
+#pragma unroll
+      for (int v = 0; v < (Cfg::VAL_FAC ? 2 : 1); ++v) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          float p[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) p[u] = __uint_as_float(sv[c + u]);
+          if constexpr (Cfg::VAL_FAC) {
+            const float4 s = *reinterpret_cast<const float4*>(vsc + 64 * v + 32 * half + c);
+            unpack2(mul2(pack2(p[0], p[1]), pack2(s.x, s.y)), p[0], p[1]);
+            unpack2(mul2(pack2(p[2], p[3]), pack2(s.z, s.w)), p[2], p[3]);
+          }
+          pk[c / 2] = pack_f16x2(p[0], p[1]);
+          pk[c / 2 + 1] = pack_f16x2(p[2], p[3]);
+        }
+        tc::st16(s_at + 32 * v + 16 * half, pk);
+      }
+      tc::wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (Cfg::HAS_F) q_arrive(&f_empty[fs]);  // this warp is done with the page's factors
+        q_arrive(&p_full[sb]);
+      }
+    }
+    // ---- this CTA's partial: (m, l) of the row, and O, the half's D dims -------------
+    if (n > 0 && live) live = wait(&o_done[(n - 1) & 1], (n - 1) >> 1);
+    tc::fence_after();
+    if (!live) *s_abort = 1;
+    float* x_at = sX + (n & 1) * 256 + m;
+    x_at[128 * half] = l;
+    asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3)) : "memory");
+    l += x_at[128 * (half ^ 1)];
+    if (live) {
+      const float m_eff = m_used == -INFINITY ? -INFINITY : m_used - static_cast<float>(k_run);
+      if (valid && half == 0) a.ws_ml[w.part * 128 + m] = make_float2(m_eff, l);
+      if (n > 0 && (!BOTH || __any_sync(0xffffffffu, valid))) {
+        float* dst = a.ws_o + (w.part * 128 + m) * (2 * D);
+#pragma unroll 1
+        for (int c0 = half * D; c0 < (half + 1) * D; c0 += 16) {
+          uint32_t v[16];
+          tc::ld16(quad + Cfg::COL_O + c0, v);
+          tc::wait_ld();
+          if constexpr (Cfg::BF16) {
+            const float f = pow2i(-reinterpret_cast<const int*>(sF + ((n - 1) % NF) * 256)[16 + c0 / Cfg::STRIP]);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * f);
+          }
+          if (valid) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<uint4*>(dst + c0 + 4 * c) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+          }
+        }
+      }
+    }
+  }
+
+  // ---- teardown: every issued MMA has completed before TMEM is freed ---------
+  if (tid == 0) mbar_wait_bounded(drain, 0, a.status, 200000000ull);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 0) tc::dealloc(tmem, 512);
+}
+
+template <int KK, int KV, int D, bool BOTH>
+cudaError_t launch_diff_tile(const nk_pool* p, int layer, const DiffTileArgs& a, dim3 grid, cudaStream_t s) {
+  using Cfg = DiffTileCfg<KK, KV, D, BOTH>;
+  auto k = diff_tile_kernel<KK, KV, D, BOTH>;
+  static std::atomic<uint64_t> granted{0};
+  const cudaError_t e = grant_smem(granted, k, Cfg::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
+}
+
+template <int KK, int KV>
+cudaError_t diff_tile_dispatch(const nk_pool* p, int layer, const DiffTileArgs& a, bool both, dim3 grid, cudaStream_t s) {
+  if (p->desc.head_dim == 64)
+    return both ? launch_diff_tile<KK, KV, 64, true>(p, layer, a, grid, s)
+                : launch_diff_tile<KK, KV, 64, false>(p, layer, a, grid, s);
+  return both ? launch_diff_tile<KK, KV, 128, true>(p, layer, a, grid, s)
+              : launch_diff_tile<KK, KV, 128, false>(p, layer, a, grid, s);
+}
+
+using DiffTileFn = cudaError_t (*)(const nk_pool*, int layer, const DiffTileArgs&, bool both, dim3 grid, cudaStream_t);
+cudaError_t diff_tile_bf16(const nk_pool*, int, const DiffTileArgs&, bool, dim3, cudaStream_t);
+cudaError_t diff_tile_int8(const nk_pool*, int, const DiffTileArgs&, bool, dim3, cudaStream_t);
+cudaError_t diff_tile_fp8(const nk_pool*, int, const DiffTileArgs&, bool, dim3, cudaStream_t);
+cudaError_t diff_tile_nvfp4(const nk_pool*, int, const DiffTileArgs&, bool, dim3, cudaStream_t);
+cudaError_t diff_tile_k8v4(const nk_pool*, int, const DiffTileArgs&, bool, dim3, cudaStream_t);
+
+// The instantiations of a profile, and the arguments that every call shares.
+inline DiffTileFn diff_tile_for(int profile) {
+  switch (profile) {
+    case NK_BF16: return diff_tile_bf16;
+    case NK_INT8_G64: return diff_tile_int8;
+    case NK_FP8_E4M3_ROW: return diff_tile_fp8;
+    case NK_NVFP4_G16: return diff_tile_nvfp4;
+    default: return diff_tile_k8v4;
+  }
+}
+
+inline DiffTileArgs diff_tile_args(const nk_pool* pool, int layer, const void* q, int Hq, const int32_t* tables,
+                                   const int32_t* table_rows, const int32_t* lengths, int B, int T, float softmax_scale,
+                                   void* ws, size_t ml_bytes) {
+  DiffTileArgs a = {};
+  const int np = pool->n_planes;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.tables = tables;
+  a.table_rows = table_rows;
+  a.lengths = lengths;
+  a.ks = np == 4 ? static_cast<const uint8_t*>(pool->ptrs[layer * np + 2]) : nullptr;
+  a.vs = np == 4 ? static_cast<const uint8_t*>(pool->ptrs[layer * np + 3]) : nullptr;
+  a.ws_ml = static_cast<float2*>(ws);
+  a.ws_o = reinterpret_cast<float*>(static_cast<char*>(ws) + ml_bytes);
+  a.status = pool->status;
+  // masked scores are -inf times the scale: 0 becomes the least normal number,
+  // which no finite score makes visible
+  a.scale_log2 = fmaxf(fabsf(softmax_scale) * kDiffLog2e, 1.17549435e-38f);
+  a.negate = softmax_scale < 0.f;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.H = pool->desc.num_kv_heads;
+  a.G = Hq / a.H;
+  a.L = pool->L;
+  a.M = pool->M;
+  a.C = pool->desc.max_concurrency;
+  a.head_major = pool->desc.order == NK_HEAD_MAJOR;
+  return a;
+}
+
+}  // namespace nk
