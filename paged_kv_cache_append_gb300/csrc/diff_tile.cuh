@@ -24,18 +24,22 @@
 //   * FP8-row and INT8-G64 values leave a factor per key to the weights, so each
 //     head has its own P (columns [0, 32) and [32, 64) of the S buffer), N = D twice;
 //   * BF16 values are rewritten in place, v 2^k with a power of two per strip of 2 D /
-//     8 dims that brings the strip's largest value so far to [2^10, 2^15): exact for
-//     every element above its 2^-27th.  k only falls (then O is rescaled), and the
-//     store divides it out.
+//     8 dims that brings the strip's largest value so far below 2^15 and above 2^-3
+//     (0 while it is there by itself): exact for every element above its 2^-14th, and
+//     to 2^-22 of the largest below.  k only falls (then O is rescaled), and the store
+//     divides it out.
 // FP8-row value factors are lifted by a power of two of their own (v_lift).
 //
 // Warps (576 threads): 0-7 softmax, warp w lanes 32 (w & 3) and keys 32 (w >> 2) of
-// a page (the two warps of a row exchange its maximum through shared memory and move
-// the reference lazily); 8 TMA producer; 9 MMA issuer; 10-17 converters.
+// a page; 8 TMA producer; 9 MMA issuer; 10-17 converters.  The two warps of a row
+// tell each other its maximum while they already take the exponentials under the old
+// reference, which moves lazily (by a score more than 2^8 above it); only then are
+// they taken again.  The MMAs are issued by an elected lane of a warp that runs the
+// loop as a whole: from a branch of one lane each issue took 47-54 cycles (probe:
+// M 128, N 64, A in tensor memory), from the whole warp the 33 of the tensor core.
 //
-// All waits are bounded.  Where warps meet at named barriers, a wait that ran out
-// lets the loop run on without waiting, so that they stay matched; the CTA leaves
-// without results once the copies in flight have landed.
+// All waits are bounded; a wait that ran out ends its warp's work, the others' waits
+// run out too, and the CTA leaves without results once the copies in flight landed.
 #pragma once
 
 #include "diff.cuh"
@@ -100,7 +104,7 @@ struct DiffTileCfg {
   static constexpr int OFF_F = OFF_RV + NRV * RV_STAGE;
   static constexpr int OFF_X = OFF_F + NF * 1024;  // [2][2][128] maxima of the rows' halves
   static constexpr int OFF_BAR = OFF_X + 2048;
-  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NRK + 2 * NRV + 2 * NF + 8;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NRK + 2 * NRV + 2 * NF + 8 + 16;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 64 + 1024;
   static constexpr uint32_t COL_S = 0, COL_Q = 128, COL_O = 256;
   static constexpr uint32_t ID_S = K8MMA  ? tc::idesc_e4m3(128, 64)
@@ -179,8 +183,19 @@ __device__ __forceinline__ DiffWork diff_decode_work(const DiffTileArgs& a, int*
   return w;
 }
 
+// True in one lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ uint32_t bf16x2_lift(uint32_t w, float f) {  // two bf16 values times f as f16x2
   return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+}
+
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
+  return pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
 // Converter warps of BF16 values: warp cw rewrites its strip of every staged V
@@ -226,10 +241,10 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
   uint64_t* o_done = p_full + 2;    // [2]
   uint64_t* q_ready = o_done + 2;
   uint64_t* drain = q_ready + 1;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
+  uint64_t* x_full = drain + 1;  // [2][8] a softmax warp's maxima of a page are there
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(x_full + 16);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   griddep_wait();  // launched with programmatic stream serialization
   griddep_launch_dependents();
   DiffWork w;
@@ -269,7 +284,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     }
     mbar_init(q_ready, Cfg::NSOFT);
     mbar_init(drain, 1);
-    *s_abort = 0;
+    for (int i = 0; i < 16; ++i) mbar_init(&x_full[i], 1);
     fence_barrier_init();
     prefetch_tmap(&tmk);
     prefetch_tmap(&tmv);
@@ -282,7 +297,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tslot;
-  const auto wait = [&](uint64_t* bar, int use) { return mbar_wait_bounded(bar, use & 1, a.status) && !*s_abort; };
+  const auto wait = [&](uint64_t* bar, int use) { return mbar_wait_bounded(bar, use & 1, a.status); };
 
   if (warp == Cfg::NSOFT) {
     // ------------- TMA producer: code and scale tiles of each page ---------------
@@ -329,7 +344,6 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
           }
           ++nv;
         }
-        if (stop) *s_abort = 1;
       }
       if (__shfl_sync(0xffffffffu, stop, 0)) break;
     }
@@ -352,7 +366,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
         if (!ok) break;
         uint8_t* tile = sV + vs * Cfg::V_STAGE + blk;
         uint4 v[St::UNITS];
-        uint32_t most = 0u;  // largest magnitudes of the pairs' low and high halves
+        __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);  // largest magnitudes
         int off[St::UNITS];
 #pragma unroll
         for (int u = 0; u < St::UNITS; ++u) {
@@ -360,15 +374,26 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
           off[u] = r * 128 + ((c ^ (r & 7)) << 4);
           v[u] = *reinterpret_cast<const uint4*>(tile + off[u]);
           if (r >= kvalid) v[u] = make_uint4(0u, 0u, 0u, 0u);  // stale keys
-          most = __vmaxu2(most, __vmaxu2(__vmaxu2(v[u].x & 0x7FFF7FFFu, v[u].y & 0x7FFF7FFFu),
-                                         __vmaxu2(v[u].z & 0x7FFF7FFFu, v[u].w & 0x7FFF7FFFu)));
         }
-        most = __reduce_max_sync(0xffffffffu, max(most & 0xFFFFu, most >> 16));
-        // a new k where the strip's largest value leaves [., 2^15), and on its first page
-        const int e = static_cast<int>(most >> 7) - 127;
+#pragma unroll
+        for (int u = 0; u < St::UNITS; ++u) {
+          const uint32_t w4[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w4[c])));
+        }
+        const uint32_t both = *reinterpret_cast<const uint32_t*>(&top2);
+        const uint32_t mine = max(both & 0xFFFFu, both >> 16);
+        // k stays 0 while the strip's largest value lies in [2^-3, 2^15) (its first
+        // page) and below 2^15 (later): no lift to apply
         const int was = k;
-        if (i == 0) k = strip_lift(most);
-        else if (most && e + k >= 15) k = min(k, strip_lift(most));
+        const bool plain = k == 0 && !__any_sync(0xffffffffu, mine >= 0x4700u) &&
+                           (i > 0 || __any_sync(0xffffffffu, mine >= 0x3E00u));
+        if (!plain) {
+          const uint32_t most = __reduce_max_sync(0xffffffffu, mine);
+          const int e = static_cast<int>(most >> 7) - 127;
+          if (i == 0) k = strip_lift(most);
+          else if (most && e + k >= 15) k = min(k, strip_lift(most));
+        }
         if (i >= NF) ok = wait(&f_empty[fs], i / NF - 1);
         if (!ok) break;
         if (lane == 0) {
@@ -377,11 +402,18 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
           slot[8 + cw] = pow2i(i > 0 ? max(k - was, -126) : 0);
           reinterpret_cast<int*>(slot)[16 + cw] = k;
         }
-        const float f = pow2i(k);
+        if (plain) {
 #pragma unroll
-        for (int u = 0; u < St::UNITS; ++u)
-          *reinterpret_cast<uint4*>(tile + off[u]) = make_uint4(bf16x2_lift(v[u].x, f), bf16x2_lift(v[u].y, f),
-                                                                bf16x2_lift(v[u].z, f), bf16x2_lift(v[u].w, f));
+          for (int u = 0; u < St::UNITS; ++u)
+            *reinterpret_cast<uint4*>(tile + off[u]) = make_uint4(bf16x2_to_f16x2(v[u].x), bf16x2_to_f16x2(v[u].y),
+                                                                  bf16x2_to_f16x2(v[u].z), bf16x2_to_f16x2(v[u].w));
+        } else {
+          const float f = pow2i(k);
+#pragma unroll
+          for (int u = 0; u < St::UNITS; ++u)
+            *reinterpret_cast<uint4*>(tile + off[u]) = make_uint4(bf16x2_lift(v[u].x, f), bf16x2_lift(v[u].y, f),
+                                                                  bf16x2_lift(v[u].z, f), bf16x2_lift(v[u].w, f));
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
@@ -453,19 +485,18 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
         }
       }
     }
-    if (!ok) *s_abort = 1;
   } else if (warp == Cfg::NSOFT + 1) {
     // ------------------------------ MMA issuer --------------------------------
-    if (lane == 0) {
-      bool ok = wait(q_ready, 0);
-      tc::fence_after();
-      for (int j = 0; ok && j <= n; ++j) {
-        if (j < n) {  // S(j) into buffer j & 1
-          const uint32_t s_at = tmem + Cfg::COL_S + 64 * (j & 1);
-          const int ring = Cfg::K_RAW ? NRK : NK, ks = j % ring;
-          ok = wait(Cfg::K_RAW ? &rk_full[ks] : &k_full[ks], j / ring);
-          if (!ok) break;
-          tc::fence_after();
+    bool ok = wait(q_ready, 0);
+    tc::fence_after();
+    for (int j = 0; j <= n; ++j) {
+      if (j < n) {  // S(j) into buffer j & 1
+        const uint32_t s_at = tmem + Cfg::COL_S + 64 * (j & 1);
+        const int ring = Cfg::K_RAW ? NRK : NK, ks = j % ring;
+        ok = ok && wait(Cfg::K_RAW ? &rk_full[ks] : &k_full[ks], j / ring);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc::fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int h = 0; h < KH; ++h) {
             const uint32_t qa = tmem + Cfg::COL_Q + h * (D / 2);
@@ -491,12 +522,14 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
           tc::commit(&s_full[j & 1]);
           tc::commit(Cfg::K_RAW ? &rk_empty[ks] : &k_empty[ks]);
         }
-        if (j >= 1) {  // O += P(j - 1) V(j - 1)
-          const int jj = j - 1, vs = jj % NV;
-          ok = wait(&v_full[vs], jj / NV);
-          if (ok) ok = wait(&p_full[jj & 1], jj >> 1);
-          if (!ok) break;
-          tc::fence_after();
+        __syncwarp();
+      }
+      if (j >= 1) {  // O += P(j - 1) V(j - 1)
+        const int jj = j - 1, vs = jj % NV;
+        ok = ok && wait(&v_full[vs], jj / NV) && wait(&p_full[jj & 1], jj >> 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc::fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int v = 0; v < (Cfg::VAL_FAC ? 2 : 1); ++v) {
             const uint64_t vd = tc::smem_desc(smem_u32(sV + vs * Cfg::V_STAGE + v * Cfg::F16), 8192, 1024);
@@ -508,10 +541,11 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
           tc::commit(&o_done[jj & 1]);
           tc::commit(&v_empty[vs]);
         }
+        __syncwarp();
       }
-      if (!ok) *s_abort = 1;
-      tc::commit(drain);  // arrives once every MMA issued above has completed
     }
+    __syncwarp();
+    if (elect_one()) tc::commit(drain);  // arrives once every MMA issued above has completed
   } else {
     // ------------------------------ softmax warps -----------------------------
     const int half = warp >> 2, m = tid & 127;  // query row = TMEM lane; keys [32 half, +32) of a page
@@ -598,20 +632,56 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     const F2 c2 = pack2(c_row, c_row);
     float m_used = -INFINITY, l = 0.f;
     int k_run = KV == KIND_FP8 ? kVLiftInit : 0;  // FP8-row V: the weights, l and O carry 2^k_run, one lift for both heads
+    const int mate = warp ^ 4;  // the warp of the rows' other keys
+    uint32_t sv[32], pk[Cfg::VAL_FAC ? 2 : 1][16];
+    float mu = 0.f;
+    // The weights of this half's keys under the reference mu into pk; returns their sum.
+    const auto weights = [&](const float* vsc) {
+      const F2 mu2 = pack2(-mu, -mu);
+      F2 sum2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        float p[4];
+#pragma unroll
+        for (int u = 0; u < 4; u += 2) {
+          unpack2(fma2(pack2(__uint_as_float(sv[c + u]), __uint_as_float(sv[c + u + 1])), c2, mu2), p[u], p[u + 1]);
+          p[u] = ex2(p[u]);
+          p[u + 1] = ex2(p[u + 1]);
+          sum2[u >> 1] = add2(sum2[u >> 1], pack2(p[u], p[u + 1]));
+        }
+        if constexpr (Cfg::VAL_FAC) {
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const float4 f = *reinterpret_cast<const float4*>(vsc + 64 * v + c);
+            float x[4];
+            unpack2(mul2(pack2(p[0], p[1]), pack2(f.x, f.y)), x[0], x[1]);
+            unpack2(mul2(pack2(p[2], p[3]), pack2(f.z, f.w)), x[2], x[3]);
+            pk[v][c / 2] = pack_f16x2(x[0], x[1]);
+            pk[v][c / 2 + 1] = pack_f16x2(x[2], x[3]);
+          }
+        } else {
+          pk[0][c / 2] = pack_f16x2(p[0], p[1]);
+          pk[0][c / 2 + 1] = pack_f16x2(p[2], p[3]);
+        }
+      }
+      float s0, s1;
+      unpack2(add2(sum2[0], sum2[1]), s0, s1);
+      return s0 + s1;
+    };
     bool live = true;
     for (int j = 0; j < n; ++j) {
       const int sb = j & 1, fs = j % NF;
       const uint32_t s_at = quad + Cfg::COL_S + 64 * sb;
-      if (live) live = wait(&s_full[sb], j >> 1);
-      if constexpr (Cfg::HAS_F)
-        if (live) live = wait(&f_full[fs], j / NF);
+      live = live && wait(&s_full[sb], j >> 1);
+      // PV(j - 2) is complete with S(j): its barrier, and the other P buffer's, may turn
+      if (j >= 2) live = live && wait(&o_done[sb], (j - 2) >> 1);
       tc::fence_after();
-      uint32_t sv[32];
       tc::ld32(s_at + 32 * half, sv);
-      tc::wait_ld();
+      if constexpr (Cfg::HAS_F) live = live && wait(&f_full[fs], j / NF);
       const float* ksc = sF + fs * 256 + (BOTH ? 64 * map : 0) + 32 * half;
       const float* vsc = sF + fs * 256 + 128;
       const int kmax = (valid ? pos - 64 * (w.p_lo + j) : -1) - 32 * half;  // of this half's keys
+      tc::wait_ldn(sv);
       if constexpr (Cfg::KEY_FAC) {
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
@@ -628,103 +698,78 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
         for (int c = 0; c < 32; ++c)
           if (c > kmax) sv[c] = 0xFF800000u;  // -inf
       }
-      float top = -INFINITY;
+      float top4[4];
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) top = max3(top, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-      // the row's maximum over both halves (both have read their S by then, so
-      // that P may go over it)
-      float* x_at = sX + sb * 256 + m;
-      x_at[128 * half] = top;
-      asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3)) : "memory");
-      top = fmaxf(top, x_at[128 * (half ^ 1)]);
-      const float rmax = top == -INFINITY ? -INFINITY : top * c_row;
+      for (int u = 0; u < 4; ++u) top4[u] = fmaxf(__uint_as_float(sv[u]), __uint_as_float(sv[4 + u]));
+#pragma unroll
+      for (int c = 8; c < 32; c += 8)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) top4[u] = max3(top4[u], __uint_as_float(sv[c + u]), __uint_as_float(sv[c + 4 + u]));
+      float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
+      sX[sb * 256 + 128 * half + m] = top;
+      __syncwarp();
+      if (lane == 0) q_arrive(&x_full[8 * sb + warp]);  // and: this half has read its S, so P may go over it
+      float sum = 0.f;
+      if (j > 0) sum = weights(vsc + 32 * half);
       int knew = k_run;
       if constexpr (KV == KIND_FP8) {
         const float4 s4 = *reinterpret_cast<const float4*>(vsc + 4 * lane);  // both heads' 128 scales
         knew = v_lift(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(s4.x, s4.y), fmaxf(s4.z, s4.w)))), k_run);
       }
+      bool strips = false;  // BF16 values: a strip's k fell
+      if constexpr (Cfg::BF16) strips = *reinterpret_cast<const unsigned long long*>(sF + fs * 256) != 0ull;
+      live = live && wait(&x_full[8 * sb + mate], j >> 1);
+      top = fmaxf(top, sX[sb * 256 + 128 * (half ^ 1) + m]);
+      const float rmax = top == -INFINITY ? -INFINITY : top * c_row;
       // lazy: the reference moves when a score passes it by more than 2^8, or the lift drops
       float factor = 1.f;
       const float mnew = fmaxf(m_used, rmax);
-      bool resc = false;
-      if (mnew != -INFINITY && (m_used == -INFINITY || mnew > m_used + kLazyThr || knew != k_run)) {
-        factor = m_used == -INFINITY ? 0.f : ex2((m_used - mnew) + static_cast<float>(knew - k_run));
-        m_used = mnew;
-        resc = true;
-      }
-      k_run = knew;
-      const float mu = m_used == -INFINITY ? 0.f : m_used - static_cast<float>(k_run);
-      const F2 mu2 = pack2(-mu, -mu);
-      F2 sum2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
-#pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        float x, y;
-        unpack2(fma2(pack2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), c2, mu2), x, y);
-        x = ex2(x);
-        y = ex2(y);
-        sum2[(c >> 1) & 1] = add2(sum2[(c >> 1) & 1], pack2(x, y));
-        sv[c] = __float_as_uint(x);
-        sv[c + 1] = __float_as_uint(y);
-      }
-      float s0, s1;
-      unpack2(add2(sum2[0], sum2[1]), s0, s1);
-      l = l * factor + (s0 + s1);
-      bool strips = false;  // BF16 values: a strip's k fell
-      if constexpr (Cfg::BF16) strips = *reinterpret_cast<const unsigned long long*>(sF + fs * 256) != 0ull;
-      // PV(j - 2) is complete (so the other P buffer's barriers may turn), and
-      // PV(j - 1) before a rescale
-      if (j >= 2 && live) live = wait(&o_done[sb], (j - 2) >> 1);
-      if (j >= 1 && __any_sync(0xffffffffu, resc || strips)) {
-        if (live) live = wait(&o_done[sb ^ 1], (j - 1) >> 1);
-        tc::fence_after();
-        const float f = resc ? factor : 1.f;
+      const bool resc =
+          mnew != -INFINITY && (m_used == -INFINITY || mnew > m_used + kLazyThr || knew != k_run);
+      if (j == 0 || __any_sync(0xffffffffu, resc || strips || knew != k_run)) {
+        if (resc) {
+          factor = m_used == -INFINITY ? 0.f : ex2((m_used - mnew) + static_cast<float>(knew - k_run));
+          m_used = mnew;
+        }
+        k_run = knew;
+        mu = m_used == -INFINITY ? 0.f : m_used - static_cast<float>(k_run);
+        sum = weights(vsc + 32 * half);
+        if (j >= 1) {  // O of this half's dims, once PV(j - 1) is complete
+          live = live && wait(&o_done[sb ^ 1], (j - 1) >> 1);
+          tc::fence_after();
 #pragma unroll 1
-        for (int c0 = half * D; c0 < (half + 1) * D; c0 += 16) {
-          uint32_t ov[16];
-          tc::ld16(quad + Cfg::COL_O + c0, ov);
-          tc::wait_ld();
-          float fc = f;
-          if constexpr (Cfg::BF16) fc *= sF[fs * 256 + 8 + c0 / Cfg::STRIP];
+          for (int c0 = half * D; c0 < (half + 1) * D; c0 += 16) {
+            uint32_t ov[16];
+            tc::ld16(quad + Cfg::COL_O + c0, ov);
+            tc::wait_ld();
+            float fc = factor;
+            if constexpr (Cfg::BF16) fc *= sF[fs * 256 + 8 + c0 / Cfg::STRIP];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * fc);
-          tc::st16(quad + Cfg::COL_O + c0, ov);
+            for (int c = 0; c < 16; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * fc);
+            tc::st16(quad + Cfg::COL_O + c0, ov);
+          }
         }
       }
+      l = l * factor + sum;
       // P over the S that was read: this half's 16 columns, of each head's P
 #pragma unroll
-      for (int v = 0; v < (Cfg::VAL_FAC ? 2 : 1); ++v) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          float p[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) p[u] = __uint_as_float(sv[c + u]);
-          if constexpr (Cfg::VAL_FAC) {
-            const float4 s = *reinterpret_cast<const float4*>(vsc + 64 * v + 32 * half + c);
-            unpack2(mul2(pack2(p[0], p[1]), pack2(s.x, s.y)), p[0], p[1]);
-            unpack2(mul2(pack2(p[2], p[3]), pack2(s.z, s.w)), p[2], p[3]);
-          }
-          pk[c / 2] = pack_f16x2(p[0], p[1]);
-          pk[c / 2 + 1] = pack_f16x2(p[2], p[3]);
-        }
-        tc::st16(s_at + 32 * v + 16 * half, pk);
-      }
+      for (int v = 0; v < (Cfg::VAL_FAC ? 2 : 1); ++v) tc::st16(s_at + 32 * v + 16 * half, pk[v]);
       tc::wait_st();
       tc::fence_before();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (Cfg::HAS_F) q_arrive(&f_empty[fs]);  // this warp is done with the page's factors
         q_arrive(&p_full[sb]);
+        if constexpr (Cfg::HAS_F) q_arrive(&f_empty[fs]);  // this warp is done with the page's factors
       }
     }
     // ---- this CTA's partial: (m, l) of the row, and O, the half's D dims -------------
     if (n > 0 && live) live = wait(&o_done[(n - 1) & 1], (n - 1) >> 1);
     tc::fence_after();
-    if (!live) *s_abort = 1;
-    float* x_at = sX + (n & 1) * 256 + m;
-    x_at[128 * half] = l;
-    asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3)) : "memory");
-    l += x_at[128 * (half ^ 1)];
+    sX[(n & 1) * 256 + 128 * half + m] = l;
+    __syncwarp();
+    if (lane == 0) q_arrive(&x_full[8 * (n & 1) + warp]);
+    live = live && wait(&x_full[8 * (n & 1) + mate], n >> 1);
+    l += sX[(n & 1) * 256 + 128 * (half ^ 1) + m];
     if (live) {
       const float m_eff = m_used == -INFINITY ? -INFINITY : m_used - static_cast<float>(k_run);
       if (valid && half == 0) a.ws_ml[w.part * 128 + m] = make_float2(m_eff, l);
