@@ -26,7 +26,7 @@
 //   * BF16 values are rewritten in place, v 2^k with a power of two per strip of 2 D /
 //     8 dims that brings the strip's largest value so far below 2^15 and above 2^-3
 //     (0 while it is there by itself): exact for every element above its 2^-14th, and
-//     to 2^-22 of the largest below.  k only falls (then O is rescaled), and the store
+//     to 2^-19 of the largest below.  k only falls (then O is rescaled), and the store
 //     divides it out.
 // FP8-row value factors are lifted by a power of two of their own (v_lift).
 //
@@ -194,16 +194,27 @@ __device__ __forceinline__ uint32_t bf16x2_lift(uint32_t w, float f) {  // two b
   return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
 }
 
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
-  return pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+// |v| 2^-112 of two bf16 values: the exponent field of an f16, for |v| < 2^16
+// (below 2^-14 gradually, to 2^-21).
+__device__ __forceinline__ uint32_t bf16x2_rebias(uint32_t w) {
+  const uint32_t k = 0x07800780u;  // 2^-112
+  const __nv_bfloat162 r =
+      __hmul2(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)), *reinterpret_cast<const __nv_bfloat162*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The f16 pair of bf16 values w from their rebiased magnitudes.
+__device__ __forceinline__ uint32_t f16x2_of(uint32_t rebiased, uint32_t w) {
+  return (rebiased << 3) | (w & 0x80008000u);
 }
 
 // Converter warps of BF16 values: warp cw rewrites its strip of every staged V
 // tile, bf16 -> f16 of v 2^k in place, and publishes what its k did.
 template <int D>
 struct StripOf {
-  static constexpr int CH = 2 * D / 8 / 8;  // 16-byte chunks of the strip in a key's row
-  static constexpr int UNITS = 64 * CH / 32;
+  static constexpr int CH = 2 * D / 8 / 8;   // 16-byte chunks of the strip in a key's row
+  static constexpr int ROWS = 32 / CH;       // keys that a warp access covers
+  static constexpr int UNITS = 64 / ROWS;
 };
 
 // 2^k that takes the largest bf16 magnitude (its 15 bits) to [2^10, 2^11).
@@ -358,7 +369,12 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       // ------------- converters of BF16 values: a strip of dims per warp -----------
       using St = StripOf<D>;
       const int cw = ct >> 5, col = cw * Cfg::STRIP;
-      const int chunk0 = (col % 64) / 8, blk = (col / D) * Cfg::F16 + (col % D) / 64 * 8192;
+      const int blk = (col / D) * Cfg::F16 + (col % D) / 64 * 8192;
+      // lane: chunk lane % CH of a key; the keys of eight lanes are apart, so that their
+      // swizzled chunks lie in different banks
+      const int row0 = D == 128 ? (lane >> 3) + 4 * ((lane >> 2) & 1)
+                                : ((lane >> 3) & 1) + 2 * ((lane >> 1) & 3) + 8 * (lane >> 4);
+      const int off0 = row0 * 128 + ((((col % 64) / 8 + lane % St::CH) ^ (row0 & 7)) << 4);
       int k = 0;
       for (int i = 0; ok && i < n; ++i) {
         const int vs = i % NV, fs = i % NF, kvalid = w.F - 64 * (w.p_lo + i);
@@ -366,33 +382,47 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
         if (!ok) break;
         uint8_t* tile = sV + vs * Cfg::V_STAGE + blk;
         uint4 v[St::UNITS];
-        __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);  // largest magnitudes
-        int off[St::UNITS];
+#pragma unroll
+        for (int u = 0; u < St::UNITS; ++u) v[u] = *reinterpret_cast<const uint4*>(tile + off0 + u * St::ROWS * 128);
+        if (kvalid < 64) {  // stale keys are zeros
+#pragma unroll
+          for (int u = 0; u < St::UNITS; ++u)
+            if (row0 + u * St::ROWS >= kvalid) v[u] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        uint32_t top2 = 0u;  // largest rebiased magnitudes
+        uint4 h[St::UNITS];
 #pragma unroll
         for (int u = 0; u < St::UNITS; ++u) {
-          const int x = u * 32 + lane, r = x / St::CH, c = chunk0 + x % St::CH;
-          off[u] = r * 128 + ((c ^ (r & 7)) << 4);
-          v[u] = *reinterpret_cast<const uint4*>(tile + off[u]);
-          if (r >= kvalid) v[u] = make_uint4(0u, 0u, 0u, 0u);  // stale keys
+          h[u] = make_uint4(bf16x2_rebias(v[u].x), bf16x2_rebias(v[u].y), bf16x2_rebias(v[u].z), bf16x2_rebias(v[u].w));
+          top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(h[u].x, h[u].y), __vmaxu2(h[u].z, h[u].w)));
         }
-#pragma unroll
-        for (int u = 0; u < St::UNITS; ++u) {
-          const uint32_t w4[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w4[c])));
-        }
-        const uint32_t both = *reinterpret_cast<const uint32_t*>(&top2);
-        const uint32_t mine = max(both & 0xFFFFu, both >> 16);
+        const uint32_t mine = max(top2 & 0xFFFFu, top2 >> 16);
         // k stays 0 while the strip's largest value lies in [2^-3, 2^15) (its first
-        // page) and below 2^15 (later): no lift to apply
+        // page) and below 2^15 (later): no lift to apply.  (2^15 and 2^-3 rebiased.)
         const int was = k;
-        const bool plain = k == 0 && !__any_sync(0xffffffffu, mine >= 0x4700u) &&
-                           (i > 0 || __any_sync(0xffffffffu, mine >= 0x3E00u));
-        if (!plain) {
-          const uint32_t most = __reduce_max_sync(0xffffffffu, mine);
+        const bool plain = k == 0 && !__any_sync(0xffffffffu, mine >= 0x0F00u) &&
+                           (i > 0 || __any_sync(0xffffffffu, mine >= 0x0600u));
+        if (plain) {
+#pragma unroll
+          for (int u = 0; u < St::UNITS; ++u)
+            *reinterpret_cast<uint4*>(tile + off0 + u * St::ROWS * 128) =
+                make_uint4(f16x2_of(h[u].x, v[u].x), f16x2_of(h[u].y, v[u].y), f16x2_of(h[u].z, v[u].z),
+                           f16x2_of(h[u].w, v[u].w));
+        } else {
+          uint32_t raw2 = 0u;
+#pragma unroll
+          for (int u = 0; u < St::UNITS; ++u)
+            raw2 = __vmaxu2(raw2, __vmaxu2(__vmaxu2(v[u].x & 0x7FFF7FFFu, v[u].y & 0x7FFF7FFFu),
+                                           __vmaxu2(v[u].z & 0x7FFF7FFFu, v[u].w & 0x7FFF7FFFu)));
+          const uint32_t most = __reduce_max_sync(0xffffffffu, max(raw2 & 0xFFFFu, raw2 >> 16));
           const int e = static_cast<int>(most >> 7) - 127;
           if (i == 0) k = strip_lift(most);
           else if (most && e + k >= 15) k = min(k, strip_lift(most));
+          const float f = pow2i(k);
+#pragma unroll
+          for (int u = 0; u < St::UNITS; ++u)
+            *reinterpret_cast<uint4*>(tile + off0 + u * St::ROWS * 128) =
+                make_uint4(bf16x2_lift(v[u].x, f), bf16x2_lift(v[u].y, f), bf16x2_lift(v[u].z, f), bf16x2_lift(v[u].w, f));
         }
         if (i >= NF) ok = wait(&f_empty[fs], i / NF - 1);
         if (!ok) break;
@@ -401,18 +431,6 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
           reinterpret_cast<uint8_t*>(slot)[cw] = i > 0 && k != was;
           slot[8 + cw] = pow2i(i > 0 ? max(k - was, -126) : 0);
           reinterpret_cast<int*>(slot)[16 + cw] = k;
-        }
-        if (plain) {
-#pragma unroll
-          for (int u = 0; u < St::UNITS; ++u)
-            *reinterpret_cast<uint4*>(tile + off[u]) = make_uint4(bf16x2_to_f16x2(v[u].x), bf16x2_to_f16x2(v[u].y),
-                                                                  bf16x2_to_f16x2(v[u].z), bf16x2_to_f16x2(v[u].w));
-        } else {
-          const float f = pow2i(k);
-#pragma unroll
-          for (int u = 0; u < St::UNITS; ++u)
-            *reinterpret_cast<uint4*>(tile + off[u]) = make_uint4(bf16x2_lift(v[u].x, f), bf16x2_lift(v[u].y, f),
-                                                                  bf16x2_lift(v[u].z, f), bf16x2_lift(v[u].w, f));
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
