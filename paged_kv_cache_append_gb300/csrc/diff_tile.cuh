@@ -13,7 +13,8 @@
 //   S = [Q1; 0] K1^T + [0; Q2] K2^T, two MMAs into one S.
 //
 // Tensor memory: S buffers [0, 64) and [64, 128), Q [128, 128 + D / 2) (BOTH: two
-// operands), O [256, 256 + 2 D).  P goes over the S it was computed from.
+// operands), O [256, 256 + 2 D).  P goes over the S that its own warp computed it from:
+// keys [32 h, +32) in columns [32 h, +16) of the buffer.
 //
 // Operands.  Scores: BF16 pages as they are; FP8-row keys of head_dim 128 as raw
 // E4M3 codes with q in two E4M3 terms, other quantized keys as exact f16 tiles
@@ -22,7 +23,7 @@
 // V therefore too:
 //   * NVFP4 values carry their scales exactly; one P serves both heads, N = 2 D;
 //   * FP8-row and INT8-G64 values leave a factor per key to the weights, so each
-//     head has its own P (columns [0, 32) and [32, 64) of the S buffer), N = D twice;
+//     head has its own P (the second 16 columns further), N = D twice;
 //   * BF16 values are rewritten in place, v 2^k with a power of two per strip of 2 D /
 //     8 dims that brings the strip's largest value so far below 2^15 and above 2^-3
 //     (0 while it is there by itself): exact for every element above its 2^-14th, and
@@ -104,7 +105,7 @@ struct DiffTileCfg {
   static constexpr int OFF_F = OFF_RV + NRV * RV_STAGE;
   static constexpr int OFF_X = OFF_F + NF * 1024;  // [2][2][128] maxima of the rows' halves
   static constexpr int OFF_BAR = OFF_X + 2048;
-  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NRK + 2 * NRV + 2 * NF + 8 + 16;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NRK + 2 * NRV + 2 * NF + 6 + 16;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 64 + 1024;
   static constexpr uint32_t COL_S = 0, COL_Q = 128, COL_O = 256;
   static constexpr uint32_t ID_S = K8MMA  ? tc::idesc_e4m3(128, 64)
@@ -249,10 +250,9 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
   uint64_t* f_empty = f_full + NF;
   uint64_t* s_full = f_empty + NF;  // [2]
   uint64_t* p_full = s_full + 2;    // [2]
-  uint64_t* o_done = p_full + 2;    // [2]
-  uint64_t* q_ready = o_done + 2;
-  uint64_t* drain = q_ready + 1;
-  uint64_t* x_full = drain + 1;  // [2][8] a softmax warp's maxima of a page are there
+  uint64_t* q_ready = p_full + 2;
+  uint64_t* drain = q_ready + 1;  // every MMA complete
+  uint64_t* x_full = drain + 1;   // [2][8] a softmax warp's maxima of a page are there
   uint32_t* tslot = reinterpret_cast<uint32_t*>(x_full + 16);
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -291,7 +291,6 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], Cfg::NSOFT);
-      mbar_init(&o_done[i], 1);
     }
     mbar_init(q_ready, Cfg::NSOFT);
     mbar_init(drain, 1);
@@ -541,6 +540,9 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
           tc::commit(Cfg::K_RAW ? &rk_empty[ks] : &k_empty[ks]);
         }
         __syncwarp();
+      } else {  // as S(j) would: everything up to PV(j - 2) is complete
+        if (elect_one()) tc::commit(&s_full[j & 1]);
+        __syncwarp();
       }
       if (j >= 1) {  // O += P(j - 1) V(j - 1)
         const int jj = j - 1, vs = jj % NV;
@@ -553,10 +555,9 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
             const uint64_t vd = tc::smem_desc(smem_u32(sV + vs * Cfg::V_STAGE + v * Cfg::F16), 8192, 1024);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc::mma_ts(tmem + Cfg::COL_O + v * D, tmem + Cfg::COL_S + 64 * (jj & 1) + 32 * v + kk * 8,
+              tc::mma_ts(tmem + Cfg::COL_O + v * D, tmem + Cfg::COL_S + 64 * (jj & 1) + 32 * (kk >> 1) + 16 * v + 8 * (kk & 1),
                          vd + static_cast<uint64_t>((kk * 2048) >> 4), Cfg::ID_O, (jj > 0 || kk > 0));
           }
-          tc::commit(&o_done[jj & 1]);
           tc::commit(&v_empty[vs]);
         }
         __syncwarp();
@@ -652,53 +653,10 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     int k_run = KV == KIND_FP8 ? kVLiftInit : 0;  // FP8-row V: the weights, l and O carry 2^k_run, one lift for both heads
     const int mate = warp ^ 4;  // the warp of the rows' other keys
     uint32_t sv[32], pk[Cfg::VAL_FAC ? 2 : 1][16];
-    float mu = 0.f;
-    // The weights of this half's keys under the reference mu into pk; returns their sum.
-    const auto weights = [&](const float* vsc) {
-      const F2 mu2 = pack2(-mu, -mu);
-      F2 sum2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
-#pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        float p[4];
-#pragma unroll
-        for (int u = 0; u < 4; u += 2) {
-          unpack2(fma2(pack2(__uint_as_float(sv[c + u]), __uint_as_float(sv[c + u + 1])), c2, mu2), p[u], p[u + 1]);
-          p[u] = ex2(p[u]);
-          p[u + 1] = ex2(p[u + 1]);
-          sum2[u >> 1] = add2(sum2[u >> 1], pack2(p[u], p[u + 1]));
-        }
-        if constexpr (Cfg::VAL_FAC) {
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const float4 f = *reinterpret_cast<const float4*>(vsc + 64 * v + c);
-            float x[4];
-            unpack2(mul2(pack2(p[0], p[1]), pack2(f.x, f.y)), x[0], x[1]);
-            unpack2(mul2(pack2(p[2], p[3]), pack2(f.z, f.w)), x[2], x[3]);
-            pk[v][c / 2] = pack_f16x2(x[0], x[1]);
-            pk[v][c / 2 + 1] = pack_f16x2(x[2], x[3]);
-          }
-        } else {
-          pk[0][c / 2] = pack_f16x2(p[0], p[1]);
-          pk[0][c / 2 + 1] = pack_f16x2(p[2], p[3]);
-        }
-      }
-      float s0, s1;
-      unpack2(add2(sum2[0], sum2[1]), s0, s1);
-      return s0 + s1;
-    };
-    bool live = true;
-    for (int j = 0; j < n; ++j) {
-      const int sb = j & 1, fs = j % NF;
-      const uint32_t s_at = quad + Cfg::COL_S + 64 * sb;
-      live = live && wait(&s_full[sb], j >> 1);
-      // PV(j - 2) is complete with S(j): its barrier, and the other P buffer's, may turn
-      if (j >= 2) live = live && wait(&o_done[sb], (j - 2) >> 1);
-      tc::fence_after();
-      tc::ld32(s_at + 32 * half, sv);
-      if constexpr (Cfg::HAS_F) live = live && wait(&f_full[fs], j / NF);
-      const float* ksc = sF + fs * 256 + (BOTH ? 64 * map : 0) + 32 * half;
-      const float* vsc = sF + fs * 256 + 128;
-      const int kmax = (valid ? pos - 64 * (w.p_lo + j) : -1) - 32 * half;  // of this half's keys
+    float mu = 0.f, top = 0.f;
+    // This half's scores of the page, factors and mask applied; their maximum in top.
+    const auto scores = [&](uint32_t at, const float* ksc, int kmax) {
+      tc::ld32(at, sv);
       tc::wait_ldn(sv);
       if constexpr (Cfg::KEY_FAC) {
 #pragma unroll
@@ -716,6 +674,63 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
         for (int c = 0; c < 32; ++c)
           if (c > kmax) sv[c] = 0xFF800000u;  // -inf
       }
+    };
+    // The weights of sv under the reference mu into pk (sv is used up); returns their sum.
+    const auto weights = [&](const float* vsc) {
+      const F2 mu2 = pack2(-mu, -mu);
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        float x, y;
+        unpack2(fma2(pack2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), c2, mu2), x, y);
+        sv[c] = __float_as_uint(x);
+        sv[c + 1] = __float_as_uint(y);
+      }
+#pragma unroll
+      for (int c = 0; c < 32; ++c) sv[c] = __float_as_uint(ex2(__uint_as_float(sv[c])));
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        if constexpr (Cfg::VAL_FAC) {
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const float2 f = *reinterpret_cast<const float2*>(vsc + 64 * v + c);
+            float x, y;
+            unpack2(mul2(pack2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), pack2(f.x, f.y)), x, y);
+            pk[v][c / 2] = pack_f16x2(x, y);
+          }
+        } else {
+          pk[0][c / 2] = pack_f16x2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+        }
+      }
+      F2 sum2[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sum2[u] = pack2(__uint_as_float(sv[2 * u]), __uint_as_float(sv[2 * u + 1]));
+#pragma unroll
+      for (int c = 8; c < 32; c += 2)
+        sum2[(c >> 1) & 3] = add2(sum2[(c >> 1) & 3], pack2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])));
+      float s0, s1;
+      unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])), s0, s1);
+      return s0 + s1;
+    };
+    bool live = true;
+    for (int j = 0; j < n; ++j) {
+      const int sb = j & 1, fs = j % NF;
+      const uint32_t s_at = quad + Cfg::COL_S + 64 * sb + 32 * half;
+      const float* ksc = sF + fs * 256 + (BOTH ? 64 * map : 0) + 32 * half;
+      const float* vsc = sF + fs * 256 + 128 + 32 * half;
+      const int kmax = (valid ? pos - 64 * (w.p_lo + j) : -1) - 32 * half;  // of this half's keys
+      bool strips = false;  // BF16 values: a strip's k fell
+      int knew = k_run;
+      if constexpr (Cfg::HAS_F) {
+        live = live && wait(&f_full[fs], j / NF);
+        if constexpr (Cfg::BF16) strips = *reinterpret_cast<const unsigned long long*>(sF + fs * 256) != 0ull;
+        if constexpr (KV == KIND_FP8) {
+          const float4 s4 = *reinterpret_cast<const float4*>(sF + fs * 256 + 128 + 4 * lane);  // both heads' 128 scales
+          knew = v_lift(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(s4.x, s4.y), fmaxf(s4.z, s4.w)))), k_run);
+        }
+      }
+      live = live && wait(&s_full[sb], j >> 1);  // and PV(j - 2) is complete: in issue order
+      tc::fence_after();
+      scores(s_at, ksc, kmax);
       float top4[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) top4[u] = fmaxf(__uint_as_float(sv[u]), __uint_as_float(sv[4 + u]));
@@ -723,19 +738,13 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       for (int c = 8; c < 32; c += 8)
 #pragma unroll
         for (int u = 0; u < 4; ++u) top4[u] = max3(top4[u], __uint_as_float(sv[c + u]), __uint_as_float(sv[c + 4 + u]));
-      float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
+      top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
       sX[sb * 256 + 128 * half + m] = top;
       __syncwarp();
-      if (lane == 0) q_arrive(&x_full[8 * sb + warp]);  // and: this half has read its S, so P may go over it
+      if (lane == 0) q_arrive(&x_full[8 * sb + warp]);
+      // under the old reference, before the other half's maximum is known
       float sum = 0.f;
-      if (j > 0) sum = weights(vsc + 32 * half);
-      int knew = k_run;
-      if constexpr (KV == KIND_FP8) {
-        const float4 s4 = *reinterpret_cast<const float4*>(vsc + 4 * lane);  // both heads' 128 scales
-        knew = v_lift(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(s4.x, s4.y), fmaxf(s4.z, s4.w)))), k_run);
-      }
-      bool strips = false;  // BF16 values: a strip's k fell
-      if constexpr (Cfg::BF16) strips = *reinterpret_cast<const unsigned long long*>(sF + fs * 256) != 0ull;
+      if (j > 0) sum = weights(vsc);
       live = live && wait(&x_full[8 * sb + mate], j >> 1);
       top = fmaxf(top, sX[sb * 256 + 128 * (half ^ 1) + m]);
       const float rmax = top == -INFINITY ? -INFINITY : top * c_row;
@@ -751,9 +760,10 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
         }
         k_run = knew;
         mu = m_used == -INFINITY ? 0.f : m_used - static_cast<float>(k_run);
-        sum = weights(vsc + 32 * half);
-        if (j >= 1) {  // O of this half's dims, once PV(j - 1) is complete
-          live = live && wait(&o_done[sb ^ 1], (j - 1) >> 1);
+        if (j > 0) scores(s_at, ksc, kmax);  // S is still there: only this warp writes over it
+        sum = weights(vsc);
+        if (j >= 1) {  // O of this half's dims, once PV(j - 1) is complete: with S(j + 1)
+          live = live && wait(&s_full[sb ^ 1], (j + 1) >> 1);
           tc::fence_after();
 #pragma unroll 1
           for (int c0 = half * D; c0 < (half + 1) * D; c0 += 16) {
@@ -769,9 +779,8 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
         }
       }
       l = l * factor + sum;
-      // P over the S that was read: this half's 16 columns, of each head's P
 #pragma unroll
-      for (int v = 0; v < (Cfg::VAL_FAC ? 2 : 1); ++v) tc::st16(s_at + 32 * v + 16 * half, pk[v]);
+      for (int v = 0; v < (Cfg::VAL_FAC ? 2 : 1); ++v) tc::st16(s_at + 16 * v, pk[v]);
       tc::wait_st();
       tc::fence_before();
       __syncwarp();
@@ -781,7 +790,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       }
     }
     // ---- this CTA's partial: (m, l) of the row, and O, the half's D dims -------------
-    if (n > 0 && live) live = wait(&o_done[(n - 1) & 1], (n - 1) >> 1);
+    live = live && wait(drain, 0);  // every PV
     tc::fence_after();
     sX[(n & 1) * 256 + 128 * half + m] = l;
     __syncwarp();
