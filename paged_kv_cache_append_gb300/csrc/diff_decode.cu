@@ -57,28 +57,24 @@ template <int D>
 __global__ void __launch_bounds__(512) diff_join_kernel(DiffJoinArgs a) {
   constexpr int COLS = D;  // 2 maps x 2 D / 4
   constexpr int LANES = 512 / COLS, EACH = kDiffMaxSplits / LANES, STEP = 8;
-  __shared__ int s_F[8], s_row[8];
   __shared__ float s_w[2][kDiffMaxSplits];
   __shared__ float4 s_acc[LANES][COLS];
   __shared__ float s_sum[16];
   __shared__ int s_any;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int head = blockIdx.x, bt = blockIdx.y, b = bt / a.T, t = bt % a.T;
-  griddep_wait();
-  griddep_launch_dependents();
-  if (tid < a.B) s_F[tid] = diff_length(a.frontiers, a.table_rows, tid, a.L, a.C, &s_row[tid], nullptr);
-  __syncthreads();
-  const int chunk = diff_chunk(s_F, a.B, a.ctas, kDiffMaxSplits);
-  int at = 0, ns = 0;
-  for (int i = 0; i <= b; ++i) {
-    at += ns;
-    ns = max(1, (((s_F[i] + 63) >> 6) + chunk - 1) / chunk);
-  }
+  // Inputs of the call: complete since before the splits' kernel let this one start,
+  // and not written by it (read past L1, which the wait below has not renewed).
+  const DiffRows rows = diff_rows(a.frontiers, a.table_rows, a.B, a.L, a.C, a.ctas, nullptr);
+  const int ns = __shfl_sync(0xffffffffu, rows.ns, b), at = __shfl_sync(0xffffffffu, rows.end, b) - ns;
+  const float lambda = __ldcg(a.o.lambda + bt * a.o.lambda_stride + head);
   const int RB = a.RB, r = t * a.G + head % a.G;
   const int64_t slot0 = static_cast<int64_t>(head / a.G) * a.ctas + at;
   const int map = tid % COLS / (COLS / 2), d = tid % (COLS / 2) * 4, sub = tid / COLS;
   const float* src = a.ws_o + ((slot0 * 2 + map) * RB + r) * (2 * D) + d;
   const int64_t step = static_cast<int64_t>(2) * RB * 2 * D;
+  griddep_wait();  // the partials
+  griddep_launch_dependents();
   if (warp < 2) {  // weights of map `warp`
     float2 ml[kDiffMaxSplits / 32];
     float M = -INFINITY, L = 0.f;
@@ -129,7 +125,6 @@ __global__ void __launch_bounds__(512) diff_join_kernel(DiffJoinArgs a) {
   __syncthreads();
   float o[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
   if (tid < COLS / 2) {
-    const float lambda = a.o.lambda[bt * a.o.lambda_stride + head];
     float x[2][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
@@ -177,7 +172,6 @@ static int diff_plan(const nk_pool* p, int B, int T, int Hq, DiffPlan* pl) {
   if (rows > 64) return fail(NK_ERR_UNSUPPORTED, "T * Hq / num_kv_heads must be <= 64");
   pl->RB = rows <= 4 ? 4 : rows <= 8 ? 8 : 64;
   pl->fn = nullptr;
-  int per_sm = 1;
   if (pl->RB < 64) {
     switch (p->desc.profile) {
       case NK_BF16: pl->fn = diff_decode_bf16; break;
@@ -186,10 +180,8 @@ static int diff_plan(const nk_pool* p, int B, int T, int Hq, DiffPlan* pl) {
       case NK_NVFP4_G16: pl->fn = diff_decode_nvfp4; break;
       default: pl->fn = diff_decode_k8v4; break;
     }
-    const cudaError_t e = pl->fn(p, 0, nullptr, pl->RB == 4, &per_sm, nullptr);
-    if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
   }
-  const int target = p->num_sms * per_sm / (H / 2);
+  const int target = p->num_sms / (H / 2);
   pl->ctas = target > B ? target : B;
   const size_t slots = static_cast<size_t>(H / 2) * pl->ctas * 2 * pl->RB;
   pl->ml_bytes = (slots * sizeof(float2) + 255) / 256 * 256;
@@ -237,7 +229,7 @@ extern "C" int nk_paged_diff_decode_attention(const void* q, int32_t Hq, const n
   if (pl.fn) {
     const DiffDecodeArgs a{t.q, t.tables, t.table_rows, t.lengths, t.ks, t.vs, t.ws_ml, t.ws_o, t.status, softmax_scale,
                            t.B, t.T, t.Hq, t.H, t.G, t.L, t.M, t.C, t.ctas, t.head_major};
-    e = pl.fn(pool, layer, &a, pl.RB == 4, nullptr, s);
+    e = pl.fn(pool, layer, a, pl.RB == 4, s);
   } else {
     e = diff_tile_for(pool->desc.profile)(pool, layer, t, true, dim3(pl.ctas, t.H / 2), s);
   }

@@ -4,19 +4,25 @@
 //
 // For KV heads 2j, 2j + 1 (keys K1, K2; values V = [V1 V2]) and the query rows
 // of the heads that share them, o = softmax(Q1 K1^T) V - lambda softmax(Q2 K2^T) V.
-// Up to 8 query rows a map (more go to diff_tile.cuh).  A CTA owns one (row b, pair
-// j, page range) and stages the four code tiles of a page together.  Its eight
-// consumer warps are four slabs of 16 keys times two sides: the warp of side m
-//   * computes S_m = K_m Q_m^T of its slab and the softmax of map m (its own
-//     running maximum, moved lazily as in decode.cuh),
-//   * hands P_m (and the rescale factors) to the other side's warp through
-//     shared memory: one exchange of a few registers per lane and page,
-//   * multiplies V_m's half of the dims by both maps' weights:
-//     O_1[:, m half] += V_m^T P_1^T, O_2[:, m half] += V_m^T P_2^T.
-// So every code is converted once, S is computed once, and only P V is done for
-// both maps.  Up to 4 query rows (PACK) the two maps' weights fill one 8-column
-// operand: map 1 in columns 0-3, map 2 in columns 4-7, half the MMAs and
-// accumulators.
+// Few query rows (the rest goes to diff_tile.cuh).  A CTA owns one (row b, pair j,
+// page range) and stages the four code tiles of a page together; each of its four
+// consumer warps owns 16 keys of every page, for both maps and both value heads, so
+// that every code is converted once and no warp waits for another:
+//   QK   mma.m16n8k16, keys as M.  Up to 4 query rows (PACK) both maps fill the 8
+//        columns (map 1 in 0-3, map 2 in 4-7): S1 = K1 [Q1 Q2]^T, S2 = K2 [Q1 Q2]^T,
+//        of which a lane keeps the one of its columns' map; 8 rows take a tile a map.
+//   softmax, base 2, per column over the warp's keys, with a lazy reference.
+//   PV   O^T += V^T P^T, dims as M, 64 dims at a time: the warp converts its 16 keys
+//        to f16 in 2 KB of its own and reads them back transposed.  FP8-row and
+//        INT8-G64 scales multiply the weights (a few products) instead of the values
+//        (32 a lane and head), lifted by a power of two per head (v_lift) that O
+//        carries.
+// Pages that all queries see whole (all but a row's last) run without masks; in the
+// last one the warp zeroes its stale value rows in place.
+//
+// Two heads to a warp halved the instructions of a page against one head to each of
+// two warps that exchange their weights (3793 warp instructions, FP8-row, head_dim
+// 128), whose issue rate bound that form at 46% of the copy rate.
 //
 // Partials of (map, query row) go to the workspace, for the join (diff_decode.cu).
 #pragma once
@@ -54,10 +60,8 @@ constexpr int diff_scale_bytes(int D) {
 
 template <int KK, int KV, int D, bool PACK>
 struct DiffCfg {
-  static constexpr int NW = 8, NCONS = 32 * NW, THREADS = NCONS + 32;
-  static constexpr int R = 8;             // columns of one map's S
-  static constexpr int RB = PACK ? 4 : R; // query rows of a partial
-  static constexpr int NT = PACK ? 1 : 2; // column tiles of P V
+  static constexpr int RB = PACK ? 4 : 8;  // query rows of a map
+  static constexpr int NT = PACK ? 1 : 2;  // column tiles: both maps, or one each
   static constexpr int KCB = diff_code_bytes<KK>(D), VCB = diff_code_bytes<KV>(D);
   static constexpr int KSB = diff_scale_bytes<KK>(D), VSB = diff_scale_bytes<KV>(D);
   static constexpr int K_RB = KCB < 128 ? KCB : 128, V_RB = VCB < 128 ? VCB : 128;
@@ -65,28 +69,33 @@ struct DiffCfg {
   static constexpr int OFF_V = 2 * K_TILE, OFF_KS = OFF_V + 2 * V_TILE, OFF_VS = OFF_KS + 2 * KS_TILE;
   static constexpr int STAGE = diff_align(OFF_VS + 2 * VS_TILE, 1024);
   static_assert(K_TILE % 1024 == 0 && V_TILE % 1024 == 0, "tiles keep the swizzle's alignment");
-  static constexpr int TX_BYTES = 2 * (K_TILE + V_TILE + KS_TILE + VS_TILE);
   static constexpr bool MMA_BF16 = KK == KIND_BF16;
+  static constexpr bool VAL_FAC = KV == KIND_INT8 || KV == KIND_FP8;
   static constexpr int PARTS = MMA_BF16 ? 2 : 1;  // bf16 weights as hi + lo
-  static constexpr int OREGS = D / 16 * NT * 4;
-  // CTAs per SM: the accumulators and the tiles of a page decide
-  static constexpr int MINB = OREGS > 64 || STAGE > 48 * 1024 ? 1 : 2;
+  static constexpr int OREGS = 2 * D / 16 * NT * 4;
   static constexpr int Q_PITCH = D * 2 + 32;
-  static constexpr int XW = PARTS * 2 + 3;  // words a lane hands over
-  static constexpr int VW_BYTES = KV == KIND_BF16 ? 0 : 16 * D * 2;  // a warp's 16 keys of V as f16
+  static constexpr int VW_BYTES = KV == KIND_BF16 ? 0 : 16 * 64 * 2;  // a warp's 16 keys x 64 dims of V as f16
   static constexpr int O_PITCH = 2 * D + 4;  // floats: rows of the combine in different banks
-  static constexpr int COMB = 4 * 2 * RB * O_PITCH * 4;
-  static constexpr int REST = 2 * R * Q_PITCH + 2 * NW * 32 * XW * 4 + 20 * R * 4 + 1024 + 512;
-  static constexpr int BUDGET = (MINB == 1 ? 226 : 113) * 1024 - REST - NW * VW_BYTES;
-  static constexpr int NSTAGE = BUDGET / STAGE < 2 ? 2 : BUDGET / STAGE > 8 ? 8 : BUDGET / STAGE;
-  // V slabs lie behind the ring; both are free for the combine at the end
+  // Stages that fit beside the rest of g groups
+  static constexpr int stages(int g) {
+    return (227 * 1024 - 1024 - 8 * NT * Q_PITCH - (8 * g + 2) * 2 * RB * 4 - 768 - 4 * g * VW_BYTES) / STAGE;
+  }
+  // Groups of four warps: as many as the accumulators' registers (128, 168 or 255 a
+  // thread) and two stages for each allow
+  static constexpr int NG_REGS = OREGS > 64 ? 2 : OREGS > 32 ? 3 : 4;
+  static constexpr int groups(int g) { return g > 1 && stages(g) < 2 * g ? groups(g - 1) : g; }
+  static constexpr int NG = groups(NG_REGS);
+  static constexpr int SG = stages(NG) / NG < 8 ? stages(NG) / NG : 8;  // stages of a group
+  static_assert(SG >= 2, "a stage is refilled while the next one is read");
+  static constexpr int NW = 4 * NG, THREADS = 32 * NW, NSTAGE = SG * NG;
+  static constexpr int COMB = NW * 2 * RB * O_PITCH * 4;
+  // V blocks lie behind the ring; both are free for the combine at the end
   static constexpr int OFF_VW = NSTAGE * STAGE;
   static constexpr int FREE = OFF_VW + NW * VW_BYTES;
   static constexpr int OFF_Q = diff_align(FREE > COMB ? FREE : COMB, 128);
-  static constexpr int OFF_X = OFF_Q + 2 * R * Q_PITCH;
-  static constexpr int OFF_RED = OFF_X + 2 * NW * 32 * XW * 4;  // m, l [4][2][R] each, M, L [2][R]
-  static constexpr int OFF_BAR = diff_align(OFF_RED + 20 * R * 4, 16);
-  static constexpr int SMEM = OFF_BAR + 2 * NSTAGE * 8 + 32 * 4 + 1024;
+  static constexpr int OFF_RED = OFF_Q + 8 * NT * Q_PITCH;  // m, l [NW][2 RB] each, M, L [2 RB]
+  static constexpr int OFF_BAR = diff_align(OFF_RED + (2 * NW + 2) * 2 * RB * 4, 16);
+  static constexpr int SMEM = OFF_BAR + 2 * NSTAGE * 8 + 64 * 4 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -190,481 +199,480 @@ __device__ __forceinline__ void diff_scores(const uint8_t* tile, const uint8_t* 
   }
 }
 
-// The slab's 16 keys x D dims of a staged quantized V tile as f16 in `vw`
-// (64-dim blocks of 16 rows x 128 bytes, 128-byte swizzle), scales applied, keys
-// past the frontier zero (`live`: of this lane's key).  Lane: key lane & 15, dims
-// [32 dh, +32) of every block, dh = lane >> 4.
+// The warp's 16 keys x 64 dims (block q) of a staged quantized V tile as f16 in
+// `blk` (16 rows x 128 bytes, 128-byte swizzle): NVFP4 values with their scales (an
+// exact product), INT8 and FP8 codes alone.  Lane: key lane & 15, dims [32 dh, +32) of
+// the block, dh = lane >> 4.
 template <int KV, int D>
-__device__ __forceinline__ void diff_values(const uint8_t* tile, const uint8_t* scales, uint8_t* vw, int slab, int lane,
-                                            bool live, uint32_t lift2) {
+__device__ __forceinline__ void diff_values(const uint8_t* tile, const uint8_t* scales, uint8_t* blk, int q, int slab,
+                                            int lane) {
   constexpr int VCB = diff_code_bytes<KV>(D), VSB = diff_scale_bytes<KV>(D), RB = VCB < 128 ? VCB : 128;
   const int kr = lane & 15, dh = lane >> 4, key = 16 * slab + kr;
+  const int d0 = 64 * q + 32 * dh;
+  uint32_t w[8], h[16];
+  if constexpr (KV == KIND_NVFP4) {
+    const int col = d0 / 2;
+    const uint4 x = *reinterpret_cast<const uint4*>(tile + (col / RB) * (64 * RB) + swz<RB>(key, col % RB));
+    const uint32_t s2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(scales + key * VSB + d0 / 16));
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
 #pragma unroll
-  for (int q = 0; q < D / 64; ++q) {
-    uint8_t* blk = vw + q * (16 * 128);
-    const int d0 = 64 * q + 32 * dh;
-    if constexpr (KV == KIND_NVFP4) {
-      const int col = d0 / 2;
-      const uint4 w = *reinterpret_cast<const uint4*>(tile + (col / RB) * (64 * RB) + swz<RB>(key, col % RB));
-      // finite codes: a zero scale zeroes a key past the frontier
-      const uint32_t s2 = live ? e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(scales + key * VSB + d0 / 16)) : 0u;
-      const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
+    for (int k = 0; k < 4; ++k) {  // 8 dims; two words to a scale group
+      const uint32_t sq = __byte_perm(s2, 0, k >> 1 ? 0x3232 : 0x1010);
+      h[4 * k + 0] = hmul2_u32(e2m1x2_byte_to_f16x2<0>(w[k]), sq);
+      h[4 * k + 1] = hmul2_u32(e2m1x2_byte_to_f16x2<1>(w[k]), sq);
+      h[4 * k + 2] = hmul2_u32(e2m1x2_byte_to_f16x2<2>(w[k]), sq);
+      h[4 * k + 3] = hmul2_u32(e2m1x2_byte_to_f16x2<3>(w[k]), sq);
+    }
+  } else {
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {  // 16 dims, one scale group
-        const uint32_t sq = __byte_perm(s2, 0, sub ? 0x3232 : 0x1010);
-        uint32_t h[8];
+    for (int sub = 0; sub < 2; ++sub) {
+      const int dd = d0 + 16 * sub;
+      const uint4 x = *reinterpret_cast<const uint4*>(tile + (dd / RB) * (64 * RB) + swz<RB>(key, dd % RB));
+      w[4 * sub] = x.x, w[4 * sub + 1] = x.y, w[4 * sub + 2] = x.z, w[4 * sub + 3] = x.w;
+    }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          h[4 * k + 0] = hmul2_u32(e2m1x2_byte_to_f16x2<0>(wv[2 * sub + k]), sq);
-          h[4 * k + 1] = hmul2_u32(e2m1x2_byte_to_f16x2<1>(wv[2 * sub + k]), sq);
-          h[4 * k + 2] = hmul2_u32(e2m1x2_byte_to_f16x2<2>(wv[2 * sub + k]), sq);
-          h[4 * k + 3] = hmul2_u32(e2m1x2_byte_to_f16x2<3>(wv[2 * sub + k]), sq);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          *reinterpret_cast<uint4*>(blk + swz<128>(kr, 64 * dh + 32 * sub + 16 * k)) =
-              make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
-      }
-    } else {
-      const uint16_t* sp = reinterpret_cast<const uint16_t*>(scales + key * VSB);
-      const uint32_t s1 = KV == KIND_INT8 ? sp[d0 / 64] : sp[0];
-      // INT8 codes are finite; FP8 codes may encode NaN and are selected away
-      const uint32_t s2 = KV == KIND_INT8 && !live ? 0u : hmul2_u32(s1 | (s1 << 16), lift2);
-#pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {
-        const int dd = d0 + 16 * sub;
-        const uint4 w = *reinterpret_cast<const uint4*>(tile + (dd / RB) * (64 * RB) + swz<RB>(key, dd % RB));
-        const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
-        uint32_t h[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          h[2 * k] = hmul2_u32(diff_cvt_pair<KV, false>(wv[k]), s2);
-          h[2 * k + 1] = hmul2_u32(diff_cvt_pair<KV, true>(wv[k]), s2);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          *reinterpret_cast<uint4*>(blk + swz<128>(kr, 64 * dh + 32 * sub + 16 * k)) =
-              KV == KIND_INT8 || live ? make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3])
-                                      : make_uint4(0u, 0u, 0u, 0u);
-      }
+    for (int k = 0; k < 8; ++k) {
+      h[2 * k] = diff_cvt_pair<KV, false>(w[k]);
+      h[2 * k + 1] = diff_cvt_pair<KV, true>(w[k]);
     }
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    *reinterpret_cast<uint4*>(blk + swz<128>(kr, 64 * dh + 16 * k)) =
+        make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
 }
 
 template <int KK, int KV, int D, bool PACK>
-__global__ void __launch_bounds__((DiffCfg<KK, KV, D, PACK>::THREADS), (DiffCfg<KK, KV, D, PACK>::MINB))
+__global__ void __launch_bounds__((DiffCfg<KK, KV, D, PACK>::THREADS), 1)
     diff_decode_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                        DiffDecodeArgs a) {
   using Cfg = DiffCfg<KK, KV, D, PACK>;
-  constexpr int R = Cfg::R, RB = Cfg::RB, NT = Cfg::NT, NSTAGE = Cfg::NSTAGE, NW = Cfg::NW, NCONS = Cfg::NCONS;
-  constexpr int PARTS = Cfg::PARTS, MT = D / 16, XW = Cfg::XW;
+  constexpr int RB = Cfg::RB, NT = Cfg::NT, NSTAGE = Cfg::NSTAGE, NW = Cfg::NW, NG = Cfg::NG, SG = Cfg::SG;
+  constexpr int PARTS = Cfg::PARTS, MT = D / 16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* qs = smem + Cfg::OFF_Q;                                 // [2][R][Q_PITCH]
-  uint32_t* sx = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_X);   // [2][NW][XW][32]
-  float* red_m = reinterpret_cast<float*>(smem + Cfg::OFF_RED);    // [4][2][R]
-  float* red_l = red_m + 8 * R;
-  float* row_M = red_l + 8 * R;                                    // [2][R]
-  float* row_L = row_M + 2 * R;
+  uint8_t* qs = smem + Cfg::OFF_Q;                               // [8 NT columns][Q_PITCH]
+  float* red_m = reinterpret_cast<float*>(smem + Cfg::OFF_RED);  // [NW][2][RB]
+  float* red_l = red_m + 2 * NW * RB;
+  float* row_M = red_l + 2 * NW * RB;                                 // [2][RB]
+  float* row_L = row_M + 2 * RB;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
   uint64_t* empty = full + NSTAGE;
   int* s_flags = reinterpret_cast<int*>(empty + NSTAGE);  // [0] abort
-  int* s_F = s_flags + 4;                                 // [8]
-  int* s_row = s_flags + 12;                              // [8]
-  float* s_qmax = reinterpret_cast<float*>(s_flags + 20); // [8]
+  float* s_qmax = reinterpret_cast<float*>(s_flags + 4);  // [2][NW]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, c = lane & 3;
-  const int slab = warp >> 1, side = warp & 1;  // consumers: keys [16 slab, +16), map and V half
+  const int grp = warp >> 2, slab = warp & 3;  // keys [16 slab, +16) of pages grp, grp + NG, ..
   const int cta = blockIdx.x, pair = blockIdx.y;
 
   if (tid == 0) {
     for (int s = 0; s < NSTAGE; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], NW);
+      mbar_init(&full[s], 4);
+      mbar_init(&empty[s], 4);
     }
     s_flags[0] = 0;
     fence_barrier_init();
     prefetch_tmap(&tmk);
     prefetch_tmap(&tmv);
   }
+  __syncthreads();
   griddep_wait();  // pages, lengths and q may come from the kernel ahead
   griddep_launch_dependents();
-  if (tid < a.B)
-    s_F[tid] = diff_length(a.frontiers, a.table_rows, tid, a.L, a.C, &s_row[tid],
-                           cta == 0 && pair == 0 ? a.status : nullptr);
-  __syncthreads();
-
-  // ---- which (row, split) this CTA owns ----------------------------------------
-  const int chunk = diff_chunk(s_F, a.B, a.ctas, kDiffMaxSplits);
-  int b = -1, split = 0, npages = 0;
-  for (int i = 0, at = 0; i < a.B; ++i) {
-    const int np = (s_F[i] + 63) >> 6, ns = max(1, (np + chunk - 1) / chunk);
-    if (cta < at + ns) {
-      b = i, split = cta - at, npages = np;
-      break;
-    }
-    at += ns;
-  }
-  if (b < 0) return;
-  const int F = s_F[b], p0 = split * chunk;
-  const int n = min(chunk, npages - p0);  // 0 only for a row without keys
+  const DiffSplit own = diff_split(diff_rows(a.frontiers, a.table_rows, a.B, a.L, a.C, a.ctas,
+                                             cta == 0 && pair == 0 && warp == 0 ? a.status : nullptr),
+                                   a.B, cta);
+  if (own.b < 0) return;
+  const int b = own.b, F = own.F, p0 = own.p0, n = own.n;
   const int rows = a.T * a.G;  // query rows of a map
 
-  // ---- producer warp --------------------------------------------------------------
-  if (warp == NW) {
-    const int32_t* table = a.tables + static_cast<int64_t>(s_row[b]) * a.L + p0;
-    int gnext = 0;
-    for (int i = 0; i < n; ++i) {
-      if ((i & 31) == 0) gnext = (i + lane < n) ? table[i + lane] : 0;
-      int g = __shfl_sync(0xffffffffu, gnext, i & 31);
-      int stop = 0;
-      if (lane == 0) {
-        const int s = i % NSTAGE;
-        if (i >= NSTAGE && !mbar_wait_bounded(&empty[s], ((i / NSTAGE) - 1) & 1, a.status)) {
-          s_flags[0] = 1;
-          stop = 1;
-        } else {
-          if (g < 0 || g >= a.M) {  // never copy from outside the pool
-            set_status(a.status, NK_STATUS_PAGE_RANGE);
-            g = 0;
-          }
-          uint8_t* st = smem + s * Cfg::STAGE;
-          mbar_arrive_expect_tx(&full[s], Cfg::TX_BYTES);
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const int y = static_cast<int>(tile_row(g, 2 * pair + m, a.H, a.M, a.head_major));
-#pragma unroll
-            for (int j = 0; j < Cfg::KCB / Cfg::K_RB; ++j)
-              tma_load_2d(st + m * Cfg::K_TILE + j * 64 * Cfg::K_RB, &tmk, j * Cfg::K_RB, y, &full[s]);
-#pragma unroll
-            for (int j = 0; j < Cfg::VCB / Cfg::V_RB; ++j)
-              tma_load_2d(st + Cfg::OFF_V + m * Cfg::V_TILE + j * 64 * Cfg::V_RB, &tmv, j * Cfg::V_RB, y, &full[s]);
-            if constexpr (Cfg::KS_TILE > 0) {
-              bulk_load(st + Cfg::OFF_KS + m * Cfg::KS_TILE, a.ks + static_cast<int64_t>(y) * Cfg::KSB, Cfg::KS_TILE,
-                        &full[s]);
-              bulk_load(st + Cfg::OFF_VS + m * Cfg::VS_TILE, a.vs + static_cast<int64_t>(y) * Cfg::VSB, Cfg::VS_TILE,
-                        &full[s]);
-            }
-          }
-        }
+  // ---- copies: a group's ring of SG stages, one of the four tiles from each warp ------
+  const int ng = n > grp ? (n - grp + NG - 1) / NG : 0;  // pages of this group
+  const int32_t* table = a.tables + static_cast<int64_t>(own.row) * a.L + p0 + grp;
+  const int tm = slab & 1;  // warps 0, 1: the pair's keys; 2, 3: its values
+  int gnext = 0;
+  auto load = [&](int i) {  // page i of the group; called in order, by the whole warp
+    if ((i & 31) == 0) gnext = (i + lane < ng) ? table[(i + lane) * NG] : 0;
+    int g = __shfl_sync(0xffffffffu, gnext, i & 31);
+    if (lane == 0) {
+      if (g < 0 || g >= a.M) {  // never copy from outside the pool
+        set_status(a.status, NK_STATUS_PAGE_RANGE);
+        g = 0;
       }
-      if (__shfl_sync(0xffffffffu, stop, 0)) break;
+      const int s = grp * SG + i % SG;
+      uint8_t* st = smem + s * Cfg::STAGE;
+      const int y = static_cast<int>(tile_row(g, 2 * pair + tm, a.H, a.M, a.head_major));
+      if (slab < 2) {
+        mbar_arrive_expect_tx(&full[s], Cfg::K_TILE + Cfg::KS_TILE);
+#pragma unroll
+        for (int j = 0; j < Cfg::KCB / Cfg::K_RB; ++j)
+          tma_load_2d(st + tm * Cfg::K_TILE + j * 64 * Cfg::K_RB, &tmk, j * Cfg::K_RB, y, &full[s]);
+        if constexpr (Cfg::KS_TILE > 0)
+          bulk_load(st + Cfg::OFF_KS + tm * Cfg::KS_TILE, a.ks + static_cast<int64_t>(y) * Cfg::KSB, Cfg::KS_TILE,
+                    &full[s]);
+      } else {
+        mbar_arrive_expect_tx(&full[s], Cfg::V_TILE + Cfg::VS_TILE);
+#pragma unroll
+        for (int j = 0; j < Cfg::VCB / Cfg::V_RB; ++j)
+          tma_load_2d(st + Cfg::OFF_V + tm * Cfg::V_TILE + j * 64 * Cfg::V_RB, &tmv, j * Cfg::V_RB, y, &full[s]);
+        if constexpr (Cfg::VS_TILE > 0)
+          bulk_load(st + Cfg::OFF_VS + tm * Cfg::VS_TILE, a.vs + static_cast<int64_t>(y) * Cfg::VSB, Cfg::VS_TILE,
+                    &full[s]);
+      }
     }
-    return;  // the copies land in the shared memory of the still-running CTA
-  }
+    __syncwarp();
+  };
+  int issued = 0;
+  for (; issued < min(SG, ng); ++issued) load(issued);
 
   // ---- q rows of both maps to shared memory, f16 with a power-of-two prescale --------
-  // Row t G + g of map m is q[b][t][2 (pair G + g) + m][:].  Quantized pages run
-  // f16 MMAs: q is scaled by 2^e with max|q| 2^e in [2^14, 2^15) over the map's rows
-  // (exact for every element above max|q| 2^-31) and the scores divide it out.
-  // PACK: map 2's rows sit in columns 4-7.
-  {
-    const int st = tid & 127, m = tid >> 7;  // warps 0-3: map 0, 4-7: map 1
-    float mx = 0.f;
-    for (int i = st; i < R * (D / 8); i += 128) {
-      const int col = i / (D / 8), d8 = i % (D / 8);
-      const int qr = PACK ? col - 4 * m : col;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (qr >= 0 && qr < rows) {
-        const int t = qr / a.G, g = qr % a.G;
-        v = *reinterpret_cast<const uint4*>(
-            a.q + ((static_cast<int64_t>(b) * a.T + t) * a.Hq + 2 * (pair * a.G + g) + m) * D + d8 * 8);
-      }
-      *reinterpret_cast<uint4*>(qs + (m * R + col) * Cfg::Q_PITCH + d8 * 16) = v;
-      const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(__bfloat162float(e[k])));
+  // Column c of the 8 NT: map c / RB, row t G + g = c % RB, q[b][t][2 (pair G + g) + map].
+  // Quantized pages run f16 MMAs: a map's q is scaled by 2^e with max|q| 2^e in [2^14,
+  // 2^15) over its rows (exact for every element above max|q| 2^-31), and the scores
+  // divide it out.
+  float mx[2] = {0.f, 0.f};
+  for (int i = tid; i < 8 * NT * (D / 8); i += 32 * NW) {
+    const int col = i / (D / 8), d8 = i % (D / 8), m = col / RB, qr = col % RB;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (qr < rows) {
+      const int t = qr / a.G, g = qr % a.G;
+      v = *reinterpret_cast<const uint4*>(
+          a.q + ((static_cast<int64_t>(b) * a.T + t) * a.Hq + 2 * (pair * a.G + g) + m) * D + d8 * 8);
     }
+    *reinterpret_cast<uint4*>(qs + col * Cfg::Q_PITCH + d8 * 16) = v;
+    const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&v);
+    float most = 0.f;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    if (lane == 0) s_qmax[warp] = mx;
+    for (int k = 0; k < 8; ++k) most = fmaxf(most, fabsf(__bfloat162float(e[k])));
+    mx[0] = fmaxf(mx[0], m ? 0.f : most);
+    mx[1] = fmaxf(mx[1], m ? most : 0.f);
   }
-  asm volatile("bar.sync 1, %0;" ::"n"(NCONS) : "memory");
-  const auto q_exponent = [&](int m) {
-    float mx = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) mx = fmaxf(mx, s_qmax[4 * m + w]);
+  for (int m = 0; m < 2; ++m) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx[m] = fmaxf(mx[m], __shfl_xor_sync(0xffffffffu, mx[m], off));
+    if (lane == 0) s_qmax[NW * m + warp] = mx[m];
+  }
+  __syncthreads();
+  float sc[NT];       // scores to base 2: of the columns' map
+  float qmul[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    float most = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) most = fmaxf(most, s_qmax[NW * m + k]);
     int ex = 0;
-    if (mx > 0.f) frexpf(mx, &ex);
-    return mx > 0.f ? min(15 - ex, 100) : 0;
-  };
-  float sc = a.softmax_scale * kDiffLog2e;
-  if constexpr (!Cfg::MMA_BF16) {
-    const float mul = ldexpf(1.f, q_exponent(tid >> 7));
-    for (int i = tid & 127; i < R * D / 2; i += 128) {
-      uint32_t* p = reinterpret_cast<uint32_t*>(qs + ((tid >> 7) * R + i / (D / 2)) * Cfg::Q_PITCH + (i % (D / 2)) * 4);
-      const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(p);
-      *p = pack_f16x2(__low2float(v) * mul, __high2float(v) * mul);
-    }
-    sc *= exp2f(-static_cast<float>(q_exponent(side)));
-    asm volatile("bar.sync 1, %0;" ::"n"(NCONS) : "memory");
+    if (most > 0.f) frexpf(most, &ex);
+    const int e = Cfg::MMA_BF16 || !(most > 0.f) ? 0 : min(15 - ex, 100);
+    qmul[m] = ldexpf(1.f, e);
+    const float f = a.softmax_scale * kDiffLog2e * exp2f(-static_cast<float>(e));
+    if (PACK ? (c >> 1) == m : true) sc[PACK ? 0 : m] = f;
   }
-  uint32_t q[D / 16][2];  // operands of this side's map
+  uint32_t q[NT][D / 16][2];
 #pragma unroll
-  for (int s = 0; s < D / 16; ++s) {
-    const uint8_t* p = qs + (side * R + r) * Cfg::Q_PITCH;
-    q[s][0] = *reinterpret_cast<const uint32_t*>(p + 2 * diff_q_dim<KK>(s, 0, c));
-    q[s][1] = *reinterpret_cast<const uint32_t*>(p + 2 * diff_q_dim<KK>(s, 2, c));
-  }
-
-  // ---- running state: map `side` for the softmax, both maps for this half of V --------
-  float nm[2] = {0.f, 0.f}, l_part[2] = {0.f, 0.f};  // minus the reference maximum; sum
-  float o[MT][NT][4];                                // tiles: own map, the other's (PACK: one for both)
-  int k_run = 0;  // O carries 2^k_run (INT8 / FP8 values near the f16 limit, v_lift)
-  int lim[2];     // last key that a column's query sees
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int col = 2 * c + u, qr = PACK ? max(0, col - 4 * side) : col;
-    lim[u] = min(F - a.T + qr / a.G, F - 1);
-  }
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) o[mt][j][0] = o[mt][j][1] = o[mt][j][2] = o[mt][j][3] = 0.f;
-  // PACK: whether this lane's row r (of P^T) and columns 2c, 2c + 1 (of O) are the own map's
-  const bool own_r = (r < 4) == (side == 0), own_c = (c < 2) == (side == 0);
-  const int kr0 = 16 * slab + r, kr1 = kr0 + 8;
-
-  // A wait that ran out makes the rest of the loop run on whatever the stages
-  // hold, without waiting, so that the warps' barriers stay matched; the CTA
-  // leaves without results.
-  bool aborted = false;
-  for (int i = 0; i < n; ++i) {
-    const int s = i % NSTAGE;
-    const uint8_t* st = smem + s * Cfg::STAGE;
-    if (!aborted && !mbar_wait_bounded(&full[s], (i / NSTAGE) & 1, a.status)) aborted = true;
-    const int key0 = (p0 + i) * 64;
-    const uint8_t* vs_tile = st + Cfg::OFF_VS + side * Cfg::VS_TILE;
-
-    int knew = k_run;
-    if constexpr (KV == KIND_INT8 || KV == KIND_FP8) {  // the slab's largest value scale below the frontier
-      const int vk = 16 * slab + (lane & 15);
-      float smax = 0.f;
-      if (key0 + vk < F) {
-        if constexpr (KV == KIND_INT8) {
-#pragma unroll
-          for (int gi = lane >> 4; gi < D / 64; gi += 2) smax = fmaxf(smax, f16_at(vs_tile + vk * Cfg::VSB + 2 * gi));
-        } else {
-          smax = f16_at(vs_tile + vk * Cfg::VSB);
-        }
-      }
-      knew = v_lift(__reduce_max_sync(0xffffffffu, __float_as_uint(smax)), k_run);
-    }
-
-    float S[4];
-    diff_scores<KK, D>(st + side * Cfg::K_TILE, st + Cfg::OFF_KS + side * Cfg::KS_TILE, slab, lane, q, S);
-
-    // ---- softmax of this side's map over the slab's keys (lazy reference, base 2) ------
-    const int kg0 = key0 + kr0, kg1 = key0 + kr1;
-    const bool first = i == 0;
-    float alpha[2] = {1.f, 1.f}, top[2];
-    S[0] = kg0 <= lim[0] ? fmaf(S[0], sc, nm[0]) : -INFINITY;
-    S[1] = kg0 <= lim[1] ? fmaf(S[1], sc, nm[1]) : -INFINITY;
-    S[2] = kg1 <= lim[0] ? fmaf(S[2], sc, nm[0]) : -INFINITY;
-    S[3] = kg1 <= lim[1] ? fmaf(S[3], sc, nm[1]) : -INFINITY;
-    top[0] = fmaxf(S[0], S[2]);
-    top[1] = fmaxf(S[1], S[3]);
-    bool rescale = false;
-    if (__any_sync(0xffffffffu, first || top[0] > 8.f || top[1] > 8.f)) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float v = top[u];
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-        // the first page takes the exact maximum (a query's keys are a prefix:
-        // one that sees none here sees none later), later ones the excess
-        const float shift = first ? (v == -INFINITY ? 0.f : v) : fmaxf(v, 0.f);
-        alpha[u] = first ? 0.f : ex2(-shift);
-        rescale |= shift > 0.f;
-        nm[u] -= shift;
-        S[u] -= shift;
-        S[2 + u] -= shift;
-        l_part[u] *= alpha[u];
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      S[u] = ex2(S[u]);
-      S[2 + u] = ex2(S[2 + u]);
-      l_part[u] += S[u] + S[2 + u];
-    }
-    rescale = __any_sync(0xffffffffu, rescale) && !first;  // O is 0 before the first page
-
-    // ---- P^T as B operands, and the exchange with the other side's warp -----------------
-    uint32_t pb[PARTS][NT][2];
-    float al[NT][2];
-    {
-      uint32_t mine[XW];
-      if constexpr (Cfg::MMA_BF16) {  // bf16 weights as hi + lo (about 16 significant bits)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const __nv_bfloat162 hi = __floats2bfloat162_rn(S[2 * h], S[2 * h + 1]);
-          const __nv_bfloat162 lo = __floats2bfloat162_rn(S[2 * h] - __low2float(hi), S[2 * h + 1] - __high2float(hi));
-          mine[h] = diff_movm(*reinterpret_cast<const uint32_t*>(&hi));
-          mine[2 * (PARTS - 1) + h] = diff_movm(*reinterpret_cast<const uint32_t*>(&lo));
-        }
-      } else {
-        mine[0] = diff_movm(pack_f16x2(S[0], S[1]));
-        mine[1] = diff_movm(pack_f16x2(S[2], S[3]));
-      }
-      mine[2 * PARTS] = __float_as_uint(alpha[0]);
-      mine[2 * PARTS + 1] = __float_as_uint(alpha[1]);
-      mine[XW - 1] = rescale;
-      uint32_t* to = sx + ((i & 1) * NW + warp) * (XW * 32) + lane;
-      const uint32_t* from = sx + ((i & 1) * NW + (warp ^ 1)) * (XW * 32) + lane;
-#pragma unroll
-      for (int x = 0; x < XW; ++x) to[x * 32] = mine[x];
-      asm volatile("bar.sync %0, 64;" ::"r"(2 + slab) : "memory");
-      uint32_t other[XW];
-#pragma unroll
-      for (int x = 0; x < XW; ++x) other[x] = from[x * 32];
-      rescale |= other[XW - 1] != 0u;
+    for (int k = 0; k < D / 16; ++k) {
+      const uint8_t* p = qs + (8 * j + r) * Cfg::Q_PITCH;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(p + 2 * diff_q_dim<KK>(k, 2 * h, c));
+        if constexpr (Cfg::MMA_BF16) {
+          q[j][k][h] = x;
+        } else {
+          const float f = qmul[PACK ? r >> 2 : j];
+          q[j][k][h] = pack_f16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xFFFF0000u) * f);
+        }
+      }
+    }
+
+  // ---- running state ------------------------------------------------------------------
+  float nm[NT][2], l_part[NT][2];  // per column: minus the reference maximum; sum
+  float o[2][MT][NT][4];           // per value head
+  // FP8-row / INT8-G64 values: the weights of head v carry 2^lift[v], and so does its O;
+  // it falls when a scale's bits reach lift_at[v]
+  int lift[2] = {kVLiftInit, kVLiftInit};
+  int lim[NT][2];  // last key that a column's query sees
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) {
-          const int x = 2 * part + h;
-          if constexpr (PACK) {
-            pb[part][0][h] = own_r ? mine[x] : other[x];
-          } else {
-            pb[part][0][h] = mine[x];
-            pb[part][NT - 1][h] = other[x];
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      nm[j][u] = l_part[j][u] = 0.f;
+      lim[j][u] = min(F - a.T + ((8 * j + 2 * c + u) % RB) / a.G, F - 1);
+    }
+#pragma unroll
+  for (int v = 0; v < 2; ++v)
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) o[v][mt][j][0] = o[v][mt][j][1] = o[v][mt][j][2] = o[v][mt][j][3] = 0.f;
+  uint8_t* vw = smem + Cfg::OFF_VW + warp * Cfg::VW_BYTES;
+  const int ld_row = (lane & 7) + ((lane >> 4) & 1) * 8, ld_col = 16 * ((lane >> 3) & 1);  // transposed reads
+
+  bool aborted = false;
+  for (int i = 0; i < ng; ++i) {
+    const int s = grp * SG + i % SG;
+    uint8_t* st = smem + s * Cfg::STAGE;
+    if (!mbar_wait_bounded(&full[s], (i / SG) & 1, a.status)) {
+      aborted = true;
+      break;
+    }
+    const int key0 = (p0 + grp + i * NG) * 64 + 16 * slab;  // this warp's first key
+    const uint8_t* vst[2] = {st + Cfg::OFF_VS, st + Cfg::OFF_VS + Cfg::VS_TILE};
+
+    if (key0 + 16 > F) {  // stale value rows become zero, codes and scales
+      const int kz = max(0, F - key0);
+      for (int x = lane; x < (16 - kz) * 2 * (Cfg::VCB / 16); x += 32) {
+        const int v = x / ((16 - kz) * (Cfg::VCB / 16)), y = x % ((16 - kz) * (Cfg::VCB / 16));
+        const int key = 16 * slab + kz + y / (Cfg::VCB / 16), col = y % (Cfg::VCB / 16) * 16;
+        *reinterpret_cast<uint4*>(st + Cfg::OFF_V + v * Cfg::V_TILE + (col / Cfg::V_RB) * (64 * Cfg::V_RB) +
+                                  key * Cfg::V_RB + col % Cfg::V_RB) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if constexpr (Cfg::VSB > 0)
+        for (int x = lane; x < (16 - kz) * 2 * Cfg::VSB; x += 32) {
+          const int v = x / ((16 - kz) * Cfg::VSB), y = x % ((16 - kz) * Cfg::VSB);
+          st[Cfg::OFF_VS + v * Cfg::VS_TILE + (16 * slab + kz) * Cfg::VSB + y] = 0;
+        }
+      __syncwarp();
+    }
+
+    float S[NT][4];
+    if constexpr (PACK) {  // both heads' scores of all columns; a lane's are those of its map's head
+      float S2[4];
+      diff_scores<KK, D>(st, st + Cfg::OFF_KS, slab, lane, q[0], S[0]);
+      diff_scores<KK, D>(st + Cfg::K_TILE, st + Cfg::OFF_KS + Cfg::KS_TILE, slab, lane, q[0], S2);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[0][e] = c >> 1 ? S2[e] : S[0][e];
+    } else {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        diff_scores<KK, D>(st + j * Cfg::K_TILE, st + Cfg::OFF_KS + j * Cfg::KS_TILE, slab, lane, q[j], S[j]);
+    }
+
+    // ---- the stage of the page before, for the page SG further on ------------------------
+    // (here the group's other warps have long left it)
+    if (i > 0 && issued < ng) {
+      const int e = i - 1;
+      if (!mbar_wait_bounded(&empty[grp * SG + e % SG], (e / SG) & 1, a.status)) {
+        aborted = true;
+        break;
+      }
+      load(issued++);
+    }
+
+    // ---- softmax over the warp's keys (lazy reference, base 2) --------------------------
+    const bool first = i == 0;
+    float alpha[NT][2];
+    bool need = first, rescale = false;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[j][e] = fmaf(S[j][e], sc[j], nm[j][e & 1]);
+      alpha[j][0] = alpha[j][1] = 1.f;
+    }
+    if (key0 + 15 > F - a.T) {  // not seen whole by every query
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (key0 + r + 8 * (e >> 1) > lim[j][e & 1]) S[j][e] = -INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) need = need || fmaxf(fmaxf(S[j][0], S[j][1]), fmaxf(S[j][2], S[j][3])) > 8.f;
+    if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float v = fmaxf(S[j][u], S[j][2 + u]);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+          // the first page takes the exact maximum (a query's keys are a prefix:
+          // one that sees none here sees none later), later ones the excess
+          const float shift = first ? (v == -INFINITY ? 0.f : v) : fmaxf(v, 0.f);
+          alpha[j][u] = first ? 0.f : ex2(-shift);
+          rescale |= shift > 0.f;
+          nm[j][u] -= shift;
+          S[j][u] -= shift;
+          S[j][2 + u] -= shift;
+          l_part[j][u] *= alpha[j][u];
+        }
+      rescale = __any_sync(0xffffffffu, rescale) && !first;  // O is 0 before the first page
+    }
+    uint32_t pb[PARTS][NT][2];  // P^T as B operands
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[j][e] = ex2(S[j][e]);
+      l_part[j][0] += S[j][0] + S[j][2];
+      l_part[j][1] += S[j][1] + S[j][3];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (Cfg::MMA_BF16) {  // bf16 weights as hi + lo (about 16 significant bits)
+          const __nv_bfloat162 hi = __floats2bfloat162_rn(S[j][2 * h], S[j][2 * h + 1]);
+          const __nv_bfloat162 lo =
+              __floats2bfloat162_rn(S[j][2 * h] - __low2float(hi), S[j][2 * h + 1] - __high2float(hi));
+          pb[0][j][h] = diff_movm(*reinterpret_cast<const uint32_t*>(&hi));
+          pb[PARTS - 1][j][h] = diff_movm(*reinterpret_cast<const uint32_t*>(&lo));
+        } else {
+          pb[0][j][h] = diff_movm(pack_f16x2(S[j][2 * h], S[j][2 * h + 1]));
+        }
+      }
+    }
+
+    // ---- O^T (dims x columns) += V^T P^T, head by head ----------------------------------
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      float kf = 1.f;
+      bool fall = false;
+      if constexpr (Cfg::VAL_FAC) {  // does a scale take the lifted weights past 2^15?
+        constexpr int GR = KV == KIND_INT8 ? D / 64 : 1;  // scales of a key
+        uint32_t most = 0u;
+#pragma unroll
+        for (int g = 0; g < GR; ++g)
+          most = max(most, static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(
+                               vst[v] + (16 * slab + (lane & 15)) * Cfg::VSB + 2 * g)));
+        // s 2^lift >= 2^7, for the binary16 bits of s (lift <= 30: subnormal scales too)
+        const float sm = __half2float(__ushort_as_half(static_cast<uint16_t>(most)));
+        fall = __any_sync(0xffffffffu, sm * pow2i(lift[v]) >= 128.f);
+        if (fall) {
+          const int k = v_lift(__reduce_max_sync(0xffffffffu, __float_as_uint(sm)), lift[v]);
+          kf = pow2i(k - lift[v]);
+          lift[v] = k;
+        }
+      }
+      if (rescale || fall) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[v][mt][j][e] *= alpha[j][e & 1] * kf;
+      }
+      const uint8_t* vtile = st + Cfg::OFF_V + v * Cfg::V_TILE;
+      if constexpr (KV == KIND_BF16) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int col = 32 * mt + ld_col;
+          uint32_t A[4];
+          ldsm_x4_t(smem_u32(vtile) + (col / 128) * (64 * 128) + swz<128>(16 * slab + ld_row, col % 128), A[0], A[1],
+                    A[2], A[3]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) mma16816<true>(o[v][mt][j], A, pb[part][j][0], pb[part][j][1]);
+        }
+      } else {
+        uint32_t ps[NT][2];  // the weights of this head's (and group's) scales
+#pragma unroll
+        for (int q64 = 0; q64 < D / 64; ++q64) {
+          __syncwarp();  // the block before has been read
+          diff_values<KV, D>(vtile, vst[v], vw, q64, slab, lane);
+          if constexpr (Cfg::VAL_FAC) {
+            if (q64 == 0 || KV == KIND_INT8) {
+              // weights of keys 2c, 2c + 1 (h = 0) and 2c + 8, 2c + 9; each product rounds once more
+              const uint32_t l2 = static_cast<uint32_t>(static_cast<uint16_t>(__half_as_ushort(__float2half_rn(pow2i(min(lift[v], 15)))))) * 0x00010001u;
+              const uint32_t l3 = static_cast<uint32_t>(static_cast<uint16_t>(__half_as_ushort(__float2half_rn(pow2i(max(lift[v] - 15, 0)))))) * 0x00010001u;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint8_t* at = vst[v] + (16 * slab + 2 * c + 8 * h) * Cfg::VSB + (KV == KIND_INT8 ? 2 * q64 : 0);
+                const uint32_t s2 = Cfg::VSB == 2 ? *reinterpret_cast<const uint32_t*>(at)
+                                                  : static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at)) |
+                                                        static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at + Cfg::VSB)) << 16;
+                const uint32_t f = hmul2_u32(hmul2_u32(s2, l2), l3);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) ps[j][h] = hmul2_u32(pb[0][j][h], f);
+              }
+            }
+          } else if (q64 == 0) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) ps[j][0] = pb[0][j][0], ps[j][1] = pb[0][j][1];
+          }
+          __syncwarp();
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            uint32_t A[4];
+            ldsm_x4_t(smem_u32(vw) + swz<128>(ld_row, 32 * mt + ld_col), A[0], A[1], A[2], A[3]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma16816<false>(o[v][4 * q64 + mt][j], A, ps[j][0], ps[j][1]);
           }
         }
-        const int x = 2 * PARTS + h;
-        if constexpr (PACK) {
-          al[0][h] = __uint_as_float(own_c ? mine[x] : other[x]);
-        } else {
-          al[0][h] = __uint_as_float(mine[x]);
-          al[NT - 1][h] = __uint_as_float(other[x]);
-        }
-      }
-    }
-    if (rescale || knew != k_run) {
-      const float kf = pow2i(knew - k_run);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          o[mt][j][0] *= al[j][0] * kf;
-          o[mt][j][1] *= al[j][1] * kf;
-          o[mt][j][2] *= al[j][0] * kf;
-          o[mt][j][3] *= al[j][1] * kf;
-        }
-    }
-    k_run = knew;
-
-    // ---- O^T (D dims of half `side` x columns) += V^T P^T -----------------------------------
-    const uint8_t* vtile = st + Cfg::OFF_V + side * Cfg::V_TILE;
-    if constexpr (KV == KIND_BF16) {
-      const int kvalid = F - key0, kk0 = 16 * slab + 2 * c;
-      uint32_t mlo = 0xFFFFFFFFu, mhi = 0xFFFFFFFFu;  // stale values past the frontier become zero
-      if (kvalid < 64) {
-        mlo = (kk0 < kvalid ? 0x0000FFFFu : 0u) | (kk0 + 1 < kvalid ? 0xFFFF0000u : 0u);
-        mhi = (kk0 + 8 < kvalid ? 0x0000FFFFu : 0u) | (kk0 + 9 < kvalid ? 0xFFFF0000u : 0u);
-      }
-      const int key = 16 * slab + (lane & 7) + ((lane >> 4) & 1) * 8;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int col = (16 * mt + 8 * ((lane >> 3) & 1)) * 2;
-        uint32_t A[4];
-        ldsm_x4_t(smem_u32(vtile) + (col / 128) * (64 * 128) + swz<128>(key, col % 128), A[0], A[1], A[2], A[3]);
-        A[0] &= mlo, A[1] &= mlo, A[2] &= mhi, A[3] &= mhi;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int part = 0; part < PARTS; ++part) mma16816<true>(o[mt][j], A, pb[part][j][0], pb[part][j][1]);
-      }
-    } else {
-      uint8_t* vw = smem + Cfg::OFF_VW + warp * Cfg::VW_BYTES;
-      const uint32_t lift2 = static_cast<uint32_t>(k_run + 15) * 0x04000400u;  // f16x2 of 2^k_run
-      // (the previous page's fragments were read before the barrier above)
-      diff_values<KV, D>(vtile, vs_tile, vw, slab, lane, key0 + 16 * slab + (lane & 15) < F, lift2);
-      __syncwarp();
-      const int key = (lane & 7) + ((lane >> 4) & 1) * 8;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int col = (16 * (mt & 3) + 8 * ((lane >> 3) & 1)) * 2;
-        uint32_t A[4];
-        ldsm_x4_t(smem_u32(vw + (mt >> 2) * (16 * 128)) + swz<128>(key, col), A[0], A[1], A[2], A[3]);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) mma16816<false>(o[mt][j], A, pb[0][j][0], pb[0][j][1]);
       }
     }
     __syncwarp();
     if (lane == 0) diff_arrive(&empty[s]);
   }
 
-  // ---- the slabs' results into one partial ----------------------------------------------
+  // ---- the warps' results into one partial ----------------------------------------------
   // Sums of a column over the lanes that hold its keys; the reference maximum is
   // -inf for a query that saw no key (one that saw a key has l >= 1; NaN stays).
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    float v = l_part[u];
-    v += __shfl_xor_sync(0xffffffffu, v, 4);
-    v += __shfl_xor_sync(0xffffffffu, v, 8);
-    v += __shfl_xor_sync(0xffffffffu, v, 16);
-    if (r == 0) {
-      red_m[(slab * 2 + side) * R + 2 * c + u] = v == 0.f ? -INFINITY : -nm[u];
-      red_l[(slab * 2 + side) * R + 2 * c + u] = v;
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float v = l_part[j][u];
+      v += __shfl_xor_sync(0xffffffffu, v, 4);
+      v += __shfl_xor_sync(0xffffffffu, v, 8);
+      v += __shfl_xor_sync(0xffffffffu, v, 16);
+      if (r == 0) {
+        red_m[warp * 2 * RB + 8 * j + 2 * c + u] = v == 0.f ? -INFINITY : -nm[j][u];
+        red_l[warp * 2 * RB + 8 * j + 2 * c + u] = v;
+      }
     }
-  }
   if (aborted && lane == 0) s_flags[0] = 1;
-  asm volatile("bar.sync 1, %0;" ::"n"(NCONS) : "memory");
+  __syncthreads();
   if (s_flags[0]) {  // copies in flight land before the CTA leaves
-    if (tid == 0)
-      for (int k = max(0, n - NSTAGE); k < n; ++k)
-        mbar_wait_bounded(&full[k % NSTAGE], (k / NSTAGE) & 1, a.status, 100000000ull);
+    for (int k = max(0, issued - SG); k < issued; ++k)
+      mbar_wait_bounded(&full[grp * SG + k % SG], (k / SG) & 1, a.status, 100000000ull);
     return;
   }
-  if (tid < 2 * R) {
+  if (tid < 2 * RB) {
     float M = -INFINITY, Ls = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, red_m[w * 2 * R + tid]);
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, red_m[w * 2 * RB + tid]);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float l = red_l[w * 2 * R + tid];
-      if (l != 0.f) Ls += l * ex2(red_m[w * 2 * R + tid] - M);
+    for (int w = 0; w < NW; ++w) {
+      const float l = red_l[w * 2 * RB + tid];
+      if (l != 0.f) Ls += l * ex2(red_m[w * 2 * RB + tid] - M);
     }
     row_M[tid] = M;
     row_L[tid] = Ls;
   }
-  asm volatile("bar.sync 1, %0;" ::"n"(NCONS) : "memory");
-  float* comb = reinterpret_cast<float*>(smem);  // [4 slabs][2 maps][RB][O_PITCH], over the ring
-  {
-    const float unlift = pow2i(-k_run);
+  __syncthreads();
+  float* comb = reinterpret_cast<float*>(smem);  // [NW][2 maps][RB][O_PITCH], over the ring
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int col = 2 * c + u, map = PACK ? c >> 1 : side ^ j;
-        const int qr = PACK ? col & 3 : col;
-        const float m = red_m[(slab * 2 + map) * R + col];
-        const float f = m == -INFINITY ? 0.f : ex2(m - row_M[map * R + col]) * unlift;
-        float* dst = comb + ((slab * 2 + map) * RB + qr) * Cfg::O_PITCH + side * D + r;
+    for (int u = 0; u < 2; ++u) {
+      const int col = 8 * j + 2 * c + u;  // = map RB + row
+      const float m = red_m[warp * 2 * RB + col];
+      const float f = m == -INFINITY ? 0.f : ex2(m - row_M[col]);
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const float fv = Cfg::VAL_FAC ? f * pow2i(-lift[v]) : f;
+        float* dst = comb + (warp * 2 * RB + col) * Cfg::O_PITCH + v * D + r;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          dst[16 * mt] = o[mt][j][u] * f;
-          dst[16 * mt + 8] = o[mt][j][2 + u] * f;
+          dst[16 * mt] = o[v][mt][j][u] * fv;
+          dst[16 * mt + 8] = o[v][mt][j][2 + u] * fv;
         }
       }
-  }
-  asm volatile("bar.sync 1, %0;" ::"n"(NCONS) : "memory");
+    }
+  __syncthreads();
   const int64_t slot = static_cast<int64_t>(pair) * a.ctas + cta;
-  for (int idx = tid; idx < 2 * rows * (D / 2); idx += NCONS) {
+  for (int idx = tid; idx < 2 * rows * (D / 2); idx += 32 * NW) {
     const int d = (idx % (D / 2)) * 4, map = idx / (D / 2) / rows, qr = idx / (D / 2) % rows;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < NW; ++w) {
       const float4 x = *reinterpret_cast<const float4*>(comb + ((w * 2 + map) * RB + qr) * Cfg::O_PITCH + d);
       v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
     }
     *reinterpret_cast<float4*>(a.ws_o + ((slot * 2 + map) * RB + qr) * (2 * D) + d) = v;
   }
   if (tid < 2 * rows) {
-    const int map = tid / rows, qr = tid % rows, col = PACK ? qr + 4 * map : qr;
-    a.ws_ml[(slot * 2 + map) * RB + qr] = make_float2(row_M[map * R + col], row_L[map * R + col]);
+    const int map = tid / rows, qr = tid % rows;
+    a.ws_ml[(slot * 2 + map) * RB + qr] = make_float2(row_M[map * RB + qr], row_L[map * RB + qr]);
   }
 }
 
@@ -679,49 +687,22 @@ cudaError_t launch_diff_decode(const nk_pool* p, int layer, const DiffDecodeArgs
                     p->tmap[layer * 2 + 1], a);
 }
 
-template <int KK, int KV, int D, bool PACK>
-int diff_ctas_per_sm() {
-  using Cfg = DiffCfg<KK, KV, D, PACK>;
-  static std::atomic<uint64_t> granted{0};
-  static std::atomic<int> cached[64];
-  int device = 0;
-  if (cudaGetDevice(&device) != cudaSuccess) return 1;
-  int n = device < 64 ? cached[device].load(std::memory_order_relaxed) : 0;
-  if (n) return n;
-  auto k = diff_decode_kernel<KK, KV, D, PACK>;
-  if (grant_smem(granted, k, Cfg::SMEM) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, Cfg::THREADS, Cfg::SMEM) != cudaSuccess || n < 1)
-    n = 1;
-  if (device < 64) cached[device].store(n, std::memory_order_relaxed);
-  return n;
-}
-
-// Per-profile entries (diff_decode_*.cu).  pack: up to 4 query rows.  a ==
-// nullptr: only the CTAs per SM are asked, in *per_sm.
-using DiffDecodeFn = cudaError_t (*)(const nk_pool*, int layer, const DiffDecodeArgs* a, bool pack, int* per_sm,
-                                     cudaStream_t);
-
-template <int KK, int KV, int D, bool PACK>
-cudaError_t diff_decode_one(const nk_pool* p, int layer, const DiffDecodeArgs* a, int* per_sm, cudaStream_t s) {
-  if (a) return launch_diff_decode<KK, KV, D, PACK>(p, layer, *a, s);
-  *per_sm = diff_ctas_per_sm<KK, KV, D, PACK>();
-  return cudaSuccess;
-}
+// Per-profile entries (diff_decode_*.cu).  pack: up to 4 query rows.
+using DiffDecodeFn = cudaError_t (*)(const nk_pool*, int layer, const DiffDecodeArgs&, bool pack, cudaStream_t);
 
 template <int KK, int KV>
-cudaError_t diff_decode_dispatch(const nk_pool* p, int layer, const DiffDecodeArgs* a, bool pack, int* per_sm,
-                                 cudaStream_t s) {
-  if (p->desc.head_dim == 64)
-    return pack ? diff_decode_one<KK, KV, 64, true>(p, layer, a, per_sm, s)
-                : diff_decode_one<KK, KV, 64, false>(p, layer, a, per_sm, s);
-  return pack ? diff_decode_one<KK, KV, 128, true>(p, layer, a, per_sm, s)
-              : diff_decode_one<KK, KV, 128, false>(p, layer, a, per_sm, s);
+cudaError_t diff_decode_dispatch(const nk_pool* p, int layer, const DiffDecodeArgs& a, bool pack, cudaStream_t s) {
+  if (p->desc.head_dim == 128)
+    return pack ? launch_diff_decode<KK, KV, 128, true>(p, layer, a, s)
+                : launch_diff_decode<KK, KV, 128, false>(p, layer, a, s);
+  return pack ? launch_diff_decode<KK, KV, 64, true>(p, layer, a, s)
+              : launch_diff_decode<KK, KV, 64, false>(p, layer, a, s);
 }
 
-cudaError_t diff_decode_bf16(const nk_pool*, int, const DiffDecodeArgs*, bool, int*, cudaStream_t);
-cudaError_t diff_decode_int8(const nk_pool*, int, const DiffDecodeArgs*, bool, int*, cudaStream_t);
-cudaError_t diff_decode_fp8(const nk_pool*, int, const DiffDecodeArgs*, bool, int*, cudaStream_t);
-cudaError_t diff_decode_nvfp4(const nk_pool*, int, const DiffDecodeArgs*, bool, int*, cudaStream_t);
-cudaError_t diff_decode_k8v4(const nk_pool*, int, const DiffDecodeArgs*, bool, int*, cudaStream_t);
+cudaError_t diff_decode_bf16(const nk_pool*, int, const DiffDecodeArgs&, bool, cudaStream_t);
+cudaError_t diff_decode_int8(const nk_pool*, int, const DiffDecodeArgs&, bool, cudaStream_t);
+cudaError_t diff_decode_fp8(const nk_pool*, int, const DiffDecodeArgs&, bool, cudaStream_t);
+cudaError_t diff_decode_nvfp4(const nk_pool*, int, const DiffDecodeArgs&, bool, cudaStream_t);
+cudaError_t diff_decode_k8v4(const nk_pool*, int, const DiffDecodeArgs&, bool, cudaStream_t);
 
 }  // namespace nk

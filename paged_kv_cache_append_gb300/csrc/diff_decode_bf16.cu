@@ -3,8 +3,8 @@
 
 namespace nk {
 
-cudaError_t diff_decode_bf16(const nk_pool* p, int layer, const DiffDecodeArgs* a, bool pack, int* per_sm, cudaStream_t s) {
-  return diff_decode_dispatch<KIND_BF16, KIND_BF16>(p, layer, a, pack, per_sm, s);
+cudaError_t diff_decode_bf16(const nk_pool* p, int layer, const DiffDecodeArgs& a, bool pack, cudaStream_t s) {
+  return diff_decode_dispatch<KIND_BF16, KIND_BF16>(p, layer, a, pack, s);
 }
 
 }  // namespace nk

@@ -3,8 +3,8 @@
 
 namespace nk {
 
-cudaError_t diff_decode_int8(const nk_pool* p, int layer, const DiffDecodeArgs* a, bool pack, int* per_sm, cudaStream_t s) {
-  return diff_decode_dispatch<KIND_INT8, KIND_INT8>(p, layer, a, pack, per_sm, s);
+cudaError_t diff_decode_int8(const nk_pool* p, int layer, const DiffDecodeArgs& a, bool pack, cudaStream_t s) {
+  return diff_decode_dispatch<KIND_INT8, KIND_INT8>(p, layer, a, pack, s);
 }
 
 }  // namespace nk

@@ -152,35 +152,23 @@ __device__ __forceinline__ DiffWork diff_chunk_work(const DiffTileArgs& a) {
   return w;
 }
 
-// Decode: the split plan of all rows, from the frontiers (scratch: 16 ints of
-// shared memory; every thread of the CTA takes part).
-__device__ __forceinline__ DiffWork diff_decode_work(const DiffTileArgs& a, int* s_F) {
+// Decode: the CTA's split of the plan of all rows.
+__device__ __forceinline__ DiffWork diff_decode_work(const DiffTileArgs& a) {
   DiffWork w;
-  const int cta = blockIdx.x, tid = threadIdx.x;
   w.pair = blockIdx.y;
   w.map = 0;
-  w.n = -1;
-  if (tid < a.B)
-    s_F[tid] = diff_length(a.lengths, a.table_rows, tid, a.L, a.C, &s_F[8 + tid],
-                           cta == 0 && w.pair == 0 ? a.status : nullptr);
-  __syncthreads();
-  const int chunk = diff_chunk(s_F, a.B, a.ctas, kDiffMaxSplits);
-  for (int b = 0, at = 0; b < a.B; ++b) {
-    const int np = (s_F[b] + 63) >> 6, ns = max(1, (np + chunk - 1) / chunk);
-    if (cta < at + ns) {
-      w.b = b;
-      w.row = s_F[8 + b];
-      w.F = s_F[b];
-      w.t0 = 0;
-      w.limit = a.T;
-      w.pos0 = w.F - a.T;
-      w.p_lo = (cta - at) * chunk;
-      w.n = min(chunk, np - w.p_lo);  // 0 only for a row without keys
-      w.part = static_cast<int64_t>(w.pair) * a.ctas + cta;
-      break;
-    }
-    at += ns;
-  }
+  const DiffSplit own = diff_split(diff_rows(a.lengths, a.table_rows, a.B, a.L, a.C, a.ctas,
+                                             blockIdx.x == 0 && w.pair == 0 && threadIdx.x < 32 ? a.status : nullptr),
+                                   a.B, blockIdx.x);
+  w.b = own.b;
+  w.row = own.row;
+  w.F = own.F;
+  w.t0 = 0;
+  w.limit = a.T;
+  w.pos0 = w.F - a.T;
+  w.p_lo = own.p0;
+  w.n = own.b < 0 ? -1 : own.n;
+  w.part = static_cast<int64_t>(w.pair) * a.ctas + blockIdx.x;
   return w;
 }
 
@@ -259,7 +247,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
   griddep_wait();  // launched with programmatic stream serialization
   griddep_launch_dependents();
   DiffWork w;
-  if constexpr (BOTH) w = diff_decode_work(a, reinterpret_cast<int*>(sX));
+  if constexpr (BOTH) w = diff_decode_work(a);
   else w = diff_chunk_work(a);
   const int n = w.n;
   if (n < 0) return;
