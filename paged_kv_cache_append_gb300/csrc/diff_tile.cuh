@@ -12,9 +12,9 @@
 // 1, lanes 64-127 those of map 2, so that every page is read and converted once:
 //   S = [Q1; 0] K1^T + [0; Q2] K2^T, two MMAs into one S.
 //
-// Tensor memory: S buffers [0, 64) and [64, 128), Q [128, 128 + D / 2) (BOTH: two
-// operands), O [256, 256 + 2 D).  P goes over the S that its own warp computed it from:
-// keys [32 h, +32) in columns [32 h, +16) of the buffer.
+// Tensor memory: NS S buffers of 64 columns, Q (D / 2 columns; BOTH: two operands), O
+// [256, 256 + 2 D).  P goes over the S that its own warp computed it from: keys
+// [32 h, +32) in columns [32 h, +16) of the buffer.
 //
 // Operands.  Scores: BF16 pages as they are; FP8-row keys of head_dim 128 as raw
 // E4M3 codes with q in two E4M3 terms, other quantized keys as exact f16 tiles
@@ -31,11 +31,13 @@
 //     divides it out.
 // FP8-row value factors are lifted by a power of two of their own (v_lift).
 //
-// Warps (576 threads): 0-7 softmax, warp w lanes 32 (w & 3) and keys 32 (w >> 2) of
-// a page; 8 TMA producer; 9 MMA issuer; 10-17 converters.  The two warps of a row
-// tell each other its maximum while they already take the exponentials under the old
-// reference, which moves lazily (by a score more than 2^8 above it); only then are
-// they taken again.  The MMAs are issued by an elected lane of a warp that runs the
+// Warps (640 threads): 0-7 softmax, warp w lanes 32 (w & 3) of every second page, from
+// w >> 2 on; 8 TMA producer; 9 and 10 MMA issuers, of S and of PV; 11 factors of the
+// keys' scales; 12-19 converters, in two groups on alternate pages.  A page's softmax is a
+// chain of waits and tensor-memory trips of some 1200 cycles, longer than the MMAs of a
+// page (800, head_dim 128): so two pages are in it at a time, S NS - 1 pages ahead of PV.
+// The warps of a row hand on its reference maximum from page to page, right after the
+// page's maximum; it moves lazily (by a score more than 2^8 above it).  The MMAs are issued by an elected lane of a warp that runs the
 // loop as a whole: from a branch of one lane each issue took 47-54 cycles (probe:
 // M 128, N 64, A in tensor memory), from the whole warp the 33 of the tensor core.
 //
@@ -75,8 +77,12 @@ constexpr int kDiffSplitPages = 4;
 
 template <int KK, int KV, int D, bool BOTH>
 struct DiffTileCfg {
-  static constexpr int NSOFT = 8, NCONV = 8, THREADS = 32 * (NSOFT + 2 + NCONV);
   static constexpr bool BF16 = KK == KIND_BF16;
+  static constexpr int NSOFT = 8, NCONV = 8, THREADS = 32 * (NSOFT + 4 + NCONV);
+  // Registers: 640 threads start with 96 each; the softmax warps (64 scores and 16 or 32
+  // packed weights at a time) take over what the others do not need.
+  static constexpr int R_SOFT = BF16 ? 128 : 144, R_MISC = 40, R_CONV = BF16 ? 88 : 72;
+  static_assert(256 * R_SOFT + 128 * R_MISC + 256 * R_CONV <= 640 * 96, "registers of the CTA");
   static constexpr int KCB = BF16 ? 2 * D : code_row_bytes<KK>(D), VCB = BF16 ? 2 * D : code_row_bytes<KV>(D);
   static constexpr int KSB = scale_row_bytes<KK>(D), VSB = scale_row_bytes<KV>(D);
   static constexpr int K_RB = KCB < 128 ? KCB : 128, V_RB = VCB < 128 ? VCB : 128;
@@ -93,21 +99,27 @@ struct DiffTileCfg {
   static constexpr int RV_HEAD = (RV_CODES + 64 * VSB + 1023) / 1024 * 1024, RV_STAGE = BF16 ? 0 : 2 * RV_HEAD;
   static constexpr int K_HEAD = K_SPLIT ? 2 * F16 : F16, K_STAGE = K_RAW ? 0 : KH * K_HEAD;
   static constexpr int V_STAGE = 2 * F16;
-  // ring depths, as shared memory allows
-  static constexpr int NRK = D == 64 ? (BF16 && !BOTH ? 8 : 4) : K_SPLIT ? (BOTH ? 2 : 3) : BOTH && KV != KIND_NVFP4 ? 3 : BOTH && !K_RAW ? 3 : 4;
-  static constexpr int NK = K_RAW ? 1 : D == 64 ? (K_SPLIT && BOTH ? 2 : 3) : K_SPLIT ? (BOTH ? 1 : 2) : BOTH ? 2 : 3;
-  static constexpr int NV = D == 64 ? 4 : K_SPLIT ? 2 : K_RAW && !BOTH && KV != KIND_FP8 ? 4 : 3;
-  static constexpr int NRV = BF16 ? NV : D == 64 ? 4 : K_SPLIT ? 2 : BOTH && !K_RAW ? 2 : 3;
+  // Groups of converter warps, on alternate pages; one where the f16 keys fit once
+  // (INT8-G64 decode, head_dim 128), and for BF16, whose strips go from page to page.
+  static constexpr int NCG = BF16 || (K_SPLIT && BOTH && D == 128) ? 1 : 2, CGW = NCONV / NCG;
+  // Ring depths, as shared memory allows; a group's slots are its own.
+  static constexpr int NRK = D == 64 ? (BF16 && !BOTH ? 8 : 4) : BOTH ? (BF16 || (K8MMA && KV == KIND_NVFP4) ? 3 : K_SPLIT ? 2 : 4) : 4;
+  static constexpr int NK = K_RAW ? 1 : D == 64 ? (K_SPLIT && BOTH ? 2 : 4) : K_SPLIT && BOTH ? 1 : 2;
+  static constexpr int NV = D == 64 ? 4 : BF16 ? (BOTH ? 3 : 4) : K_SPLIT || (BOTH && KV != KIND_NVFP4) || (BOTH && !K_RAW) ? 2 : 4;
+  static constexpr int NRV = BF16 ? NV : D == 64 ? 4 : BOTH && !K_SPLIT && !(K8MMA && KV == KIND_NVFP4) ? 4 : 2;
+  static_assert(NCG == 1 || (NV % 2 == 0 && NRV % 2 == 0 && (K_RAW || (NK % 2 == 0 && NRK % 2 == 0))), "a group's slots");
   static constexpr int NF = 4;  // factor ring: 1 KB per page
   static constexpr int OFF_V = NK * K_STAGE;
   static constexpr int OFF_RK = OFF_V + NV * V_STAGE;
   static constexpr int OFF_RV = OFF_RK + NRK * RK_STAGE;
   static constexpr int OFF_F = OFF_RV + NRV * RV_STAGE;
-  static constexpr int OFF_X = OFF_F + NF * 1024;  // [2][2][128] maxima of the rows' halves
-  static constexpr int OFF_BAR = OFF_X + 2048;
-  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NRK + 2 * NRV + 2 * NF + 6 + 16;
+  static constexpr int NS = BOTH && D == 128 ? 2 : 3;  // S buffers
+  static constexpr int OFF_X = OFF_F + NF * 1024;  // [2][128] references, [2][128] final (reference, sum)
+  static constexpr int OFF_BAR = OFF_X + 4096;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NRK + 2 * NRV + 2 * NF + 3 * NS + 2 + 8;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 64 + 1024;
-  static constexpr uint32_t COL_S = 0, COL_Q = 128, COL_O = 256;
+  static constexpr uint32_t COL_S = 0, COL_Q = 64 * NS, COL_O = 256;
+  static_assert(COL_Q + KH * (D / 2) <= COL_O, "tensor memory");
   static constexpr uint32_t ID_S = K8MMA  ? tc::idesc_e4m3(128, 64)
                                    : BF16 ? tc::idesc_bf16(128, 64, false, false)
                                           : tc::idesc_f16(128, 64, false, false);
@@ -172,6 +184,15 @@ __device__ __forceinline__ DiffWork diff_decode_work(const DiffTileArgs& a) {
   return w;
 }
 
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // True in one lane of a converged warp, always the same.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -216,8 +237,7 @@ template <int KK, int KV, int D, bool BOTH>
 __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     diff_tile_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, DiffTileArgs a) {
   using Cfg = DiffTileCfg<KK, KV, D, BOTH>;
-  constexpr int NK = Cfg::NK, NV = Cfg::NV, NRK = Cfg::NRK, NRV = Cfg::NRV, NF = Cfg::NF, KH = Cfg::KH;
-  constexpr int NCT = 32 * Cfg::NCONV;
+  constexpr int NK = Cfg::NK, NV = Cfg::NV, NRK = Cfg::NRK, NRV = Cfg::NRV, NF = Cfg::NF, KH = Cfg::KH, NS = Cfg::NS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem;
@@ -225,7 +245,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
   uint8_t* sRK = smem + Cfg::OFF_RK;
   uint8_t* sRV = Cfg::BF16 ? sV : smem + Cfg::OFF_RV;
   float* sF = reinterpret_cast<float*>(smem + Cfg::OFF_F);  // [NF][256]: K factors of 2 heads, V factors of 2 heads
-  float* sX = reinterpret_cast<float*>(smem + Cfg::OFF_X);
+  float2* sX = reinterpret_cast<float2*>(smem + Cfg::OFF_X);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);  // f16 K tiles ready (converters)
   uint64_t* k_empty = k_full + NK;                                      // their S done (MMA commit)
   uint64_t* v_full = k_empty + NK;                                      // f16 V tiles ready
@@ -236,12 +256,13 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
   uint64_t* rv_empty = rv_full + NRV;
   uint64_t* f_full = rv_empty + NRV;  // factors of a page written
   uint64_t* f_empty = f_full + NF;
-  uint64_t* s_full = f_empty + NF;  // [2]
-  uint64_t* p_full = s_full + 2;    // [2]
-  uint64_t* q_ready = p_full + 2;
+  uint64_t* s_full = f_empty + NF;  // [NS]
+  uint64_t* p_full = s_full + NS;   // [NS]
+  uint64_t* o_done = p_full + NS;   // [NS] PV of the page in S buffer i complete
+  uint64_t* q_ready = o_done + NS;
   uint64_t* drain = q_ready + 1;  // every MMA complete
-  uint64_t* x_full = drain + 1;   // [2][8] a softmax warp's maxima of a page are there
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(x_full + 16);
+  uint64_t* x_full = drain + 1;   // [2][4] the references of 32 rows after a page are there
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(x_full + 8);
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   griddep_wait();  // launched with programmatic stream serialization
@@ -255,34 +276,35 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
 
   if (tid == 0) {
     for (int i = 0; i < NK; ++i) {
-      mbar_init(&k_full[i], Cfg::NCONV);
+      mbar_init(&k_full[i], Cfg::CGW);
       mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < NV; ++i) {
-      mbar_init(&v_full[i], Cfg::NCONV);
+      mbar_init(&v_full[i], Cfg::CGW);
       mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < NRK; ++i) {
       mbar_init(&rk_full[i], 1);
-      // released by the converters; a raw operand by the MMA's commit, and where
-      // its scales are read (FP8-row) by both
-      mbar_init(&rk_empty[i], Cfg::BF16 ? 1 : Cfg::K8MMA ? 1 + Cfg::NCONV : Cfg::NCONV);
+      // released by the converters, a raw operand by the MMA's commit; and where key
+      // factors are read, by the warp that does
+      mbar_init(&rk_empty[i], (Cfg::K_RAW ? 1 : Cfg::CGW) + (Cfg::KEY_FAC ? 1 : 0));
     }
     for (int i = 0; i < NRV; ++i) {
       mbar_init(&rv_full[i], 1);
-      mbar_init(&rv_empty[i], Cfg::NCONV);
+      mbar_init(&rv_empty[i], Cfg::CGW + (Cfg::VAL_FAC ? 1 : 0));
     }
     for (int i = 0; i < NF; ++i) {
-      mbar_init(&f_full[i], Cfg::NCONV);
-      mbar_init(&f_empty[i], Cfg::NSOFT);
+      mbar_init(&f_full[i], Cfg::BF16 ? Cfg::NCONV : 1);
+      mbar_init(&f_empty[i], Cfg::NSOFT / 2);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NS; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], Cfg::NSOFT);
+      mbar_init(&p_full[i], Cfg::NSOFT / 2);
+      mbar_init(&o_done[i], 1);
     }
     mbar_init(q_ready, Cfg::NSOFT);
-    mbar_init(drain, 1);
-    for (int i = 0; i < 16; ++i) mbar_init(&x_full[i], 1);
+    mbar_init(drain, 2);
+    for (int i = 0; i < 8; ++i) mbar_init(&x_full[i], 1);
     fence_barrier_init();
     prefetch_tmap(&tmk);
     prefetch_tmap(&tmv);
@@ -297,7 +319,9 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
   const uint32_t tmem = *tslot;
   const auto wait = [&](uint64_t* bar, int use) { return mbar_wait_bounded(bar, use & 1, a.status); };
 
-  if (warp == Cfg::NSOFT) {
+  if (warp >= Cfg::NSOFT && warp < Cfg::NSOFT + 4) {
+   fewer_registers<Cfg::R_MISC>();
+   if (warp == Cfg::NSOFT) {
     // ------------- TMA producer: code and scale tiles of each page ---------------
     int gnext = 0, nk = 0, nv = 0;  // copies issued (lane 0)
     for (int j = 0; j < n; ++j) {
@@ -349,8 +373,103 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       for (int j = max(0, nk - NRK); j < nk; ++j) mbar_wait_bounded(&rk_full[j % NRK], (j / NRK) & 1, a.status);
       for (int j = max(0, nv - NRV); j < nv; ++j) mbar_wait_bounded(&rv_full[j % NRV], (j / NRV) & 1, a.status);
     }
-  } else if (warp > Cfg::NSOFT + 1) {
-    const int ct = tid - 32 * (Cfg::NSOFT + 2);
+  } else if (warp == Cfg::NSOFT + 3) {
+    // ------------- factors: per-key factors of the scores and of the weights -------------
+    if constexpr (Cfg::KEY_FAC || Cfg::VAL_FAC) {
+      bool ok = true;
+      for (int i = 0; i < n; ++i) {
+        const int rk = i % NRK, rv = i % NRV, fs = i % NF, kvalid = w.F - 64 * (w.p_lo + i);
+        float* slot = sF + fs * 256;
+        if constexpr (Cfg::KEY_FAC) ok = wait(&rk_full[rk], i / NRK);
+        if constexpr (Cfg::VAL_FAC) ok = ok && wait(&rv_full[rv], i / NRV);
+        if (ok && i >= NF) ok = wait(&f_empty[fs], i / NF - 1);
+        if (!ok) break;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = lane + 32 * (k & 1), h = k >> 1;
+          const bool in = key < kvalid;
+          if constexpr (Cfg::KEY_FAC)
+            if (h < KH)
+              slot[64 * h + key] =
+                  in ? key_factor<KK, D>(sRK + rk * Cfg::RK_STAGE + h * Cfg::RK_HEAD + Cfg::RK_CODES, key) * a.scale_log2 : 0.f;
+          if constexpr (Cfg::VAL_FAC)
+            slot[128 + 64 * h + key] =
+                in ? key_factor<KV, D>(sRV + rv * Cfg::RV_STAGE + h * Cfg::RV_HEAD + Cfg::RV_CODES, key) : 0.f;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          q_arrive(&f_full[fs]);
+          if constexpr (Cfg::KEY_FAC) q_arrive(&rk_empty[rk]);
+          if constexpr (Cfg::VAL_FAC) q_arrive(&rv_empty[rv]);
+        }
+      }
+    }
+  } else if (warp == Cfg::NSOFT + 1) {
+    // ------------------------------ MMA issuer: S ------------------------------
+    bool ok = wait(q_ready, 0);
+    for (int j = 0; j < n; ++j) {
+      const int ring = Cfg::K_RAW ? NRK : NK, ks = j % ring, sb = j % NS;
+      const uint32_t s_at = tmem + Cfg::COL_S + 64 * sb;
+      if (j >= NS) ok = ok && wait(&o_done[sb], j / NS - 1);  // P of the page before in this buffer was read
+      ok = ok && wait(Cfg::K_RAW ? &rk_full[ks] : &k_full[ks], j / ring);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc::fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int h = 0; h < KH; ++h) {
+          const uint32_t qa = tmem + Cfg::COL_Q + h * (D / 2);
+#pragma unroll
+          for (int part = 0; part < (Cfg::K_SPLIT || Cfg::K8MMA ? 2 : 1); ++part) {
+            const uint8_t* tile = Cfg::K_RAW ? sRK + ks * Cfg::RK_STAGE + h * Cfg::RK_HEAD
+                                             : sK + ks * Cfg::K_STAGE + h * Cfg::K_HEAD + part * Cfg::F16;
+            const uint64_t kd = tc::smem_desc(smem_u32(tile), 16, 1024);
+            if constexpr (Cfg::K8MMA) {  // q_hi, then q_lo, in D / 4 columns each
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk)
+                tc::mma_ts_f8(s_at, qa + part * (D / 4) + kk * 8,
+                              kd + static_cast<uint64_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), Cfg::ID_S,
+                              h > 0 || part > 0 || kk > 0);
+            } else {  // INT8-G64: Q k1^T - Q k2'^T
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc::mma_ts(s_at, qa + kk * 8, kd + static_cast<uint64_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
+                           part > 0 ? tc::idesc_negate_b(Cfg::ID_S) : Cfg::ID_S, h > 0 || part > 0 || kk > 0);
+            }
+          }
+        }
+        tc::commit(&s_full[sb]);
+        tc::commit(Cfg::K_RAW ? &rk_empty[ks] : &k_empty[ks]);
+      }
+      __syncwarp();
+    }
+    if (elect_one()) tc::commit(drain);  // arrives once every MMA issued above has completed
+  } else if (warp == Cfg::NSOFT + 2) {
+    // ------------------------------ MMA issuer: O += P V -----------------------
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const int vs = j % NV, sb = j % NS;
+      ok = ok && wait(&v_full[vs], j / NV) && wait(&p_full[sb], j / NS);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc::fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int v = 0; v < (Cfg::VAL_FAC ? 2 : 1); ++v) {
+          const uint64_t vd = tc::smem_desc(smem_u32(sV + vs * Cfg::V_STAGE + v * Cfg::F16), 8192, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc::mma_ts(tmem + Cfg::COL_O + v * D, tmem + Cfg::COL_S + 64 * sb + 32 * (kk >> 1) + 16 * v + 8 * (kk & 1),
+                       vd + static_cast<uint64_t>((kk * 2048) >> 4), Cfg::ID_O, (j > 0 || kk > 0));
+        }
+        tc::commit(&o_done[sb]);
+        tc::commit(&v_empty[vs]);
+      }
+      __syncwarp();
+    }
+    if (elect_one()) tc::commit(drain);
+   }
+  } else if (warp >= Cfg::NSOFT + 4) {
+    fewer_registers<Cfg::R_CONV>();
+    const int ct = tid - 32 * (Cfg::NSOFT + 4);
     bool ok = true;
     if constexpr (Cfg::BF16) {
       // ------------- converters of BF16 values: a strip of dims per warp -----------
@@ -427,135 +546,47 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
         }
       }
     } else {
-      // ------------- converters: K(0), K(1), V(0), K(2), V(1), ... -----------------
-      for (int i = 0; ok && i <= n; ++i) {
-        if (i < n) {  // K(i) and the factors of page i
-          const int rk = i % NRK, rv = i % NRV, fs = i % NF;
-          if constexpr (!Cfg::K_RAW || Cfg::HAS_F) {
-            ok = wait(&rk_full[rk], i / NRK);
-            if (!ok) break;
-          }
-          const uint8_t* raw = sRK + rk * Cfg::RK_STAGE;
-          const int kvalid = w.F - 64 * (w.p_lo + i);
-          const int key = ct & 63, what = ct >> 6;  // threads 0-127: K factors, 128-255: V factors
-          const bool live = key < kvalid;
-          float fac = 0.f;  // of the K scales, read before their slot can be released
-          if constexpr (Cfg::KEY_FAC)
-            if (what < KH && live) fac = key_factor<KK, D>(raw + what * Cfg::RK_HEAD + Cfg::RK_CODES, key) * a.scale_log2;
-          if constexpr (!Cfg::K_RAW) {
-            const int ks = i % NK;
-            if (i >= NK) ok = wait(&k_empty[ks], i / NK - 1);
-            if (!ok) break;
-#pragma unroll
-            for (int h = 0; h < KH; ++h)
-              convert_tile<KK, D, Cfg::K_RB, NCT, Cfg::K_SPLIT>(raw + h * Cfg::RK_HEAD, Cfg::RK_CODES,
-                                                               sK + ks * Cfg::K_STAGE + h * Cfg::K_HEAD, ct, kvalid);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-              q_arrive(&rk_empty[rk]);
-              q_arrive(&k_full[ks]);
-            }
-          }
-          if constexpr (Cfg::HAS_F) {
-            if constexpr (Cfg::VAL_FAC) ok = wait(&rv_full[rv], i / NRV);
-            if (ok && i >= NF) ok = wait(&f_empty[fs], i / NF - 1);
-            if (!ok) break;
-            if constexpr (Cfg::VAL_FAC)
-              if (what >= 2 && live)
-                fac = key_factor<KV, D>(sRV + rv * Cfg::RV_STAGE + (what - 2) * Cfg::RV_HEAD + Cfg::RV_CODES, key);
-            sF[fs * 256 + ct] = fac;
-            __syncwarp();
-            if (lane == 0) {
-              q_arrive(&f_full[fs]);
-              if constexpr (Cfg::K8MMA) q_arrive(&rk_empty[rk]);
-            }
-          }
-        }
-        if (i >= 1) {  // V(i - 1), both heads
-          const int jj = i - 1, rv = jj % NRV, vs = jj % NV;
-          ok = wait(&rv_full[rv], jj / NRV);
-          if (ok && jj >= NV) ok = wait(&v_empty[vs], jj / NV - 1);
+      // ------------- converters: K(i), V(i) of the group's pages i -------------------
+      constexpr int NCG = Cfg::NCG, NCT = 32 * Cfg::CGW;
+      const int cg = ct / NCT, gt = ct % NCT;
+      for (int i = cg; ok && i < n; i += NCG) {
+        const int kvalid = w.F - 64 * (w.p_lo + i);
+        if constexpr (!Cfg::K_RAW) {
+          const int rk = i % NRK, ks = i % NK;
+          ok = wait(&rk_full[rk], i / NRK);
+          if (ok && i >= NK) ok = wait(&k_empty[ks], i / NK - 1);
           if (!ok) break;
 #pragma unroll
-          for (int v = 0; v < 2; ++v)
-            convert_tile<KV, D, Cfg::V_RB, NCT>(sRV + rv * Cfg::RV_STAGE + v * Cfg::RV_HEAD, Cfg::RV_CODES,
-                                                sV + vs * Cfg::V_STAGE + v * Cfg::F16, ct, w.F - 64 * (w.p_lo + jj));
+          for (int h = 0; h < KH; ++h)
+            convert_tile<KK, D, Cfg::K_RB, NCT, Cfg::K_SPLIT>(sRK + rk * Cfg::RK_STAGE + h * Cfg::RK_HEAD, Cfg::RK_CODES,
+                                                             sK + ks * Cfg::K_STAGE + h * Cfg::K_HEAD, gt, kvalid);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            q_arrive(&rv_empty[rv]);
-            q_arrive(&v_full[vs]);
+            q_arrive(&rk_empty[rk]);
+            q_arrive(&k_full[ks]);
           }
+        }
+        const int rv = i % NRV, vs = i % NV;
+        ok = wait(&rv_full[rv], i / NRV);
+        if (ok && i >= NV) ok = wait(&v_empty[vs], i / NV - 1);
+        if (!ok) break;
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+          convert_tile<KV, D, Cfg::V_RB, NCT>(sRV + rv * Cfg::RV_STAGE + v * Cfg::RV_HEAD, Cfg::RV_CODES,
+                                              sV + vs * Cfg::V_STAGE + v * Cfg::F16, gt, kvalid);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          q_arrive(&rv_empty[rv]);
+          q_arrive(&v_full[vs]);
         }
       }
     }
-  } else if (warp == Cfg::NSOFT + 1) {
-    // ------------------------------ MMA issuer --------------------------------
-    bool ok = wait(q_ready, 0);
-    tc::fence_after();
-    for (int j = 0; j <= n; ++j) {
-      if (j < n) {  // S(j) into buffer j & 1
-        const uint32_t s_at = tmem + Cfg::COL_S + 64 * (j & 1);
-        const int ring = Cfg::K_RAW ? NRK : NK, ks = j % ring;
-        ok = ok && wait(Cfg::K_RAW ? &rk_full[ks] : &k_full[ks], j / ring);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc::fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int h = 0; h < KH; ++h) {
-            const uint32_t qa = tmem + Cfg::COL_Q + h * (D / 2);
-#pragma unroll
-            for (int part = 0; part < (Cfg::K_SPLIT || Cfg::K8MMA ? 2 : 1); ++part) {
-              const uint8_t* tile = Cfg::K_RAW ? sRK + ks * Cfg::RK_STAGE + h * Cfg::RK_HEAD
-                                               : sK + ks * Cfg::K_STAGE + h * Cfg::K_HEAD + part * Cfg::F16;
-              const uint64_t kd = tc::smem_desc(smem_u32(tile), 16, 1024);
-              if constexpr (Cfg::K8MMA) {  // q_hi, then q_lo, in D / 4 columns each
-#pragma unroll
-                for (int kk = 0; kk < D / 32; ++kk)
-                  tc::mma_ts_f8(s_at, qa + part * (D / 4) + kk * 8,
-                                kd + static_cast<uint64_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), Cfg::ID_S,
-                                h > 0 || part > 0 || kk > 0);
-              } else {  // INT8-G64: Q k1^T - Q k2'^T
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                  tc::mma_ts(s_at, qa + kk * 8, kd + static_cast<uint64_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
-                             part > 0 ? tc::idesc_negate_b(Cfg::ID_S) : Cfg::ID_S, h > 0 || part > 0 || kk > 0);
-              }
-            }
-          }
-          tc::commit(&s_full[j & 1]);
-          tc::commit(Cfg::K_RAW ? &rk_empty[ks] : &k_empty[ks]);
-        }
-        __syncwarp();
-      } else {  // as S(j) would: everything up to PV(j - 2) is complete
-        if (elect_one()) tc::commit(&s_full[j & 1]);
-        __syncwarp();
-      }
-      if (j >= 1) {  // O += P(j - 1) V(j - 1)
-        const int jj = j - 1, vs = jj % NV;
-        ok = ok && wait(&v_full[vs], jj / NV) && wait(&p_full[jj & 1], jj >> 1);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc::fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int v = 0; v < (Cfg::VAL_FAC ? 2 : 1); ++v) {
-            const uint64_t vd = tc::smem_desc(smem_u32(sV + vs * Cfg::V_STAGE + v * Cfg::F16), 8192, 1024);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_ts(tmem + Cfg::COL_O + v * D, tmem + Cfg::COL_S + 64 * (jj & 1) + 32 * (kk >> 1) + 16 * v + 8 * (kk & 1),
-                         vd + static_cast<uint64_t>((kk * 2048) >> 4), Cfg::ID_O, (jj > 0 || kk > 0));
-          }
-          tc::commit(&v_empty[vs]);
-        }
-        __syncwarp();
-      }
-    }
-    __syncwarp();
-    if (elect_one()) tc::commit(drain);  // arrives once every MMA issued above has completed
   } else {
     // ------------------------------ softmax warps -----------------------------
-    const int half = warp >> 2, m = tid & 127;  // query row = TMEM lane; keys [32 half, +32) of a page
+    more_registers<Cfg::R_SOFT>();
+    const int half = warp >> 2, quad32 = warp & 3, m = tid & 127;  // query row = TMEM lane; pages half, half + 2, ..
     const int map = BOTH ? m >> 6 : w.map, r = BOTH ? m & 63 : m;
     const int tl = r / a.G, g = r % a.G, token = w.t0 + tl;
     const bool valid = (BOTH || tl < a.TQ) && token < w.limit;
@@ -637,15 +668,13 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     // what turns a raw score into one in base 2: per key and row, or for all keys
     const float c_row = Cfg::KEY_FAC ? rs : fmaxf(a.scale_log2 * rs, 1.17549435e-38f);
     const F2 c2 = pack2(c_row, c_row);
-    float m_used = -INFINITY, l = 0.f;
-    int k_run = KV == KIND_FP8 ? kVLiftInit : 0;  // FP8-row V: the weights, l and O carry 2^k_run, one lift for both heads
-    const int mate = warp ^ 4;  // the warp of the rows' other keys
-    uint32_t sv[32], pk[Cfg::VAL_FAC ? 2 : 1][16];
-    float mu = 0.f, top = 0.f;
-    // This half's scores of the page, factors and mask applied; their maximum in top.
-    const auto scores = [&](uint32_t at, const float* ksc, int kmax) {
-      tc::ld32(at, sv);
-      tc::wait_ldn(sv);
+    // of this warp's pages: sum, and the reference and lift (FP8-row V) that it carries
+    constexpr int kLift0 = KV == KIND_FP8 ? kVLiftInit : 0;
+    float l = 0.f, m_own = -INFINITY;
+    int k_own = kLift0;
+    float mu = 0.f;
+    // Scores of 32 keys of the page: factors and mask.
+    const auto finish = [&](uint32_t (&sv)[32], const float* ksc, int kmax) {
       if constexpr (Cfg::KEY_FAC) {
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
@@ -663,8 +692,18 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
           if (c > kmax) sv[c] = 0xFF800000u;  // -inf
       }
     };
-    // The weights of sv under the reference mu into pk (sv is used up); returns their sum.
-    const auto weights = [&](const float* vsc) {
+    const auto top_of = [](const uint32_t (&sv)[32]) {
+      float t4[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) t4[u] = fmaxf(__uint_as_float(sv[u]), __uint_as_float(sv[4 + u]));
+#pragma unroll
+      for (int c = 8; c < 32; c += 8)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) t4[u] = max3(t4[u], __uint_as_float(sv[c + u]), __uint_as_float(sv[c + 4 + u]));
+      return fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+    };
+    // The weights of 32 scores under the reference mu, to P's columns; returns their sum.
+    const auto weights = [&](uint32_t (&sv)[32], const float* vsc, uint32_t p_at) {
       const F2 mu2 = pack2(-mu, -mu);
 #pragma unroll
       for (int c = 0; c < 32; c += 2) {
@@ -675,19 +714,21 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       }
 #pragma unroll
       for (int c = 0; c < 32; ++c) sv[c] = __float_as_uint(ex2(__uint_as_float(sv[c])));
+      uint32_t pk[16];
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        if constexpr (Cfg::VAL_FAC) {
+      for (int v = 0; v < (Cfg::VAL_FAC ? 2 : 1); ++v) {
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
+        for (int c = 0; c < 32; c += 2) {
+          if constexpr (Cfg::VAL_FAC) {
             const float2 f = *reinterpret_cast<const float2*>(vsc + 64 * v + c);
             float x, y;
             unpack2(mul2(pack2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), pack2(f.x, f.y)), x, y);
-            pk[v][c / 2] = pack_f16x2(x, y);
+            pk[c / 2] = pack_f16x2(x, y);
+          } else {
+            pk[c / 2] = pack_f16x2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
           }
-        } else {
-          pk[0][c / 2] = pack_f16x2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
         }
+        tc::st16(p_at + 16 * v, pk);
       }
       F2 sum2[4];
 #pragma unroll
@@ -700,75 +741,87 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       return s0 + s1;
     };
     bool live = true;
-    for (int j = 0; j < n; ++j) {
-      const int sb = j & 1, fs = j % NF;
-      const uint32_t s_at = quad + Cfg::COL_S + 64 * sb + 32 * half;
-      const float* ksc = sF + fs * 256 + (BOTH ? 64 * map : 0) + 32 * half;
-      const float* vsc = sF + fs * 256 + 128 + 32 * half;
-      const int kmax = (valid ? pos - 64 * (w.p_lo + j) : -1) - 32 * half;  // of this half's keys
+    const bool rows = __any_sync(0xffffffffu, valid);
+    if (!rows)  // rows past the last query: P is whatever the buffers hold, and their O is not stored
+      for (int j = half; live && j < n; j += 2) {
+        live = wait(&s_full[j % NS], j / NS);
+        if constexpr (Cfg::HAS_F) live = live && wait(&f_full[j % NF], j / NF);
+        tc::fence_after();
+        tc::fence_before();
+        if (lane == 0) {
+          q_arrive(&p_full[j % NS]);
+          if constexpr (Cfg::HAS_F) q_arrive(&f_empty[j % NF]);
+        }
+      }
+    for (int j = half; rows && j < n; j += 2) {
+      const int sb = j % NS, fs = j % NF;
+      const uint32_t s_at = quad + Cfg::COL_S + 64 * sb;
+      const float* ksc = sF + fs * 256 + (BOTH ? 64 * map : 0);
+      const float* vsc = sF + fs * 256 + 128;
+      const int kmax = valid ? pos - 64 * (w.p_lo + j) : -1;
       bool strips = false;  // BF16 values: a strip's k fell
-      int knew = k_run;
+      float most = 0.f;     // FP8-row V: the largest scale of the page
       if constexpr (Cfg::HAS_F) {
         live = live && wait(&f_full[fs], j / NF);
         if constexpr (Cfg::BF16) strips = *reinterpret_cast<const unsigned long long*>(sF + fs * 256) != 0ull;
         if constexpr (KV == KIND_FP8) {
           const float4 s4 = *reinterpret_cast<const float4*>(sF + fs * 256 + 128 + 4 * lane);  // both heads' 128 scales
-          knew = v_lift(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(s4.x, s4.y), fmaxf(s4.z, s4.w)))), k_run);
+          most = fmaxf(fmaxf(s4.x, s4.y), fmaxf(s4.z, s4.w));
         }
       }
-      live = live && wait(&s_full[sb], j >> 1);  // and PV(j - 2) is complete: in issue order
+      live = live && wait(&s_full[sb], j / NS);
       tc::fence_after();
-      scores(s_at, ksc, kmax);
-      float top4[4];
+      uint32_t sv[2][32];
+      tc::ld32(s_at, sv[0]);
+      tc::ld32(s_at + 32, sv[1]);
+      tc::wait_ldn(sv[0]);
+      tc::wait_ldn(sv[1]);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) top4[u] = fmaxf(__uint_as_float(sv[u]), __uint_as_float(sv[4 + u]));
-#pragma unroll
-      for (int c = 8; c < 32; c += 8)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) top4[u] = max3(top4[u], __uint_as_float(sv[c + u]), __uint_as_float(sv[c + 4 + u]));
-      top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
-      sX[sb * 256 + 128 * half + m] = top;
-      __syncwarp();
-      if (lane == 0) q_arrive(&x_full[8 * sb + warp]);
-      // under the old reference, before the other half's maximum is known
-      float sum = 0.f;
-      if (j > 0) sum = weights(vsc);
-      live = live && wait(&x_full[8 * sb + mate], j >> 1);
-      top = fmaxf(top, sX[sb * 256 + 128 * (half ^ 1) + m]);
+      for (int h = 0; h < 2; ++h) finish(sv[h], ksc + 32 * h, kmax - 32 * h);
+      const float top = fmaxf(top_of(sv[0]), top_of(sv[1]));
+      // the reference and lift after the page before, from the warp of the other pages
+      float m_was = -INFINITY;
+      int k_was = kLift0, k_now = kLift0;
+      if (j > 0) {
+        live = live && wait(&x_full[4 * ((j - 1) & 1) + quad32], (j - 1) >> 1);
+        const float2 x = sX[((j - 1) & 1) * 128 + m];
+        m_was = x.x;
+        if constexpr (KV == KIND_FP8) k_was = __float_as_int(x.y);
+      }
+      if constexpr (KV == KIND_FP8) k_now = v_lift(__reduce_max_sync(0xffffffffu, __float_as_uint(most)), k_was);
       const float rmax = top == -INFINITY ? -INFINITY : top * c_row;
       // lazy: the reference moves when a score passes it by more than 2^8, or the lift drops
-      float factor = 1.f;
-      const float mnew = fmaxf(m_used, rmax);
-      const bool resc =
-          mnew != -INFINITY && (m_used == -INFINITY || mnew > m_used + kLazyThr || knew != k_run);
-      if (j == 0 || __any_sync(0xffffffffu, resc || strips || knew != k_run)) {
-        if (resc) {
-          factor = m_used == -INFINITY ? 0.f : ex2((m_used - mnew) + static_cast<float>(knew - k_run));
-          m_used = mnew;
-        }
-        k_run = knew;
-        mu = m_used == -INFINITY ? 0.f : m_used - static_cast<float>(k_run);
-        if (j > 0) scores(s_at, ksc, kmax);  // S is still there: only this warp writes over it
-        sum = weights(vsc);
-        if (j >= 1) {  // O of this half's dims, once PV(j - 1) is complete: with S(j + 1)
-          live = live && wait(&s_full[sb ^ 1], (j + 1) >> 1);
-          tc::fence_after();
-#pragma unroll 1
-          for (int c0 = half * D; c0 < (half + 1) * D; c0 += 16) {
-            uint32_t ov[16];
-            tc::ld16(quad + Cfg::COL_O + c0, ov);
-            tc::wait_ld();
-            float fc = factor;
-            if constexpr (Cfg::BF16) fc *= sF[fs * 256 + 8 + c0 / Cfg::STRIP];
+      const float m_new = fmaxf(m_was, rmax);
+      const bool resc = m_new != -INFINITY && (m_was == -INFINITY || m_new > m_was + kLazyThr || k_now != k_was);
+      const float m_now = resc ? m_new : m_was;
+      sX[(j & 1) * 128 + m] = make_float2(m_now, __int_as_float(k_now));
+      __syncwarp();
+      if (lane == 0) q_arrive(&x_full[4 * (j & 1) + quad32]);
+      if (m_now != m_own || k_now != k_own) {
+        l *= m_own == -INFINITY ? 0.f : ex2((m_own - m_now) + static_cast<float>(k_now - k_own));
+        m_own = m_now;
+        k_own = k_now;
+      }
+      mu = m_now == -INFINITY ? 0.f : m_now - static_cast<float>(k_now);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * fc);
-            tc::st16(quad + Cfg::COL_O + c0, ov);
-          }
+      for (int h = 0; h < 2; ++h) l += weights(sv[h], vsc + 32 * h, s_at + 32 * h);
+      if (j >= 1 && __any_sync(0xffffffffu, resc || strips || k_now != k_was)) {
+        // O, once PV(j - 1) is complete
+        const float factor = !resc ? 1.f : m_was == -INFINITY ? 0.f : ex2((m_was - m_now) + static_cast<float>(k_now - k_was));
+        live = live && wait(&o_done[(j - 1) % NS], (j - 1) / NS);
+        tc::fence_after();
+#pragma unroll 1
+        for (int c0 = 0; c0 < 2 * D; c0 += 16) {
+          uint32_t ov[16];
+          tc::ld16(quad + Cfg::COL_O + c0, ov);
+          tc::wait_ld();
+          float fc = factor;
+          if constexpr (Cfg::BF16) fc *= sF[fs * 256 + 8 + c0 / Cfg::STRIP];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * fc);
+          tc::st16(quad + Cfg::COL_O + c0, ov);
         }
       }
-      l = l * factor + sum;
-#pragma unroll
-      for (int v = 0; v < (Cfg::VAL_FAC ? 2 : 1); ++v) tc::st16(s_at + 16 * v, pk[v]);
       tc::wait_st();
       tc::fence_before();
       __syncwarp();
@@ -780,14 +833,15 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     // ---- this CTA's partial: (m, l) of the row, and O, the half's D dims -------------
     live = live && wait(drain, 0);  // every PV
     tc::fence_after();
-    sX[(n & 1) * 256 + 128 * half + m] = l;
-    __syncwarp();
-    if (lane == 0) q_arrive(&x_full[8 * (n & 1) + warp]);
-    live = live && wait(&x_full[8 * (n & 1) + mate], n >> 1);
-    l += sX[(n & 1) * 256 + 128 * (half ^ 1) + m];
+    const float m_eff = m_own == -INFINITY ? -INFINITY : m_own - static_cast<float>(k_own);
+    sX[256 + 128 * half + m] = make_float2(m_eff, l);
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + quad32) : "memory");  // the two warps of these rows
+    if (live && valid && half == 0) {  // the sums, under the reference after the last page
+      const float2 last = sX[256 + 128 * (n > 0 ? (n - 1) & 1 : 0) + m], other = sX[256 + 128 * (n > 0 ? n & 1 : 1) + m];
+      const float f = other.x == -INFINITY ? 0.f : ex2(other.x - last.x);
+      a.ws_ml[w.part * 128 + m] = make_float2(last.x, fmaf(other.y, f, last.y));
+    }
     if (live) {
-      const float m_eff = m_used == -INFINITY ? -INFINITY : m_used - static_cast<float>(k_run);
-      if (valid && half == 0) a.ws_ml[w.part * 128 + m] = make_float2(m_eff, l);
       if (n > 0 && (!BOTH || __any_sync(0xffffffffu, valid))) {
         float* dst = a.ws_o + (w.part * 128 + m) * (2 * D);
 #pragma unroll 1
