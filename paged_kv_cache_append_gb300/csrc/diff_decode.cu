@@ -1,7 +1,7 @@
 // diff_decode.cu -- differential decode: the join of the splits, and the host side
 // (checks, plan, launches).
 #include "diff_decode.cuh"
-#include "diff_tile.cuh"
+#include "diff_join.cuh"
 
 namespace nk {
 
@@ -183,7 +183,7 @@ static int diff_plan(const nk_pool* p, int B, int T, int Hq, DiffPlan* pl) {
   }
   const int target = p->num_sms / (H / 2);
   pl->ctas = target > B ? target : B;
-  const size_t slots = static_cast<size_t>(H / 2) * pl->ctas * 2 * pl->RB;
+  const size_t slots = static_cast<size_t>(H / 2) * pl->ctas * 2 * pl->RB;  // query rows of all partials
   pl->ml_bytes = (slots * sizeof(float2) + 255) / 256 * 256;
   pl->bytes = pl->ml_bytes + slots * 2 * D * sizeof(float);
   return NK_OK;
@@ -209,9 +209,9 @@ extern "C" int nk_paged_diff_decode_attention(const void* q, int32_t Hq, const n
                                               const nk_diff* diff, void* out, float* lse, void* workspace,
                                               size_t workspace_bytes, void* stream) {
   clear_error();
-  DiffJoinArgs j;
+  DiffOut o;
   int rc = check_diff("nk_paged_diff_decode_attention", q, Hq, pool, layer, block_tables, table_rows, frontiers, B, T,
-                      softmax_scale, diff, out, lse, &j.o);
+                      softmax_scale, diff, out, lse, &o);
   if (rc) return rc;
   DiffPlan pl;
   if ((rc = diff_plan(pool, B, T, Hq, &pl))) return rc;
@@ -234,7 +234,13 @@ extern "C" int nk_paged_diff_decode_attention(const void* q, int32_t Hq, const n
     e = diff_tile_for(pool->desc.profile)(pool, layer, t, true, dim3(pl.ctas, t.H / 2), s);
   }
   if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
-  j = DiffJoinArgs{t.table_rows, t.lengths, t.ws_ml, t.ws_o, B, T, Hq, t.G, t.L, t.C, pl.ctas, pl.RB, j.o};
+  if (!pl.fn) {
+    const DiffTileJoinArgs tj{t.table_rows, t.lengths, nullptr, t.ws_ml, t.ws_o, B, T, Hq, t.H, t.G, t.L, t.C, 0, 1, 1, pl.ctas, o};
+    e = launch_diff_tile_join<true>(pool->desc.head_dim, tj, s);
+    if (e != cudaSuccess) return cuda_fail(e, "differential decode join launch");
+    return NK_OK;
+  }
+  const DiffJoinArgs j{t.table_rows, t.lengths, t.ws_ml, t.ws_o, B, T, Hq, t.G, t.L, t.C, pl.ctas, pl.RB, o};
   const dim3 grid(Hq / 2, B * T);
   e = pool->desc.head_dim == 64 ? launch_pdl(diff_join_kernel<64>, grid, dim3(512), 0, s, j)
                                 : launch_pdl(diff_join_kernel<128>, grid, dim3(512), 0, s, j);

@@ -60,20 +60,74 @@ struct DiffTileArgs {
   const int32_t* chunk_len;  // chunks
   const uint8_t* ks;         // scale planes of the layer (nullptr for BF16)
   const uint8_t* vs;
-  float2* ws_ml;  // [part][128] (m, l); chunks: part = (((b pairs + pair) tiles + qt) nsplit + split) 2 + map,
-  float* ws_o;    // [part][128][2 D];   decode: part = pair ctas + cta
+  float2* ws_ml;  // [part][128] (m, l)
+  float* ws_o;    // [part][D / 2][128][4]: neighbouring rows store next to each other
   int* status;
   float scale_log2;  // |softmax_scale| log2 e, > 0
   int negate;        // softmax_scale < 0: the queries change sign
   int B, T, Hq, H, G, L, M, C;
-  int TQ, tiles, nsplit;  // chunks
+  int TQ, tiles;          // chunks
   int ctas;               // decode: CTAs per pair
   int head_major;
 };
 
-// At least this many pages per range of a chunk's tile: shorter ones cost more in
-// start-up and partials than they win.
-constexpr int kDiffSplitPages = 4;
+// CTAs to a tile of a chunk: a pair, but for profiles whose halves of a value would be
+// less than the 64 dims of a swizzle atom.
+constexpr int diff_chunk_group(int kind_v, int D) { return (kind_v == KIND_FP8 || kind_v == KIND_INT8) && D == 64 ? 1 : 2; }
+
+// Chunks: the work of all tiles is one line, in order of (row b, pair, map, tile, page),
+// a tile's pages after kDiffTileCost units for its start and end (queries, first scores,
+// partial), and cluster c of n takes the units [c W / n, (c + 1) W / n): a tile that crosses
+// a boundary has a partial from each of its clusters, numbered tile + cluster.  n is at
+// most one CTA per SM and leaves each at least kDiffLeastUnits.
+constexpr int kDiffTileCost = 6, kDiffLeastUnits = 10;
+
+// Units of tiles [0, upto) of a row (a warp).
+__device__ __forceinline__ int64_t diff_tile_units(int prefix, int chunk, int TQ, int upto) {
+  int64_t sum = 0;
+  for (int t = threadIdx.x & 31; t < upto; t += 32) sum += (prefix + min((t + 1) * TQ, chunk) + 63) / 64 + kDiffTileCost;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  return sum;
+}
+
+// The rows of a call, as every CTA of the chunk kernel and of its join sees them.
+struct DiffChunkRows {
+  int row[8], prefix[8], chunk[8], tiles[8];
+  int64_t units[8];  // of one (pair, map)
+
+  // Warp b fills row b; a refused row has no tiles.
+  __device__ void fill(const int32_t* table_rows, const int32_t* prefix_len, const int32_t* chunk_len, int B, int T, int L,
+                       int C, int TQ, int warp, int* report) {
+    if (warp >= B) return;
+    const int rw = __ldcg(table_rows + warp), pre = __ldcg(prefix_len + warp);
+    int ch = __ldcg(chunk_len + warp);
+    if (rw < 0 || rw >= C || pre < 0 || ch < 0 || ch > T ||
+        static_cast<int64_t>(pre) + ch > static_cast<int64_t>(L) * 64) {
+      if (report && (threadIdx.x & 31) == 0) set_status(report, NK_STATUS_FRONTIER);
+      ch = 0;
+    }
+    const int n = (ch + TQ - 1) / TQ;
+    const int64_t sum = diff_tile_units(pre, ch, TQ, n);
+    if ((threadIdx.x & 31) == 0) {
+      row[warp] = rw;
+      prefix[warp] = pre;
+      chunk[warp] = ch;
+      tiles[warp] = n;
+      units[warp] = sum;
+    }
+  }
+  __device__ int64_t total(int B, int maps) const {
+    int64_t w = 0;
+    for (int b = 0; b < B; ++b) w += units[b] * maps;
+    return w;
+  }
+  __device__ int tile_pages(int b, int qt, int TQ) const { return (prefix[b] + min((qt + 1) * TQ, chunk[b]) + 63) / 64; }
+};
+
+__device__ __forceinline__ int diff_chunk_ctas(int64_t W, int most) {
+  return static_cast<int>(min(static_cast<int64_t>(most), max(W / kDiffLeastUnits, static_cast<int64_t>(1))));
+}
 
 template <int KK, int KV, int D, bool BOTH>
 struct DiffTileCfg {
@@ -81,7 +135,8 @@ struct DiffTileCfg {
   static constexpr int NSOFT = 8, NCONV = 8, THREADS = 32 * (NSOFT + 4 + NCONV);
   // Registers: 640 threads start with 96 each; the softmax warps (64 scores and 16 or 32
   // packed weights at a time) take over what the others do not need.
-  static constexpr int R_SOFT = BF16 ? 128 : 144, R_MISC = 40, R_CONV = BF16 ? 88 : 72;
+  static constexpr int R_SOFT = 136, R_MISC = 56, R_CONV = 72;
+  // (two CTAs of an SM would not fit: each takes all of the tensor memory)
   static_assert(256 * R_SOFT + 128 * R_MISC + 256 * R_CONV <= 640 * 96, "registers of the CTA");
   static constexpr int KCB = BF16 ? 2 * D : code_row_bytes<KK>(D), VCB = BF16 ? 2 * D : code_row_bytes<KV>(D);
   static constexpr int KSB = scale_row_bytes<KK>(D), VSB = scale_row_bytes<KV>(D);
@@ -94,19 +149,25 @@ struct DiffTileCfg {
   static constexpr bool VAL_FAC = KV == KIND_FP8 || KV == KIND_INT8;  // weights take one per key and head
   static constexpr bool HAS_F = KEY_FAC || VAL_FAC || BF16;
   static constexpr int KH = BOTH ? 2 : 1;  // K tiles of a page
+  static constexpr int CG = BOTH ? 1 : diff_chunk_group(KV, D);  // CTAs to an MMA
+  static constexpr int KR = 64 / CG;                             // keys of a K tile in this CTA
+  static constexpr int VH = CG == 2 && !VAL_FAC ? 1 : 2;         // value heads in this CTA
+  static constexpr bool V_HALF = CG == 2 && VAL_FAC;             // 64 of the 128 dims of both
+  static constexpr int VPART = V_HALF ? 64 * 64 * 2 : 64 * D * 2;  // f16 bytes of a value head here
   static constexpr int RK_CODES = (64 * KCB + 1023) / 1024 * 1024, RV_CODES = (64 * VCB + 1023) / 1024 * 1024;
   static constexpr int RK_HEAD = (RK_CODES + 64 * KSB + 1023) / 1024 * 1024, RK_STAGE = KH * RK_HEAD;
-  static constexpr int RV_HEAD = (RV_CODES + 64 * VSB + 1023) / 1024 * 1024, RV_STAGE = BF16 ? 0 : 2 * RV_HEAD;
+  static constexpr int RV_HEAD = (RV_CODES + 64 * VSB + 1023) / 1024 * 1024, RV_STAGE = BF16 ? 0 : VH * RV_HEAD;
   static constexpr int K_HEAD = K_SPLIT ? 2 * F16 : F16, K_STAGE = K_RAW ? 0 : KH * K_HEAD;
-  static constexpr int V_STAGE = 2 * F16;
+  static constexpr int V_STAGE = VH * VPART;
   // Groups of converter warps, on alternate pages; one where the f16 keys fit once
   // (INT8-G64 decode, head_dim 128), and for BF16, whose strips go from page to page.
   static constexpr int NCG = BF16 || (K_SPLIT && BOTH && D == 128) ? 1 : 2, CGW = NCONV / NCG;
   // Ring depths, as shared memory allows; a group's slots are its own.
-  static constexpr int NRK = D == 64 ? (BF16 && !BOTH ? 8 : 4) : BOTH ? (BF16 || (K8MMA && KV == KIND_NVFP4) ? 3 : K_SPLIT ? 2 : 4) : 4;
-  static constexpr int NK = K_RAW ? 1 : D == 64 ? (K_SPLIT && BOTH ? 2 : 4) : K_SPLIT && BOTH ? 1 : 2;
-  static constexpr int NV = D == 64 ? 4 : BF16 ? (BOTH ? 3 : 4) : K_SPLIT || (BOTH && KV != KIND_NVFP4) || (BOTH && !K_RAW) ? 2 : 4;
-  static constexpr int NRV = BF16 ? NV : D == 64 ? 4 : BOTH && !K_SPLIT && !(K8MMA && KV == KIND_NVFP4) ? 4 : 2;
+  static constexpr int NRK = CG == 2 ? (K_SPLIT ? 4 : 6)
+                           : D == 64 ? 4 : BF16 || (K8MMA && KV == KIND_NVFP4) ? 3 : K_SPLIT ? 2 : 4;
+  static constexpr int NK = K_RAW ? 1 : CG == 2 ? (K_SPLIT ? 2 : 4) : D == 64 ? (K_SPLIT && BOTH ? 2 : 4) : K_SPLIT ? 1 : 2;
+  static constexpr int NV = CG == 2 ? (BF16 ? 6 : K_SPLIT ? 2 : 4) : D == 64 ? 4 : BF16 ? 3 : K8MMA && KV == KIND_NVFP4 ? 4 : 2;
+  static constexpr int NRV = BF16 ? NV : CG == 2 ? (K_SPLIT ? 2 : 4) : D == 64 ? 4 : K_SPLIT || (K8MMA && KV == KIND_NVFP4) ? 2 : 4;
   static_assert(NCG == 1 || (NV % 2 == 0 && NRV % 2 == 0 && (K_RAW || (NK % 2 == 0 && NRK % 2 == 0))), "a group's slots");
   static constexpr int NF = 4;  // factor ring: 1 KB per page
   static constexpr int OFF_V = NK * K_STAGE;
@@ -115,75 +176,134 @@ struct DiffTileCfg {
   static constexpr int OFF_F = OFF_RV + NRV * RV_STAGE;
   static constexpr int NS = BOTH && D == 128 ? 2 : 3;  // S buffers
   static constexpr int OFF_X = OFF_F + NF * 1024;  // [2][128] references, [2][128] final (reference, sum)
-  static constexpr int OFF_BAR = OFF_X + 4096;
-  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NRK + 2 * NRV + 2 * NF + 3 * NS + 2 + 8;
+  static constexpr int OFF_ROWS = OFF_X + 4096 + 256;  // [4][16] lifts of the BF16 strips
+  static constexpr int OFF_BAR = OFF_ROWS + 256;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NRK + 2 * NRV + 2 * NF + 4 * NS + 3 + 8 + (K_RAW ? NRK : NK);
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 64 + 1024;
   static constexpr uint32_t COL_S = 0, COL_Q = 64 * NS, COL_O = 256;
   static_assert(COL_Q + KH * (D / 2) <= COL_O, "tensor memory");
-  static constexpr uint32_t ID_S = K8MMA  ? tc::idesc_e4m3(128, 64)
-                                   : BF16 ? tc::idesc_bf16(128, 64, false, false)
-                                          : tc::idesc_f16(128, 64, false, false);
-  static constexpr uint32_t ID_O = tc::idesc_f16(128, VAL_FAC ? D : 2 * D, false, true);
-  static constexpr int STRIP = 2 * D / NCONV;  // dims that a converter warp of BF16 values owns
+  static constexpr uint32_t ID_S = K8MMA  ? tc::idesc_e4m3(128 * CG, 64)
+                                   : BF16 ? tc::idesc_bf16(128 * CG, 64, false, false)
+                                          : tc::idesc_f16(128 * CG, 64, false, false);
+  static constexpr uint32_t ID_O = tc::idesc_f16(128 * CG, VAL_FAC ? D : 2 * D, false, true);
+  static constexpr int STRIPS = NCONV * CG, STRIP = 2 * D / STRIPS;  // a converter warp of BF16 values owns a strip of dims
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
-  static_assert(SMEM > 114 * 1024, "one CTA per SM: each takes all of the tensor memory");
 };
 
-// What a CTA works on; n < 0: nothing.
+// What a CTA works on: pages [p_lo, p_lo + n) of one tile (n < 0: nothing).
 struct DiffWork {
-  int b, pair, map, row, F, t0, limit, pos0, p_lo, n;
-  int64_t part;
+  int b, pm, qt, p_lo, n;  // pm = 2 pair + map
+  int left;                // units of this cluster beyond these (the host bounds them)
 };
 
-// Chunks: later tiles see more keys and are launched first; the two maps of a
-// tile are neighbours.
-__device__ __forceinline__ DiffWork diff_chunk_work(const DiffTileArgs& a) {
+// The pages of tile w.qt from its unit `u` on, as far as w.left goes.
+__device__ __forceinline__ void diff_take(const DiffChunkRows& rows, int TQ, int u, DiffWork& w) {
+  const int pages = rows.tile_pages(w.b, w.qt, TQ), take = min(pages + kDiffTileCost - u, w.left);
+  w.p_lo = max(u - kDiffTileCost, 0);
+  w.n = max(u + take - kDiffTileCost, 0) - w.p_lo;
+  w.left -= take;
+}
+
+// The next piece with pages; TQ: tokens of a tile (of a cluster).
+__device__ __forceinline__ bool diff_chunk_next(const DiffChunkRows& rows, int maps, int TQ, DiffWork& w) {
+  do {
+    if (w.left == 0) return false;
+    if (++w.qt >= rows.tiles[w.b]) {
+      w.qt = 0;
+      if (++w.pm >= maps) {
+        w.pm = 0;
+        do ++w.b;
+        while (rows.tiles[w.b] == 0);  // units are left: a row with tiles follows
+      }
+    }
+    diff_take(rows, TQ, 0, w);
+  } while (w.n == 0);
+  return true;
+}
+
+// The first piece of cluster c of (at most) `most`; every warp computes it.
+__device__ __forceinline__ DiffWork diff_chunk_first(const DiffChunkRows& rows, int B, int maps, int TQ, int c, int most) {
   DiffWork w;
-  w.map = blockIdx.x & 1;
-  const int x = blockIdx.x >> 1, split = x % a.nsplit, qt = a.tiles - 1 - x / a.nsplit;
-  w.pair = blockIdx.y;
-  w.b = blockIdx.z;
-  w.row = a.table_rows[w.b];
-  const int prefix = a.lengths[w.b], chunk = a.chunk_len[w.b];
   w.n = -1;
-  if (w.row < 0 || w.row >= a.C || prefix < 0 || chunk < 0 || chunk > a.T ||
-      static_cast<int64_t>(prefix) + chunk > static_cast<int64_t>(a.L) * 64) {
-    if (threadIdx.x == 0 && blockIdx.x == 0 && w.pair == 0) set_status(a.status, NK_STATUS_FRONTIER);
-    return w;
+  const int lane = threadIdx.x & 31;
+  const int64_t W = rows.total(B, maps);
+  const int n = diff_chunk_ctas(W, most);
+  if (W == 0 || c >= n) return w;
+  int64_t at = c * W / n;
+  w.left = static_cast<int>((c + 1) * W / n - at);
+  w.b = 0;
+  while (at >= rows.units[w.b] * maps) at -= rows.units[w.b++] * maps;
+  w.pm = static_cast<int>(at / rows.units[w.b]);
+  at -= w.pm * rows.units[w.b];
+  for (w.qt = 0;; w.qt += 32) {  // the tile that holds unit `at`, 32 tiles at a time
+    const int mine = w.qt + lane < rows.tiles[w.b] ? rows.tile_pages(w.b, w.qt + lane, TQ) + kDiffTileCost : 0;
+    int64_t end = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, end, off);
+      if (lane >= off) end += x;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, at < end);
+    if (past) {
+      const int k = __ffs(past) - 1;
+      w.qt += k;
+      at -= __shfl_sync(0xffffffffu, end - mine, k);
+      break;
+    }
+    at -= __shfl_sync(0xffffffffu, end, 31);
   }
-  w.t0 = qt * a.TQ;
-  if (w.t0 >= chunk) return w;
-  w.limit = chunk;
-  w.F = prefix + chunk;
-  w.pos0 = prefix;
-  const int pages = (prefix + min(w.t0 + a.TQ, chunk) - 1 + 64) / 64;
-  const int per = max((pages + a.nsplit - 1) / a.nsplit, kDiffSplitPages);
-  w.p_lo = min(split * per, pages);
-  w.n = min(w.p_lo + per, pages) - w.p_lo;
-  w.part = (((static_cast<int64_t>(w.b) * (a.H / 2) + w.pair) * a.tiles + qt) * a.nsplit + split) * 2 + w.map;
+  diff_take(rows, TQ, static_cast<int>(at), w);
+  if (w.n == 0 && !diff_chunk_next(rows, maps, TQ, w)) w.n = -1;
   return w;
 }
 
-// Decode: the CTA's split of the plan of all rows.
-__device__ __forceinline__ DiffWork diff_decode_work(const DiffTileArgs& a) {
+// Decode: the CTA's split of the plan of all rows; the row as a chunk of T tokens
+// after F - T.
+__device__ __forceinline__ DiffWork diff_decode_work(const DiffTileArgs& a, DiffChunkRows* rows) {
   DiffWork w;
-  w.pair = blockIdx.y;
-  w.map = 0;
   const DiffSplit own = diff_split(diff_rows(a.lengths, a.table_rows, a.B, a.L, a.C, a.ctas,
-                                             blockIdx.x == 0 && w.pair == 0 && threadIdx.x < 32 ? a.status : nullptr),
+                                             blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32 ? a.status : nullptr),
                                    a.B, blockIdx.x);
   w.b = own.b;
-  w.row = own.row;
-  w.F = own.F;
-  w.t0 = 0;
-  w.limit = a.T;
-  w.pos0 = w.F - a.T;
+  w.pm = 2 * blockIdx.y;
+  w.qt = 0;
   w.p_lo = own.p0;
-  w.n = own.b < 0 ? -1 : own.n;
-  w.part = static_cast<int64_t>(w.pair) * a.ctas + blockIdx.x;
+  w.n = own.b < 0 ? -1 : own.n;  // 0 only for a row without keys
+  w.left = 0;
+  if (threadIdx.x == 0 && own.b >= 0) {
+    rows->row[own.b] = own.row;
+    rows->prefix[own.b] = own.F - a.T;
+    rows->chunk[own.b] = a.T;
+  }
   return w;
 }
 
+// ---- the other CTA of a pair ----------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t peer_u32(const void* p, uint32_t rank) {  // p's place in CTA `rank`
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+// What such an arrival announces lies in tensor memory, or in shared memory behind a proxy
+// fence, for the tensor core: no release at cluster scope, which cost 1500 cycles a page.
+__device__ __forceinline__ void peer_arrive(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(peer_u32(bar, rank)) : "memory");
+}
+// 16 bytes to p's place in CTA `rank`, counted by the barrier at bar's place there.
+__device__ __forceinline__ void peer_store(float4* p, float4 v, uint64_t* bar, uint32_t rank) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                   peer_u32(p, rank)),
+               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(peer_u32(bar, rank))
+               : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
 template <int N>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -220,10 +340,10 @@ __device__ __forceinline__ uint32_t f16x2_of(uint32_t rebiased, uint32_t w) {
 
 // Converter warps of BF16 values: warp cw rewrites its strip of every staged V
 // tile, bf16 -> f16 of v 2^k in place, and publishes what its k did.
-template <int D>
+template <int STRIP>
 struct StripOf {
-  static constexpr int CH = 2 * D / 8 / 8;   // 16-byte chunks of the strip in a key's row
-  static constexpr int ROWS = 32 / CH;       // keys that a warp access covers
+  static constexpr int CH = STRIP / 8;  // 16-byte chunks of the strip in a key's row
+  static constexpr int ROWS = 32 / CH;  // keys that a warp access covers
   static constexpr int UNITS = 64 / ROWS;
 };
 
@@ -246,6 +366,9 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
   uint8_t* sRV = Cfg::BF16 ? sV : smem + Cfg::OFF_RV;
   float* sF = reinterpret_cast<float*>(smem + Cfg::OFF_F);  // [NF][256]: K factors of 2 heads, V factors of 2 heads
   float2* sX = reinterpret_cast<float2*>(smem + Cfg::OFF_X);
+  float* sDown = reinterpret_cast<float*>(smem + Cfg::OFF_X + 4096);
+  DiffChunkRows* rows = reinterpret_cast<DiffChunkRows*>(smem + Cfg::OFF_ROWS);
+  static_assert(sizeof(DiffChunkRows) <= 256, "rows");
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);  // f16 K tiles ready (converters)
   uint64_t* k_empty = k_full + NK;                                      // their S done (MMA commit)
   uint64_t* v_full = k_empty + NK;                                      // f16 V tiles ready
@@ -261,18 +384,27 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
   uint64_t* o_done = p_full + NS;   // [NS] PV of the page in S buffer i complete
   uint64_t* q_ready = o_done + NS;
   uint64_t* drain = q_ready + 1;  // every MMA complete
-  uint64_t* x_full = drain + 1;   // [2][4] the references of 32 rows after a page are there
+  uint64_t* o_free = drain + 1;   // O of a piece was read
+  uint64_t* peer_v = o_free + 1;  // [NS] of CTA 0: CTA 1 is ready for PV
+  uint64_t* peer_k = peer_v + NS;  // [ring] and for S
+  uint64_t* x_full = peer_k + (Cfg::K_RAW ? NRK : NK);  // [2][4] the references of 32 rows after a page are there
   uint32_t* tslot = reinterpret_cast<uint32_t*>(x_full + 8);
 
+  constexpr int CG = Cfg::CG;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;  // this CTA's in its pair
+  const int TQ = a.TQ * CG;                                         // tokens of a tile
   griddep_wait();  // launched with programmatic stream serialization
   griddep_launch_dependents();
-  DiffWork w;
-  if constexpr (BOTH) w = diff_decode_work(a);
-  else w = diff_chunk_work(a);
-  const int n = w.n;
-  if (n < 0) return;
-  const int32_t* table = a.tables + static_cast<int64_t>(w.row) * a.L + w.p_lo;
+  DiffWork first;
+  if constexpr (BOTH) {
+    first = diff_decode_work(a, rows);
+  } else {
+    rows->fill(a.table_rows, a.lengths, a.chunk_len, a.B, a.T, a.L, a.C, TQ, warp, blockIdx.x == 0 ? a.status : nullptr);
+    __syncthreads();
+    first = diff_chunk_first(*rows, a.B, a.H, TQ, blockIdx.x / CG, gridDim.x / CG);
+  }
+  if (first.n < 0) return;  // a pair's CTAs alike
 
   if (tid == 0) {
     for (int i = 0; i < NK; ++i) {
@@ -295,28 +427,54 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     }
     for (int i = 0; i < NF; ++i) {
       mbar_init(&f_full[i], Cfg::BF16 ? Cfg::NCONV : 1);
-      mbar_init(&f_empty[i], Cfg::NSOFT / 2);
+      mbar_init(&f_empty[i], Cfg::NSOFT / 2 * (Cfg::BF16 ? CG : 1));
     }
     for (int i = 0; i < NS; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], Cfg::NSOFT / 2);
       mbar_init(&o_done[i], 1);
+      mbar_init(&peer_v[i], 1);
     }
     mbar_init(q_ready, Cfg::NSOFT);
+    for (int i = 0; i < (Cfg::K_RAW ? NRK : NK); ++i) mbar_init(&peer_k[i], 1);
     mbar_init(drain, 2);
+    mbar_init(o_free, Cfg::NSOFT);
     for (int i = 0; i < 8; ++i) mbar_init(&x_full[i], 1);
     fence_barrier_init();
     prefetch_tmap(&tmk);
     prefetch_tmap(&tmv);
   }
   if (warp == 0) {
-    tc::alloc(tslot, 512);
-    tc::relinquish();
+    if constexpr (CG == 2) {
+      tc::alloc2(tslot, 512);
+      tc::relinquish2();
+    } else {
+      tc::alloc(tslot, 512);
+      tc::relinquish();
+    }
   }
   tc::fence_before();
   __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // the other CTA's barriers exist
   tc::fence_after();
   const uint32_t tmem = *tslot;
+  // Every role goes through the CTA's pieces; `base` counts the pages of those before.
+  const auto next = [&](DiffWork& w, int& base) {
+    base += w.n;
+    return !BOTH && diff_chunk_next(*rows, a.H, TQ, w);
+  };
+  const auto mma = [](uint32_t d, uint32_t am, uint64_t bd, uint32_t id, uint32_t acc) {
+    if constexpr (CG == 2) tc::mma_ts2(d, am, bd, id, acc);
+    else tc::mma_ts(d, am, bd, id, acc);
+  };
+  const auto mma_f8 = [](uint32_t d, uint32_t am, uint64_t bd, uint32_t id, uint32_t acc) {
+    if constexpr (CG == 2) tc::mma_ts2_f8(d, am, bd, id, acc);
+    else tc::mma_ts_f8(d, am, bd, id, acc);
+  };
+  const auto commit = [](uint64_t* bar) {  // in both CTAs
+    if constexpr (CG == 2) tc::commit2(bar);
+    else tc::commit(bar);
+  };
   const auto wait = [&](uint64_t* bar, int use) { return mbar_wait_bounded(bar, use & 1, a.status); };
 
   if (warp >= Cfg::NSOFT && warp < Cfg::NSOFT + 4) {
@@ -324,28 +482,33 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
    if (warp == Cfg::NSOFT) {
     // ------------- TMA producer: code and scale tiles of each page ---------------
     int gnext = 0, nk = 0, nv = 0;  // copies issued (lane 0)
-    for (int j = 0; j < n; ++j) {
-      if ((j & 31) == 0) gnext = (j + lane < n) ? table[j + lane] : 0;
-      int g = __shfl_sync(0xffffffffu, gnext, j & 31);
-      int stop = 0;
+    DiffWork w = first;
+    int base = 0, stop = 0;
+    do {
+     const int32_t* table = a.tables + static_cast<int64_t>(rows->row[w.b]) * a.L + w.p_lo;
+     const int pair = w.pm >> 1;
+     for (int i = 0; i < w.n; ++i) {
+      const int j = base + i;
+      if ((i & 31) == 0) gnext = (i + lane < w.n) ? table[i + lane] : 0;
+      int g = __shfl_sync(0xffffffffu, gnext, i & 31);
       if (lane == 0) {
         if (g < 0 || g >= a.M) {  // never copy from outside the pool
           set_status(a.status, NK_STATUS_PAGE_RANGE);
           g = 0;
         }
-        const int y[2] = {static_cast<int>(tile_row(g, 2 * w.pair, a.H, a.M, a.head_major)),
-                          static_cast<int>(tile_row(g, 2 * w.pair + 1, a.H, a.M, a.head_major))};
+        const int y[2] = {static_cast<int>(tile_row(g, 2 * pair, a.H, a.M, a.head_major)),
+                          static_cast<int>(tile_row(g, 2 * pair + 1, a.H, a.M, a.head_major))};
         const int rk = j % NRK, rv = j % NRV;
         if (j >= NRK && !wait(&rk_empty[rk], j / NRK - 1)) stop = 1;
         if (!stop) {
-          mbar_arrive_expect_tx(&rk_full[rk], KH * (64 * Cfg::KCB + 64 * Cfg::KSB));
+          mbar_arrive_expect_tx(&rk_full[rk], KH * (Cfg::KR * Cfg::KCB + 64 * Cfg::KSB));
 #pragma unroll
-          for (int i = 0; i < KH; ++i) {
-            uint8_t* st = sRK + rk * Cfg::RK_STAGE + i * Cfg::RK_HEAD;
-            const int yk = BOTH ? y[i] : y[w.map];
+          for (int h = 0; h < KH; ++h) {
+            uint8_t* st = sRK + rk * Cfg::RK_STAGE + h * Cfg::RK_HEAD;
+            const int yk = y[BOTH ? h : w.pm & 1];
 #pragma unroll
             for (int c = 0; c < Cfg::KCB / Cfg::K_RB; ++c)
-              tma_load_2d(st + c * 64 * Cfg::K_RB, &tmk, c * Cfg::K_RB, yk, &rk_full[rk]);
+              tma_load_2d(st + c * 64 * Cfg::K_RB, &tmk, c * Cfg::K_RB, yk + Cfg::KR * rank, &rk_full[rk]);
             if constexpr (Cfg::KSB > 0)
               bulk_load(st + Cfg::RK_CODES, a.ks + static_cast<int64_t>(yk) * Cfg::KSB, 64 * Cfg::KSB, &rk_full[rk]);
           }
@@ -354,21 +517,24 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
         // BF16 values land where the MMA reads them: their slot is free once it has
         if (!stop && j >= NRV && !wait(Cfg::BF16 ? &v_empty[rv] : &rv_empty[rv], j / NRV - 1)) stop = 1;
         if (!stop) {
-          mbar_arrive_expect_tx(&rv_full[rv], 2 * (64 * Cfg::VCB + 64 * Cfg::VSB));
+          mbar_arrive_expect_tx(&rv_full[rv], Cfg::VH * (64 * Cfg::VCB + 64 * Cfg::VSB));
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
+          for (int v = 0; v < Cfg::VH; ++v) {
             uint8_t* st = Cfg::BF16 ? sV + rv * Cfg::V_STAGE + v * Cfg::F16 : sRV + rv * Cfg::RV_STAGE + v * Cfg::RV_HEAD;
+            const int yv = y[Cfg::VH == 2 ? v : rank];
 #pragma unroll
             for (int c = 0; c < Cfg::VCB / Cfg::V_RB; ++c)
-              tma_load_2d(st + c * 64 * Cfg::V_RB, &tmv, c * Cfg::V_RB, y[v], &rv_full[rv]);
+              tma_load_2d(st + c * 64 * Cfg::V_RB, &tmv, c * Cfg::V_RB, yv, &rv_full[rv]);
             if constexpr (Cfg::VSB > 0)
-              bulk_load(st + Cfg::RV_CODES, a.vs + static_cast<int64_t>(y[v]) * Cfg::VSB, 64 * Cfg::VSB, &rv_full[rv]);
+              bulk_load(st + Cfg::RV_CODES, a.vs + static_cast<int64_t>(yv) * Cfg::VSB, 64 * Cfg::VSB, &rv_full[rv]);
           }
           ++nv;
         }
       }
-      if (__shfl_sync(0xffffffffu, stop, 0)) break;
-    }
+      stop = __shfl_sync(0xffffffffu, stop, 0);
+      if (stop) break;
+     }
+    } while (!stop && next(w, base));
     if (lane == 0) {  // every copy lands before the CTA may leave
       for (int j = max(0, nk - NRK); j < nk; ++j) mbar_wait_bounded(&rk_full[j % NRK], (j / NRK) & 1, a.status);
       for (int j = max(0, nv - NRV); j < nv; ++j) mbar_wait_bounded(&rv_full[j % NRV], (j / NRV) & 1, a.status);
@@ -377,8 +543,12 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     // ------------- factors: per-key factors of the scores and of the weights -------------
     if constexpr (Cfg::KEY_FAC || Cfg::VAL_FAC) {
       bool ok = true;
-      for (int i = 0; i < n; ++i) {
-        const int rk = i % NRK, rv = i % NRV, fs = i % NF, kvalid = w.F - 64 * (w.p_lo + i);
+      DiffWork w = first;
+      int base = 0;
+      do {
+       const int F = rows->prefix[w.b] + rows->chunk[w.b];
+       for (int i = base; i < base + w.n; ++i) {
+        const int rk = i % NRK, rv = i % NRV, fs = i % NF, kvalid = F - 64 * (w.p_lo + i - base);
         float* slot = sF + fs * 256;
         if constexpr (Cfg::KEY_FAC) ok = wait(&rk_full[rk], i / NRK);
         if constexpr (Cfg::VAL_FAC) ok = ok && wait(&rv_full[rv], i / NRV);
@@ -402,19 +572,28 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
           if constexpr (Cfg::KEY_FAC) q_arrive(&rk_empty[rk]);
           if constexpr (Cfg::VAL_FAC) q_arrive(&rv_empty[rv]);
         }
-      }
+       }
+      } while (ok && next(w, base));
     }
   } else if (warp == Cfg::NSOFT + 1) {
     // ------------------------------ MMA issuer: S ------------------------------
-    bool ok = wait(q_ready, 0);
-    for (int j = 0; j < n; ++j) {
+    bool ok = true;
+    DiffWork w = first;
+    int base = 0, piece = 0;
+    do {
+     ok = ok && wait(q_ready, piece++);
+     for (int j = base; j < base + w.n; ++j) {
       const int ring = Cfg::K_RAW ? NRK : NK, ks = j % ring, sb = j % NS;
       const uint32_t s_at = tmem + Cfg::COL_S + 64 * sb;
-      if (j >= NS) ok = ok && wait(&o_done[sb], j / NS - 1);  // P of the page before in this buffer was read
+      if (j >= NS && rank == 0) ok = ok && wait(&o_done[sb], j / NS - 1);  // P of the page before in this buffer was read
       ok = ok && wait(Cfg::K_RAW ? &rk_full[ks] : &k_full[ks], j / ring);
+      if (CG == 2 && rank == 0) ok = ok && wait(&peer_k[ks], j / ring);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::fence_after();
-      if (elect_one()) {
+      if (rank != 0) {  // CTA 0 issues for both
+        tc::fence_before();
+        if (lane == 0) peer_arrive(&peer_k[ks], 0);
+      } else if (elect_one()) {
 #pragma unroll
         for (int h = 0; h < KH; ++h) {
           const uint32_t qa = tmem + Cfg::COL_Q + h * (D / 2);
@@ -426,46 +605,58 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
             if constexpr (Cfg::K8MMA) {  // q_hi, then q_lo, in D / 4 columns each
 #pragma unroll
               for (int kk = 0; kk < D / 32; ++kk)
-                tc::mma_ts_f8(s_at, qa + part * (D / 4) + kk * 8,
+                mma_f8(s_at, qa + part * (D / 4) + kk * 8,
                               kd + static_cast<uint64_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), Cfg::ID_S,
                               h > 0 || part > 0 || kk > 0);
             } else {  // INT8-G64: Q k1^T - Q k2'^T
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk)
-                tc::mma_ts(s_at, qa + kk * 8, kd + static_cast<uint64_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
+                mma(s_at, qa + kk * 8, kd + static_cast<uint64_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
                            part > 0 ? tc::idesc_negate_b(Cfg::ID_S) : Cfg::ID_S, h > 0 || part > 0 || kk > 0);
             }
           }
         }
-        tc::commit(&s_full[sb]);
-        tc::commit(Cfg::K_RAW ? &rk_empty[ks] : &k_empty[ks]);
+        commit(&s_full[sb]);
+        commit(Cfg::K_RAW ? &rk_empty[ks] : &k_empty[ks]);
       }
       __syncwarp();
-    }
-    if (elect_one()) tc::commit(drain);  // arrives once every MMA issued above has completed
+     }
+    } while (__all_sync(0xffffffffu, ok) && next(w, base));
+    __syncwarp();
+    if (rank == 0 && elect_one()) commit(drain);  // arrives once every MMA issued above has completed
   } else if (warp == Cfg::NSOFT + 2) {
     // ------------------------------ MMA issuer: O += P V -----------------------
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
+    DiffWork w = first;
+    int base = 0, piece = 0;
+    do {
+     if (piece++ > 0) ok = ok && wait(o_free, piece - 2);  // the piece before is stored
+     for (int j = base; j < base + w.n; ++j) {
       const int vs = j % NV, sb = j % NS;
       ok = ok && wait(&v_full[vs], j / NV) && wait(&p_full[sb], j / NS);
+      if (CG == 2 && rank == 0) ok = ok && wait(&peer_v[sb], j / NS);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::fence_after();
-      if (elect_one()) {
+      if (rank != 0) {
+        tc::fence_before();
+        if (lane == 0) peer_arrive(&peer_v[sb], 0);
+      } else if (elect_one()) {
 #pragma unroll
         for (int v = 0; v < (Cfg::VAL_FAC ? 2 : 1); ++v) {
-          const uint64_t vd = tc::smem_desc(smem_u32(sV + vs * Cfg::V_STAGE + v * Cfg::F16), 8192, 1024);
+          const uint64_t vd = tc::smem_desc(smem_u32(sV + vs * Cfg::V_STAGE + v * Cfg::VPART), 8192, 1024);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc::mma_ts(tmem + Cfg::COL_O + v * D, tmem + Cfg::COL_S + 64 * sb + 32 * (kk >> 1) + 16 * v + 8 * (kk & 1),
-                       vd + static_cast<uint64_t>((kk * 2048) >> 4), Cfg::ID_O, (j > 0 || kk > 0));
+            mma(tmem + Cfg::COL_O + v * D, tmem + Cfg::COL_S + 64 * sb + 32 * (kk >> 1) + 16 * v + 8 * (kk & 1),
+                       vd + static_cast<uint64_t>((kk * 2048) >> 4), Cfg::ID_O, (j > base || kk > 0));
         }
-        tc::commit(&o_done[sb]);
-        tc::commit(&v_empty[vs]);
+        commit(&o_done[sb]);
+        commit(&v_empty[vs]);
       }
       __syncwarp();
-    }
-    if (elect_one()) tc::commit(drain);
+     }
+    } while (__all_sync(0xffffffffu, ok) && next(w, base));
+    __syncwarp();
+    if (rank == 0 && elect_one()) commit(drain);
    }
   } else if (warp >= Cfg::NSOFT + 4) {
     fewer_registers<Cfg::R_CONV>();
@@ -473,18 +664,24 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     bool ok = true;
     if constexpr (Cfg::BF16) {
       // ------------- converters of BF16 values: a strip of dims per warp -----------
-      using St = StripOf<D>;
+      using St = StripOf<Cfg::STRIP>;
       const int cw = ct >> 5, col = cw * Cfg::STRIP;
       const int blk = (col / D) * Cfg::F16 + (col % D) / 64 * 8192;
       // lane: chunk lane % CH of a key; the keys of eight lanes are apart, so that their
       // swizzled chunks lie in different banks
-      const int row0 = D == 128 ? (lane >> 3) + 4 * ((lane >> 2) & 1)
-                                : ((lane >> 3) & 1) + 2 * ((lane >> 1) & 3) + 8 * (lane >> 4);
+      const int row0 = St::CH == 4   ? (lane >> 3) + 4 * ((lane >> 2) & 1)
+                       : St::CH == 2 ? ((lane >> 3) & 1) + 2 * ((lane >> 1) & 3) + 8 * (lane >> 4)
+                                     : lane;
+      const int strip = Cfg::NCONV * rank + cw;  // of all that O's dims have
       const int off0 = row0 * 128 + ((((col % 64) / 8 + lane % St::CH) ^ (row0 & 7)) << 4);
-      int k = 0;
-      for (int i = 0; ok && i < n; ++i) {
-        const int vs = i % NV, fs = i % NF, kvalid = w.F - 64 * (w.p_lo + i);
-        ok = wait(&rv_full[vs], i / NV);
+      DiffWork w = first;
+      int base = 0;
+      do {
+       const int F = rows->prefix[w.b] + rows->chunk[w.b];
+       int k = 0;
+       for (int i = 0; ok && i < w.n; ++i) {
+        const int j = base + i, vs = j % NV, fs = j % NF, kvalid = F - 64 * (w.p_lo + i);
+        ok = wait(&rv_full[vs], j / NV);
         if (!ok) break;
         uint8_t* tile = sV + vs * Cfg::V_STAGE + blk;
         uint4 v[St::UNITS];
@@ -496,12 +693,10 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
             if (row0 + u * St::ROWS >= kvalid) v[u] = make_uint4(0u, 0u, 0u, 0u);
         }
         uint32_t top2 = 0u;  // largest rebiased magnitudes
-        uint4 h[St::UNITS];
 #pragma unroll
-        for (int u = 0; u < St::UNITS; ++u) {
-          h[u] = make_uint4(bf16x2_rebias(v[u].x), bf16x2_rebias(v[u].y), bf16x2_rebias(v[u].z), bf16x2_rebias(v[u].w));
-          top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(h[u].x, h[u].y), __vmaxu2(h[u].z, h[u].w)));
-        }
+        for (int u = 0; u < St::UNITS; ++u)
+          top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(bf16x2_rebias(v[u].x), bf16x2_rebias(v[u].y)),
+                                         __vmaxu2(bf16x2_rebias(v[u].z), bf16x2_rebias(v[u].w))));
         const uint32_t mine = max(top2 & 0xFFFFu, top2 >> 16);
         // k stays 0 while the strip's largest value lies in [2^-3, 2^15) (its first
         // page) and below 2^15 (later): no lift to apply.  (2^15 and 2^-3 rebiased.)
@@ -512,8 +707,8 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
 #pragma unroll
           for (int u = 0; u < St::UNITS; ++u)
             *reinterpret_cast<uint4*>(tile + off0 + u * St::ROWS * 128) =
-                make_uint4(f16x2_of(h[u].x, v[u].x), f16x2_of(h[u].y, v[u].y), f16x2_of(h[u].z, v[u].z),
-                           f16x2_of(h[u].w, v[u].w));
+                make_uint4(f16x2_of(bf16x2_rebias(v[u].x), v[u].x), f16x2_of(bf16x2_rebias(v[u].y), v[u].y),
+                           f16x2_of(bf16x2_rebias(v[u].z), v[u].z), f16x2_of(bf16x2_rebias(v[u].w), v[u].w));
         } else {
           uint32_t raw2 = 0u;
 #pragma unroll
@@ -530,27 +725,35 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
             *reinterpret_cast<uint4*>(tile + off0 + u * St::ROWS * 128) =
                 make_uint4(bf16x2_lift(v[u].x, f), bf16x2_lift(v[u].y, f), bf16x2_lift(v[u].z, f), bf16x2_lift(v[u].w, f));
         }
-        if (i >= NF) ok = wait(&f_empty[fs], i / NF - 1);
+        if (j >= NF) ok = wait(&f_empty[fs], j / NF - 1);
         if (!ok) break;
         if (lane == 0) {
-          float* slot = sF + fs * 256;
-          reinterpret_cast<uint8_t*>(slot)[cw] = i > 0 && k != was;
-          slot[8 + cw] = pow2i(i > 0 ? max(k - was, -126) : 0);
-          reinterpret_cast<int*>(slot)[16 + cw] = k;
+          // of a strip: whether its k fell, O's factor for that, 2^-k.  O of the pair's other
+          // CTA has these dims too.
+          float4* slot = reinterpret_cast<float4*>(sF + fs * 256);
+          const float4 x = make_float4(i > 0 && k != was ? 1.f : 0.f, pow2i(i > 0 ? max(k - was, -126) : 0), pow2i(-k), 0.f);
+          slot[strip] = x;
+          if constexpr (CG == 2) peer_store(slot + strip, x, &f_full[fs], rank ^ 1);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          q_arrive(&f_full[fs]);
+          if (CG == 2 && cw == 0) mbar_arrive_expect_tx(&f_full[fs], 16 * Cfg::NCONV);  // and the other CTA's strips
+          else q_arrive(&f_full[fs]);
           q_arrive(&v_full[vs]);
         }
-      }
+       }
+      } while (ok && next(w, base));
     } else {
       // ------------- converters: K(i), V(i) of the group's pages i -------------------
       constexpr int NCG = Cfg::NCG, NCT = 32 * Cfg::CGW;
       const int cg = ct / NCT, gt = ct % NCT;
-      for (int i = cg; ok && i < n; i += NCG) {
-        const int kvalid = w.F - 64 * (w.p_lo + i);
+      DiffWork w = first;
+      int base = 0;
+      do {
+       const int F = rows->prefix[w.b] + rows->chunk[w.b];
+       for (int i = base + (base + cg) % NCG; ok && i < base + w.n; i += NCG) {  // pages i = cg mod NCG
+        const int kvalid = F - 64 * (w.p_lo + i - base);
         if constexpr (!Cfg::K_RAW) {
           const int rk = i % NRK, ks = i % NK;
           ok = wait(&rk_full[rk], i / NRK);
@@ -558,8 +761,9 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
           if (!ok) break;
 #pragma unroll
           for (int h = 0; h < KH; ++h)
-            convert_tile<KK, D, Cfg::K_RB, NCT, Cfg::K_SPLIT>(sRK + rk * Cfg::RK_STAGE + h * Cfg::RK_HEAD, Cfg::RK_CODES,
-                                                             sK + ks * Cfg::K_STAGE + h * Cfg::K_HEAD, gt, kvalid);
+            convert_tile<KK, D, Cfg::K_RB, NCT, Cfg::K_SPLIT, Cfg::KR>(
+                sRK + rk * Cfg::RK_STAGE + h * Cfg::RK_HEAD, Cfg::RK_CODES + Cfg::KR * rank * Cfg::KSB,
+                sK + ks * Cfg::K_STAGE + h * Cfg::K_HEAD, gt, kvalid - Cfg::KR * rank);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
@@ -572,30 +776,36 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
         if (ok && i >= NV) ok = wait(&v_empty[vs], i / NV - 1);
         if (!ok) break;
 #pragma unroll
-        for (int v = 0; v < 2; ++v)
-          convert_tile<KV, D, Cfg::V_RB, NCT>(sRV + rv * Cfg::RV_STAGE + v * Cfg::RV_HEAD, Cfg::RV_CODES,
-                                              sV + vs * Cfg::V_STAGE + v * Cfg::F16, gt, kvalid);
+        for (int v = 0; v < Cfg::VH; ++v)
+          convert_tile<KV, D, Cfg::V_RB, NCT, false, 64, Cfg::V_HALF ? 4 : D / 16>(
+              sRV + rv * Cfg::RV_STAGE + v * Cfg::RV_HEAD, Cfg::RV_CODES, sV + vs * Cfg::V_STAGE + v * Cfg::VPART, gt,
+              kvalid, Cfg::V_HALF ? 4 * rank : 0);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
           q_arrive(&rv_empty[rv]);
           q_arrive(&v_full[vs]);
         }
-      }
+       }
+      } while (ok && next(w, base));
     }
   } else {
     // ------------------------------ softmax warps -----------------------------
     more_registers<Cfg::R_SOFT>();
     const int half = warp >> 2, quad32 = warp & 3, m = tid & 127;  // query row = TMEM lane; pages half, half + 2, ..
-    const int map = BOTH ? m >> 6 : w.map, r = BOTH ? m & 63 : m;
-    const int tl = r / a.G, g = r % a.G, token = w.t0 + tl;
-    const bool valid = (BOTH || tl < a.TQ) && token < w.limit;
-    const int pos = w.pos0 + token;  // keys <= pos are visible
+    const int r = BOTH ? m & 63 : m, tl = r / a.G, g = r % a.G;
+    bool live = true;
+    DiffWork w = first;
+    int base = 0;
+    do {
+    const int n = w.n, map = BOTH ? m >> 6 : w.pm & 1, pair = w.pm >> 1, token = (w.qt * CG + rank) * a.TQ + tl;
+    const bool valid = (BOTH || tl < a.TQ) && token < rows->chunk[w.b];
+    const int pos = rows->prefix[w.b] + token;  // keys <= pos are visible
     const uint32_t quad = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     float rs = 1.f;  // 2^-e of this query row
     {
       const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + ((static_cast<int64_t>(w.b) * a.T + token) * a.Hq + 2 * (w.pair * a.G + g) + map) * D);
+          a.q + ((static_cast<int64_t>(w.b) * a.T + token) * a.Hq + 2 * (pair * a.G + g) + map) * D);
       const uint32_t flip = a.negate ? 0x80008000u : 0u;
       float qf = 1.f;
       if constexpr (!Cfg::BF16) {
@@ -740,30 +950,32 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])), s0, s1);
       return s0 + s1;
     };
-    bool live = true;
-    const bool rows = __any_sync(0xffffffffu, valid);
-    if (!rows)  // rows past the last query: P is whatever the buffers hold, and their O is not stored
-      for (int j = half; live && j < n; j += 2) {
+    const bool any = __any_sync(0xffffffffu, valid);
+    const int from = base + (base + half) % 2;  // this warp's first page
+    if (!any)  // rows past the last query: P is whatever the buffers hold, and their O is not stored
+      for (int j = from; live && j < base + n; j += 2) {
         live = wait(&s_full[j % NS], j / NS);
         if constexpr (Cfg::HAS_F) live = live && wait(&f_full[j % NF], j / NF);
         tc::fence_after();
         tc::fence_before();
         if (lane == 0) {
+          q_arrive(&x_full[4 * (j & 1) + quad32]);
           q_arrive(&p_full[j % NS]);
           if constexpr (Cfg::HAS_F) q_arrive(&f_empty[j % NF]);
+          if constexpr (Cfg::BF16 && CG == 2) peer_arrive(&f_empty[j % NF], rank ^ 1);
         }
       }
-    for (int j = half; rows && j < n; j += 2) {
+    for (int j = from; any && j < base + n; j += 2) {
       const int sb = j % NS, fs = j % NF;
       const uint32_t s_at = quad + Cfg::COL_S + 64 * sb;
       const float* ksc = sF + fs * 256 + (BOTH ? 64 * map : 0);
       const float* vsc = sF + fs * 256 + 128;
-      const int kmax = valid ? pos - 64 * (w.p_lo + j) : -1;
+      const int kmax = valid ? pos - 64 * (w.p_lo + j - base) : -1;
       bool strips = false;  // BF16 values: a strip's k fell
       float most = 0.f;     // FP8-row V: the largest scale of the page
       if constexpr (Cfg::HAS_F) {
         live = live && wait(&f_full[fs], j / NF);
-        if constexpr (Cfg::BF16) strips = *reinterpret_cast<const unsigned long long*>(sF + fs * 256) != 0ull;
+        if constexpr (Cfg::BF16) strips = lane < Cfg::STRIPS && sF[fs * 256 + 4 * lane] != 0.f;  // any lane's, below
         if constexpr (KV == KIND_FP8) {
           const float4 s4 = *reinterpret_cast<const float4*>(sF + fs * 256 + 128 + 4 * lane);  // both heads' 128 scales
           most = fmaxf(fmaxf(s4.x, s4.y), fmaxf(s4.z, s4.w));
@@ -782,7 +994,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       // the reference and lift after the page before, from the warp of the other pages
       float m_was = -INFINITY;
       int k_was = kLift0, k_now = kLift0;
-      if (j > 0) {
+      if (j > base) {
         live = live && wait(&x_full[4 * ((j - 1) & 1) + quad32], (j - 1) >> 1);
         const float2 x = sX[((j - 1) & 1) * 128 + m];
         m_was = x.x;
@@ -805,7 +1017,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       mu = m_now == -INFINITY ? 0.f : m_now - static_cast<float>(k_now);
 #pragma unroll
       for (int h = 0; h < 2; ++h) l += weights(sv[h], vsc + 32 * h, s_at + 32 * h);
-      if (j >= 1 && __any_sync(0xffffffffu, resc || strips || k_now != k_was)) {
+      if (j > base && __any_sync(0xffffffffu, resc || strips || k_now != k_was)) {
         // O, once PV(j - 1) is complete
         const float factor = !resc ? 1.f : m_was == -INFINITY ? 0.f : ex2((m_was - m_now) + static_cast<float>(k_now - k_was));
         live = live && wait(&o_done[(j - 1) % NS], (j - 1) / NS);
@@ -815,52 +1027,72 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
           uint32_t ov[16];
           tc::ld16(quad + Cfg::COL_O + c0, ov);
           tc::wait_ld();
-          float fc = factor;
-          if constexpr (Cfg::BF16) fc *= sF[fs * 256 + 8 + c0 / Cfg::STRIP];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * fc);
+          for (int c8 = 0; c8 < 16; c8 += 8) {
+            const float fc = Cfg::BF16 ? factor * sF[fs * 256 + 4 * ((c0 + c8) / Cfg::STRIP) + 1] : factor;
+#pragma unroll
+            for (int c = c8; c < c8 + 8; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * fc);
+          }
           tc::st16(quad + Cfg::COL_O + c0, ov);
         }
       }
+      if constexpr (Cfg::BF16)  // the strips' lifts that the piece ends with
+        if (j == base + n - 1 && lane < Cfg::STRIPS) sDown[16 * quad32 + lane] = sF[fs * 256 + 4 * lane + 2];
       tc::wait_st();
       tc::fence_before();
       __syncwarp();
       if (lane == 0) {
         q_arrive(&p_full[sb]);
         if constexpr (Cfg::HAS_F) q_arrive(&f_empty[fs]);  // this warp is done with the page's factors
+        if constexpr (Cfg::BF16 && CG == 2) peer_arrive(&f_empty[fs], rank ^ 1);
       }
     }
-    // ---- this CTA's partial: (m, l) of the row, and O, the half's D dims -------------
-    live = live && wait(drain, 0);  // every PV
+    // ---- the piece's partial: (m, l) of the row, and O, the half's D dims -------------
+    if (n > 0) live = live && wait(&o_done[(base + n - 1) % NS], (base + n - 1) / NS);  // every PV
     tc::fence_after();
     const float m_eff = m_own == -INFINITY ? -INFINITY : m_own - static_cast<float>(k_own);
     sX[256 + 128 * half + m] = make_float2(m_eff, l);
     asm volatile("bar.sync %0, 64;" ::"r"(1 + quad32) : "memory");  // the two warps of these rows
+    const int64_t part = BOTH ? static_cast<int64_t>(pair) * a.ctas + blockIdx.x
+                              : ((static_cast<int64_t>(w.b) * a.H + w.pm) * a.tiles + w.qt + blockIdx.x / CG) * CG + rank;
     if (live && valid && half == 0) {  // the sums, under the reference after the last page
-      const float2 last = sX[256 + 128 * (n > 0 ? (n - 1) & 1 : 0) + m], other = sX[256 + 128 * (n > 0 ? n & 1 : 1) + m];
+      const int last_half = n > 0 ? (base + n - 1) & 1 : 0;
+      const float2 last = sX[256 + 128 * last_half + m], other = sX[256 + 128 * (last_half ^ 1) + m];
       const float f = other.x == -INFINITY ? 0.f : ex2(other.x - last.x);
-      a.ws_ml[w.part * 128 + m] = make_float2(last.x, fmaf(other.y, f, last.y));
+      a.ws_ml[part * 128 + m] = make_float2(last.x, fmaf(other.y, f, last.y));
     }
-    if (live) {
-      if (n > 0 && (!BOTH || __any_sync(0xffffffffu, valid))) {
-        float* dst = a.ws_o + (w.part * 128 + m) * (2 * D);
+    if (live && n > 0 && any) {
+      float4* dst = reinterpret_cast<float4*>(a.ws_o) + part * (D / 2) * 128 + m;
 #pragma unroll 1
-        for (int c0 = half * D; c0 < (half + 1) * D; c0 += 16) {
-          uint32_t v[16];
-          tc::ld16(quad + Cfg::COL_O + c0, v);
-          tc::wait_ld();
-          if constexpr (Cfg::BF16) {
-            const float f = pow2i(-reinterpret_cast<const int*>(sF + ((n - 1) % NF) * 256)[16 + c0 / Cfg::STRIP]);
+      for (int c0 = half * D; c0 < (half + 1) * D; c0 += 16) {
+        uint32_t v[16];
+        tc::ld16(quad + Cfg::COL_O + c0, v);
+        tc::wait_ld();
+        if constexpr (Cfg::BF16) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * f);
-          }
-          if (valid) {
+          for (int c8 = 0; c8 < 16; c8 += 8) {
+            const float f = sDown[16 * quad32 + (c0 + c8) / Cfg::STRIP];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              *reinterpret_cast<uint4*>(dst + c0 + 4 * c) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            for (int c = c8; c < c8 + 8; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * f);
           }
         }
+        if (valid) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            dst[(c0 / 4 + c) * 128] = make_float4(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]),
+                                                  __uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3]));
+        }
       }
+    }
+    tc::fence_before();
+    __syncwarp();
+    if (lane == 0) q_arrive(o_free);
+    } while (live && next(w, base));
+    if (CG == 2 && live && tid == 0) {  // the last commits that nobody else waits for have arrived
+      constexpr int ring = Cfg::K_RAW ? NRK : NK;
+      const int j = base - 1;
+      wait(&v_empty[j % NV], j / NV);
+      wait(Cfg::K_RAW ? &rk_empty[j % ring] : &k_empty[j % ring], j / ring);
     }
   }
 
@@ -869,7 +1101,12 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (warp == 0) tc::dealloc(tmem, 512);
+  if constexpr (CG == 2) {  // neither CTA leaves while the other may reach into it
+    cluster_sync();
+    if (warp == 0) tc::dealloc2(tmem, 512);
+  } else {
+    if (warp == 0) tc::dealloc(tmem, 512);
+  }
 }
 
 template <int KK, int KV, int D, bool BOTH>
@@ -879,7 +1116,10 @@ cudaError_t launch_diff_tile(const nk_pool* p, int layer, const DiffTileArgs& a,
   static std::atomic<uint64_t> granted{0};
   const cudaError_t e = grant_smem(granted, k, Cfg::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
+  if constexpr (Cfg::CG == 2)
+    return launch_pdl_cluster(k, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, 2, p->tmap_half[layer], p->tmap[layer * 2 + 1], a);
+  else
+    return launch_pdl(k, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, p->tmap[layer * 2 + 0], p->tmap[layer * 2 + 1], a);
 }
 
 template <int KK, int KV>

@@ -33,6 +33,7 @@ struct nk_pool {
   nk::PlaneGeom plane[4];  // [K code, V code, K scale, V scale]
   std::vector<void*> ptrs;            // [layer * n_planes + i]
   std::vector<CUtensorMap> tmap;      // [layer * 2 + {0: K code, 1: V code}]
+  std::vector<CUtensorMap> tmap_half; // [layer]: K code, boxes of half a page (32 rows)
   int device;
   int num_sms;
   int* status;            // device address of the status word of `device`
@@ -65,6 +66,6 @@ int* status_word();
 
 // 2-D TMA descriptor over `rows` rows of `row_bytes` bytes (viewed as uint8):
 // boxes of 64 rows x min(row_bytes, 128) bytes with the matching swizzle.
-int encode_code_tmap(CUtensorMap* m, void* base, int row_bytes, int64_t rows);
+int encode_code_tmap(CUtensorMap* m, void* base, int row_bytes, int64_t rows, int box_rows = 64);
 
 }  // namespace nk

@@ -182,10 +182,10 @@ extern "C" int nk_pool_plane_bytes(const nk_pool_desc* desc, int32_t M, int32_t*
 }
 
 // TMA descriptor of one code plane: a 2-D uint8 tensor of rows of row_bytes
-// bytes (one row per (g, h, o) token), boxes of 64 rows x min(row_bytes, 128)
+// bytes (one row per (g, h, o) token), boxes of box_rows x min(row_bytes, 128)
 // bytes, swizzled so that rows of a box land in distinct shared-memory banks.
 namespace nk {
-int encode_code_tmap(CUtensorMap* m, void* base, int row_bytes, int64_t rows) {
+int encode_code_tmap(CUtensorMap* m, void* base, int row_bytes, int64_t rows, int box_rows) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::mutex mu;
   std::lock_guard<std::mutex> lock(mu);
@@ -204,7 +204,7 @@ int encode_code_tmap(CUtensorMap* m, void* base, int row_bytes, int64_t rows) {
                                         : CU_TENSOR_MAP_SWIZZLE_32B;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_x), 64u};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_x), static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1u, 1u};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -258,6 +258,7 @@ extern "C" int nk_pool_create(const nk_pool_desc* desc, int32_t M, void* const* 
     return fail(NK_ERR_CUDA, "device query failed (status word / SM count)");
   }
   p->tmap.resize(static_cast<size_t>(desc->num_layers) * 2);
+  p->tmap_half.resize(static_cast<size_t>(desc->num_layers));
   for (int l = 0; l < desc->num_layers; ++l) {
     for (int s = 0; s < 2; ++s) {
       rc = encode_code_tmap(&p->tmap[l * 2 + s], p->ptrs[l * n_planes + s], g[s].row_bytes, rows);
@@ -265,6 +266,11 @@ extern "C" int nk_pool_create(const nk_pool_desc* desc, int32_t M, void* const* 
         delete p;
         return rc;
       }
+    }
+    rc = encode_code_tmap(&p->tmap_half[l], p->ptrs[l * n_planes], g[0].row_bytes, rows, 32);
+    if (rc) {
+      delete p;
+      return rc;
     }
   }
   *out = p;

@@ -147,21 +147,24 @@ __device__ __forceinline__ float key_factor(const uint8_t* scales, int r) {
 // significant bits, so the remainder (at most 7 bits, the same multiple) is an
 // f16 value and k1 - k2' = c s' exactly: one f16 FMA per pair, fma(c, -s', k1),
 // gives it, and the MMA that reads k2' negates its B operand.
-template <int KIND, int D, int RB, int NCT, bool SPLIT = false>
-__device__ __forceinline__ void convert_tile(const uint8_t* raw, int raw_codes, uint8_t* f16, int ct, int kvalid) {
-  constexpr int GPR = D / 16;            // 16-dim groups per key
-  constexpr int UPT = (64 * GPR) / NCT;  // units per thread
-  static_assert(UPT * NCT == 64 * GPR && UPT >= 1, "converter units");
+//
+// ROWS keys (the raw tile's first) and GPR groups from g0 on: all of the tile, or a part
+// that becomes a tile of its own.
+template <int KIND, int D, int RB, int NCT, bool SPLIT = false, int ROWS = 64, int GPR = D / 16>
+__device__ __forceinline__ void convert_tile(const uint8_t* raw, int raw_codes, uint8_t* f16, int ct, int kvalid,
+                                             int g0 = 0) {
+  constexpr int UPT = (ROWS * GPR) / NCT;  // units per thread
+  static_assert(UPT * NCT == ROWS * GPR && UPT >= 1, "converter units");
   static_assert(!SPLIT || KIND == KIND_INT8, "split tiles are for INT8-G64 keys");
   // a thread's UPT groups start at a multiple of UPT, so with 16 UPT dividing
   // 64 they share one INT8-G64 scale group
   static_assert(KIND != KIND_INT8 || 64 % (16 * UPT) == 0, "one scale group per thread");
   constexpr int SB = scale_row_bytes<KIND>(D);
   const uint8_t* scales = raw + raw_codes;
-  const int r = (ct & 7) + 8 * ((ct >> 3) & 7);  // the thread's key
+  const int r = (ct & 7) + 8 * ((ct >> 3) & (ROWS / 8 - 1));  // the thread's key
   int gg[UPT];
 #pragma unroll
-  for (int k = 0; k < UPT; ++k) gg[k] = UPT * (ct >> 6) + (k + ((ct >> 3) & 1)) % UPT;
+  for (int k = 0; k < UPT; ++k) gg[k] = UPT * (ct / ROWS) + (k + ((ct >> 3) & 1)) % UPT;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   if (r >= kvalid) {  // a key at or past the frontier: zeros in every tile
 #pragma unroll
@@ -182,12 +185,12 @@ __device__ __forceinline__ void convert_tile(const uint8_t* raw, int raw_codes, 
     // the product rounded once (k1); SPLIT also stores the remainder k2
     const float shift = pow2_neg(int8_row_shift<D>(scales + r * SB));
     const __half s16 =
-        __float2half_rn(__half2float(*reinterpret_cast<const __half*>(scales + r * SB + 2 * ((16 * gg[0]) / 64))) * shift);
+        __float2half_rn(__half2float(*reinterpret_cast<const __half*>(scales + r * SB + 2 * ((16 * (g0 + gg[0])) / 64))) * shift);
     const uint32_t s2 = pack_h2(s16, s16), s2n = s2 ^ 0x80008000u;  // s', -s'
     // every raw load of the thread before any store (the stores could alias)
     uint4 w[UPT];
 #pragma unroll
-    for (int k = 0; k < UPT; ++k) w[k] = *reinterpret_cast<const uint4*>(raw + raw_off<RB>(r, 16 * gg[k]));
+    for (int k = 0; k < UPT; ++k) w[k] = *reinterpret_cast<const uint4*>(raw + raw_off<RB>(r, 16 * (g0 + gg[k])));
 #pragma unroll
     for (int k = 0; k < UPT; ++k) {
       const uint32_t wv[4] = {w[k].x ^ 0x80808080u, w[k].y ^ 0x80808080u, w[k].z ^ 0x80808080u,
@@ -216,7 +219,7 @@ __device__ __forceinline__ void convert_tile(const uint8_t* raw, int raw_codes, 
     uint4 lo[UPT], hi[UPT];
     // every raw load of the thread before any store (the stores could alias)
 #pragma unroll
-    for (int k = 0; k < UPT; ++k) convert16<KIND, D, RB>(raw, scales, r, gg[k], lo[k], hi[k]);
+    for (int k = 0; k < UPT; ++k) convert16<KIND, D, RB>(raw, scales, r, g0 + gg[k], lo[k], hi[k]);
 #pragma unroll
     for (int k = 0; k < UPT; ++k) {
       *reinterpret_cast<uint4*>(f16 + f16_off(r, 16 * gg[k])) = lo[k];
