@@ -236,7 +236,7 @@ extern "C" int nk_paged_diff_decode_attention(const void* q, int32_t Hq, const n
   if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
   if (!pl.fn) {
     const DiffTileJoinArgs tj{t.table_rows, t.lengths, nullptr, t.ws_ml, t.ws_o, B, T, Hq, t.H, t.G, t.L, t.C, 0, 1, 1, pl.ctas, o};
-    e = launch_diff_tile_join<true>(pool->desc.head_dim, tj, s);
+    e = launch_diff_tile_join<true>(pool->desc.head_dim, pool->num_sms, tj, s);
     if (e != cudaSuccess) return cuda_fail(e, "differential decode join launch");
     return NK_OK;
   }

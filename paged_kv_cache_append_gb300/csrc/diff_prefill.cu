@@ -70,7 +70,7 @@ extern "C" int nk_paged_diff_prefill_attention(const void* q_chunk, int32_t Hq, 
   if (e != cudaSuccess) return cuda_fail(e, "differential prefill launch");
   const DiffTileJoinArgs j{table_rows, prefix_len, chunk_len, a.ws_ml, a.ws_o, B,       Tc,       Hq,
                            a.H,        a.G,        a.L,       a.C,     pl.TQ,  pl.tiles, pl.cg, pl.ctas, o};
-  e = launch_diff_tile_join<false>(pool->desc.head_dim, j, s);
+  e = launch_diff_tile_join<false>(pool->desc.head_dim, pool->num_sms, j, s);
   if (e != cudaSuccess) return cuda_fail(e, "differential prefill join launch");
   return NK_OK;
 }

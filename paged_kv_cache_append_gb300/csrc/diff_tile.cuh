@@ -80,7 +80,7 @@ constexpr int diff_chunk_group(int kind_v, int D) { return (kind_v == KIND_FP8 |
 // partial), and cluster c of n takes the units [c W / n, (c + 1) W / n): a tile that crosses
 // a boundary has a partial from each of its clusters, numbered tile + cluster.  n is at
 // most one CTA per SM and leaves each at least kDiffLeastUnits.
-constexpr int kDiffTileCost = 6, kDiffLeastUnits = 10;
+constexpr int kDiffTileCost = 6, kDiffLeastUnits = 5;
 
 // Units of tiles [0, upto) of a row (a warp).
 __device__ __forceinline__ int64_t diff_tile_units(int prefix, int chunk, int TQ, int upto) {
@@ -135,7 +135,7 @@ struct DiffTileCfg {
   static constexpr int NSOFT = 8, NCONV = 8, THREADS = 32 * (NSOFT + 4 + NCONV);
   // Registers: 640 threads start with 96 each; the softmax warps (64 scores and 16 or 32
   // packed weights at a time) take over what the others do not need.
-  static constexpr int R_SOFT = 136, R_MISC = 56, R_CONV = 72;
+  static constexpr int R_SOFT = BOTH ? 144 : 136, R_MISC = BOTH ? 40 : 56, R_CONV = 72;
   // (two CTAs of an SM would not fit: each takes all of the tensor memory)
   static_assert(256 * R_SOFT + 128 * R_MISC + 256 * R_CONV <= 640 * 96, "registers of the CTA");
   static constexpr int KCB = BF16 ? 2 * D : code_row_bytes<KK>(D), VCB = BF16 ? 2 * D : code_row_bytes<KV>(D);
@@ -229,8 +229,12 @@ __device__ __forceinline__ DiffWork diff_chunk_first(const DiffChunkRows& rows, 
   const int64_t W = rows.total(B, maps);
   const int n = diff_chunk_ctas(W, most);
   if (W == 0 || c >= n) return w;
-  int64_t at = c * W / n;
-  w.left = static_cast<int>((c + 1) * W / n - at);
+  const auto cut = [&](int k) {  // k W / n, in 32 bits where they do
+    return W < (1 << 22) ? static_cast<int64_t>(static_cast<unsigned>(k) * static_cast<unsigned>(W) / static_cast<unsigned>(n))
+                         : k * W / n;
+  };
+  int64_t at = cut(c);
+  w.left = static_cast<int>(cut(c + 1) - at);
   w.b = 0;
   while (at >= rows.units[w.b] * maps) at -= rows.units[w.b++] * maps;
   w.pm = static_cast<int>(at / rows.units[w.b]);
@@ -394,18 +398,6 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;  // this CTA's in its pair
   const int TQ = a.TQ * CG;                                         // tokens of a tile
-  griddep_wait();  // launched with programmatic stream serialization
-  griddep_launch_dependents();
-  DiffWork first;
-  if constexpr (BOTH) {
-    first = diff_decode_work(a, rows);
-  } else {
-    rows->fill(a.table_rows, a.lengths, a.chunk_len, a.B, a.T, a.L, a.C, TQ, warp, blockIdx.x == 0 ? a.status : nullptr);
-    __syncthreads();
-    first = diff_chunk_first(*rows, a.B, a.H, TQ, blockIdx.x / CG, gridDim.x / CG);
-  }
-  if (first.n < 0) return;  // a pair's CTAs alike
-
   if (tid == 0) {
     for (int i = 0; i < NK; ++i) {
       mbar_init(&k_full[i], Cfg::CGW);
@@ -444,6 +436,20 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     prefetch_tmap(&tmk);
     prefetch_tmap(&tmv);
   }
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // the other CTA's barriers exist
+  griddep_wait();  // launched with programmatic stream serialization
+  griddep_launch_dependents();
+  DiffWork first;
+  if constexpr (BOTH) {
+    first = diff_decode_work(a, rows);
+  } else {
+    rows->fill(a.table_rows, a.lengths, a.chunk_len, a.B, a.T, a.L, a.C, TQ, warp, blockIdx.x == 0 ? a.status : nullptr);
+    __syncthreads();
+    first = diff_chunk_first(*rows, a.B, a.H, TQ, blockIdx.x / CG, gridDim.x / CG);
+  }
+  if (first.n < 0) return;  // a pair's CTAs alike
+
   if (warp == 0) {
     if constexpr (CG == 2) {
       tc::alloc2(tslot, 512);
@@ -455,7 +461,6 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
   }
   tc::fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();  // the other CTA's barriers exist
   tc::fence_after();
   const uint32_t tmem = *tslot;
   // Every role goes through the CTA's pieces; `base` counts the pages of those before.
@@ -828,7 +833,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       const uint32_t q_at = quad + Cfg::COL_Q + (BOTH ? map * (D / 2) : 0);
       const uint32_t z_at = quad + Cfg::COL_Q + (map ^ 1) * (D / 2);
       const uint32_t zero[16] = {};
-#pragma unroll 1
+#pragma unroll
       for (int d0 = half * (D / 2); d0 < (half + 1) * (D / 2); d0 += (Cfg::K8MMA ? 64 : 32)) {
         if constexpr (Cfg::K8MMA) {  // q' = hi + lo in E4M3, as in qprefill.cu
           uint32_t hv[16], lv[16];
@@ -973,15 +978,13 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       const int kmax = valid ? pos - 64 * (w.p_lo + j - base) : -1;
       bool strips = false;  // BF16 values: a strip's k fell
       float most = 0.f;     // FP8-row V: the largest scale of the page
-      if constexpr (Cfg::HAS_F) {
-        live = live && wait(&f_full[fs], j / NF);
-        if constexpr (Cfg::BF16) strips = lane < Cfg::STRIPS && sF[fs * 256 + 4 * lane] != 0.f;  // any lane's, below
-        if constexpr (KV == KIND_FP8) {
-          const float4 s4 = *reinterpret_cast<const float4*>(sF + fs * 256 + 128 + 4 * lane);  // both heads' 128 scales
-          most = fmaxf(fmaxf(s4.x, s4.y), fmaxf(s4.z, s4.w));
-        }
-      }
+      if constexpr (Cfg::HAS_F) live = live && wait(&f_full[fs], j / NF);
       live = live && wait(&s_full[sb], j / NS);
+      if constexpr (Cfg::BF16) strips = lane < Cfg::STRIPS && sF[fs * 256 + 4 * lane] != 0.f;  // any lane's, below
+      if constexpr (KV == KIND_FP8) {
+        const float4 s4 = *reinterpret_cast<const float4*>(sF + fs * 256 + 128 + 4 * lane);  // both heads' 128 scales
+        most = fmaxf(fmaxf(s4.x, s4.y), fmaxf(s4.z, s4.w));
+      }
       tc::fence_after();
       uint32_t sv[2][32];
       tc::ld32(s_at, sv[0]);
@@ -1064,13 +1067,13 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     if (live && n > 0 && any) {
       float4* dst = reinterpret_cast<float4*>(a.ws_o) + part * (D / 2) * 128 + m;
 #pragma unroll 1
-      for (int c0 = half * D; c0 < (half + 1) * D; c0 += 16) {
-        uint32_t v[16];
-        tc::ld16(quad + Cfg::COL_O + c0, v);
-        tc::wait_ld();
+      for (int c0 = half * D; c0 < (half + 1) * D; c0 += 32) {
+        uint32_t v[32];
+        tc::ld32(quad + Cfg::COL_O + c0, v);
+        tc::wait_ldn(v);
         if constexpr (Cfg::BF16) {
 #pragma unroll
-          for (int c8 = 0; c8 < 16; c8 += 8) {
+          for (int c8 = 0; c8 < 32; c8 += 8) {
             const float f = sDown[16 * quad32 + (c0 + c8) / Cfg::STRIP];
 #pragma unroll
             for (int c = c8; c < c8 + 8; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * f);
@@ -1078,7 +1081,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
         }
         if (valid) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 8; ++c)
             dst[(c0 / 4 + c) * 128] = make_float4(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]),
                                                   __uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3]));
         }
