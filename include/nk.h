@@ -482,9 +482,11 @@ int nk_diff_decode_workspace_bytes(const nk_pool* pool, int32_t B, int32_t T, in
  * A NaN among the keys or values that a token sees makes its outputs NaN, and
  * a NaN or an infinity among the values of a row's T tokens may reach the
  * outputs of all T; stale bytes past the frontier do not enter.
- * Two launches (csrc/diff_decode.cuh): split-K over the pages, then the join of
- * the splits with the difference and the norm.  Softmax weights and values are
- * rounded as in nk_paged_decode_attention's warp-level kernel.
+ * Two launches: split-K over the pages, then the join of the splits with the
+ * difference and the norm.  Up to 8 query rows (T * Hq / H) a map they are
+ * warp-level (csrc/diff_decode.cuh), their softmax weights f16, or bf16 in two
+ * terms over BF16 pages; beyond that on the tensor cores, rounded as in
+ * nk_paged_diff_prefill_attention.
  * The pool's device must be current.
  * Errors: NK_ERR_INVALID_ARG, NK_ERR_SHAPE (H odd, Hq not a multiple of H, B > C,
  * T < 1), NK_ERR_UNSUPPORTED (head_dim 256; T * Hq / H > 64), NK_ERR_ALIGN,
@@ -506,9 +508,12 @@ int nk_diff_prefill_workspace_bytes(const nk_pool* pool, int32_t B, int32_t Tc, 
  *   workspace: nk_diff_prefill_workspace_bytes bytes, no initialisation needed;
  *   two calls that share a workspace must not overlap.
  * A NaN or an infinity among the values of a chunk may reach all of its outputs.
- * Two launches: on the tensor cores (csrc/diff_tile.cuh)
- * and for the join.  Softmax weights and values are rounded as in
- * nk_paged_prefill_attention.
+ * Two launches: on the tensor cores (csrc/diff_tile.cuh) and for the join
+ * (csrc/diff_join.cuh).  Softmax weights are f16 for every profile (relative
+ * error <= 2^-11), scores exact products as in nk_paged_prefill_attention;
+ * BF16 values are taken as f16 times a power of two per strip of 8 to 32 dims:
+ * exact above 2^-14 of the strip's largest value so far, within 2^-19 of it
+ * below; the quantized pages' values as there.
  * The pool's device must be current.
  * Errors: as nk_paged_diff_decode_attention; NK_ERR_UNSUPPORTED for Hq / H > 64. */
 int nk_paged_diff_prefill_attention(const void* q_chunk, int32_t Hq, const nk_pool* pool,

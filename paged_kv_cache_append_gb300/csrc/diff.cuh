@@ -44,7 +44,7 @@ __device__ __forceinline__ uint2 diff_finish(const float (&o)[4], float f, const
   return make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
 }
 
-// At most this many splits of a decoded row: bounds the join's work.
+// At most this many splits of a decoded row: bounds the join's work and its shared memory.
 constexpr int kDiffMaxSplits = 128;
 
 // Valid length of row b as the decode kernels take it (0: refused, no keys).

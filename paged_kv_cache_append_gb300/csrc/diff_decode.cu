@@ -163,7 +163,9 @@ struct DiffPlan {
 };
 
 // Up to 8 query rows a map the warp-level kernel (4 or 8 rows of both maps in
-// one column tile or two), beyond that the 64-row tiles, one CTA per SM.
+// one column tile or two), beyond that the 64-row tiles; both with one CTA per SM.
+// 8 rows over 8 x 32768 tokens, head_dim 128, by the warps and by the tiles: FP8-row 59
+// and 88 us, INT8-G64 61 and 108; over 8 x 131072, K8V4: 144 and 203.
 static int diff_plan(const nk_pool* p, int B, int T, int Hq, DiffPlan* pl) {
   const int rc = check_diff_shape(p, B, T, Hq);
   if (rc) return rc;

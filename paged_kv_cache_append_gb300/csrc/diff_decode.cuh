@@ -4,10 +4,12 @@
 //
 // For KV heads 2j, 2j + 1 (keys K1, K2; values V = [V1 V2]) and the query rows
 // of the heads that share them, o = softmax(Q1 K1^T) V - lambda softmax(Q2 K2^T) V.
-// Few query rows (the rest goes to diff_tile.cuh).  A CTA owns one (row b, pair j,
-// page range) and stages the four code tiles of a page together; each of its four
-// consumer warps owns 16 keys of every page, for both maps and both value heads, so
-// that every code is converted once and no warp waits for another:
+// Up to 8 query rows a map (the rest goes to diff_tile.cuh).  A CTA, one per SM, owns one
+// (row b, pair j, page range) and NG groups of four warps, each with a ring of SG stages of
+// its own and every NG-th page; each warp owns 16 keys of a page, for both maps and both
+// value heads, so that every code is converted once and no warp waits for another's
+// results, and copies one of the group's four tiles (no producer: its warp would cost the
+// others registers):
 //   QK   mma.m16n8k16, keys as M.  Up to 4 query rows (PACK) both maps fill the 8
 //        columns (map 1 in 0-3, map 2 in 4-7): S1 = K1 [Q1 Q2]^T, S2 = K2 [Q1 Q2]^T,
 //        of which a lane keeps the one of its columns' map; 8 rows take a tile a map.
@@ -21,8 +23,13 @@
 // last one the warp zeroes its stale value rows in place.
 //
 // Two heads to a warp halved the instructions of a page against one head to each of
-// two warps that exchange their weights (3793 warp instructions, FP8-row, head_dim
-// 128), whose issue rate bound that form at 46% of the copy rate.
+// two warps that exchange their weights (FP8-row, head_dim 128: 3800 warp instructions a
+// page, whose issue bound that form at 46% of the copy rate).
+//
+// Measured (with the join, L2 cold): 8 rows of 25500 tokens, 16 heads over 4, FP8-row: 45 us,
+// 69% of the copy rate; of 131072: each further page at 94-100% of it (FP8-row, BF16, K8V4),
+// at 64% for NVFP4, whose conversion bounds it.  What is left is the start (plan, first
+// copies) and the join, 15 us of every call.
 //
 // Partials of (map, query row) go to the workspace, for the join (diff_decode.cu).
 #pragma once

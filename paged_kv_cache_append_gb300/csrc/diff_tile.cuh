@@ -1,16 +1,26 @@
-// diff_tile.cuh -- differential attention of 128 query rows at a time on the
+// diff_tile.cuh -- differential attention of 128 query rows to a CTA on the
 // 5th-generation tensor cores (kernel template; instantiated per profile in
 // diff_tile_*.cu): prompt chunks, and decode / verify tokens of many query rows.
 //
-// Chunks (BOTH = false).  A CTA owns 128 query rows of one map of one (row b,
-// pair of KV heads): TQ = floor(128 / G) consecutive tokens times the G heads that
-// share the pair, and one range of pages.  Per page of 64 keys
-//   S = Q_m K_m^T   M 128 x N 64 x K D;   P = exp2(S - m);
-//   O += P [V1 V2]  M 128 x N 2 D x K 64,
+// Per page of 64 keys, for the query rows of a map m of a pair of KV heads:
+//   S = Q_m K_m^T;   P = exp2(S - reference);   O += P [V1 V2]
 // 2 D + 4 D flops per (query row, key): the least for two maps over one wide value.
-// Decode / verify (BOTH = true).  Lanes 0-63 are the (up to 64) query rows of map
+//
+// Chunks (BOTH = false).  A cluster of two CTAs owns 2 TQ consecutive tokens, TQ =
+// floor(128 / G), of one map: 128 query rows in each CTA (TQ tokens times the G heads
+// that share the pair), and every MMA is one of both (cta_group::2, M 256).  A CTA
+// stages and converts one half of each operand: 32 of a page's keys, and the value head
+// of its rank (FP8-row and INT8-G64 values: 64 of the dims of both heads, since each head
+// has its own P; at head_dim 64 that half would be less than a swizzle atom, so there a
+// CTA works alone, M 128).  With one CTA to an MMA a BF16 chunk read its pages at 8.3
+// TB/s from L2, which bound it: 8192 tokens behind 0, 731 us, 490 in pairs.
+// The grid is one cluster for every two SMs; the line of all tiles' pages is cut into equal
+// parts (diff_chunk_first), so that a CTA sets up once and no wave is short: with a CTA
+// to a tile and range, each started and drained for 10 us.
+//
+// Decode / verify (BOTH = true).  One CTA; lanes 0-63 are the (up to 64) query rows of map
 // 1, lanes 64-127 those of map 2, so that every page is read and converted once:
-//   S = [Q1; 0] K1^T + [0; Q2] K2^T, two MMAs into one S.
+//   S = [Q1; 0] K1^T + [0; Q2] K2^T, two MMAs (M 128) into one S.
 //
 // Tensor memory: NS S buffers of 64 columns, Q (D / 2 columns; BOTH: two operands), O
 // [256, 256 + 2 D).  P goes over the S that its own warp computed it from: keys
@@ -19,27 +29,35 @@
 // Operands.  Scores: BF16 pages as they are; FP8-row keys of head_dim 128 as raw
 // E4M3 codes with q in two E4M3 terms, other quantized keys as exact f16 tiles
 // (INT8-G64: two), their per-key factors applied to the scores in fp32, as in
-// qprefill.cu.  P is f16 for every profile, so that its weights keep 11 bits, and
-// V therefore too:
+// qprefill.cu.  P is f16 for every profile, so that its weights keep 11 bits (bf16
+// weights: an error of 0.0025 against 0.0017 over a BF16 chunk), and V therefore too:
 //   * NVFP4 values carry their scales exactly; one P serves both heads, N = 2 D;
 //   * FP8-row and INT8-G64 values leave a factor per key to the weights, so each
 //     head has its own P (the second 16 columns further), N = D twice;
-//   * BF16 values are rewritten in place, v 2^k with a power of two per strip of 2 D /
-//     8 dims that brings the strip's largest value so far below 2^15 and above 2^-3
-//     (0 while it is there by itself): exact for every element above its 2^-14th, and
-//     to 2^-19 of the largest below.  k only falls (then O is rescaled), and the store
-//     divides it out.
+//   * BF16 values are rewritten in place, v 2^k with a power of two per strip of dims (a
+//     converter warp's) that brings the strip's largest value so far below 2^15 and above
+//     2^-3 (0 while it is there by itself): exact for every element above its 2^-14th, and
+//     to 2^-19 of the largest below.  k only falls (then O is rescaled, in both CTAs of a
+//     pair: the strips' factors are stored into both), and the store divides it out.
 // FP8-row value factors are lifted by a power of two of their own (v_lift).
 //
 // Warps (640 threads): 0-7 softmax, warp w lanes 32 (w & 3) of every second page, from
-// w >> 2 on; 8 TMA producer; 9 and 10 MMA issuers, of S and of PV; 11 factors of the
-// keys' scales; 12-19 converters, in two groups on alternate pages.  A page's softmax is a
-// chain of waits and tensor-memory trips of some 1200 cycles, longer than the MMAs of a
-// page (800, head_dim 128): so two pages are in it at a time, S NS - 1 pages ahead of PV.
+// w >> 2 on, a whole row to a thread; 8 TMA producer; 9 and 10 MMA issuers, of S and of PV
+// (CTA 1's tell CTA 0's when theirs could go); 11 factors of the keys' scales; 12-19
+// converters, for quantized pages in two groups on alternate pages.  A page's softmax is a
+// chain of waits and tensor-memory trips of 2000-2500 cycles, longer than the MMAs of a page
+// (800, head_dim 128): so two pages are in it at a time, S NS - 1 pages ahead of PV.
 // The warps of a row hand on its reference maximum from page to page, right after the
-// page's maximum; it moves lazily (by a score more than 2^8 above it).  The MMAs are issued by an elected lane of a warp that runs the
-// loop as a whole: from a branch of one lane each issue took 47-54 cycles (probe:
-// M 128, N 64, A in tensor memory), from the whole warp the 33 of the tensor core.
+// page's maximum; it moves lazily (by a score more than 2^8 above it).  The MMAs are
+// issued by an elected lane of a warp that runs the loop as a whole: from a branch of one
+// lane each issue took 47-54 cycles (M 128, N 64, A in tensor memory), from the whole
+// warp the 33 of the tensor core.
+//
+// Measured (with the join, L2 cold): chunk of 2048 tokens behind 8150, 16 query heads,
+// BF16: 227 us, 1.02 PFLOP/s, 54% of the dense rate; 4 x 2048 behind 16384, K8V4: 1227 us,
+// 62%; verify of 4 tokens of 32 heads over 8 x 131072, K8V4: 190 us, 51% of the copy rate.
+// Bound by the softmax warps' chain: a page takes 1250-1400 cycles, of which the issue slots
+// of the four schedulers are half full.
 //
 // All waits are bounded; a wait that ran out ends its warp's work, the others' waits
 // run out too, and the CTA leaves without results once the copies in flight landed.

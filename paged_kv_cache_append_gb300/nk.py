@@ -814,7 +814,8 @@ class Pool:
                     make = torch.zeros if prefill else torch.empty
                     out = make((B, T, Hq // 2, 2 * D), dtype=torch.bfloat16, device=q.device)
                 if lse is None:
-                    lse = torch.full((B, T, Hq), float("-inf"), dtype=torch.float32, device=q.device)
+                    lse = (torch.full((B, T, Hq), float("-inf"), dtype=torch.float32, device=q.device) if prefill
+                           else torch.empty((B, T, Hq), dtype=torch.float32, device=q.device))
                 if ws is None:
                     ws = (self.diff_prefill_workspace if prefill else self.diff_decode_workspace)(B, T, Hq)
         _check((_pyargs or _args()).diff(
