@@ -103,35 +103,36 @@ __global__ void __launch_bounds__((DiffJoinCfg<D, ROWS>::THREADS)) diff_tile_joi
           ahead[map][s][k] = __ldcs(src[map] + (static_cast<int64_t>(s) * cg * Cfg::C4 + sl * V + k) * 128);
   }
 
-  // ---- weights: a warp per row -----------------------------------------------------------
-  for (int wr = warp; wr < ROWS; wr += NWARP) {
-    const int x = r0 + wr;
-    if (!there(x)) continue;
-    const int head = pair * a.G + x % a.G;
-    const int64_t bt = static_cast<int64_t>(b) * a.T + token_of(x);
+  // ---- weights: LP lanes per (map, row), every one at once --------------------------------
+  {
+    constexpr int LP = Cfg::THREADS / (2 * ROWS);
+    static_assert(LP >= 1 && LP <= 32 && (LP & (LP - 1)) == 0, "lanes of a (map, row)");
+    const int sub = tid % LP, map = tid / LP / ROWS, wr = tid / LP % ROWS, x = r0 + wr;
+    const int pieces = there(x) ? (map ? np[1] : np[0]) : 0;
+    const float2* ml = a.ws_ml + (map ? slot0[1] : slot0[0]) * 128 + (BOTH ? 64 * map : 0) + x;
+    float M = -INFINITY, L = 0.f;
+    float2 first = make_float2(-INFINITY, 0.f);
+    for (int s = sub; s < pieces; s += LP) {
+      const float2 v = ml[static_cast<int64_t>(s) * cg * 128];
+      if (s < LP) first = v;
+      M = fmaxf(M, v.x);
+    }
 #pragma unroll
-    for (int map = 0; map < 2; ++map) {
-      const float2* ml = a.ws_ml + slot0[map] * 128 + (BOTH ? 64 * map : 0) + x;
-      float M = -INFINITY, L = 0.f;
-      float2 first = make_float2(-INFINITY, 0.f);
-      for (int s = lane; s < np[map]; s += 32) {
-        const float2 v = ml[static_cast<int64_t>(s) * cg * 128];
-        if (s < 32) first = v;
-        M = fmaxf(M, v.x);
-      }
+    for (int off = LP / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    for (int s = sub; s < pieces; s += LP) {
+      const float2 v = s < LP ? first : ml[static_cast<int64_t>(s) * cg * 128];
+      const float e = v.y == 0.f ? 0.f : ex2(v.x - M);  // a piece that saw no key weighs nothing
+      s_w[map][wr][s] = e;
+      L += e * v.y;
+    }
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-      for (int s = lane; s < np[map]; s += 32) {
-        const float2 v = s < 32 ? first : ml[static_cast<int64_t>(s) * cg * 128];
-        const float e = v.y == 0.f ? 0.f : ex2(v.x - M);  // a piece that saw no key weighs nothing
-        s_w[map][wr][s] = e;
-        L += e * v.y;
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    for (int off = LP / 2; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    if (pieces > 0) {
+      const int head = pair * a.G + x % a.G;
+      const int64_t bt = static_cast<int64_t>(b) * a.T + token_of(x);
       const float f = L == 0.f ? 0.f : (map ? -a.o.lambda[bt * a.o.lambda_stride + head] : 1.f) / L;
-      for (int s = lane; s < np[map]; s += 32) s_w[map][wr][s] *= f;
-      if (a.o.lse && lane == 0)
+      for (int s = sub; s < pieces; s += LP) s_w[map][wr][s] *= f;
+      if (a.o.lse && sub == 0)
         a.o.lse[bt * a.Hq + 2 * head + map] = L == 0.f ? -INFINITY : (M + log2f(L)) * kDiffLn2;
     }
   }
