@@ -38,7 +38,7 @@ template <int D, int ROWS, bool BOTH>
 __global__ void __launch_bounds__((DiffJoinCfg<D, ROWS>::THREADS)) diff_tile_join_kernel(DiffTileJoinArgs a) {
   using Cfg = DiffJoinCfg<D, ROWS>;
   constexpr int SL = Cfg::SL, V = Cfg::V, NWARP = Cfg::THREADS / 32;
-  constexpr int AHEAD = BOTH ? 8 : 0;  // pieces that are read ahead (chunks have their V slices in flight)
+  constexpr int AHEAD = BOTH ? 8 : ROWS == 32 ? 0 : 2;  // pieces that are read ahead (32 rows have V slices in flight)
   __shared__ DiffChunkRows s_rows;
   __shared__ int64_t s_slot[2];
   __shared__ int s_np[2];

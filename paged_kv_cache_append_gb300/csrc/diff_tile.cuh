@@ -499,6 +499,15 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     else tc::commit(bar);
   };
   const auto wait = [&](uint64_t* bar, int use) { return mbar_wait_bounded(bar, use & 1, a.status); };
+  // Two or three at once: a wait on a complete barrier is mostly its latency.
+  const auto wait2 = [&](uint64_t* p, int up, uint64_t* q, int uq) {
+    const bool x = mbar_try_wait(p, up & 1), y = mbar_try_wait(q, uq & 1);
+    return (x & y) || (wait(p, up) && wait(q, uq));
+  };
+  const auto wait3 = [&](uint64_t* p, int up, uint64_t* q, int uq, uint64_t* r, int ur) {
+    const bool x = mbar_try_wait(p, up & 1), y = mbar_try_wait(q, uq & 1), z = mbar_try_wait(r, ur & 1);
+    return (x & y & z) || (wait(p, up) && wait(q, uq) && wait(r, ur));
+  };
 
   if (warp >= Cfg::NSOFT && warp < Cfg::NSOFT + 4) {
    fewer_registers<Cfg::R_MISC>();
@@ -608,9 +617,12 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
      for (int j = base; j < base + w.n; ++j) {
       const int ring = Cfg::K_RAW ? NRK : NK, ks = j % ring, sb = j % NS;
       const uint32_t s_at = tmem + Cfg::COL_S + 64 * sb;
-      if (j >= NS && rank == 0) ok = ok && wait(&o_done[sb], j / NS - 1);  // P of the page before in this buffer was read
-      ok = ok && wait(Cfg::K_RAW ? &rk_full[ks] : &k_full[ks], j / ring);
-      if (CG == 2 && rank == 0) ok = ok && wait(&peer_k[ks], j / ring);
+      // the operand, here and in the other CTA; P of the page before in this buffer was read
+      uint64_t* kb = Cfg::K_RAW ? &rk_full[ks] : &k_full[ks];
+      if (rank != 0 || (CG == 1 && j < NS)) ok = ok && wait(kb, j / ring);
+      else if (CG == 1) ok = ok && wait2(kb, j / ring, &o_done[sb], j / NS - 1);
+      else if (j < NS) ok = ok && wait2(kb, j / ring, &peer_k[ks], j / ring);
+      else ok = ok && wait3(kb, j / ring, &peer_k[ks], j / ring, &o_done[sb], j / NS - 1);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::fence_after();
       if (rank != 0) {  // CTA 0 issues for both
@@ -656,8 +668,8 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
      if (piece++ > 0) ok = ok && wait(o_free, piece - 2);  // the piece before is stored
      for (int j = base; j < base + w.n; ++j) {
       const int vs = j % NV, sb = j % NS;
-      ok = ok && wait(&v_full[vs], j / NV) && wait(&p_full[sb], j / NS);
-      if (CG == 2 && rank == 0) ok = ok && wait(&peer_v[sb], j / NS);
+      if (CG == 2 && rank == 0) ok = ok && wait3(&v_full[vs], j / NV, &p_full[sb], j / NS, &peer_v[sb], j / NS);
+      else ok = ok && wait2(&v_full[vs], j / NV, &p_full[sb], j / NS);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::fence_after();
       if (rank != 0) {
@@ -779,8 +791,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
         const int kvalid = F - 64 * (w.p_lo + i - base);
         if constexpr (!Cfg::K_RAW) {
           const int rk = i % NRK, ks = i % NK;
-          ok = wait(&rk_full[rk], i / NRK);
-          if (ok && i >= NK) ok = wait(&k_empty[ks], i / NK - 1);
+          ok = i >= NK ? wait2(&rk_full[rk], i / NRK, &k_empty[ks], i / NK - 1) : wait(&rk_full[rk], i / NRK);
           if (!ok) break;
 #pragma unroll
           for (int h = 0; h < KH; ++h)
@@ -795,8 +806,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
           }
         }
         const int rv = i % NRV, vs = i % NV;
-        ok = wait(&rv_full[rv], i / NRV);
-        if (ok && i >= NV) ok = wait(&v_empty[vs], i / NV - 1);
+        ok = i >= NV ? wait2(&rv_full[rv], i / NRV, &v_empty[vs], i / NV - 1) : wait(&rv_full[rv], i / NRV);
         if (!ok) break;
 #pragma unroll
         for (int v = 0; v < Cfg::VH; ++v)
@@ -996,8 +1006,15 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       const int kmax = valid ? pos - 64 * (w.p_lo + j - base) : -1;
       bool strips = false;  // BF16 values: a strip's k fell
       float most = 0.f;     // FP8-row V: the largest scale of the page
-      if constexpr (Cfg::HAS_F) live = live && wait(&f_full[fs], j / NF);
-      live = live && wait(&s_full[sb], j / NS);
+      // the scores, their factors, and the reference after the page before
+      uint64_t* xb = &x_full[4 * ((j - 1) & 1) + quad32];
+      if (j > base) {
+        if constexpr (Cfg::HAS_F) live = live && wait3(&f_full[fs], j / NF, &s_full[sb], j / NS, xb, (j - 1) >> 1);
+        else live = live && wait2(&s_full[sb], j / NS, xb, (j - 1) >> 1);
+      } else {
+        if constexpr (Cfg::HAS_F) live = live && wait2(&f_full[fs], j / NF, &s_full[sb], j / NS);
+        else live = live && wait(&s_full[sb], j / NS);
+      }
       if constexpr (Cfg::BF16) strips = lane < Cfg::STRIPS && sF[fs * 256 + 4 * lane] != 0.f;  // any lane's, below
       if constexpr (KV == KIND_FP8) {
         const float4 s4 = *reinterpret_cast<const float4*>(sF + fs * 256 + 128 + 4 * lane);  // both heads' 128 scales
@@ -1016,7 +1033,6 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       float m_was = -INFINITY;
       int k_was = kLift0, k_now = kLift0;
       if (j > base) {
-        live = live && wait(&x_full[4 * ((j - 1) & 1) + quad32], (j - 1) >> 1);
         const float2 x = sX[((j - 1) & 1) * 128 + m];
         m_was = x.x;
         if constexpr (KV == KIND_FP8) k_was = __float_as_int(x.y);
