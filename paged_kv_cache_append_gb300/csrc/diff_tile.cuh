@@ -42,9 +42,9 @@
 // FP8-row value factors are lifted by a power of two of their own (v_lift).
 //
 // Warps (640 threads): 0-7 softmax, warp w lanes 32 (w & 3) of every second page, from
-// w >> 2 on, a whole row to a thread; 8 TMA producer; 9 and 10 MMA issuers, of S and of PV
-// (CTA 1's tell CTA 0's when theirs could go); 11 factors of the keys' scales; 12-19
-// converters, for quantized pages in two groups on alternate pages.  A page's softmax is a
+// w >> 2 on, a whole row to a thread; 8 TMA producer; 9 MMA issuer (CTA 1's tells CTA 0's
+// when it could go); 10 idle (registers move by warpgroups); 11 factors of the keys'
+// scales; 12-19 converters, for quantized pages in two groups on alternate pages.  A page's softmax is a
 // chain of waits and tensor-memory trips of 2000-2500 cycles, longer than the MMAs of a page
 // (800, head_dim 128): so two pages are in it at a time, S NS - 1 pages ahead of PV.
 // The warps of a row hand on its reference maximum from page to page, right after the
@@ -196,7 +196,7 @@ struct DiffTileCfg {
   static constexpr int OFF_X = OFF_F + NF * 1024;  // [2][128] references, [2][128] final (reference, sum)
   static constexpr int OFF_ROWS = OFF_X + 4096 + 256;  // [4][16] lifts of the BF16 strips
   static constexpr int OFF_BAR = OFF_ROWS + 256;
-  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NRK + 2 * NRV + 2 * NF + 4 * NS + 3 + 8 + (K_RAW ? NRK : NK);
+  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NRK + 2 * NRV + 2 * NF + 4 * NS + 2 + 8 + (K_RAW ? NRK : NK);
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 64 + 1024;
   static constexpr uint32_t COL_S = 0, COL_Q = 64 * NS, COL_O = 256;
   static_assert(COL_Q + KH * (D / 2) <= COL_O, "tensor memory");
@@ -406,8 +406,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
   uint64_t* o_done = p_full + NS;   // [NS] PV of the page in S buffer i complete
   uint64_t* q_ready = o_done + NS;
   uint64_t* drain = q_ready + 1;  // every MMA complete
-  uint64_t* o_free = drain + 1;   // O of a piece was read
-  uint64_t* peer_v = o_free + 1;  // [NS] of CTA 0: CTA 1 is ready for PV
+  uint64_t* peer_v = drain + 1;  // [NS] of CTA 0: CTA 1 is ready for PV
   uint64_t* peer_k = peer_v + NS;  // [ring] and for S
   uint64_t* x_full = peer_k + (Cfg::K_RAW ? NRK : NK);  // [2][4] the references of 32 rows after a page are there
   uint32_t* tslot = reinterpret_cast<uint32_t*>(x_full + 8);
@@ -447,8 +446,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     }
     mbar_init(q_ready, Cfg::NSOFT);
     for (int i = 0; i < (Cfg::K_RAW ? NRK : NK); ++i) mbar_init(&peer_k[i], 1);
-    mbar_init(drain, 2);
-    mbar_init(o_free, Cfg::NSOFT);
+    mbar_init(drain, 1);
     for (int i = 0; i < 8; ++i) mbar_init(&x_full[i], 1);
     fence_barrier_init();
     prefetch_tmap(&tmk);
@@ -582,8 +580,9 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
        for (int i = base; i < base + w.n; ++i) {
         const int rk = i % NRK, rv = i % NRV, fs = i % NF, kvalid = F - 64 * (w.p_lo + i - base);
         float* slot = sF + fs * 256;
-        if constexpr (Cfg::KEY_FAC) ok = wait(&rk_full[rk], i / NRK);
-        if constexpr (Cfg::VAL_FAC) ok = ok && wait(&rv_full[rv], i / NRV);
+        if constexpr (Cfg::KEY_FAC && Cfg::VAL_FAC) ok = wait2(&rk_full[rk], i / NRK, &rv_full[rv], i / NRV);
+        else if constexpr (Cfg::KEY_FAC) ok = wait(&rk_full[rk], i / NRK);
+        else ok = wait(&rv_full[rv], i / NRV);
         if (ok && i >= NF) ok = wait(&f_empty[fs], i / NF - 1);
         if (!ok) break;
 #pragma unroll
@@ -608,90 +607,83 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       } while (ok && next(w, base));
     }
   } else if (warp == Cfg::NSOFT + 1) {
-    // ------------------------------ MMA issuer: S ------------------------------
+    // ------------------------------ MMA issuer ---------------------------------
     bool ok = true;
     DiffWork w = first;
     int base = 0, piece = 0;
     do {
-     ok = ok && wait(q_ready, piece++);
-     for (int j = base; j < base + w.n; ++j) {
-      const int ring = Cfg::K_RAW ? NRK : NK, ks = j % ring, sb = j % NS;
-      const uint32_t s_at = tmem + Cfg::COL_S + 64 * sb;
-      // the operand, here and in the other CTA; P of the page before in this buffer was read
-      uint64_t* kb = Cfg::K_RAW ? &rk_full[ks] : &k_full[ks];
-      if (rank != 0 || (CG == 1 && j < NS)) ok = ok && wait(kb, j / ring);
-      else if (CG == 1) ok = ok && wait2(kb, j / ring, &o_done[sb], j / NS - 1);
-      else if (j < NS) ok = ok && wait2(kb, j / ring, &peer_k[ks], j / ring);
-      else ok = ok && wait3(kb, j / ring, &peer_k[ks], j / ring, &o_done[sb], j / NS - 1);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc::fence_after();
-      if (rank != 0) {  // CTA 0 issues for both
-        tc::fence_before();
-        if (lane == 0) peer_arrive(&peer_k[ks], 0);
-      } else if (elect_one()) {
+     ok = ok && wait(q_ready, piece++);  // and O of the piece before is stored: the same warps, in that order
+     for (int i = 0; i < w.n + NS - 1; ++i) {  // S(i), then O += P V of page i - NS + 1
+      if (i < w.n) {
+        const int j = base + i;
+        const int ring = Cfg::K_RAW ? NRK : NK, ks = j % ring, sb = j % NS;
+        const uint32_t s_at = tmem + Cfg::COL_S + 64 * sb;
+        // the operand, here and in the other CTA; P of the page before in this buffer is read
+        // by MMAs issued before
+        uint64_t* kb = Cfg::K_RAW ? &rk_full[ks] : &k_full[ks];
+        if (CG == 2 && rank == 0) ok = ok && wait2(kb, j / ring, &peer_k[ks], j / ring);
+        else ok = ok && wait(kb, j / ring);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc::fence_after();
+        if (rank != 0) {  // CTA 0 issues for both
+          tc::fence_before();
+          if (lane == 0) peer_arrive(&peer_k[ks], 0);
+        } else if (elect_one()) {
 #pragma unroll
-        for (int h = 0; h < KH; ++h) {
-          const uint32_t qa = tmem + Cfg::COL_Q + h * (D / 2);
+          for (int h = 0; h < KH; ++h) {
+            const uint32_t qa = tmem + Cfg::COL_Q + h * (D / 2);
 #pragma unroll
-          for (int part = 0; part < (Cfg::K_SPLIT || Cfg::K8MMA ? 2 : 1); ++part) {
-            const uint8_t* tile = Cfg::K_RAW ? sRK + ks * Cfg::RK_STAGE + h * Cfg::RK_HEAD
-                                             : sK + ks * Cfg::K_STAGE + h * Cfg::K_HEAD + part * Cfg::F16;
-            const uint64_t kd = tc::smem_desc(smem_u32(tile), 16, 1024);
-            if constexpr (Cfg::K8MMA) {  // q_hi, then q_lo, in D / 4 columns each
+            for (int part = 0; part < (Cfg::K_SPLIT || Cfg::K8MMA ? 2 : 1); ++part) {
+              const uint8_t* tile = Cfg::K_RAW ? sRK + ks * Cfg::RK_STAGE + h * Cfg::RK_HEAD
+                                               : sK + ks * Cfg::K_STAGE + h * Cfg::K_HEAD + part * Cfg::F16;
+              const uint64_t kd = tc::smem_desc(smem_u32(tile), 16, 1024);
+              if constexpr (Cfg::K8MMA) {  // q_hi, then q_lo, in D / 4 columns each
 #pragma unroll
-              for (int kk = 0; kk < D / 32; ++kk)
-                mma_f8(s_at, qa + part * (D / 4) + kk * 8,
-                              kd + static_cast<uint64_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), Cfg::ID_S,
-                              h > 0 || part > 0 || kk > 0);
-            } else {  // INT8-G64: Q k1^T - Q k2'^T
+                for (int kk = 0; kk < D / 32; ++kk)
+                  mma_f8(s_at, qa + part * (D / 4) + kk * 8,
+                                kd + static_cast<uint64_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), Cfg::ID_S,
+                                h > 0 || part > 0 || kk > 0);
+              } else {  // INT8-G64: Q k1^T - Q k2'^T
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                mma(s_at, qa + kk * 8, kd + static_cast<uint64_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
-                           part > 0 ? tc::idesc_negate_b(Cfg::ID_S) : Cfg::ID_S, h > 0 || part > 0 || kk > 0);
+                for (int kk = 0; kk < D / 16; ++kk)
+                  mma(s_at, qa + kk * 8, kd + static_cast<uint64_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
+                             part > 0 ? tc::idesc_negate_b(Cfg::ID_S) : Cfg::ID_S, h > 0 || part > 0 || kk > 0);
+              }
             }
           }
+          commit(&s_full[sb]);
+          commit(Cfg::K_RAW ? &rk_empty[ks] : &k_empty[ks]);
         }
-        commit(&s_full[sb]);
-        commit(Cfg::K_RAW ? &rk_empty[ks] : &k_empty[ks]);
+        __syncwarp();
       }
-      __syncwarp();
+      if (i >= NS - 1) {
+        const int j = base + i - (NS - 1);
+        const int vs = j % NV, sb = j % NS;
+        if (CG == 2 && rank == 0) ok = ok && wait3(&v_full[vs], j / NV, &p_full[sb], j / NS, &peer_v[sb], j / NS);
+        else ok = ok && wait2(&v_full[vs], j / NV, &p_full[sb], j / NS);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc::fence_after();
+        if (rank != 0) {
+          tc::fence_before();
+          if (lane == 0) peer_arrive(&peer_v[sb], 0);
+        } else if (elect_one()) {
+#pragma unroll
+          for (int v = 0; v < (Cfg::VAL_FAC ? 2 : 1); ++v) {
+            const uint64_t vd = tc::smem_desc(smem_u32(sV + vs * Cfg::V_STAGE + v * Cfg::VPART), 8192, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma(tmem + Cfg::COL_O + v * D, tmem + Cfg::COL_S + 64 * sb + 32 * (kk >> 1) + 16 * v + 8 * (kk & 1),
+                         vd + static_cast<uint64_t>((kk * 2048) >> 4), Cfg::ID_O, (j > base || kk > 0));
+          }
+          commit(&o_done[sb]);
+          commit(&v_empty[vs]);
+        }
+        __syncwarp();
+      }
      }
     } while (__all_sync(0xffffffffu, ok) && next(w, base));
     __syncwarp();
     if (rank == 0 && elect_one()) commit(drain);  // arrives once every MMA issued above has completed
-  } else if (warp == Cfg::NSOFT + 2) {
-    // ------------------------------ MMA issuer: O += P V -----------------------
-    bool ok = true;
-    DiffWork w = first;
-    int base = 0, piece = 0;
-    do {
-     if (piece++ > 0) ok = ok && wait(o_free, piece - 2);  // the piece before is stored
-     for (int j = base; j < base + w.n; ++j) {
-      const int vs = j % NV, sb = j % NS;
-      if (CG == 2 && rank == 0) ok = ok && wait3(&v_full[vs], j / NV, &p_full[sb], j / NS, &peer_v[sb], j / NS);
-      else ok = ok && wait2(&v_full[vs], j / NV, &p_full[sb], j / NS);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc::fence_after();
-      if (rank != 0) {
-        tc::fence_before();
-        if (lane == 0) peer_arrive(&peer_v[sb], 0);
-      } else if (elect_one()) {
-#pragma unroll
-        for (int v = 0; v < (Cfg::VAL_FAC ? 2 : 1); ++v) {
-          const uint64_t vd = tc::smem_desc(smem_u32(sV + vs * Cfg::V_STAGE + v * Cfg::VPART), 8192, 1024);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma(tmem + Cfg::COL_O + v * D, tmem + Cfg::COL_S + 64 * sb + 32 * (kk >> 1) + 16 * v + 8 * (kk & 1),
-                       vd + static_cast<uint64_t>((kk * 2048) >> 4), Cfg::ID_O, (j > base || kk > 0));
-        }
-        commit(&o_done[sb]);
-        commit(&v_empty[vs]);
-      }
-      __syncwarp();
-     }
-    } while (__all_sync(0xffffffffu, ok) && next(w, base));
-    __syncwarp();
-    if (rank == 0 && elect_one()) commit(drain);
    }
   } else if (warp >= Cfg::NSOFT + 4) {
     fewer_registers<Cfg::R_CONV>();
@@ -716,7 +708,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
        int k = 0;
        for (int i = 0; ok && i < w.n; ++i) {
         const int j = base + i, vs = j % NV, fs = j % NF, kvalid = F - 64 * (w.p_lo + i);
-        ok = wait(&rv_full[vs], j / NV);
+        ok = j >= NF ? wait2(&rv_full[vs], j / NV, &f_empty[fs], j / NF - 1) : wait(&rv_full[vs], j / NV);
         if (!ok) break;
         uint8_t* tile = sV + vs * Cfg::V_STAGE + blk;
         uint4 v[St::UNITS];
@@ -760,8 +752,6 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
             *reinterpret_cast<uint4*>(tile + off0 + u * St::ROWS * 128) =
                 make_uint4(bf16x2_lift(v[u].x, f), bf16x2_lift(v[u].y, f), bf16x2_lift(v[u].z, f), bf16x2_lift(v[u].w, f));
         }
-        if (j >= NF) ok = wait(&f_empty[fs], j / NF - 1);
-        if (!ok) break;
         if (lane == 0) {
           // of a strip: whether its k fell, O's factor for that, 2^-k.  O of the pair's other
           // CTA has these dims too.
@@ -1122,8 +1112,6 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       }
     }
     tc::fence_before();
-    __syncwarp();
-    if (lane == 0) q_arrive(o_free);
     } while (live && next(w, base));
     if (CG == 2 && live && tid == 0) {  // the last commits that nobody else waits for have arrived
       constexpr int ring = Cfg::K_RAW ? NRK : NK;
