@@ -5,7 +5,9 @@
 // read 16 ROWS consecutive bytes of a partial (rows are its innermost index), a thread
 // owns V neighbouring 4-dim slices of its row.  Which partials a tile has follows
 // from the lengths, which are read before the wait for the partials.  Every partial is
-// read once and the output written once: bound by L2, after a chain of three loads.
+// read once and the output written once: bound by L2, after a chain of three loads (2048
+// tokens of 8 heads, 52 MB of partials: 21 us with cold caches; with the weights of four
+// rows one after the other in a warp, 29).
 #pragma once
 
 #include <type_traits>
@@ -196,7 +198,8 @@ __global__ void __launch_bounds__((DiffJoinCfg<D, ROWS>::THREADS)) diff_tile_joi
 }
 
 // Rows of a CTA: 32 (512 bytes of a partial at a time, one plan for them) where that
-// still makes a CTA per SM, else 8; a decode, of at most 64 rows, 4 or 8.
+// still makes a CTA per SM, else 8; a decode, of at most 64 rows, 4 or 8.  With 8 rows and
+// with 32, us: 4 x 2048 tokens of 8 heads 85 and 68, 501 tokens of 2 heads 8 and 18.
 template <bool BOTH>
 inline cudaError_t launch_diff_tile_join(int D, int sms, const DiffTileJoinArgs& j, cudaStream_t s) {
   const auto blocks = [&](int rows) {

@@ -13,7 +13,7 @@
 // of its rank (FP8-row and INT8-G64 values: 64 of the dims of both heads, since each head
 // has its own P; at head_dim 64 that half would be less than a swizzle atom, so there a
 // CTA works alone, M 128).  With one CTA to an MMA a BF16 chunk read its pages at 8.3
-// TB/s from L2, which bound it: 8192 tokens behind 0, 731 us, 490 in pairs.
+// TB/s from L2, which bound it: 8192 tokens behind 0, 731 us, 500 in pairs.
 // The grid is one cluster for every two SMs; the line of all tiles' pages is cut into equal
 // parts (diff_chunk_first), so that a CTA sets up once and no wave is short: with a CTA
 // to a tile and range, each started and drained for 10 us.
@@ -44,9 +44,12 @@
 // Warps (640 threads): 0-7 softmax, warp w lanes 32 (w & 3) of every second page, from
 // w >> 2 on, a whole row to a thread; 8 TMA producer; 9 MMA issuer (CTA 1's tells CTA 0's
 // when it could go); 10 idle (registers move by warpgroups); 11 factors of the keys'
-// scales; 12-19 converters, for quantized pages in two groups on alternate pages.  A page's softmax is a
-// chain of waits and tensor-memory trips of 2000-2500 cycles, longer than the MMAs of a page
-// (800, head_dim 128): so two pages are in it at a time, S NS - 1 pages ahead of PV.
+// scales; 12-19 converters, for quantized pages in two groups on alternate pages.  A
+// page's softmax is a chain of waits and tensor-memory trips of 1600-2000 cycles, longer
+// than the MMAs of a page (800, head_dim 128): so two pages are in it at a time, S NS - 1
+// pages ahead of PV.  A wait on a complete barrier takes 120-250 cycles beside 19 busy
+// warps, most of it latency: a role's barriers of a page are tried together (K8V4 batch
+// below: 1196 us one by one, 1104 together).
 // The warps of a row hand on its reference maximum from page to page, right after the
 // page's maximum; it moves lazily (by a score more than 2^8 above it).  The MMAs are
 // issued by an elected lane of a warp that runs the loop as a whole: from a branch of one
@@ -54,10 +57,12 @@
 // warp the 33 of the tensor core.
 //
 // Measured (with the join, L2 cold): chunk of 2048 tokens behind 8150, 16 query heads,
-// BF16: 227 us, 1.02 PFLOP/s, 54% of the dense rate; 4 x 2048 behind 16384, K8V4: 1227 us,
-// 62%; verify of 4 tokens of 32 heads over 8 x 131072, K8V4: 190 us, 51% of the copy rate.
-// Bound by the softmax warps' chain: a page takes 1250-1400 cycles, of which the issue slots
-// of the four schedulers are half full.
+// BF16: 209 us, 58% of the dense rate; 4 x 2048 behind 16384, K8V4: 1133 us, 67%; verify
+// of 4 tokens of 32 heads over 8 x 131072, K8V4: 173 us, 56% of the copy rate.  A page takes
+// 1050 (K8V4) to 1350 cycles (BF16): what bounds it is the loop from S over the softmax to
+// the PV that frees S's buffer, three pages long; two warps for S and PV, which shorten that
+// of the issue, gained as much for BF16 as they lost for the verify.  A piece of a tile costs
+// 7 us beside its pages (queries, first scores, partial).
 //
 // All waits are bounded; a wait that ran out ends its warp's work, the others' waits
 // run out too, and the CTA leaves without results once the copies in flight landed.
@@ -97,8 +102,10 @@ constexpr int diff_chunk_group(int kind_v, int D) { return (kind_v == KIND_FP8 |
 // a tile's pages after kDiffTileCost units for its start and end (queries, first scores,
 // partial), and cluster c of n takes the units [c W / n, (c + 1) W / n): a tile that crosses
 // a boundary has a partial from each of its clusters, numbered tile + cluster.  n is at
-// most one CTA per SM and leaves each at least kDiffLeastUnits.
-constexpr int kDiffTileCost = 6, kDiffLeastUnits = 5;
+// most one CTA per SM and leaves each at least kDiffLeastUnits.  8192 tokens behind 0
+// (many short tiles), us, by a tile's cost: 532 with 0, 434 with 6, 421 with 12, 434 with 18;
+// 2 x 64 tokens behind 1000, by the least units: 26 with 5, 31 with 16, 34 with 24.
+constexpr int kDiffTileCost = 12, kDiffLeastUnits = 5;
 
 // Units of tiles [0, upto) of a row (a warp).
 __device__ __forceinline__ int64_t diff_tile_units(int prefix, int chunk, int TQ, int upto) {

@@ -3,9 +3,9 @@
 Tolerances, derived: every term p v of a map's sum is off by at most c of its
 size, a = sum p |v| over both maps, and oracle.differential.tolerance carries
 that through the norm to the output and its one rounding to bf16 (2^-8).
- * weights: f16 2^-11 (BF16 pages: two terms, 2^-16, in the decode; bf16, 2^-8,
-   in the prefill);  values: f16 products of INT8-G64 and FP8-row, 2^-11 (the
-   prefill keeps FP8-row values exact);  so c0 = 2^-10, or 2^-8 for BF16 prefill;
+ * weights: f16 2^-11 (BF16 pages in the decode: two terms, 2^-16);  values: f16
+   products of INT8-G64 and FP8-row, 2^-11 (the tensor-core form keeps FP8-row
+   values exactly, BF16 ones to 2^-19 of their strip's largest);  so c0 = 2^-10;
  * the decode takes q exactly (f16 or bf16); the prefill over FP8-row keys of
    head_dim 128 takes q in two E4M3 terms, each element to 2^-17 of the largest:
    with |q| <= 4.5, sum |k| <= 128 and a scale of 1/11 a score is off by at most
@@ -13,8 +13,7 @@ that through the norm to the output and its one rounding to bf16 (2^-8).
    too: 8e-4 more;
  * fp32 sums of D products, the exponential (2 ulp) and the reference's fold
    (|s| 2^-24): below 1e-4 with |s| < 30 and D <= 128.
-So c = 2^-10 + 1e-4 (decode), the same + 8e-4 (prefill, quantized), 2^-8 + 1e-4
-(prefill, BF16); lse within 1e-3.
+So c = 2^-10 + 1e-4 (decode), the same + 8e-4 (prefill); lse within 1e-3.
 """
 
 import math
@@ -112,7 +111,7 @@ class Batch:
         if c is None:
             c = 2.0 ** -10 + 1e-4
             if self.chunk is not None:
-                c = 2.0 ** -8 + 1e-4 if self.profile == "bf16" else 2.0 ** -10 + 9e-4
+                c = 2.0 ** -10 + 9e-4
         w = None if self.w is None else self.w.double().numpy()
         for b, (o, l, raw, a) in enumerate(self.reference()):
             n = o.shape[0]
