@@ -57,7 +57,7 @@
 // warp the 33 of the tensor core.
 //
 // Measured (with the join, L2 cold): chunk of 2048 tokens behind 8150, 16 query heads,
-// BF16: 209 us, 58% of the dense rate; 4 x 2048 behind 16384, K8V4: 1133 us, 67%; verify
+// BF16: 209 us, 58% of the dense rate; 4 x 2048 behind 16384, K8V4: 1125 us, 68%; verify
 // of 4 tokens of 32 heads over 8 x 131072, K8V4: 173 us, 56% of the copy rate.  A page takes
 // 1050 (K8V4) to 1350 cycles (BF16): what bounds it is the loop from S over the softmax to
 // the PV that frees S's buffer, three pages long; two warps for S and PV, which shorten that
