@@ -150,6 +150,20 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   return true;
 }
 
+// Barrier `id` of `threads` threads (whole warps): in all of them, whether `x` holds in each.  Warps that
+// meet at a barrier in a loop have to leave it together: one that stayed behind would wait for ever.
+__device__ __forceinline__ bool barrier_and(uint32_t id, uint32_t threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %3, 0;\n"
+      " barrier.cta.red.and.pred p, %1, %2, q;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
+}
+
 // ------------------------------------------------------------ async copies
 
 // L2 prefetch of `bytes` (a multiple of 16) at a 16-byte aligned address.  L2

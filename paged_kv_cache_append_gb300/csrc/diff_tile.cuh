@@ -1086,7 +1086,8 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     tc::fence_after();
     const float m_eff = m_own == -INFINITY ? -INFINITY : m_own - static_cast<float>(k_own);
     sX[256 + 128 * half + m] = make_float2(m_eff, l);
-    asm volatile("bar.sync %0, 64;" ::"r"(1 + quad32) : "memory");  // the two warps of these rows
+    // the two warps of these rows, which meet here once a piece: both go on to the next or neither
+    live = barrier_and(1 + quad32, 64, live);
     const int64_t part = BOTH ? static_cast<int64_t>(pair) * a.ctas + blockIdx.x
                               : ((static_cast<int64_t>(w.b) * a.H + w.pm) * a.tiles + w.qt + blockIdx.x / CG) * CG + rank;
     if (live && valid && half == 0) {  // the sums, under the reference after the last page

@@ -38,3 +38,17 @@ def test_bounded_wait_rejects_limits_outside_the_range():
         with pytest.raises(nk.NkError) as e:
             nk.nk_selftest_bounded_wait(bad)
         assert e.value.code == -1
+
+
+def test_warps_that_share_work_stop_together():
+    """A warp whose wait completed leaves the loop over pieces with the one whose wait ran out, at the barrier of that
+    very piece: had it gone on, waited would be -1."""
+    nk.load()
+    s = torch.cuda.current_stream()
+    nk.nk_status_read(clear=True, stream=s.cuda_stream)
+    for limit_us in (1, 50, 1000):
+        waited = torch.zeros(1, dtype=torch.int64, device="cuda")
+        nk.nk_selftest_bounded_wait(limit_us, waited.data_ptr(), s.cuda_stream)
+        s.synchronize()
+        assert nk.nk_status_read(clear=True, stream=s.cuda_stream) == nk.STATUS_TIMEOUT
+        assert int(waited.item()) >= 1000 * limit_us
