@@ -692,8 +692,9 @@ int nk_status_read(int32_t* status, int32_t clear, void* stream);
  * `limit_us` microseconds (1 .. 1000000).  Afterwards NK_STATUS_TIMEOUT is
  * set in the status word of the current device (nk_status_read), and, when
  * `waited_ns` is a device pointer, it receives the nanoseconds the wait took
- * (-1 if the wait had completed, or if a second warp whose own wait completed
- * did not stop with this one, as warps that share a piece of work have to).  Asynchronous; errors:
+ * (-1 if the wait had completed, or if other lanes of its warp, or a second
+ * warp, whose own waits completed did not stop with it, as lanes of a warp and
+ * warps that share a piece of work have to).  Asynchronous; errors:
  * NK_ERR_INVALID_ARG for a limit outside the range, NK_ERR_CUDA on a launch
  * failure. */
 int nk_selftest_bounded_wait(int32_t limit_us, long long* waited_ns, void* stream);

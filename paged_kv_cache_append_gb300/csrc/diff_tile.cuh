@@ -64,8 +64,9 @@
 // of the issue, gained as much for BF16 as they lost for the verify.  A piece of a tile costs
 // 7 us beside its pages (queries, first scores, partial).
 //
-// All waits are bounded; a wait that ran out ends its warp's work, the others' waits
-// run out too, and the CTA leaves without results once the copies in flight landed.
+// All waits are bounded; a wait that ran out ends its warp's work (for all lanes, and for
+// both softmax warps of a row), the others' waits run out too, and the CTA leaves without
+// results once the copies in flight landed.
 #pragma once
 
 #include "diff.cuh"
@@ -591,6 +592,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
         else if constexpr (Cfg::KEY_FAC) ok = wait(&rk_full[rk], i / NRK);
         else ok = wait(&rv_full[rv], i / NRV);
         if (ok && i >= NF) ok = wait(&f_empty[fs], i / NF - 1);
+        ok = __all_sync(0xffffffffu, ok);  // the warp stops as one
         if (!ok) break;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -695,6 +697,10 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
   } else if (warp >= Cfg::NSOFT + 4) {
     fewer_registers<Cfg::R_CONV>();
     const int ct = tid - 32 * (Cfg::NSOFT + 4);
+    // Lanes measure the time of a wait each for itself, and the warp stops as one, by a vote at
+    // the end of a page: lanes that left alone would be missed at its next collective
+    // instruction.  (INT8-G64, with a vote there and without any: verify 140 us and 132, chunk of
+    // 2048 behind 8192 363 and 373; the other page types the same.)
     bool ok = true;
     if constexpr (Cfg::BF16) {
       // ------------- converters of BF16 values: a strip of dims per warp -----------
@@ -716,7 +722,6 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
        for (int i = 0; ok && i < w.n; ++i) {
         const int j = base + i, vs = j % NV, fs = j % NF, kvalid = F - 64 * (w.p_lo + i);
         ok = j >= NF ? wait2(&rv_full[vs], j / NV, &f_empty[fs], j / NF - 1) : wait(&rv_full[vs], j / NV);
-        if (!ok) break;
         uint8_t* tile = sV + vs * Cfg::V_STAGE + blk;
         uint4 v[St::UNITS];
 #pragma unroll
@@ -765,15 +770,17 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
           float4* slot = reinterpret_cast<float4*>(sF + fs * 256);
           const float4 x = make_float4(i > 0 && k != was ? 1.f : 0.f, pow2i(i > 0 ? max(k - was, -126) : 0), pow2i(-k), 0.f);
           slot[strip] = x;
-          if constexpr (CG == 2) peer_store(slot + strip, x, &f_full[fs], rank ^ 1);
+          if constexpr (CG == 2)
+            if (ok) peer_store(slot + strip, x, &f_full[fs], rank ^ 1);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) {
+        if (ok && lane == 0) {
           if (CG == 2 && cw == 0) mbar_arrive_expect_tx(&f_full[fs], 16 * Cfg::NCONV);  // and the other CTA's strips
           else q_arrive(&f_full[fs]);
           q_arrive(&v_full[vs]);
         }
+        ok = __all_sync(0xffffffffu, ok);
        }
       } while (ok && next(w, base));
     } else {
@@ -789,33 +796,36 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
         if constexpr (!Cfg::K_RAW) {
           const int rk = i % NRK, ks = i % NK;
           ok = i >= NK ? wait2(&rk_full[rk], i / NRK, &k_empty[ks], i / NK - 1) : wait(&rk_full[rk], i / NRK);
-          if (!ok) break;
+          if (ok) {
 #pragma unroll
-          for (int h = 0; h < KH; ++h)
-            convert_tile<KK, D, Cfg::K_RB, NCT, Cfg::K_SPLIT, Cfg::KR>(
-                sRK + rk * Cfg::RK_STAGE + h * Cfg::RK_HEAD, Cfg::RK_CODES + Cfg::KR * rank * Cfg::KSB,
-                sK + ks * Cfg::K_STAGE + h * Cfg::K_HEAD, gt, kvalid - Cfg::KR * rank);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            for (int h = 0; h < KH; ++h)
+              convert_tile<KK, D, Cfg::K_RB, NCT, Cfg::K_SPLIT, Cfg::KR>(
+                  sRK + rk * Cfg::RK_STAGE + h * Cfg::RK_HEAD, Cfg::RK_CODES + Cfg::KR * rank * Cfg::KSB,
+                  sK + ks * Cfg::K_STAGE + h * Cfg::K_HEAD, gt, kvalid - Cfg::KR * rank);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
           __syncwarp();
-          if (lane == 0) {
+          if (ok && lane == 0) {
             q_arrive(&rk_empty[rk]);
             q_arrive(&k_full[ks]);
           }
         }
         const int rv = i % NRV, vs = i % NV;
-        ok = i >= NV ? wait2(&rv_full[rv], i / NRV, &v_empty[vs], i / NV - 1) : wait(&rv_full[rv], i / NRV);
-        if (!ok) break;
+        ok = ok && (i >= NV ? wait2(&rv_full[rv], i / NRV, &v_empty[vs], i / NV - 1) : wait(&rv_full[rv], i / NRV));
+        if (ok) {
 #pragma unroll
-        for (int v = 0; v < Cfg::VH; ++v)
-          convert_tile<KV, D, Cfg::V_RB, NCT, false, 64, Cfg::V_HALF ? 4 : D / 16>(
-              sRV + rv * Cfg::RV_STAGE + v * Cfg::RV_HEAD, Cfg::RV_CODES, sV + vs * Cfg::V_STAGE + v * Cfg::VPART, gt,
-              kvalid, Cfg::V_HALF ? 4 * rank : 0);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          for (int v = 0; v < Cfg::VH; ++v)
+            convert_tile<KV, D, Cfg::V_RB, NCT, false, 64, Cfg::V_HALF ? 4 : D / 16>(
+                sRV + rv * Cfg::RV_STAGE + v * Cfg::RV_HEAD, Cfg::RV_CODES, sV + vs * Cfg::V_STAGE + v * Cfg::VPART, gt,
+                kvalid, Cfg::V_HALF ? 4 * rank : 0);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
         __syncwarp();
-        if (lane == 0) {
+        if (ok && lane == 0) {
           q_arrive(&rv_empty[rv]);
           q_arrive(&v_full[vs]);
         }
+        ok = __all_sync(0xffffffffu, ok);
        }
       } while (ok && next(w, base));
     }

@@ -3,10 +3,11 @@
 // after a wall-clock limit, record NK_STATUS_TIMEOUT, return) can be checked
 // on a GPU without any fault or hang.
 //
-// One warp waits on an mbarrier that expects two arrivals and gets one, so
-// the phase can never complete; no copy or other thread is involved.  The
-// wait gives up after `limit_us` microseconds and the kernel returns
-// normally: the context stays usable and the status word tells the host.
+// A lane waits on an mbarrier that expects two arrivals and gets one, so the
+// phase can never complete; no copy or other thread is involved.  The wait
+// gives up after `limit_us` microseconds and the kernel returns normally: the
+// context stays usable and the status word tells the host.  The other lanes of
+// its warp, whose waits complete, have to give up with it (mbar_wait_warp).
 // A second warp, whose wait completes at once, goes through pieces of work
 // with the first and has to leave the loop with it (barrier_and).
 #include "device.cuh"
@@ -17,7 +18,6 @@ namespace nk {
 __global__ void bounded_wait_selftest_kernel(int* status, uint64_t limit_ns, long long* waited_ns) {
   __shared__ __align__(8) uint64_t bar[2];
   __shared__ int pieces;
-  const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     mbar_init(&bar[0], 2);
     mbar_init(&bar[1], 1);
@@ -26,8 +26,9 @@ __global__ void bounded_wait_selftest_kernel(int* status, uint64_t limit_ns, lon
   }
   __syncthreads();
   const uint64_t t0 = globaltimer_ns();
-  const bool done = mbar_wait_bounded(&bar[warp], 0, status, limit_ns);
+  const bool done = mbar_wait_warp(&bar[threadIdx.x == 0 ? 0 : 1], 0, status, limit_ns);
   const uint64_t t1 = globaltimer_ns();
+  const bool any = __any_sync(0xffffffffu, done);
   bool live = done;
   int n = 0;
   do {
@@ -36,7 +37,7 @@ __global__ void bounded_wait_selftest_kernel(int* status, uint64_t limit_ns, lon
   } while (live && n < 4);
   if (threadIdx.x == 32) pieces = n;
   __syncthreads();
-  if (threadIdx.x == 0 && waited_ns) *waited_ns = done || pieces != 1 ? -1 : static_cast<long long>(t1 - t0);
+  if (threadIdx.x == 0 && waited_ns) *waited_ns = any || pieces != 1 ? -1 : static_cast<long long>(t1 - t0);
 }
 
 }  // namespace nk

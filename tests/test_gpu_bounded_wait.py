@@ -52,3 +52,15 @@ def test_warps_that_share_work_stop_together():
         s.synchronize()
         assert nk.nk_status_read(clear=True, stream=s.cuda_stream) == nk.STATUS_TIMEOUT
         assert int(waited.item()) >= 1000 * limit_us
+
+
+def test_lanes_of_a_warp_stop_together():
+    """One lane's wait runs out, the others' complete at once: none goes on (waited would be -1)."""
+    nk.load()
+    s = torch.cuda.current_stream()
+    nk.nk_status_read(clear=True, stream=s.cuda_stream)
+    waited = torch.zeros(1, dtype=torch.int64, device="cuda")
+    nk.nk_selftest_bounded_wait(300, waited.data_ptr(), s.cuda_stream)
+    s.synchronize()
+    assert nk.nk_status_read(clear=True, stream=s.cuda_stream) == nk.STATUS_TIMEOUT
+    assert int(waited.item()) >= 300000
