@@ -150,13 +150,6 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   return true;
 }
 
-// The same by a whole converged warp, with one answer for all lanes: each lane measures its own time, and
-// lanes that left a loop alone would be missed at the warp's next collective instruction.
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, int* status,
-                                               uint64_t limit_ns = 2000000000ull) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, status, limit_ns));
-}
-
 // Barrier `id` of `threads` threads (whole warps): in all of them, whether `x` holds in each.  Warps that
 // meet at a barrier in a loop have to leave it together: one that stayed behind would wait for ever.
 __device__ __forceinline__ bool barrier_and(uint32_t id, uint32_t threads, bool x) {

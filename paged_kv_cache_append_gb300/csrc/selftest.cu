@@ -7,7 +7,7 @@
 // phase can never complete; no copy or other thread is involved.  The wait
 // gives up after `limit_us` microseconds and the kernel returns normally: the
 // context stays usable and the status word tells the host.  The other lanes of
-// its warp, whose waits complete, have to give up with it (mbar_wait_warp).
+// its warp, whose waits complete, have to give up with it (a vote).
 // A second warp, whose wait completes at once, goes through pieces of work
 // with the first and has to leave the loop with it (barrier_and).
 #include "device.cuh"
@@ -26,7 +26,7 @@ __global__ void bounded_wait_selftest_kernel(int* status, uint64_t limit_ns, lon
   }
   __syncthreads();
   const uint64_t t0 = globaltimer_ns();
-  const bool done = mbar_wait_warp(&bar[threadIdx.x == 0 ? 0 : 1], 0, status, limit_ns);
+  const bool done = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[threadIdx.x == 0 ? 0 : 1], 0, status, limit_ns));
   const uint64_t t1 = globaltimer_ns();
   const bool any = __any_sync(0xffffffffu, done);
   bool live = done;
