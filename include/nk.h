@@ -484,9 +484,9 @@ int nk_diff_decode_workspace_bytes(const nk_pool* pool, int32_t B, int32_t T, in
  * outputs of all T; stale bytes past the frontier do not enter.
  * Two launches: split-K over the pages, then the join of the splits with the
  * difference and the norm.  Up to 8 query rows (T * Hq / H) a map they are
- * warp-level (csrc/diff_decode.cuh), their softmax weights f16, or bf16 in two
- * terms over BF16 pages; beyond that on the tensor cores, rounded as in
- * nk_paged_diff_prefill_attention.
+ * warp-level (csrc/diff_decode.cuh), their softmax weights f16 as in
+ * nk_paged_diff_prefill_attention, or bf16 in two terms over BF16 pages; beyond
+ * that on the tensor cores, rounded as there.
  * The pool's device must be current.
  * Errors: NK_ERR_INVALID_ARG, NK_ERR_SHAPE (H odd, Hq not a multiple of H, B > C,
  * T < 1), NK_ERR_UNSUPPORTED (head_dim 256; T * Hq / H > 64), NK_ERR_ALIGN,
@@ -509,8 +509,10 @@ int nk_diff_prefill_workspace_bytes(const nk_pool* pool, int32_t B, int32_t Tc, 
  *   two calls that share a workspace must not overlap.
  * A NaN or an infinity among the values of a chunk may reach all of its outputs.
  * Two launches: on the tensor cores (csrc/diff_tile.cuh) and for the join
- * (csrc/diff_join.cuh).  Softmax weights are f16 for every profile (relative
- * error <= 2^-11), scores exact products as in nk_paged_prefill_attention;
+ * (csrc/diff_join.cuh).  Softmax weights are f16 for every profile: within
+ * 2^-11 of themselves from 2^-21 of the row's largest on, within 2^-32 of the
+ * largest below (with FP8-row and INT8-G64 values, whose scales they carry,
+ * 2^-20 and 2^-31); scores exact products as in nk_paged_prefill_attention;
  * BF16 values are taken as f16 times a power of two per strip of 8 to 32 dims:
  * exact above 2^-14 of the strip's largest value so far, within 2^-19 of it
  * below; the quantized pages' values as there.

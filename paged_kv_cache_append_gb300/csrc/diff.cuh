@@ -18,6 +18,10 @@ namespace nk {
 constexpr float kDiffLog2e = 1.4426950408889634f;
 constexpr float kDiffLn2 = 0.6931471805599453f;
 
+// f16 weights without a factor per key are stored times 2^this: they are at most 2^8 (the lazy
+// reference's lag), and what lies below 2^-14 of f16's range is held to a fixed step only.
+constexpr int kDiffWeightLift = 7;
+
 struct DiffOut {
   const float* lambda;
   int64_t lambda_stride;

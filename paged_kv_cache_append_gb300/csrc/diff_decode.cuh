@@ -16,9 +16,9 @@
 //   softmax, base 2, per column over the warp's keys, with a lazy reference.
 //   PV   O^T += V^T P^T, dims as M, 64 dims at a time: the warp converts its 16 keys
 //        to f16 in 2 KB of its own and reads them back transposed.  FP8-row and
-//        INT8-G64 scales multiply the weights (a few products) instead of the values
-//        (32 a lane and head), lifted by a power of two per head (v_lift) that O
-//        carries.
+//        INT8-G64 scales multiply the weights instead of the values (32 a lane and
+//        head), in fp32 and rounded once, lifted by a power of two per head (v_lift)
+//        that O carries; weights over NVFP4 values carry 2^7 (kDiffWeightLift).
 // Pages that all queries see whole (all but a row's last) run without masks; in the
 // last one the warp zeroes its stale value rows in place.
 //
@@ -256,6 +256,9 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, PACK>::THREADS), 1)
   using Cfg = DiffCfg<KK, KV, D, PACK>;
   constexpr int RB = Cfg::RB, NT = Cfg::NT, NSTAGE = Cfg::NSTAGE, NW = Cfg::NW, NG = Cfg::NG, SG = Cfg::SG;
   constexpr int PARTS = Cfg::PARTS, MT = D / 16;
+  // How far the largest weight of a warp's first keys lies above 1, in base 2: f16 weights that
+  // take no factor are stored as high as they may be (kDiffWeightLift)
+  constexpr float TOP = Cfg::MMA_BF16 || Cfg::VAL_FAC ? 0.f : static_cast<float>(kDiffWeightLift);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qs = smem + Cfg::OFF_Q;                               // [8 NT columns][Q_PITCH]
@@ -486,7 +489,7 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, PACK>::THREADS), 1)
           if (key0 + r + 8 * (e >> 1) > lim[j][e & 1]) S[j][e] = -INFINITY;
     }
 #pragma unroll
-    for (int j = 0; j < NT; ++j) need = need || fmaxf(fmaxf(S[j][0], S[j][1]), fmaxf(S[j][2], S[j][3])) > 8.f;
+    for (int j = 0; j < NT; ++j) need = need || fmaxf(fmaxf(S[j][0], S[j][1]), fmaxf(S[j][2], S[j][3])) > 8.f + TOP;
     if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, PACK>::THREADS), 1)
           for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
           // the first page takes the exact maximum (a query's keys are a prefix:
           // one that sees none here sees none later), later ones the excess
-          const float shift = first ? (v == -INFINITY ? 0.f : v) : fmaxf(v, 0.f);
+          const float shift = first ? (v == -INFINITY ? 0.f : v - TOP) : fmaxf(v - TOP, 0.f);
           alpha[j][u] = first ? 0.f : ex2(-shift);
           rescale |= shift > 0.f;
           nm[j][u] -= shift;
@@ -507,7 +510,7 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, PACK>::THREADS), 1)
         }
       rescale = __any_sync(0xffffffffu, rescale) && !first;  // O is 0 before the first page
     }
-    uint32_t pb[PARTS][NT][2];  // P^T as B operands
+    uint32_t pb[PARTS][NT][2];  // P^T as B operands (with a factor per key: below, by head)
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -522,7 +525,7 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, PACK>::THREADS), 1)
               __floats2bfloat162_rn(S[j][2 * h] - __low2float(hi), S[j][2 * h + 1] - __high2float(hi));
           pb[0][j][h] = diff_movm(*reinterpret_cast<const uint32_t*>(&hi));
           pb[PARTS - 1][j][h] = diff_movm(*reinterpret_cast<const uint32_t*>(&lo));
-        } else {
+        } else if constexpr (!Cfg::VAL_FAC) {
           pb[0][j][h] = diff_movm(pack_f16x2(S[j][2 * h], S[j][2 * h + 1]));
         }
       }
@@ -578,18 +581,12 @@ __global__ void __launch_bounds__((DiffCfg<KK, KV, D, PACK>::THREADS), 1)
           diff_values<KV, D>(vtile, vst[v], vw, q64, slab, lane);
           if constexpr (Cfg::VAL_FAC) {
             if (q64 == 0 || KV == KIND_INT8) {
-              // weights of keys 2c, 2c + 1 (h = 0) and 2c + 8, 2c + 9; each product rounds once more
-              const uint32_t l2 = static_cast<uint32_t>(static_cast<uint16_t>(__half_as_ushort(__float2half_rn(pow2i(min(lift[v], 15)))))) * 0x00010001u;
-              const uint32_t l3 = static_cast<uint32_t>(static_cast<uint16_t>(__half_as_ushort(__float2half_rn(pow2i(max(lift[v] - 15, 0)))))) * 0x00010001u;
+              // weights of keys r (h = 0) and r + 8 with their lifted scales, rounded once
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint8_t* at = vst[v] + (16 * slab + 2 * c + 8 * h) * Cfg::VSB + (KV == KIND_INT8 ? 2 * q64 : 0);
-                const uint32_t s2 = Cfg::VSB == 2 ? *reinterpret_cast<const uint32_t*>(at)
-                                                  : static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at)) |
-                                                        static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at + Cfg::VSB)) << 16;
-                const uint32_t f = hmul2_u32(hmul2_u32(s2, l2), l3);
+                const float f = f16_at(vst[v] + (16 * slab + r + 8 * h) * Cfg::VSB + (KV == KIND_INT8 ? 2 * q64 : 0)) * pow2i(lift[v]);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) ps[j][h] = hmul2_u32(pb[0][j][h], f);
+                for (int j = 0; j < NT; ++j) ps[j][h] = diff_movm(pack_f16x2(S[j][2 * h] * f, S[j][2 * h + 1] * f));
               }
             }
           } else if (q64 == 0) {

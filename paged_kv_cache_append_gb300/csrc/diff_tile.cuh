@@ -39,7 +39,10 @@
 //     2^-3 (0 while it is there by itself): exact for every element above its 2^-14th, and
 //     to 2^-19 of the largest below.  k only falls (then O is rescaled, in both CTAs of a
 //     pair: the strips' factors are stored into both), and the store divides it out.
-// FP8-row value factors are lifted by a power of two of their own (v_lift).
+// Weights are stored lifted: 2^(s - reference) is at most 2^8, so 2^7 of it (with value factors,
+// 2^k by the largest of them, v_lift) stays below 2^15, and the weights that f16 holds to 11 bits
+// reach down to 2^-21 of a row's largest instead of 2^-14; below, they are within 2^-32 of it
+// (beside one key of weight 1, keys of 2^-20 each were off by 3%).
 //
 // Warps (640 threads): 0-7 softmax, warp w lanes 32 (w & 3) of every second page, from
 // w >> 2 on, a whole row to a thread; 8 TMA producer; 9 MMA issuer (CTA 1's tells CTA 0's
@@ -918,8 +921,9 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     // what turns a raw score into one in base 2: per key and row, or for all keys
     const float c_row = Cfg::KEY_FAC ? rs : fmaxf(a.scale_log2 * rs, 1.17549435e-38f);
     const F2 c2 = pack2(c_row, c_row);
-    // of this warp's pages: sum, and the reference and lift (FP8-row V) that it carries
-    constexpr int kLift0 = KV == KIND_FP8 ? kVLiftInit : 0;
+    // of this warp's pages: sum, and the reference and lift of the weights that it carries
+    // (without factors per key the reference itself lies kDiffWeightLift below the largest score)
+    constexpr int kLift0 = Cfg::VAL_FAC ? kVLiftInit : 0;
     float l = 0.f, m_own = -INFINITY;
     int k_own = kLift0;
     float mu = 0.f;
@@ -1012,7 +1016,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       const float* vsc = sF + fs * 256 + 128;
       const int kmax = valid ? pos - 64 * (w.p_lo + j - base) : -1;
       bool strips = false;  // BF16 values: a strip's k fell
-      float most = 0.f;     // FP8-row V: the largest scale of the page
+      float most = 0.f;     // the largest value factor of the page
       // the scores, their factors, and the reference after the page before
       uint64_t* xb = &x_full[4 * ((j - 1) & 1) + quad32];
       if (j > base) {
@@ -1023,7 +1027,7 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
         else live = live && wait(&s_full[sb], j / NS);
       }
       if constexpr (Cfg::BF16) strips = lane < Cfg::STRIPS && sF[fs * 256 + 4 * lane] != 0.f;  // any lane's, below
-      if constexpr (KV == KIND_FP8) {
+      if constexpr (Cfg::VAL_FAC) {
         const float4 s4 = *reinterpret_cast<const float4*>(sF + fs * 256 + 128 + 4 * lane);  // both heads' 128 scales
         most = fmaxf(fmaxf(s4.x, s4.y), fmaxf(s4.z, s4.w));
       }
@@ -1042,10 +1046,10 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
       if (j > base) {
         const float2 x = sX[((j - 1) & 1) * 128 + m];
         m_was = x.x;
-        if constexpr (KV == KIND_FP8) k_was = __float_as_int(x.y);
+        if constexpr (Cfg::VAL_FAC) k_was = __float_as_int(x.y);
       }
-      if constexpr (KV == KIND_FP8) k_now = v_lift(__reduce_max_sync(0xffffffffu, __float_as_uint(most)), k_was);
-      const float rmax = top == -INFINITY ? -INFINITY : top * c_row;
+      if constexpr (Cfg::VAL_FAC) k_now = v_lift(__reduce_max_sync(0xffffffffu, __float_as_uint(most)), k_was);
+      const float rmax = top == -INFINITY ? -INFINITY : fmaf(top, c_row, Cfg::VAL_FAC ? 0.f : -static_cast<float>(kDiffWeightLift));
       // lazy: the reference moves when a score passes it by more than 2^8, or the lift drops
       const float m_new = fmaxf(m_was, rmax);
       const bool resc = m_new != -INFINITY && (m_was == -INFINITY || m_new > m_was + kLazyThr || k_now != k_was);

@@ -1,0 +1,141 @@
+"""The differential attentions where their softmax and their values move far.
+
+Tolerances as derived in test_gpu_diff.py: c = 2^-10 + 1e-4 for the weights, the
+values and the fp32 steps, and for the scores of E4M3 queries (chunks and decodes
+of more than 8 query rows over FP8-row keys of head_dim 128) 2 e more, e = 2^-17
+max|q| max sum|k| |scale|.  What a case adds to that stands at the case.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_append_gb300 import nk
+from paged_kv_cache_append_gb300.workloads import bf16_to_bits
+from tests.test_gpu_diff import DEV, PROFILES, Batch, dev, f64, normal
+
+pytestmark = pytest.mark.gpu
+BASE = 2.0 ** -10 + 1e-4
+#: G, T, chunk: decodes of 1, 4, 8, 10 and 64 query rows; a chunk of many tiles to a cluster, one that is cut
+FORMS = {"one": (1, 1, None), "packed": (2, 2, None), "eight": (4, 2, None), "ten": (5, 2, None), "tiles": (16, 4, None),
+         "chunk": (2, 90, [90, 61]), "cut": (1, 9, [9, 4])}
+
+
+def e4m3_scores(b, keys):
+    """Twice the error of a score whose query is taken in two E4M3 terms."""
+    if b.D != 128 or b.profile not in ("fp8_row", "k8v4"):
+        return 0.0
+    most = float(keys.float().abs().sum(-1).max())
+    return 2 * 2.0 ** -17 * float(b.q.float().abs().max()) * most * abs(b.scale)
+
+
+def set_row(b, r, k, v, at=0):
+    """Tokens at .. of row r of the batch, on the GPU and in the oracle; k, v bf16 [n, H, D]."""
+    row = int(b.rows[r])
+    b.gpu.append(0, dev(b.tables), dev([row], torch.int32), dev([at], torch.int32), k[None].contiguous().to(DEV),
+                 v[None].contiguous().to(DEV))
+    b.img.append(0, b.tables, np.array([row]), np.array([at]), bf16_to_bits(k[None]), bf16_to_bits(v[None]))
+
+
+def batch(profile, D, form, F, **kw):
+    G, T, chunk = FORMS[form]
+    return Batch(profile, D, 2, G, T, F, chunk=chunk, **kw)
+
+
+def signs(n, seed):
+    return torch.where(torch.rand(n, generator=torch.Generator().manual_seed(seed)) < 0.5, -1.0, 1.0)
+
+
+def direct_queries(b, coef, seed):
+    """Queries coef[head] u + noise along one direction u of signs; returns u."""
+    u = signs(b.D, seed)
+    q = coef[None, None, :, None] * u + 0.25 * normal(tuple(b.q.shape), seed + 1).float()
+    b.q = q.to(torch.bfloat16)
+    b.d["q"] = b.q.to(DEV)
+    return u
+
+
+@pytest.mark.parametrize("profile", PROFILES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_maxima_that_rise_in_steps(profile, D, form):
+    """Keys along the queries' direction, larger step by step: a map's largest score rises by up to 10 in base 2 four
+    times (more than the 8 that a reference may lag), by less for other heads, and falls for some.  |s| stays below 32."""
+    b = batch(profile, D, form, [1500, 700])
+    coef = torch.tensor([(1.0, 0.6, -0.8, 0.3, 0.0, 1.0, 0.9)[i % 7] for i in range(b.Hq)])
+    beta = 28 / (2 * b.scale * D)   # the last step's score of coef 1: 28
+    u = direct_queries(b, beta * coef, 31)
+    most = torch.zeros(1, b.D)
+    for r, F in enumerate(b.F):
+        F = int(F)
+        step = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0])[torch.bucketize(torch.arange(F), torch.tensor(
+            [70, 64 * 3 + 17 + 16 * r, F // 2, F - 150]), right=True)]
+        k = (step[:, None, None] * u + 0.5 * normal((F, b.H, D), 41 + r).float()).to(torch.bfloat16)
+        set_row(b, r, k, normal((F, b.H, D), 51 + r))
+        most = torch.cat((most, k.flatten(0, 1).float()))
+    b.check(*b.run(), c=BASE + e4m3_scores(b, most))
+    assert nk.nk_status_read(True) == 0
+
+
+@pytest.mark.parametrize("profile", PROFILES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_values_that_rise_along_a_row(profile, D, form):
+    """Values, and with them the pages' value scales, 2^-9 times a normal one first, then 1, then 2^9: what a kernel
+    carries for their range changes over results that it has."""
+    b = batch(profile, D, form, [1500, 700])
+    for r, F in enumerate(b.F):
+        F = int(F)
+        size = torch.tensor([2.0 ** -9, 1.0, 2.0 ** 9])[torch.bucketize(torch.arange(F), torch.tensor(
+            [F // 3, F - 190]), right=True)]
+        v = (size[:, None, None] * normal((F, b.H, D), 61 + r).float()).to(torch.bfloat16)
+        set_row(b, r, normal((F, b.H, D), 71 + r), v)
+    b.check(*b.run(), c=BASE + (8e-4 if e4m3_scores(b, torch.ones(1, D)) else 0.0))
+    assert nk.nk_status_read(True) == 0
+
+
+@pytest.mark.parametrize("profile", PROFILES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("form,F", [(f, [1500, 700]) for f in FORMS if f != "chunk"] + [("chunk", [90, 61])]
+                         + [(f, [16, 16]) for f in ("packed", "eight", "tiles")])
+def test_small_weights_beside_one_that_dominates(profile, D, form, F):
+    """The first key takes nearly all of the softmax and its value is zero, so that the output is made of the others'
+    weights, about 2^-19 of it and the same for all (one key for all of them), of values of one sign.
+
+    A weight is held to 2^-11 from 2^-20 of the largest on, below it to 2^-31 of the largest: with weights of at least
+    2^-21.6, which the case asserts, 2^-9.4 at the worst."""
+    b = batch(profile, D, form, F)
+    coef = torch.ones(b.Hq)
+    beta = 13.2 / (b.scale * D)
+    u = direct_queries(b, beta * coef, 81)
+    other = 0.25 * signs(D, 83)
+    keys = []
+    for r, n in enumerate(b.F):
+        n = int(n)
+        k = other.expand(n, b.H, D).clone()
+        k[0] = u
+        v = 512 * (1 + 0.3 * normal((n, b.H, D), 91 + r).float())
+        v[0] = 0
+        keys.append(k)
+        set_row(b, r, k.to(torch.bfloat16), v.to(torch.bfloat16))
+    for r in range(b.B):   # the weights that the queries give: one key for all but the first
+        K, _ = b.img.gather(0, b.tables[b.rows[r]], 2)
+        s = b.scale * np.einsum("tjgmd,njmd->ntjgm", f64(b.q[r]).reshape(b.T, b.H // 2, b.G, 2, D),
+                                K.reshape(2, b.H // 2, 2, D))
+        assert np.all((s[0] - s[1]) / np.log(2) > 15) and np.all((s[0] - s[1]) / np.log(2) < 21.6)
+    b.check(*b.run(), c=BASE + 2.0 ** -9.4 + e4m3_scores(b, torch.cat([k.flatten(0, 1) for k in keys])))
+
+
+@pytest.mark.parametrize("profile", PROFILES)
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_chunk_and_the_decode_agree(profile, D):
+    """The last tokens of a chunk are a decode of them over the same pages: each within its own tolerance of the
+    definition, so within the sum of both of one another."""
+    b = Batch(profile, D, 2, 2, 5, [705, 133], chunk=[5, 5])
+    out, lse = b.run()
+    b.check(out, lse)
+    for T in (1, 5):
+        one = Batch(profile, D, 2, 2, T, [705, 133])
+        one.q = b.q[:, -T:].contiguous()
+        one.d["q"] = one.q.to(DEV)
+        one.check(*one.run())
