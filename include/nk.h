@@ -507,7 +507,8 @@ int nk_diff_prefill_workspace_bytes(const nk_pool* pool, int32_t B, int32_t Tc, 
  * above (n = b * Tc + i).  Rows i >= chunk_len[b] of out and lse are not written.
  *   workspace: nk_diff_prefill_workspace_bytes bytes, no initialisation needed;
  *   two calls that share a workspace must not overlap.
- * A NaN or an infinity among the values of a chunk may reach all of its outputs.
+ * A NaN or an infinity among the values of a chunk may reach the outputs of all
+ * of its tokens (without a norm, in the value's own dim).
  * Two launches: on the tensor cores (csrc/diff_tile.cuh) and for the join
  * (csrc/diff_join.cuh).  Softmax weights are f16 for every profile: within
  * 2^-11 of themselves from 2^-21 of the row's largest on, within 2^-32 of the

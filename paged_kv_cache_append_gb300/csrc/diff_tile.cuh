@@ -366,6 +366,13 @@ __device__ __forceinline__ uint32_t bf16x2_rebias(uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// The magnitudes of two bf16 values, 0 for an infinity or a NaN.
+__device__ __forceinline__ uint32_t bf16x2_finite(uint32_t w) {
+  const uint32_t infinity = 0x7F807F80u;
+  w &= 0x7FFF7FFFu;
+  return w & __hlt2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&infinity));
+}
+
 // The f16 pair of bf16 values w from their rebiased magnitudes.
 __device__ __forceinline__ uint32_t f16x2_of(uint32_t rebiased, uint32_t w) {
   return (rebiased << 3) | (w & 0x80008000u);
@@ -752,11 +759,11 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
                 make_uint4(f16x2_of(bf16x2_rebias(v[u].x), v[u].x), f16x2_of(bf16x2_rebias(v[u].y), v[u].y),
                            f16x2_of(bf16x2_rebias(v[u].z), v[u].z), f16x2_of(bf16x2_rebias(v[u].w), v[u].w));
         } else {
-          uint32_t raw2 = 0u;
+          uint32_t raw2 = 0u;  // of the finite values: an infinity or a NaN leaves its neighbours' k alone
 #pragma unroll
           for (int u = 0; u < St::UNITS; ++u)
-            raw2 = __vmaxu2(raw2, __vmaxu2(__vmaxu2(v[u].x & 0x7FFF7FFFu, v[u].y & 0x7FFF7FFFu),
-                                           __vmaxu2(v[u].z & 0x7FFF7FFFu, v[u].w & 0x7FFF7FFFu)));
+            raw2 = __vmaxu2(raw2, __vmaxu2(__vmaxu2(bf16x2_finite(v[u].x), bf16x2_finite(v[u].y)),
+                                           __vmaxu2(bf16x2_finite(v[u].z), bf16x2_finite(v[u].w))));
           const uint32_t most = __reduce_max_sync(0xffffffffu, max(raw2 & 0xFFFFu, raw2 >> 16));
           const int e = static_cast<int>(most >> 7) - 127;
           if (i == 0) k = strip_lift(most);

@@ -126,6 +126,24 @@ def test_small_weights_beside_one_that_dominates(profile, D, form, F):
     b.check(*b.run(), c=BASE + 2.0 ** -9.4 + e4m3_scores(b, torch.cat([k.flatten(0, 1) for k in keys])))
 
 
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_an_infinite_value_stays_in_its_dim(form, D, bad):
+    """Without a norm an infinity or a NaN among BF16 values reaches its own output dim and no other, whatever shares
+    its strip of dims."""
+    b = batch("bf16", D, form, [300, 200], norm=False)
+    want = b.reference()
+    page, at, head, d = int(b.tables[b.rows[0], 1]), 17, 1, 21
+    b.gpu.planes[0][1].view(torch.bfloat16).view(-1, 2, 64, D)[page, head, at, d] = bad
+    out, lse = b.run()
+    torch.cuda.synchronize()
+    n = want[0][0].shape[0]
+    assert not torch.isfinite(out[0, :n, :, head * D + d]).any()
+    out[0, :n, :, head * D + d] = torch.from_numpy(want[0][0][:, :, head * D + d]).to(out)
+    b.check(out, lse)
+
+
 @pytest.mark.parametrize("profile", PROFILES)
 @pytest.mark.parametrize("D", [64, 128])
 def test_a_chunk_and_the_decode_agree(profile, D):
