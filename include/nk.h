@@ -515,8 +515,8 @@ int nk_diff_prefill_workspace_bytes(const nk_pool* pool, int32_t B, int32_t Tc, 
  * largest below (with FP8-row and INT8-G64 values, whose scales they carry,
  * 2^-20 and 2^-31); scores exact products as in nk_paged_prefill_attention;
  * BF16 values are taken as f16 times a power of two per strip of 8 to 32 dims:
- * exact above 2^-14 of the strip's largest value so far, within 2^-19 of it
- * below; the quantized pages' values as there.
+ * exact from 2^-11 of the strip's largest value so far on, within 2^-19 of that
+ * largest below; the quantized pages' values as there.
  * The pool's device must be current.
  * Errors: as nk_paged_diff_decode_attention; NK_ERR_UNSUPPORTED for Hq / H > 64. */
 int nk_paged_diff_prefill_attention(const void* q_chunk, int32_t Hq, const nk_pool* pool,

@@ -36,8 +36,8 @@
 //     head has its own P (the second 16 columns further), N = D twice;
 //   * BF16 values are rewritten in place, v 2^k with a power of two per strip of dims (a
 //     converter warp's) that brings the strip's largest value so far below 2^15 and above
-//     2^-3 (0 while it is there by itself): exact for every element above its 2^-14th, and
-//     to 2^-19 of the largest below.  k only falls (then O is rescaled, in both CTAs of a
+//     2^-3 (0 while it is there by itself): exact for every element from 2^-11 of the largest
+//     on (2^-14 itself, where k = 0), and to 2^-19 of the largest below.  k only falls (then O is rescaled, in both CTAs of a
 //     pair: the strips' factors are stored into both), and the store divides it out.
 // Weights are stored lifted: 2^(s - reference) is at most 2^8, so 2^7 of it (with value factors,
 // 2^k by the largest of them, v_lift) stays below 2^15, and the weights that f16 holds to 11 bits

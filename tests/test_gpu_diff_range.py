@@ -144,6 +144,62 @@ def test_an_infinite_value_stays_in_its_dim(form, D, bad):
     b.check(out, lse)
 
 
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("size", [2.0 ** -3, 1.0, 2.0 ** 14, 2.0 ** 40])
+def test_a_dim_far_above_its_neighbours(form, D, size):
+    """One dim of every 16 holds values up to about `size`, its neighbours 2^-13 of that.
+
+    On the tensor cores a BF16 value is exact from 2^-11 of the largest in its strip of dims on, and within 2^-19 of the
+    largest below: 2^-19 of a dim's largest for each of its neighbours, against their own size of 2^-13, is 2^-6 of a
+    neighbour at the worst, so an output (no norm) may be off by (1 + lambda) 2^-19 of the largest."""
+    b = batch("bf16", D, form, [300, 200], norm=False)
+    scale = torch.full((D,), size * 2.0 ** -15)
+    scale[3::16] = size * 2.0 ** -2      # normal values stay below 4.5
+    most = 0.0
+    for r, n in enumerate(b.F):
+        v = (normal((int(n), b.H, D), 15 + r).float() * scale).to(torch.bfloat16)
+        v[0, :, 3::16] = size * 0.5       # a strip's first page holds its size
+        most = max(most, float(v.float().abs().max()))
+        set_row(b, r, normal((int(n), b.H, D), 25 + r), v)
+    out, lse = b.run()
+    torch.cuda.synchronize()
+    for r, (o, l, raw, a) in enumerate(b.reference()):
+        n = o.shape[0]
+        got, s = out[r, :n].double().cpu().numpy(), 0.2
+        lam = np.abs(b.lam.double().numpy())[None, :, None]
+        tol = s * (BASE * a + (0.0 if FORMS[form][0] * FORMS[form][1] <= 8 and b.chunk is None else
+                               (1 + lam) * 2.0 ** -19 * most))
+        tol = tol + 2.0 ** -8 * (np.abs(o) + tol)
+        assert np.all(np.abs(got - o) <= tol), (r, np.max(np.abs(got - o) - tol))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("form", ["chunk", "tiles"])
+@pytest.mark.parametrize("size", [2.0 ** -90, 2.0 ** -3, 0.25, 1.0, 2.0 ** 14, 2.0 ** 15, 2.0 ** 90])
+def test_one_bf16_value_comes_back(D, form, size):
+    """A token that sees one key, lambda 0, no norm, a scale of 1: its output is the key's value as the tensor cores
+    take it, exact from 2^-11 of the largest of a strip (one in every 8 dims is `size`) on, within 2^-19 of it below."""
+    G, T, _ = FORMS[form]
+    b = Batch("bf16", D, 2, G, T, [1, 1], chunk=[1, 1] if form == "chunk" else None, norm=False)
+    g = torch.Generator().manual_seed(7)
+    small = torch.zeros(0)
+    for r in range(2):
+        v = size * signs(2 * D, r) * 2.0 ** (-24 * torch.rand(2 * D, generator=g))
+        v[::8] = size
+        v = v.to(torch.bfloat16)
+        small = torch.cat((small, v.float()[None])) if r else v.float()[None]
+        set_row(b, r, normal((1, 2, D), 5 + r), v.view(1, 2, D))
+    b.diff = nk.Diff(torch.zeros(b.Hq // 2, device=DEV), None, 1e-5, 1.0)
+    out, _ = b.run()
+    torch.cuda.synchronize()
+    got = (out[:, 0] if form == "chunk" else out[:, -1]).double().cpu()   # of a decode the last token sees the key
+    want = small.double()[:, None].expand_as(got)
+    large = want.abs() >= size * 2.0 ** -11
+    assert torch.equal(got[large], want[large])
+    assert bool(((got - want).abs() <= 2.0 ** -19 * size + 2.0 ** -8 * want.abs())[~large].all())
+
+
 @pytest.mark.parametrize("profile", PROFILES)
 @pytest.mark.parametrize("D", [64, 128])
 def test_a_chunk_and_the_decode_agree(profile, D):
