@@ -44,6 +44,16 @@ __device__ __forceinline__ uint4 pack_bf16(const float (&f)[8]) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
+// x / (1 + e^-g).  With e^-|g| = t^2 the divisor stays in [1, 2], where __fdividef holds, and a
+// gate far below 0 scales x by t twice: the factor by itself would leave fp32's range from -87 on,
+// where an x of 2^127 still gives results of ordinary size (2048 gated rows of 4096: 20.5 us with
+// 1 / (1 + e^-g) at once, 21.3 so).
+__device__ __forceinline__ float gated(float x, float g) {
+  const float t = ex2(-0.7213475204f * fabsf(g));  // log2(e) / 2
+  if (g < 0.f) x = x * t * t;
+  return __fdividef(x, fmaf(t, t, 1.f));
+}
+
 // Sum over the group of `lanes` (a power of two up to 32) or, beyond a warp,
 // over the CTA; `part` is one slot per warp.
 __device__ __forceinline__ float group_sum(float v, int lanes, float* part) {
@@ -113,8 +123,7 @@ __global__ void __launch_bounds__(512) block_norm_kernel(NormArgs a, int lanes) 
       for (int k = 0; k < 8; ++k) {
         float x = u[i][k];
         if (a.post) x *= f * (p[k] + a.offset);
-        // a sigmoid below 2^-126 is 0 (__fdividef), far below what u's bf16 distinguishes from it
-        if (a.gate) x *= a.sigmoid ? __fdividef(1.f, 1.f + __expf(-g[k])) : g[k];
+        if (a.gate) x = a.sigmoid ? gated(x, g[k]) : x * g[k];
         h[i][k] = fmaf(a.scale, x, a.residual_scale * h[i][k]);
       }
     }

@@ -158,3 +158,21 @@ def test_captured_and_on_a_given_stream():
         g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, out))
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("power,low", [(127, -170.0), (60, -120.0), (0, -80.0)])
+def test_gates_far_below_zero_scale_large_values(power, low, wide):
+    """A logistic gate that fp32 cannot hold by itself (from -88 on) times a value that makes an ordinary number of it.
+
+    e^-|g| is the square of 2^z, z = |g| / 2 log2 e <= 123: z is off by 2 half steps (2^-24 z each), which 2^z takes times
+    ln 2, and by 2 ulp (2^-23) of the exponential: 2 * (123 * ln 2 + 2) ulp = 175, and 8 for the products and the
+    division, less than 2^-15.2; then half a step of the output."""
+    n = 512
+    g = torch.linspace(low, 0.0, n).bfloat16().repeat(2, 1)
+    y = ((1 + torch.rand((2, n), generator=torch.Generator().manual_seed(3)) * 0.9) * 2.0 ** power).bfloat16()
+    r = torch.zeros((2, n), dtype=torch.float32 if wide else torch.bfloat16)
+    _, h = nk.residual_norm(y.to(DEV), r.to(DEV), nk.ResidualNorm(None, sigmoid_gate=True), gate=g.to(DEV))
+    torch.cuda.synchronize()
+    want = f64(y) / (1 + np.exp(-f64(g)))
+    assert np.all(np.abs(f64(h) - want) <= (2.0 ** -15.2 + (0 if wide else 2.0 ** -8)) * want)
