@@ -170,3 +170,12 @@ def test_captured_steps_grow_and_trim():
     assert int(n) == ref["n_free"] and np.array_equal(free.cpu(), ref["free"])
     assert np.array_equal(out[0].cpu(), a["frontiers"]) and np.array_equal(out[2].cpu(), a["slots"])
     assert np.array_equal(trimmed.cpu(), length)
+
+
+@pytest.mark.parametrize("B,T", [(8, 256), (8, 257), (1, 2048), (1, 2049), (3, 682), (3, 683)])
+def test_tokens_beside_the_tables_and_in_a_launch_of_their_own(B, T):
+    """Up to 2048 tokens of a batch get their positions and slots from the CTA of the tables, more from a second kernel."""
+    used = [1, 2, 3, 4, 9, 0, 7, 30][:B]
+    committed = [0, 1, 63, 64, 65, 127, 128, 400][:B]
+    Case(B, 64, B * 64, used, list(range(B))[::-1], committed, T).check()
+    Case(B, 64, B * 64, used, list(range(B)), committed, T, counts=[max(0, T - 5 * i) for i in range(B)]).check()
