@@ -164,8 +164,9 @@ struct DiffPlan {
 
 // Up to 8 query rows a map the warp-level kernel (4 or 8 rows of both maps in
 // one column tile or two), beyond that the 64-row tiles; both with one CTA per SM.
-// 8 rows over 8 x 32768 tokens, head_dim 128, by the warps and by the tiles: FP8-row 59
-// and 88 us, INT8-G64 61 and 108; over 8 x 131072, K8V4: 144 and 203.
+// 8 rows by the warps, and the tiles, whose time up to 64 rows is one (head_dim 128, 8
+// requests up to 32768 tokens): FP8-row 55 and 76 us, INT8-G64 64 and 113; up to 131072,
+// K8V4: 143 and 174.
 static int diff_plan(const nk_pool* p, int B, int T, int Hq, DiffPlan* pl) {
   const int rc = check_diff_shape(p, B, T, Hq);
   if (rc) return rc;

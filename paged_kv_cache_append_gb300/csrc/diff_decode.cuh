@@ -26,10 +26,13 @@
 // two warps that exchange their weights (FP8-row, head_dim 128: 3800 warp instructions a
 // page, whose issue bound that form at 46% of the copy rate).
 //
-// Measured (with the join, L2 cold): 8 rows of 25500 tokens, 16 heads over 4, FP8-row: 45 us,
-// 69% of the copy rate; of 131072: each further page at 94-100% of it (FP8-row, BF16, K8V4),
-// at 64% for NVFP4, whose conversion bounds it.  What is left is the start (plan, first
-// copies) and the join, 15 us of every call.
+// Measured (with the join, L2 cold): 8 requests of 25500 tokens, 16 heads over 4, FP8-row: 45
+// us, 69% of the copy rate.  From 65536 to 131072 tokens a request, each further page at this
+// share of the copy rate, with up to 4 query rows and with 5 to 8 (head_dim 128: two groups of
+// warps instead of three, for the registers): BF16 more than 100% and the same, FP8-row 106%
+// and 88%, K8V4 99% and 79%, INT8-G64 92% and 74%, NVFP4 65% and 50% (conversion and
+// products bound the shares below 90%).  Beside the pages, the start (plan, first copies) and
+// the join take 15 us of every call.
 //
 // Partials of (map, query row) go to the workspace, for the join (diff_decode.cu).
 #pragma once

@@ -60,12 +60,21 @@
 // warp the 33 of the tensor core.
 //
 // Measured (with the join, L2 cold): chunk of 2048 tokens behind 8150, 16 query heads,
-// BF16: 209 us, 58% of the dense rate; 4 x 2048 behind 16384, K8V4: 1125 us, 68%; verify
-// of 4 tokens of 32 heads over 8 x 131072, K8V4: 173 us, 56% of the copy rate.  A page takes
-// 1050 (K8V4) to 1350 cycles (BF16): what bounds it is the loop from S over the softmax to
-// the PV that frees S's buffer, three pages long; two warps for S and PV, which shorten that
-// of the issue, gained as much for BF16 as they lost for the verify.  A piece of a tile costs
-// 7 us beside its pages (queries, first scores, partial).
+// BF16: 210 us, 57% of the dense rate; 4 x 2048 behind 16384, K8V4: 1127 us, 66%; verify
+// of 4 tokens of 32 heads over 8 x 131072, K8V4: 172 us, 57% of the copy rate.  A page of a
+// chunk takes 1050 (K8V4) to 1350 cycles (BF16): what bounds it is the loop from S over the
+// softmax to the PV that frees S's buffer, three pages long; two warps for S and PV, which
+// shorten that of the issue, were 4 us faster for a BF16 chunk (head_dim 64: 17 of 250) and 7
+// slower for the verify.  A piece of a tile costs 7 us beside its pages (queries, first
+// scores, partial).  The verify's two MMAs for S, each with half of its rows zero, and M 128 of
+// values are 8.4 MFLOP a page and pair whatever the rows: 110 us of those 172 at the dense rate.
+// The roles' registers do not hold everything (-Xptxas -v): the chunk kernels spill 176 (BF16)
+// to 280 bytes (INT8-G64) a thread, the decodes 0 to 72; executed, 16 local loads a CTA's page
+// for BF16, 13 K8V4, 51 FP8-row, 55 INT8-G64, of 2900 to 5000 warp instructions.
+//
+// S(j) goes over the P that PV(j - NS) reads, with no wait between: the MMAs that one thread
+// issues run in issue order, here also across kinds (E4M3 scores, f16 values), shapes and the
+// two CTAs of a pair.
 //
 // All waits are bounded; a wait that ran out ends its warp's work (for all lanes, and for
 // both softmax warps of a row), the others' waits run out too, and the CTA leaves without
