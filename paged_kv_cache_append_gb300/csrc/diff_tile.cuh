@@ -36,8 +36,9 @@
 //     head has its own P (the second 16 columns further), N = D twice;
 //   * BF16 values are rewritten in place, v 2^k with a power of two per strip of dims (a
 //     converter warp's) that brings the strip's largest value so far below 2^15 and above
-//     2^-3 (0 while it is there by itself): exact for every element from 2^-11 of the largest
-//     on (2^-14 itself, where k = 0), and to 2^-19 of the largest below.  k only falls (then O is rescaled, in both CTAs of a
+//     2^-3 (0 while it is there by itself): exact for every element from 2^-11 of the
+//     largest on (2^-14 itself, where k = 0), and to 2^-19 of the largest below; infinities
+//     and NaN have no part in k.  k only falls (then O is rescaled, in both CTAs of a
 //     pair: the strips' factors are stored into both), and the store divides it out.
 // Weights are stored lifted: 2^(s - reference) is at most 2^8, so 2^7 of it (with value factors,
 // 2^k by the largest of them, v_lift) stays below 2^15, and the weights that f16 holds to 11 bits
@@ -718,8 +719,8 @@ __global__ void __launch_bounds__((DiffTileCfg<KK, KV, D, BOTH>::THREADS), 1)
     const int ct = tid - 32 * (Cfg::NSOFT + 4);
     // Lanes measure the time of a wait each for itself, and the warp stops as one, by a vote at
     // the end of a page: lanes that left alone would be missed at its next collective
-    // instruction.  (INT8-G64, with a vote there and without any: verify 140 us and 132, chunk of
-    // 2048 behind 8192 363 and 373; the other page types the same.)
+    // instruction.  (INT8-G64, with a vote there and without any: 8 x 4 tokens of 32 heads over
+    // 32768 140 us and 132, chunk of 2048 behind 8192 363 and 373; the other page types the same.)
     bool ok = true;
     if constexpr (Cfg::BF16) {
       // ------------- converters of BF16 values: a strip of dims per warp -----------
